@@ -326,6 +326,96 @@ int gla_chunk_fwd_host(const void* q, const void* k, const void* v, const float*
                        int dk, int dv, int dtype, int pieces, void* workspace, size_t ws_bytes,
                        gla_stream_t stream);
 
+/* Sequences that continue a shared prefix ("Beyond the KV cache", section "Optimizing inference on
+ * Trainium2", keeps one page of state per sequence; the calls below, without counterpart there, serve
+ * many sequences from one state).  A prefix - a prompt, a system message - is run once and leaves its
+ * state S_p in a pool; a sequence that continues it keeps only its own tokens after the prefix, its
+ * tail:
+ *     S_n = lambda^L S_p + sum_{j < L} lambda^(L-1-j) k_j v_j^T     (L tokens in the tail).
+ *   pool         [pool_rows, H, 96, 192] fp32 states (a forward's hT, a decode pool); read only.
+ *   prefix_row   [n] int32 device: the pool row that each sequence continues.  Rows may repeat, in
+ *                any order; sequences of one row that stand next to each other share one read of it.
+ *   gla_tail     host struct of the tails, which live in device memory that the caller owns:
+ *                  k [rows, H, cap, 96], v [rows, H, cap, 192], the head before the token;
+ *                  GLA_TAIL_PLAIN: elements of the call's dtype; k_scales and v_scales unused.
+ *                  GLA_TAIL_MXFP8: E4M3 codes with E8M0 scales k_scales [rows, H, cap, 3] and
+ *                  v_scales [rows, H, cap, 6], one per 32 values, quantised by the rule of
+ *                  gla_decode_step_mxfp8_state (nothing saturates; an infinity becomes the
+ *                  largest finite code, a NaN stays one).
+ *                cap >= 16 and a multiple of 16 (else GLA_ERR_SHAPE); every array 16-byte aligned.
+ *   tail_slot    [n] int32 device: the tail row of each sequence, NULL = row n (then rows >= n is
+ *                required).  Rows that a call writes must be distinct.
+ *   tail_len     [n] int32 device: tokens in each tail, at places 0 .. tail_len - 1.  The calls
+ *                read it and never change it: the caller advances it after a decode step.  Places
+ *                from tail_len on may hold anything, NaN included.
+ * A sequence whose row, slot, length or places lie outside the pool or its tail is skipped (its
+ * outputs and its tail are left as they were) and records GLA_ERR_SHAPE in the device error word.
+ * Each call returns once its work is queued on `stream`, may be captured into a graph, and needs no
+ * workspace except where it takes one. */
+typedef enum { GLA_TAIL_PLAIN = 0, GLA_TAIL_MXFP8 = 1 } gla_tail_format;
+typedef struct gla_tail {
+  void* k;
+  void* v;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int rows, cap, format;
+} gla_tail;
+
+/* One decode step for N sequences: with L = tail_len[n],
+ *     o = scale (lambda^(L+1) S_p^T q + sum_{j < L} lambda^(L-j) (q . k_j) v_j + (q . k) v),
+ * the readout after the token's own update, with the token's k and v as they are given; then k and
+ * v are written to place L of the tail (quantised where it is MXFP8), which needs L < cap.
+ *   q, k [N, H, 96]; v, o [N, H, 192]; dtype `dtype`.  One launch.  For L beyond about 256 (bf16)
+ *   or 500 (MXFP8) tokens a state of its own (gla_tail_fold, then gla_decode_step) is less to read. */
+int gla_prefix_decode_step(const void* q, const void* k, const void* v, const float* log_lambda, float scale,
+                           const float* pool, int pool_rows, const int32_t* prefix_row, const gla_tail* tail,
+                           const int32_t* tail_slot, const int32_t* tail_len, void* o, int N, int H, int dk, int dv,
+                           int dtype, gla_stream_t stream);
+
+/* Packed tokens written to the tails, and read back.
+ *   k, v         packed [T, H, 96 / 192], dtype `dtype` (read by append, written by read).
+ *   pos          [n_seq] int32 device: sequence n's tokens go to (come from) places pos[n],
+ *                pos[n] + 1, ... of its tail (for an append, usually tail_len).
+ *   cu_seqlens   [n_seq + 1] int32 device packed offsets, as in gla_chunk_fwd; rows from
+ *                cu_seqlens[n_seq] on are left alone.
+ * An MXFP8 tail is quantised as it is written and widened as it is read: exactly, where dtype holds
+ * the value (always, but for values of bf16's or fp32's subnormal range). */
+int gla_tail_append(const void* k, const void* v, const gla_tail* tail, const int32_t* tail_slot, const int32_t* pos,
+                    const int32_t* cu_seqlens, int n_seq, int T, int H, int dk, int dv, int dtype, gla_stream_t stream);
+int gla_tail_read(const gla_tail* tail, const int32_t* tail_slot, const int32_t* pos, const int32_t* cu_seqlens, void* k,
+                  void* v, int n_seq, int T, int H, int dk, int dv, int dtype, gla_stream_t stream);
+
+/* Tails folded into states of their own:
+ *     out[out_row[n]] = lambda^L pool[prefix_row[n]] + sum_{j < L} lambda^(L-1-j) k_j v_j^T,
+ * L = tail_len[n]; the state from which gla_decode_step, or more sequences, continue.
+ *   out          [out_rows, H, 96, 192] fp32; out_row [N] int32 device, or NULL: row n (then
+ *                out_rows >= N is required).  Rows must be distinct.  out may be the pool itself, and
+ *                a sequence may be folded into the row it continues, as long as no other sequence of
+ *                the call continues a row that the call writes.
+ *   dtype        type of the tail's elements (GLA_TAIL_PLAIN). */
+int gla_tail_fold(const float* log_lambda, const float* pool, int pool_rows, const int32_t* prefix_row,
+                  const gla_tail* tail, const int32_t* tail_slot, const int32_t* tail_len, float* out, int out_rows,
+                  const int32_t* out_row, int N, int H, int dk, int dv, int dtype, gla_stream_t stream);
+
+/* gla_chunk_fwd and gla_chunk_bwd on packed sequences that continue shared states: sequence n's
+ * initial state is pool[prefix_row[n]], read where it stands (no copies).  cu_seqlens is required;
+ * every other argument as there.  A prefix_row outside the pool starts that sequence from zeros and
+ * records GLA_ERR_SHAPE.
+ *   dpool        [pool_rows, H, 96, 192] fp32 output, or NULL to skip: the pool's gradient, row p
+ *                the sum of dh0 over the sequences that continue p, added in their order; zeros for
+ *                a row that none continues.
+ *   workspace    >= gla_workspace_bytes(n_seq, H) (forward) or gla_prefix_bwd_workspace_bytes(n_seq,
+ *                T, H, dtype) bytes (backward: gla_chunk_bwd's and one state per sequence). */
+int gla_prefix_fwd(const void* q, const void* k, const void* v, const float* log_lambda, const float* pool,
+                   int pool_rows, const int32_t* prefix_row, float scale, void* o, float* hT,
+                   const int32_t* cu_seqlens, int n_seq, int T, int H, int dk, int dv, int dtype, void* workspace,
+                   size_t ws_bytes, gla_stream_t stream);
+size_t gla_prefix_bwd_workspace_bytes(int n_seq, int T, int H, int dtype);
+int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log_lambda, const float* pool,
+                   int pool_rows, const int32_t* prefix_row, float scale, const void* dO, const float* dhT, void* dq,
+                   void* dk, void* dv, float* dpool, const int32_t* cu_seqlens, int n_seq, int T, int H, int dk_size,
+                   int dv_size, int dtype, void* workspace, size_t ws_bytes, gla_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the current device's sticky error word:
  * GLA_OK, GLA_ERR_TIMEOUT or GLA_ERR_SHAPE (or, in the debug-bounds build, GLA_ERR_BOUNDS);
  * GLA_ERR_LAUNCH if the stream itself failed.

@@ -14,6 +14,7 @@ import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -23,7 +24,8 @@ __all__ = [
     "gla_chunk_bwd", "gla_decode_step", "gla_chunk_fwd_noalloc", "gla_head_norm_gate", "gla_chunk_fwd_split",
     "gla_split_choose_seg_chunks", "gla_get_device_error",
     "gla_set_wait_limit_ns", "gla_debug_bounds", "debug_bounds_library", "gla_chunk_fwd_host",
-    "gla_chunk_fwd_host_workspace_bytes",
+    "gla_chunk_fwd_host_workspace_bytes", "GlaTail", "gla_tail_alloc", "gla_tail_append", "gla_tail_read",
+    "gla_tail_fold", "gla_prefix_decode_step", "gla_prefix_fwd", "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes",
     "gla_status_string", "DK", "DV", "CHUNK", "EXPORTS",
 ]
 
@@ -35,7 +37,9 @@ EXPORTS = ("gla_workspace_bytes", "gla_bwd_workspace_bytes", "gla_chunk_fwd", "g
            "gla_decode_step_norm_gate", "gla_decode_step_mxfp8_state", "gla_state_to_mxfp8",
            "gla_state_from_mxfp8",
            "gla_split_choose_seg_chunks", "gla_chunk_fwd_noalloc", "gla_get_device_error", "gla_set_wait_limit_ns",
-           "gla_debug_bounds", "gla_chunk_fwd_host", "gla_chunk_fwd_host_workspace_bytes", "gla_status_string")
+           "gla_debug_bounds", "gla_chunk_fwd_host", "gla_chunk_fwd_host_workspace_bytes", "gla_status_string",
+           "gla_prefix_decode_step", "gla_tail_append", "gla_tail_read", "gla_tail_fold", "gla_prefix_fwd",
+           "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes")
 NOALLOC_MAX_SEQS = 16384
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -121,6 +125,20 @@ def load_library(build: bool = True, debug: bool | None = None):
         lib.gla_chunk_fwd_host_workspace_bytes.restype = Z
         lib.gla_chunk_fwd_host.argtypes = [P, P, P, P, P, F, P, P, I, I, I, I, I, I, I, P, Z, P]
         lib.gla_chunk_fwd_host.restype = I
+        lib.gla_prefix_decode_step.argtypes = [P, P, P, P, F, P, I, P, P, P, P, P, I, I, I, I, I, P]
+        lib.gla_prefix_decode_step.restype = I
+        lib.gla_tail_append.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, P]
+        lib.gla_tail_append.restype = I
+        lib.gla_tail_read.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, P]
+        lib.gla_tail_read.restype = I
+        lib.gla_tail_fold.argtypes = [P, P, I, P, P, P, P, P, I, P, I, I, I, I, I, P]
+        lib.gla_tail_fold.restype = I
+        lib.gla_prefix_fwd.argtypes = [P, P, P, P, P, I, P, F, P, P, P, I, I, I, I, I, I, P, Z, P]
+        lib.gla_prefix_fwd.restype = I
+        lib.gla_prefix_bwd_workspace_bytes.argtypes = [I, I, I, I]
+        lib.gla_prefix_bwd_workspace_bytes.restype = Z
+        lib.gla_prefix_bwd.argtypes = [P, P, P, P, P, I, P, F, P, P, P, P, P, P, P, I, I, I, I, I, I, P, Z, P]
+        lib.gla_prefix_bwd.restype = I
         _libs[debug] = lib
         return lib
 
@@ -653,6 +671,264 @@ def gla_head_norm_gate(o, g, weight, tier, eps=1e-6, y=None):
                                     _ptr(y), rows, H, DV, dt, _stream(dev))
     _check(rc, "gla_head_norm_gate")
     return y
+
+
+class GlaTail(NamedTuple):
+    """Tail caches of sequences that continue a shared prefix: keys ``[R, H, cap, 96]`` and values
+    ``[R, H, cap, 192]`` in the type of the calls' q, k, v, or as MXFP8 (uint8 E4M3 codes of the same
+    shapes, with uint8 E8M0 scales ``[R, H, cap, 3]`` and ``[R, H, cap, 6]``)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: Optional[torch.Tensor] = None
+    v_scales: Optional[torch.Tensor] = None
+
+
+class _CTail(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("rows", ctypes.c_int), ("cap", ctypes.c_int),
+                ("format", ctypes.c_int)]
+
+
+def gla_tail_alloc(rows: int, H: int, cap: int, dtype=torch.bfloat16, device="cuda") -> GlaTail:
+    """Zeroed tails of ``rows`` rows with room for ``cap`` tokens (rounded up to a multiple of 16);
+    ``dtype`` bfloat16 or float32, or ``torch.float8_e4m3fn`` for MXFP8."""
+    cap = max(16, -(-int(cap) // 16) * 16)
+    if dtype == torch.float8_e4m3fn:
+        z = lambda d: torch.zeros((rows, H, cap, d), dtype=torch.uint8, device=device)  # noqa: E731
+        return GlaTail(z(DK), z(DV), z(DK // 32), z(DV // 32))
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"tails are bfloat16, float32 or float8_e4m3fn (MXFP8), got {dtype}")
+    z = lambda d: torch.zeros((rows, H, cap, d), dtype=dtype, device=device)  # noqa: E731
+    return GlaTail(z(DK), z(DV))
+
+
+def _tail(tail, H, dtype, dev):
+    """Checks the tails' tensors and returns the C struct."""
+    k, v, ks, vs = tail
+    mx = ks is not None or vs is not None
+    et = torch.uint8 if mx else dtype
+    _need(k, "tail.k", et, dev)
+    _need(v, "tail.v", et, dev)
+    if k.dim() != 4 or k.shape[1] != H or k.shape[3] != DK or v.shape != (*k.shape[:3], DV):
+        raise ValueError("the tail must be k [R, H, cap, 96] and v [R, H, cap, 192]")
+    if mx:
+        _need(ks, "tail.k_scales", torch.uint8, dev)
+        _need(vs, "tail.v_scales", torch.uint8, dev)
+        if ks.shape != (*k.shape[:3], DK // 32) or vs.shape != (*k.shape[:3], DV // 32):
+            raise ValueError("tail scales must be [R, H, cap, 3] and [R, H, cap, 6]")
+    return _CTail(k.data_ptr(), v.data_ptr(), ks.data_ptr() if mx else None, vs.data_ptr() if mx else None,
+                  k.shape[0], k.shape[2], int(mx))
+
+
+def _index(t, name, n, dev):
+    if t is not None:
+        _need(t, name, torch.int32, dev, n)
+
+
+def _pool(pool, H, dev):
+    _need(pool, "pool", torch.float32, dev)
+    if pool.dim() != 4 or pool.shape[1:] != (H, DK, DV):
+        raise ValueError("pool must be [P, H, 96, 192]")
+
+
+def gla_prefix_decode_step(q, k, v, log_lambda, pool, prefix_row, tail, tail_len, tail_slot=None, scale=None, o=None):
+    """One decode step of N sequences that continue shared states (``gla_prefix_decode_step``).
+
+    q, k ``[N, H, 96]``; v ``[N, H, 192]``; ``pool`` fp32 ``[P, H, 96, 192]`` (read only);
+    ``prefix_row`` ``[N]`` int32: the pool row each sequence continues (best sorted: neighbours with
+    one row share its read); ``tail`` a :class:`GlaTail` with ``tail_len`` ``[N]`` int32 tokens in
+    row ``tail_slot[n]`` (None: row n).  Returns ``o [N, H, 192]`` and writes k, v to place
+    ``tail_len[n]``; the caller advances ``tail_len``."""
+    lib = load_library()
+    dev = q.device
+    dt = _dtype_code(q)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(t, name, q.dtype, dev)
+    if q.dim() != 3 or q.shape[2] != DK or k.shape != q.shape or v.shape != (*q.shape[:2], DV):
+        raise ValueError("expected q, k [N, H, 96] and v [N, H, 192]")
+    N, H = q.shape[:2]
+    _need(log_lambda, "log_lambda", torch.float32, dev, H)
+    _pool(pool, H, dev)
+    ct = _tail(tail, H, q.dtype, dev)
+    for name, t in (("prefix_row", prefix_row), ("tail_len", tail_len), ("tail_slot", tail_slot)):
+        _index(t, name, N, dev)
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    _need(o, "o", v.dtype, dev, v.numel())
+    s = float(DK ** -0.5) if scale is None else float(scale)
+    with torch.cuda.device(dev):
+        rc = lib.gla_prefix_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_lambda), s, _ptr(pool), pool.shape[0],
+                                        _ptr(prefix_row), ctypes.byref(ct), _ptr(tail_slot), _ptr(tail_len), _ptr(o),
+                                        N, H, DK, DV, dt, _stream(dev))
+    _check(rc, "gla_prefix_decode_step")
+    return o
+
+
+def _packed_kv(k, v):
+    if k.dim() != 3 or k.shape[2] != DK or v.shape != (*k.shape[:2], DV):
+        raise ValueError("expected packed k [T, H, 96] and v [T, H, 192]")
+    return k.shape[:2]
+
+
+def gla_tail_append(k, v, tail, pos, cu_seqlens, tail_slot=None):
+    """Writes packed tokens (k ``[T, H, 96]``, v ``[T, H, 192]``, offsets ``cu_seqlens``) to the
+    tails: sequence n's to places ``pos[n]``, ``pos[n] + 1``, ... of row ``tail_slot[n]`` (None: row
+    n), quantised where the tail is MXFP8."""
+    lib = load_library()
+    dev = k.device
+    dt = _dtype_code(k)
+    _need(k, "k", k.dtype, dev)
+    _need(v, "v", k.dtype, dev)
+    T, H = _packed_kv(k, v)
+    ct = _tail(tail, H, k.dtype, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    n_seq = cu_seqlens.numel() - 1
+    _index(pos, "pos", n_seq, dev)
+    _index(tail_slot, "tail_slot", n_seq, dev)
+    with torch.cuda.device(dev):
+        rc = lib.gla_tail_append(_ptr(k), _ptr(v), ctypes.byref(ct), _ptr(tail_slot), _ptr(pos), _ptr(cu_seqlens),
+                                 n_seq, T, H, DK, DV, dt, _stream(dev))
+    _check(rc, "gla_tail_append")
+
+
+def gla_tail_read(tail, pos, cu_seqlens, T, tail_slot=None, dtype=None, k=None, v=None):
+    """The tokens at places ``pos[n]``, ``pos[n] + 1``, ... of the tails as packed ``(k [T, H, 96],
+    v [T, H, 192])`` with offsets ``cu_seqlens`` (``T`` their total), the reverse of
+    :func:`gla_tail_append`.  ``dtype`` of the results: bfloat16 or float32 (default: the tail's
+    own type, bfloat16 for MXFP8; a plain tail is read in its own type)."""
+    lib = load_library()
+    dev = tail[0].device
+    mx = tail[2] is not None
+    if dtype is None:
+        dtype = k.dtype if k is not None else (torch.bfloat16 if mx else tail[0].dtype)
+    H, T = tail[0].shape[1], int(T)
+    ct = _tail(tail, H, dtype, dev)
+    k = torch.empty((T, H, DK), dtype=dtype, device=dev) if k is None else k
+    v = torch.empty((T, H, DV), dtype=dtype, device=dev) if v is None else v
+    dt = _dtype_code(k)
+    _need(k, "k", dtype, dev, T * H * DK)
+    _need(v, "v", dtype, dev, T * H * DV)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    n_seq = cu_seqlens.numel() - 1
+    _index(pos, "pos", n_seq, dev)
+    _index(tail_slot, "tail_slot", n_seq, dev)
+    with torch.cuda.device(dev):
+        rc = lib.gla_tail_read(ctypes.byref(ct), _ptr(tail_slot), _ptr(pos), _ptr(cu_seqlens), _ptr(k), _ptr(v),
+                               n_seq, T, H, DK, DV, dt, _stream(dev))
+    _check(rc, "gla_tail_read")
+    return k, v
+
+
+def gla_tail_fold(log_lambda, pool, prefix_row, tail, tail_len, out=None, out_row=None, tail_slot=None):
+    """Folds each sequence's tail into a state of its own (``gla_tail_fold``):
+    ``out[out_row[n]] = lambda^L pool[prefix_row[n]] + sum_j lambda^(L-1-j) k_j v_j^T`` with
+    L = ``tail_len[n]``.  ``out`` fp32 ``[P', H, 96, 192]`` (None: a new ``[N, H, 96, 192]``; may be
+    ``pool`` itself, see the header), ``out_row`` None: row n.  Returns ``out``."""
+    lib = load_library()
+    dev = pool.device
+    H = log_lambda.numel()
+    _need(log_lambda, "log_lambda", torch.float32, dev)
+    _pool(pool, H, dev)
+    et = tail[0].dtype if tail[2] is None else torch.bfloat16
+    if et not in (torch.bfloat16, torch.float32):
+        raise TypeError("a tail without scales must be bfloat16 or float32")
+    ct = _tail(tail, H, et, dev)
+    N = prefix_row.numel()
+    for name, t in (("prefix_row", prefix_row), ("tail_len", tail_len), ("tail_slot", tail_slot), ("out_row", out_row)):
+        _index(t, name, N, dev)
+    if out is None:
+        if out_row is not None:
+            raise ValueError("out_row needs out")
+        out = torch.empty((N, H, DK, DV), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.float32, dev)
+    if out.dim() != 4 or out.shape[1:] != (H, DK, DV):
+        raise ValueError("out must be [P, H, 96, 192]")
+    with torch.cuda.device(dev):
+        rc = lib.gla_tail_fold(_ptr(log_lambda), _ptr(pool), pool.shape[0], _ptr(prefix_row), ctypes.byref(ct),
+                               _ptr(tail_slot), _ptr(tail_len), _ptr(out), out.shape[0], _ptr(out_row), N, H, DK, DV,
+                               GLA_F32 if et == torch.float32 else GLA_BF16, _stream(dev))
+    _check(rc, "gla_tail_fold")
+    return out
+
+
+def gla_prefix_fwd(q, k, v, log_lambda, pool, prefix_row, cu_seqlens, scale=None, output_final_state: bool = True,
+                   o=None, hT=None, workspace=None):
+    """Chunked forward of packed sequences that continue shared states (``gla_prefix_fwd``): as
+    :func:`gla_chunk_fwd` with ``cu_seqlens``, sequence n starting from ``pool[prefix_row[n]]``
+    (``pool`` fp32 ``[P, H, 96, 192]``, ``prefix_row`` ``[n_seq]`` int32, rows may repeat).  Returns
+    ``(o, hT)``."""
+    lib = load_library()
+    dev = q.device
+    dt = _dtype_code(q)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(t, name, q.dtype, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    n_seq, T, H = _layout(q, k, v, cu_seqlens)
+    _need(log_lambda, "log_lambda", torch.float32, dev, H)
+    _pool(pool, H, dev)
+    _need(prefix_row, "prefix_row", torch.int32, dev, n_seq)
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    _need(o, "o", v.dtype, dev, v.numel())
+    if output_final_state and hT is None:
+        hT = torch.empty((n_seq, H, DK, DV), dtype=torch.float32, device=dev)
+    if hT is not None:
+        _need(hT, "hT", torch.float32, dev, n_seq * H * DK * DV)
+    ws, ws_bytes = _workspace(cu_seqlens, n_seq, H, dev, workspace)
+    s = float(DK ** -0.5) if scale is None else float(scale)
+    with torch.cuda.device(dev):
+        rc = lib.gla_prefix_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_lambda), _ptr(pool), pool.shape[0],
+                                _ptr(prefix_row), s, _ptr(o), _ptr(hT), _ptr(cu_seqlens), n_seq, T, H, DK, DV, dt,
+                                _ptr(ws), ws_bytes, _stream(dev))
+    _check(rc, "gla_prefix_fwd")
+    return o, hT
+
+
+def gla_prefix_bwd_workspace_bytes(n_seq: int, T: int, H: int, dtype_code: int) -> int:
+    return int(load_library().gla_prefix_bwd_workspace_bytes(int(n_seq), int(T), int(H), int(dtype_code)))
+
+
+def gla_prefix_bwd(q, k, v, log_lambda, dO, pool, prefix_row, cu_seqlens, scale=None, dhT=None,
+                   need_dpool: bool = True, workspace=None, dq=None, dk=None, dv=None, dpool=None):
+    """Backward of :func:`gla_prefix_fwd` (``gla_prefix_bwd``).  Returns ``(dq, dk, dv, dpool)``;
+    ``dpool`` has the shape of ``pool``: row p is the sum of the initial-state gradients of the
+    sequences that continue p, in their order, zeros where none does (None if not requested)."""
+    lib = load_library()
+    dev = q.device
+    dt = _dtype_code(q)
+    for name, t in (("q", q), ("k", k), ("v", v), ("dO", dO)):
+        _need(t, name, q.dtype, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    n_seq, T, H = _layout(q, k, v, cu_seqlens)
+    if dO.shape != v.shape:
+        raise ValueError("dO must have the shape of v")
+    _need(log_lambda, "log_lambda", torch.float32, dev, H)
+    _pool(pool, H, dev)
+    _need(prefix_row, "prefix_row", torch.int32, dev, n_seq)
+    if dhT is not None:
+        _need(dhT, "dhT", torch.float32, dev)
+        if dhT.shape != (n_seq, H, DK, DV):
+            raise ValueError("dhT must be [n_seq, H, 96, 192]")
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=v.dtype, device=dev) if dv is None else dv
+    if dpool is None and need_dpool:
+        dpool = torch.empty(pool.shape, dtype=torch.float32, device=dev)
+    for name, t, ref in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _need(t, name, q.dtype, dev, ref.numel())
+    if dpool is not None:
+        _need(dpool, "dpool", torch.float32, dev, pool.numel())
+    if workspace is None:
+        workspace = torch.empty(gla_prefix_bwd_workspace_bytes(n_seq, T, H, dt), dtype=torch.uint8, device=dev)
+    s = float(DK ** -0.5) if scale is None else float(scale)
+    with torch.cuda.device(dev):
+        rc = lib.gla_prefix_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_lambda), _ptr(pool), pool.shape[0],
+                                _ptr(prefix_row), s, _ptr(dO), _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dpool),
+                                _ptr(cu_seqlens), n_seq, T, H, DK, DV, dt, _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), _stream(dev))
+    _check(rc, "gla_prefix_bwd")
+    return dq, dk, dv, dpool
+
 
 
 def gla_get_device_error(device=None) -> int:

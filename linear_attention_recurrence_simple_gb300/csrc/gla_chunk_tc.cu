@@ -369,7 +369,7 @@ struct TmaMaps {
 // initial state, the final-state output, and the output (bf16 rows, or fp32 partial sums).
 struct ScanParams {
   ChunkArgs a;
-  const float* s0;  // [n_seq, H, 96, 192] initial state (h0 or dhT), or null = zeros
+  const float* s0;  // [n_seq, H, 96, 192] initial state (h0, by row a.h0_row[n] if given, or dhT), or null = zeros
   float* s_out;     // final state (hT or dh0), or null
   void* out;        // FWD / DV: bf16 [T, H, 192];  DQ / DK: fp32 [T, H, 96] accumulator
   int balanced = 0;  // chunk ranges split evenly over the CTAs (forward, equal lengths, s_out given)
@@ -1018,15 +1018,22 @@ __global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1) tc_scan_kernel(const __
                S[4 * x + 3] = __uint_as_float(v.w);
              }
            }
-         } else if (prm.s0 && r_ < DK && GLA_IN_BOUNDS(srow0 + r_ < state_rows && col0 + TN <= DV, a.err)) {
-           const float4* src = reinterpret_cast<const float4*>(prm.s0 + ((long long)srow0 + r_) * DV + col0);
+         } else if (prm.s0 && r_ < DK) {
+           // (h0_row is for the initial states; the reverse scans start from dhT, row n)
+           const int row_in = C::REVERSE ? w.n : h0_row_of(a, w.n);
+           const long long srow = ((long long)row_in * a.H + h) * DK + r_;
+           if (row_in >= 0 &&
+               GLA_IN_BOUNDS(srow < (a.h0_row && !C::REVERSE ? (long long)a.h0_rows * a.H * DK : state_rows) &&
+                                 col0 + TN <= DV, a.err)) {
+             const float4* src = reinterpret_cast<const float4*>(prm.s0 + srow * DV + col0);
 #pragma unroll
-           for (int x = 0; x < TN / 4; ++x) {
-             const float4 v4 = src[x];
-             S[4 * x] = v4.x;
-             S[4 * x + 1] = v4.y;
-             S[4 * x + 2] = v4.z;
-             S[4 * x + 3] = v4.w;
+             for (int x = 0; x < TN / 4; ++x) {
+               const float4 v4 = src[x];
+               S[4 * x] = v4.x;
+               S[4 * x + 1] = v4.y;
+               S[4 * x + 2] = v4.z;
+               S[4 * x + 3] = v4.w;
+             }
            }
          }
        }

@@ -25,6 +25,8 @@ struct ChunkArgs {
   const void* dO;          // backward only
   const float* log_lambda;
   const float* h0;         // may be null
+  const int32_t* h0_row;   // row of h0 that each sequence starts from (rows may repeat), or null: row n
+  int h0_rows;             // rows of h0 (used with h0_row only)
   const float* aug;        // forward only: aug_balance [H, 96] (self-augmentation), or null
   const float* dhT;        // backward only; may be null
   void* o;                 // forward output (or dq in the backward)
@@ -94,6 +96,16 @@ __device__ __forceinline__ void seq_range(const ChunkArgs& a, int n, long long& 
     begin = (long long)n * a.T;
     end = begin + a.T;
   }
+}
+
+// Row of the initial states that sequence n starts from.  A row outside [0, h0_rows) records
+// ERR_SHAPE and gives -1: the sequence then starts from zeros.
+__device__ __forceinline__ int h0_row_of(const ChunkArgs& a, int n) {
+  if (!a.h0_row) return n;
+  const int row = a.h0_row[n];
+  if (row >= 0 && row < a.h0_rows) return row;
+  raise_error(a.err, ERR_SHAPE);
+  return -1;
 }
 
 // Splits a 1-D work-unit index into (sequence, head, tile) with the sequence slowest, so that

@@ -141,11 +141,13 @@ __global__ void __launch_bounds__(NT, 2) simt_wide_kernel(ChunkArgs a) {
   const float* s0 = REVERSE ? a.dhT : a.h0;
   const bool aug = !REVERSE && a.aug;
   const long long sbase = ((long long)n * a.H + h) * DK * DV;
+  const int row_in = REVERSE ? n : h0_row_of(a, n);  // row of s0 that the scan starts from
+  const long long s0base = ((long long)row_in * a.H + h) * DK * DV;
 
   fill_powers(pw, a.log_lambda[h]);
   for (int e = tid; e < DK * FWD_TILE; e += NT) {
     const int r = e / FWD_TILE, c = e % FWD_TILE;
-    Ss[r * VP + c] = s0 ? s0[sbase + (long long)r * DV + col0 + c] : 0.f;
+    Ss[r * VP + c] = s0 && row_in >= 0 ? s0[s0base + (long long)r * DV + col0 + c] : 0.f;
   }
   __syncthreads();
 
@@ -364,11 +366,13 @@ __global__ void __launch_bounds__(NT, 1) simt_bwd_narrow_kernel(ChunkArgs a) {
   T* out = (T*)(REVERSE ? a.dk : a.o);
   const float* s0 = REVERSE ? a.dhT : a.h0;
   const long long sbase = ((long long)n * a.H + h) * DK * DV;
+  const int row_in = REVERSE ? n : h0_row_of(a, n);  // row of s0 that the scan starts from
+  const long long s0base = ((long long)row_in * a.H + h) * DK * DV;
 
   fill_powers(pw, a.log_lambda[h]);
   for (int e = tid; e < BQ_TILE * DV; e += NT) {
     const int r = e / DV, c = e % DV;
-    Ss[r * XP + c] = s0 ? s0[sbase + (long long)(row0 + r) * DV + c] : 0.f;
+    Ss[r * XP + c] = s0 && row_in >= 0 ? s0[s0base + (long long)(row0 + r) * DV + c] : 0.f;
   }
   __syncthreads();
   const long long nchunks = (te - tb + SC - 1) / SC;
