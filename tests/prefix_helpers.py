@@ -51,7 +51,7 @@ class Tails:
         if self.fmt == "mxfp8":
             return gla.GlaTail(*(torch.from_numpy(x.copy()).to(dev) for x in (self.kc, self.vc, self.ks, self.vs)))
         dt = torch.bfloat16 if self.bf16 else torch.float32
-        return gla.GlaTail(torch.from_numpy(self.k).to(dev).to(dt), torch.from_numpy(self.v).to(dev).to(dt))
+        return gla.GlaTail(torch.from_numpy(self.k).to(dt).to(dev), torch.from_numpy(self.v).to(dt).to(dev))  # (converted on the host: one NaN pattern)
 
 
 def ref_decode(q, k, v, ll, scale, pool, prefix_row, tk, tv, slots, lens):

@@ -101,7 +101,8 @@ def bits(x):
 
 def same_tails(tail, want):
     for x, y in zip([x for x in tail if x is not None], want):
-        assert torch.equal(bits(x.cpu()), bits(y))
+        differ = (bits(x.cpu()) != bits(y)).nonzero()
+        assert differ.numel() == 0, differ[:4].tolist()
 
 
 def check_decode(c, o=None):
@@ -364,8 +365,6 @@ def test_packed_gradients_against_differences():
     for name, grad in (("pool", dpool), ("v", dv), ("q", dq)):
         step = torch.from_numpy(gs.normal(441, 1, tuple(grad.shape), 0.5)).cuda()
         (a, ma), (b, mb) = out(**{name: g[name] + step}), out(**{name: g[name] - step})
-        if name in ("q", "v"):
-            pass  # o and hT are linear in v, o in q (hT does not depend on it): the differences are exact too
         want = float((grad.double() * step.double()).sum())
         assert abs((a - b) / 2 - want) <= 2.0 ** -18 * (ma + mb), name
 
