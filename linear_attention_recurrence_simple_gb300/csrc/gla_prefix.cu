@@ -9,6 +9,7 @@
 // write) per (sequence, head); this form reads every shared state once for all its sequences and
 // 576 bytes (bf16) or 297 (MXFP8) per tail token.
 #include <algorithm>
+#include <atomic>
 
 #include "gla_tail.cuh"
 
@@ -38,7 +39,7 @@ __device__ __forceinline__ float tail_value(const TailArgs& t, long long token, 
   }
 }
 
-// One CTA per (sequence, head).
+// fp32 calls.  One CTA per (sequence, head).
 template <class T, bool MX>
 __global__ void __launch_bounds__(DEC_THREADS)
 prefix_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
@@ -104,6 +105,505 @@ prefix_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* 
   }
   acc = fmaf(s_self, to_f(v[nh * DV + tid]), acc);
   store_out(o + nh * DV + tid, scale * acc);
+}
+
+// ---- bf16 calls: tiles of sequences, tensor cores ----------------------------------------------
+// One CTA per (tile of up to 16 consecutive sequences, head).
+//   Shared states: for every run of equal prefix rows in the tile, [16 x 96] q times [96 x 192] S with
+//     mma.m16n8k16 (bf16, fp32 sums), S split into hi + lo bf16 as it is read (16 significant bits; a
+//     single bf16 would put 2^-9 into every term).  A warp owns 48 columns; the S fragments go from
+//     global memory (L2 for all but one tile) to registers, nothing is staged.
+//   Tails: 16-token chunks, in order, of all the tile's sequences form one list that is cut evenly
+//     over the warps, so one long tail among short ones, or a tile of one sequence, still feeds
+//     all of them.  A warp streams its chunks through a ring of its own in shared memory (bulk
+//     copies: the tokens of a (row, head) are contiguous) and multiplies on the tensor cores:
+//       weights   K [16 tokens x 96] times q (one column of N = 8 used): exact products.  E4M3 codes
+//                 widen exactly to f16; q is brought to f16 by a power of two (its 8 bits fit; what
+//                 lies 2^-35 below the largest is lost).  Block scales enter in fp32, per 32 columns.
+//       output    w [16 x 16 tokens] times V [16 tokens x 192].  bf16 tails: row 0 of w holds the high
+//                 bf16 of the weight, row 8 the low one.  MXFP8: rows b and b + 8 hold the high and
+//                 low f16 of w_j 2^(e_jb), the weight times the scale of column block b, so that the
+//                 codes enter unscaled; each row is kept in f16's range by a power of two of its own,
+//                 raised (and the sums rescaled) when a weight outgrows it.
+//     A sequence whose chunks fall to one warp is added to the tile's sums directly; the first and
+//     last sequence of a warp's range may be shared, and those parts meet in warp order.
+constexpr int TILE_MAX = 16;
+constexpr int PD_WARPS = 4, PD_THREADS = 32 * PD_WARPS;
+constexpr int PD_TOK = 16;  // tokens of a chunk
+
+template <bool MX>
+struct PdStage {
+  static constexpr uint32_t K_ROW = MX ? DK : 2 * DK, V_ROW = MX ? DV : 2 * DV;  // bytes of a token
+  static constexpr uint32_t K = 0, V = K + PD_TOK * K_ROW, KS = V + PD_TOK * V_ROW, VS = KS + (MX ? 48 : 0);
+  static constexpr uint32_t BYTES = VS + (MX ? 96 : 0);
+  static constexpr int N = MX ? 3 : 2;  // stages of a warp's ring
+};
+template <bool MX>
+struct PdSmem {
+  static constexpr uint32_t O = PD_WARPS * PdStage<MX>::N * PdStage<MX>::BYTES;  // [16][192] sums
+  static constexpr uint32_t PART = O + TILE_MAX * DV * 4;                        // [warps][2][192]
+  static constexpr uint32_t BAR = PART + PD_WARPS * 2 * DV * 4;
+  static constexpr uint32_t BYTES = BAR + PD_WARPS * PdStage<MX>::N * 8;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_h(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// (x, y) as hi + lo bf16 pairs.
+__device__ __forceinline__ void split_bf(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf(x, y);
+  lo = pack_bf(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+}
+__device__ __forceinline__ void split_h(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_h(x - f.x, y - f.y);
+}
+// Two E4M3 codes to an f16 pair (exact; a NaN code stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
+  return r;
+}
+__device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+template <bool MX>
+__global__ void __launch_bounds__(PD_THREADS, MX ? 3 : 2)
+prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
+                          const __nv_bfloat16* __restrict__ v, const float* __restrict__ log_lambda, float scale,
+                          const float* __restrict__ pool, int pool_rows, const int32_t* __restrict__ prefix_row, TailArgs t,
+                          __nv_bfloat16* __restrict__ o, int N, int H, int tile_seqs, unsigned* err,
+                          unsigned long long wait_ns) {
+  using ST = PdStage<MX>;
+  using SM = PdSmem<MX>;
+  using BF = __nv_bfloat16;
+  extern __shared__ __align__(128) uint8_t pd_smem[];
+  __shared__ int s_row[TILE_MAX], s_len[TILE_MAX], s_cu[TILE_MAX + 1], s_part[2 * PD_WARPS];
+  __shared__ long long s_tok0[TILE_MAX];
+  __shared__ float s_self[TILE_MAX];
+  __shared__ int s_abort;
+  float* sO = reinterpret_cast<float*>(pd_smem + SM::O);
+  float* sPart = reinterpret_cast<float*>(pd_smem + SM::PART);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  uint64_t* full = reinterpret_cast<uint64_t*>(pd_smem + SM::BAR) + warp * ST::N;
+  const int h = (int)(blockIdx.x % (unsigned)H), n0 = (int)(blockIdx.x / (unsigned)H) * tile_seqs;
+  const int cnt = min(tile_seqs, N - n0);
+  if (warp == 0) {
+    int row = -1, L = -1;
+    long long tok0 = -1;
+    if (lane < cnt) {
+      row = prefix_row[n0 + lane];
+      tok0 = tail_token0(t, n0 + lane, H, h, 1, L, err);
+      if (row < 0 || row >= pool_rows) {
+        raise_error(err, ERR_SHAPE);
+        row = -1;
+      }
+      if (tok0 < 0) row = -1;  // row -1: the sequence is skipped
+    }
+    int chunks = row >= 0 ? (L + PD_TOK - 1) / PD_TOK : 0;
+    if (lane < TILE_MAX) {
+      s_row[lane] = row;
+      s_len[lane] = L;
+      s_tok0[lane] = tok0;
+    }
+#pragma unroll
+    for (int d = 1; d < TILE_MAX; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, chunks, d);
+      if (lane >= d) chunks += up;
+    }
+    if (lane < TILE_MAX) s_cu[lane + 1] = chunks;
+    if (lane == 0) {
+      s_cu[0] = 0;
+      s_abort = 0;
+    }
+  }
+  if (lane == 0) {
+    for (int i = 0; i < ST::N; ++i) mbar_init(&full[i], 1);
+    s_part[2 * warp] = s_part[2 * warp + 1] = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  // ---- this warp's chunks [c0, c1) of the tile's list; the ring's first loads
+  const long long total = s_cu[TILE_MAX];
+  const int c0 = (int)(total * warp / PD_WARPS), c1 = (int)(total * (warp + 1) / PD_WARPS);
+  const uint32_t ring = smem_u32(pd_smem) + (uint32_t)(warp * ST::N) * ST::BYTES;
+  uint8_t* const ring_p = pd_smem + (size_t)(warp * ST::N) * ST::BYTES;
+  int issue_i = 0;  // (lane 0) sequence of the next chunk to load
+  auto issue = [&](int c) {
+    while (c >= s_cu[issue_i + 1]) ++issue_i;
+    const int j0 = (c - s_cu[issue_i]) * PD_TOK, m = min(PD_TOK, s_len[issue_i] - j0);
+    const long long tok = s_tok0[issue_i] + j0;
+    const int s = (c - c0) % ST::N;
+    const uint32_t dst = ring + (uint32_t)s * ST::BYTES;
+    const uint32_t ks = MX ? (uint32_t)(3 * m + 15) / 16 * 16 : 0, vs = MX ? (uint32_t)(6 * m + 15) / 16 * 16 : 0;
+    mbar_expect_tx(&full[s], (uint32_t)m * (ST::K_ROW + ST::V_ROW) + ks + vs);
+    bulk_copy(dst + ST::K, static_cast<const uint8_t*>(t.k) + tok * ST::K_ROW, (uint32_t)m * ST::K_ROW, &full[s]);
+    bulk_copy(dst + ST::V, static_cast<const uint8_t*>(t.v) + tok * ST::V_ROW, (uint32_t)m * ST::V_ROW, &full[s]);
+    if (MX) {
+      bulk_copy(dst + ST::KS, t.ks + tok * (DK / 32), ks, &full[s]);
+      bulk_copy(dst + ST::VS, t.vs + tok * (DV / 32), vs, &full[s]);
+    }
+  };
+  int issued = 0;
+  if (lane == 0)
+    for (; issued < ST::N && c0 + issued < c1; ++issued) issue(c0 + issued);
+  __syncwarp();
+
+  const float ll = log_lambda[h];
+  // ---- the new tokens: q . k, and their places in the tails
+  for (int i = warp; i < cnt; i += PD_WARPS) {
+    if (s_row[i] < 0) continue;
+    const long long nh = (long long)(n0 + i) * H + h;
+    float x[16] = {};
+    float d = 0.f;
+    if (lane < DK / 16) {
+      float y[16];
+      load16(k + nh * DK + 16 * lane, x);
+      load16(q + nh * DK + 16 * lane, y);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) d = fmaf(x[e], y[e], d);
+    }
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (lane == 0) s_self[i] = d;
+    const long long at = s_tok0[i] + s_len[i];
+    tail_store16<BF, MX, DK>(t.k, t.ks, at, lane, x, lane < DK / 16);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    if (lane < DV / 16) load16(v + nh * DV + 16 * lane, x);
+    tail_store16<BF, MX, DV>(t.v, t.vs, at, lane, x, lane < DV / 16);
+  }
+
+  // ---- the shared states
+  {
+    // q fragments; K step s of thread tq: columns 16 s + 4 tq .. + 3 (the same order as S's rows)
+    uint2 qa[6], qb[6];
+    const BF* q0 = q + ((long long)(n0 + g) * H + h) * DK + 4 * tq;
+    const BF* q1 = q + ((long long)(n0 + g + 8) * H + h) * DK + 4 * tq;
+#pragma unroll
+    for (int s = 0; s < 6; ++s) {
+      qa[s] = g < cnt ? *reinterpret_cast<const uint2*>(q0 + 16 * s) : make_uint2(0u, 0u);
+      qb[s] = g + 8 < cnt ? *reinterpret_cast<const uint2*>(q1 + 16 * s) : make_uint2(0u, 0u);
+    }
+    const float f0 = g < cnt && s_row[g] >= 0 ? decay_pow(ll, s_len[g] + 1) : 0.f;
+    const float f1 = g + 8 < cnt && s_row[g + 8] >= 0 ? decay_pow(ll, s_len[g + 8] + 1) : 0.f;
+    for (int r0 = 0; r0 < cnt;) {
+      const int row = s_row[r0];
+      int r1 = r0 + 1;
+      while (r1 < cnt && s_row[r1] == row) ++r1;
+      if (row >= 0) {
+        float d[6][4] = {};
+        const float* S = pool + ((long long)row * H + h) * (DK * DV) + 48 * warp;
+#pragma unroll
+        for (int s = 0; s < 6; ++s) {
+          float4 x[4];
+          float2 y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float* p = S + (16 * s + 4 * tq + e) * DV;
+            x[e] = *reinterpret_cast<const float4*>(p + 4 * g);
+            y[e] = *reinterpret_cast<const float2*>(p + 32 + 2 * g);
+          }
+          const uint32_t a[4] = {qa[s].x, qb[s].x, qa[s].y, qb[s].y};
+          auto col = [&](float (&dd)[4], float v0, float v1, float v2, float v3) {
+            uint32_t h0, l0, h1, l1;
+            split_bf(v0, v1, h0, l0);
+            split_bf(v2, v3, h1, l1);
+            mma_bf16(dd, a, h0, h1);
+            mma_bf16(dd, a, l0, l1);
+          };
+          col(d[0], x[0].x, x[1].x, x[2].x, x[3].x);
+          col(d[1], x[0].y, x[1].y, x[2].y, x[3].y);
+          col(d[2], x[0].z, x[1].z, x[2].z, x[3].z);
+          col(d[3], x[0].w, x[1].w, x[2].w, x[3].w);
+          col(d[4], y[0].x, y[1].x, y[2].x, y[3].x);
+          col(d[5], y[0].y, y[1].y, y[2].y, y[3].y);
+        }
+        // only this run's rows: a state's infinities and NaN stay with its own sequences
+#pragma unroll
+        for (int j = 0; j < 6; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = g + 8 * (e >> 1), nn = 2 * tq + (e & 1);
+            const int c = 48 * warp + (j < 4 ? 4 * nn + j : 32 + 2 * nn + (j - 4));
+            if (r >= r0 && r < r1) sO[r * DV + c] = d[j][e] * (e >> 1 ? f1 : f0);
+          }
+      }
+      r0 = r1;
+    }
+  }
+  __syncthreads();
+
+  // ---- the tails
+  bool ok = true;
+  int seq = 0;
+  for (int c = c0; c < c1 && ok;) {
+    while (c >= s_cu[seq + 1]) ++seq;
+    const int first = s_cu[seq], last = min(s_cu[seq + 1], c1), L = s_len[seq];
+    const bool whole = c == first && last == s_cu[seq + 1];
+    // q as the B operand: one column (n = 0, the lanes with g = 0); block b, K step u of thread tq:
+    // columns 32 b + 8 tq + 4 u .. + 3
+    uint32_t qf[3][4];
+    float qn = 1.f;  // what the weights are to be multiplied with
+    {
+      const BF* qr = q + ((long long)(n0 + seq) * H + h) * DK + 8 * tq;
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        const uint4 u = *reinterpret_cast<const uint4*>(qr + 32 * b);
+        qf[b][0] = u.x;
+        qf[b][1] = u.y;
+        qf[b][2] = u.z;
+        qf[b][3] = u.w;
+      }
+      if (MX) {
+        float m = 0.f;
+#pragma unroll
+        for (int b = 0; b < 3; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(qf[b][e] << 16)), fabsf(__uint_as_float(qf[b][e] & 0xFFFF0000u))));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e2 = max(exponent_of(m), -100) - 10;  // the largest comes to [2^10, 2^11)
+        const float inv = pow2i(-e2);
+        qn = pow2i(e2);
+#pragma unroll
+        for (int b = 0; b < 3; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            qf[b][e] = pack_h(__uint_as_float(qf[b][e] << 16) * inv, __uint_as_float(qf[b][e] & 0xFFFF0000u) * inv);
+      }
+#pragma unroll
+      for (int b = 0; b < 3; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qf[b][e] = g == 0 ? qf[b][e] : 0u;
+    }
+    float acc[24][4];
+#pragma unroll
+    for (int i = 0; i < 24; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    int E = -1000;  // (MXFP8) exponent of row g's power of two
+    for (; c < last; ++c) {
+      const int it = c - c0, s = it % ST::N;
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)(it / ST::N) & 1u, wait_ns, &s_abort));
+      if (!ok) break;
+      uint8_t* st = ring_p + (size_t)s * ST::BYTES;
+      const int j0 = (c - first) * PD_TOK, m = min(PD_TOK, L - j0);
+      if (m < PD_TOK) {
+        // rows past the tail's end hold another chunk's values or nothing: zero, so that their
+        // zero weights give zero
+        for (uint32_t e = lane; e < (uint32_t)(PD_TOK - m) * ST::V_ROW / 16; e += 32)
+          *reinterpret_cast<uint4*>(st + ST::V + (uint32_t)m * ST::V_ROW + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
+      // weights: token g in lanes tq = 0, element 0; token g + 8, element 2
+      float sc0 = 0.f, sc1 = 0.f;
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (MX) {
+          const uint2 x = *reinterpret_cast<const uint2*>(st + ST::K + (uint32_t)g * DK + 32 * b + 8 * tq);
+          const uint2 y = *reinterpret_cast<const uint2*>(st + ST::K + (uint32_t)(g + 8) * DK + 32 * b + 8 * tq);
+          const uint32_t a0[4] = {e4m3x2_to_h2(x.x & 0xFFFFu), e4m3x2_to_h2(y.x & 0xFFFFu), e4m3x2_to_h2(x.x >> 16),
+                                  e4m3x2_to_h2(y.x >> 16)};
+          const uint32_t a1[4] = {e4m3x2_to_h2(x.y & 0xFFFFu), e4m3x2_to_h2(y.y & 0xFFFFu), e4m3x2_to_h2(x.y >> 16),
+                                  e4m3x2_to_h2(y.y >> 16)};
+          mma_f16(d, a0, qf[b][0], qf[b][1]);
+          mma_f16(d, a1, qf[b][2], qf[b][3]);
+          sc0 = fmaf(d[0], e8m0_to_f(st[ST::KS + 3 * g + b]), sc0);
+          sc1 = fmaf(d[2], e8m0_to_f(st[ST::KS + 3 * (g + 8) + b]), sc1);
+        } else {
+          const uint4 x = *reinterpret_cast<const uint4*>(st + ST::K + (uint32_t)g * ST::K_ROW + 64 * b + 16 * tq);
+          const uint4 y = *reinterpret_cast<const uint4*>(st + ST::K + (uint32_t)(g + 8) * ST::K_ROW + 64 * b + 16 * tq);
+          const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+          mma_bf16(d, a0, qf[b][0], qf[b][1]);
+          mma_bf16(d, a1, qf[b][2], qf[b][3]);
+          sc0 += d[0];
+          sc1 += d[2];
+        }
+      }
+      // lane j < 16 takes token j's weight
+      const float from0 = __shfl_sync(0xffffffffu, sc0, (lane & 7) * 4), from1 = __shfl_sync(0xffffffffu, sc1, (lane & 7) * 4);
+      const float w = (lane & 15) < m ? ((lane & 8) ? from1 : from0) * qn * decay_pow(ll, L - j0 - (lane & 15)) : 0.f;
+      float wt[4];  // tokens tq, tq + 4, tq + 8, tq + 12
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wt[i] = __shfl_sync(0xffffffffu, w, tq + 4 * i);
+      uint32_t a[4];
+      if constexpr (MX) {
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = tq + 4 * i;
+          wt[i] = g < DV / 32 && j < m ? wt[i] * e8m0_to_f(st[ST::VS + 6 * j + (g < DV / 32 ? g : 0)]) : 0.f;
+          mx = fmaxf(mx, fabsf(wt[i]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int need = mx > 0.f ? max(exponent_of(mx), -120) : -1000;
+        const bool grow = need > E + 10;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = !grow ? 1.f : (E < -126 ? 0.f : pow2i(E - need));
+#pragma unroll
+          for (int i = 0; i < 24; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+          if (grow) E = need;
+        }
+        const float up = pow2i(4 - E);
+        split_h(wt[0] * up, wt[1] * up, a[0], a[1]);
+        split_h(wt[2] * up, wt[3] * up, a[2], a[3]);
+#pragma unroll
+        for (int B = 0; B < 3; ++B) {
+          uint2 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = *reinterpret_cast<const uint2*>(st + ST::V + (uint32_t)(tq + 4 * i) * DV + 64 * B + 8 * g);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t x0 = half ? x[0].y : x[0].x, x1 = half ? x[1].y : x[1].x, x2 = half ? x[2].y : x[2].x,
+                           x3 = half ? x[3].y : x[3].x;
+            const uint32_t p0 = __byte_perm(x0, x1, 0x5140), p1 = __byte_perm(x0, x1, 0x7362);
+            const uint32_t r0 = __byte_perm(x2, x3, 0x5140), r1 = __byte_perm(x2, x3, 0x7362);
+            mma_f16(acc[8 * B + 4 * half], a, e4m3x2_to_h2(p0 & 0xFFFFu), e4m3x2_to_h2(r0 & 0xFFFFu));
+            mma_f16(acc[8 * B + 4 * half + 1], a, e4m3x2_to_h2(p0 >> 16), e4m3x2_to_h2(r0 >> 16));
+            mma_f16(acc[8 * B + 4 * half + 2], a, e4m3x2_to_h2(p1 & 0xFFFFu), e4m3x2_to_h2(r1 & 0xFFFFu));
+            mma_f16(acc[8 * B + 4 * half + 3], a, e4m3x2_to_h2(p1 >> 16), e4m3x2_to_h2(r1 >> 16));
+          }
+        }
+      } else {
+        split_bf(wt[0], wt[1], a[0], a[1]);
+        split_bf(wt[2], wt[3], a[2], a[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = g == 0 ? a[e] : 0u;
+#pragma unroll
+        for (int B = 0; B < 3; ++B) {
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(st + ST::V + (uint32_t)(tq + 4 * i) * ST::V_ROW + 128 * B + 16 * g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x0 = e == 0 ? x[0].x : e == 1 ? x[0].y : e == 2 ? x[0].z : x[0].w;
+            const uint32_t x1 = e == 0 ? x[1].x : e == 1 ? x[1].y : e == 2 ? x[1].z : x[1].w;
+            const uint32_t x2 = e == 0 ? x[2].x : e == 1 ? x[2].y : e == 2 ? x[2].z : x[2].w;
+            const uint32_t x3 = e == 0 ? x[3].x : e == 1 ? x[3].y : e == 2 ? x[3].z : x[3].w;
+            mma_bf16(acc[8 * B + 2 * e], a, __byte_perm(x0, x1, 0x5410), __byte_perm(x2, x3, 0x5410));
+            mma_bf16(acc[8 * B + 2 * e + 1], a, __byte_perm(x0, x1, 0x7632), __byte_perm(x2, x3, 0x7632));
+          }
+        }
+      }
+      // the stage is read: refill it (the zeros above were written through the generic proxy)
+      if (m < PD_TOK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0 && c0 + issued < c1) {
+        issue(c0 + issued);
+        ++issued;
+      }
+    }
+    if (!ok) break;
+    // the sequence's sums (this warp's part of them)
+    const int part = 2 * warp + (last == c1 && c0 < first ? 1 : 0);
+    float* dst = whole ? sO + seq * DV : sPart + part * DV;
+    if (!whole && lane == 0) s_part[part] = seq;
+    const float back = MX ? pow2i(E - 4) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 24; ++i) {
+      const int B = i >> 3, jj = i & 7;
+      // MXFP8: column block 2 B + (tq >> 1) is row g of the product; bf16: row 0
+      if (MX ? g == 2 * B + (tq >> 1) : g == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = 64 * B + 8 * (2 * tq + e) + jj;
+          const float x = (acc[i][e] + acc[i][e + 2]) * back;
+          dst[col] = whole ? dst[col] + x : x;
+        }
+      }
+    }
+  }
+  if (!ok) {
+    // a wait gave up: no copy into this CTA's shared memory may be in flight when it exits
+    if (lane == 0) {
+      for (int i = 0; i < ST::N; ++i) {
+        const int n_i = (issued - i + ST::N - 1) / ST::N;  // loads that went through stage i
+        if (n_i > 0) mbar_wait_drain(&full[i], (uint32_t)(n_i - 1) & 1u, 1000000000ull, err);
+      }
+      raise_error(err, ERR_TIMEOUT);
+    }
+  }
+  __syncthreads();
+  if (s_abort) return;
+  // ---- shared parts in warp order, the new tokens, and out
+  for (int col = tid; col < DV; col += PD_THREADS)
+#pragma unroll
+    for (int p = 0; p < 2 * PD_WARPS; ++p)
+      if (s_part[p] >= 0) sO[s_part[p] * DV + col] += sPart[p * DV + col];
+  __syncthreads();
+  for (int e = tid; e < cnt * (DV / 2); e += PD_THREADS) {
+    const int i = e / (DV / 2), c = 2 * (e % (DV / 2));
+    if (s_row[i] < 0) continue;
+    const long long at = ((long long)(n0 + i) * H + h) * DV + c;
+    const uint32_t vv = *reinterpret_cast<const uint32_t*>(v + at);
+    const float2 x = *reinterpret_cast<const float2*>(sO + i * DV + c);
+    *reinterpret_cast<uint32_t*>(o + at) = pack_bf(scale * fmaf(s_self[i], __uint_as_float(vv << 16), x.x),
+                                                   scale * fmaf(s_self[i], __uint_as_float(vv & 0xFFFF0000u), x.y));
+  }
+}
+
+// Sequences of a tile: as many as leave two CTAs for every SM (16 sequences share one pass over a
+// state; fewer, when there are few, spread the tails over more SMs).
+int decode_tile(int N, int H, int sms) {
+  int ts = TILE_MAX;
+  while (ts > 1 && (long long)((N + ts - 1) / ts) * H < 2ll * sms) ts /= 2;
+  return ts;
+}
+
+template <bool MX>
+cudaError_t launch_decode_tile(const void* q, const void* k, const void* v, const float* log_lambda, float scale,
+                               const float* pool, int pool_rows, const int32_t* prefix_row, const TailArgs& t, void* o,
+                               int N, int H, unsigned* err, unsigned long long wait_ns, cudaStream_t s) {
+  static std::atomic<int> sms_of[64];  // per device: its SM count, once the kernel's shared memory is allowed
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int sms = dev < 64 ? sms_of[dev].load() : 0;
+  if (sms == 0) {
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(prefix_decode_tile_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)PdSmem<MX>::BYTES)) != cudaSuccess)
+      return e;
+    if (dev < 64) sms_of[dev].store(sms);
+  }
+  const int ts = decode_tile(N, H, sms);
+  const unsigned blocks = (unsigned)((N + ts - 1) / ts) * (unsigned)H;
+  using BF = __nv_bfloat16;
+  prefix_decode_tile_kernel<MX><<<blocks, PD_THREADS, PdSmem<MX>::BYTES, s>>>(
+      (const BF*)q, (const BF*)k, (const BF*)v, log_lambda, scale, pool, pool_rows, prefix_row, t, (BF*)o, N, H, ts, err,
+      wait_ns);
+  return cudaGetLastError();
 }
 
 // dpool[p] = sum of dh0[n] over the sequences n that started from row p, in the order of n (so the
@@ -183,20 +683,18 @@ int gla_prefix_decode_step(const void* q, const void* k, const void* v, const fl
   const unsigned blocks = (unsigned)N * (unsigned)H;
   const bool mx = tail->format == GLA_TAIL_MXFP8;
   cudaStream_t s = (cudaStream_t)stream;
-  using BF = __nv_bfloat16;
   using gla::DEC_THREADS;
   if (dtype == GLA_F32) {
     if (mx)
       gla::prefix_decode_kernel<float, true><<<blocks, DEC_THREADS, 0, s>>>((const float*)q, (const float*)k, (const float*)v, log_lambda, scale, pool, pool_rows, prefix_row, t, (float*)o, H, err);
     else
       gla::prefix_decode_kernel<float, false><<<blocks, DEC_THREADS, 0, s>>>((const float*)q, (const float*)k, (const float*)v, log_lambda, scale, pool, pool_rows, prefix_row, t, (float*)o, H, err);
-  } else {
-    if (mx)
-      gla::prefix_decode_kernel<BF, true><<<blocks, DEC_THREADS, 0, s>>>((const BF*)q, (const BF*)k, (const BF*)v, log_lambda, scale, pool, pool_rows, prefix_row, t, (BF*)o, H, err);
-    else
-      gla::prefix_decode_kernel<BF, false><<<blocks, DEC_THREADS, 0, s>>>((const BF*)q, (const BF*)k, (const BF*)v, log_lambda, scale, pool, pool_rows, prefix_row, t, (BF*)o, H, err);
+    return gla::to_status(cudaGetLastError());
   }
-  return gla::to_status(cudaGetLastError());
+  return gla::to_status(mx ? gla::launch_decode_tile<true>(q, k, v, log_lambda, scale, pool, pool_rows, prefix_row, t, o,
+                                                           N, H, err, wait_ns, s)
+                           : gla::launch_decode_tile<false>(q, k, v, log_lambda, scale, pool, pool_rows, prefix_row, t, o,
+                                                            N, H, err, wait_ns, s));
 }
 
 size_t gla_prefix_bwd_workspace_bytes(int n_seq, int T, int H, int dtype) {
