@@ -702,33 +702,67 @@ def gla_tail_alloc(rows: int, H: int, cap: int, dtype=torch.bfloat16, device="cu
     return GlaTail(z(DK), z(DV))
 
 
+# The calls below are made once per layer and token, where a microsecond on the host counts: their
+# checks are those of _need, which is entered (and says what is wrong) only when one fails.
+def _good(t, name, dtype, dev, numel=None):
+    if (type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != dev.index or not t.is_contiguous()
+            or (numel is not None and t.numel() != numel)):
+        _need(t, name, dtype, dev, numel)
+
+
+def _device_of(t, name):
+    """The CUDA device of a call's first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _need(t, name)
+    return t.device
+
+
+# The current stream's handle without a Stream object around it, where torch has that call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(fn, where, dev, *args):
+    """Calls the library with `dev` current, on its current stream."""
+    stream = _raw_stream(dev.index)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise GlaError(rc, where)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _tail(tail, H, dtype, dev):
     """Checks the tails' tensors and returns the C struct."""
     k, v, ks, vs = tail
     mx = ks is not None or vs is not None
     et = torch.uint8 if mx else dtype
-    _need(k, "tail.k", et, dev)
-    _need(v, "tail.v", et, dev)
-    if k.dim() != 4 or k.shape[1] != H or k.shape[3] != DK or v.shape != (*k.shape[:3], DV):
+    _good(k, "tail.k", et, dev)
+    _good(v, "tail.v", et, dev)
+    shape = tuple(k.shape)
+    if len(shape) != 4 or shape[1] != H or shape[3] != DK or tuple(v.shape) != shape[:3] + (DV,):
         raise ValueError("the tail must be k [R, H, cap, 96] and v [R, H, cap, 192]")
-    if mx:
-        _need(ks, "tail.k_scales", torch.uint8, dev)
-        _need(vs, "tail.v_scales", torch.uint8, dev)
-        if ks.shape != (*k.shape[:3], DK // 32) or vs.shape != (*k.shape[:3], DV // 32):
-            raise ValueError("tail scales must be [R, H, cap, 3] and [R, H, cap, 6]")
-    return _CTail(k.data_ptr(), v.data_ptr(), ks.data_ptr() if mx else None, vs.data_ptr() if mx else None,
-                  k.shape[0], k.shape[2], int(mx))
+    if not mx:
+        return _CTail(k.data_ptr(), v.data_ptr(), None, None, shape[0], shape[2], 0)
+    _good(ks, "tail.k_scales", torch.uint8, dev)
+    _good(vs, "tail.v_scales", torch.uint8, dev)
+    if tuple(ks.shape) != shape[:3] + (DK // 32,) or tuple(vs.shape) != shape[:3] + (DV // 32,):
+        raise ValueError("tail scales must be [R, H, cap, 3] and [R, H, cap, 6]")
+    return _CTail(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], 1)
 
 
-def _index(t, name, n, dev):
-    if t is not None:
-        _need(t, name, torch.int32, dev, n)
-
-
-def _pool(pool, H, dev):
-    _need(pool, "pool", torch.float32, dev)
-    if pool.dim() != 4 or pool.shape[1:] != (H, DK, DV):
-        raise ValueError("pool must be [P, H, 96, 192]")
+def _pool(pool, H, dev, name="pool"):
+    _good(pool, name, torch.float32, dev)
+    shape = tuple(pool.shape)
+    if len(shape) != 4 or shape[1:] != (H, DK, DV):
+        raise ValueError(f"{name} must be [P, H, 96, 192]")
+    return shape[0]
 
 
 def gla_prefix_decode_step(q, k, v, log_lambda, pool, prefix_row, tail, tail_len, tail_slot=None, scale=None, o=None):
@@ -739,56 +773,59 @@ def gla_prefix_decode_step(q, k, v, log_lambda, pool, prefix_row, tail, tail_len
     one row share its read); ``tail`` a :class:`GlaTail` with ``tail_len`` ``[N]`` int32 tokens in
     row ``tail_slot[n]`` (None: row n).  Returns ``o [N, H, 192]`` and writes k, v to place
     ``tail_len[n]``; the caller advances ``tail_len``."""
-    lib = load_library()
-    dev = q.device
-    dt = _dtype_code(q)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, q.dtype, dev)
-    if q.dim() != 3 or q.shape[2] != DK or k.shape != q.shape or v.shape != (*q.shape[:2], DV):
+    lib = _libs.get(_use_debug) or load_library()
+    dt, dtype = _dtype_code(q), q.dtype
+    dev = _device_of(q, "q")
+    _good(q, "q", dtype, dev)
+    _good(k, "k", dtype, dev)
+    _good(v, "v", dtype, dev)
+    shape = tuple(q.shape)
+    if len(shape) != 3 or shape[2] != DK or tuple(k.shape) != shape or tuple(v.shape) != shape[:2] + (DV,):
         raise ValueError("expected q, k [N, H, 96] and v [N, H, 192]")
-    N, H = q.shape[:2]
-    _need(log_lambda, "log_lambda", torch.float32, dev, H)
-    _pool(pool, H, dev)
-    ct = _tail(tail, H, q.dtype, dev)
-    for name, t in (("prefix_row", prefix_row), ("tail_len", tail_len), ("tail_slot", tail_slot)):
-        _index(t, name, N, dev)
+    N, H = shape[:2]
+    _good(log_lambda, "log_lambda", torch.float32, dev, H)
+    rows = _pool(pool, H, dev)
+    ct = _tail(tail, H, dtype, dev)
+    _good(prefix_row, "prefix_row", torch.int32, dev, N)
+    _good(tail_len, "tail_len", torch.int32, dev, N)
+    if tail_slot is not None:
+        _good(tail_slot, "tail_slot", torch.int32, dev, N)
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    _need(o, "o", v.dtype, dev, v.numel())
-    s = float(DK ** -0.5) if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        rc = lib.gla_prefix_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_lambda), s, _ptr(pool), pool.shape[0],
-                                        _ptr(prefix_row), ctypes.byref(ct), _ptr(tail_slot), _ptr(tail_len), _ptr(o),
-                                        N, H, DK, DV, dt, _stream(dev))
-    _check(rc, "gla_prefix_decode_step")
+        o = torch.empty_like(v)
+    else:
+        _good(o, "o", dtype, dev, N * H * DV)
+    _run(lib.gla_prefix_decode_step, "gla_prefix_decode_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         log_lambda.data_ptr(), DK ** -0.5 if scale is None else float(scale), pool.data_ptr(), rows,
+         prefix_row.data_ptr(), ctypes.byref(ct), _addr(tail_slot), tail_len.data_ptr(), o.data_ptr(), N, H, DK, DV, dt)
     return o
 
 
-def _packed_kv(k, v):
-    if k.dim() != 3 or k.shape[2] != DK or v.shape != (*k.shape[:2], DV):
-        raise ValueError("expected packed k [T, H, 96] and v [T, H, 192]")
-    return k.shape[:2]
+def _packed_offsets(cu_seqlens, pos, tail_slot, dev):
+    _good(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    n_seq = cu_seqlens.numel() - 1
+    _good(pos, "pos", torch.int32, dev, n_seq)
+    if tail_slot is not None:
+        _good(tail_slot, "tail_slot", torch.int32, dev, n_seq)
+    return n_seq
 
 
 def gla_tail_append(k, v, tail, pos, cu_seqlens, tail_slot=None):
     """Writes packed tokens (k ``[T, H, 96]``, v ``[T, H, 192]``, offsets ``cu_seqlens``) to the
     tails: sequence n's to places ``pos[n]``, ``pos[n] + 1``, ... of row ``tail_slot[n]`` (None: row
     n), quantised where the tail is MXFP8."""
-    lib = load_library()
-    dev = k.device
+    lib = _libs.get(_use_debug) or load_library()
     dt = _dtype_code(k)
-    _need(k, "k", k.dtype, dev)
-    _need(v, "v", k.dtype, dev)
-    T, H = _packed_kv(k, v)
+    dev = _device_of(k, "k")
+    _good(k, "k", k.dtype, dev)
+    _good(v, "v", k.dtype, dev)
+    shape = tuple(k.shape)
+    if len(shape) != 3 or shape[2] != DK or tuple(v.shape) != shape[:2] + (DV,):
+        raise ValueError("expected packed k [T, H, 96] and v [T, H, 192]")
+    T, H = shape[:2]
     ct = _tail(tail, H, k.dtype, dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    n_seq = cu_seqlens.numel() - 1
-    _index(pos, "pos", n_seq, dev)
-    _index(tail_slot, "tail_slot", n_seq, dev)
-    with torch.cuda.device(dev):
-        rc = lib.gla_tail_append(_ptr(k), _ptr(v), ctypes.byref(ct), _ptr(tail_slot), _ptr(pos), _ptr(cu_seqlens),
-                                 n_seq, T, H, DK, DV, dt, _stream(dev))
-    _check(rc, "gla_tail_append")
+    n_seq = _packed_offsets(cu_seqlens, pos, tail_slot, dev)
+    _run(lib.gla_tail_append, "gla_tail_append", dev, k.data_ptr(), v.data_ptr(), ctypes.byref(ct), _addr(tail_slot),
+         pos.data_ptr(), cu_seqlens.data_ptr(), n_seq, T, H, DK, DV, dt)
 
 
 def gla_tail_read(tail, pos, cu_seqlens, T, tail_slot=None, dtype=None, k=None, v=None):
@@ -796,26 +833,24 @@ def gla_tail_read(tail, pos, cu_seqlens, T, tail_slot=None, dtype=None, k=None, 
     v [T, H, 192])`` with offsets ``cu_seqlens`` (``T`` their total), the reverse of
     :func:`gla_tail_append`.  ``dtype`` of the results: bfloat16 or float32 (default: the tail's
     own type, bfloat16 for MXFP8; a plain tail is read in its own type)."""
-    lib = load_library()
-    dev = tail[0].device
-    mx = tail[2] is not None
+    lib = _libs.get(_use_debug) or load_library()
+    dev = _device_of(tail[0], "tail.k")
     if dtype is None:
-        dtype = k.dtype if k is not None else (torch.bfloat16 if mx else tail[0].dtype)
+        dtype = k.dtype if k is not None else (torch.bfloat16 if tail[2] is not None else tail[0].dtype)
+    if tail[0].dim() != 4:
+        raise ValueError("the tail must be k [R, H, cap, 96] and v [R, H, cap, 192]")
     H, T = tail[0].shape[1], int(T)
     ct = _tail(tail, H, dtype, dev)
-    k = torch.empty((T, H, DK), dtype=dtype, device=dev) if k is None else k
-    v = torch.empty((T, H, DV), dtype=dtype, device=dev) if v is None else v
+    if k is None:
+        k = torch.empty((T, H, DK), dtype=dtype, device=dev)
+    if v is None:
+        v = torch.empty((T, H, DV), dtype=dtype, device=dev)
     dt = _dtype_code(k)
-    _need(k, "k", dtype, dev, T * H * DK)
-    _need(v, "v", dtype, dev, T * H * DV)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    n_seq = cu_seqlens.numel() - 1
-    _index(pos, "pos", n_seq, dev)
-    _index(tail_slot, "tail_slot", n_seq, dev)
-    with torch.cuda.device(dev):
-        rc = lib.gla_tail_read(ctypes.byref(ct), _ptr(tail_slot), _ptr(pos), _ptr(cu_seqlens), _ptr(k), _ptr(v),
-                               n_seq, T, H, DK, DV, dt, _stream(dev))
-    _check(rc, "gla_tail_read")
+    _good(k, "k", dtype, dev, T * H * DK)
+    _good(v, "v", dtype, dev, T * H * DV)
+    n_seq = _packed_offsets(cu_seqlens, pos, tail_slot, dev)
+    _run(lib.gla_tail_read, "gla_tail_read", dev, ctypes.byref(ct), _addr(tail_slot), pos.data_ptr(),
+         cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), n_seq, T, H, DK, DV, dt)
     return k, v
 
 
@@ -824,31 +859,45 @@ def gla_tail_fold(log_lambda, pool, prefix_row, tail, tail_len, out=None, out_ro
     ``out[out_row[n]] = lambda^L pool[prefix_row[n]] + sum_j lambda^(L-1-j) k_j v_j^T`` with
     L = ``tail_len[n]``.  ``out`` fp32 ``[P', H, 96, 192]`` (None: a new ``[N, H, 96, 192]``; may be
     ``pool`` itself, see the header), ``out_row`` None: row n.  Returns ``out``."""
-    lib = load_library()
-    dev = pool.device
+    lib = _libs.get(_use_debug) or load_library()
+    dev = _device_of(pool, "pool")
+    _good(log_lambda, "log_lambda", torch.float32, dev)
     H = log_lambda.numel()
-    _need(log_lambda, "log_lambda", torch.float32, dev)
-    _pool(pool, H, dev)
+    rows = _pool(pool, H, dev)
     et = tail[0].dtype if tail[2] is None else torch.bfloat16
     if et not in (torch.bfloat16, torch.float32):
         raise TypeError("a tail without scales must be bfloat16 or float32")
     ct = _tail(tail, H, et, dev)
+    _good(prefix_row, "prefix_row", torch.int32, dev)
     N = prefix_row.numel()
-    for name, t in (("prefix_row", prefix_row), ("tail_len", tail_len), ("tail_slot", tail_slot), ("out_row", out_row)):
-        _index(t, name, N, dev)
+    _good(tail_len, "tail_len", torch.int32, dev, N)
+    for name, t in (("tail_slot", tail_slot), ("out_row", out_row)):
+        if t is not None:
+            _good(t, name, torch.int32, dev, N)
     if out is None:
         if out_row is not None:
             raise ValueError("out_row needs out")
         out = torch.empty((N, H, DK, DV), dtype=torch.float32, device=dev)
-    _need(out, "out", torch.float32, dev)
-    if out.dim() != 4 or out.shape[1:] != (H, DK, DV):
-        raise ValueError("out must be [P, H, 96, 192]")
-    with torch.cuda.device(dev):
-        rc = lib.gla_tail_fold(_ptr(log_lambda), _ptr(pool), pool.shape[0], _ptr(prefix_row), ctypes.byref(ct),
-                               _ptr(tail_slot), _ptr(tail_len), _ptr(out), out.shape[0], _ptr(out_row), N, H, DK, DV,
-                               GLA_F32 if et == torch.float32 else GLA_BF16, _stream(dev))
-    _check(rc, "gla_tail_fold")
+    out_rows = _pool(out, H, dev, "out")
+    _run(lib.gla_tail_fold, "gla_tail_fold", dev, log_lambda.data_ptr(), pool.data_ptr(), rows, prefix_row.data_ptr(),
+         ctypes.byref(ct), _addr(tail_slot), tail_len.data_ptr(), out.data_ptr(), out_rows, _addr(out_row), N, H, DK, DV,
+         GLA_F32 if et is torch.float32 else GLA_BF16)
     return out
+
+
+def _prefix_call(q, k, v, log_lambda, pool, prefix_row, cu_seqlens):
+    """Checks shared by the packed calls; returns (device, dtype code, n_seq, T, H, pool rows)."""
+    dt, dtype = _dtype_code(q), q.dtype
+    dev = _device_of(q, "q")
+    _good(q, "q", dtype, dev)
+    _good(k, "k", dtype, dev)
+    _good(v, "v", dtype, dev)
+    _good(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    n_seq, T, H = _layout(q, k, v, cu_seqlens)
+    _good(log_lambda, "log_lambda", torch.float32, dev, H)
+    rows = _pool(pool, H, dev)
+    _good(prefix_row, "prefix_row", torch.int32, dev, n_seq)
+    return dev, dt, n_seq, T, H, rows
 
 
 def gla_prefix_fwd(q, k, v, log_lambda, pool, prefix_row, cu_seqlens, scale=None, output_final_state: bool = True,
@@ -857,30 +906,21 @@ def gla_prefix_fwd(q, k, v, log_lambda, pool, prefix_row, cu_seqlens, scale=None
     :func:`gla_chunk_fwd` with ``cu_seqlens``, sequence n starting from ``pool[prefix_row[n]]``
     (``pool`` fp32 ``[P, H, 96, 192]``, ``prefix_row`` ``[n_seq]`` int32, rows may repeat).  Returns
     ``(o, hT)``."""
-    lib = load_library()
-    dev = q.device
-    dt = _dtype_code(q)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, q.dtype, dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    n_seq, T, H = _layout(q, k, v, cu_seqlens)
-    _need(log_lambda, "log_lambda", torch.float32, dev, H)
-    _pool(pool, H, dev)
-    _need(prefix_row, "prefix_row", torch.int32, dev, n_seq)
+    lib = _libs.get(_use_debug) or load_library()
+    dev, dt, n_seq, T, H, rows = _prefix_call(q, k, v, log_lambda, pool, prefix_row, cu_seqlens)
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    _need(o, "o", v.dtype, dev, v.numel())
-    if output_final_state and hT is None:
-        hT = torch.empty((n_seq, H, DK, DV), dtype=torch.float32, device=dev)
-    if hT is not None:
-        _need(hT, "hT", torch.float32, dev, n_seq * H * DK * DV)
+        o = torch.empty_like(v)
+    else:
+        _good(o, "o", v.dtype, dev, T * H * DV)
+    if hT is None:
+        if output_final_state:
+            hT = torch.empty((n_seq, H, DK, DV), dtype=torch.float32, device=dev)
+    else:
+        _good(hT, "hT", torch.float32, dev, n_seq * H * DK * DV)
     ws, ws_bytes = _workspace(cu_seqlens, n_seq, H, dev, workspace)
-    s = float(DK ** -0.5) if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        rc = lib.gla_prefix_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_lambda), _ptr(pool), pool.shape[0],
-                                _ptr(prefix_row), s, _ptr(o), _ptr(hT), _ptr(cu_seqlens), n_seq, T, H, DK, DV, dt,
-                                _ptr(ws), ws_bytes, _stream(dev))
-    _check(rc, "gla_prefix_fwd")
+    _run(lib.gla_prefix_fwd, "gla_prefix_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_lambda.data_ptr(),
+         pool.data_ptr(), rows, prefix_row.data_ptr(), DK ** -0.5 if scale is None else float(scale), o.data_ptr(),
+         _addr(hT), cu_seqlens.data_ptr(), n_seq, T, H, DK, DV, dt, ws.data_ptr(), ws_bytes)
     return o, hT
 
 
@@ -893,42 +933,32 @@ def gla_prefix_bwd(q, k, v, log_lambda, dO, pool, prefix_row, cu_seqlens, scale=
     """Backward of :func:`gla_prefix_fwd` (``gla_prefix_bwd``).  Returns ``(dq, dk, dv, dpool)``;
     ``dpool`` has the shape of ``pool``: row p is the sum of the initial-state gradients of the
     sequences that continue p, in their order, zeros where none does (None if not requested)."""
-    lib = load_library()
-    dev = q.device
-    dt = _dtype_code(q)
-    for name, t in (("q", q), ("k", k), ("v", v), ("dO", dO)):
-        _need(t, name, q.dtype, dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    n_seq, T, H = _layout(q, k, v, cu_seqlens)
+    lib = _libs.get(_use_debug) or load_library()
+    dev, dt, n_seq, T, H, rows = _prefix_call(q, k, v, log_lambda, pool, prefix_row, cu_seqlens)
+    _good(dO, "dO", q.dtype, dev)
     if dO.shape != v.shape:
         raise ValueError("dO must have the shape of v")
-    _need(log_lambda, "log_lambda", torch.float32, dev, H)
-    _pool(pool, H, dev)
-    _need(prefix_row, "prefix_row", torch.int32, dev, n_seq)
     if dhT is not None:
-        _need(dhT, "dhT", torch.float32, dev)
-        if dhT.shape != (n_seq, H, DK, DV):
+        _good(dhT, "dhT", torch.float32, dev)
+        if tuple(dhT.shape) != (n_seq, H, DK, DV):
             raise ValueError("dhT must be [n_seq, H, 96, 192]")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=v.dtype, device=dev) if dv is None else dv
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
     if dpool is None and need_dpool:
-        dpool = torch.empty(pool.shape, dtype=torch.float32, device=dev)
-    for name, t, ref in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _need(t, name, q.dtype, dev, ref.numel())
+        dpool = torch.empty_like(pool)
+    _good(dq, "dq", q.dtype, dev, q.numel())
+    _good(dk, "dk", q.dtype, dev, k.numel())
+    _good(dv, "dv", q.dtype, dev, v.numel())
     if dpool is not None:
-        _need(dpool, "dpool", torch.float32, dev, pool.numel())
+        _good(dpool, "dpool", torch.float32, dev, pool.numel())
     if workspace is None:
         workspace = torch.empty(gla_prefix_bwd_workspace_bytes(n_seq, T, H, dt), dtype=torch.uint8, device=dev)
-    s = float(DK ** -0.5) if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        rc = lib.gla_prefix_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_lambda), _ptr(pool), pool.shape[0],
-                                _ptr(prefix_row), s, _ptr(dO), _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dpool),
-                                _ptr(cu_seqlens), n_seq, T, H, DK, DV, dt, _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), _stream(dev))
-    _check(rc, "gla_prefix_bwd")
+    _run(lib.gla_prefix_bwd, "gla_prefix_bwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_lambda.data_ptr(),
+         pool.data_ptr(), rows, prefix_row.data_ptr(), DK ** -0.5 if scale is None else float(scale), dO.data_ptr(),
+         _addr(dhT), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _addr(dpool), cu_seqlens.data_ptr(), n_seq, T, H, DK,
+         DV, dt, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dv, dpool
-
 
 
 def gla_get_device_error(device=None) -> int:
