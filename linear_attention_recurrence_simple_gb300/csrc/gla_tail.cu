@@ -6,8 +6,10 @@
 // has, written out, S = lambda^L S_p + sum_j lambda^(L-1-j) k_j v_j^T: the tail holds the (k_j, v_j),
 // the fold evaluates the sum.
 #include <algorithm>
+#include <atomic>
 
 #include "gla_tail.cuh"
+#include "gla_tc.cuh"
 
 namespace gla {
 
@@ -132,12 +134,11 @@ cudaError_t launch_copy(int f32, bool mx, void* k, void* v, const TailArgs& t, c
 }
 
 // ---- the fold --------------------------------------------------------------------------------
-// One CTA per (sequence, head): the 96 x 192 sum in registers (a thread holds 6 rows x 12 columns),
-// tokens staged FOLD_TOK at a time in shared memory as fp32, keys already weighted by lambda^(L-1-j).
+// fp32 tails.  One CTA per (sequence, head): the 96 x 192 sum in registers (a thread holds 6 rows x 12
+// columns), tokens staged FOLD_TOK at a time in shared memory as fp32, keys already weighted by lambda^(L-1-j).
 // Bound by the fp32 FMA rate from a few dozen tokens on.
 constexpr int FOLD_THREADS = 256, FOLD_TOK = 16;
 
-template <class T, bool MX>
 __global__ void __launch_bounds__(FOLD_THREADS)
 tail_fold_kernel(const float* __restrict__ log_lambda, const float* pool, int pool_rows, const int32_t* __restrict__ prefix_row,
                  TailArgs t, float* out, int out_rows, const int32_t* __restrict__ out_row, int H, unsigned* err) {
@@ -166,12 +167,12 @@ tail_fold_kernel(const float* __restrict__ log_lambda, const float* pool, int po
       const int j = e / TOKEN_PIECES, p = e % TOKEN_PIECES;
       float x[16];
       if (p < DK / 16) {
-        tail_load16<T, MX, DK>(t.k, t.ks, tok0 + j0 + j, p, x);
+        tail_load16<float, false, DK>(t.k, t.ks, tok0 + j0 + j, p, x);
         const float w = decay_pow(ll, L - 1 - j0 - j);
 #pragma unroll
         for (int i = 0; i < 16; ++i) sk[j][16 * p + i] = w * x[i];
       } else {
-        tail_load16<T, MX, DV>(t.v, t.vs, tok0 + j0 + j, p - DK / 16, x);
+        tail_load16<float, false, DV>(t.v, t.vs, tok0 + j0 + j, p - DK / 16, x);
 #pragma unroll
         for (int i = 0; i < 16; ++i) sv[j][16 * (p - DK / 16) + i] = x[i];
       }
@@ -210,6 +211,235 @@ tail_fold_kernel(const float* __restrict__ log_lambda, const float* pool, int po
           make_float4(fmaf(lamL, s.x, acc[r][4 * c]), fmaf(lamL, s.y, acc[r][4 * c + 1]),
                       fmaf(lamL, s.z, acc[r][4 * c + 2]), fmaf(lamL, s.w, acc[r][4 * c + 3]));
     }
+}
+
+// bf16 and MXFP8 tails: the same sum on the tensor cores.  One CTA per (sequence, head) computes the
+// state transposed, D^T [192 x 96] = V^T (lambda^(L-1-j) K), so that tensor memory's lanes are the
+// state's columns and the epilogue's reads of S_p and writes of the state are whole 128-byte lines
+// straight from and to global memory:
+//     D1 = columns 0 .. 127 (M = 128), D2 = columns 128 .. 191 (M = 128, its upper half unused),
+//     N = 96, K = tokens, 16 a step; both operands MN-major (a token is a row of 128-byte panels).
+// The weighted key is split into hi + lo bf16 (16 significant bits; two MMAs into one sum), the value
+// is bf16 or an E4M3 code times a power of two: exact in bf16.  Threads load 16-value pieces of the next
+// 32 tokens into registers while the tensor core works on the previous ones, widen, weight and
+// split them, and store them swizzled; two buffers.  Bound by HBM: 73.7 KB written per
+// (sequence, head) and the tail read once; two CTAs per SM cover each other's epilogue.
+constexpr int FT_THREADS = 192, FT_TOK = 32;
+constexpr uint32_t FT_PANEL = FT_TOK * 128;                       // 32 tokens x 64 columns of bf16
+constexpr uint32_t FT_V = 0, FT_KH = 3 * FT_PANEL, FT_KL = 5 * FT_PANEL, FT_BUF = 7 * FT_PANEL;
+// (D2's unused upper half reads the panel after V's last, which is KH's first)
+constexpr uint32_t FT_SMEM = 80 * 1024;  // two buffers and alignment; sized for two CTAs per SM (tensor memory)
+static_assert(2 * FT_BUF + 1024 <= FT_SMEM, "fold buffers");
+constexpr int FT_PER = FT_TOK * TOKEN_PIECES / FT_THREADS;  // 3 pieces of a thread
+static_assert(FT_PER * FT_THREADS == FT_TOK * TOKEN_PIECES, "whole pieces");
+constexpr uint32_t FT_TMEM = 256;  // columns: D1 at 0, D2 at 96
+
+__device__ __forceinline__ uint32_t fold_pack(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <bool MX>
+__global__ void __launch_bounds__(FT_THREADS, 2)
+tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int pool_rows,
+                    const int32_t* __restrict__ prefix_row, TailArgs t, float* out, int out_rows,
+                    const int32_t* __restrict__ out_row, int H, unsigned* err, unsigned long long wait_ns) {
+  extern __shared__ uint8_t ft_raw[];
+  __shared__ uint64_t s_bar[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const uint32_t base = (smem_u32(ft_raw) + 1023u) & ~1023u;
+  const int n = (int)(blockIdx.x / (unsigned)H), h = (int)(blockIdx.x % (unsigned)H);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int L;
+  const long long tok0 = tail_token0(t, n, H, h, 0, L, err);
+  const int src = prefix_row[n], dst = out_row ? out_row[n] : n;
+  if (src < 0 || src >= pool_rows || dst < 0 || dst >= out_rows) {
+    raise_error(err, ERR_SHAPE);
+    return;
+  }
+  if (tok0 < 0) return;
+  const float ll = log_lambda[h];
+  const int chunks = (L + FT_TOK - 1) / FT_TOK;
+
+  // this thread's pieces of a chunk: token jt[i] of 32, piece pp of 18 (6 of k, then 12 of v)
+  uint4 raw[FT_PER][MX ? 1 : 2];
+  uint32_t rs[FT_PER];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < FT_PER; ++i) {
+      const int e = tid + FT_THREADS * i, jt = e / TOKEN_PIECES, p = e % TOKEN_PIECES, j = c * FT_TOK + jt;
+      const bool is_k = p < DK / 16;
+      const int pp = is_k ? p : p - DK / 16;
+      raw[i][0] = make_uint4(0u, 0u, 0u, 0u);
+      if (!MX) raw[i][MX ? 0 : 1] = make_uint4(0u, 0u, 0u, 0u);
+      rs[i] = 0;
+      if (j < L) {
+        const long long at = tok0 + j;
+        const int d = is_k ? DK : DV;
+        const uint8_t* b = static_cast<const uint8_t*>(is_k ? t.k : t.v);
+        if constexpr (MX) {
+          raw[i][0] = *(reinterpret_cast<const uint4*>(b + at * d) + pp);
+          rs[i] = (is_k ? t.ks : t.vs)[at * (d / 32) + (pp >> 1)];
+        } else {
+          raw[i][0] = *(reinterpret_cast<const uint4*>(b + at * 2 * d) + 2 * pp);
+          raw[i][1] = *(reinterpret_cast<const uint4*>(b + at * 2 * d) + 2 * pp + 1);
+        }
+      }
+    }
+  };
+  // widened, weighted, split and stored to buffer b
+  auto store = [&](int c, int b) {
+#pragma unroll
+    for (int i = 0; i < FT_PER; ++i) {
+      const int e = tid + FT_THREADS * i, jt = e / TOKEN_PIECES, p = e % TOKEN_PIECES, j = c * FT_TOK + jt;
+      const bool is_k = p < DK / 16;
+      const int pp = is_k ? p : p - DK / 16;
+      const uint32_t row = base + (uint32_t)b * FT_BUF + (uint32_t)(pp >> 2) * FT_PANEL + (uint32_t)jt * 128u;
+      const uint32_t x0 = (uint32_t)(((pp & 3) * 2) ^ (jt & 7)) << 4, x1 = (uint32_t)(((pp & 3) * 2 + 1) ^ (jt & 7)) << 4;
+      if (!MX && !is_k) {
+        st_shared_v4(row + FT_V + x0, raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w);
+        const uint4 r1 = raw[i][MX ? 0 : 1];
+        st_shared_v4(row + FT_V + x1, r1.x, r1.y, r1.z, r1.w);
+        continue;
+      }
+      float x[16];
+      if constexpr (MX) {
+        dequantise16(raw[i][0], e8m0_to_f(rs[i]), x);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t w[4] = {raw[i][q].x, raw[i][q].y, raw[i][q].z, raw[i][q].w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            x[8 * q + 2 * s] = __uint_as_float(w[s] << 16);
+            x[8 * q + 2 * s + 1] = __uint_as_float(w[s] & 0xFFFF0000u);
+          }
+        }
+      }
+      uint32_t hi[8];
+      if (is_k) {
+        const float w = j < L ? decay_pow(ll, L - 1 - j) : 0.f;
+        uint32_t lo[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const float a = w * x[2 * s], c2 = w * x[2 * s + 1];
+          hi[s] = fold_pack(a, c2);
+          lo[s] = fold_pack(a - __uint_as_float(hi[s] << 16), c2 - __uint_as_float(hi[s] & 0xFFFF0000u));
+        }
+        st_shared_v4(row + FT_KL + x0, lo[0], lo[1], lo[2], lo[3]);
+        st_shared_v4(row + FT_KL + x1, lo[4], lo[5], lo[6], lo[7]);
+      } else {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) hi[s] = fold_pack(x[2 * s], x[2 * s + 1]);
+      }
+      const uint32_t to = row + (is_k ? FT_KH : FT_V);
+      st_shared_v4(to + x0, hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(to + x1, hi[4], hi[5], hi[6], hi[7]);
+    }
+  };
+
+  if (chunks > 0) load(0);
+  if (tid == 0) {
+    mbar_init(&s_bar[0], 2);  // the two issuers' commits
+    mbar_init(&s_bar[1], 2);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(FT_TMEM));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  int issued = 0;
+  bool bad = false;
+  for (int c = 0; c < chunks; ++c) {
+    const int b = c & 1;
+    const bool ok = c < 2 || mbar_wait(&s_bar[b], (uint32_t)((c >> 1) - 1) & 1u, wait_ns, &s_abort);
+    store(c, b);
+    if (c + 1 < chunks) load(c + 1);
+    fence_async_smem();
+    bad = __syncthreads_or(!ok);
+    if (bad) break;
+    if (lane == 0 && warp < 2) {  // one issuer per sum
+      constexpr uint32_t ID = idesc_bf16(128, DK, 1, 1);
+      tc_fence_after();
+      const uint32_t buf = base + (uint32_t)b * FT_BUF;
+      const SDesc a = sdesc(buf + FT_V + (uint32_t)warp * 2u * FT_PANEL, FT_PANEL, 1024, LAYOUT_SW128);
+      const SDesc kh = sdesc(buf + FT_KH, FT_PANEL, 1024, LAYOUT_SW128), kl = sdesc(buf + FT_KL, FT_PANEL, 1024, LAYOUT_SW128);
+#pragma unroll
+      for (int kk = 0; kk < FT_TOK / 16; ++kk) {
+        umma(tmem + (uint32_t)warp * DK, a + (uint32_t)kk * 2048u, kh + (uint32_t)kk * 2048u, ID, c > 0 || kk > 0);
+        umma(tmem + (uint32_t)warp * DK, a + (uint32_t)kk * 2048u, kl + (uint32_t)kk * 2048u, ID, 1);
+      }
+      umma_commit(&s_bar[b]);
+    }
+    ++issued;
+  }
+  if (chunks > 0 && !bad) {
+    const bool ok = mbar_wait(&s_bar[(chunks - 1) & 1], (uint32_t)((chunks - 1) >> 1) & 1u, wait_ns, &s_abort);
+    bad = __syncthreads_or(!ok);
+    tc_fence_after();
+  }
+  if (!bad) {
+    // each thread reads exactly the entries of the shared state that it writes, and before it does:
+    // a sequence may be folded into the row that it started from
+    const float lamL = decay_pow(ll, L);
+    const int col = 32 * warp + lane;  // warps 0-3: D1, columns 0 .. 127; warps 4, 5: D2
+    const float* S = pool + ((long long)src * H + h) * (DK * DV) + col;
+    float* O = out + ((long long)dst * H + h) * (DK * DV) + col;
+    const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + (warp < 4 ? 0u : (uint32_t)DK);
+#pragma unroll 1
+    for (int a0 = 0; a0 < DK; a0 += 32) {
+      float s[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = S[(a0 + i) * DV];
+      if (chunks > 0) {
+        uint32_t d[32];
+        tmem_ld32(ta + (uint32_t)a0, d);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = fmaf(lamL, s[i], __uint_as_float(d[i]));
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) O[(a0 + i) * DV] = s[i];
+    }
+  } else {
+    // a wait gave up: the MMAs in flight end before tensor memory is freed
+    if (tid == 0) {
+      if (issued > 0) mbar_wait_drain(&s_bar[(issued - 1) & 1], (uint32_t)((issued - 1) >> 1) & 1u, 1000000000ull, err);
+      raise_error(err, ERR_TIMEOUT);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(FT_TMEM));
+  }
+}
+
+template <bool MX>
+cudaError_t launch_fold_tc(const float* log_lambda, const float* pool, int pool_rows, const int32_t* prefix_row,
+                           const TailArgs& t, float* out, int out_rows, const int32_t* out_row, unsigned blocks, int H,
+                           unsigned* err, unsigned long long wait_ns, cudaStream_t s) {
+  static std::atomic<bool> allowed[64];  // per device: the kernel's shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !allowed[dev].load()) {
+    if ((e = cudaFuncSetAttribute(tail_fold_tc_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FT_SMEM)) !=
+        cudaSuccess)
+      return e;
+    if (dev < 64) allowed[dev].store(true);
+  }
+  tail_fold_tc_kernel<MX><<<blocks, FT_THREADS, FT_SMEM, s>>>(log_lambda, pool, pool_rows, prefix_row, t, out, out_rows,
+                                                              out_row, H, err, wait_ns);
+  return cudaGetLastError();
 }
 
 bool aligned(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -287,14 +517,15 @@ int gla_tail_fold(const float* log_lambda, const float* pool, int pool_rows, con
   const unsigned blocks = (unsigned)N * (unsigned)H;
   const bool mx = tail->format == GLA_TAIL_MXFP8;
   cudaStream_t s = (cudaStream_t)stream;
-  using gla::FOLD_THREADS;
-  if (dtype == GLA_F32 && !mx)
-    gla::tail_fold_kernel<float, false><<<blocks, FOLD_THREADS, 0, s>>>(log_lambda, pool, pool_rows, prefix_row, t, out, out_rows, out_row, H, err);
-  else if (mx)
-    gla::tail_fold_kernel<__nv_bfloat16, true><<<blocks, FOLD_THREADS, 0, s>>>(log_lambda, pool, pool_rows, prefix_row, t, out, out_rows, out_row, H, err);
-  else
-    gla::tail_fold_kernel<__nv_bfloat16, false><<<blocks, FOLD_THREADS, 0, s>>>(log_lambda, pool, pool_rows, prefix_row, t, out, out_rows, out_row, H, err);
-  return gla::to_status(cudaGetLastError());
+  if (dtype == GLA_F32 && !mx) {
+    gla::tail_fold_kernel<<<blocks, gla::FOLD_THREADS, 0, s>>>(log_lambda, pool, pool_rows, prefix_row, t, out, out_rows,
+                                                               out_row, H, err);
+    return gla::to_status(cudaGetLastError());
+  }
+  return gla::to_status(mx ? gla::launch_fold_tc<true>(log_lambda, pool, pool_rows, prefix_row, t, out, out_rows, out_row,
+                                                       blocks, H, err, wait_ns, s)
+                           : gla::launch_fold_tc<false>(log_lambda, pool, pool_rows, prefix_row, t, out, out_rows, out_row,
+                                                        blocks, H, err, wait_ns, s));
 }
 
 }  // extern "C"
