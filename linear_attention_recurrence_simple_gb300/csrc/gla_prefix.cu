@@ -120,11 +120,12 @@ prefix_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* 
 //       weights   K [16 tokens x 96] times q (one column of N = 8 used): exact products.  E4M3 codes
 //                 widen exactly to f16; q is brought to f16 by a power of two (its 8 bits fit; what
 //                 lies 2^-35 below the largest is lost).  Block scales enter in fp32, per 32 columns.
-//       output    w [16 x 16 tokens] times V [16 tokens x 192].  bf16 tails: row 0 of w holds the high
-//                 bf16 of the weight, row 8 the low one.  MXFP8: rows b and b + 8 hold the high and
-//                 low f16 of w_j 2^(e_jb), the weight times the scale of column block b, so that the
-//                 codes enter unscaled; each row is kept in f16's range by a power of two of its own,
-//                 raised (and the sums rescaled) when a weight outgrows it.
+//       output    V^T [16 columns x 16 tokens] times w [16 tokens x 8].  bf16 tails: w's even columns
+//                 hold the high bf16 of the weight, the odd ones the low one (their sums meet in one
+//                 thread).  MXFP8: column b holds w_j 2^(e_jb), the weight times the scale of column
+//                 block b, so that the codes enter unscaled (exact in f16); its high and low f16 go
+//                 in turn.  Each column is kept in f16's range by a power of two of its own, raised
+//                 (and the sums rescaled) when a weight outgrows it.
 //     A sequence whose chunks fall to one warp is added to the tile's sums directly; the first and
 //     last sequence of a warp's range may be shared, and those parts meet in warp order.
 constexpr int TILE_MAX = 16;
@@ -136,25 +137,33 @@ struct PdStage {
   static constexpr uint32_t K_ROW = MX ? DK : 2 * DK, V_ROW = MX ? DV : 2 * DV;  // bytes of a token
   static constexpr uint32_t K = 0, V = K + PD_TOK * K_ROW, KS = V + PD_TOK * V_ROW, VS = KS + (MX ? 48 : 0);
   static constexpr uint32_t BYTES = VS + (MX ? 96 : 0);
-  static constexpr int N = MX ? 3 : 2;  // stages of a warp's ring
+  static constexpr int N = 2;  // stages of a warp's ring
 };
 template <bool MX>
 struct PdSmem {
   static constexpr uint32_t O = PD_WARPS * PdStage<MX>::N * PdStage<MX>::BYTES;  // [16][192] sums
-  static constexpr uint32_t PART = O + TILE_MAX * DV * 4;                        // [warps][2][192]
-  static constexpr uint32_t BAR = PART + PD_WARPS * 2 * DV * 4;
+  static constexpr uint32_t PART = O + TILE_MAX * DV * 4;                        // [warps][192], a warp's first part
+  static constexpr uint32_t Q = PART + PD_WARPS * DV * 4;                        // [16][96] bf16
+  static constexpr uint32_t BAR = Q + TILE_MAX * DK * 2;
   static constexpr uint32_t BYTES = BAR + PD_WARPS * PdStage<MX>::N * 8;
 };
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1, float c0, float c1, float c2, float c3) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool F16>
+__device__ __forceinline__ void mma16_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  mma16<F16>(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
 }
 __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -181,6 +190,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
   return r;
 }
+// Two E8M0 scale bytes to a bf16 pair, 2^(b - 127) (exact; 255: NaN).
+__device__ __forceinline__ uint32_t e8m0x2_to_bf2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
+  return r;
+}
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -190,7 +205,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
 }
 
 template <bool MX>
-__global__ void __launch_bounds__(PD_THREADS, MX ? 3 : 2)
+__global__ void __launch_bounds__(PD_THREADS, MX ? 4 : 2)
 prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
                           const __nv_bfloat16* __restrict__ v, const float* __restrict__ log_lambda, float scale,
                           const float* __restrict__ pool, int pool_rows, const int32_t* __restrict__ prefix_row, TailArgs t,
@@ -200,12 +215,14 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   using SM = PdSmem<MX>;
   using BF = __nv_bfloat16;
   extern __shared__ __align__(128) uint8_t pd_smem[];
-  __shared__ int s_row[TILE_MAX], s_len[TILE_MAX], s_cu[TILE_MAX + 1], s_part[2 * PD_WARPS];
+  __shared__ int s_row[TILE_MAX], s_len[TILE_MAX], s_cu[TILE_MAX + 1], s_part[2 * PD_WARPS];  // sequences of the shared parts, -1: none
+ 
   __shared__ long long s_tok0[TILE_MAX];
   __shared__ float s_self[TILE_MAX];
   __shared__ int s_abort;
   float* sO = reinterpret_cast<float*>(pd_smem + SM::O);
   float* sPart = reinterpret_cast<float*>(pd_smem + SM::PART);
+  BF* sQ = reinterpret_cast<BF*>(pd_smem + SM::Q);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
   uint64_t* full = reinterpret_cast<uint64_t*>(pd_smem + SM::BAR) + warp * ST::N;
   const int h = (int)(blockIdx.x % (unsigned)H), n0 = (int)(blockIdx.x / (unsigned)H) * tile_seqs;
@@ -251,27 +268,31 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   const int c0 = (int)(total * warp / PD_WARPS), c1 = (int)(total * (warp + 1) / PD_WARPS);
   const uint32_t ring = smem_u32(pd_smem) + (uint32_t)(warp * ST::N) * ST::BYTES;
   uint8_t* const ring_p = pd_smem + (size_t)(warp * ST::N) * ST::BYTES;
-  int issue_i = 0;  // (lane 0) sequence of the next chunk to load
-  auto issue = [&](int c) {
+  int issue_i = 0;  // sequence of the next chunk to load
+  auto issue = [&](int c) {  // whole warp; lanes 0 .. 3 take one of the copies each
     while (c >= s_cu[issue_i + 1]) ++issue_i;
     const int j0 = (c - s_cu[issue_i]) * PD_TOK, m = min(PD_TOK, s_len[issue_i] - j0);
     const long long tok = s_tok0[issue_i] + j0;
     const int s = (c - c0) % ST::N;
     const uint32_t dst = ring + (uint32_t)s * ST::BYTES;
     const uint32_t ks = MX ? (uint32_t)(3 * m + 15) / 16 * 16 : 0, vs = MX ? (uint32_t)(6 * m + 15) / 16 * 16 : 0;
-    mbar_expect_tx(&full[s], (uint32_t)m * (ST::K_ROW + ST::V_ROW) + ks + vs);
-    bulk_copy(dst + ST::K, static_cast<const uint8_t*>(t.k) + tok * ST::K_ROW, (uint32_t)m * ST::K_ROW, &full[s]);
-    bulk_copy(dst + ST::V, static_cast<const uint8_t*>(t.v) + tok * ST::V_ROW, (uint32_t)m * ST::V_ROW, &full[s]);
-    if (MX) {
-      bulk_copy(dst + ST::KS, t.ks + tok * (DK / 32), ks, &full[s]);
-      bulk_copy(dst + ST::VS, t.vs + tok * (DV / 32), vs, &full[s]);
+    if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)m * (ST::K_ROW + ST::V_ROW) + ks + vs);
+    __syncwarp();
+    if (lane < (MX ? 4 : 2)) {
+      const uint8_t* from = static_cast<const uint8_t*>(lane == 0 ? t.k : lane == 1 ? t.v : lane == 2 ? t.ks : t.vs);
+      const uint32_t row = lane == 0 ? ST::K_ROW : lane == 1 ? ST::V_ROW : lane == 2 ? DK / 32 : DV / 32;
+      bulk_copy(dst + (lane == 0 ? ST::K : lane == 1 ? ST::V : lane == 2 ? ST::KS : ST::VS), from + tok * row,
+                lane < 2 ? (uint32_t)m * row : lane == 2 ? ks : vs, &full[s]);
     }
   };
   int issued = 0;
-  if (lane == 0)
-    for (; issued < ST::N && c0 + issued < c1; ++issued) issue(c0 + issued);
-  __syncwarp();
+  for (; issued < ST::N && c0 + issued < c1; ++issued) issue(c0 + issued);
 
+  for (int e = tid; e < cnt * (DK / 8); e += PD_THREADS) {
+    const int i = e / (DK / 8), p = e % (DK / 8);
+    reinterpret_cast<uint4*>(sQ)[e] = *reinterpret_cast<const uint4*>(q + ((long long)(n0 + i) * H + h) * DK + 8 * p);
+  }
+  __syncthreads();
   const float ll = log_lambda[h];
   // ---- the new tokens: q . k, and their places in the tails
   for (int i = warp; i < cnt; i += PD_WARPS) {
@@ -282,7 +303,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     if (lane < DK / 16) {
       float y[16];
       load16(k + nh * DK + 16 * lane, x);
-      load16(q + nh * DK + 16 * lane, y);
+      load16(sQ + i * DK + 16 * lane, y);
 #pragma unroll
       for (int e = 0; e < 16; ++e) d = fmaf(x[e], y[e], d);
     }
@@ -301,8 +322,8 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   {
     // q fragments; K step s of thread tq: columns 16 s + 4 tq .. + 3 (the same order as S's rows)
     uint2 qa[6], qb[6];
-    const BF* q0 = q + ((long long)(n0 + g) * H + h) * DK + 4 * tq;
-    const BF* q1 = q + ((long long)(n0 + g + 8) * H + h) * DK + 4 * tq;
+    const BF* q0 = sQ + g * DK + 4 * tq;
+    const BF* q1 = q0 + 8 * DK;
 #pragma unroll
     for (int s = 0; s < 6; ++s) {
       qa[s] = g < cnt ? *reinterpret_cast<const uint2*>(q0 + 16 * s) : make_uint2(0u, 0u);
@@ -327,13 +348,12 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
             x[e] = *reinterpret_cast<const float4*>(p + 4 * g);
             y[e] = *reinterpret_cast<const float2*>(p + 32 + 2 * g);
           }
-          const uint32_t a[4] = {qa[s].x, qb[s].x, qa[s].y, qb[s].y};
           auto col = [&](float (&dd)[4], float v0, float v1, float v2, float v3) {
             uint32_t h0, l0, h1, l1;
             split_bf(v0, v1, h0, l0);
             split_bf(v2, v3, h1, l1);
-            mma_bf16(dd, a, h0, h1);
-            mma_bf16(dd, a, l0, l1);
+            mma16_add<false>(dd, qa[s].x, qb[s].x, qa[s].y, qb[s].y, h0, h1);
+            mma16_add<false>(dd, qa[s].x, qb[s].x, qa[s].y, qb[s].y, l0, l1);
           };
           col(d[0], x[0].x, x[1].x, x[2].x, x[3].x);
           col(d[1], x[0].y, x[1].y, x[2].y, x[3].y);
@@ -369,7 +389,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     uint32_t qf[3][4];
     float qn = 1.f;  // what the weights are to be multiplied with
     {
-      const BF* qr = q + ((long long)(n0 + seq) * H + h) * DK + 8 * tq;
+      const BF* qr = sQ + seq * DK + 8 * tq;
 #pragma unroll
       for (int b = 0; b < 3; ++b) {
         const uint4 u = *reinterpret_cast<const uint4*>(qr + 32 * b);
@@ -401,12 +421,12 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
 #pragma unroll
         for (int e = 0; e < 4; ++e) qf[b][e] = g == 0 ? qf[b][e] : 0u;
     }
-    float acc[24][4];
+    float acc[12][4];  // 16 columns each: see the flush below
 #pragma unroll
-    for (int i = 0; i < 24; ++i)
+    for (int i = 0; i < 12; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-    int E = -1000;  // (MXFP8) exponent of row g's power of two
+    int E = -1000;  // (MXFP8) exponent of the power of two of column g of w
     for (; c < last; ++c) {
       const int it = c - c0, s = it % ST::N;
       ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)(it / ST::N) & 1u, wait_ns, &s_abort));
@@ -421,29 +441,43 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
         __syncwarp();
       }
       // weights: token g in lanes tq = 0, element 0; token g + 8, element 2
-      float sc0 = 0.f, sc1 = 0.f;
-#pragma unroll
-      for (int b = 0; b < 3; ++b) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+      float sc0, sc1;
+      {
+        float d[3][4];
+        float k0[3], k1[3];  // block scales of the two tokens' keys
         if constexpr (MX) {
-          const uint2 x = *reinterpret_cast<const uint2*>(st + ST::K + (uint32_t)g * DK + 32 * b + 8 * tq);
-          const uint2 y = *reinterpret_cast<const uint2*>(st + ST::K + (uint32_t)(g + 8) * DK + 32 * b + 8 * tq);
-          const uint32_t a0[4] = {e4m3x2_to_h2(x.x & 0xFFFFu), e4m3x2_to_h2(y.x & 0xFFFFu), e4m3x2_to_h2(x.x >> 16),
-                                  e4m3x2_to_h2(y.x >> 16)};
-          const uint32_t a1[4] = {e4m3x2_to_h2(x.y & 0xFFFFu), e4m3x2_to_h2(y.y & 0xFFFFu), e4m3x2_to_h2(x.y >> 16),
-                                  e4m3x2_to_h2(y.y >> 16)};
-          mma_f16(d, a0, qf[b][0], qf[b][1]);
-          mma_f16(d, a1, qf[b][2], qf[b][3]);
-          sc0 = fmaf(d[0], e8m0_to_f(st[ST::KS + 3 * g + b]), sc0);
-          sc1 = fmaf(d[2], e8m0_to_f(st[ST::KS + 3 * (g + 8) + b]), sc1);
+          const uint8_t* kp = st + ST::KS + 3 * g;
+          const uint32_t u0 = e8m0x2_to_bf2(kp[0] | (uint32_t)kp[1] << 8), u1 = e8m0x2_to_bf2(kp[24] | (uint32_t)kp[25] << 8),
+                         u2 = e8m0x2_to_bf2(kp[2] | (uint32_t)kp[26] << 8);
+          k0[0] = __uint_as_float(u0 << 16);
+          k0[1] = __uint_as_float(u0 & 0xFFFF0000u);
+          k0[2] = __uint_as_float(u2 << 16);
+          k1[0] = __uint_as_float(u1 << 16);
+          k1[1] = __uint_as_float(u1 & 0xFFFF0000u);
+          k1[2] = __uint_as_float(u2 & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {
+          if constexpr (MX) {
+            const uint2 x = *reinterpret_cast<const uint2*>(st + ST::K + (uint32_t)g * DK + 32 * b + 8 * tq);
+            const uint2 y = *reinterpret_cast<const uint2*>(st + ST::K + (uint32_t)(g + 8) * DK + 32 * b + 8 * tq);
+            mma16<true>(d[b], e4m3x2_to_h2(x.x & 0xFFFFu), e4m3x2_to_h2(y.x & 0xFFFFu), e4m3x2_to_h2(x.x >> 16),
+                        e4m3x2_to_h2(y.x >> 16), qf[b][0], qf[b][1], 0.f, 0.f, 0.f, 0.f);
+            mma16_add<true>(d[b], e4m3x2_to_h2(x.y & 0xFFFFu), e4m3x2_to_h2(y.y & 0xFFFFu), e4m3x2_to_h2(x.y >> 16),
+                            e4m3x2_to_h2(y.y >> 16), qf[b][2], qf[b][3]);
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(st + ST::K + (uint32_t)g * ST::K_ROW + 64 * b + 16 * tq);
+            const uint4 y = *reinterpret_cast<const uint4*>(st + ST::K + (uint32_t)(g + 8) * ST::K_ROW + 64 * b + 16 * tq);
+            mma16<false>(d[b], x.x, y.x, x.y, y.y, qf[b][0], qf[b][1], 0.f, 0.f, 0.f, 0.f);
+            mma16_add<false>(d[b], x.z, y.z, x.w, y.w, qf[b][2], qf[b][3]);
+          }
+        }
+        if constexpr (MX) {
+          sc0 = fmaf(d[2][0], k0[2], fmaf(d[1][0], k0[1], d[0][0] * k0[0]));
+          sc1 = fmaf(d[2][2], k1[2], fmaf(d[1][2], k1[1], d[0][2] * k1[0]));
         } else {
-          const uint4 x = *reinterpret_cast<const uint4*>(st + ST::K + (uint32_t)g * ST::K_ROW + 64 * b + 16 * tq);
-          const uint4 y = *reinterpret_cast<const uint4*>(st + ST::K + (uint32_t)(g + 8) * ST::K_ROW + 64 * b + 16 * tq);
-          const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-          mma_bf16(d, a0, qf[b][0], qf[b][1]);
-          mma_bf16(d, a1, qf[b][2], qf[b][3]);
-          sc0 += d[0];
-          sc1 += d[2];
+          sc0 = d[0][0] + d[1][0] + d[2][0];
+          sc1 = d[0][2] + d[1][2] + d[2][2];
         }
       }
       // lane j < 16 takes token j's weight
@@ -452,13 +486,15 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
       float wt[4];  // tokens tq, tq + 4, tq + 8, tq + 12
 #pragma unroll
       for (int i = 0; i < 4; ++i) wt[i] = __shfl_sync(0xffffffffu, w, tq + 4 * i);
-      uint32_t a[4];
       if constexpr (MX) {
+        const uint8_t* vp = st + ST::VS + 6 * tq + min(g, DV / 32 - 1);
+        const uint32_t u0 = e8m0x2_to_bf2(vp[0] | (uint32_t)vp[24] << 8), u1 = e8m0x2_to_bf2(vp[48] | (uint32_t)vp[72] << 8);
+        const float vs[4] = {__uint_as_float(u0 << 16), __uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 << 16),
+                             __uint_as_float(u1 & 0xFFFF0000u)};
         float mx = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int j = tq + 4 * i;
-          wt[i] = g < DV / 32 && j < m ? wt[i] * e8m0_to_f(st[ST::VS + 6 * j + (g < DV / 32 ? g : 0)]) : 0.f;
+          wt[i] = g < DV / 32 && tq + 4 * i < m ? wt[i] * vs[i] : 0.f;  // (a scale past the tail's end may be NaN)
           mx = fmaxf(mx, fabsf(wt[i]));
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -467,15 +503,17 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
         const bool grow = need > E + 10;
         if (__any_sync(0xffffffffu, grow)) {
           const float f = !grow ? 1.f : (E < -126 ? 0.f : pow2i(E - need));
+          const float f0 = __shfl_sync(0xffffffffu, f, 8 * tq), f1 = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
 #pragma unroll
-          for (int i = 0; i < 24; ++i)
+          for (int i = 0; i < 12; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] *= f;
+            for (int e = 0; e < 4; ++e) acc[i][e] *= (e & 1) ? f1 : f0;
           if (grow) E = need;
         }
         const float up = pow2i(4 - E);
-        split_h(wt[0] * up, wt[1] * up, a[0], a[1]);
-        split_h(wt[2] * up, wt[3] * up, a[2], a[3]);
+        uint32_t h0, h1, l0, l1;
+        split_h(wt[0] * up, wt[1] * up, h0, l0);
+        split_h(wt[2] * up, wt[3] * up, h1, l1);
 #pragma unroll
         for (int B = 0; B < 3; ++B) {
           uint2 x[4];
@@ -483,22 +521,21 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
           for (int i = 0; i < 4; ++i)
             x[i] = *reinterpret_cast<const uint2*>(st + ST::V + (uint32_t)(tq + 4 * i) * DV + 64 * B + 8 * g);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t x0 = half ? x[0].y : x[0].x, x1 = half ? x[1].y : x[1].x, x2 = half ? x[2].y : x[2].x,
-                           x3 = half ? x[3].y : x[3].x;
-            const uint32_t p0 = __byte_perm(x0, x1, 0x5140), p1 = __byte_perm(x0, x1, 0x7362);
-            const uint32_t r0 = __byte_perm(x2, x3, 0x5140), r1 = __byte_perm(x2, x3, 0x7362);
-            mma_f16(acc[8 * B + 4 * half], a, e4m3x2_to_h2(p0 & 0xFFFFu), e4m3x2_to_h2(r0 & 0xFFFFu));
-            mma_f16(acc[8 * B + 4 * half + 1], a, e4m3x2_to_h2(p0 >> 16), e4m3x2_to_h2(r0 >> 16));
-            mma_f16(acc[8 * B + 4 * half + 2], a, e4m3x2_to_h2(p1 & 0xFFFFu), e4m3x2_to_h2(r1 & 0xFFFFu));
-            mma_f16(acc[8 * B + 4 * half + 3], a, e4m3x2_to_h2(p1 >> 16), e4m3x2_to_h2(r1 >> 16));
+          for (int jj = 0; jj < 4; ++jj) {  // columns 64 B + 8 g + 2 jj (row g) and the next (row g + 8)
+            const uint32_t sel = jj & 1 ? 0x7362 : 0x5140;
+            const uint32_t p = __byte_perm(jj & 2 ? x[0].y : x[0].x, jj & 2 ? x[1].y : x[1].x, sel);
+            const uint32_t r = __byte_perm(jj & 2 ? x[2].y : x[2].x, jj & 2 ? x[3].y : x[3].x, sel);
+            const uint32_t a0 = e4m3x2_to_h2(p & 0xFFFFu), a1 = e4m3x2_to_h2(p >> 16), a2 = e4m3x2_to_h2(r & 0xFFFFu),
+                           a3 = e4m3x2_to_h2(r >> 16);
+            mma16_add<true>(acc[4 * B + jj], a0, a1, a2, a3, h0, h1);
+            mma16_add<true>(acc[4 * B + jj], a0, a1, a2, a3, l0, l1);
           }
         }
       } else {
-        split_bf(wt[0], wt[1], a[0], a[1]);
-        split_bf(wt[2], wt[3], a[2], a[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a[e] = g == 0 ? a[e] : 0u;
+        uint32_t h0, h1, l0, l1;
+        split_bf(wt[0], wt[1], h0, l0);
+        split_bf(wt[2], wt[3], h1, l1);
+        const uint32_t b0 = g & 1 ? l0 : h0, b1 = g & 1 ? l1 : h1;
 #pragma unroll
         for (int B = 0; B < 3; ++B) {
           uint4 x[4];
@@ -506,42 +543,57 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
           for (int i = 0; i < 4; ++i)
             x[i] = *reinterpret_cast<const uint4*>(st + ST::V + (uint32_t)(tq + 4 * i) * ST::V_ROW + 128 * B + 16 * g);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t x0 = e == 0 ? x[0].x : e == 1 ? x[0].y : e == 2 ? x[0].z : x[0].w;
-            const uint32_t x1 = e == 0 ? x[1].x : e == 1 ? x[1].y : e == 2 ? x[1].z : x[1].w;
-            const uint32_t x2 = e == 0 ? x[2].x : e == 1 ? x[2].y : e == 2 ? x[2].z : x[2].w;
-            const uint32_t x3 = e == 0 ? x[3].x : e == 1 ? x[3].y : e == 2 ? x[3].z : x[3].w;
-            mma_bf16(acc[8 * B + 2 * e], a, __byte_perm(x0, x1, 0x5410), __byte_perm(x2, x3, 0x5410));
-            mma_bf16(acc[8 * B + 2 * e + 1], a, __byte_perm(x0, x1, 0x7632), __byte_perm(x2, x3, 0x7632));
+          for (int jj = 0; jj < 4; ++jj) {
+            const uint32_t x0 = jj == 0 ? x[0].x : jj == 1 ? x[0].y : jj == 2 ? x[0].z : x[0].w;
+            const uint32_t x1 = jj == 0 ? x[1].x : jj == 1 ? x[1].y : jj == 2 ? x[1].z : x[1].w;
+            const uint32_t x2 = jj == 0 ? x[2].x : jj == 1 ? x[2].y : jj == 2 ? x[2].z : x[2].w;
+            const uint32_t x3 = jj == 0 ? x[3].x : jj == 1 ? x[3].y : jj == 2 ? x[3].z : x[3].w;
+            mma16_add<false>(acc[4 * B + jj], __byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
+                             __byte_perm(x2, x3, 0x5410), __byte_perm(x2, x3, 0x7632), b0, b1);
           }
         }
       }
       // the stage is read: refill it (the zeros above were written through the generic proxy)
       if (m < PD_TOK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0 && c0 + issued < c1) {
+      if (c0 + issued < c1) {
         issue(c0 + issued);
         ++issued;
       }
     }
     if (!ok) break;
-    // the sequence's sums (this warp's part of them)
-    const int part = 2 * warp + (last == c1 && c0 < first ? 1 : 0);
-    float* dst = whole ? sO + seq * DV : sPart + part * DV;
-    if (!whole && lane == 0) s_part[part] = seq;
-    const float back = MX ? pow2i(E - 4) : 1.f;
+    // the sequence's sums (this warp's part of them): thread (g, tq < 3) holds columns 64 tq + 8 g
+    // .. + 7.  A part that the warp ends with goes to its ring (whose chunks have all been read).
+    const bool second = last == c1 && c0 < first;
+    float* dst = whole ? sO + seq * DV : second ? reinterpret_cast<float*>(ring_p) : sPart + warp * DV;
+    if (!whole && lane == 0) s_part[2 * warp + second] = seq;
+    const float back = MX ? pow2i(__shfl_sync(0xffffffffu, E, 4 * ((2 * tq + (g >> 2)) & 7)) - 4) : 1.f;
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 24; ++i) {
-      const int B = i >> 3, jj = i & 7;
-      // MXFP8: column block 2 B + (tq >> 1) is row g of the product; bf16: row 0
-      if (MX ? g == 2 * B + (tq >> 1) : g == 0) {
+    for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int col = 64 * B + 8 * (2 * tq + e) + jj;
-          const float x = (acc[i][e] + acc[i][e + 2]) * back;
-          dst[col] = whole ? dst[col] + x : x;
+      for (int u = 0; u < 2; ++u) {
+        float x = 0.f;
+#pragma unroll
+        for (int B = 0; B < 3; ++B) {
+          const float(&a)[4] = acc[4 * B + jj];
+          // MXFP8: the column's block is 2 B + (g >> 2), column tq = B of the product, its first or
+          // second element; bf16: the high and the low part
+          const float z = MX ? (g >> 2 ? a[2 * u + 1] : a[2 * u]) * back : a[2 * u] + a[2 * u + 1];
+          x = tq == B ? z : x;
         }
+        y[2 * jj + u] = x;
       }
+    if (tq < 3) {
+      float4* p = reinterpret_cast<float4*>(dst + 64 * tq + 8 * g);
+      float4 u = make_float4(y[0], y[1], y[2], y[3]), w = make_float4(y[4], y[5], y[6], y[7]);
+      if (whole) {
+        const float4 a = p[0], b = p[1];
+        u = make_float4(u.x + a.x, u.y + a.y, u.z + a.z, u.w + a.w);
+        w = make_float4(w.x + b.x, w.y + b.y, w.z + b.z, w.w + b.w);
+      }
+      p[0] = u;
+      p[1] = w;
     }
   }
   if (!ok) {
@@ -560,7 +612,10 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   for (int col = tid; col < DV; col += PD_THREADS)
 #pragma unroll
     for (int p = 0; p < 2 * PD_WARPS; ++p)
-      if (s_part[p] >= 0) sO[s_part[p] * DV + col] += sPart[p * DV + col];
+      if (s_part[p] >= 0) {
+        const float* part = p & 1 ? reinterpret_cast<const float*>(pd_smem + (p >> 1) * ST::N * ST::BYTES) : sPart + (p >> 1) * DV;
+        sO[s_part[p] * DV + col] += part[col];
+      }
   __syncthreads();
   for (int e = tid; e < cnt * (DV / 2); e += PD_THREADS) {
     const int i = e / (DV / 2), c = 2 * (e % (DV / 2));
