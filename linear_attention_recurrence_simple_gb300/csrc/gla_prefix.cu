@@ -113,9 +113,9 @@ prefix_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* 
 //     mma.m16n8k16 (bf16, fp32 sums), S split into hi + lo bf16 as it is read (16 significant bits; a
 //     single bf16 would put 2^-9 into every term).  A warp owns 48 columns; the S fragments go from
 //     global memory (L2 for all but one tile) to registers, nothing is staged.
-//   Tails: 16-token chunks, in order, of all the tile's sequences form one list that is cut evenly
+//   Tails: chunks of 16 or 32 tokens, in order, of all the tile's sequences form one list that is cut evenly
 //     over the warps, so one long tail among short ones, or a tile of one sequence, still feeds
-//     all of them.  A warp streams its chunks through a ring of its own in shared memory (bulk
+//     all of them.  A warp streams its chunks through a stage of its own in shared memory (bulk
 //     copies: the tokens of a (row, head) are contiguous) and multiplies on the tensor cores:
 //       weights   K [16 tokens x 96] times q (one column of N = 8 used): exact products.  E4M3 codes
 //                 widen exactly to f16; q is brought to f16 by a power of two (its 8 bits fit; what
@@ -130,22 +130,23 @@ prefix_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* 
 //     last sequence of a warp's range may be shared, and those parts meet in warp order.
 constexpr int TILE_MAX = 16;
 constexpr int PD_WARPS = 4, PD_THREADS = 32 * PD_WARPS;
-constexpr int PD_TOK = 16;  // tokens of a chunk
 
+// A warp's stage: one chunk, 32 tokens of MXFP8 or 16 of bf16 (9.5 and 9.2 KB: four CTAs per SM).  Keys
+// and values have a barrier each, so that the next chunk's keys land while this one's values are used.
 template <bool MX>
 struct PdStage {
+  static constexpr int TOK = MX ? 32 : 16, SUB = TOK / 16;  // tokens; 16-token steps of the MMAs
   static constexpr uint32_t K_ROW = MX ? DK : 2 * DK, V_ROW = MX ? DV : 2 * DV;  // bytes of a token
-  static constexpr uint32_t K = 0, V = K + PD_TOK * K_ROW, KS = V + PD_TOK * V_ROW, VS = KS + (MX ? 48 : 0);
-  static constexpr uint32_t BYTES = VS + (MX ? 96 : 0);
-  static constexpr int N = 2;  // stages of a warp's ring
+  static constexpr uint32_t K = 0, V = K + TOK * K_ROW, KS = V + TOK * V_ROW, VS = KS + (MX ? TOK * 3 : 0);
+  static constexpr uint32_t BYTES = VS + (MX ? TOK * 6 : 0);
 };
 template <bool MX>
 struct PdSmem {
-  static constexpr uint32_t O = PD_WARPS * PdStage<MX>::N * PdStage<MX>::BYTES;  // [16][192] sums
+  static constexpr uint32_t O = PD_WARPS * PdStage<MX>::BYTES;  // [16][192] sums
   static constexpr uint32_t PART = O + TILE_MAX * DV * 4;                        // [warps][192], a warp's first part
   static constexpr uint32_t Q = PART + PD_WARPS * DV * 4;                        // [16][96] bf16
   static constexpr uint32_t BAR = Q + TILE_MAX * DK * 2;
-  static constexpr uint32_t BYTES = BAR + PD_WARPS * PdStage<MX>::N * 8;
+  static constexpr uint32_t BYTES = BAR + PD_WARPS * 2 * 8;
 };
 
 template <bool F16>
@@ -205,7 +206,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
 }
 
 template <bool MX>
-__global__ void __launch_bounds__(PD_THREADS, MX ? 4 : 2)
+__global__ void __launch_bounds__(PD_THREADS, 4)
 prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
                           const __nv_bfloat16* __restrict__ v, const float* __restrict__ log_lambda, float scale,
                           const float* __restrict__ pool, int pool_rows, const int32_t* __restrict__ prefix_row, TailArgs t,
@@ -224,7 +225,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   float* sPart = reinterpret_cast<float*>(pd_smem + SM::PART);
   BF* sQ = reinterpret_cast<BF*>(pd_smem + SM::Q);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
-  uint64_t* full = reinterpret_cast<uint64_t*>(pd_smem + SM::BAR) + warp * ST::N;
+  uint64_t* full = reinterpret_cast<uint64_t*>(pd_smem + SM::BAR) + warp * 2;  // keys, values
   const int h = (int)(blockIdx.x % (unsigned)H), n0 = (int)(blockIdx.x / (unsigned)H) * tile_seqs;
   const int cnt = min(tile_seqs, N - n0);
   if (warp == 0) {
@@ -239,7 +240,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
       }
       if (tok0 < 0) row = -1;  // row -1: the sequence is skipped
     }
-    int chunks = row >= 0 ? (L + PD_TOK - 1) / PD_TOK : 0;
+    int chunks = row >= 0 ? (L + ST::TOK - 1) / ST::TOK : 0;
     if (lane < TILE_MAX) {
       s_row[lane] = row;
       s_len[lane] = L;
@@ -257,36 +258,48 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     }
   }
   if (lane == 0) {
-    for (int i = 0; i < ST::N; ++i) mbar_init(&full[i], 1);
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
     s_part[2 * warp] = s_part[2 * warp + 1] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
 
-  // ---- this warp's chunks [c0, c1) of the tile's list; the ring's first loads
+  // ---- this warp's chunks [c0, c1) of the tile's list; its first loads
   const long long total = s_cu[TILE_MAX];
   const int c0 = (int)(total * warp / PD_WARPS), c1 = (int)(total * (warp + 1) / PD_WARPS);
-  const uint32_t ring = smem_u32(pd_smem) + (uint32_t)(warp * ST::N) * ST::BYTES;
-  uint8_t* const ring_p = pd_smem + (size_t)(warp * ST::N) * ST::BYTES;
-  int issue_i = 0;  // sequence of the next chunk to load
-  auto issue = [&](int c) {  // whole warp; lanes 0 .. 3 take one of the copies each
-    while (c >= s_cu[issue_i + 1]) ++issue_i;
-    const int j0 = (c - s_cu[issue_i]) * PD_TOK, m = min(PD_TOK, s_len[issue_i] - j0);
-    const long long tok = s_tok0[issue_i] + j0;
-    const int s = (c - c0) % ST::N;
-    const uint32_t dst = ring + (uint32_t)s * ST::BYTES;
-    const uint32_t ks = MX ? (uint32_t)(3 * m + 15) / 16 * 16 : 0, vs = MX ? (uint32_t)(6 * m + 15) / 16 * 16 : 0;
-    if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)m * (ST::K_ROW + ST::V_ROW) + ks + vs);
-    __syncwarp();
-    if (lane < (MX ? 4 : 2)) {
-      const uint8_t* from = static_cast<const uint8_t*>(lane == 0 ? t.k : lane == 1 ? t.v : lane == 2 ? t.ks : t.vs);
-      const uint32_t row = lane == 0 ? ST::K_ROW : lane == 1 ? ST::V_ROW : lane == 2 ? DK / 32 : DV / 32;
-      bulk_copy(dst + (lane == 0 ? ST::K : lane == 1 ? ST::V : lane == 2 ? ST::KS : ST::VS), from + tok * row,
-                lane < 2 ? (uint32_t)m * row : lane == 2 ? ks : vs, &full[s]);
+  uint8_t* const st = pd_smem + (size_t)warp * ST::BYTES;
+  const uint32_t st32 = smem_u32(st);
+  // The next chunk to load (whole warp): lane 0 copies the elements or codes, lane 1 the scales.
+  int next = c0, next_seq = 0, next_m = 0, loads_k = 0, loads_v = 0;
+  long long next_tok = 0;
+  auto load_keys = [&]() {
+    while (next >= s_cu[next_seq + 1]) ++next_seq;
+    const int j0 = (next - s_cu[next_seq]) * ST::TOK;
+    next_m = min(ST::TOK, s_len[next_seq] - j0);
+    next_tok = s_tok0[next_seq] + j0;
+    ++next;
+    ++loads_k;
+    const uint32_t bytes = (uint32_t)next_m * ST::K_ROW, ks = MX ? (uint32_t)(3 * next_m + 15) / 16 * 16 : 0;
+    if (lane == 0) {
+      mbar_expect_tx(&full[0], bytes + ks);
+      bulk_copy(st32 + ST::K, static_cast<const uint8_t*>(t.k) + next_tok * ST::K_ROW, bytes, &full[0]);
+      if (MX) bulk_copy(st32 + ST::KS, t.ks + next_tok * (DK / 32), ks, &full[0]);
     }
   };
-  int issued = 0;
-  for (; issued < ST::N && c0 + issued < c1; ++issued) issue(c0 + issued);
+  auto load_values = [&]() {  // of the chunk whose keys were loaded last
+    ++loads_v;
+    const uint32_t bytes = (uint32_t)next_m * ST::V_ROW, vs = MX ? (uint32_t)(6 * next_m + 15) / 16 * 16 : 0;
+    if (lane == 0) {
+      mbar_expect_tx(&full[1], bytes + vs);
+      bulk_copy(st32 + ST::V, static_cast<const uint8_t*>(t.v) + next_tok * ST::V_ROW, bytes, &full[1]);
+      if (MX) bulk_copy(st32 + ST::VS, t.vs + next_tok * (DV / 32), vs, &full[1]);
+    }
+  };
+  if (c0 < c1) {
+    load_keys();
+    load_values();
+  }
 
   for (int e = tid; e < cnt * (DK / 8); e += PD_THREADS) {
     const int i = e / (DK / 8), p = e % (DK / 8);
@@ -428,74 +441,82 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
     int E = -1000;  // (MXFP8) exponent of the power of two of column g of w
     for (; c < last; ++c) {
-      const int it = c - c0, s = it % ST::N;
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)(it / ST::N) & 1u, wait_ns, &s_abort));
+      const uint32_t phase = (uint32_t)(c - c0) & 1u;
+      const int j0 = (c - first) * ST::TOK, m = min(ST::TOK, L - j0);
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[0], phase, wait_ns, &s_abort));
       if (!ok) break;
-      uint8_t* st = ring_p + (size_t)s * ST::BYTES;
-      const int j0 = (c - first) * PD_TOK, m = min(PD_TOK, L - j0);
-      if (m < PD_TOK) {
-        // rows past the tail's end hold another chunk's values or nothing: zero, so that their
-        // zero weights give zero
-        for (uint32_t e = lane; e < (uint32_t)(PD_TOK - m) * ST::V_ROW / 16; e += 32)
-          *reinterpret_cast<uint4*>(st + ST::V + (uint32_t)m * ST::V_ROW + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
-        __syncwarp();
-      }
-      // weights: token g in lanes tq = 0, element 0; token g + 8, element 2
-      float sc0, sc1;
-      {
+      // weights: token 16 u + g in lanes tq = 0, sc[u][0]; token 16 u + g + 8, sc[u][1]
+      float sc[ST::SUB][2];
+#pragma unroll
+      for (int u = 0; u < ST::SUB; ++u) {
+        const uint8_t* kr = st + ST::K + (uint32_t)(16 * u + g) * ST::K_ROW + (MX ? 8 : 16) * tq;
         float d[3][4];
-        float k0[3], k1[3];  // block scales of the two tokens' keys
-        if constexpr (MX) {
-          const uint8_t* kp = st + ST::KS + 3 * g;
-          const uint32_t u0 = e8m0x2_to_bf2(kp[0] | (uint32_t)kp[1] << 8), u1 = e8m0x2_to_bf2(kp[24] | (uint32_t)kp[25] << 8),
-                         u2 = e8m0x2_to_bf2(kp[2] | (uint32_t)kp[26] << 8);
-          k0[0] = __uint_as_float(u0 << 16);
-          k0[1] = __uint_as_float(u0 & 0xFFFF0000u);
-          k0[2] = __uint_as_float(u2 << 16);
-          k1[0] = __uint_as_float(u1 << 16);
-          k1[1] = __uint_as_float(u1 & 0xFFFF0000u);
-          k1[2] = __uint_as_float(u2 & 0xFFFF0000u);
-        }
 #pragma unroll
         for (int b = 0; b < 3; ++b) {
           if constexpr (MX) {
-            const uint2 x = *reinterpret_cast<const uint2*>(st + ST::K + (uint32_t)g * DK + 32 * b + 8 * tq);
-            const uint2 y = *reinterpret_cast<const uint2*>(st + ST::K + (uint32_t)(g + 8) * DK + 32 * b + 8 * tq);
+            const uint2 x = *reinterpret_cast<const uint2*>(kr + 32 * b), y = *reinterpret_cast<const uint2*>(kr + 8 * DK + 32 * b);
             mma16<true>(d[b], e4m3x2_to_h2(x.x & 0xFFFFu), e4m3x2_to_h2(y.x & 0xFFFFu), e4m3x2_to_h2(x.x >> 16),
                         e4m3x2_to_h2(y.x >> 16), qf[b][0], qf[b][1], 0.f, 0.f, 0.f, 0.f);
             mma16_add<true>(d[b], e4m3x2_to_h2(x.y & 0xFFFFu), e4m3x2_to_h2(y.y & 0xFFFFu), e4m3x2_to_h2(x.y >> 16),
                             e4m3x2_to_h2(y.y >> 16), qf[b][2], qf[b][3]);
           } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(st + ST::K + (uint32_t)g * ST::K_ROW + 64 * b + 16 * tq);
-            const uint4 y = *reinterpret_cast<const uint4*>(st + ST::K + (uint32_t)(g + 8) * ST::K_ROW + 64 * b + 16 * tq);
+            const uint4 x = *reinterpret_cast<const uint4*>(kr + 64 * b), y = *reinterpret_cast<const uint4*>(kr + 8 * ST::K_ROW + 64 * b);
             mma16<false>(d[b], x.x, y.x, x.y, y.y, qf[b][0], qf[b][1], 0.f, 0.f, 0.f, 0.f);
             mma16_add<false>(d[b], x.z, y.z, x.w, y.w, qf[b][2], qf[b][3]);
           }
         }
-        if constexpr (MX) {
-          sc0 = fmaf(d[2][0], k0[2], fmaf(d[1][0], k0[1], d[0][0] * k0[0]));
-          sc1 = fmaf(d[2][2], k1[2], fmaf(d[1][2], k1[1], d[0][2] * k1[0]));
+        if constexpr (MX) {  // the block scales of the two tokens' keys
+          const uint8_t* kp = st + ST::KS + 3 * (16 * u + g);
+          const uint32_t u0 = e8m0x2_to_bf2(kp[0] | (uint32_t)kp[1] << 8), u1 = e8m0x2_to_bf2(kp[24] | (uint32_t)kp[25] << 8),
+                         u2 = e8m0x2_to_bf2(kp[2] | (uint32_t)kp[26] << 8);
+          sc[u][0] = fmaf(d[2][0], __uint_as_float(u2 << 16),
+                          fmaf(d[1][0], __uint_as_float(u0 & 0xFFFF0000u), d[0][0] * __uint_as_float(u0 << 16)));
+          sc[u][1] = fmaf(d[2][2], __uint_as_float(u2 & 0xFFFF0000u),
+                          fmaf(d[1][2], __uint_as_float(u1 & 0xFFFF0000u), d[0][2] * __uint_as_float(u1 << 16)));
         } else {
-          sc0 = d[0][0] + d[1][0] + d[2][0];
-          sc1 = d[0][2] + d[1][2] + d[2][2];
+          sc[u][0] = d[0][0] + d[1][0] + d[2][0];
+          sc[u][1] = d[0][2] + d[1][2] + d[2][2];
         }
       }
-      // lane j < 16 takes token j's weight
-      const float from0 = __shfl_sync(0xffffffffu, sc0, (lane & 7) * 4), from1 = __shfl_sync(0xffffffffu, sc1, (lane & 7) * 4);
-      const float w = (lane & 15) < m ? ((lane & 8) ? from1 : from0) * qn * decay_pow(ll, L - j0 - (lane & 15)) : 0.f;
-      float wt[4];  // tokens tq, tq + 4, tq + 8, tq + 12
+      __syncwarp();
+      if (next < c1) load_keys();  // the keys are read
+      // lane j takes token j's weight (bf16: lanes 16 .. 31 repeat)
+      float w = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wt[i] = __shfl_sync(0xffffffffu, w, tq + 4 * i);
+      for (int u = 0; u < ST::SUB; ++u) {
+        const float lo = __shfl_sync(0xffffffffu, sc[u][0], (lane & 7) * 4), hi = __shfl_sync(0xffffffffu, sc[u][1], (lane & 7) * 4);
+        if (ST::SUB == 1 || (lane >> 4) == u) w = lane & 8 ? hi : lo;
+      }
+      const int jl = lane & (ST::TOK - 1);
+      w = jl < m ? w * qn * decay_pow(ll, L - j0 - jl) : 0.f;
+      float wt[ST::SUB][4];  // tokens 16 u + tq + 4 i
+#pragma unroll
+      for (int u = 0; u < ST::SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wt[u][i] = __shfl_sync(0xffffffffu, w, 16 * u + tq + 4 * i);
+
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[1], phase, wait_ns, &s_abort));
+      if (!ok) break;
+      if (m < ST::TOK) {
+        // rows past the tail's end hold another chunk's values or nothing: zero, so that their
+        // zero weights give zero
+        for (uint32_t e = lane; e < (uint32_t)(ST::TOK - m) * ST::V_ROW / 16; e += 32)
+          *reinterpret_cast<uint4*>(st + ST::V + (uint32_t)m * ST::V_ROW + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
       if constexpr (MX) {
-        const uint8_t* vp = st + ST::VS + 6 * tq + min(g, DV / 32 - 1);
-        const uint32_t u0 = e8m0x2_to_bf2(vp[0] | (uint32_t)vp[24] << 8), u1 = e8m0x2_to_bf2(vp[48] | (uint32_t)vp[72] << 8);
-        const float vs[4] = {__uint_as_float(u0 << 16), __uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 << 16),
-                             __uint_as_float(u1 & 0xFFFF0000u)};
         float mx = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          wt[i] = g < DV / 32 && tq + 4 * i < m ? wt[i] * vs[i] : 0.f;  // (a scale past the tail's end may be NaN)
-          mx = fmaxf(mx, fabsf(wt[i]));
+        for (int u = 0; u < ST::SUB; ++u) {
+          const uint8_t* vp = st + ST::VS + 6 * (16 * u + tq) + min(g, DV / 32 - 1);
+          const uint32_t u0 = e8m0x2_to_bf2(vp[0] | (uint32_t)vp[24] << 8), u1 = e8m0x2_to_bf2(vp[48] | (uint32_t)vp[72] << 8);
+          const float vs[4] = {__uint_as_float(u0 << 16), __uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 << 16),
+                               __uint_as_float(u1 & 0xFFFF0000u)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            wt[u][i] = g < DV / 32 && 16 * u + tq + 4 * i < m ? wt[u][i] * vs[i] : 0.f;  // (past the end: maybe NaN)
+            mx = fmaxf(mx, fabsf(wt[u][i]));
+          }
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -510,62 +531,62 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
             for (int e = 0; e < 4; ++e) acc[i][e] *= (e & 1) ? f1 : f0;
           if (grow) E = need;
         }
-        const float up = pow2i(4 - E);
+      }
+      const float up = MX ? pow2i(4 - E) : 1.f;
+#pragma unroll
+      for (int u = 0; u < ST::SUB; ++u) {
         uint32_t h0, h1, l0, l1;
-        split_h(wt[0] * up, wt[1] * up, h0, l0);
-        split_h(wt[2] * up, wt[3] * up, h1, l1);
+        const uint8_t* vr = st + ST::V + (uint32_t)(16 * u + tq) * ST::V_ROW + (MX ? 8 : 16) * g;
+        if constexpr (MX) {
+          split_h(wt[u][0] * up, wt[u][1] * up, h0, l0);
+          split_h(wt[u][2] * up, wt[u][3] * up, h1, l1);
 #pragma unroll
-        for (int B = 0; B < 3; ++B) {
-          uint2 x[4];
+          for (int B = 0; B < 3; ++B) {
+            uint2 x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = *reinterpret_cast<const uint2*>(st + ST::V + (uint32_t)(tq + 4 * i) * DV + 64 * B + 8 * g);
+            for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint2*>(vr + 4 * i * DV + 64 * B);
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {  // columns 64 B + 8 g + 2 jj (row g) and the next (row g + 8)
-            const uint32_t sel = jj & 1 ? 0x7362 : 0x5140;
-            const uint32_t p = __byte_perm(jj & 2 ? x[0].y : x[0].x, jj & 2 ? x[1].y : x[1].x, sel);
-            const uint32_t r = __byte_perm(jj & 2 ? x[2].y : x[2].x, jj & 2 ? x[3].y : x[3].x, sel);
-            const uint32_t a0 = e4m3x2_to_h2(p & 0xFFFFu), a1 = e4m3x2_to_h2(p >> 16), a2 = e4m3x2_to_h2(r & 0xFFFFu),
-                           a3 = e4m3x2_to_h2(r >> 16);
-            mma16_add<true>(acc[4 * B + jj], a0, a1, a2, a3, h0, h1);
-            mma16_add<true>(acc[4 * B + jj], a0, a1, a2, a3, l0, l1);
+            for (int jj = 0; jj < 4; ++jj) {  // columns 64 B + 8 g + 2 jj (row g) and the next (row g + 8)
+              const uint32_t sel = jj & 1 ? 0x7362 : 0x5140;
+              const uint32_t p = __byte_perm(jj & 2 ? x[0].y : x[0].x, jj & 2 ? x[1].y : x[1].x, sel);
+              const uint32_t r = __byte_perm(jj & 2 ? x[2].y : x[2].x, jj & 2 ? x[3].y : x[3].x, sel);
+              const uint32_t a0 = e4m3x2_to_h2(p & 0xFFFFu), a1 = e4m3x2_to_h2(p >> 16), a2 = e4m3x2_to_h2(r & 0xFFFFu),
+                             a3 = e4m3x2_to_h2(r >> 16);
+              mma16_add<true>(acc[4 * B + jj], a0, a1, a2, a3, h0, h1);
+              mma16_add<true>(acc[4 * B + jj], a0, a1, a2, a3, l0, l1);
+            }
           }
-        }
-      } else {
-        uint32_t h0, h1, l0, l1;
-        split_bf(wt[0], wt[1], h0, l0);
-        split_bf(wt[2], wt[3], h1, l1);
-        const uint32_t b0 = g & 1 ? l0 : h0, b1 = g & 1 ? l1 : h1;
+        } else {
+          split_bf(wt[u][0], wt[u][1], h0, l0);
+          split_bf(wt[u][2], wt[u][3], h1, l1);
+          const uint32_t b0 = g & 1 ? l0 : h0, b1 = g & 1 ? l1 : h1;
 #pragma unroll
-        for (int B = 0; B < 3; ++B) {
-          uint4 x[4];
+          for (int B = 0; B < 3; ++B) {
+            uint4 x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = *reinterpret_cast<const uint4*>(st + ST::V + (uint32_t)(tq + 4 * i) * ST::V_ROW + 128 * B + 16 * g);
+            for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(vr + 4 * i * ST::V_ROW + 128 * B);
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            const uint32_t x0 = jj == 0 ? x[0].x : jj == 1 ? x[0].y : jj == 2 ? x[0].z : x[0].w;
-            const uint32_t x1 = jj == 0 ? x[1].x : jj == 1 ? x[1].y : jj == 2 ? x[1].z : x[1].w;
-            const uint32_t x2 = jj == 0 ? x[2].x : jj == 1 ? x[2].y : jj == 2 ? x[2].z : x[2].w;
-            const uint32_t x3 = jj == 0 ? x[3].x : jj == 1 ? x[3].y : jj == 2 ? x[3].z : x[3].w;
-            mma16_add<false>(acc[4 * B + jj], __byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
-                             __byte_perm(x2, x3, 0x5410), __byte_perm(x2, x3, 0x7632), b0, b1);
+            for (int jj = 0; jj < 4; ++jj) {
+              const uint32_t x0 = jj == 0 ? x[0].x : jj == 1 ? x[0].y : jj == 2 ? x[0].z : x[0].w;
+              const uint32_t x1 = jj == 0 ? x[1].x : jj == 1 ? x[1].y : jj == 2 ? x[1].z : x[1].w;
+              const uint32_t x2 = jj == 0 ? x[2].x : jj == 1 ? x[2].y : jj == 2 ? x[2].z : x[2].w;
+              const uint32_t x3 = jj == 0 ? x[3].x : jj == 1 ? x[3].y : jj == 2 ? x[3].z : x[3].w;
+              mma16_add<false>(acc[4 * B + jj], __byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
+                               __byte_perm(x2, x3, 0x5410), __byte_perm(x2, x3, 0x7632), b0, b1);
+            }
           }
         }
       }
-      // the stage is read: refill it (the zeros above were written through the generic proxy)
-      if (m < PD_TOK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      // the values are read (the zeros above were written through the generic proxy)
+      if (m < ST::TOK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (c0 + issued < c1) {
-        issue(c0 + issued);
-        ++issued;
-      }
+      if (loads_v < loads_k) load_values();
     }
     if (!ok) break;
     // the sequence's sums (this warp's part of them): thread (g, tq < 3) holds columns 64 tq + 8 g
-    // .. + 7.  A part that the warp ends with goes to its ring (whose chunks have all been read).
+    // .. + 7.  A part that the warp ends with goes to its stage (whose chunks have all been read).
     const bool second = last == c1 && c0 < first;
-    float* dst = whole ? sO + seq * DV : second ? reinterpret_cast<float*>(ring_p) : sPart + warp * DV;
+    float* dst = whole ? sO + seq * DV : second ? reinterpret_cast<float*>(st) : sPart + warp * DV;
     if (!whole && lane == 0) s_part[2 * warp + second] = seq;
     const float back = MX ? pow2i(__shfl_sync(0xffffffffu, E, 4 * ((2 * tq + (g >> 2)) & 7)) - 4) : 1.f;
     float y[8];
@@ -599,10 +620,8 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   if (!ok) {
     // a wait gave up: no copy into this CTA's shared memory may be in flight when it exits
     if (lane == 0) {
-      for (int i = 0; i < ST::N; ++i) {
-        const int n_i = (issued - i + ST::N - 1) / ST::N;  // loads that went through stage i
-        if (n_i > 0) mbar_wait_drain(&full[i], (uint32_t)(n_i - 1) & 1u, 1000000000ull, err);
-      }
+      if (loads_k) mbar_wait_drain(&full[0], (uint32_t)(loads_k - 1) & 1u, 1000000000ull, err);
+      if (loads_v) mbar_wait_drain(&full[1], (uint32_t)(loads_v - 1) & 1u, 1000000000ull, err);
       raise_error(err, ERR_TIMEOUT);
     }
   }
@@ -613,7 +632,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
 #pragma unroll
     for (int p = 0; p < 2 * PD_WARPS; ++p)
       if (s_part[p] >= 0) {
-        const float* part = p & 1 ? reinterpret_cast<const float*>(pd_smem + (p >> 1) * ST::N * ST::BYTES) : sPart + (p >> 1) * DV;
+        const float* part = p & 1 ? reinterpret_cast<const float*>(pd_smem + (p >> 1) * ST::BYTES) : sPart + (p >> 1) * DV;
         sO[s_part[p] * DV + col] += part[col];
       }
   __syncthreads();
