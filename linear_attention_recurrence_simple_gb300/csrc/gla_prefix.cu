@@ -216,8 +216,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   using SM = PdSmem<MX>;
   using BF = __nv_bfloat16;
   extern __shared__ __align__(128) uint8_t pd_smem[];
-  __shared__ int s_row[TILE_MAX], s_len[TILE_MAX], s_cu[TILE_MAX + 1], s_part[2 * PD_WARPS];  // sequences of the shared parts, -1: none
- 
+  __shared__ int s_row[TILE_MAX], s_len[TILE_MAX], s_cu[TILE_MAX + 1], s_part[2 * PD_WARPS];  // s_part: sequences of the shared parts, -1: none
   __shared__ long long s_tok0[TILE_MAX];
   __shared__ float s_self[TILE_MAX];
   __shared__ int s_abort;
@@ -301,38 +300,52 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     load_values();
   }
 
+  for (int e = tid; e < cnt * (DV / 4); e += PD_THREADS) reinterpret_cast<float4*>(sO)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int e = tid; e < cnt * (DK / 8); e += PD_THREADS) {
     const int i = e / (DK / 8), p = e % (DK / 8);
     reinterpret_cast<uint4*>(sQ)[e] = *reinterpret_cast<const uint4*>(q + ((long long)(n0 + i) * H + h) * DK + 8 * p);
   }
   __syncthreads();
   const float ll = log_lambda[h];
-  // ---- the new tokens: q . k, and their places in the tails
-  for (int i = warp; i < cnt; i += PD_WARPS) {
-    if (s_row[i] < 0) continue;
-    const long long nh = (long long)(n0 + i) * H + h;
-    float x[16] = {};
-    float d = 0.f;
-    if (lane < DK / 16) {
-      float y[16];
-      load16(k + nh * DK + 16 * lane, x);
-      load16(sQ + i * DK + 16 * lane, y);
+  // The shared states' part and the new tokens first in one half of the CTAs and last in the other: their
+  // latencies then fall into the others' streams.
+  // (the hash mixes both halves on every SM: CTAs i, i + 152, ... tend to share one)
+  const int late = (int)((blockIdx.x ^ (blockIdx.x >> 3)) & 1u);
+  bool ok = true;
+  for (int step = 0; step < 2; ++step) {
+   if (step == late) {
+    // ---- the new tokens: q . k, and their places in the tails.  All of a thread's loads go out at
+    // once: eight lanes a sequence for its key, sixteen for its value.
+    {
+      float x[16] = {}, y[2][16] = {};
+      const int ik = warp + PD_WARPS * (lane >> 3), pk = lane & 7;
+      const bool live = ik < cnt && s_row[ik] >= 0 && pk < DK / 16;
+      if (live) load16(k + ((long long)(n0 + ik) * H + h) * DK + 16 * pk, x);
+      const int pv = lane & 15;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) d = fmaf(x[e], y[e], d);
+      for (int u = 0; u < 2; ++u) {
+        const int iv = warp + PD_WARPS * (2 * u + (lane >> 4));
+        if (iv < cnt && s_row[iv] >= 0 && pv < DV / 16) load16(v + ((long long)(n0 + iv) * H + h) * DV + 16 * pv, y[u]);
+      }
+      float d = 0.f;
+      if (live) {
+        float z[16];
+        load16(sQ + ik * DK + 16 * pk, z);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) d = fmaf(x[e], z[e], d);
+      }
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+      if (live && pk == 0) s_self[ik] = d;
+      tail_store16<BF, MX, DK>(t.k, t.ks, live ? s_tok0[ik] + s_len[ik] : 0, pk, x, live);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int iv = warp + PD_WARPS * (2 * u + (lane >> 4));
+        const bool lv = iv < cnt && s_row[iv] >= 0 && pv < DV / 16;
+        tail_store16<BF, MX, DV>(t.v, t.vs, lv ? s_tok0[iv] + s_len[iv] : 0, pv, y[u], lv);
+      }
     }
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-    if (lane == 0) s_self[i] = d;
-    const long long at = s_tok0[i] + s_len[i];
-    tail_store16<BF, MX, DK>(t.k, t.ks, at, lane, x, lane < DK / 16);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.f;
-    if (lane < DV / 16) load16(v + nh * DV + 16 * lane, x);
-    tail_store16<BF, MX, DV>(t.v, t.vs, at, lane, x, lane < DV / 16);
-  }
-
-  // ---- the shared states
-  {
+    // ---- the shared states
     // q fragments; K step s of thread tq: columns 16 s + 4 tq .. + 3 (the same order as S's rows)
     uint2 qa[6], qb[6];
     const BF* q0 = sQ + g * DK + 4 * tq;
@@ -382,16 +395,13 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
           for (int e = 0; e < 4; ++e) {
             const int r = g + 8 * (e >> 1), nn = 2 * tq + (e & 1);
             const int c = 48 * warp + (j < 4 ? 4 * nn + j : 32 + 2 * nn + (j - 4));
-            if (r >= r0 && r < r1) sO[r * DV + c] = d[j][e] * (e >> 1 ? f1 : f0);
+            if (r >= r0 && r < r1) sO[r * DV + c] += d[j][e] * (e >> 1 ? f1 : f0);
           }
       }
       r0 = r1;
     }
-  }
-  __syncthreads();
-
+   } else {
   // ---- the tails
-  bool ok = true;
   int seq = 0;
   for (int c = c0; c < c1 && ok;) {
     while (c >= s_cu[seq + 1]) ++seq;
@@ -616,6 +626,9 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
       p[0] = u;
       p[1] = w;
     }
+  }
+   }
+   __syncthreads();
   }
   if (!ok) {
     // a wait gave up: no copy into this CTA's shared memory may be in flight when it exits
