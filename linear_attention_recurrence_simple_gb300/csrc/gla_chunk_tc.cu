@@ -1376,6 +1376,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_stream_mu;
 cudaStream_t g_side[kMaxDevices][2];
+}  // namespace
 
 cudaError_t side_streams(cudaStream_t (&out)[2]) {
   int dev = 0;
@@ -1392,7 +1393,6 @@ cudaError_t side_streams(cudaStream_t (&out)[2]) {
   }
   return cudaSuccess;
 }
-}  // namespace
 
 // Backward in bf16: dv and dh0 directly; dq and dk through fp32 partial sums in acc_q / acc_k
 // (each tc_bwd_acc_bytes, 16-byte aligned), each rounded to bf16 once its scan is done.  The three

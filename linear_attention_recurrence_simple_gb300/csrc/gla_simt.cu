@@ -25,6 +25,9 @@
 #include "gla_common.cuh"
 
 namespace gla {
+
+cudaError_t side_streams(cudaStream_t (&out)[2]);  // the backward's two, per device
+
 namespace {
 
 constexpr int SC = 64;          // chunk length of these kernels
@@ -522,12 +525,31 @@ cudaError_t launch_simt_fwd(const ChunkArgs& a, cudaStream_t stream) {
   return launch(simt_wide_kernel<float, false>, FWD_TILES, FWD_SMEM, a, stream);
 }
 
-// The fp32 mode's backward (bf16 inputs go through the tensor-core scans).
+// The fp32 mode's backward (bf16 inputs go through the tensor-core scans).  The three scans are
+// independent: continuations of shared states, of which a call may hold few and short ones, run them
+// side by side on the backward's side streams.
 cudaError_t launch_simt_bwd(int dtype_f32, const ChunkArgs& a, cudaStream_t stream) {
   if (!dtype_f32) return cudaErrorInvalidValue;
-  cudaError_t e = launch(simt_bwd_narrow_kernel<float, false>, BQ_TILES, BQ_SMEM, a, stream);
-  if (e == cudaSuccess) e = launch(simt_bwd_narrow_kernel<float, true>, BQ_TILES, BQ_SMEM, a, stream);
+  cudaStream_t side[2] = {stream, stream};
+  cudaEvent_t ev[3] = {nullptr, nullptr, nullptr};
+  cudaError_t e = cudaSuccess;
+  if (a.h0_row) {
+    e = side_streams(side);
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = cudaEventCreateWithFlags(&ev[i], cudaEventDisableTiming);
+    if (e == cudaSuccess) e = cudaEventRecord(ev[2], stream);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = cudaStreamWaitEvent(side[i], ev[2], 0);
+  }
+  if (e == cudaSuccess) e = launch(simt_bwd_narrow_kernel<float, false>, BQ_TILES, BQ_SMEM, a, side[0]);
+  if (e == cudaSuccess) e = launch(simt_bwd_narrow_kernel<float, true>, BQ_TILES, BQ_SMEM, a, side[1]);
   if (e == cudaSuccess) e = launch(simt_wide_kernel<float, true>, FWD_TILES, FWD_SMEM, a, stream);
+  if (a.h0_row) {
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+      e = cudaEventRecord(ev[i], side[i]);
+      if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, ev[i], 0);
+    }
+    for (int i = 0; i < 3; ++i)
+      if (ev[i]) cudaEventDestroy(ev[i]);
+  }
   return e;
 }
 

@@ -37,8 +37,9 @@ int current_device_state(unsigned** err, unsigned long long* wait_ns);
 namespace {
 
 // ---- packed tokens to and from the tails -----------------------------------------------------
-// One CTA takes TOK consecutive packed tokens of one head: its reads (writes) of the packed arrays
-// are rows of >= 192 bytes, its writes (reads) of the tails contiguous pieces of TOK tokens.
+// One CTA takes COPY_TOK consecutive packed tokens of one head: its reads (writes) of the packed arrays
+// are rows of >= 192 bytes, its writes (reads) of the tails contiguous pieces of COPY_TOK tokens.
+// The heads of the same tokens are neighbouring CTAs, which share the packed arrays' lines in L2.
 // A thread holds one 16-value piece; the 18 pieces of a token sit in consecutive lanes, so the two
 // halves of a 32-value block are lanes l and l ^ 1 (18 and 32 are even).
 constexpr int COPY_THREADS = 288;  // 16 tokens' pieces a pass
@@ -51,9 +52,7 @@ tail_copy_kernel(T* __restrict__ k, T* __restrict__ v, TailArgs t, const int32_t
                  int H, unsigned* err) {
   __shared__ long long s_token[COPY_TOK];
   const int tid = threadIdx.x;
-  const int tiles = (T_total + COPY_TOK - 1) / COPY_TOK;
-  const int tile = (int)(blockIdx.x % (unsigned)tiles), h = (int)(blockIdx.x / (unsigned)tiles);
-  const int t0 = tile * COPY_TOK;
+  const int h = (int)(blockIdx.x % (unsigned)H), t0 = (int)(blockIdx.x / (unsigned)H) * COPY_TOK;
   if (tid < COPY_TOK) {
     // the sequence n with cu[n] <= tok < cu[n + 1]: the last n with cu[n] <= tok
     const int tok = t0 + tid;
@@ -77,42 +76,55 @@ tail_copy_kernel(T* __restrict__ k, T* __restrict__ v, TailArgs t, const int32_t
     s_token[tid] = at;
   }
   __syncthreads();
+  // All of the thread's loads first (the tails and the packed arrays may not be assumed apart by the
+  // compiler), then the conversions and stores.
+  constexpr int PER = COPY_TOK * TOKEN_PIECES / COPY_THREADS;
+  constexpr int WORDS = !WRITE && MX ? 1 : (int)sizeof(T);  // 16-byte words of a piece as it is read
   const int p = tid % TOKEN_PIECES;
+  const bool is_k = p < DK / 16;
+  const int pp = is_k ? p : p - DK / 16, d = is_k ? DK : DV;
+  T* const packed = is_k ? k : v;
+  uint8_t* const tail = static_cast<uint8_t*>(is_k ? t.k : t.v);
+  uint8_t* const scales = is_k ? t.ks : t.vs;
+  uint4 raw[PER][WORDS];
+  uint32_t sc[PER];
 #pragma unroll
-  for (int i = 0; i < COPY_TOK * TOKEN_PIECES / COPY_THREADS; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int r = tid / TOKEN_PIECES + i * (COPY_THREADS / TOKEN_PIECES);
-    const long long at = s_token[r];
-    const long long row = ((long long)(t0 + r) * H + h);
-    const bool live = at >= 0;
-    float x[16];
-    if constexpr (WRITE) {
+    const long long at = s_token[r], row = (long long)(t0 + r) * H + h;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.f;
-      if (live) {
-        if (p < DK / 16) load16(k + row * DK + 16 * p, x);
-        else load16(v + row * DV + 16 * (p - DK / 16), x);
+    for (int w = 0; w < WORDS; ++w) raw[i][w] = make_uint4(0u, 0u, 0u, 0u);
+    sc[i] = 0;
+    if (at >= 0) {
+      const uint8_t* from = WRITE ? reinterpret_cast<const uint8_t*>(packed + row * d + 16 * pp)
+                                  : tail + at * d * (MX ? 1 : sizeof(T)) + 16 * WORDS * pp;
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w) raw[i][w] = reinterpret_cast<const uint4*>(from)[w];
+      if (!WRITE && MX) sc[i] = scales[at * (d / 32) + (pp >> 1)];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int r = tid / TOKEN_PIECES + i * (COPY_THREADS / TOKEN_PIECES);
+    const long long at = s_token[r], row = (long long)(t0 + r) * H + h;
+    if constexpr (WRITE && MX) {
+      float x[16];
+      load16(reinterpret_cast<const T*>(raw[i]), x);
+      const int se = mx_shared_exp(block_max(x));  // (every lane of the warp: the halves of a block exchange)
+      if (at >= 0) {
+        *(reinterpret_cast<uint4*>(tail + at * d) + pp) = quantise16(x, se);
+        if ((pp & 1) == 0) scales[at * (d / 32) + (pp >> 1)] = (uint8_t)(se + 127);
       }
-      // one shape of call for both arrays, so that every lane of the warp meets in its shuffle
-      const bool is_k = p < DK / 16;
-      if constexpr (MX) {
-        const int se = mx_shared_exp(block_max(x));
-        if (live) {
-          const int pp = is_k ? p : p - DK / 16;
-          uint8_t* codes = static_cast<uint8_t*>(is_k ? t.k : t.v) + at * (is_k ? DK : DV) + 16 * pp;
-          *reinterpret_cast<uint4*>(codes) = quantise16(x, se);
-          if ((pp & 1) == 0) (is_k ? t.ks : t.vs)[at * (is_k ? DK / 32 : DV / 32) + (pp >> 1)] = (uint8_t)(se + 127);
-        }
-      } else if (live) {
-        if (is_k) store16(static_cast<T*>(t.k) + at * DK + 16 * p, x);
-        else store16(static_cast<T*>(t.v) + at * DV + 16 * (p - DK / 16), x);
-      }
-    } else if (live) {
-      if (p < DK / 16) {
-        tail_load16<T, MX, DK>(t.k, t.ks, at, p, x);
-        store16(k + row * DK + 16 * p, x);
+    } else if (at >= 0) {
+      if constexpr (!WRITE && MX) {
+        float x[16];
+        dequantise16(raw[i][0], e8m0_to_f(sc[i]), x);
+        store16(packed + row * d + 16 * pp, x);
       } else {
-        tail_load16<T, MX, DV>(t.v, t.vs, at, p - DK / 16, x);
-        store16(v + row * DV + 16 * (p - DK / 16), x);
+        uint8_t* to = WRITE ? tail + at * d * (long long)sizeof(T) + 16 * WORDS * pp
+                            : reinterpret_cast<uint8_t*>(packed + row * d + 16 * pp);
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) reinterpret_cast<uint4*>(to)[w] = raw[i][w];
       }
     }
   }
@@ -219,15 +231,16 @@ tail_fold_kernel(const float* __restrict__ log_lambda, const float* pool, int po
 // straight from and to global memory:
 //     D1 = columns 0 .. 127 (M = 128), D2 = columns 128 .. 191 (M = 128, its upper half unused),
 //     N = 96, K = tokens, 16 a step; both operands MN-major (a token is a row of 128-byte panels).
-// The weighted key is split into hi + lo bf16 (16 significant bits; two MMAs into one sum), the value
-// is bf16 or an E4M3 code times a power of two: exact in bf16.  Threads load 16-value pieces of the next
+// The weighted key is split into three bf16 (24 significant bits, all that its fp32 value has; three
+// MMAs into one sum: two would leave 2.5e-6 of the state's norm), the value is bf16 or an E4M3 code
+// times a power of two: exact in bf16.  Threads load 16-value pieces of the next
 // 32 tokens into registers while the tensor core works on the previous ones, widen, weight and
 // split them, and store them swizzled; two buffers.  Bound by HBM: 73.7 KB written per
 // (sequence, head) and the tail read once; two CTAs per SM cover each other's epilogue.
 constexpr int FT_THREADS = 192, FT_TOK = 32;
 constexpr uint32_t FT_PANEL = FT_TOK * 128;                       // 32 tokens x 64 columns of bf16
-constexpr uint32_t FT_V = 0, FT_KH = 3 * FT_PANEL, FT_KL = 5 * FT_PANEL, FT_BUF = 7 * FT_PANEL;
-// (D2's unused upper half reads the panel after V's last, which is KH's first)
+constexpr uint32_t FT_V = 0, FT_K = 3 * FT_PANEL, FT_TERM = 2 * FT_PANEL, FT_BUF = FT_K + 3 * FT_TERM;
+// (D2's unused upper half reads the panel after V's last, which is the key's first)
 constexpr uint32_t FT_SMEM = 80 * 1024;  // two buffers and alignment; sized for two CTAs per SM (tensor memory)
 static_assert(2 * FT_BUF + 1024 <= FT_SMEM, "fold buffers");
 constexpr int FT_PER = FT_TOK * TOKEN_PIECES / FT_THREADS;  // 3 pieces of a thread
@@ -320,20 +333,32 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
       uint32_t hi[8];
       if (is_k) {
         const float w = j < L ? decay_pow(ll, L - 1 - j) : 0.f;
-        uint32_t lo[8];
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          const float a = w * x[2 * s], c2 = w * x[2 * s + 1];
-          hi[s] = fold_pack(a, c2);
-          lo[s] = fold_pack(a - __uint_as_float(hi[s] << 16), c2 - __uint_as_float(hi[s] & 0xFFFF0000u));
+          x[2 * s] *= w;
+          x[2 * s + 1] *= w;
         }
-        st_shared_v4(row + FT_KL + x0, lo[0], lo[1], lo[2], lo[3]);
-        st_shared_v4(row + FT_KL + x1, lo[4], lo[5], lo[6], lo[7]);
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          if (term > 0) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {  // what the terms so far leave (exact)
+              x[2 * s] -= __uint_as_float(hi[s] << 16);
+              x[2 * s + 1] -= __uint_as_float(hi[s] & 0xFFFF0000u);
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < 8; ++s) hi[s] = fold_pack(x[2 * s], x[2 * s + 1]);
+          if (term < 2) {
+            st_shared_v4(row + FT_K + (uint32_t)term * FT_TERM + x0, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(row + FT_K + (uint32_t)term * FT_TERM + x1, hi[4], hi[5], hi[6], hi[7]);
+          }
+        }
       } else {
 #pragma unroll
         for (int s = 0; s < 8; ++s) hi[s] = fold_pack(x[2 * s], x[2 * s + 1]);
       }
-      const uint32_t to = row + (is_k ? FT_KH : FT_V);
+      const uint32_t to = row + (is_k ? FT_K + 2 * FT_TERM : FT_V);
       st_shared_v4(to + x0, hi[0], hi[1], hi[2], hi[3]);
       st_shared_v4(to + x1, hi[4], hi[5], hi[6], hi[7]);
     }
@@ -371,12 +396,13 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
       tc_fence_after();
       const uint32_t buf = base + (uint32_t)b * FT_BUF;
       const SDesc a = sdesc(buf + FT_V + (uint32_t)warp * 2u * FT_PANEL, FT_PANEL, 1024, LAYOUT_SW128);
-      const SDesc kh = sdesc(buf + FT_KH, FT_PANEL, 1024, LAYOUT_SW128), kl = sdesc(buf + FT_KL, FT_PANEL, 1024, LAYOUT_SW128);
+      const SDesc kd = sdesc(buf + FT_K, FT_PANEL, 1024, LAYOUT_SW128);
 #pragma unroll
-      for (int kk = 0; kk < FT_TOK / 16; ++kk) {
-        umma(tmem + (uint32_t)warp * DK, a + (uint32_t)kk * 2048u, kh + (uint32_t)kk * 2048u, ID, c > 0 || kk > 0);
-        umma(tmem + (uint32_t)warp * DK, a + (uint32_t)kk * 2048u, kl + (uint32_t)kk * 2048u, ID, 1);
-      }
+      for (int kk = 0; kk < FT_TOK / 16; ++kk)
+#pragma unroll
+        for (int term = 0; term < 3; ++term)
+          umma(tmem + (uint32_t)warp * DK, a + (uint32_t)kk * 2048u, kd + (uint32_t)term * FT_TERM + (uint32_t)kk * 2048u, ID,
+               c > 0 || kk > 0 || term > 0);
       umma_commit(&s_bar[b]);
     }
     ++issued;
