@@ -243,8 +243,7 @@ constexpr uint32_t FT_V = 0, FT_K = 3 * FT_PANEL, FT_TERM = 2 * FT_PANEL, FT_BUF
 // (D2's unused upper half reads the panel after V's last, which is the key's first)
 constexpr uint32_t FT_SMEM = 80 * 1024;  // two buffers and alignment; sized for two CTAs per SM (tensor memory)
 static_assert(2 * FT_BUF + 1024 <= FT_SMEM, "fold buffers");
-constexpr int FT_PER = FT_TOK * TOKEN_PIECES / FT_THREADS;  // 3 pieces of a thread
-static_assert(FT_PER * FT_THREADS == FT_TOK * TOKEN_PIECES, "whole pieces");
+static_assert(FT_TOK * 6 == FT_THREADS && FT_TOK * 12 == 2 * FT_THREADS, "whole pieces");
 constexpr uint32_t FT_TMEM = 256;  // columns: D1 at 0, D2 at 96
 
 __device__ __forceinline__ uint32_t fold_pack(float lo, float hi) {
@@ -275,92 +274,86 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
   const float ll = log_lambda[h];
   const int chunks = (L + FT_TOK - 1) / FT_TOK;
 
-  // this thread's pieces of a chunk: token jt[i] of 32, piece pp of 18 (6 of k, then 12 of v)
-  uint4 raw[FT_PER][MX ? 1 : 2];
-  uint32_t rs[FT_PER];
+  // This thread's pieces of a chunk: one 16-value piece of a key (token tid / 6, piece tid % 6) and two
+  // of values (tokens tid / 12 and 16 + tid / 12, piece tid % 12), so that no warp mixes the two.
+  constexpr int W = MX ? 1 : 2;  // 16-byte words of a piece
+  constexpr uint32_t K_ROW = (MX ? 1 : 2) * DK, V_ROW = (MX ? 1 : 2) * DV;
+  const int kj = tid / 6, kp = tid % 6, vj = tid / 12, vp = tid % 12;
+  const uint8_t* k_at = static_cast<const uint8_t*>(t.k) + (tok0 + kj) * K_ROW + 16 * W * kp;
+  const uint8_t* v_at = static_cast<const uint8_t*>(t.v) + (tok0 + vj) * V_ROW + 16 * W * vp;
+  const uint8_t* ks_at = MX ? t.ks + (tok0 + kj) * (DK / 32) + (kp >> 1) : nullptr;
+  const uint8_t* vs_at = MX ? t.vs + (tok0 + vj) * (DV / 32) + (vp >> 1) : nullptr;
+  uint4 rk[W], rv[2][W];
+  uint32_t sk = 0, sv[2] = {0, 0};
   auto load = [&](int c) {
+    const bool lk = c * FT_TOK + kj < L;
 #pragma unroll
-    for (int i = 0; i < FT_PER; ++i) {
-      const int e = tid + FT_THREADS * i, jt = e / TOKEN_PIECES, p = e % TOKEN_PIECES, j = c * FT_TOK + jt;
-      const bool is_k = p < DK / 16;
-      const int pp = is_k ? p : p - DK / 16;
-      raw[i][0] = make_uint4(0u, 0u, 0u, 0u);
-      if (!MX) raw[i][MX ? 0 : 1] = make_uint4(0u, 0u, 0u, 0u);
-      rs[i] = 0;
-      if (j < L) {
-        const long long at = tok0 + j;
-        const int d = is_k ? DK : DV;
-        const uint8_t* b = static_cast<const uint8_t*>(is_k ? t.k : t.v);
-        if constexpr (MX) {
-          raw[i][0] = *(reinterpret_cast<const uint4*>(b + at * d) + pp);
-          rs[i] = (is_k ? t.ks : t.vs)[at * (d / 32) + (pp >> 1)];
-        } else {
-          raw[i][0] = *(reinterpret_cast<const uint4*>(b + at * 2 * d) + 2 * pp);
-          raw[i][1] = *(reinterpret_cast<const uint4*>(b + at * 2 * d) + 2 * pp + 1);
-        }
-      }
+    for (int w = 0; w < W; ++w) rk[w] = lk ? reinterpret_cast<const uint4*>(k_at)[w] : make_uint4(0u, 0u, 0u, 0u);
+    if (MX) sk = lk ? *ks_at : 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool lv = c * FT_TOK + vj + 16 * u < L;
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        rv[u][w] = lv ? reinterpret_cast<const uint4*>(v_at + 16 * u * V_ROW)[w] : make_uint4(0u, 0u, 0u, 0u);
+      if (MX) sv[u] = lv ? vs_at[16 * u * (DV / 32)] : 0;
+    }
+    k_at += FT_TOK * K_ROW;
+    v_at += FT_TOK * V_ROW;
+    if (MX) {
+      ks_at += FT_TOK * (DK / 32);
+      vs_at += FT_TOK * (DV / 32);
     }
   };
-  // widened, weighted, split and stored to buffer b
+  // Stores a piece's two 16-byte halves, swizzled; odd panels store the second half first, so that the
+  // eight lanes of a store phase meet eight different bank groups.
+  auto put = [&](uint32_t panels, int j, int piece, const uint32_t (&x)[8]) {
+    const uint32_t row = panels + (uint32_t)(piece >> 2) * FT_PANEL + (uint32_t)j * 128u;
+    const uint32_t a0 = row + ((uint32_t)(((piece & 3) * 2) ^ (j & 7)) << 4), a1 = row + ((uint32_t)(((piece & 3) * 2 + 1) ^ (j & 7)) << 4);
+    const bool odd = piece & 4;
+    st_shared_v4(odd ? a1 : a0, odd ? x[4] : x[0], odd ? x[5] : x[1], odd ? x[6] : x[2], odd ? x[7] : x[3]);
+    st_shared_v4(odd ? a0 : a1, odd ? x[0] : x[4], odd ? x[1] : x[5], odd ? x[2] : x[6], odd ? x[3] : x[7]);
+  };
+  // Widened, weighted, split and stored to buffer b.
   auto store = [&](int c, int b) {
+    const uint32_t buf = base + (uint32_t)b * FT_BUF;
+    float x[16];
+    if constexpr (MX) dequantise16(rk[0], e8m0_to_f(sk), x);
+    else load16(reinterpret_cast<const __nv_bfloat16*>(rk), x);
+    const int j = c * FT_TOK + kj;
+    const float w = j < L ? decay_pow(ll, L - 1 - j) : 0.f;
 #pragma unroll
-    for (int i = 0; i < FT_PER; ++i) {
-      const int e = tid + FT_THREADS * i, jt = e / TOKEN_PIECES, p = e % TOKEN_PIECES, j = c * FT_TOK + jt;
-      const bool is_k = p < DK / 16;
-      const int pp = is_k ? p : p - DK / 16;
-      const uint32_t row = base + (uint32_t)b * FT_BUF + (uint32_t)(pp >> 2) * FT_PANEL + (uint32_t)jt * 128u;
-      const uint32_t x0 = (uint32_t)(((pp & 3) * 2) ^ (jt & 7)) << 4, x1 = (uint32_t)(((pp & 3) * 2 + 1) ^ (jt & 7)) << 4;
-      if (!MX && !is_k) {
-        st_shared_v4(row + FT_V + x0, raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w);
-        const uint4 r1 = raw[i][MX ? 0 : 1];
-        st_shared_v4(row + FT_V + x1, r1.x, r1.y, r1.z, r1.w);
-        continue;
+    for (int s = 0; s < 16; ++s) x[s] *= w;
+#pragma unroll
+    for (int term = 0; term < 3; ++term) {
+      uint32_t y[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        y[s] = fold_pack(x[2 * s], x[2 * s + 1]);
+        if (term < 2) {  // what this term leaves (exact)
+          x[2 * s] -= __uint_as_float(y[s] << 16);
+          x[2 * s + 1] -= __uint_as_float(y[s] & 0xFFFF0000u);
+        }
       }
-      float x[16];
+      put(buf + FT_K + (uint32_t)term * FT_TERM, kj, kp, y);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t y[8];
       if constexpr (MX) {
-        dequantise16(raw[i][0], e8m0_to_f(rs[i]), x);
+        dequantise16(rv[u][0], e8m0_to_f(sv[u]), x);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) y[s] = fold_pack(x[2 * s], x[2 * s + 1]);
       } else {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t w[4] = {raw[i][q].x, raw[i][q].y, raw[i][q].z, raw[i][q].w};
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            x[8 * q + 2 * s] = __uint_as_float(w[s] << 16);
-            x[8 * q + 2 * s + 1] = __uint_as_float(w[s] & 0xFFFF0000u);
-          }
+        for (int q = 0; q < W; ++q) {
+          y[4 * q] = rv[u][q].x;
+          y[4 * q + 1] = rv[u][q].y;
+          y[4 * q + 2] = rv[u][q].z;
+          y[4 * q + 3] = rv[u][q].w;
         }
       }
-      uint32_t hi[8];
-      if (is_k) {
-        const float w = j < L ? decay_pow(ll, L - 1 - j) : 0.f;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          x[2 * s] *= w;
-          x[2 * s + 1] *= w;
-        }
-#pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          if (term > 0) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {  // what the terms so far leave (exact)
-              x[2 * s] -= __uint_as_float(hi[s] << 16);
-              x[2 * s + 1] -= __uint_as_float(hi[s] & 0xFFFF0000u);
-            }
-          }
-#pragma unroll
-          for (int s = 0; s < 8; ++s) hi[s] = fold_pack(x[2 * s], x[2 * s + 1]);
-          if (term < 2) {
-            st_shared_v4(row + FT_K + (uint32_t)term * FT_TERM + x0, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(row + FT_K + (uint32_t)term * FT_TERM + x1, hi[4], hi[5], hi[6], hi[7]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int s = 0; s < 8; ++s) hi[s] = fold_pack(x[2 * s], x[2 * s + 1]);
-      }
-      const uint32_t to = row + (is_k ? FT_K + 2 * FT_TERM : FT_V);
-      st_shared_v4(to + x0, hi[0], hi[1], hi[2], hi[3]);
-      st_shared_v4(to + x1, hi[4], hi[5], hi[6], hi[7]);
+      put(buf + FT_V, vj + 16 * u, vp, y);
     }
   };
 
