@@ -7,6 +7,7 @@
 // the fold evaluates the sum.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "gla_tail.cuh"
 #include "gla_tc.cuh"
@@ -283,20 +284,22 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
   const uint8_t* v_at = static_cast<const uint8_t*>(t.v) + (tok0 + vj) * V_ROW + 16 * W * vp;
   const uint8_t* ks_at = MX ? t.ks + (tok0 + kj) * (DK / 32) + (kp >> 1) : nullptr;
   const uint8_t* vs_at = MX ? t.vs + (tok0 + vj) * (DV / 32) + (vp >> 1) : nullptr;
-  uint4 rk[W], rv[2][W];
-  uint32_t sk = 0, sv[2] = {0, 0};
-  auto load = [&](int c) {
+  // Two chunks' pieces in flight: chunk c's sit in set c & 1 (a compile-time index).
+  uint4 rk[2][W], rv[2][2][W];
+  uint32_t sk[2] = {0, 0}, sv[2][2] = {{0, 0}, {0, 0}};
+  auto load = [&](auto set_t, int c) {
+    constexpr int S = decltype(set_t)::value;
     const bool lk = c * FT_TOK + kj < L;
 #pragma unroll
-    for (int w = 0; w < W; ++w) rk[w] = lk ? reinterpret_cast<const uint4*>(k_at)[w] : make_uint4(0u, 0u, 0u, 0u);
-    if (MX) sk = lk ? *ks_at : 0;
+    for (int w = 0; w < W; ++w) rk[S][w] = lk ? reinterpret_cast<const uint4*>(k_at)[w] : make_uint4(0u, 0u, 0u, 0u);
+    if (MX) sk[S] = lk ? *ks_at : 0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool lv = c * FT_TOK + vj + 16 * u < L;
 #pragma unroll
       for (int w = 0; w < W; ++w)
-        rv[u][w] = lv ? reinterpret_cast<const uint4*>(v_at + 16 * u * V_ROW)[w] : make_uint4(0u, 0u, 0u, 0u);
-      if (MX) sv[u] = lv ? vs_at[16 * u * (DV / 32)] : 0;
+        rv[S][u][w] = lv ? reinterpret_cast<const uint4*>(v_at + 16 * u * V_ROW)[w] : make_uint4(0u, 0u, 0u, 0u);
+      if (MX) sv[S][u] = lv ? vs_at[16 * u * (DV / 32)] : 0;
     }
     k_at += FT_TOK * K_ROW;
     v_at += FT_TOK * V_ROW;
@@ -314,12 +317,13 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
     st_shared_v4(odd ? a1 : a0, odd ? x[4] : x[0], odd ? x[5] : x[1], odd ? x[6] : x[2], odd ? x[7] : x[3]);
     st_shared_v4(odd ? a0 : a1, odd ? x[0] : x[4], odd ? x[1] : x[5], odd ? x[2] : x[6], odd ? x[3] : x[7]);
   };
-  // Widened, weighted, split and stored to buffer b.
-  auto store = [&](int c, int b) {
-    const uint32_t buf = base + (uint32_t)b * FT_BUF;
+  // Widened, weighted, split and stored to the chunk's buffer.
+  auto store = [&](auto set_t, int c) {  // (buffers alternate with the sets)
+    constexpr int S = decltype(set_t)::value;
+    const uint32_t buf = base + (uint32_t)S * FT_BUF;
     float x[16];
-    if constexpr (MX) dequantise16(rk[0], e8m0_to_f(sk), x);
-    else load16(reinterpret_cast<const __nv_bfloat16*>(rk), x);
+    if constexpr (MX) dequantise16(rk[S][0], e8m0_to_f(sk[S]), x);
+    else load16(reinterpret_cast<const __nv_bfloat16*>(rk[S]), x);
     const int j = c * FT_TOK + kj;
     const float w = j < L ? decay_pow(ll, L - 1 - j) : 0.f;
 #pragma unroll
@@ -341,23 +345,26 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
     for (int u = 0; u < 2; ++u) {
       uint32_t y[8];
       if constexpr (MX) {
-        dequantise16(rv[u][0], e8m0_to_f(sv[u]), x);
+        dequantise16(rv[S][u][0], e8m0_to_f(sv[S][u]), x);
 #pragma unroll
         for (int s = 0; s < 8; ++s) y[s] = fold_pack(x[2 * s], x[2 * s + 1]);
       } else {
 #pragma unroll
         for (int q = 0; q < W; ++q) {
-          y[4 * q] = rv[u][q].x;
-          y[4 * q + 1] = rv[u][q].y;
-          y[4 * q + 2] = rv[u][q].z;
-          y[4 * q + 3] = rv[u][q].w;
+          y[4 * q] = rv[S][u][q].x;
+          y[4 * q + 1] = rv[S][u][q].y;
+          y[4 * q + 2] = rv[S][u][q].z;
+          y[4 * q + 3] = rv[S][u][q].w;
         }
       }
       put(buf + FT_V, vj + 16 * u, vp, y);
     }
   };
 
-  if (chunks > 0) load(0);
+  std::integral_constant<int, 0> set0;
+  std::integral_constant<int, 1> set1;
+  if (chunks > 0) load(set0, 0);
+  if (chunks > 1) load(set1, 1);
   if (tid == 0) {
     mbar_init(&s_bar[0], 2);  // the two issuers' commits
     mbar_init(&s_bar[1], 2);
@@ -376,14 +383,14 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
 
   int issued = 0;
   bool bad = false;
-  for (int c = 0; c < chunks; ++c) {
-    const int b = c & 1;
+  auto step = [&](auto set_t, int c) {
+    constexpr int b = decltype(set_t)::value;
     const bool ok = c < 2 || mbar_wait(&s_bar[b], (uint32_t)((c >> 1) - 1) & 1u, wait_ns, &s_abort);
-    store(c, b);
-    if (c + 1 < chunks) load(c + 1);
+    store(set_t, c);
+    if (c + 2 < chunks) load(set_t, c + 2);
     fence_async_smem();
     bad = __syncthreads_or(!ok);
-    if (bad) break;
+    if (bad) return;
     if (lane == 0 && warp < 2) {  // one issuer per sum
       constexpr uint32_t ID = idesc_bf16(128, DK, 1, 1);
       tc_fence_after();
@@ -399,6 +406,10 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
       umma_commit(&s_bar[b]);
     }
     ++issued;
+  };
+  for (int c = 0; c < chunks && !bad; c += 2) {
+    step(set0, c);
+    if (c + 1 < chunks && !bad) step(set1, c + 1);
   }
   if (chunks > 0 && !bad) {
     const bool ok = mbar_wait(&s_bar[(chunks - 1) & 1], (uint32_t)((chunks - 1) >> 1) & 1u, wait_ns, &s_abort);
