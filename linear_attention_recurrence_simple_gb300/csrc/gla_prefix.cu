@@ -227,6 +227,31 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   uint64_t* full = reinterpret_cast<uint64_t*>(pd_smem + SM::BAR) + warp * 2;  // keys, values
   const int h = (int)(blockIdx.x % (unsigned)H), n0 = (int)(blockIdx.x / (unsigned)H) * tile_seqs;
   const int cnt = min(tile_seqs, N - n0);
+  // Loads that need no index go out before anything is waited for: q, and the new tokens (eight lanes a
+  // sequence for its key, sixteen for its value).
+  const int ik = warp + PD_WARPS * (lane >> 3), pk = lane & 7, pv = lane & 15;
+  auto iv = [&](int u) { return warp + PD_WARPS * (2 * u + (lane >> 4)); };
+  uint4 rq[2], nk[2], nv[2][2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int e = tid + u * PD_THREADS;
+    if (e < cnt * (DK / 8))
+      rq[u] = *reinterpret_cast<const uint4*>(q + ((long long)(n0 + e / (DK / 8)) * H + h) * DK + 8 * (e % (DK / 8)));
+    nk[u] = nv[u][0] = nv[u][1] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (ik < cnt && pk < DK / 16) {
+    const uint4* from = reinterpret_cast<const uint4*>(k + ((long long)(n0 + ik) * H + h) * DK + 16 * pk);
+    nk[0] = from[0];
+    nk[1] = from[1];
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (iv(u) < cnt && pv < DV / 16) {
+      const uint4* from = reinterpret_cast<const uint4*>(v + ((long long)(n0 + iv(u)) * H + h) * DV + 16 * pv);
+      nv[u][0] = from[0];
+      nv[u][1] = from[1];
+    }
+  const float ll = log_lambda[h];
   if (warp == 0) {
     int row = -1, L = -1;
     long long tok0 = -1;
@@ -262,6 +287,10 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     s_part[2 * warp] = s_part[2 * warp + 1] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (tid + u * PD_THREADS < cnt * (DK / 8)) reinterpret_cast<uint4*>(sQ)[tid + u * PD_THREADS] = rq[u];
+  for (int e = tid; e < cnt * (DV / 4); e += PD_THREADS) reinterpret_cast<float4*>(sO)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
 
   // ---- this warp's chunks [c0, c1) of the tile's list; its first loads
@@ -300,51 +329,45 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     load_values();
   }
 
-  for (int e = tid; e < cnt * (DV / 4); e += PD_THREADS) reinterpret_cast<float4*>(sO)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int e = tid; e < cnt * (DK / 8); e += PD_THREADS) {
-    const int i = e / (DK / 8), p = e % (DK / 8);
-    reinterpret_cast<uint4*>(sQ)[e] = *reinterpret_cast<const uint4*>(q + ((long long)(n0 + i) * H + h) * DK + 8 * p);
+  // The shared states' lines into L2 (a tile that meets a state first would wait for DRAM row by row).
+  for (int r0 = 0; r0 < cnt; ++r0) {
+    const int row = s_row[r0];
+    if (row < 0 || (r0 > 0 && s_row[r0 - 1] == row)) continue;
+    const char* S = reinterpret_cast<const char*>(pool + ((long long)row * H + h) * (DK * DV));
+    for (int e = tid; e < DK * DV * 4 / 128; e += PD_THREADS) asm volatile("prefetch.global.L2 [%0];" ::"l"(S + 128 * e));
   }
-  __syncthreads();
-  const float ll = log_lambda[h];
-  // The shared states' part and the new tokens first in one half of the CTAs and last in the other: their
-  // latencies then fall into the others' streams.
+
+  // ---- the new tokens: q . k, and their places in the tails
+  {
+    float x[16], d = 0.f;
+    const bool live = ik < cnt && s_row[ik] >= 0 && pk < DK / 16;
+    load16(reinterpret_cast<const BF*>(nk), x);
+    if (live) {
+      float z[16];
+      load16(sQ + ik * DK + 16 * pk, z);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) d = fmaf(x[e], z[e], d);
+    }
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (live && pk == 0) s_self[ik] = d;
+    tail_store16<BF, MX, DK>(t.k, t.ks, live ? s_tok0[ik] + s_len[ik] : 0, pk, x, live);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = iv(u);
+      const bool lv = i < cnt && s_row[i] >= 0 && pv < DV / 16;
+      load16(reinterpret_cast<const BF*>(nv[u]), x);
+      tail_store16<BF, MX, DV>(t.v, t.vs, lv ? s_tok0[i] + s_len[i] : 0, pv, x, lv);
+    }
+  }
+
+  // The shared states' part first in one half of the CTAs and last in the other: its latencies then fall
+  // into the others' streams.
   // (the hash mixes both halves on every SM: CTAs i, i + 152, ... tend to share one)
   const int late = (int)((blockIdx.x ^ (blockIdx.x >> 3)) & 1u);
   bool ok = true;
   for (int step = 0; step < 2; ++step) {
    if (step == late) {
-    // ---- the new tokens: q . k, and their places in the tails.  All of a thread's loads go out at
-    // once: eight lanes a sequence for its key, sixteen for its value.
-    {
-      float x[16] = {}, y[2][16] = {};
-      const int ik = warp + PD_WARPS * (lane >> 3), pk = lane & 7;
-      const bool live = ik < cnt && s_row[ik] >= 0 && pk < DK / 16;
-      if (live) load16(k + ((long long)(n0 + ik) * H + h) * DK + 16 * pk, x);
-      const int pv = lane & 15;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int iv = warp + PD_WARPS * (2 * u + (lane >> 4));
-        if (iv < cnt && s_row[iv] >= 0 && pv < DV / 16) load16(v + ((long long)(n0 + iv) * H + h) * DV + 16 * pv, y[u]);
-      }
-      float d = 0.f;
-      if (live) {
-        float z[16];
-        load16(sQ + ik * DK + 16 * pk, z);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) d = fmaf(x[e], z[e], d);
-      }
-#pragma unroll
-      for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-      if (live && pk == 0) s_self[ik] = d;
-      tail_store16<BF, MX, DK>(t.k, t.ks, live ? s_tok0[ik] + s_len[ik] : 0, pk, x, live);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int iv = warp + PD_WARPS * (2 * u + (lane >> 4));
-        const bool lv = iv < cnt && s_row[iv] >= 0 && pv < DV / 16;
-        tail_store16<BF, MX, DV>(t.v, t.vs, lv ? s_tok0[iv] + s_len[iv] : 0, pv, y[u], lv);
-      }
-    }
     // ---- the shared states
     // q fragments; K step s of thread tq: columns 16 s + 4 tq .. + 3 (the same order as S's rows)
     uint2 qa[6], qb[6];
@@ -640,7 +663,14 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   }
   __syncthreads();
   if (s_abort) return;
-  // ---- shared parts in warp order, the new tokens, and out
+  // ---- shared parts in warp order, the new tokens (their values on the way meanwhile), and out
+  uint4 ov[3];
+#pragma unroll
+  for (int u = 0; u < 3; ++u) {
+    const int e = tid + u * PD_THREADS;
+    if (e < cnt * (DV / 8))
+      ov[u] = *reinterpret_cast<const uint4*>(v + ((long long)(n0 + e / (DV / 8)) * H + h) * DV + 8 * (e % (DV / 8)));
+  }
   for (int col = tid; col < DV; col += PD_THREADS)
 #pragma unroll
     for (int p = 0; p < 2 * PD_WARPS; ++p)
@@ -649,14 +679,20 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
         sO[s_part[p] * DV + col] += part[col];
       }
   __syncthreads();
-  for (int e = tid; e < cnt * (DV / 2); e += PD_THREADS) {
-    const int i = e / (DV / 2), c = 2 * (e % (DV / 2));
-    if (s_row[i] < 0) continue;
-    const long long at = ((long long)(n0 + i) * H + h) * DV + c;
-    const uint32_t vv = *reinterpret_cast<const uint32_t*>(v + at);
-    const float2 x = *reinterpret_cast<const float2*>(sO + i * DV + c);
-    *reinterpret_cast<uint32_t*>(o + at) = pack_bf(scale * fmaf(s_self[i], __uint_as_float(vv << 16), x.x),
-                                                   scale * fmaf(s_self[i], __uint_as_float(vv & 0xFFFF0000u), x.y));
+#pragma unroll
+  for (int u = 0; u < 3; ++u) {
+    const int e = tid + u * PD_THREADS, i = e / (DV / 8), c = 8 * (e % (DV / 8));
+    if (e >= cnt * (DV / 8) || s_row[i] < 0) continue;
+    const float g8 = s_self[i];
+    const float4 x = *reinterpret_cast<const float4*>(sO + i * DV + c), y = *reinterpret_cast<const float4*>(sO + i * DV + c + 4);
+    const uint32_t w[4] = {ov[u].x, ov[u].y, ov[u].z, ov[u].w};
+    const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int k2 = 0; k2 < 4; ++k2)
+      r[k2] = pack_bf(scale * fmaf(g8, __uint_as_float(w[k2] << 16), z[2 * k2]),
+                      scale * fmaf(g8, __uint_as_float(w[k2] & 0xFFFF0000u), z[2 * k2 + 1]));
+    *reinterpret_cast<uint4*>(o + ((long long)(n0 + i) * H + h) * DV + c) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
