@@ -26,85 +26,154 @@ size_t tc_bwd_acc_bytes(long long T_total, int H);
 
 namespace {
 
-constexpr int DEC_THREADS = DV;  // one thread per output column
-constexpr int DEC_TOK = 96;      // tokens whose weights are staged together
+// ---- fp32 calls -------------------------------------------------------------------------------
+// All arithmetic in fp32 on the CUDA cores.  One CTA per (tile of up to 4 consecutive sequences, head), 192
+// threads.  Shared states: a thread owns a column and reads it once for the run of sequences that
+// continue it.  Tails, 32 tokens at a time: thread (j, p) = (tid / 6, tid % 6) takes piece p of key j
+// (16 values, against the same 16 of q in registers), the six partial products of a token meet in
+// shared memory; thread (r, p) = (tid / 12, tid % 12) adds piece p of the values of tokens r and r + 16, loaded
+// before the keys are waited for, into 16 sums of its own; the 16 threads of a piece meet once per
+// sequence.  MXFP8 tails are bound by the widening and the FMAs, fp32 ones by HBM.
+constexpr int DEC_THREADS = DV;
+constexpr int DEC_TOK = 32;
+constexpr int DEC_TILE = 4;
+static_assert(DEC_TOK * 6 == DEC_THREADS && 16 * 12 == DEC_THREADS, "pieces of a chunk");
 
-template <class T, bool MX>
-__device__ __forceinline__ float tail_value(const TailArgs& t, long long token, int c) {
-  if constexpr (MX) {
-    const uint32_t code = static_cast<const uint8_t*>(t.v)[token * DV + c];
-    return e4m3x2_to_f2(code).x * e8m0_to_f(t.vs[token * (DV / 32) + (c >> 5)]);
-  } else {
-    return to_f(static_cast<const T*>(t.v)[token * DV + c]);
+// A 16-value piece as it is stored: fp32, or codes and their block's scale byte.
+template <bool MX, int D>
+struct TailPiece {
+  uint4 w[MX ? 1 : 4];
+  uint32_t s;
+  __device__ __forceinline__ void load(const void* base, const uint8_t* scales, long long token, int p, bool live) {
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + token * (MX ? D : 4 * D)) + (MX ? 1 : 4) * p;
+#pragma unroll
+    for (int i = 0; i < (MX ? 1 : 4); ++i) w[i] = live ? from[i] : make_uint4(0u, 0u, 0u, 0u);
+    s = MX && live ? scales[token * (D / 32) + (p >> 1)] : 127u;
   }
-}
+  // f(e, value without the scale) for the 16 elements
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int i = 0; i < (MX ? 1 : 4); ++i) {
+      const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (MX) {
+          const float2 a = e4m3x2_to_f2(v[j] & 0xFFFFu), b = e4m3x2_to_f2(v[j] >> 16);
+          f(4 * j, a.x);
+          f(4 * j + 1, a.y);
+          f(4 * j + 2, b.x);
+          f(4 * j + 3, b.y);
+        } else {
+          f(4 * i + j, __uint_as_float(v[j]));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float scale() const { return MX ? e8m0_to_f(s) : 1.f; }
+};
 
-// fp32 calls.  One CTA per (sequence, head).
-template <class T, bool MX>
-__global__ void __launch_bounds__(DEC_THREADS)
-prefix_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+template <bool MX>
+__global__ void __launch_bounds__(DEC_THREADS, MX ? 4 : 3)
+prefix_decode_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                      const float* __restrict__ log_lambda, float scale, const float* __restrict__ pool, int pool_rows,
-                     const int32_t* __restrict__ prefix_row, TailArgs t, T* __restrict__ o, int H, unsigned* err) {
-  __shared__ float sq[DK];
-  __shared__ float sw[DEC_TOK];
-  __shared__ float s_self;
-  const int n = (int)(blockIdx.x / (unsigned)H), h = (int)(blockIdx.x % (unsigned)H);
+                     const int32_t* __restrict__ prefix_row, TailArgs t, float* __restrict__ o, int N, int H, int tile_seqs,
+                     unsigned* err) {
+  __shared__ __align__(16) float sq[DEC_TILE][DK];
+  __shared__ float sw[DEC_TOK][6];
+  __shared__ __align__(16) float sp[16][DV];
+  __shared__ float s_self[DEC_TILE];
+  __shared__ int s_row[DEC_TILE], s_len[DEC_TILE];
+  __shared__ long long s_tok0[DEC_TILE];
+  const int h = (int)(blockIdx.x % (unsigned)H), n0 = (int)(blockIdx.x / (unsigned)H) * tile_seqs;
+  const int cnt = min(tile_seqs, N - n0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int L;
-  const long long tok0 = tail_token0(t, n, H, h, 1, L, err);
-  const int row = prefix_row[n];
-  if (row < 0 || row >= pool_rows) {
-    raise_error(err, ERR_SHAPE);
-    return;
+  if (tid < cnt) {
+    int row = prefix_row[n0 + tid], L;
+    const long long tok0 = tail_token0(t, n0 + tid, H, h, 1, L, err);
+    if (row < 0 || row >= pool_rows) {
+      raise_error(err, ERR_SHAPE);
+      row = -1;
+    }
+    s_row[tid] = tok0 < 0 ? -1 : row;  // -1: the sequence is skipped
+    s_len[tid] = L;
+    s_tok0[tid] = tok0;
   }
-  if (tok0 < 0) return;
-  const float ll = log_lambda[h];
-  const long long nh = (long long)n * H + h;
-  if (tid < DK) sq[tid] = to_f(q[nh * DK + tid]);
+  for (int e = tid; e < cnt * DK; e += DEC_THREADS) sq[e / DK][e % DK] = q[((long long)(n0 + e / DK) * H + h) * DK + e % DK];
   __syncthreads();
-  if (warp == 0) {  // q . k of the new token, and its place in the tail
-    float g = 0.f;
+  const float ll = log_lambda[h];
+  // the new tokens: q . k (warps 0 .. 3, one sequence each), and their places in the tails
+  if (warp < cnt && s_row[warp] >= 0) {
+    const long long nh = (long long)(n0 + warp) * H + h, at = s_tok0[warp] + s_len[warp];
+    float d = 0.f;
 #pragma unroll
-    for (int d = lane; d < DK; d += 32) g = fmaf(sq[d], to_f(k[nh * DK + d]), g);
+    for (int e = lane; e < DK; e += 32) d = fmaf(sq[warp][e], k[nh * DK + e], d);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) g += __shfl_xor_sync(0xffffffffu, g, off);
-    if (lane == 0) s_self = g;
-  } else if (warp == 1) {
+    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (lane == 0) s_self[warp] = d;
     float x[16] = {};
     if (lane < DK / 16) load16(k + nh * DK + 16 * lane, x);
-    tail_store16<T, MX, DK>(t.k, t.ks, tok0 + L, lane, x, lane < DK / 16);
-  } else if (warp == 2) {
-    float x[16] = {};
+    tail_store16<float, MX, DK>(t.k, t.ks, at, lane, x, lane < DK / 16);
     if (lane < DV / 16) load16(v + nh * DV + 16 * lane, x);
-    tail_store16<T, MX, DV>(t.v, t.vs, tok0 + L, lane, x, lane < DV / 16);
+    tail_store16<float, MX, DV>(t.v, t.vs, at, lane, x, lane < DV / 16);
   }
-  const float* S = pool + ((long long)row * H + h) * (DK * DV);
-  float acc = 0.f;
+  float acc[DEC_TILE] = {};
+  for (int r0 = 0; r0 < cnt;) {
+    const int row = s_row[r0];
+    int r1 = r0 + 1;
+    while (r1 < cnt && s_row[r1] == row) ++r1;
+    if (row >= 0) {  // only this run's sequences: a state's infinities and NaN stay with its own
+      const float* S = pool + ((long long)row * H + h) * (DK * DV) + tid;
 #pragma unroll 8
-  for (int a = 0; a < DK; ++a) acc = fmaf(sq[a], S[a * DV + tid], acc);
-  acc *= decay_pow(ll, L + 1);
-  for (int j0 = 0; j0 < L; j0 += DEC_TOK) {
-    const int m = min(DEC_TOK, L - j0);
-    __syncthreads();
-    // eight lanes a token, six of them with a 16-value piece of its key
-    for (int j = warp * 4 + (lane >> 3); j - (lane >> 3) < m; j += DEC_THREADS / 8) {
-      float g = 0.f;
-      if (j < m && (lane & 7) < DK / 16) {
-        float x[16];
-        tail_load16<T, MX, DK>(t.k, t.ks, tok0 + j0 + j, lane & 7, x);
+      for (int a = 0; a < DK; ++a) {
+        const float x = S[a * DV];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) g = fmaf(x[e], sq[16 * (lane & 7) + e], g);
+        for (int i = 0; i < DEC_TILE; ++i)
+          if (i >= r0 && i < r1) acc[i] = fmaf(sq[i][a], x, acc[i]);
       }
-#pragma unroll
-      for (int off = 4; off > 0; off >>= 1) g += __shfl_xor_sync(0xffffffffu, g, off);
-      if (j < m && (lane & 7) == 0) sw[j] = g * decay_pow(ll, L - j0 - j);
     }
-    __syncthreads();
-#pragma unroll 4
-    for (int j = 0; j < m; ++j) acc = fmaf(sw[j], tail_value<T, MX>(t, tok0 + j0 + j, tid), acc);
+    r0 = r1;
   }
-  acc = fmaf(s_self, to_f(v[nh * DV + tid]), acc);
-  store_out(o + nh * DV + tid, scale * acc);
+  const int kj = tid / 6, kp = tid % 6, vr = tid / 12, vp = tid % 12;
+#pragma unroll
+  for (int i = 0; i < DEC_TILE; ++i) {
+    if (i >= cnt || s_row[i] < 0) continue;
+    const int L = s_len[i];
+    const long long tok0 = s_tok0[i];
+    float qv[16], sum[16];
+    load16(&sq[i][16 * kp], qv);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+    for (int j0 = 0; j0 < L; j0 += DEC_TOK) {
+      TailPiece<MX, DV> x[2];
+      TailPiece<MX, DK> y;
+      y.load(t.k, t.ks, tok0 + j0 + kj, kp, j0 + kj < L);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) x[u].load(t.v, t.vs, tok0 + j0 + vr + 16 * u, vp, j0 + vr + 16 * u < L);
+      float d = 0.f;
+      y.each([&](int e, float c) { d = fmaf(c, qv[e], d); });
+      __syncthreads();  // the weights of the chunk before have been used
+      sw[kj][kp] = d * y.scale();
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int jj = vr + 16 * u, j = j0 + jj;
+        if (j < L) {
+          const float w = (((sw[jj][0] + sw[jj][1]) + (sw[jj][2] + sw[jj][3])) + (sw[jj][4] + sw[jj][5])) * decay_pow(ll, L - j) *
+                          x[u].scale();
+          x[u].each([&](int e, float c) { sum[e] = fmaf(w, c, sum[e]); });
+        }
+      }
+    }
+    store16(&sp[vr][16 * vp], sum);
+    __syncthreads();
+    float tail_sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) tail_sum += sp[r][tid];
+    const long long at = ((long long)(n0 + i) * H + h) * DV + tid;
+    o[at] = scale * fmaf(s_self[i], v[at], fmaf(decay_pow(ll, L + 1), acc[i], tail_sum));
+    __syncthreads();  // the sums are free again
+  }
 }
 
 // ---- bf16 calls: tiles of sequences, tensor cores ----------------------------------------------
@@ -814,15 +883,18 @@ int gla_prefix_decode_step(const void* q, const void* k, const void* v, const fl
   if ((rc = gla::current_device_state(&err, &wait_ns))) return rc;
   t.slot = tail_slot;
   t.len = tail_len;
-  const unsigned blocks = (unsigned)N * (unsigned)H;
   const bool mx = tail->format == GLA_TAIL_MXFP8;
   cudaStream_t s = (cudaStream_t)stream;
-  using gla::DEC_THREADS;
   if (dtype == GLA_F32) {
-    if (mx)
-      gla::prefix_decode_kernel<float, true><<<blocks, DEC_THREADS, 0, s>>>((const float*)q, (const float*)k, (const float*)v, log_lambda, scale, pool, pool_rows, prefix_row, t, (float*)o, H, err);
-    else
-      gla::prefix_decode_kernel<float, false><<<blocks, DEC_THREADS, 0, s>>>((const float*)q, (const float*)k, (const float*)v, log_lambda, scale, pool, pool_rows, prefix_row, t, (float*)o, H, err);
+    // four sequences a CTA once that leaves two CTAs for every SM (152); fewer spread one by one
+    const int ts = (long long)((N + gla::DEC_TILE - 1) / gla::DEC_TILE) * H >= 2 * 152 ? gla::DEC_TILE : 1;
+    const unsigned blocks = (unsigned)((N + ts - 1) / ts) * (unsigned)H;
+    auto run = [&](auto kernel) {
+      kernel<<<blocks, gla::DEC_THREADS, 0, s>>>((const float*)q, (const float*)k, (const float*)v, log_lambda, scale, pool,
+                                                 pool_rows, prefix_row, t, (float*)o, N, H, ts, err);
+    };
+    if (mx) run(gla::prefix_decode_kernel<true>);
+    else run(gla::prefix_decode_kernel<false>);
     return gla::to_status(cudaGetLastError());
   }
   return gla::to_status(mx ? gla::launch_decode_tile<true>(q, k, v, log_lambda, scale, pool, pool_rows, prefix_row, t, o,
