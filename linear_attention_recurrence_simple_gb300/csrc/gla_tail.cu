@@ -411,32 +411,37 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
     step(set0, c);
     if (c + 1 < chunks && !bad) step(set1, c + 1);
   }
+  // Each thread reads exactly the entries of the shared state that it writes, and before it does: a
+  // sequence may be folded into the row that it started from.  Rows go 32 at a time; a batch's
+  // loads are on their way while the batch before is stored (the first one's while the last MMAs run).
+  const int col = 32 * warp + lane;  // warps 0-3: D1, columns 0 .. 127; warps 4, 5: D2
+  const float* S = pool + ((long long)src * H + h) * (DK * DV) + col;
+  float* O = out + ((long long)dst * H + h) * (DK * DV) + col;
+  float s[2][32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[0][i] = S[i * DV];
   if (chunks > 0 && !bad) {
     const bool ok = mbar_wait(&s_bar[(chunks - 1) & 1], (uint32_t)((chunks - 1) >> 1) & 1u, wait_ns, &s_abort);
     bad = __syncthreads_or(!ok);
     tc_fence_after();
   }
   if (!bad) {
-    // each thread reads exactly the entries of the shared state that it writes, and before it does:
-    // a sequence may be folded into the row that it started from
     const float lamL = decay_pow(ll, L);
-    const int col = 32 * warp + lane;  // warps 0-3: D1, columns 0 .. 127; warps 4, 5: D2
-    const float* S = pool + ((long long)src * H + h) * (DK * DV) + col;
-    float* O = out + ((long long)dst * H + h) * (DK * DV) + col;
     const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + (warp < 4 ? 0u : (uint32_t)DK);
-#pragma unroll 1
-    for (int a0 = 0; a0 < DK; a0 += 32) {
-      float s[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = S[(a0 + i) * DV];
+    for (int b = 0; b < DK / 32; ++b) {
+      if (b + 1 < DK / 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[(b + 1) & 1][i] = S[(32 * (b + 1) + i) * DV];
+      }
       if (chunks > 0) {
         uint32_t d[32];
-        tmem_ld32(ta + (uint32_t)a0, d);
+        tmem_ld32(ta + 32u * (uint32_t)b, d);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = fmaf(lamL, s[i], __uint_as_float(d[i]));
+        for (int i = 0; i < 32; ++i) s[b & 1][i] = fmaf(lamL, s[b & 1][i], __uint_as_float(d[i]));
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) O[(a0 + i) * DV] = s[i];
+      for (int i = 0; i < 32; ++i) O[(32 * b + i) * DV] = s[b & 1][i];
     }
   } else {
     // a wait gave up: the MMAs in flight end before tensor memory is freed
