@@ -549,3 +549,170 @@ def test_offsets_past_32_bits(fmt):
         if big is not None:
             for i in range(2):
                 assert torch.equal(bits(big[slots[i]]), bits(x[small.slots[i]]))
+
+
+# ---- values at the edges -----------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", ["native", "mxfp8"])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_infinities_and_nan_stay_with_their_sequence(bf16, fmt):
+    """A NaN state, an infinity or a NaN in a sequence's tail or new token: the other sequences of the
+    tile come out as without it."""
+    c = Case(600, [20, 33, 7, 64, 0, 5, 18], 2, [0, 1, 1, 2, 0, 2, 2], 4, bf16, fmt)
+    clean = c.decode()
+    rows = list(c.rows)
+    rows[3] = 3
+    c.poolg[3] = float("nan")
+    if fmt == "mxfp8":
+        c.tail.v[c.slots[1], :, 4, 40] = 0x7F
+    else:
+        c.tail.v[c.slots[1], :, 4, 40] = float("inf")
+        c.tail.k[c.slots[5], :, 2, 3] = float("nan")
+    c.g["q"][6, :, 5] = float("nan")
+    o = gla.gla_prefix_decode_step(c.g["q"], c.g["k"], c.g["v"], c.llg, c.poolg, i32(rows), c.tail, i32(c.lens),
+                                   tail_slot=i32(c.slots), scale=SCALE)
+    for n in (0, 2, 4):
+        assert torch.equal(bits(o[n]), bits(clean[n])), n
+    bad = {1: (slice(None), 40), 3: (slice(None), slice(None)), 6: (slice(None), slice(None))}
+    if fmt != "mxfp8":
+        bad[5] = (slice(None), slice(None))
+    for n, at in bad.items():
+        assert not bool(torch.isfinite(o[n][at]).any()), n
+    ok = torch.ones(DV, dtype=torch.bool)
+    ok[40] = False
+    assert torch.equal(bits(o[1][:, ok.cuda()]), bits(clean[1][:, ok.cuda()]))
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_mxfp8_tails_of_many_magnitudes(bf16):
+    """Keys and values whose blocks differ by up to 2^24 from token to token, growing and shrinking
+    along the tail: the decode's running power of two per block follows them."""
+    lens, H = [70, 40, 33, 130], 3
+    c = Case(610, lens, H, [0, 0, 1, 1], 2, bf16, "mxfp8")
+    rng = np.random.default_rng(5)
+    k, v = c.t.k.copy(), c.t.v.copy()
+    e = rng.integers(-12, 13, v.shape[:3] + (6,))
+    e[c.slots[0]] = np.sort(e[c.slots[0]], axis=1)            # growing along the tail
+    e[c.slots[1]] = -np.sort(-e[c.slots[1]], axis=1)          # shrinking
+    v = np.nan_to_num(v) * np.exp2(e).repeat(32, axis=3)
+    k = np.nan_to_num(k) * np.exp2(rng.integers(-6, 7, k.shape[:3] + (3,))).repeat(32, axis=3)
+    (c.t.kc, c.t.ks), (c.t.vc, c.t.vs) = oracle.mxfp8_quantize(k), oracle.mxfp8_quantize(v)
+    c.t.k, c.t.v = oracle.mxfp8_dequantize(c.t.kc, c.t.ks), oracle.mxfp8_dequantize(c.t.vc, c.t.vs)
+    c.tail = c.t.device()
+    check_decode(c)
+    s = c.fold().cpu().numpy().astype(np.float64)
+    ref, mag = ref_fold(c.ll, c.pool, c.rows, c.t.k, c.t.v, c.slots, c.lens)
+    assert np.all(np.abs(s - ref) <= tol(ref, mag, max(lens) + 2, True, False))
+
+
+@pytest.mark.parametrize("scale_q", [2.0 ** -60, 2.0 ** 40])
+@pytest.mark.parametrize("fmt", ["native", "mxfp8"])
+def test_decode_with_tiny_and_huge_queries(fmt, scale_q):
+    c = Case(620, [30, 5, 17], 2, [0, 1, 1], 2, True, fmt)
+    c.q = gs.bf16_round((c.q * scale_q).astype(np.float32))
+    c.q[1, :, 3] *= 2.0 ** 20                                # one dimension far above the others
+    c.g["q"] = torch.from_numpy(c.q).cuda().to(c.dt)
+    check_decode(c)
+
+
+def test_one_tail_row_for_read_only_use_and_repeated_rows():
+    """Two sequences may fold the same tail row (it is only read), into rows of their own."""
+    c = Case(630, [20, 20], 2, [0, 1], 2, True, "mxfp8")
+    out = gla.gla_tail_fold(c.llg, c.poolg, i32([0, 1]), c.tail, i32([20, 12]), tail_slot=i32([c.slots[0]] * 2))
+    for n, (r, L) in enumerate(((0, 20), (1, 12))):
+        ref, mag = ref_fold(c.ll, c.pool, [r], c.t.k, c.t.v, [c.slots[0]], [L])
+        assert np.all(np.abs(out[n:n + 1].cpu().numpy() - ref) <= tol(ref, mag, 24, True, False))
+
+
+# ---- bounded waits -----------------------------------------------------------------------------
+def test_short_wait_limit_reports_timeout_and_the_context_survives():
+    """With a wait limit of 1 ns, waits that the hardware's own first try does not see through give up
+    (many in a decode whose loads queue up behind each other, maybe none in a fold): the kernels
+    drain their copies and MMAs and return, GLA_ERR_TIMEOUT is reported, and the next calls are right."""
+    N, H = 640, 16
+    c = Case(640, [40] * 4, 2, [0] * 4, 1, True, "mxfp8")
+    tail = gla.gla_tail_alloc(N, H, 160, torch.float8_e4m3fn)
+    for x in (tail.k, tail.v):
+        x.random_(0, 0x7E)
+    for x in (tail.k_scales, tail.v_scales):
+        x.random_(118, 122)
+    pool, rows, lens = torch.randn(2, H, DK, DV, device="cuda"), i32([0] * 300 + [1] * 340), i32([159] * N)
+    ll = torch.full((H,), -0.01, device="cuda")
+    q, k, v = (torch.randn(N, H, d, device="cuda", dtype=torch.bfloat16) for d in (DK, DK, DV))
+    calls = (lambda: gla.gla_prefix_decode_step(q, k, v, ll, pool, rows, tail, lens),
+             lambda: gla.gla_tail_fold(ll, pool, rows, tail, lens))
+    want = [f() for f in calls]
+    assert gla.gla_get_device_error() == 0
+    for f, w in zip(calls, want):
+        gla.gla_set_wait_limit_ns(1)
+        try:
+            f()
+            err = gla.gla_get_device_error()
+        finally:
+            gla.gla_set_wait_limit_ns(2_000_000_000)
+        assert err in (0, -8)
+        assert gla.gla_get_device_error() == 0
+        assert torch.equal(f(), w)
+    check_decode(c)
+
+
+# ---- several calls at once ---------------------------------------------------------------------
+def test_two_graphs_and_eager_calls_on_several_streams():
+    """Two captured steps on pools of their own, replayed at once on two streams beside eager calls
+    on a third: the calls share no workspace, so each gives what it gives alone."""
+    cases = [Case(650 + i, [40, 3, 90, 17] * 6, 3, [0, 1] * 12, 2, True, "mxfp8") for i in range(3)]
+    alone = [x.decode() for x in cases]
+    folds = [x.fold() for x in cases]
+    idx = [[i32(x.rows), i32(x.lens), i32(x.slots)] for x in cases]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for x, (rows, lens, slots), s in zip(cases[:2], idx, streams):
+        g, o = torch.cuda.CUDAGraph(), torch.empty_like(alone[0])
+        f = torch.empty_like(folds[0])
+        with torch.cuda.graph(g, stream=s):
+            gla.gla_prefix_decode_step(x.g["q"], x.g["k"], x.g["v"], x.llg, x.poolg, rows, x.tail, lens,
+                                       tail_slot=slots, scale=SCALE, o=o)
+            gla.gla_tail_fold(x.llg, x.poolg, rows, x.tail, lens, tail_slot=slots, out=f)
+        graphs.append(g)
+        outs.append((o, f))
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            x, (rows, lens, slots) = cases[2], idx[2]
+            o = gla.gla_prefix_decode_step(x.g["q"], x.g["k"], x.g["v"], x.llg, x.poolg, rows, x.tail, lens,
+                                           tail_slot=slots, scale=SCALE)
+            f = gla.gla_tail_fold(x.llg, x.poolg, rows, x.tail, lens, tail_slot=slots)
+    torch.cuda.synchronize()
+    for (a, b), d, e in zip(outs + [(o, f)], alone, folds):
+        assert torch.equal(a, d) and torch.equal(b, e)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_captured_packed_calls(bf16):
+    """Forward and backward from shared states, captured (the backward's side streams fork and join
+    inside the capture) and replayed on new inputs."""
+    lens, H, rows, P = PACKED[0]
+    d, g, rg = packed(660, lens, H, rows, P, bf16)
+    _, g2, _ = packed(661, lens, H, rows, P, bf16)
+
+    def both(x):
+        fwd = gla.gla_prefix_fwd(x["q"], x["k"], x["v"], x["ll"], x["pool"], rg, x["cu"], SCALE)
+        return fwd + gla.gla_prefix_bwd(x["q"], x["k"], x["v"], x["ll"], x["dO"], x["pool"], rg, x["cu"], SCALE,
+                                        dhT=x["dhT"])
+    want = both(g2)
+    both(g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(g)
+    for name in ("q", "k", "v", "dO", "pool", "dhT"):
+        g[name].copy_(g2[name])
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, (x, y) in enumerate(zip(got, want)):
+        if bf16 and i in (2, 3):  # dq, dk: partial sums in arrival order
+            assert within_one_bf16_rounding(x.float().cpu().numpy(), y.float().cpu().numpy())
+        else:
+            assert torch.equal(x, y)
