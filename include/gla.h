@@ -340,8 +340,8 @@ int gla_chunk_fwd_host(const void* q, const void* k, const void* v, const float*
  *                  GLA_TAIL_PLAIN: elements of the call's dtype; k_scales and v_scales unused.
  *                  GLA_TAIL_MXFP8: E4M3 codes with E8M0 scales k_scales [rows, H, cap, 3] and
  *                  v_scales [rows, H, cap, 6], one per 32 values, quantised by the rule of
- *                  gla_decode_step_mxfp8_state (nothing saturates; an infinity becomes the
- *                  largest finite code, a NaN stays one).
+ *                  gla_decode_step_mxfp8_state (no finite value saturates; an infinity stays one and
+ *                  costs its block's other values, a NaN stays one).
  *                cap >= 16 and a multiple of 16 (else GLA_ERR_SHAPE); every array 16-byte aligned.
  *   tail_slot    [n] int32 device: the tail row of each sequence, NULL = row n (then rows >= n is
  *                required).  Rows that a call writes must be distinct.
@@ -350,8 +350,8 @@ int gla_chunk_fwd_host(const void* q, const void* k, const void* v, const float*
  *                from tail_len on may hold anything, NaN included.
  * A sequence whose row, slot, length or places lie outside the pool or its tail is skipped (its
  * outputs and its tail are left as they were) and records GLA_ERR_SHAPE in the device error word.
- * Each call returns once its work is queued on `stream`, may be captured into a graph, and needs no
- * workspace except where it takes one. */
+ * Each call returns once its work is queued on `stream`, may be captured into a graph (after a first
+ * call of the library on the device), and needs no workspace except where it takes one. */
 typedef enum { GLA_TAIL_PLAIN = 0, GLA_TAIL_MXFP8 = 1 } gla_tail_format;
 typedef struct gla_tail {
   void* k;
@@ -365,7 +365,7 @@ typedef struct gla_tail {
  *     o = scale (lambda^(L+1) S_p^T q + sum_{j < L} lambda^(L-j) (q . k_j) v_j + (q . k) v),
  * the readout after the token's own update, with the token's k and v as they are given; then k and
  * v are written to place L of the tail (quantised where it is MXFP8), which needs L < cap.
- *   q, k [N, H, 96]; v, o [N, H, 192]; dtype `dtype`.  One launch.  For L beyond about 256 (bf16)
+ *   q, k [N, H, 96]; v, o [N, H, 192]; dtype `dtype`; N * H below 2^31.  One launch.  For L beyond about 256 (bf16)
  *   or 500 (MXFP8) tokens a state of its own (gla_tail_fold, then gla_decode_step) is less to read. */
 int gla_prefix_decode_step(const void* q, const void* k, const void* v, const float* log_lambda, float scale,
                            const float* pool, int pool_rows, const int32_t* prefix_row, const gla_tail* tail,
@@ -377,7 +377,7 @@ int gla_prefix_decode_step(const void* q, const void* k, const void* v, const fl
  *   pos          [n_seq] int32 device: sequence n's tokens go to (come from) places pos[n],
  *                pos[n] + 1, ... of its tail (for an append, usually tail_len).
  *   cu_seqlens   [n_seq + 1] int32 device packed offsets, as in gla_chunk_fwd; rows from
- *                cu_seqlens[n_seq] on are left alone.
+ *                cu_seqlens[n_seq] on are left alone.  T <= 2^31 - 64.
  * An MXFP8 tail is quantised as it is written and widened as it is read: exactly, where dtype holds
  * the value (always, but for values of bf16's or fp32's subnormal range). */
 int gla_tail_append(const void* k, const void* v, const gla_tail* tail, const int32_t* tail_slot, const int32_t* pos,
@@ -392,7 +392,9 @@ int gla_tail_read(const gla_tail* tail, const int32_t* tail_slot, const int32_t*
  *                out_rows >= N is required).  Rows must be distinct.  out may be the pool itself, and
  *                a sequence may be folded into the row it continues, as long as no other sequence of
  *                the call continues a row that the call writes.
- *   dtype        type of the tail's elements (GLA_TAIL_PLAIN). */
+ *   dtype        type of the tail's elements (GLA_TAIL_PLAIN).
+ * Sums in fp32, of keys weighted in fp32: on the CUDA cores for fp32 tails, on the tensor cores (the
+ * weighted key in three bf16 terms) for bf16 and MXFP8 ones. */
 int gla_tail_fold(const float* log_lambda, const float* pool, int pool_rows, const int32_t* prefix_row,
                   const gla_tail* tail, const int32_t* tail_slot, const int32_t* tail_len, float* out, int out_rows,
                   const int32_t* out_row, int N, int H, int dk, int dv, int dtype, gla_stream_t stream);
@@ -400,7 +402,8 @@ int gla_tail_fold(const float* log_lambda, const float* pool, int pool_rows, con
 /* gla_chunk_fwd and gla_chunk_bwd on packed sequences that continue shared states: sequence n's
  * initial state is pool[prefix_row[n]], read where it stands (no copies).  cu_seqlens is required;
  * every other argument as there.  A prefix_row outside the pool starts that sequence from zeros and
- * records GLA_ERR_SHAPE.
+ * records GLA_ERR_SHAPE.  (bf16: as there, a sequence's last chunk reads on into the next sequence with
+ * zero weights, so an infinity or a NaN in the first 127 tokens of one can reach the one before.)
  *   dpool        [pool_rows, H, 96, 192] fp32 output, or NULL to skip: the pool's gradient, row p
  *                the sum of dh0 over the sequences that continue p, added in their order; zeros for
  *                a row that none continues.

@@ -486,7 +486,7 @@ int check_copy(const void* k, const void* v, const gla_tail* tail, const int32_t
   if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_DTYPE;
   if (dk != GLA_DK || dv != GLA_DV) return GLA_ERR_UNSUPPORTED;
   if (n_seq < 0 || T < 0 || H < 1) return GLA_ERR_SHAPE;
-  if ((long long)((T + (long long)COPY_TOK - 1) / COPY_TOK) * H >= (1ll << 31)) return GLA_ERR_SHAPE;
+  if (T > INT32_MAX - COPY_TOK + 1 || (T + COPY_TOK - 1) / COPY_TOK * (long long)H >= (1ll << 31)) return GLA_ERR_SHAPE;
   const int rc = check_tail(tail, H, t);
   if (rc) return rc;
   if (n_seq == 0 || T == 0) return GLA_OK;

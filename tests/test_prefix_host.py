@@ -92,6 +92,8 @@ def test_append_and_read_argument_errors(lib):
             assert call(**{name: A + 1}) == ALIGN, name
         assert call(n=-1) == SHAPE
         assert call(T=-1) == SHAPE
+        assert call(T=2 ** 31 - 63) == SHAPE
+        assert call(T=2 ** 30, H=200) == SHAPE
         assert call(n=9) == SHAPE
         assert call(n=0, k=None, v=None, pos=None, cu=None) == OK
         assert call(T=0, k=None, v=None, pos=None, cu=None) == OK
