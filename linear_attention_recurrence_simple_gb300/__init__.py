@@ -702,11 +702,22 @@ def gla_tail_alloc(rows: int, H: int, cap: int, dtype=torch.bfloat16, device="cu
     return GlaTail(z(DK), z(DV))
 
 
-# The calls below are made once per layer and token, where a microsecond on the host counts: their
-# checks are those of _need, which is entered (and says what is wrong) only when one fails.
+# The calls below are made once per layer and token, where a microsecond on the host counts: a call tests
+# its tensors in one expression and goes through them one by one (_need says what is wrong) only when
+# that fails.
+def _like(i, dtype, *tensors):
+    """Whether the tensors are contiguous, of this type and on CUDA device i."""
+    try:
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != i or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return True
+
+
 def _good(t, name, dtype, dev, numel=None):
-    if (type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != dev.index or not t.is_contiguous()
-            or (numel is not None and t.numel() != numel)):
+    if not _like(dev.index, dtype, t) or (numel is not None and t.numel() != numel):
         _need(t, name, dtype, dev, numel)
 
 
@@ -724,12 +735,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _run(fn, where, dev, *args):
     """Calls the library with `dev` current, on its current stream."""
-    stream = _raw_stream(dev.index)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, stream)
+    i = dev.index
+    if torch.cuda.current_device() == i:
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream)
+            rc = fn(*args, _raw_stream(i))
     if rc != 0:
         raise GlaError(rc, where)
 
@@ -742,27 +753,27 @@ def _tail(tail, H, dtype, dev):
     """Checks the tails' tensors and returns the C struct."""
     k, v, ks, vs = tail
     mx = ks is not None or vs is not None
-    et = torch.uint8 if mx else dtype
-    _good(k, "tail.k", et, dev)
-    _good(v, "tail.v", et, dev)
-    shape = tuple(k.shape)
-    if len(shape) != 4 or shape[1] != H or shape[3] != DK or tuple(v.shape) != shape[:3] + (DV,):
+    if not (_like(dev.index, torch.uint8, k, v, ks, vs) if mx else _like(dev.index, dtype, k, v)):
+        for name, t in (("k", k), ("v", v)) + ((("k_scales", ks), ("v_scales", vs)) if mx else ()):
+            _need(t, "tail." + name, torch.uint8 if mx else dtype, dev)
+    if k.dim() != 4:
+        raise ValueError("the tail must be k [R, H, cap, 96] and v [R, H, cap, 192]")
+    R, h, cap, d = k.shape
+    if h != H or d != DK or v.shape != (R, H, cap, DV):
         raise ValueError("the tail must be k [R, H, cap, 96] and v [R, H, cap, 192]")
     if not mx:
-        return _CTail(k.data_ptr(), v.data_ptr(), None, None, shape[0], shape[2], 0)
-    _good(ks, "tail.k_scales", torch.uint8, dev)
-    _good(vs, "tail.v_scales", torch.uint8, dev)
-    if tuple(ks.shape) != shape[:3] + (DK // 32,) or tuple(vs.shape) != shape[:3] + (DV // 32,):
+        return _CTail(k.data_ptr(), v.data_ptr(), None, None, R, cap, 0)
+    if ks.shape != (R, H, cap, DK // 32) or vs.shape != (R, H, cap, DV // 32):
         raise ValueError("tail scales must be [R, H, cap, 3] and [R, H, cap, 6]")
-    return _CTail(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[2], 1)
+    return _CTail(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), R, cap, 1)
 
 
 def _pool(pool, H, dev, name="pool"):
     _good(pool, name, torch.float32, dev)
-    shape = tuple(pool.shape)
-    if len(shape) != 4 or shape[1:] != (H, DK, DV):
+    P = pool.shape[0] if pool.dim() == 4 else -1
+    if pool.shape != (P, H, DK, DV):
         raise ValueError(f"{name} must be [P, H, 96, 192]")
-    return shape[0]
+    return P
 
 
 def gla_prefix_decode_step(q, k, v, log_lambda, pool, prefix_row, tail, tail_len, tail_slot=None, scale=None, o=None):
@@ -776,20 +787,22 @@ def gla_prefix_decode_step(q, k, v, log_lambda, pool, prefix_row, tail, tail_len
     lib = _libs.get(_use_debug) or load_library()
     dt, dtype = _dtype_code(q), q.dtype
     dev = _device_of(q, "q")
-    _good(q, "q", dtype, dev)
-    _good(k, "k", dtype, dev)
-    _good(v, "v", dtype, dev)
-    shape = tuple(q.shape)
-    if len(shape) != 3 or shape[2] != DK or tuple(k.shape) != shape or tuple(v.shape) != shape[:2] + (DV,):
+    i = dev.index
+    if not _like(i, dtype, q, k, v):
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _need(t, name, dtype, dev)
+    N, H, d = q.shape if q.dim() == 3 else (0, 0, 0)
+    if d != DK or k.shape != q.shape or v.shape != (N, H, DV):
         raise ValueError("expected q, k [N, H, 96] and v [N, H, 192]")
-    N, H = shape[:2]
-    _good(log_lambda, "log_lambda", torch.float32, dev, H)
+    if not _like(i, torch.float32, log_lambda) or log_lambda.numel() != H:
+        _need(log_lambda, "log_lambda", torch.float32, dev, H)
     rows = _pool(pool, H, dev)
     ct = _tail(tail, H, dtype, dev)
-    _good(prefix_row, "prefix_row", torch.int32, dev, N)
-    _good(tail_len, "tail_len", torch.int32, dev, N)
-    if tail_slot is not None:
-        _good(tail_slot, "tail_slot", torch.int32, dev, N)
+    slot = tail_len if tail_slot is None else tail_slot
+    if (not _like(i, torch.int32, prefix_row, tail_len, slot) or prefix_row.numel() != N or tail_len.numel() != N
+            or slot.numel() != N):
+        for name, t in (("prefix_row", prefix_row), ("tail_len", tail_len), ("tail_slot", slot)):
+            _need(t, name, torch.int32, dev, N)
     if o is None:
         o = torch.empty_like(v)
     else:
