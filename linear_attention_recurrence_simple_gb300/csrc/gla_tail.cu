@@ -236,15 +236,16 @@ tail_fold_kernel(const float* __restrict__ log_lambda, const float* pool, int po
 // MMAs into one sum: two would leave 2.5e-6 of the state's norm), the value is bf16 or an E4M3 code
 // times a power of two: exact in bf16.  Threads load 16-value pieces of the next
 // 32 tokens into registers while the tensor core works on the previous ones, widen, weight and
-// split them, and store them swizzled; two buffers.  Bound by HBM: 73.7 KB written per
+// split them, and store them swizzled; two buffers, handed to two issuing warps and back through
+// mbarriers.  Bound by HBM: 73.7 KB written per
 // (sequence, head) and the tail read once; two CTAs per SM cover each other's epilogue.
-constexpr int FT_THREADS = 192, FT_TOK = 32;
+constexpr int FT_WIDEN = 192, FT_THREADS = 256, FT_TOK = 32;  // warps 0 .. 5 widen and store, 6 and 7 issue
 constexpr uint32_t FT_PANEL = FT_TOK * 128;                       // 32 tokens x 64 columns of bf16
 constexpr uint32_t FT_V = 0, FT_K = 3 * FT_PANEL, FT_TERM = 2 * FT_PANEL, FT_BUF = FT_K + 3 * FT_TERM;
 // (D2's unused upper half reads the panel after V's last, which is the key's first)
 constexpr uint32_t FT_SMEM = 80 * 1024;  // two buffers and alignment; sized for two CTAs per SM (tensor memory)
 static_assert(2 * FT_BUF + 1024 <= FT_SMEM, "fold buffers");
-static_assert(FT_TOK * 6 == FT_THREADS && FT_TOK * 12 == 2 * FT_THREADS, "whole pieces");
+static_assert(FT_TOK * 6 == FT_WIDEN && FT_TOK * 12 == 2 * FT_WIDEN, "whole pieces");
 constexpr uint32_t FT_TMEM = 256;  // columns: D1 at 0, D2 at 96
 
 __device__ __forceinline__ uint32_t fold_pack(float lo, float hi) {
@@ -258,7 +259,7 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
                     const int32_t* __restrict__ prefix_row, TailArgs t, float* out, int out_rows,
                     const int32_t* __restrict__ out_row, int H, unsigned* err, unsigned long long wait_ns) {
   extern __shared__ uint8_t ft_raw[];
-  __shared__ uint64_t s_bar[2];
+  __shared__ uint64_t s_full[2], s_empty[2], s_drain[2];  // a buffer is written; its MMAs are done; an issuer's are
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t base = (smem_u32(ft_raw) + 1023u) & ~1023u;
@@ -363,11 +364,16 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
 
   std::integral_constant<int, 0> set0;
   std::integral_constant<int, 1> set1;
-  if (chunks > 0) load(set0, 0);
-  if (chunks > 1) load(set1, 1);
+  if (tid < FT_WIDEN) {
+    if (chunks > 0) load(set0, 0);
+    if (chunks > 1) load(set1, 1);
+  }
   if (tid == 0) {
-    mbar_init(&s_bar[0], 2);  // the two issuers' commits
-    mbar_init(&s_bar[1], 2);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], FT_WIDEN);
+      mbar_init(&s_empty[b], 2);  // the two issuers' commits
+      mbar_init(&s_drain[b], 1);
+    }
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -381,77 +387,83 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
-  int issued = 0;
-  bool bad = false;
-  auto step = [&](auto set_t, int c) {
-    constexpr int b = decltype(set_t)::value;
-    const bool ok = c < 2 || mbar_wait(&s_bar[b], (uint32_t)((c >> 1) - 1) & 1u, wait_ns, &s_abort);
-    store(set_t, c);
-    if (c + 2 < chunks) load(set_t, c + 2);
-    fence_async_smem();
-    bad = __syncthreads_or(!ok);
-    if (bad) return;
-    if (lane == 0 && warp < 2) {  // one issuer per sum
+  if (tid >= FT_WIDEN) {
+    // ---- issuers, one per sum (a thread issues an MMA per ~70 cycles: off the widening warps' path)
+    if (lane == 0) {
+      const uint32_t which = (uint32_t)(warp - FT_WIDEN / 32);
       constexpr uint32_t ID = idesc_bf16(128, DK, 1, 1);
-      tc_fence_after();
-      const uint32_t buf = base + (uint32_t)b * FT_BUF;
-      const SDesc a = sdesc(buf + FT_V + (uint32_t)warp * 2u * FT_PANEL, FT_PANEL, 1024, LAYOUT_SW128);
-      const SDesc kd = sdesc(buf + FT_K, FT_PANEL, 1024, LAYOUT_SW128);
+      bool ok = true;
+      for (int c = 0; c < chunks; ++c) {
+        if (!(ok = mbar_wait(&s_full[c & 1], (uint32_t)(c >> 1) & 1u, wait_ns, &s_abort))) break;
+        tc_fence_after();
+        const uint32_t buf = base + (uint32_t)(c & 1) * FT_BUF;
+        const SDesc a = sdesc(buf + FT_V + which * 2u * FT_PANEL, FT_PANEL, 1024, LAYOUT_SW128);
+        const SDesc kd = sdesc(buf + FT_K, FT_PANEL, 1024, LAYOUT_SW128);
 #pragma unroll
-      for (int kk = 0; kk < FT_TOK / 16; ++kk)
+        for (int kk = 0; kk < FT_TOK / 16; ++kk)
 #pragma unroll
-        for (int term = 0; term < 3; ++term)
-          umma(tmem + (uint32_t)warp * DK, a + (uint32_t)kk * 2048u, kd + (uint32_t)term * FT_TERM + (uint32_t)kk * 2048u, ID,
-               c > 0 || kk > 0 || term > 0);
-      umma_commit(&s_bar[b]);
-    }
-    ++issued;
-  };
-  for (int c = 0; c < chunks && !bad; c += 2) {
-    step(set0, c);
-    if (c + 1 < chunks && !bad) step(set1, c + 1);
-  }
-  // Each thread reads exactly the entries of the shared state that it writes, and before it does: a
-  // sequence may be folded into the row that it started from.  Rows go 32 at a time; a batch's
-  // loads are on their way while the batch before is stored (the first one's while the last MMAs run).
-  const int col = 32 * warp + lane;  // warps 0-3: D1, columns 0 .. 127; warps 4, 5: D2
-  const float* S = pool + ((long long)src * H + h) * (DK * DV) + col;
-  float* O = out + ((long long)dst * H + h) * (DK * DV) + col;
-  float s[2][32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) s[0][i] = S[i * DV];
-  if (chunks > 0 && !bad) {
-    const bool ok = mbar_wait(&s_bar[(chunks - 1) & 1], (uint32_t)((chunks - 1) >> 1) & 1u, wait_ns, &s_abort);
-    bad = __syncthreads_or(!ok);
-    tc_fence_after();
-  }
-  if (!bad) {
-    const float lamL = decay_pow(ll, L);
-    const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + (warp < 4 ? 0u : (uint32_t)DK);
-#pragma unroll
-    for (int b = 0; b < DK / 32; ++b) {
-      if (b + 1 < DK / 32) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[(b + 1) & 1][i] = S[(32 * (b + 1) + i) * DV];
+          for (int term = 0; term < 3; ++term)
+            umma(tmem + which * DK, a + (uint32_t)kk * 2048u, kd + (uint32_t)term * FT_TERM + (uint32_t)kk * 2048u, ID,
+                 c > 0 || kk > 0 || term > 0);
+        umma_commit(&s_empty[c & 1]);
       }
-      if (chunks > 0) {
-        uint32_t d[32];
-        tmem_ld32(ta + 32u * (uint32_t)b, d);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[b & 1][i] = fmaf(lamL, s[b & 1][i], __uint_as_float(d[i]));
+      if (!ok) {  // the MMAs in flight end before tensor memory is freed
+        umma_commit(&s_drain[which]);
+        mbar_wait_drain(&s_drain[which], 0u, 1000000000ull, err);
       }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) O[(32 * b + i) * DV] = s[b & 1][i];
     }
+    __syncwarp();
   } else {
-    // a wait gave up: the MMAs in flight end before tensor memory is freed
-    if (tid == 0) {
-      if (issued > 0) mbar_wait_drain(&s_bar[(issued - 1) & 1], (uint32_t)((issued - 1) >> 1) & 1u, 1000000000ull, err);
-      raise_error(err, ERR_TIMEOUT);
+    auto step = [&](auto set_t, int c) {
+      constexpr int b = decltype(set_t)::value;
+      if (c >= 2 && !__all_sync(0xffffffffu, mbar_wait(&s_empty[b], (uint32_t)((c >> 1) - 1) & 1u, wait_ns, &s_abort)))
+        return false;
+      store(set_t, c);
+      if (c + 2 < chunks) load(set_t, c + 2);
+      fence_async_smem();
+      mbar_arrive(&s_full[b]);
+      return true;
+    };
+    bool ok = true;
+    for (int c = 0; c < chunks && ok; c += 2) {
+      ok = step(set0, c);
+      if (ok && c + 1 < chunks) ok = step(set1, c + 1);
+    }
+    // Each thread reads exactly the entries of the shared state that it writes, and before it does: a
+    // sequence may be folded into the row that it started from.  Rows go 32 at a time, the first batch's
+    // loads while the last MMAs run.
+    const int col = 32 * warp + lane;  // warps 0-3: D1, columns 0 .. 127; warps 4, 5: D2
+    const float* S = pool + ((long long)src * H + h) * (DK * DV) + col;
+    float* O = out + ((long long)dst * H + h) * (DK * DV) + col;
+    float s[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = S[i * DV];
+    if (chunks > 0 && ok)
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[(chunks - 1) & 1], (uint32_t)((chunks - 1) >> 1) & 1u, wait_ns, &s_abort));
+    if (ok) {
+      tc_fence_after();
+      const float lamL = decay_pow(ll, L);
+      const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21) + (warp < 4 ? 0u : (uint32_t)DK);
+#pragma unroll
+      for (int b = 0; b < DK / 32; ++b) {
+        if (b > 0) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = S[(32 * b + i) * DV];
+        }
+        if (chunks > 0) {
+          uint32_t d[32];
+          tmem_ld32(ta + 32u * (uint32_t)b, d);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = fmaf(lamL, s[i], __uint_as_float(d[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) O[(32 * b + i) * DV] = s[i];
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && s_abort) raise_error(err, ERR_TIMEOUT);
   if (warp == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(FT_TMEM));
