@@ -45,6 +45,7 @@ namespace {
 // halves of a 32-value block are lanes l and l ^ 1 (18 and 32 are even).
 constexpr int COPY_THREADS = 288;  // 16 tokens' pieces a pass
 constexpr int COPY_TOK = 64;
+constexpr int COPY_CU = 1024;  // offsets kept in shared memory (more are searched where they stand)
 
 // WRITE: packed k, v -> tails; otherwise tails -> packed k, v.
 template <class T, bool MX, bool WRITE>
@@ -52,25 +53,32 @@ __global__ void __launch_bounds__(COPY_THREADS)
 tail_copy_kernel(T* __restrict__ k, T* __restrict__ v, TailArgs t, const int32_t* __restrict__ cu, int n_seq, int T_total,
                  int H, unsigned* err) {
   __shared__ long long s_token[COPY_TOK];
+  __shared__ int s_cu[COPY_CU];
   const int tid = threadIdx.x;
   const int h = (int)(blockIdx.x % (unsigned)H), t0 = (int)(blockIdx.x / (unsigned)H) * COPY_TOK;
+  const int32_t* offsets = cu;
+  if (n_seq < COPY_CU) {  // a search in global memory is a chain of latencies
+    for (int i = tid; i <= n_seq; i += COPY_THREADS) s_cu[i] = cu[i];
+    offsets = s_cu;
+    __syncthreads();
+  }
   if (tid < COPY_TOK) {
-    // the sequence n with cu[n] <= tok < cu[n + 1]: the last n with cu[n] <= tok
+    // the sequence n with offsets[n] <= tok < offsets[n + 1]: the last n with offsets[n] <= tok
     const int tok = t0 + tid;
     long long at = -1;
     if (tok < T_total) {
-      int lo = 0, hi = n_seq;  // cu[lo] <= tok is the invariant (checked below), cu[hi] > tok
+      int lo = 0, hi = n_seq;  // offsets[lo] <= tok is the invariant (checked below), offsets[hi] > tok
       while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2;
-        if (cu[mid] <= tok) lo = mid;
+        if (offsets[mid] <= tok) lo = mid;
         else hi = mid;
       }
-      const int b = cu[lo], e = cu[lo + 1];
+      const int b = offsets[lo], e = offsets[lo + 1];
       if (b >= 0 && b <= tok && tok < e && e <= T_total) {
         int first;
         const long long base = tail_token0(t, lo, H, h, e - b, first, err);
         if (base >= 0) at = base + first + (tok - b);
-      } else if (tok < cu[n_seq] || b > tok) {
+      } else if (tok < offsets[n_seq] || b > tok) {
         raise_error(err, ERR_SHAPE);  // offsets that decrease, start past 0 or pass the total
       }
     }

@@ -220,7 +220,7 @@ def test_fold_skips_bad_sequences():
 
 @pytest.mark.parametrize("fmt", ["native", "mxfp8"])
 @pytest.mark.parametrize("bf16", [True, False])
-@pytest.mark.parametrize("lens", [[1], [0, 3, 64, 1, 65, 0, 130], [1] * 40])
+@pytest.mark.parametrize("lens", [[1], [0, 3, 64, 1, 65, 0, 130], [1] * 40, [1, 0, 2] * 400])
 def test_append_and_read(lens, bf16, fmt):
     """Written places hold the tokens (quantised bit for bit as the oracle does), the others are
     untouched; the read gives the values back exactly, rows behind the last sequence left alone."""
