@@ -189,12 +189,12 @@ tail_fold_kernel(const float* __restrict__ log_lambda, const float* pool, int po
       const int j = e / TOKEN_PIECES, p = e % TOKEN_PIECES;
       float x[16];
       if (p < DK / 16) {
-        tail_load16<float, false, DK>(t.k, t.ks, tok0 + j0 + j, p, x);
+        load16(static_cast<const float*>(t.k) + (tok0 + j0 + j) * DK + 16 * p, x);
         const float w = decay_pow(ll, L - 1 - j0 - j);
 #pragma unroll
         for (int i = 0; i < 16; ++i) sk[j][16 * p + i] = w * x[i];
       } else {
-        tail_load16<float, false, DV>(t.v, t.vs, tok0 + j0 + j, p - DK / 16, x);
+        load16(static_cast<const float*>(t.v) + (tok0 + j0 + j) * DV + 16 * (p - DK / 16), x);
 #pragma unroll
         for (int i = 0; i < 16; ++i) sv[j][16 * (p - DK / 16) + i] = x[i];
       }

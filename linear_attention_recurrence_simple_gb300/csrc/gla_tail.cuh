@@ -38,18 +38,6 @@ __device__ __forceinline__ long long tail_token0(const TailArgs& t, int n, int H
   return ((long long)row * H + h) * t.cap;
 }
 
-// 16 consecutive values (piece p of a row of D) of one token, widened to fp32 (exactly).
-template <class T, bool MX, int D>
-__device__ __forceinline__ void tail_load16(const void* base, const uint8_t* scales, long long token, int p,
-                                            float (&x)[16]) {
-  if constexpr (MX) {
-    const uint4 c = *(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + token * D) + p);
-    dequantise16(c, e8m0_to_f(scales[token * (D / 32) + (p >> 1)]), x);
-  } else {
-    load16(static_cast<const T*>(base) + token * D + 16 * p, x);
-  }
-}
-
 template <class T>
 __device__ __forceinline__ void store16(T* p, const float (&x)[16]);
 template <>
