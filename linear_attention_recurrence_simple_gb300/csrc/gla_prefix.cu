@@ -817,6 +817,7 @@ cudaError_t launch_decode_tile(const void* q, const void* k, const void* v, cons
 
 // dpool[p] = sum of dh0[n] over the sequences n that started from row p, in the order of n (so the
 // result does not depend on the schedule); zeros for a row that none started from.
+// Bound by reading the per-sequence gradients once: 75 MB for 64 sequences x 16 heads, 15 us.
 constexpr int RED_THREADS = 256;
 constexpr int STATE4 = DK * DV / 4;
 constexpr int RED_CTAS = STATE4 / RED_THREADS;  // 18 per (row, head)
