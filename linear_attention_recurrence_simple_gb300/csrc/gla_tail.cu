@@ -274,7 +274,7 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
                     const int32_t* __restrict__ prefix_row, TailArgs t, float* out, int out_rows,
                     const int32_t* __restrict__ out_row, int H, unsigned* err, unsigned long long wait_ns) {
   extern __shared__ uint8_t ft_raw[];
-  __shared__ uint64_t s_full[2], s_empty[2], s_drain[2];  // a buffer is written; its MMAs are done; an issuer's are
+  __shared__ uint64_t s_full[2], s_empty[2], s_drain[2];  // a buffer is written; its MMAs are done; an issuer's are (after an abort)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t base = (smem_u32(ft_raw) + 1023u) & ~1023u;
@@ -407,9 +407,8 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
     if (lane == 0) {
       const uint32_t which = (uint32_t)(warp - FT_WIDEN / 32);
       constexpr uint32_t ID = idesc_bf16(128, DK, 1, 1);
-      bool ok = true;
       for (int c = 0; c < chunks; ++c) {
-        if (!(ok = mbar_wait(&s_full[c & 1], (uint32_t)(c >> 1) & 1u, wait_ns, &s_abort))) break;
+        if (!mbar_wait(&s_full[c & 1], (uint32_t)(c >> 1) & 1u, wait_ns, &s_abort)) break;
         tc_fence_after();
         const uint32_t buf = base + (uint32_t)(c & 1) * FT_BUF;
         const SDesc a = sdesc(buf + FT_V + which * 2u * FT_PANEL, FT_PANEL, 1024, LAYOUT_SW128);
@@ -421,10 +420,6 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
             umma(tmem + which * DK, a + (uint32_t)kk * 2048u, kd + (uint32_t)term * FT_TERM + (uint32_t)kk * 2048u, ID,
                  c > 0 || kk > 0 || term > 0);
         umma_commit(&s_empty[c & 1]);
-      }
-      if (!ok) {  // the MMAs in flight end before tensor memory is freed
-        umma_commit(&s_drain[which]);
-        mbar_wait_drain(&s_drain[which], 0u, 1000000000ull, err);
       }
     }
     __syncwarp();
@@ -478,7 +473,15 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && s_abort) raise_error(err, ERR_TIMEOUT);
+  if (s_abort) {  // a wait gave up, here or there: each issuer's MMAs end before tensor memory is freed
+    if (tid >= FT_WIDEN && lane == 0) {
+      uint64_t* drain = &s_drain[warp - FT_WIDEN / 32];
+      umma_commit(drain);
+      mbar_wait_drain(drain, 0u, 1000000000ull, err);
+    }
+    if (tid == 0) raise_error(err, ERR_TIMEOUT);
+    __syncthreads();
+  }
   if (warp == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(FT_TMEM));
