@@ -65,6 +65,7 @@
 #include <atomic>
 #include <mutex>
 #include <type_traits>
+#include <vector>
 
 #include "gla_common.cuh"
 #include "gla_tc.cuh"
@@ -1372,25 +1373,61 @@ cudaError_t tc_clear_handover(cudaStream_t stream) {
 }
 
 namespace {
-// Two side streams per device for the backward's independent scans (created on first use).
+// Pairs of side streams per device for the backward's independent scans.  Eager calls use the first; a
+// stream that joined a capture stays in it until the capture ends, so a call that meets a pair inside
+// another capture takes the next one (created when there is none).
 constexpr int kMaxDevices = 64;
 std::mutex g_stream_mu;
-cudaStream_t g_side[kMaxDevices][2];
+struct SidePair {
+  cudaStream_t s[2];
+};
+std::vector<SidePair> g_side[kMaxDevices];
+
+// The capture that a stream is in: 0 none, ~0 one that has failed.
+cudaError_t capture_of(cudaStream_t s, unsigned long long& id) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  id = 0;
+  const cudaError_t e = cudaStreamGetCaptureInfo(s, &st, &id);
+  if (st == cudaStreamCaptureStatusNone) id = 0;
+  if (st == cudaStreamCaptureStatusInvalidated) id = ~0ull;
+  return e;
+}
 }  // namespace
 
-cudaError_t side_streams(cudaStream_t (&out)[2]) {
+// `hold` is held until the caller has forked, filled and joined the streams: a capture that took them
+// in between would swallow an eager call's launches.
+cudaError_t side_streams(cudaStream_t stream, cudaStream_t (&out)[2], std::unique_lock<std::mutex>& hold) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(g_stream_mu);
-  for (int i = 0; i < 2; ++i) {
-    if (!g_side[dev][i]) {
-      e = cudaStreamCreateWithFlags(&g_side[dev][i], cudaStreamNonBlocking);
-      if (e != cudaSuccess) return e;
+  unsigned long long mine = 0;
+  if ((e = capture_of(stream, mine)) != cudaSuccess) return e;
+  hold = std::unique_lock<std::mutex>(g_stream_mu);
+  for (const SidePair& p : g_side[dev]) {
+    bool fits = true;
+    for (cudaStream_t s : p.s) {
+      unsigned long long id = 0;
+      if ((e = capture_of(s, id)) != cudaSuccess) return e;
+      fits = fits && (id == 0 || id == mine);
     }
-    out[i] = g_side[dev][i];
+    if (fits) {
+      out[0] = p.s[0];
+      out[1] = p.s[1];
+      return cudaSuccess;
+    }
   }
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // (the caller may be capturing)
+  if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
+  SidePair p = {};
+  e = cudaStreamCreateWithFlags(&p.s[0], cudaStreamNonBlocking);
+  if (e == cudaSuccess && (e = cudaStreamCreateWithFlags(&p.s[1], cudaStreamNonBlocking)) != cudaSuccess)
+    cudaStreamDestroy(p.s[0]);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return e;
+  g_side[dev].push_back(p);
+  out[0] = p.s[0];
+  out[1] = p.s[1];
   return cudaSuccess;
 }
 
@@ -1405,7 +1442,8 @@ cudaError_t launch_tc_bwd(const ChunkArgs& a, float* acc_q, float* acc_k, cudaSt
   const long long n4 = T_total * a.H * DK / 4;
   cudaError_t e;
   cudaStream_t side[2];
-  if ((e = side_streams(side)) != cudaSuccess) return e;
+  std::unique_lock<std::mutex> hold;
+  if ((e = side_streams(stream, side, hold)) != cudaSuccess) return e;
   int dev = 0, sms = 152;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

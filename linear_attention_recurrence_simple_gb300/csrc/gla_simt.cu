@@ -20,13 +20,15 @@
 // These kernels use 64-token chunks so that their fp32 tiles fit in shared memory; the chunk size
 // does not change the result.  One CTA of 256 threads runs the chunk scan of one (sequence,
 // head, column tile).  Rows past the end of a sequence are loaded as zeros, so they add nothing.
+#include <mutex>
 #include <type_traits>
 
 #include "gla_common.cuh"
 
 namespace gla {
 
-cudaError_t side_streams(cudaStream_t (&out)[2]);  // the backward's two, per device
+// The backward's two, to be used while `hold` is held.
+cudaError_t side_streams(cudaStream_t stream, cudaStream_t (&out)[2], std::unique_lock<std::mutex>& hold);
 
 namespace {
 
@@ -531,10 +533,11 @@ cudaError_t launch_simt_fwd(const ChunkArgs& a, cudaStream_t stream) {
 cudaError_t launch_simt_bwd(int dtype_f32, const ChunkArgs& a, cudaStream_t stream) {
   if (!dtype_f32) return cudaErrorInvalidValue;
   cudaStream_t side[2] = {stream, stream};
+  std::unique_lock<std::mutex> hold;
   cudaEvent_t ev[3] = {nullptr, nullptr, nullptr};
   cudaError_t e = cudaSuccess;
   if (a.h0_row) {
-    e = side_streams(side);
+    e = side_streams(stream, side, hold);
     for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = cudaEventCreateWithFlags(&ev[i], cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaEventRecord(ev[2], stream);
     for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = cudaStreamWaitEvent(side[i], ev[2], 0);

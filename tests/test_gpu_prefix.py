@@ -11,6 +11,8 @@ Bounds.  With M the sum of the magnitudes of an entry's terms (in 64 bits, from 
       operands do not occur, so 2^-15 M covers the split and its second-order terms.
   the rounding of a bf16 output: 2^-8 of its value.
 The tails' contents are compared bit for bit."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -716,3 +718,93 @@ def test_captured_packed_calls(bf16):
             assert within_one_bf16_rounding(x.float().cpu().numpy(), y.float().cpu().numpy())
         else:
             assert torch.equal(x, y)
+
+
+def backward_into(x, rg):
+    """A function that runs the backward into tensors of its own (nothing is allocated by the call)."""
+    n_seq, T, H = rg.numel(), x["q"].shape[0], x["q"].shape[1]
+    code = 0 if x["q"].dtype == torch.bfloat16 else 1
+    out = {"d" + n: torch.empty_like(x[n]) for n in ("q", "k", "v", "pool")}
+    out["workspace"] = torch.empty(gla.gla_prefix_bwd_workspace_bytes(n_seq, T, H, code), dtype=torch.uint8,
+                                   device="cuda")
+    return lambda: gla.gla_prefix_bwd(x["q"], x["k"], x["v"], x["ll"], x["dO"], x["pool"], rg, x["cu"], SCALE,
+                                      dhT=x["dhT"], **out)
+
+
+def same_gradients(got, want, bf16):
+    for i, (x, y) in enumerate(zip(got, want)):
+        if bf16 and i < 2:  # dq, dk: partial sums in arrival order
+            assert within_one_bf16_rounding(x.float().cpu().numpy(), y.float().cpu().numpy())
+        else:
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_backward_beside_an_open_capture(bf16):
+    """An eager backward on one stream, and a second capture's on another, while a capture that holds a
+    backward is open: the captures' side streams are their own."""
+    lens, H, rows, P = PACKED[0]
+    cases = [packed(662 + i, lens, H, rows, P, bf16) for i in range(3)]
+    runs = [backward_into(g, rg) for _, g, rg in cases]
+    want = [[t.clone() for t in run()] for run in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    with torch.cuda.stream(streams[0]):
+        graphs[0].capture_begin(capture_error_mode="thread_local")
+        first = runs[0]()
+        with torch.cuda.stream(streams[2]):
+            eager = runs[2]()
+        runs[0]()  # (twice in one capture)
+        graphs[0].capture_end()
+    same_gradients(eager, want[2], bf16)
+    with torch.cuda.stream(streams[1]):
+        graphs[1].capture_begin(capture_error_mode="thread_local")
+        second = runs[1]()
+        graphs[1].capture_end()
+    for t in first + second:
+        t.zero_()
+    torch.cuda.synchronize()
+    for g, s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    same_gradients(first, want[0], bf16)
+    same_gradients(second, want[1], bf16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_backwards_of_several_threads(bf16):
+    """Threads that run backwards on streams of their own, eagerly, one of them capturing its calls."""
+    lens, H, rows, P = PACKED[0]
+    cases = [packed(665 + i, lens, H, rows, P, bf16) for i in range(4)]
+    runs = [backward_into(g, rg) for _, g, rg in cases]
+    want = [[t.clone() for t in run()] for run in runs]
+    torch.cuda.synchronize()
+    got, failed = [None] * 4, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(8):
+                    if i == 0:
+                        g = torch.cuda.CUDAGraph()
+                        g.capture_begin(capture_error_mode="thread_local")
+                        got[i] = runs[i]()
+                        g.capture_end()
+                        for t in got[i]:
+                            t.zero_()
+                        g.replay()
+                    else:
+                        got[i] = runs[i]()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001 (reported below)
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for x, y in zip(got, want):
+        same_gradients(x, y, bf16)
