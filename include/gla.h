@@ -340,8 +340,9 @@ int gla_chunk_fwd_host(const void* q, const void* k, const void* v, const float*
  *                  GLA_TAIL_PLAIN: elements of the call's dtype; k_scales and v_scales unused.
  *                  GLA_TAIL_MXFP8: E4M3 codes with E8M0 scales k_scales [rows, H, cap, 3] and
  *                  v_scales [rows, H, cap, 6], one per 32 values, quantised by the rule of
- *                  gla_decode_step_mxfp8_state (no finite value saturates; an infinity stays one and
- *                  costs its block's other values, a NaN stays one).
+ *                  gla_decode_step_mxfp8_state (no finite value saturates; an infinity costs its
+ *                  block's other values).  In every call an element is code x scale in fp32: an
+ *                  infinity stays one, a NaN stays one.
  *                cap >= 16 and a multiple of 16 (else GLA_ERR_SHAPE); every array 16-byte aligned.
  *   tail_slot    [n] int32 device: the tail row of each sequence, NULL = row n (then rows >= n is
  *                required).  Rows that a call writes must be distinct.

@@ -33,11 +33,17 @@ namespace {
 // (16 values, against the same 16 of q in registers), the six partial products of a token meet in
 // shared memory; thread (r, p) = (tid / 12, tid % 12) adds piece p of the values of tokens r and r + 16, loaded
 // before the keys are waited for, into 16 sums of its own; the 16 threads of a piece meet once per
-// sequence.  MXFP8 tails are bound by the widening and the FMAs, fp32 ones by HBM: 1,000 x 16 heads, 143
+// sequence.  A block's scale multiplies the piece's sum (keys) or the weight (values), once for 16 codes; where
+// scale, query or weight is so large that this could pass fp32's range, or that code x scale is an infinity, it
+// multiplies the codes.  MXFP8 tails are bound by the widening and the FMAs, fp32 ones by HBM: 1,000 x 16 heads, 143
 // tokens on average, 265 us (MXFP8) and 492 us (fp32, 0.81 of the measured copy bandwidth).
 constexpr int DEC_THREADS = DV;
 constexpr int DEC_TOK = 32;
 constexpr int DEC_TILE = 4;
+// Scales of 2^65 and more (the code of an infinity stands under 2^120): the element is formed before it is
+// multiplied with anything.
+constexpr uint32_t WIDE_SCALE = 192;
+constexpr float WIDE_FACTOR = 1.152921504606846976e18f;  // 2^60: below it, 448 x 2^64 x factor x 96 stays in fp32's range
 static_assert(DEC_TOK * 6 == DEC_THREADS && 16 * 12 == DEC_THREADS, "pieces of a chunk");
 
 // A 16-value piece as it is stored: fp32, or codes and their block's scale byte.
@@ -143,6 +149,9 @@ prefix_decode_kernel(const float* __restrict__ q, const float* __restrict__ k, c
     const long long tok0 = s_tok0[i];
     float qv[16], sum[16];
     load16(&sq[i][16 * kp], qv);
+    bool wide_q = false;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) wide_q = wide_q || !(fabsf(qv[e]) < WIDE_FACTOR);
 #pragma unroll
     for (int e = 0; e < 16; ++e) sum[e] = 0.f;
     for (int j0 = 0; j0 < L; j0 += DEC_TOK) {
@@ -152,17 +161,26 @@ prefix_decode_kernel(const float* __restrict__ q, const float* __restrict__ k, c
 #pragma unroll
       for (int u = 0; u < 2; ++u) x[u].load(t.v, t.vs, tok0 + j0 + vr + 16 * u, vp, j0 + vr + 16 * u < L);
       float d = 0.f;
-      y.each([&](int e, float c) { d = fmaf(c, qv[e], d); });
+      if (MX && (wide_q || y.s >= WIDE_SCALE)) {
+        y.each([&](int e, float c) { d = fmaf(c * y.scale(), qv[e], d); });
+      } else {
+        y.each([&](int e, float c) { d = fmaf(c, qv[e], d); });
+        d *= y.scale();
+      }
       __syncthreads();  // the weights of the chunk before have been used
-      sw[kj][kp] = d * y.scale();
+      sw[kj][kp] = d;
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int jj = vr + 16 * u, j = j0 + jj;
         if (j < L) {
-          const float w = (((sw[jj][0] + sw[jj][1]) + (sw[jj][2] + sw[jj][3])) + (sw[jj][4] + sw[jj][5])) * decay_pow(ll, L - j) *
-                          x[u].scale();
-          x[u].each([&](int e, float c) { sum[e] = fmaf(w, c, sum[e]); });
+          float w = (((sw[jj][0] + sw[jj][1]) + (sw[jj][2] + sw[jj][3])) + (sw[jj][4] + sw[jj][5])) * decay_pow(ll, L - j);
+          if (MX && (x[u].s >= WIDE_SCALE || !(fabsf(w) < WIDE_FACTOR))) {
+            x[u].each([&](int e, float c) { sum[e] = fmaf(w, c * x[u].scale(), sum[e]); });
+          } else {
+            w *= x[u].scale();
+            x[u].each([&](int e, float c) { sum[e] = fmaf(w, c, sum[e]); });
+          }
         }
       }
     }
@@ -197,8 +215,11 @@ prefix_decode_kernel(const float* __restrict__ q, const float* __restrict__ k, c
 //                 in turn.  Each column is kept in f16's range by a power of two of its own, raised
 //                 (and the sums rescaled) when a weight outgrows it; a weight 2^-28 of the
 //                 column's largest so far is lost.
-//     A sequence whose chunks fall to one warp is added to the tile's sums directly; the first and
-//     last sequence of a warp's range may be shared, and those parts meet in warp order.
+//       A chunk that holds a scale of 2^65 or more (an infinity is code 448 under 2^120), or whose weights
+//       could leave fp32's range under their scales, goes through the CUDA cores instead: elements code x scale
+//       in fp32, products and sums in fp32 (far_sums).
+//     The warp that has a sequence's first chunk adds to the tile's sums directly; the others that share it
+//     keep their parts, which meet in warp order.
 // mma.sync rather than tcgen05: a sequence brings one query row, so a 128-row tile would stand empty, and
 // the codes are widened in registers either way.  Bound by instruction issue (about 820 warp
 // instructions per 32 MXFP8 tokens) beside HBM: 1,280 x 16 heads, 143 tokens on average, MXFP8, 187 us (0.73
@@ -218,7 +239,7 @@ struct PdStage {
 template <bool MX>
 struct PdSmem {
   static constexpr uint32_t O = PD_WARPS * PdStage<MX>::BYTES;  // [16][192] sums
-  static constexpr uint32_t PART = O + TILE_MAX * DV * 4;                        // [warps][192], a warp's first part
+  static constexpr uint32_t PART = O + TILE_MAX * DV * 4;                        // [warps][192], a warp's part of a sequence that another begins
   static constexpr uint32_t Q = PART + PD_WARPS * DV * 4;                        // [16][96] bf16
   static constexpr uint32_t BAR = Q + TILE_MAX * DK * 2;
   static constexpr uint32_t BYTES = BAR + PD_WARPS * 2 * 8;
@@ -272,12 +293,59 @@ __device__ __forceinline__ uint32_t e8m0x2_to_bf2(uint32_t two) {
   asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
   return r;
 }
+constexpr int WIDE_SUM = 100;  // the MMAs take weights under their scales of up to 2^100, and 2^100 times a run's first
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+// The first n bytes of a word (n <= 0: none).
+__device__ __forceinline__ uint32_t cut_bytes(uint32_t x, int n) { return n >= 4 ? x : n <= 0 ? 0u : x & ((1u << (8 * n)) - 1u); }
+
+struct Sums8 {
+  float v[8];
+};
+// An MXFP8 chunk's share of the output in fp32 (whole warp): tokens tok .. tok + m - 1, of ages `age` and less, keys
+// from where they stand (the stage may hold the next chunk's), values from the stage.  Lane (g, tq < 3) has
+// columns 64 tq + 8 g .. + 7.  Kept out of the kernel's loop, whose registers it would take.
+__device__ __noinline__ Sums8 far_sums(const TailArgs& t, long long tok, int m, float ll, int age, const __nv_bfloat16* q,
+                                          const uint8_t* v, const uint8_t* vs) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  float w = 0.f;  // lane j: token j's weight
+  if (lane < m) {
+    const uint8_t* k = static_cast<const uint8_t*>(t.k) + (tok + lane) * DK;
+    const uint8_t* ks = t.ks + (tok + lane) * (DK / 32);
+#pragma unroll 1
+    for (int e = 0; e < DK; e += 4) {
+      const float s = e8m0_to_f(ks[e >> 5]);
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(k + e);
+      const uint2 y = *reinterpret_cast<const uint2*>(q + e);
+      const float2 c0 = e4m3x2_to_f2(x & 0xFFFFu), c1 = e4m3x2_to_f2(x >> 16);
+      w = fmaf(c0.x * s, __uint_as_float(y.x << 16), w);
+      w = fmaf(c0.y * s, __uint_as_float(y.x & 0xFFFF0000u), w);
+      w = fmaf(c1.x * s, __uint_as_float(y.y << 16), w);
+      w = fmaf(c1.y * s, __uint_as_float(y.y & 0xFFFF0000u), w);
+    }
+    w *= decay_pow(ll, age - lane);
+  }
+  Sums8 r = {};
+#pragma unroll 1
+  for (int j = 0; j < m; ++j) {
+    const float wj = __shfl_sync(0xffffffffu, w, j);
+    if (tq < 3) {
+      const float s = e8m0_to_f(vs[6 * j + 2 * tq + (g >> 2)]);
+      const uint2 x = *reinterpret_cast<const uint2*>(v + j * DV + 64 * tq + 8 * g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 c = e4m3x2_to_f2((e < 2 ? x.x : x.y) >> (16 * (e & 1)) & 0xFFFFu);
+        r.v[2 * e] = fmaf(wj, c.x * s, r.v[2 * e]);
+        r.v[2 * e + 1] = fmaf(wj, c.y * s, r.v[2 * e + 1]);
+      }
+    }
+  }
+  return r;
 }
 
 template <bool MX>
@@ -291,7 +359,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   using SM = PdSmem<MX>;
   using BF = __nv_bfloat16;
   extern __shared__ __align__(128) uint8_t pd_smem[];
-  __shared__ int s_row[TILE_MAX], s_len[TILE_MAX], s_cu[TILE_MAX + 1], s_part[2 * PD_WARPS];  // s_part: sequences of the shared parts, -1: none
+  __shared__ int s_row[TILE_MAX], s_len[TILE_MAX], s_cu[TILE_MAX + 1], s_part[PD_WARPS];  // s_part: sequences of the warps' parts, -1: none
   __shared__ long long s_tok0[TILE_MAX];
   __shared__ float s_self[TILE_MAX];
   __shared__ int s_abort;
@@ -359,13 +427,14 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   if (lane == 0) {
     mbar_init(&full[0], 1);
     mbar_init(&full[1], 1);
-    s_part[2 * warp] = s_part[2 * warp + 1] = -1;
+    s_part[warp] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u)
     if (tid + u * PD_THREADS < cnt * (DK / 8)) reinterpret_cast<uint4*>(sQ)[tid + u * PD_THREADS] = rq[u];
   for (int e = tid; e < cnt * (DV / 4); e += PD_THREADS) reinterpret_cast<float4*>(sO)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int e = tid; e < PD_WARPS * (DV / 4); e += PD_THREADS) reinterpret_cast<float4*>(sPart)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
 
   // ---- this warp's chunks [c0, c1) of the tile's list; its first loads
@@ -398,6 +467,11 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
       bulk_copy(st32 + ST::V, static_cast<const uint8_t*>(t.v) + next_tok * ST::V_ROW, bytes, &full[1]);
       if (MX) bulk_copy(st32 + ST::VS, t.vs + next_tok * (DV / 32), vs, &full[1]);
     }
+  };
+  auto release = [&](int m) {  // a chunk's values are read (the zeros behind its m tokens were written through the generic proxy)
+    if (m < ST::TOK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (loads_v < loads_k) load_values();
   };
   if (c0 < c1) {
     load_keys();
@@ -504,7 +578,9 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   for (int c = c0; c < c1 && ok;) {
     while (c >= s_cu[seq + 1]) ++seq;
     const int first = s_cu[seq], last = min(s_cu[seq + 1], c1), L = s_len[seq];
-    const bool whole = c == first && last == s_cu[seq + 1];
+    float* const dst = first >= c0 ? sO + seq * DV : sPart + warp * DV;
+    if (first < c0 && lane == 0) s_part[warp] = seq;
+    bool wide_q = false;  // q's magnitude calls for weights in fp32 throughout
     // q as the B operand: one column (n = 0, the lanes with g = 0); block b, K step u of thread tq:
     // columns 32 b + 8 tq + 4 u .. + 3
     uint32_t qf[3][4];
@@ -529,6 +605,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int e2 = max(exponent_of(m), -100) - 10;  // the largest comes to [2^10, 2^11)
+        wide_q = e2 > 50 || e2 < -50;
         const float inv = pow2i(-e2);
         qn = pow2i(e2);
 #pragma unroll
@@ -542,6 +619,8 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
 #pragma unroll
         for (int e = 0; e < 4; ++e) qf[b][e] = g == 0 ? qf[b][e] : 0u;
     }
+    while (c < last && ok) {  // runs of chunks that the MMAs take, each but the last with one chunk behind it that they do not
+    bool far_chunk = false;
     float acc[12][4];  // 16 columns each: see the flush below
 #pragma unroll
     for (int i = 0; i < 12; ++i)
@@ -586,6 +665,12 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
           sc[u][1] = d[0][2] + d[1][2] + d[2][2];
         }
       }
+      uint32_t far = wide_q;  // (MXFP8) not zero in some lane: the chunk goes through the CUDA cores
+      if constexpr (MX) {     // the scales' bytes, four a lane: 2^65 and more have their two top bits set
+        uint32_t x = lane < DK / 32 * ST::TOK / 4 ? reinterpret_cast<const uint32_t*>(st + ST::KS)[lane] : 0u;
+        if (m < ST::TOK) x = cut_bytes(x, 3 * m - 4 * lane);
+        far |= x & (x << 1) & 0x80808080u;
+      }
       __syncwarp();
       if (next < c1) load_keys();  // the keys are read
       // lane j takes token j's weight (bf16: lanes 16 .. 31 repeat)
@@ -628,9 +713,14 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int need = mx > 0.f ? max(exponent_of(mx), -120) : -1000;
-        const bool grow = need > E + 10;
-        if (__any_sync(0xffffffffu, grow)) {
+        int need = mx > 0.f ? max(exponent_of(mx), -120) : -1000;
+        uint2 x = lane < DV / 32 * ST::TOK / 8 ? reinterpret_cast<const uint2*>(st + ST::VS)[lane] : make_uint2(0u, 0u);
+        if (m < ST::TOK) x = make_uint2(cut_bytes(x.x, 6 * m - 8 * lane), cut_bytes(x.y, 6 * m - 8 * lane - 4));
+        far |= ((x.x & (x.x << 1)) | (x.y & (x.y << 1))) & 0x80808080u;
+        if (__any_sync(0xffffffffu, far != 0u || need > E + 10)) {
+          far_chunk = __any_sync(0xffffffffu, far != 0u || need > min(E == -1000 ? 0 : E, 0) + WIDE_SUM);
+          if (far_chunk) break;
+          const bool grow = need > E + 10;
           const float f = !grow ? 1.f : (E < -126 ? 0.f : pow2i(E - need));
           const float f0 = __shfl_sync(0xffffffffu, f, 8 * tq), f1 = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
 #pragma unroll
@@ -685,17 +775,10 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
           }
         }
       }
-      // the values are read (the zeros above were written through the generic proxy)
-      if (m < ST::TOK) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (loads_v < loads_k) load_values();
+      release(m);
     }
     if (!ok) break;
-    // the sequence's sums (this warp's part of them): thread (g, tq < 3) holds columns 64 tq + 8 g
-    // .. + 7.  A part that the warp ends with goes to its stage (whose chunks have all been read).
-    const bool second = last == c1 && c0 < first;
-    float* dst = whole ? sO + seq * DV : second ? reinterpret_cast<float*>(st) : sPart + warp * DV;
-    if (!whole && lane == 0) s_part[2 * warp + second] = seq;
+    // the run's sums: thread (g, tq < 3) holds columns 64 tq + 8 g .. + 7
     const float back = MX ? pow2i(__shfl_sync(0xffffffffu, E, 4 * ((2 * tq + (g >> 2)) & 7)) - 4) : 1.f;
     float y[8];
 #pragma unroll
@@ -715,14 +798,22 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
       }
     if (tq < 3) {
       float4* p = reinterpret_cast<float4*>(dst + 64 * tq + 8 * g);
-      float4 u = make_float4(y[0], y[1], y[2], y[3]), w = make_float4(y[4], y[5], y[6], y[7]);
-      if (whole) {
-        const float4 a = p[0], b = p[1];
-        u = make_float4(u.x + a.x, u.y + a.y, u.z + a.z, u.w + a.w);
-        w = make_float4(w.x + b.x, w.y + b.y, w.z + b.z, w.w + b.w);
+      const float4 a = p[0], b = p[1];
+      p[0] = make_float4(y[0] + a.x, y[1] + a.y, y[2] + a.z, y[3] + a.w);
+      p[1] = make_float4(y[4] + b.x, y[5] + b.y, y[6] + b.z, y[7] + b.w);
+    }
+    if constexpr (MX) {
+      if (far_chunk) {
+        const int j0 = (c - first) * ST::TOK, m = min(ST::TOK, L - j0);
+        const Sums8 z = far_sums(t, s_tok0[seq] + j0, m, ll, L - j0, sQ + seq * DK, st + ST::V, st + ST::VS);
+        if (tq < 3) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[64 * tq + 8 * g + e] += z.v[e];
+        }
+        release(m);
+        ++c;
       }
-      p[0] = u;
-      p[1] = w;
+    }
     }
   }
    }
@@ -748,11 +839,8 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   }
   for (int col = tid; col < DV; col += PD_THREADS)
 #pragma unroll
-    for (int p = 0; p < 2 * PD_WARPS; ++p)
-      if (s_part[p] >= 0) {
-        const float* part = p & 1 ? reinterpret_cast<const float*>(pd_smem + (p >> 1) * ST::BYTES) : sPart + (p >> 1) * DV;
-        sO[s_part[p] * DV + col] += part[col];
-      }
+    for (int p = 0; p < PD_WARPS; ++p)
+      if (s_part[p] >= 0) sO[s_part[p] * DV + col] += sPart[p * DV + col];
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < 3; ++u) {
