@@ -366,6 +366,8 @@ typedef struct gla_tail {
  *     o = scale (lambda^(L+1) S_p^T q + sum_{j < L} lambda^(L-j) (q . k_j) v_j + (q . k) v),
  * the readout after the token's own update, with the token's k and v as they are given; then k and
  * v are written to place L of the tail (quantised where it is MXFP8), which needs L < cap.
+ * bf16 calls: sums in fp32; states, and the weights lambda^(L-j) (q . k_j), with 16 bits or more each, however far
+ * apart the elements of a tail, its weights or its blocks lie; o rounded once.  fp32 calls: fp32 throughout.
  *   q, k [N, H, 96]; v, o [N, H, 192]; dtype `dtype`; N * H below 2^31.  One launch.  For L beyond about 256 (bf16)
  *   or 500 (MXFP8) tokens a state of its own (gla_tail_fold, then gla_decode_step) is less to read. */
 int gla_prefix_decode_step(const void* q, const void* k, const void* v, const float* log_lambda, float scale,

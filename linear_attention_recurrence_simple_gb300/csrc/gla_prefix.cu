@@ -206,18 +206,21 @@ prefix_decode_kernel(const float* __restrict__ q, const float* __restrict__ k, c
 //     all of them.  A warp streams its chunks through a stage of its own in shared memory (bulk
 //     copies: the tokens of a (row, head) are contiguous) and multiplies on the tensor cores:
 //       weights   K [16 tokens x 96] times q (one column of N = 8 used): exact products.  E4M3 codes
-//                 widen exactly to f16; q is brought to f16 by a power of two (its 8 bits fit; what
-//                 lies 2^-35 below the largest is lost).  Block scales enter in fp32, per 32 columns.
+//                 widen exactly to f16; q is brought to f16 by a power of two (its 8 bits fit down to
+//                 2^-27 of the largest).  Block scales enter in fp32, per 32 columns.
 //       output    V^T [16 columns x 16 tokens] times w [16 tokens x 8].  bf16 tails: w's even columns
 //                 hold the high bf16 of the weight, the odd ones the low one (their sums meet in one
 //                 thread).  MXFP8: column b holds w_j 2^(e_jb), the weight times the scale of column
 //                 block b, so that the codes enter unscaled (exact in f16); its high and low f16 go
 //                 in turn.  Each column is kept in f16's range by a power of two of its own, raised
-//                 (and the sums rescaled) when a weight outgrows it; a weight 2^-28 of the
-//                 column's largest so far is lost.
-//       A chunk that holds a scale of 2^65 or more (an infinity is code 448 under 2^120), or whose weights
-//       could leave fp32's range under their scales, goes through the CUDA cores instead: elements code x scale
-//       in fp32, products and sums in fp32 (far_sums).
+//                 (and the sums rescaled) when a weight outgrows it.  A pair has 16 bits of a weight
+//                 down to 2^-19 of that power.
+//       A chunk with weights below that (the block's largest element may be zero in a column whose sum is made
+//       of the others), with a scale of 2^65 or more (an infinity is code 448 under 2^120) or with weights that could
+//       leave fp32's range under their scales, and a sequence whose q does not fit, go through the CUDA cores
+//       instead: elements code x scale in fp32, products and sums in fp32 (far_sums).  That takes four times as
+//       long (1,280 x 16 with such a scale in every chunk: 740 us), but of normally distributed keys and values
+//       about one chunk in ten thousand calls for it.
 //     The warp that has a sequence's first chunk adds to the tile's sums directly; the others that share it
 //     keep their parts, which meet in warp order.
 // mma.sync rather than tcgen05: a sequence brings one query row, so a 128-row tile would stand empty, and
@@ -296,6 +299,8 @@ __device__ __forceinline__ uint32_t e8m0x2_to_bf2(uint32_t two) {
 constexpr int WIDE_SUM = 100;  // the MMAs take weights under their scales of up to 2^100, and 2^100 times a run's first
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+// Weights whose bits - 1 are below this are less than 2^-19 of the power of two e (but not zero).
+__device__ __forceinline__ uint32_t weak_below(int e) { return __float_as_uint(pow2i(e - 19)) - 1u; }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
@@ -597,15 +602,19 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
       }
       if (MX) {
         float m = 0.f;
+        uint32_t low = ~0u;  // the smallest but zero (bits - 1)
 #pragma unroll
         for (int b = 0; b < 3; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(qf[b][e] << 16)), fabsf(__uint_as_float(qf[b][e] & 0xFFFF0000u))));
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x = qf[b][e] << 16 & 0x7FFFFFFFu, y = qf[b][e] & 0x7FFF0000u;
+            m = fmaxf(m, fmaxf(__uint_as_float(x), __uint_as_float(y)));
+            low = min(low, min(x - 1u, y - 1u));
+          }
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int e2 = max(exponent_of(m), -100) - 10;  // the largest comes to [2^10, 2^11)
-        wide_q = e2 > 50 || e2 < -50;
+        wide_q = e2 > 50 || e2 < -50 || __any_sync(0xffffffffu, low < __float_as_uint(pow2i(e2 - 17)) - 1u);
         const float inv = pow2i(-e2);
         qn = pow2i(e2);
 #pragma unroll
@@ -699,6 +708,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
       }
       if constexpr (MX) {
         float mx = 0.f;
+        uint32_t low = ~0u;  // the smallest but zero (bits - 1)
 #pragma unroll
         for (int u = 0; u < ST::SUB; ++u) {
           const uint8_t* vp = st + ST::VS + 6 * (16 * u + tq) + min(g, DV / 32 - 1);
@@ -709,18 +719,20 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
           for (int i = 0; i < 4; ++i) {
             wt[u][i] = g < DV / 32 && 16 * u + tq + 4 * i < m ? wt[u][i] * vs[i] : 0.f;  // (past the end: maybe NaN)
             mx = fmaxf(mx, fabsf(wt[u][i]));
+            low = min(low, (__float_as_uint(wt[u][i]) & 0x7FFFFFFFu) - 1u);
           }
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int need = mx > 0.f ? max(exponent_of(mx), -120) : -1000;
+        int need = mx > 0.f ? max(exponent_of(mx), -115) : -1000;
         uint2 x = lane < DV / 32 * ST::TOK / 8 ? reinterpret_cast<const uint2*>(st + ST::VS)[lane] : make_uint2(0u, 0u);
         if (m < ST::TOK) x = make_uint2(cut_bytes(x.x, 6 * m - 8 * lane), cut_bytes(x.y, 6 * m - 8 * lane - 4));
         far |= ((x.x & (x.x << 1)) | (x.y & (x.y << 1))) & 0x80808080u;
-        if (__any_sync(0xffffffffu, far != 0u || need > E + 10)) {
-          far_chunk = __any_sync(0xffffffffu, far != 0u || need > min(E == -1000 ? 0 : E, 0) + WIDE_SUM);
+        const bool grow = need > E + 4;
+        if (__any_sync(0xffffffffu, far != 0u || grow || low < weak_below(E))) {
+          far_chunk = __any_sync(0xffffffffu, far != 0u || need > min(E == -1000 ? 0 : E, 0) + WIDE_SUM ||
+                                                  low < weak_below(grow ? need : E));
           if (far_chunk) break;
-          const bool grow = need > E + 10;
           const float f = !grow ? 1.f : (E < -126 ? 0.f : pow2i(E - need));
           const float f0 = __shfl_sync(0xffffffffu, f, 8 * tq), f1 = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
 #pragma unroll
@@ -730,7 +742,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
           if (grow) E = need;
         }
       }
-      const float up = MX ? pow2i(4 - E) : 1.f;
+      const float up = MX ? pow2i(10 - E) : 1.f;
 #pragma unroll
       for (int u = 0; u < ST::SUB; ++u) {
         uint32_t h0, h1, l0, l1;
@@ -779,7 +791,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     }
     if (!ok) break;
     // the run's sums: thread (g, tq < 3) holds columns 64 tq + 8 g .. + 7
-    const float back = MX ? pow2i(__shfl_sync(0xffffffffu, E, 4 * ((2 * tq + (g >> 2)) & 7)) - 4) : 1.f;
+    const float back = MX ? pow2i(__shfl_sync(0xffffffffu, E, 4 * ((2 * tq + (g >> 2)) & 7)) - 10) : 1.f;
     float y[8];
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj)

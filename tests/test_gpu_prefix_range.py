@@ -131,3 +131,55 @@ def test_keys_and_values_near_the_top_of_the_range(bf16):
     keep = np.ones((3, H, DV), bool)
     keep[1, :, 70] = False
     check_columns(c, o, keep)
+
+
+# ---- one element far above the rest ------------------------------------------------------------
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("ratio", [16, 20, 24, 40, 90])
+def test_a_value_far_above_its_block_leaves_the_other_columns_alone(ratio, bf16):
+    """One element 2^ratio times the others in one token's value, early, late and twice: the tokens
+    without it keep their weights' bits in the block's other 31 columns."""
+    lens, H = [70, 8, 140, 40], 3
+    c = Case(940 + ratio, lens, H, [0, 0, 1, 1], 2, bf16, "mxfp8")
+    v = c.t.v.copy()
+    for n, places in enumerate(([3], [6], [20, 120], [39])):
+        for j in places:
+            v[c.slots[n], :, j, 40] = 2.0 ** ratio
+            v[c.slots[n], :, j, 191] = -(2.0 ** ratio)
+    requantise(c, c.t.k, v)
+    check_columns(c, c.decode())
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_tokens_whose_weights_are_far_apart(bf16):
+    """Weights of one sequence spread over 2^60 by their keys, the large ones on tokens whose values are
+    zero in most columns; and a head with lambda = 0.5."""
+    lens, H = [64, 33, 90], 5
+    c = Case(950, lens, H, [0, 1, 1], 2, bf16, "mxfp8")
+    rng = np.random.default_rng(7)
+    k, v = c.t.k.copy(), c.t.v.copy()
+    e = rng.integers(-30, 31, k.shape[:3])
+    k *= np.exp2(e)[..., None]
+    v[e > -10] = 0.0
+    v[..., 100] = 1.0                                    # (a column that has them all)
+    requantise(c, k, v)
+    check_columns(c, c.decode())
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("ratio", [20, 30, 60])
+def test_a_query_element_far_above_the_rest_over_keys_without_it(ratio, bf16):
+    """One element of q 2^ratio times the others, keys that are zero there: what the rest of q gives is
+    all there is."""
+    lens, H = [50, 20, 33], 2
+    c = Case(960 + ratio, lens, H, [0, 1, 1], 2, bf16, "mxfp8")
+    k = c.t.k.copy()
+    k[..., 3] = 0.0
+    requantise(c, k, c.t.v)
+    c.q[:, :, 3] = 2.0 ** ratio
+    c.k[:, :, 3] = 0.0
+    c.pool[:, :, 3] = 0.0
+    c.poolg = torch.from_numpy(c.pool).cuda()
+    for x in "qk":
+        c.g[x] = torch.from_numpy(getattr(c, x)).cuda().to(c.dt)
+    check_columns(c, c.decode())
