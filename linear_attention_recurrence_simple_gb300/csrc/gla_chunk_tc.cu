@@ -63,11 +63,10 @@
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 #include <type_traits>
-#include <vector>
 
 #include "gla_common.cuh"
+#include "gla_side.cuh"
 #include "gla_tc.cuh"
 
 namespace gla {
@@ -1372,65 +1371,6 @@ cudaError_t tc_clear_handover(cudaStream_t stream) {
   return cudaMemsetAsync(p, 0, sizeof(g_handover), stream);
 }
 
-namespace {
-// Pairs of side streams per device for the backward's independent scans.  Eager calls use the first; a
-// stream that joined a capture stays in it until the capture ends, so a call that meets a pair inside
-// another capture takes the next one (created when there is none).
-constexpr int kMaxDevices = 64;
-std::mutex g_stream_mu;
-struct SidePair {
-  cudaStream_t s[2];
-};
-std::vector<SidePair> g_side[kMaxDevices];
-
-// The capture that a stream is in: 0 none, ~0 one that has failed.
-cudaError_t capture_of(cudaStream_t s, unsigned long long& id) {
-  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  id = 0;
-  const cudaError_t e = cudaStreamGetCaptureInfo(s, &st, &id);
-  if (st == cudaStreamCaptureStatusNone) id = 0;
-  if (st == cudaStreamCaptureStatusInvalidated) id = ~0ull;
-  return e;
-}
-}  // namespace
-
-// `hold` is held until the caller has forked, filled and joined the streams: a capture that took them
-// in between would swallow an eager call's launches.
-cudaError_t side_streams(cudaStream_t stream, cudaStream_t (&out)[2], std::unique_lock<std::mutex>& hold) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  unsigned long long mine = 0;
-  if ((e = capture_of(stream, mine)) != cudaSuccess) return e;
-  hold = std::unique_lock<std::mutex>(g_stream_mu);
-  for (const SidePair& p : g_side[dev]) {
-    bool fits = true;
-    for (cudaStream_t s : p.s) {
-      unsigned long long id = 0;
-      if ((e = capture_of(s, id)) != cudaSuccess) return e;
-      fits = fits && (id == 0 || id == mine);
-    }
-    if (fits) {
-      out[0] = p.s[0];
-      out[1] = p.s[1];
-      return cudaSuccess;
-    }
-  }
-  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // (the caller may be capturing)
-  if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
-  SidePair p = {};
-  e = cudaStreamCreateWithFlags(&p.s[0], cudaStreamNonBlocking);
-  if (e == cudaSuccess && (e = cudaStreamCreateWithFlags(&p.s[1], cudaStreamNonBlocking)) != cudaSuccess)
-    cudaStreamDestroy(p.s[0]);
-  cudaThreadExchangeStreamCaptureMode(&mode);
-  if (e != cudaSuccess) return e;
-  g_side[dev].push_back(p);
-  out[0] = p.s[0];
-  out[1] = p.s[1];
-  return cudaSuccess;
-}
-
 // Backward in bf16: dv and dh0 directly; dq and dk through fp32 partial sums in acc_q / acc_k
 // (each tc_bwd_acc_bytes, 16-byte aligned), each rounded to bf16 once its scan is done.  The three
 // scans are independent: DV runs on the caller's stream, and DK and DQ (each with its zeroing and
@@ -1441,9 +1381,7 @@ cudaError_t launch_tc_bwd(const ChunkArgs& a, float* acc_q, float* acc_k, cudaSt
   const size_t acc = tc_bwd_acc_bytes(T_total, a.H);
   const long long n4 = T_total * a.H * DK / 4;
   cudaError_t e;
-  cudaStream_t side[2];
-  std::unique_lock<std::mutex> hold;
-  if ((e = side_streams(stream, side, hold)) != cudaSuccess) return e;
+  SideFork<CudaSideApi> sides;
   int dev = 0, sms = 152;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1473,14 +1411,9 @@ cudaError_t launch_tc_bwd(const ChunkArgs& a, float* acc_q, float* acc_k, cudaSt
     }
     return r;
   };
-  cudaEvent_t ev[3] = {nullptr, nullptr, nullptr};
-  for (int i = 0; i < 3; ++i)
-    if ((e = cudaEventCreateWithFlags(&ev[i], cudaEventDisableTiming)) != cudaSuccess) break;
-  if (e == cudaSuccess) e = cudaEventRecord(ev[0], stream);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(side[0], ev[0], 0);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(side[1], ev[0], 0);
-  if (e == cudaSuccess) e = partial_scan(side[0], acc_k, a.dk, true);
-  if (e == cudaSuccess) e = partial_scan(side[1], acc_q, a.o, false);  // a.o carries dq here
+  e = sides.fork(side_pool(), stream);
+  if (e == cudaSuccess) e = partial_scan(sides.side(0), acc_k, a.dk, true);
+  if (e == cudaSuccess) e = partial_scan(sides.side(1), acc_q, a.o, false);  // a.o carries dq here
   if (e == cudaSuccess) {
     ScanParams p;
     p.a = a;
@@ -1489,13 +1422,7 @@ cudaError_t launch_tc_bwd(const ChunkArgs& a, float* acc_q, float* acc_k, cudaSt
     p.out = a.dv;
     e = launch_scan<MODE_DV>(a.k, a.q, a.dO, p, stream, max_ctas);
   }
-  if (e == cudaSuccess) e = cudaEventRecord(ev[1], side[0]);
-  if (e == cudaSuccess) e = cudaEventRecord(ev[2], side[1]);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, ev[1], 0);
-  if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, ev[2], 0);
-  for (int i = 0; i < 3; ++i)
-    if (ev[i]) cudaEventDestroy(ev[i]);
-  return e;
+  return sides.join(e);
 }
 
 }  // namespace gla

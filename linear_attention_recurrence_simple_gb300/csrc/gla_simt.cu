@@ -20,15 +20,12 @@
 // These kernels use 64-token chunks so that their fp32 tiles fit in shared memory; the chunk size
 // does not change the result.  One CTA of 256 threads runs the chunk scan of one (sequence,
 // head, column tile).  Rows past the end of a sequence are loaded as zeros, so they add nothing.
-#include <mutex>
 #include <type_traits>
 
 #include "gla_common.cuh"
+#include "gla_side.cuh"
 
 namespace gla {
-
-// The backward's two, to be used while `hold` is held.
-cudaError_t side_streams(cudaStream_t stream, cudaStream_t (&out)[2], std::unique_lock<std::mutex>& hold);
 
 namespace {
 
@@ -532,28 +529,14 @@ cudaError_t launch_simt_fwd(const ChunkArgs& a, cudaStream_t stream) {
 // side by side on the backward's side streams.
 cudaError_t launch_simt_bwd(int dtype_f32, const ChunkArgs& a, cudaStream_t stream) {
   if (!dtype_f32) return cudaErrorInvalidValue;
-  cudaStream_t side[2] = {stream, stream};
-  std::unique_lock<std::mutex> hold;
-  cudaEvent_t ev[3] = {nullptr, nullptr, nullptr};
-  cudaError_t e = cudaSuccess;
-  if (a.h0_row) {
-    e = side_streams(stream, side, hold);
-    for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = cudaEventCreateWithFlags(&ev[i], cudaEventDisableTiming);
-    if (e == cudaSuccess) e = cudaEventRecord(ev[2], stream);
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = cudaStreamWaitEvent(side[i], ev[2], 0);
-  }
-  if (e == cudaSuccess) e = launch(simt_bwd_narrow_kernel<float, false>, BQ_TILES, BQ_SMEM, a, side[0]);
-  if (e == cudaSuccess) e = launch(simt_bwd_narrow_kernel<float, true>, BQ_TILES, BQ_SMEM, a, side[1]);
+  SideFork<CudaSideApi> sides;
+  cudaError_t e = a.h0_row ? sides.fork(side_pool(), stream) : cudaSuccess;
+  if (e == cudaSuccess)
+    e = launch(simt_bwd_narrow_kernel<float, false>, BQ_TILES, BQ_SMEM, a, a.h0_row ? sides.side(0) : stream);
+  if (e == cudaSuccess)
+    e = launch(simt_bwd_narrow_kernel<float, true>, BQ_TILES, BQ_SMEM, a, a.h0_row ? sides.side(1) : stream);
   if (e == cudaSuccess) e = launch(simt_wide_kernel<float, true>, FWD_TILES, FWD_SMEM, a, stream);
-  if (a.h0_row) {
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-      e = cudaEventRecord(ev[i], side[i]);
-      if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, ev[i], 0);
-    }
-    for (int i = 0; i < 3; ++i)
-      if (ev[i]) cudaEventDestroy(ev[i]);
-  }
-  return e;
+  return sides.join(e);
 }
 
 }  // namespace gla
