@@ -20,6 +20,7 @@ class SidePool {
 
   // The current device's pair for a call on `stream`.  `hold` is held until the caller has forked, filled
   // and joined the streams: a capture that took them in between would swallow an eager call's launches.
+  // One lock per device: calls on different devices do not wait for one another.
   Error take(Stream stream, Stream (&out)[2], std::unique_lock<std::mutex>& hold) {
     int dev = 0;
     Error e = Api::device(dev);
@@ -28,7 +29,7 @@ class SidePool {
     unsigned long long mine = 0;
     if ((e = Api::capture_of(stream, mine)) != Api::kSuccess) return e;
     Device& d = devices_[dev];
-    hold = std::unique_lock<std::mutex>(mu_);
+    hold = std::unique_lock<std::mutex>(d.mu);
     for (const Pair& p : d.pairs) {
       bool fits = true;
       for (Stream s : p.s) {
@@ -55,9 +56,9 @@ class SidePool {
     Stream s[2];
   };
   struct Device {
+    std::mutex mu;
     std::vector<Pair> pairs;
   };
-  std::mutex mu_;
   Device devices_[kMaxDevices];
 };
 

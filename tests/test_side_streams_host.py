@@ -1,5 +1,6 @@
 """The backwards' side streams (csrc/gla_side.cuh) against a fake of the runtime's calls, on the CPU: whichever
-call fails, what was forked is joined; a pair inside another capture is left alone."""
+call fails, what was forked is joined; each device has a lock of its own; a pair inside another capture is
+left alone."""
 import os
 import subprocess
 
@@ -11,6 +12,8 @@ CSRC = os.path.join(ROOT, "linear_attention_recurrence_simple_gb300", "csrc")
 SOURCE = r"""
 #include <cstdio>
 #include <cstdlib>
+#include <chrono>
+#include <future>
 #include <map>
 #include <string>
 #include <vector>
@@ -101,6 +104,33 @@ static void joined_whatever_fails() {
   fail_at = -1;
 }
 
+static void a_lock_for_each_device() {
+  fail_at = -1;
+  gla::SidePool<Fake> pool;
+  long s[2];
+  std::unique_lock<std::mutex> hold;
+  current = 0;
+  CHECK(pool.take(5, s, hold) == 0);
+  auto other = [&](int dev) {
+    return std::async(std::launch::async, [&pool, dev] {
+      current = dev;
+      long t[2];
+      std::unique_lock<std::mutex> h;
+      return pool.take(6, t, h);
+    });
+  };
+  auto on1 = other(1);
+  CHECK(on1.wait_for(std::chrono::seconds(20)) == std::future_status::ready);
+  CHECK(on1.get() == 0);
+  auto on0 = other(0);
+  CHECK(on0.wait_for(std::chrono::milliseconds(200)) == std::future_status::timeout);
+  hold.unlock();
+  CHECK(on0.get() == 0);
+  current = 64;
+  CHECK(pool.take(5, s, hold) == Fake::kInvalidDevice);
+  current = 0;
+}
+
 static void captures() {
   fail_at = -1;
   gla::SidePool<Fake> pool;
@@ -128,6 +158,7 @@ static void captures() {
 int main(int, char** argv) {
   const std::string what = argv[1];
   if (what == "join") joined_whatever_fails();
+  if (what == "locks") a_lock_for_each_device();
   if (what == "captures") captures();
   std::printf("ok\n");
 }
@@ -143,7 +174,7 @@ def program(tmp_path_factory):
     return str(d / "side")
 
 
-@pytest.mark.parametrize("what", ["join", "captures"])
+@pytest.mark.parametrize("what", ["join", "locks", "captures"])
 def test_side_streams(program, what):
     r = subprocess.run([program, what], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout == "ok\n", r.stdout + r.stderr
