@@ -66,6 +66,7 @@
 #include <type_traits>
 
 #include "gla_common.cuh"
+#include "gla_once.cuh"
 #include "gla_side.cuh"
 #include "gla_tc.cuh"
 
@@ -1191,17 +1192,14 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+  static const EncodeTiledFn fn = [] {
     cudaDriverEntryPointQueryResult q;
     void* p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
+    const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                           cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess;
+    return found ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+  }();
   return fn;
 }
 
@@ -1259,18 +1257,17 @@ cudaError_t launch_scan(const void* X, const void* Y, const void* Z, const ScanP
   const long long state_rows = (long long)a.n_seq * a.H * DK;
   if (Cfg<MODE>::FWD && p.s_out && !make_state_map(&maps.s, p.s_out, state_rows))
     return cudaErrorInvalidValue;
-  static bool attr_set = false;
-  if (!attr_set) {
+  static OncePerDevice<CudaDeviceApi> once;
+  const cudaError_t ready = once([] {
     // The warpgroups' setmaxnreg split redistributes exactly the registers the CTA is launched
     // with; with any other compiled count an increase could wait forever, so refuse to launch.
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, tc_scan_kernel<MODE>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != C::REG_LAUNCH) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(tc_scan_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<MODE>::BYTES);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+    return cudaFuncSetAttribute(tc_scan_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<MODE>::BYTES);
+  });
+  if (ready != cudaSuccess) return ready;
   // A balanced launch needs all its CTAs resident at once (a CTA may wait for its predecessor's
   // flag), which a cooperative launch guarantees or refuses; refused, it runs plain instead.
   cudaLaunchConfig_t cfg;

@@ -24,6 +24,7 @@
 
 #include "gla_common.cuh"
 #include "gla_mx.cuh"
+#include "gla_once.cuh"
 
 namespace gla {
 namespace {
@@ -295,25 +296,20 @@ cudaError_t launch_decode_step_mxfp8(int dtype_f32, const void* q, const void* k
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const long long ctas = std::min(total, (long long)sms * MX_CTAS_PER_SM);
   using BF = __nv_bfloat16;
-  static bool attr_set[2] = {false, false};
-  cudaError_t e;
+  static OncePerDevice<CudaDeviceApi> once;
+  const cudaError_t e = once([] {
+    const cudaError_t f = cudaFuncSetAttribute(decode_step_mxfp8_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)MxSmem<float>::BYTES);
+    return f != cudaSuccess ? f
+                            : cudaFuncSetAttribute(decode_step_mxfp8_kernel<BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)MxSmem<BF>::BYTES);
+  });
+  if (e != cudaSuccess) return e;
   if (dtype_f32) {
-    if (!attr_set[1]) {
-      if ((e = cudaFuncSetAttribute(decode_step_mxfp8_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)MxSmem<float>::BYTES)) != cudaSuccess)
-        return e;
-      attr_set[1] = true;
-    }
     decode_step_mxfp8_kernel<float><<<(unsigned)ctas, MX_THREADS, MxSmem<float>::BYTES, stream>>>(
         (const float*)q, (const float*)k, (const float*)v, log_lambda, scale, codes, scales, slot, pool_rows,
         (float*)o, total, H, aug, err, wait_ns);
   } else {
-    if (!attr_set[0]) {
-      if ((e = cudaFuncSetAttribute(decode_step_mxfp8_kernel<BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)MxSmem<BF>::BYTES)) != cudaSuccess)
-        return e;
-      attr_set[0] = true;
-    }
     decode_step_mxfp8_kernel<BF><<<(unsigned)ctas, MX_THREADS, MxSmem<BF>::BYTES, stream>>>(
         (const BF*)q, (const BF*)k, (const BF*)v, log_lambda, scale, codes, scales, slot, pool_rows, (BF*)o,
         total, H, aug, err, wait_ns);

@@ -6,9 +6,9 @@
 // has, written out, S = lambda^L S_p + sum_j lambda^(L-1-j) k_j v_j^T: the tail holds the (k_j, v_j),
 // the fold evaluates the sum.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
+#include "gla_once.cuh"
 #include "gla_tail.cuh"
 #include "gla_tc.cuh"
 
@@ -492,16 +492,10 @@ template <bool MX>
 cudaError_t launch_fold_tc(const float* log_lambda, const float* pool, int pool_rows, const int32_t* prefix_row,
                            const TailArgs& t, float* out, int out_rows, const int32_t* out_row, unsigned blocks, int H,
                            unsigned* err, unsigned long long wait_ns, cudaStream_t s) {
-  static std::atomic<bool> allowed[64];  // per device: the kernel's shared memory
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static OncePerDevice<CudaDeviceApi> once;
+  const cudaError_t e = once(
+      [] { return cudaFuncSetAttribute(tail_fold_tc_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FT_SMEM); });
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !allowed[dev].load()) {
-    if ((e = cudaFuncSetAttribute(tail_fold_tc_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FT_SMEM)) !=
-        cudaSuccess)
-      return e;
-    if (dev < 64) allowed[dev].store(true);
-  }
   tail_fold_tc_kernel<MX><<<blocks, FT_THREADS, FT_SMEM, s>>>(log_lambda, pool, pool_rows, prefix_row, t, out, out_rows,
                                                               out_row, H, err, wait_ns);
   return cudaGetLastError();
