@@ -442,6 +442,13 @@ int gla_debug_bounds(void);
  * tensor memory and returns.  Meant for tests of that path; applies to the current device. */
 int gla_set_wait_limit_ns(unsigned long long ns);
 
+/* For tests of that path, debug-bounds build only (GLA_ERR_UNSUPPORTED in the release build): from now on one
+ * warp of every CTA of gla_prefix_decode_step's bf16 kernel (its second) and of gla_tail_fold's bf16 and MXFP8
+ * kernel gives up its wait for chunk `chunk` (of its own, from 0; below 4,096) as if the limit had passed.  role:
+ * the decode's wait for keys (0) or values (1); the fold's issuing (0), widening (1; from chunk 2 on) or, for the
+ * last chunk, storing warps (2).  role -1: no more. */
+int gla_debug_give_up(int role, int chunk);
+
 /* Human-readable name of a gla_status value. */
 const char* gla_status_string(int status);
 

@@ -23,7 +23,7 @@ __all__ = [
     "gla_chunk_fwd",
     "gla_chunk_bwd", "gla_decode_step", "gla_chunk_fwd_noalloc", "gla_head_norm_gate", "gla_chunk_fwd_split",
     "gla_split_choose_seg_chunks", "gla_get_device_error",
-    "gla_set_wait_limit_ns", "gla_debug_bounds", "debug_bounds_library", "gla_chunk_fwd_host",
+    "gla_set_wait_limit_ns", "gla_debug_bounds", "gla_debug_give_up", "debug_bounds_library", "gla_chunk_fwd_host",
     "gla_chunk_fwd_host_workspace_bytes", "GlaTail", "gla_tail_alloc", "gla_tail_append", "gla_tail_read",
     "gla_tail_fold", "gla_prefix_decode_step", "gla_prefix_fwd", "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes",
     "gla_status_string", "DK", "DV", "CHUNK", "EXPORTS",
@@ -39,7 +39,7 @@ EXPORTS = ("gla_workspace_bytes", "gla_bwd_workspace_bytes", "gla_chunk_fwd", "g
            "gla_split_choose_seg_chunks", "gla_chunk_fwd_noalloc", "gla_get_device_error", "gla_set_wait_limit_ns",
            "gla_debug_bounds", "gla_chunk_fwd_host", "gla_chunk_fwd_host_workspace_bytes", "gla_status_string",
            "gla_prefix_decode_step", "gla_tail_append", "gla_tail_read", "gla_tail_fold", "gla_prefix_fwd",
-           "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes")
+           "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes", "gla_debug_give_up")
 NOALLOC_MAX_SEQS = 16384
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -121,6 +121,8 @@ def load_library(build: bool = True, debug: bool | None = None):
         lib.gla_status_string.restype = ctypes.c_char_p
         lib.gla_debug_bounds.argtypes = []
         lib.gla_debug_bounds.restype = I
+        lib.gla_debug_give_up.argtypes = [I, I]
+        lib.gla_debug_give_up.restype = I
         lib.gla_chunk_fwd_host_workspace_bytes.argtypes = [I, I, I, I]
         lib.gla_chunk_fwd_host_workspace_bytes.restype = Z
         lib.gla_chunk_fwd_host.argtypes = [P, P, P, P, P, F, P, P, I, I, I, I, I, I, I, P, Z, P]
@@ -160,6 +162,12 @@ def debug_bounds_library():
 def gla_debug_bounds() -> int:
     """1 when calls go to the debug-bounds build, 0 for the release build."""
     return int(load_library().gla_debug_bounds())
+
+
+def gla_debug_give_up(role: int, chunk: int = 0) -> None:
+    """Makes one warp of the tails' decode and fold kernels give up its wait for ``chunk`` (debug-bounds build
+    only, for tests of the bounded waits; ``role`` -1: no more)."""
+    _check(load_library().gla_debug_give_up(int(role), int(chunk)), "gla_debug_give_up")
 
 
 def gla_status_string(status: int) -> str:

@@ -1,5 +1,6 @@
 // C ABI of libgla.so: argument validation, kernel choice, launches on the caller's stream, and
 // the per-device sticky error word.  Nothing here allocates device memory.
+#include <atomic>
 #include <mutex>
 
 #include "gla.h"
@@ -126,6 +127,13 @@ int check_chunk_sizes(int n_seq, int T, int H, int dk, int dv, int dtype, const 
 }
 // Internal accessors for the allocation-free entry point (gla_noalloc.cu); the entry points
 // above do not go through them.
+#ifdef GLA_DEBUG_BOUNDS
+static std::atomic<unsigned long long> g_give_up{0};
+unsigned long long debug_give_up() { return g_give_up; }
+#else
+unsigned long long debug_give_up() { return 0; }
+#endif
+
 int current_device_state(unsigned** err, unsigned long long* wait_ns) {
   int dev;
   return device_state(&dev, err, wait_ns);
@@ -448,6 +456,17 @@ int gla_set_wait_limit_ns(unsigned long long ns) {
 }
 
 int gla_debug_bounds(void) { return gla::kDebugBounds ? 1 : 0; }
+
+int gla_debug_give_up(int role, int chunk) {
+#ifdef GLA_DEBUG_BOUNDS
+  if (role < -1 || role > 2 || (role >= 0 && (chunk < 0 || chunk >= 1 << 12))) return GLA_ERR_SHAPE;
+  gla::g_give_up = role < 0 ? 0 : gla::give_up_code(role, chunk);
+  return GLA_OK;
+#else
+  (void)role, (void)chunk;
+  return GLA_ERR_UNSUPPORTED;
+#endif
+}
 
 const char* gla_status_string(int status) {
   switch (status) {

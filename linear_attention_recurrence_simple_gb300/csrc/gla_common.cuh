@@ -197,6 +197,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   return true;
 }
 
+// A wait that the debug-bounds build can be told to give up (gla_debug_give_up: a role of the kernel and a
+// chunk of that role's, kept above a limit of 2^48 ns); otherwise, and in the release build, mbar_wait.
+#ifdef GLA_DEBUG_BOUNDS
+constexpr unsigned long long GIVE_UP_BIT = 1ull << 63;
+__host__ __device__ constexpr unsigned long long give_up_code(int role, int chunk) {
+  return GIVE_UP_BIT | (unsigned long long)role << 60 | (unsigned long long)chunk << 48;
+}
+__device__ __forceinline__ bool mbar_wait_at(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, volatile int* abort,
+                                             int role, int chunk) {
+  const unsigned long long limit = limit_ns & ((1ull << 48) - 1);
+  if (chunk >= 0 && chunk < 1 << 12 && limit_ns - limit == give_up_code(role, chunk)) {
+    *abort = 1;
+    return false;
+  }
+  return mbar_wait(bar, parity, limit, abort);
+}
+#else
+__device__ __forceinline__ bool mbar_wait_at(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, volatile int* abort,
+                                             int, int) {
+  return mbar_wait(bar, parity, limit_ns, abort);
+}
+#endif
+// What the host adds to a limit for it: 0, but in the debug-bounds build after gla_debug_give_up.
+unsigned long long debug_give_up();
+
 // Bounded wait on the exit path (no abort flag): raises ERR_TIMEOUT itself.
 __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity, unsigned long long limit_ns,
                                                 unsigned* err) {

@@ -639,7 +639,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     for (; c < last; ++c) {
       const uint32_t phase = (uint32_t)(c - c0) & 1u;
       const int j0 = (c - first) * ST::TOK, m = min(ST::TOK, L - j0);
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[0], phase, wait_ns, &s_abort));
+      ok = __all_sync(0xffffffffu, mbar_wait_at(&full[0], phase, wait_ns, &s_abort, 0, warp == 1 ? c - c0 : -1));
       if (!ok) break;
       // weights: token 16 u + g in lanes tq = 0, sc[u][0]; token 16 u + g + 8, sc[u][1]
       float sc[ST::SUB][2];
@@ -697,7 +697,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
 #pragma unroll
         for (int i = 0; i < 4; ++i) wt[u][i] = __shfl_sync(0xffffffffu, w, 16 * u + tq + 4 * i);
 
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[1], phase, wait_ns, &s_abort));
+      ok = __all_sync(0xffffffffu, mbar_wait_at(&full[1], phase, wait_ns, &s_abort, 1, warp == 1 ? c - c0 : -1));
       if (!ok) break;
       if (m < ST::TOK) {
         // rows past the tail's end hold another chunk's values or nothing: zero, so that their
@@ -988,6 +988,7 @@ int gla_prefix_decode_step(const void* q, const void* k, const void* v, const fl
   unsigned* err;
   unsigned long long wait_ns;
   if ((rc = gla::current_device_state(&err, &wait_ns))) return rc;
+  wait_ns |= gla::debug_give_up();
   t.slot = tail_slot;
   t.len = tail_len;
   const bool mx = tail->format == GLA_TAIL_MXFP8;

@@ -408,7 +408,7 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
       const uint32_t which = (uint32_t)(warp - FT_WIDEN / 32);
       constexpr uint32_t ID = idesc_bf16(128, DK, 1, 1);
       for (int c = 0; c < chunks; ++c) {
-        if (!mbar_wait(&s_full[c & 1], (uint32_t)(c >> 1) & 1u, wait_ns, &s_abort)) break;
+        if (!mbar_wait_at(&s_full[c & 1], (uint32_t)(c >> 1) & 1u, wait_ns, &s_abort, 0, which == 0 ? c : -1)) break;
         tc_fence_after();
         const uint32_t buf = base + (uint32_t)(c & 1) * FT_BUF;
         const SDesc a = sdesc(buf + FT_V + which * 2u * FT_PANEL, FT_PANEL, 1024, LAYOUT_SW128);
@@ -426,7 +426,8 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
   } else {
     auto step = [&](auto set_t, int c) {
       constexpr int b = decltype(set_t)::value;
-      if (c >= 2 && !__all_sync(0xffffffffu, mbar_wait(&s_empty[b], (uint32_t)((c >> 1) - 1) & 1u, wait_ns, &s_abort)))
+      if (c >= 2 && !__all_sync(0xffffffffu, mbar_wait_at(&s_empty[b], (uint32_t)((c >> 1) - 1) & 1u, wait_ns, &s_abort, 1,
+                                                          warp == 2 ? c : -1)))
         return false;
       store(set_t, c);
       if (c + 2 < chunks) load(set_t, c + 2);
@@ -449,7 +450,8 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
 #pragma unroll
     for (int i = 0; i < 32; ++i) s[i] = S[i * DV];
     if (chunks > 0 && ok)
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_empty[(chunks - 1) & 1], (uint32_t)((chunks - 1) >> 1) & 1u, wait_ns, &s_abort));
+      ok = __all_sync(0xffffffffu, mbar_wait_at(&s_empty[(chunks - 1) & 1], (uint32_t)((chunks - 1) >> 1) & 1u, wait_ns,
+                                                &s_abort, 2, warp == 5 ? chunks - 1 : -1));
     if (ok) {
       tc_fence_after();
       const float lamL = decay_pow(ll, L);
@@ -571,6 +573,7 @@ int gla_tail_fold(const float* log_lambda, const float* pool, int pool_rows, con
   unsigned* err;
   unsigned long long wait_ns;
   if ((rc = gla::current_device_state(&err, &wait_ns))) return rc;
+  wait_ns |= gla::debug_give_up();
   t.slot = tail_slot;
   t.len = tail_len;
   const unsigned blocks = (unsigned)N * (unsigned)H;
