@@ -102,6 +102,9 @@ prefix_decode_kernel(const float* __restrict__ q, const float* __restrict__ k, c
       raise_error(err, ERR_SHAPE);
       row = -1;
     }
+    if (row >= 0 && tok0 >= 0 && !(tail_in_bounds(t, H, tok0, L + 1, err) && state_in_bounds(row, pool_rows, h, H, err) &&
+                                   GLA_IN_BOUNDS(n0 + tid < N, err)))
+      row = -1;
     s_row[tid] = tok0 < 0 ? -1 : row;  // -1: the sequence is skipped
     s_len[tid] = L;
     s_tok0[tid] = tok0;
@@ -411,6 +414,9 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
         row = -1;
       }
       if (tok0 < 0) row = -1;  // row -1: the sequence is skipped
+      if (row >= 0 && !(tail_in_bounds(t, H, tok0, L + 1, err) && state_in_bounds(row, pool_rows, h, H, err) &&
+                        GLA_IN_BOUNDS(n0 + lane < N, err)))
+        row = -1;
     }
     int chunks = row >= 0 ? (L + ST::TOK - 1) / ST::TOK : 0;
     if (lane < TILE_MAX) {
@@ -457,11 +463,14 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     next_tok = s_tok0[next_seq] + j0;
     ++next;
     ++loads_k;
+    // (what the scales' last 16 bytes hold besides lies in the same row: cap is a multiple of 16)
+    const bool in = tail_in_bounds(t, H, next_tok, next_m, err) && GLA_IN_BOUNDS(next_m > 0, err);
+    if (!in) next_m = 0;
     const uint32_t bytes = (uint32_t)next_m * ST::K_ROW, ks = MX ? (uint32_t)(3 * next_m + 15) / 16 * 16 : 0;
     if (lane == 0) {
       mbar_expect_tx(&full[0], bytes + ks);
-      bulk_copy(st32 + ST::K, static_cast<const uint8_t*>(t.k) + next_tok * ST::K_ROW, bytes, &full[0]);
-      if (MX) bulk_copy(st32 + ST::KS, t.ks + next_tok * (DK / 32), ks, &full[0]);
+      if (in) bulk_copy(st32 + ST::K, static_cast<const uint8_t*>(t.k) + next_tok * ST::K_ROW, bytes, &full[0]);
+      if (MX && in) bulk_copy(st32 + ST::KS, t.ks + next_tok * (DK / 32), ks, &full[0]);
     }
   };
   auto load_values = [&]() {  // of the chunk whose keys were loaded last
@@ -469,8 +478,9 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
     const uint32_t bytes = (uint32_t)next_m * ST::V_ROW, vs = MX ? (uint32_t)(6 * next_m + 15) / 16 * 16 : 0;
     if (lane == 0) {
       mbar_expect_tx(&full[1], bytes + vs);
-      bulk_copy(st32 + ST::V, static_cast<const uint8_t*>(t.v) + next_tok * ST::V_ROW, bytes, &full[1]);
-      if (MX) bulk_copy(st32 + ST::VS, t.vs + next_tok * (DV / 32), vs, &full[1]);
+      const bool in = GLA_IN_BOUNDS(next_m > 0, err);
+      if (in) bulk_copy(st32 + ST::V, static_cast<const uint8_t*>(t.v) + next_tok * ST::V_ROW, bytes, &full[1]);
+      if (MX && in) bulk_copy(st32 + ST::VS, t.vs + next_tok * (DV / 32), vs, &full[1]);
     }
   };
   auto release = [&](int m) {  // a chunk's values are read (the zeros behind its m tokens were written through the generic proxy)
@@ -857,7 +867,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
 #pragma unroll
   for (int u = 0; u < 3; ++u) {
     const int e = tid + u * PD_THREADS, i = e / (DV / 8), c = 8 * (e % (DV / 8));
-    if (e >= cnt * (DV / 8) || s_row[i] < 0) continue;
+    if (e >= cnt * (DV / 8) || s_row[i] < 0 || !GLA_IN_BOUNDS(n0 + i < N && h < H, err)) continue;
     const float g8 = s_self[i];
     const float4 x = *reinterpret_cast<const float4*>(sO + i * DV + c), y = *reinterpret_cast<const float4*>(sO + i * DV + c + 4);
     const uint32_t w[4] = {ov[u].x, ov[u].y, ov[u].z, ov[u].w};
@@ -924,7 +934,7 @@ constexpr int RED_CTAS = STATE4 / RED_THREADS;  // 18 per (row, head)
 
 __global__ void __launch_bounds__(RED_THREADS)
 prefix_grad_kernel(const float4* __restrict__ dh0, const int32_t* __restrict__ prefix_row, int n_seq, int H,
-                   float4* __restrict__ dpool) {
+                   float4* __restrict__ dpool, int pool_rows, [[maybe_unused]] unsigned* err) {
   __shared__ int s_n[RED_THREADS];
   __shared__ int s_warp[RED_THREADS / 32];
   const int part = (int)(blockIdx.x % RED_CTAS);
@@ -949,6 +959,7 @@ prefix_grad_kernel(const float4* __restrict__ dh0, const int32_t* __restrict__ p
     __syncthreads();
 #pragma unroll 4
     for (int i = 0; i < count; ++i) {
+      if (!state_in_bounds(s_n[i], n_seq, h, H, err)) continue;
       const float4 g = dh0[((long long)s_n[i] * H + h) * STATE4 + e];
       s.x += g.x;
       s.y += g.y;
@@ -957,7 +968,7 @@ prefix_grad_kernel(const float4* __restrict__ dh0, const int32_t* __restrict__ p
     }
     __syncthreads();
   }
-  dpool[((long long)p * H + h) * STATE4 + e] = s;
+  if (state_in_bounds(p, pool_rows, h, H, err)) dpool[((long long)p * H + h) * STATE4 + e] = s;
 }
 
 bool aligned(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -1118,7 +1129,7 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
   }
   if (reduce) {
     gla::prefix_grad_kernel<<<(unsigned)pool_rows * (unsigned)H * gla::RED_CTAS, gla::RED_THREADS, 0, s>>>(
-        (const float4*)dh0, prefix_row, n_seq, H, (float4*)dpool);
+        (const float4*)dh0, prefix_row, n_seq, H, (float4*)dpool, pool_rows, a.err);
     return gla::to_status(cudaGetLastError());
   }
   return GLA_OK;

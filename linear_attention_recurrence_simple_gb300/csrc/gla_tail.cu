@@ -101,7 +101,9 @@ tail_copy_kernel(T* __restrict__ k, T* __restrict__ v, TailArgs t, const int32_t
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int r = tid / TOKEN_PIECES + i * (COPY_THREADS / TOKEN_PIECES);
-    const long long at = s_token[r], row = (long long)(t0 + r) * H + h;
+    const long long row = (long long)(t0 + r) * H + h;
+    long long at = s_token[r];
+    if (at >= 0 && !(tail_in_bounds(t, H, at, 1, err) && GLA_IN_BOUNDS(row < (long long)T_total * H, err))) at = -1;
 #pragma unroll
     for (int w = 0; w < WORDS; ++w) raw[i][w] = make_uint4(0u, 0u, 0u, 0u);
     sc[i] = 0;
@@ -116,7 +118,9 @@ tail_copy_kernel(T* __restrict__ k, T* __restrict__ v, TailArgs t, const int32_t
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int r = tid / TOKEN_PIECES + i * (COPY_THREADS / TOKEN_PIECES);
-    const long long at = s_token[r], row = (long long)(t0 + r) * H + h;
+    const long long row = (long long)(t0 + r) * H + h;
+    long long at = s_token[r];
+    if (at >= 0 && !(tail_in_bounds(t, H, at, 1, err) && GLA_IN_BOUNDS(row < (long long)T_total * H, err))) at = -1;
     if constexpr (WRITE && MX) {
       float x[16];
       load16(reinterpret_cast<const T*>(raw[i]), x);
@@ -177,6 +181,9 @@ tail_fold_kernel(const float* __restrict__ log_lambda, const float* pool, int po
     return;
   }
   if (tok0 < 0) return;
+  if (!(tail_in_bounds(t, H, tok0, L, err) && state_in_bounds(src, pool_rows, h, H, err) &&
+        state_in_bounds(dst, out_rows, h, H, err)))
+    return;
   const float ll = log_lambda[h];
   uint64_t acc[6][6];  // pairs of columns, through the packed two-lane FMA
 #pragma unroll
@@ -288,6 +295,9 @@ tail_fold_tc_kernel(const float* __restrict__ log_lambda, const float* pool, int
     return;
   }
   if (tok0 < 0) return;
+  if (!(tail_in_bounds(t, H, tok0, L, err) && state_in_bounds(src, pool_rows, h, H, err) &&
+        state_in_bounds(dst, out_rows, h, H, err)))
+    return;
   const float ll = log_lambda[h];
   const int chunks = (L + FT_TOK - 1) / FT_TOK;
 

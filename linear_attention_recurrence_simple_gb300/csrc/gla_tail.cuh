@@ -38,6 +38,20 @@ __device__ __forceinline__ long long tail_token0(const TailArgs& t, int n, int H
   return ((long long)row * H + h) * t.cap;
 }
 
+// Debug-bounds build: a piece of `count` tokens from token index `at` lies inside the tail arrays, a (row, head) inside
+// a pool (always true in the release build).
+__device__ __forceinline__ bool tail_in_bounds([[maybe_unused]] const TailArgs& t, [[maybe_unused]] int H,
+                                               [[maybe_unused]] long long at, [[maybe_unused]] int count,
+                                               [[maybe_unused]] unsigned* err) {
+  return GLA_IN_BOUNDS(at >= 0 && count >= 0 && at + count <= (long long)t.rows * H * t.cap &&
+                           (count == 0 || at / t.cap == (at + count - 1) / t.cap),
+                       err);
+}
+__device__ __forceinline__ bool state_in_bounds([[maybe_unused]] int row, [[maybe_unused]] int rows, [[maybe_unused]] int h,
+                                                [[maybe_unused]] int H, [[maybe_unused]] unsigned* err) {
+  return GLA_IN_BOUNDS(row >= 0 && row < rows && h >= 0 && h < H, err);
+}
+
 template <class T>
 __device__ __forceinline__ void store16(T* p, const float (&x)[16]);
 template <>
