@@ -624,7 +624,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int e2 = max(exponent_of(m), -100) - 10;  // the largest comes to [2^10, 2^11)
-        wide_q = e2 > 50 || e2 < -50 || __any_sync(0xffffffffu, low < __float_as_uint(pow2i(e2 - 17)) - 1u);
+        wide_q = (m > 0.f && (e2 > 50 || e2 < -50)) || __any_sync(0xffffffffu, low < __float_as_uint(pow2i(e2 - 17)) - 1u);
         const float inv = pow2i(-e2);
         qn = pow2i(e2);
 #pragma unroll

@@ -183,3 +183,13 @@ def test_a_query_element_far_above_the_rest_over_keys_without_it(ratio, bf16):
     for x in "qk":
         c.g[x] = torch.from_numpy(getattr(c, x)).cuda().to(c.dt)
     check_columns(c, c.decode())
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_queries_of_zeros(bf16):
+    c = Case(970, [40, 100, 7], 2, [0, 1, 1], 2, bf16, "mxfp8")
+    c.q[:2] = 0.0
+    c.g["q"][:2] = 0.0
+    o = c.decode()
+    assert bool((o[:2] == 0).all())
+    check_columns(c, o)
