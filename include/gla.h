@@ -380,7 +380,8 @@ int gla_prefix_decode_step(const void* q, const void* k, const void* v, const fl
  *   pos          [n_seq] int32 device: sequence n's tokens go to (come from) places pos[n],
  *                pos[n] + 1, ... of its tail (for an append, usually tail_len).
  *   cu_seqlens   [n_seq + 1] int32 device packed offsets, as in gla_chunk_fwd; rows from
- *                cu_seqlens[n_seq] on are left alone.  T <= 2^31 - 64.
+ *                cu_seqlens[n_seq] on are left alone; offsets that decrease record GLA_ERR_SHAPE.  The row
+ *                and places of a sequence without tokens are not looked at.  T <= 2^31 - 64.
  * An MXFP8 tail is quantised as it is written and widened as it is read: exactly, where dtype holds
  * the value (always, but for values of bf16's or fp32's subnormal range). */
 int gla_tail_append(const void* k, const void* v, const gla_tail* tail, const int32_t* tail_slot, const int32_t* pos,

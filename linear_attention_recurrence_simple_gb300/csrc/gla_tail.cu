@@ -63,6 +63,9 @@ tail_copy_kernel(T* __restrict__ k, T* __restrict__ v, TailArgs t, const int32_t
     offsets = s_cu;
     __syncthreads();
   }
+  if (blockIdx.x == 0)  // offsets that decrease, wherever the searches below may lead
+    for (int i = tid; i < n_seq; i += COPY_THREADS)
+      if (offsets[i] > offsets[i + 1]) raise_error(err, ERR_SHAPE);
   if (tid < COPY_TOK) {
     // the sequence n with offsets[n] <= tok < offsets[n + 1]: the last n with offsets[n] <= tok
     const int tok = t0 + tid;
@@ -80,7 +83,7 @@ tail_copy_kernel(T* __restrict__ k, T* __restrict__ v, TailArgs t, const int32_t
         const long long base = tail_token0(t, lo, H, h, e - b, first, err);
         if (base >= 0) at = base + first + (tok - b);
       } else if (tok < offsets[n_seq] || b > tok) {
-        raise_error(err, ERR_SHAPE);  // offsets that decrease, start past 0 or pass the total
+        raise_error(err, ERR_SHAPE);  // offsets that start past 0 or pass the total
       }
     }
     s_token[tid] = at;
