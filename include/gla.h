@@ -349,6 +349,10 @@ int gla_chunk_fwd_host(const void* q, const void* k, const void* v, const float*
  *   tail_len     [n] int32 device: tokens in each tail, at places 0 .. tail_len - 1.  The calls
  *                read it and never change it: the caller advances it after a decode step.  Places
  *                from tail_len on may hold anything, NaN included.
+ * In the decode step and the fold an infinity or a NaN in a state, a tail or a token stays with the outputs that it
+ * enters.  Where operands are held as sums of several bf16 (bf16 calls, folds of bf16 and MXFP8 tails) an infinity may
+ * come out as a NaN.
+ * The self-augmentation step (gla_chunk_fwd_aug, gla_decode_step_aug) has no form among these calls.
  * A sequence whose row, slot, length or places lie outside the pool or its tail is skipped (its
  * outputs and its tail are left as they were) and records GLA_ERR_SHAPE in the device error word.
  * Each call returns once its work is queued on `stream`, may be captured into a graph (after a first
@@ -368,8 +372,12 @@ typedef struct gla_tail {
  * v are written to place L of the tail (quantised where it is MXFP8), which needs L < cap.
  * bf16 calls: sums in fp32; states, and the weights lambda^(L-j) (q . k_j), with 16 bits or more each, however far
  * apart the elements of a tail, its weights or its blocks lie; o rounded once.  fp32 calls: fp32 throughout.
- *   q, k [N, H, 96]; v, o [N, H, 192]; dtype `dtype`; N * H below 2^31.  One launch.  For L beyond about 256 (bf16)
- *   or 500 (MXFP8) tokens a state of its own (gla_tail_fold, then gla_decode_step) is less to read. */
+ *   q, k [N, H, 96]; v, o [N, H, 192]; dtype `dtype`; N * H below 2^31.  One launch.
+ * Tokens L from which a step over a state of its own (gla_tail_fold, then a decode step) moves fewer bytes:
+ *     tail      fp32 pool   bf16 pool   MXFP8 pool
+ *     bf16         256         128          66
+ *     MXFP8        496         248         128
+ * A tail's token is rounded once (MXFP8) or not at all; a bf16 or MXFP8 pool rounds the whole state at every step. */
 int gla_prefix_decode_step(const void* q, const void* k, const void* v, const float* log_lambda, float scale,
                            const float* pool, int pool_rows, const int32_t* prefix_row, const gla_tail* tail,
                            const int32_t* tail_slot, const int32_t* tail_len, void* o, int N, int H, int dk, int dv,
@@ -406,8 +414,9 @@ int gla_tail_fold(const float* log_lambda, const float* pool, int pool_rows, con
 /* gla_chunk_fwd and gla_chunk_bwd on packed sequences that continue shared states: sequence n's
  * initial state is pool[prefix_row[n]], read where it stands (no copies).  cu_seqlens is required;
  * every other argument as there.  A prefix_row outside the pool starts that sequence from zeros and
- * records GLA_ERR_SHAPE.  (bf16: as there, a sequence's last chunk reads on into the next sequence with
- * zero weights, so an infinity or a NaN in the first 127 tokens of one can reach the one before.)
+ * records GLA_ERR_SHAPE.  (bf16: as there, hT and dpool come from 16 bits of each operand, 2-3e-6 of the norm, and a
+ * sequence's last chunk reads on into the next sequence with zero weights, so an infinity or a NaN in the first
+ * 127 tokens of one can reach the one before.)
  *   dpool        [pool_rows, H, 96, 192] fp32 output, or NULL to skip: the pool's gradient, row p
  *                the sum of dh0 over the sequences that continue p, added in their order; zeros for
  *                a row that none continues.

@@ -35,8 +35,9 @@ namespace {
 // before the keys are waited for, into 16 sums of its own; the 16 threads of a piece meet once per
 // sequence.  A block's scale multiplies the piece's sum (keys) or the weight (values), once for 16 codes; where
 // scale, query or weight is so large that this could pass fp32's range, or that code x scale is an infinity, it
-// multiplies the codes.  MXFP8 tails are bound by the widening and the FMAs, fp32 ones by HBM: 1,000 x 16 heads, 143
-// tokens on average, 265 us (MXFP8) and 492 us (fp32, 0.81 of the measured copy bandwidth).
+// multiplies the codes.  fp32 tails are bound by HBM, MXFP8 ones by the latency of a chunk's loads, which go out
+// once the chunk before is used (issue slots 52 % busy, HBM at 35 %): 1,000 x 16 heads, 143 tokens on average, 497 us
+// (fp32, 0.81 of the measured copy bandwidth) and 273 us (MXFP8).
 constexpr int DEC_THREADS = DV;
 constexpr int DEC_TOK = 32;
 constexpr int DEC_TILE = 4;
@@ -227,9 +228,11 @@ prefix_decode_kernel(const float* __restrict__ q, const float* __restrict__ k, c
 //     The warp that has a sequence's first chunk adds to the tile's sums directly; the others that share it
 //     keep their parts, which meet in warp order.
 // mma.sync rather than tcgen05: a sequence brings one query row, so a 128-row tile would stand empty, and
-// the codes are widened in registers either way.  Bound by instruction issue (about 820 warp
-// instructions per 32 MXFP8 tokens) beside HBM: 1,280 x 16 heads, 143 tokens on average, MXFP8, 187 us (0.73
-// of the measured copy bandwidth on its 921 MB); 333 x 7, 146 tokens, bf16, 49 us (0.61).
+// the codes are widened in registers either way.  Bound by latency: 16 warps per SM (accumulators and stages
+// leave no room for more) hide that of about 870 warp instructions per 32 MXFP8 tokens only in part, with the
+// issue slots half busy and HBM at 56 %: 1,280 x 16 heads, 143 tokens on average, MXFP8, 195 us (0.70 of the
+// measured copy bandwidth on its 921 MB; rows in no order, so that a tile reads a state for every sequence:
+// 355 us); 333 x 7, 146 tokens, bf16, 49 us (0.62).
 constexpr int TILE_MAX = 16;
 constexpr int PD_WARPS = 4, PD_THREADS = 32 * PD_WARPS;
 
@@ -453,7 +456,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
   const int c0 = (int)(total * warp / PD_WARPS), c1 = (int)(total * (warp + 1) / PD_WARPS);
   uint8_t* const st = pd_smem + (size_t)warp * ST::BYTES;
   const uint32_t st32 = smem_u32(st);
-  // The next chunk to load (whole warp): lane 0 copies the elements or codes, lane 1 the scales.
+  // The next chunk to load (whole warp; lane 0 issues the copies).
   int next = c0, next_seq = 0, next_m = 0, loads_k = 0, loads_v = 0;
   long long next_tok = 0;
   auto load_keys = [&]() {

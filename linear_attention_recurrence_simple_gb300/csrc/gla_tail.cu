@@ -169,8 +169,9 @@ cudaError_t launch_copy(int f32, bool mx, void* k, void* v, const TailArgs& t, c
 // ---- the fold --------------------------------------------------------------------------------
 // fp32 tails.  One CTA per (sequence, head): the 96 x 192 sum in registers (a thread holds 6 rows x 12
 // columns), tokens staged FOLD_TOK at a time in shared memory as fp32, keys already weighted by lambda^(L-1-j).
-// Bound by the FMA rate and its operands from a few dozen tokens on (200 x 16 tails of 143 tokens: 0.54 ms, 42 %
-// of the FMA peak; 288 threads with 64 sums each and the next tokens' loads ahead: 0.65 ms).
+// Bound by latency: 16 warps per SM (125 registers) wait for a chunk's loads and for its two barriers, with
+// the issue slots 37 % busy (200 x 16 tails of 143 tokens: 0.53 ms, 42 % of the FMA peak; 288 threads with 64 sums
+// each and the next tokens' loads ahead: 0.65 ms).
 constexpr int FOLD_THREADS = 256, FOLD_TOK = 16;
 
 __global__ void __launch_bounds__(FOLD_THREADS)
@@ -267,7 +268,7 @@ tail_fold_kernel(const float* __restrict__ log_lambda, const float* pool, int po
 // split them, and store them swizzled; two buffers, handed to two issuing warps and back through
 // mbarriers.  Floor: 73.7 KB written per (sequence, head) and the tail read once; bound by the latency of a
 // chunk's chain, which two CTAs per SM (tensor memory allows no more) overlap in part: 256 x 16, 225 tokens
-// on average, bf16, 180 us (0.69 of the floor).
+// on average, 180 us for bf16 (0.69 of the floor) and 190 us for MXFP8 (0.45: half the bytes, the same chain).
 constexpr int FT_WIDEN = 192, FT_THREADS = 256, FT_TOK = 32;  // warps 0 .. 5 widen and store, 6 and 7 issue
 constexpr uint32_t FT_PANEL = FT_TOK * 128;                       // 32 tokens x 64 columns of bf16
 constexpr uint32_t FT_V = 0, FT_K = 3 * FT_PANEL, FT_TERM = 2 * FT_PANEL, FT_BUF = FT_K + 3 * FT_TERM;
