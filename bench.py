@@ -32,9 +32,9 @@ DK, DV, H = 96, 192, 16
 # profiles/, per unit of work; reported only while the kernel source is byte-identical to the one
 # profiled (SHA-256 prefix), else null.
 PROFILED_TRAFFIC = {
-    # B=8 T=2048 H=16 forward: 246.167808 MB read + 81.687040 MB written, one launch
-    "fwd": ("linear_attention_recurrence_simple_gb300/csrc/gla_chunk_tc.cu", "d4bc6aaecf6d3ac8",
-            327854848.0, "per launch of the B=8 T=2048 H=16 forward"),
+    # B=8 T=2048 H=16 forward: 246.310144 MB read + 81.754112 MB written, one launch
+    "fwd": ("linear_attention_recurrence_simple_gb300/csrc/gla_chunk_tc.cu", "4a7696894bc76ba6",
+            328064256.0, "per launch of the B=8 T=2048 H=16 forward"),
     # 49,152-state pool: 3.662106 GB read + 3.583718 GB written; traffic scales with the pool
     "decode": ("linear_attention_recurrence_simple_gb300/csrc/gla_decode.cu", "a4a26403a2ad2cf8",
                7245823744.0 / 49152, "per state per step"),
@@ -44,24 +44,24 @@ PROFILED_TRAFFIC = {
     # the fused norm-gate step on the fp32 pool: 3.680801 GB read + 3.583189 GB written
     "decode_norm_gate": ("linear_attention_recurrence_simple_gb300/csrc/gla_decode.cu", "a4a26403a2ad2cf8",
                          7263989504.0 / 49152, "per state per step"),
-    # the same forward with the self-augmentation step: 245.779968 MB read + 82.790656 MB written
-    "fwd_aug": ("linear_attention_recurrence_simple_gb300/csrc/gla_chunk_tc.cu", "d4bc6aaecf6d3ac8",
-                328570624.0, "per launch of the B=8 T=2048 H=16 augmented forward"),
+    # the same forward with the self-augmentation step: 245.720832 MB read + 82.703360 MB written
+    "fwd_aug": ("linear_attention_recurrence_simple_gb300/csrc/gla_chunk_tc.cu", "4a7696894bc76ba6",
+                328424192.0, "per launch of the B=8 T=2048 H=16 augmented forward"),
     # head RMSNorm + gate, 16,384 x 16 rows: 201.355776 MB read + 70.854144 MB written (part of y
     # is still in L2 when the kernel ends), one launch
     "norm_gate": ("linear_attention_recurrence_simple_gb300/csrc/gla_norm.cu", "4987f08ea9f6d8e4",
                   272209920.0, "per launch of the 16,384 x 16 rows"),
-    # the MXFP8 pool: 972.065536 MB read + 891.097600 MB written
-    "decode_mxfp8_state": ("linear_attention_recurrence_simple_gb300/csrc/gla_mxfp8.cu", "f6089eb8ba7aa3fc",
-                           1863163136.0 / 49152, "per state per step"),
-    # the all-fp32 mode's forward: 404.579072 MB read + 183.889408 MB written (part of o is still
+    # the MXFP8 pool: 972.151296 MB read + 891.126016 MB written
+    "decode_mxfp8_state": ("linear_attention_recurrence_simple_gb300/csrc/gla_mxfp8.cu", "34d304ef18040499",
+                           1863277312.0 / 49152, "per state per step"),
+    # the all-fp32 mode's forward: 404.434944 MB read + 183.803392 MB written (part of o is still
     # in L2 when the kernel ends), one launch
-    "fwd_fp32": ("linear_attention_recurrence_simple_gb300/csrc/gla_simt.cu", "5d41f691b419266d",
-                 588468480.0, "per launch of the B=8 T=2048 H=16 fp32 forward"),
-    # the all-fp32 mode's backward, its three launches per call: dq 509.791232 + 90.155520 MB,
-    # dk 519.075072 + 93.504256 MB, dv 414.464000 + 172.825344 MB (read + written)
-    "bwd_fp32": ("linear_attention_recurrence_simple_gb300/csrc/gla_simt.cu", "5d41f691b419266d",
-                 1799815424.0, "per call (three launches) of the B=8 T=2048 H=16 fp32 backward"),
+    "fwd_fp32": ("linear_attention_recurrence_simple_gb300/csrc/gla_simt.cu", "b7c0dac0f2462eba",
+                 588238336.0, "per launch of the B=8 T=2048 H=16 fp32 forward"),
+    # the all-fp32 mode's backward, its three launches per call: dq 509.637888 + 91.072512 MB,
+    # dk 519.472128 + 94.564352 MB, dv 413.842688 + 173.957376 MB (read + written)
+    "bwd_fp32": ("linear_attention_recurrence_simple_gb300/csrc/gla_simt.cu", "b7c0dac0f2462eba",
+                 1802546944.0, "per call (three launches) of the B=8 T=2048 H=16 fp32 backward"),
 }
 
 
