@@ -125,8 +125,6 @@ int check_chunk_sizes(int n_seq, int T, int H, int dk, int dv, int dtype, const 
   if (cu_seqlens && ((uintptr_t)cu_seqlens & 3u)) return GLA_ERR_ALIGN;
   return GLA_OK;
 }
-// Internal accessors for the allocation-free entry point (gla_noalloc.cu); the entry points
-// above do not go through them.
 #ifdef GLA_DEBUG_BOUNDS
 static std::atomic<unsigned long long> g_give_up{0};
 unsigned long long debug_give_up() { return g_give_up; }
@@ -134,6 +132,8 @@ unsigned long long debug_give_up() { return g_give_up; }
 unsigned long long debug_give_up() { return 0; }
 #endif
 
+// Internal accessors for the allocation-free entry point (gla_noalloc.cu); the entry points
+// above do not go through them.
 int current_device_state(unsigned** err, unsigned long long* wait_ns) {
   int dev;
   return device_state(&dev, err, wait_ns);

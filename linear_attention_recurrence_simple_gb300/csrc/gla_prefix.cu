@@ -44,7 +44,7 @@ constexpr int DEC_TILE = 4;
 // Scales of 2^65 and more (the code of an infinity stands under 2^120): the element is formed before it is
 // multiplied with anything.
 constexpr uint32_t WIDE_SCALE = 192;
-constexpr float WIDE_FACTOR = 1.152921504606846976e18f;  // 2^60: below it, 448 x 2^64 x factor x 96 stays in fp32's range
+constexpr float WIDE_FACTOR = 1.152921504606846976e18f;  // 2^60: neither codes x query nor weight x scale passes fp32's range below it
 static_assert(DEC_TOK * 6 == DEC_THREADS && 16 * 12 == DEC_THREADS, "pieces of a chunk");
 
 // A 16-value piece as it is stored: fp32, or codes and their block's scale byte.
@@ -641,7 +641,7 @@ prefix_decode_tile_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat
 #pragma unroll
         for (int e = 0; e < 4; ++e) qf[b][e] = g == 0 ? qf[b][e] : 0u;
     }
-    while (c < last && ok) {  // runs of chunks that the MMAs take, each but the last with one chunk behind it that they do not
+    while (c < last && ok) {  // runs of chunks that the MMAs take, each ended by a far chunk or the last
     bool far_chunk = false;
     float acc[12][4];  // 16 columns each: see the flush below
 #pragma unroll
