@@ -432,6 +432,87 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
                    void* dk, void* dv, float* dpool, const int32_t* cu_seqlens, int n_seq, int T, int H, int dk_size,
                    int dv_size, int dtype, void* workspace, size_t ws_bytes, gla_stream_t stream);
 
+/* The gated delta rule (no counterpart in the paper; the recurrence of Gated DeltaNet layers).  Per head the same
+ * 96 x 192 state, with a decay and a writing strength of every token's own, both learned:
+ *     S_t = a_t S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - a_t S_{t-1}^T k_t),   a_t = exp(g_t),
+ *     o_t = S_t^T (scale q_t):
+ * what the decayed state holds under the key is replaced, by the share beta_t, with the value.
+ *   g, beta      [n_seq, T, H] (or packed [T_total, H]; [N, H] in the decode step), dtype `dtype`: the natural
+ *                log of the decay (<= 0 in use; -inf allowed, a reset; values below -120 count as -120) and the
+ *                strength.  beta times the squared length of k is meant to lie in [0, 2]: beyond that the
+ *                recurrence itself grows.  (Keys of unit length and strengths in [0, 1] are the usual form.)
+ * q, k, v, o, states, scale, cu_seqlens, dtype and the layouts are those of gla_chunk_fwd.  A call's tokens are
+ * handled in chunks of 64; an infinity or a NaN in a token reaches every output of its chunk and what follows it in
+ * its sequence, and nothing of another sequence.  cu_seqlens is checked on the device: offsets that decrease or pass
+ * T are clamped and record GLA_ERR_SHAPE.
+ * Calls may be captured into a graph after a first call of the same kind on the device; calls that may overlap need
+ * workspaces of their own. */
+
+/* Chunked forward.
+ *   h0           [h0_rows, H, 96, 192] fp32 initial states, or NULL for zeros.
+ *   h0_row       [n_seq] int32 device: sequence n starts from row h0_row[n] (rows may repeat), from zeros where it
+ *                is -1; NULL = row n (then h0_rows >= n_seq).  Any other row outside h0 records GLA_ERR_SHAPE and
+ *                starts from zeros.
+ *   hT           [hT_rows, H, 96, 192] fp32 final states, or NULL to skip; hT_row [n_seq] int32 device: their
+ *                rows, distinct, -1: not wanted; NULL = row n.  Any other row outside hT records GLA_ERR_SHAPE and
+ *                is not written.  hT may be h0: a sequence may end in the row that it started from, as long as no
+ *                other sequence of the call starts from a row that it writes.  Rows that no sequence has are left.
+ *   workspace    >= gla_delta_workspace_bytes(n_seq, T, H, cu_seqlens != NULL, dtype) bytes.
+ * A sequence without tokens ends in the state it starts from. */
+size_t gla_delta_workspace_bytes(int n_seq, int T, int H, int packed, int dtype);
+int gla_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* h0,
+                  int h0_rows, const int32_t* h0_row, float scale, void* o, float* hT, int hT_rows,
+                  const int32_t* hT_row, const int32_t* cu_seqlens, int n_seq, int T, int H, int dk, int dv, int dtype,
+                  void* workspace, size_t ws_bytes, gla_stream_t stream);
+
+/* Chunked backward: gradients of L(o, hT) given dO = dL/do and dhT = dL/dhT.
+ *   h0           [n_seq, H, 96, 192] fp32, or NULL for zeros; dhT the same, or NULL for zeros.
+ *   dq, dk, dv   outputs, layouts of q, k, v; dg, dbeta outputs, layout of g; all of dtype `dtype`.
+ *   dh0          [n_seq, H, 96, 192] fp32 output, or NULL to skip.
+ *   workspace    >= gla_delta_bwd_workspace_bytes(n_seq, T, H, cu_seqlens != NULL, dtype) bytes.
+ * The chunks' states are computed again; nothing of gla_delta_fwd is needed.  No sum depends on an order of
+ * arrival: the same call gives the same bits. */
+size_t gla_delta_bwd_workspace_bytes(int n_seq, int T, int H, int packed, int dtype);
+int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* h0,
+                  float scale, const void* dO, const float* dhT, void* dq, void* dk, void* dv, void* dg, void* dbeta,
+                  float* dh0, const int32_t* cu_seqlens, int n_seq, int T, int H, int dk_size, int dv_size, int dtype,
+                  void* workspace, size_t ws_bytes, gla_stream_t stream);
+
+/* One decode step for N sequences, in place on a pool of states, fp32 or (_bf16_state) bf16.
+ *   q, k [N, H, 96]; v, o [N, H, 192]; g, beta [N, H]; state, slot, pool_rows as in gla_decode_step (rows distinct),
+ *   but that a slot of -1 leaves its sequence alone (state and o untouched) without an error.  N * H below 2^31.
+ * The readout uses the update before a bf16 pool rounds it. */
+int gla_delta_decode_step(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale,
+                          float* state, const int32_t* slot, int pool_rows, void* o, int N, int H, int dk, int dv,
+                          int dtype, gla_stream_t stream);
+int gla_delta_decode_step_bf16_state(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                     float scale, void* state, const int32_t* slot, int pool_rows, void* o, int N,
+                                     int H, int dk, int dv, int dtype, gla_stream_t stream);
+
+/* One serving step's maps, built on the device from the requests' lengths, so that a step needs no host
+ * synchronisation (and can be captured: all sizes are fixed).
+ *   new_len      [N] int32 device: tokens that request n brings; 0: none now (it keeps its row); negative: it has
+ *                finished, and its row is free.
+ *   held         [N] int32 device: the pool row that request n holds, -1: none.  Rows distinct (a row held twice
+ *                records GLA_ERR_SHAPE).  Any other row outside [0, pool_rows) records GLA_ERR_SHAPE, and the
+ *                request gets no row and no tokens.
+ *   seen         [N] int32 device: tokens before this step, or NULL for zeros (used by token_pos).
+ * Requests are served in order: one that brings tokens and holds no row takes the lowest free one (without one it gets
+ * no tokens); each gets its tokens until `budget` tokens are handed out, the one at the limit a part of them.
+ *   cu_seqlens   [N + 1]: packed offsets of the tokens handed out.
+ *   slot         [N]: row of a request that has tokens in this step, else -1 (hT_row, and the decode step's slot).
+ *   start_row    [N]: the row it goes on from, -1 where it is new or has no tokens (h0_row).
+ *   row          [N]: the row it holds after the step, -1: none (the next step's held).
+ *   token_seq, token_pos   [budget]: request and place (seen + the place in this step) of each packed token, -1
+ *                behind the last; both or neither NULL.
+ * Inputs and outputs must not overlap, but that row may be held.  pool_rows from 1 to GLA_PLAN_MAX_ROWS, N up to
+ * GLA_PLAN_MAX_REQUESTS (else GLA_ERR_SHAPE, GLA_ERR_UNSUPPORTED).  Pointers 4-byte aligned. */
+#define GLA_PLAN_MAX_ROWS (1 << 19)
+#define GLA_PLAN_MAX_REQUESTS (1 << 20)
+int gla_slot_plan(const int32_t* new_len, const int32_t* held, const int32_t* seen, int N, int pool_rows, int budget,
+                  int32_t* cu_seqlens, int32_t* slot, int32_t* start_row, int32_t* row, int32_t* token_seq,
+                  int32_t* token_pos, gla_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the current device's sticky error word:
  * GLA_OK, GLA_ERR_TIMEOUT or GLA_ERR_SHAPE (or, in the debug-bounds build, GLA_ERR_BOUNDS);
  * GLA_ERR_LAUNCH if the stream itself failed.

@@ -27,6 +27,8 @@ __all__ = [
     "gla_chunk_fwd_host_workspace_bytes", "GlaTail", "gla_tail_alloc", "gla_tail_append", "gla_tail_read",
     "gla_tail_fold", "gla_prefix_decode_step", "gla_prefix_fwd", "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes",
     "gla_status_string", "DK", "DV", "CHUNK", "EXPORTS",
+    "gla_delta_fwd", "gla_delta_bwd", "gla_delta_decode_step", "gla_delta_workspace_bytes",
+    "gla_delta_bwd_workspace_bytes", "SlotPlan", "gla_slot_plan",
 ]
 
 DK, DV, CHUNK = 96, 192, 128
@@ -39,7 +41,9 @@ EXPORTS = ("gla_workspace_bytes", "gla_bwd_workspace_bytes", "gla_chunk_fwd", "g
            "gla_split_choose_seg_chunks", "gla_chunk_fwd_noalloc", "gla_get_device_error", "gla_set_wait_limit_ns",
            "gla_debug_bounds", "gla_chunk_fwd_host", "gla_chunk_fwd_host_workspace_bytes", "gla_status_string",
            "gla_prefix_decode_step", "gla_tail_append", "gla_tail_read", "gla_tail_fold", "gla_prefix_fwd",
-           "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes", "gla_debug_give_up")
+           "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes", "gla_debug_give_up", "gla_delta_fwd", "gla_delta_bwd",
+           "gla_delta_workspace_bytes", "gla_delta_bwd_workspace_bytes", "gla_delta_decode_step",
+           "gla_delta_decode_step_bf16_state", "gla_slot_plan")
 NOALLOC_MAX_SEQS = 16384
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -141,6 +145,19 @@ def load_library(build: bool = True, debug: bool | None = None):
         lib.gla_prefix_bwd_workspace_bytes.restype = Z
         lib.gla_prefix_bwd.argtypes = [P, P, P, P, P, I, P, F, P, P, P, P, P, P, P, I, I, I, I, I, I, P, Z, P]
         lib.gla_prefix_bwd.restype = I
+        lib.gla_delta_workspace_bytes.argtypes = [I, I, I, I, I]
+        lib.gla_delta_workspace_bytes.restype = Z
+        lib.gla_delta_bwd_workspace_bytes.argtypes = [I, I, I, I, I]
+        lib.gla_delta_bwd_workspace_bytes.restype = Z
+        lib.gla_delta_fwd.argtypes = [P, P, P, P, P, P, I, P, F, P, P, I, P, P, I, I, I, I, I, I, P, Z, P]
+        lib.gla_delta_fwd.restype = I
+        lib.gla_delta_bwd.argtypes = [P, P, P, P, P, P, F, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, Z, P]
+        lib.gla_delta_bwd.restype = I
+        for fn in (lib.gla_delta_decode_step, lib.gla_delta_decode_step_bf16_state):
+            fn.argtypes = [P, P, P, P, P, F, P, P, I, P, I, I, I, I, I, P]
+            fn.restype = I
+        lib.gla_slot_plan.argtypes = [P, P, P, I, I, I, P, P, P, P, P, P, P]
+        lib.gla_slot_plan.restype = I
         _libs[debug] = lib
         return lib
 
@@ -980,6 +997,177 @@ def gla_prefix_bwd(q, k, v, log_lambda, dO, pool, prefix_row, cu_seqlens, scale=
          _addr(dhT), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _addr(dpool), cu_seqlens.data_ptr(), n_seq, T, H, DK,
          DV, dt, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dv, dpool
+
+
+def gla_delta_workspace_bytes(n_seq: int, T: int, H: int, packed: bool, dtype_code: int) -> int:
+    return int(load_library().gla_delta_workspace_bytes(int(n_seq), int(T), int(H), int(bool(packed)), int(dtype_code)))
+
+
+def gla_delta_bwd_workspace_bytes(n_seq: int, T: int, H: int, packed: bool, dtype_code: int) -> int:
+    return int(load_library().gla_delta_bwd_workspace_bytes(int(n_seq), int(T), int(H), int(bool(packed)),
+                                                            int(dtype_code)))
+
+
+def _delta_call(q, k, v, g, beta, cu_seqlens):
+    """Checks what the chunked gated delta calls share."""
+    dev = _device_of(q, "q")
+    dt = _dtype_code(q)
+    if not _like(dev.index, q.dtype, q, k, v, g, beta):
+        for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
+            _need(t, name, q.dtype, dev)
+    if cu_seqlens is not None:
+        _good(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [n_seq + 1]")
+    n_seq, T, H = _layout(q, k, v, cu_seqlens)
+    if g.shape != q.shape[:-1] or beta.shape != g.shape:
+        raise ValueError("g and beta must have the shape of q without its last dimension")
+    return dev, dt, n_seq, T, H
+
+
+def _delta_states(h, row, n_seq, H, dev, name):
+    """Rows of a [rows, H, 96, 192] array of states, and its row map, checked."""
+    if h is None:
+        if row is not None:
+            raise ValueError(f"{name}_row without {name}")
+        return 0
+    rows = _pool(h, H, dev, name)
+    if row is not None:
+        _good(row, name + "_row", torch.int32, dev)
+        if row.shape != (n_seq,):
+            raise ValueError(f"{name}_row must be [n_seq]")
+    elif rows < n_seq:
+        raise ValueError(f"{name} must have a row for each of the {n_seq} sequences")
+    return rows
+
+
+def gla_delta_fwd(q, k, v, g, beta, scale=None, h0=None, h0_row=None, hT=None, hT_row=None, cu_seqlens=None,
+                  output_final_state: bool = True, o=None, workspace=None):
+    """Chunked forward of the gated delta rule (``gla_delta_fwd``).  Returns ``(o, hT)``.
+
+    q, k ``[B, T, H, 96]``, v ``[B, T, H, 192]``, or packed ``[T_total, H, d]`` with ``cu_seqlens``; ``g`` (the log
+    of the decay) and ``beta`` ``[B, T, H]`` or ``[T_total, H]``, all of one type.  ``h0`` fp32 ``[P, H, 96, 192]``
+    with ``h0_row`` ``[n_seq]`` int32 (rows may repeat; -1: zeros), or None for row n; ``hT`` and ``hT_row`` likewise
+    (rows distinct; -1: not wanted).  ``hT`` may be ``h0``: sequences then go on from rows of a pool and end in
+    them.  Without ``hT``, ``[n_seq, H, 96, 192]`` is allocated (or None, if not requested)."""
+    lib = _libs.get(_use_debug) or load_library()
+    dev, dt, n_seq, T, H = _delta_call(q, k, v, g, beta, cu_seqlens)
+    h0_rows = _delta_states(h0, h0_row, n_seq, H, dev, "h0")
+    if hT is None and output_final_state and hT_row is None:
+        hT = torch.empty((n_seq, H, DK, DV), dtype=torch.float32, device=dev)
+    hT_rows = _delta_states(hT, hT_row, n_seq, H, dev, "hT")
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _good(o, "o", v.dtype, dev, v.numel())
+    if workspace is None:
+        workspace = torch.empty(lib.gla_delta_workspace_bytes(n_seq, T, H, int(cu_seqlens is not None), dt),
+                                dtype=torch.uint8, device=dev)
+    _run(lib.gla_delta_fwd, "gla_delta_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+         beta.data_ptr(), _addr(h0), h0_rows, _addr(h0_row), DK ** -0.5 if scale is None else float(scale), o.data_ptr(),
+         _addr(hT), hT_rows, _addr(hT_row), _addr(cu_seqlens), n_seq, T, H, DK, DV, dt, workspace.data_ptr(),
+         workspace.numel() * workspace.element_size())
+    return o, hT
+
+
+def gla_delta_bwd(q, k, v, g, beta, dO, scale=None, h0=None, dhT=None, cu_seqlens=None, need_dh0: bool = True,
+                  workspace=None):
+    """Backward of :func:`gla_delta_fwd` (``gla_delta_bwd``).  Returns ``(dq, dk, dv, dg, dbeta, dh0)`` (``dh0``
+    None if not requested); ``h0`` and ``dhT`` fp32 ``[n_seq, H, 96, 192]``, or None for zeros."""
+    lib = _libs.get(_use_debug) or load_library()
+    dev, dt, n_seq, T, H = _delta_call(q, k, v, g, beta, cu_seqlens)
+    _good(dO, "dO", q.dtype, dev)
+    if dO.shape != v.shape:
+        raise ValueError("dO must have the shape of v")
+    for name, t in (("h0", h0), ("dhT", dhT)):
+        if t is not None and _pool(t, H, dev, name) != n_seq:
+            raise ValueError(f"{name} must be [n_seq, H, 96, 192]")
+    dq, dk, dv, dg, dbeta = (torch.empty_like(t) for t in (q, k, v, g, beta))
+    dh0 = torch.empty((n_seq, H, DK, DV), dtype=torch.float32, device=dev) if need_dh0 else None
+    if workspace is None:
+        workspace = torch.empty(lib.gla_delta_bwd_workspace_bytes(n_seq, T, H, int(cu_seqlens is not None), dt),
+                                dtype=torch.uint8, device=dev)
+    _run(lib.gla_delta_bwd, "gla_delta_bwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+         beta.data_ptr(), _addr(h0), DK ** -0.5 if scale is None else float(scale), dO.data_ptr(), _addr(dhT),
+         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _addr(dh0), _addr(cu_seqlens),
+         n_seq, T, H, DK, DV, dt, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dq, dk, dv, dg, dbeta, dh0
+
+
+def gla_delta_decode_step(q, k, v, g, beta, state, slot=None, scale=None, o=None):
+    """One decode step of the gated delta rule on the pool ``state [P, H, 96, 192]`` (fp32 or bf16, updated in
+    place).  q, k ``[N, H, 96]``; v ``[N, H, 192]``; g, beta ``[N, H]``; ``slot`` ``[N]`` int32 pool rows (-1: the
+    sequence is left alone) or None (row n).  Returns ``o [N, H, 192]``."""
+    lib = _libs.get(_use_debug) or load_library()
+    dev = _device_of(q, "q")
+    dt = _dtype_code(q)
+    if not _like(dev.index, q.dtype, q, k, v, g, beta):
+        for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
+            _need(t, name, q.dtype, dev)
+    if q.dim() != 3 or q.shape[2] != DK or k.shape != q.shape or v.shape != (*q.shape[:2], DV):
+        raise ValueError("expected q, k [N, H, 96] and v [N, H, 192]")
+    N, H = q.shape[:2]
+    if g.shape != (N, H) or beta.shape != (N, H):
+        raise ValueError("g and beta must be [N, H]")
+    if not isinstance(state, torch.Tensor) or state.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("state must be float32 or bfloat16")
+    _good(state, "state", state.dtype, dev)
+    if state.dim() != 4 or state.shape[1:] != (H, DK, DV):
+        raise ValueError("state must be [P, H, 96, 192]")
+    if slot is not None:
+        _good(slot, "slot", torch.int32, dev)
+        if slot.shape != (N,):
+            raise ValueError("slot must be [N]")
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _good(o, "o", v.dtype, dev, v.numel())
+    fn, where = ((lib.gla_delta_decode_step_bf16_state, "gla_delta_decode_step_bf16_state")
+                 if state.dtype == torch.bfloat16 else (lib.gla_delta_decode_step, "gla_delta_decode_step"))
+    _run(fn, where, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+         DK ** -0.5 if scale is None else float(scale), state.data_ptr(), _addr(slot), state.shape[0], o.data_ptr(),
+         N, H, DK, DV, dt)
+    return o
+
+
+class SlotPlan(NamedTuple):
+    """One serving step's maps, all int32 (see :func:`gla_slot_plan`)."""
+    cu_seqlens: torch.Tensor  # [N + 1]
+    slot: torch.Tensor        # [N]
+    start_row: torch.Tensor   # [N]
+    row: torch.Tensor         # [N]
+    token_seq: torch.Tensor   # [budget]
+    token_pos: torch.Tensor   # [budget]
+
+
+def gla_slot_plan(new_len, held, seen, pool_rows: int, budget: int, out=None):
+    """One serving step's maps from the requests' lengths, on the device (``gla_slot_plan``).
+
+    ``new_len`` ``[N]`` int32: tokens each request brings (0: none now; negative: it has finished); ``held`` ``[N]``
+    int32: the pool row it holds, or -1; ``seen`` ``[N]`` int32: its tokens before this step, or None for zeros.  Of
+    ``budget`` tokens each request in turn gets what it brings; one without a row takes the lowest of the
+    ``pool_rows`` that is free.  Returns a :class:`SlotPlan` (``out``: one to write to): ``cu_seqlens``, ``start_row``
+    and ``slot`` are :func:`gla_delta_fwd`'s ``cu_seqlens``, ``h0_row`` and ``hT_row``, ``row`` the next step's
+    ``held``, ``token_seq`` and ``token_pos`` each packed token's request and place (-1 behind the last)."""
+    lib = _libs.get(_use_debug) or load_library()
+    dev = _device_of(new_len, "new_len")
+    N, budget = new_len.numel(), int(budget)
+    for name, t in (("new_len", new_len), ("held", held), ("seen", seen)):
+        if t is not None or name != "seen":
+            _good(t, name, torch.int32, dev)
+            if t.shape != (N,):
+                raise ValueError(f"{name} must be [N]")
+    if budget < 0:
+        raise ValueError("budget must not be negative")
+    sizes = (N + 1, N, N, N, budget, budget)
+    if out is None:
+        out = SlotPlan(*torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes))
+    else:
+        for name, t, size in zip(SlotPlan._fields, out, sizes):
+            _good(t, "out." + name, torch.int32, dev, size)
+    _run(lib.gla_slot_plan, "gla_slot_plan", dev, new_len.data_ptr(), held.data_ptr(), _addr(seen), N, int(pool_rows),
+         budget, *(t.data_ptr() for t in out))
+    return out
 
 
 def gla_get_device_error(device=None) -> int:

@@ -1,0 +1,159 @@
+// The gated delta rule: what its kernels share (arguments, chunk places, decays of a chunk).
+//
+// Per head, with a decay a_t = exp(g_t) and a strength beta_t of every token's own,
+//     S_t = a_t S_{t-1} + k_t u_t^T,   u_t = beta_t x_t,   x_t = v_t - a_t S_{t-1}^T k_t,   o_t = S_t^T (scale q_t).
+// For a chunk of C tokens, S0 the state before it, G_i = g_1 + .. + g_i, B = diag(beta):
+//     D_ij = exp(G_i - G_j) for j <= i, else 0,   P = QK^T . D,   M = KK^T . D without its diagonal
+//     R = V - diag(e^G) K S0,   (1 + M B) X = R,   U = B X
+//     O = s (diag(e^G) Q S0 + P U),   S1 = e^(G_C) S0 + (diag(e^(G_C - G)) K)^T U
+// The inverse is kept as Z = (1 + M B)^-1 M, strictly lower triangular: X = R - Z B R, so that the large part
+// of X is R itself, and its transpose serves the backward, dR = B (dU - Z^T B dU), without a division by beta.
+// Decays enter as exp of a difference of sums, never as e^G_i times e^-G_j: g = -inf (a reset) and long runs of
+// strong decay neither overflow nor lose what is left after them.
+#pragma once
+
+#include "gla_common.cuh"
+
+namespace gla {
+
+constexpr int DC = 64;  // tokens of a chunk
+
+struct DeltaArgs {
+  const void *q, *k, *v, *g, *beta;
+  const void* dO;            // backward
+  const float* h0;           // may be null: zeros
+  const int32_t* h0_row;     // row of h0 that each sequence starts from (-1: zeros), or null: row n
+  int h0_rows;
+  const float* dhT;          // backward; may be null
+  void* o;                   // forward
+  float* hT;                 // forward; may be null
+  const int32_t* hT_row;     // row of hT that each sequence's final state goes to (-1: none), or null: row n
+  int hT_rows;
+  void *dq, *dk, *dv, *dg, *dbeta;  // backward
+  float* dh0;                       // backward; may be null
+  const int32_t* cu_seqlens;        // null: fixed length T
+  float scale;
+  int n_seq;
+  int T;                     // per-sequence length (fixed) or packed total
+  int H;
+  int slots;                 // chunk places of the call (see chunk_of_slot)
+  unsigned* err;
+  unsigned long long wait_ns;
+  uint8_t* ws;               // workspace
+};
+
+// Places for the chunks of a call: sequence n's begin at base(n) = begin / C + n, which leaves room for
+// every sequence's ragged last chunk without anything to be summed up (base(n + 1) - base(n) is at least its
+// number of chunks); some places stay empty.
+__host__ __device__ inline long long delta_slots(int n_seq, int T, bool packed) {
+  return packed ? (long long)T / DC + n_seq : (long long)n_seq * (((long long)T + DC - 1) / DC);
+}
+
+struct DeltaSeq {
+  long long begin;
+  int len;
+  int slot0;  // place of its first chunk
+};
+__device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs& a, int n) {
+  DeltaSeq s;
+  if (a.cu_seqlens) {
+    const long long b = a.cu_seqlens[n], e = a.cu_seqlens[n + 1];
+    s.begin = min(max(b, 0ll), (long long)a.T);
+    const long long end = min(max(e, s.begin), (long long)a.T);
+    if (s.begin != b || end != e) raise_error(a.err, ERR_SHAPE);
+    s.len = (int)(end - s.begin);
+    s.slot0 = (int)(s.begin / DC) + n;
+  } else {
+    s.begin = (long long)n * a.T;
+    s.len = a.T;
+    s.slot0 = n * ((a.T + DC - 1) / DC);
+  }
+  return s;
+}
+
+// The chunk at a place: its first token and its tokens (0: the place is empty).
+struct DeltaChunk {
+  long long t0;
+  int len;
+};
+__device__ __forceinline__ DeltaChunk chunk_of_slot(const DeltaArgs& a, int slot) {
+  int n;
+  if (a.cu_seqlens) {
+    int lo = 0, hi = a.n_seq - 1;  // the last sequence with slot0 <= slot
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      const int b = min(max(a.cu_seqlens[mid], 0), a.T);
+      if (b / DC + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    n = lo;
+  } else {
+    n = slot / ((a.T + DC - 1) / DC);
+  }
+  const DeltaSeq s = delta_seq(a, n);
+  const long long off = (long long)(slot - s.slot0) * DC;
+  DeltaChunk c;
+  c.t0 = s.begin + off;
+  c.len = off < 0 || off >= s.len ? 0 : (int)min((long long)DC, s.len - off);
+  if (!GLA_IN_BOUNDS(c.len == 0 || (c.t0 >= 0 && c.t0 + c.len <= (a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T)), a.err))
+    c.len = 0;
+  return c;
+}
+
+// Row of a [rows, H, 96, 192] array that sequence n has: -1 where it has none.
+__device__ __forceinline__ int delta_row(const int32_t* row, int rows, int n, unsigned* err) {
+  if (!row) return n;
+  const int r = row[n];
+  if (r >= 0 && r < rows) return r;
+  if (r != -1) raise_error(err, ERR_SHAPE);
+  return -1;
+}
+
+// Running sums of a chunk's log decays, each as two fp32 (hi + lo): a difference of two of them keeps 24 bits
+// of what is left between them, whatever was decayed before.  Whole warp; x0, x1 are the log decays of tokens
+// 2 lane and 2 lane + 1.  Values below -120 count as -120: exp of it is zero in fp32.
+constexpr float LOG_FLOOR = -120.f;
+__device__ __forceinline__ void delta_sums(float x0, float x1, float2& s0, float2& s1) {
+  const double d0 = x0 < LOG_FLOOR ? LOG_FLOOR : x0, d1 = x1 < LOG_FLOOR ? LOG_FLOOR : x1;
+  double run = d0 + d1;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double up = __shfl_up_sync(0xffffffffu, run, off);
+    if ((int)(threadIdx.x & 31) >= off) run += up;
+  }
+  const double a = run - d1;
+  s0.x = (float)a;
+  s0.y = (float)(a - (double)s0.x);
+  s1.x = (float)run;
+  s1.y = (float)(run - (double)s1.x);
+}
+// exp(G_i - G_j)
+__device__ __forceinline__ float delta_decay(float2 gi, float2 gj) { return expf((gi.x - gj.x) + (gi.y - gj.y)); }
+__device__ __forceinline__ float delta_decay0(float2 gi) { return expf(gi.x + gi.y); }
+
+// Z = (1 + M B)^-1 M by forward substitution, one thread a column: z_i = M_ic - sum_{j < i} (M B)_ij z_j.
+// `m` and `mb` are [64][stride] in shared memory, zero on and above the diagonal; rows 16-byte aligned.
+template <int STRIDE>
+__device__ __forceinline__ void delta_solve_column(const float* m, const float* mb, int c, float (&z)[DC]) {
+#pragma unroll
+  for (int i = 0; i < DC; ++i) z[i] = 0.f;
+#pragma unroll
+  for (int i = 1; i < DC; ++i) {
+    float s0 = c < i ? m[i * STRIDE + c] : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+    for (int j = 0; j < i; j += 4) {
+      const float4 w = *reinterpret_cast<const float4*>(mb + i * STRIDE + j);
+      s0 = fmaf(-w.x, z[j], s0);
+      if (j + 1 < i) s1 = fmaf(-w.y, z[j + 1], s1);
+      if (j + 2 < i) s2 = fmaf(-w.z, z[j + 2], s2);
+      if (j + 3 < i) s3 = fmaf(-w.w, z[j + 3], s3);
+    }
+    z[i] = (s0 + s1) + (s2 + s3);
+  }
+}
+
+int current_device_state(unsigned** err, unsigned long long* wait_ns);
+cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t stream);
+cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t stream);
+size_t delta_simt_ws_bytes(long long slots, long long tokens, int H, bool bwd);
+
+}  // namespace gla

@@ -1,0 +1,135 @@
+// One-token decode step of the gated delta rule over a pool of states, in place.
+//
+//     u = beta (v - a S^T k),   S <- a S + k u^T,   o = S^T (scale q),   a = exp(g)
+// with a and beta of the (sequence, head).  The readout of the new state needs no second pass over it:
+// S_new^T q = a S^T q + (k . q) u, so both products with the old state, S^T k and S^T q, are formed from
+// the registers that hold it, and then the state is updated and written.
+//
+// A pure stream over the state, read once and written once, bound by HBM.  One CTA owns one (sequence,
+// head); thread (r, c), c < 48, holds columns 4c .. 4c + 3 of rows r, r + G, ..: consecutive lanes touch
+// consecutive pieces of a row.  fp32 pools with 576 threads (8 rows of 16-byte vectors each, 2 CTAs an SM: 147 KB
+// in flight), bf16 pools with 288 (16 rows of 8-byte vectors, kept packed).
+#include "gla_delta.cuh"
+
+namespace gla {
+namespace {
+
+constexpr int VCOLS = DV / 4;  // 48 four-column vectors of a row
+template <class ST> struct StepCfg;
+template <> struct StepCfg<float> { static constexpr int THREADS = 576, MIN_BLOCKS = 2; };
+template <> struct StepCfg<__nv_bfloat16> { static constexpr int THREADS = 288, MIN_BLOCKS = 4; };
+
+__device__ __forceinline__ float4 widen(float4 x) { return x; }
+__device__ __forceinline__ float4 widen(uint2 u) {
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint2 pack4(float4 x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void put4(float4* p, float4 x) { __stcs(p, x); }
+__device__ __forceinline__ void put4(uint2* p, float4 x) { __stcs(p, pack4(x)); }
+template <class T> struct Vec4;
+template <> struct Vec4<float> { using type = float4; };
+template <> struct Vec4<__nv_bfloat16> { using type = uint2; };
+
+__device__ __forceinline__ float4 fma4(float a, float4 x, float4 y) {
+  return make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
+}
+
+template <class T, class ST>
+__global__ void __launch_bounds__(StepCfg<ST>::THREADS, StepCfg<ST>::MIN_BLOCKS)
+delta_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ g,
+                    const T* __restrict__ beta, float scale, ST* __restrict__ state, const int32_t* __restrict__ slot,
+                    int pool_rows, T* __restrict__ o, int H, unsigned* err) {
+  constexpr int RG = StepCfg<ST>::THREADS / VCOLS, ROWS = DK / RG;
+  using SV = typename Vec4<ST>::type;
+  using TV = typename Vec4<T>::type;
+  __shared__ float s_q[DK], s_k[DK];
+  __shared__ float s_qk;
+  __shared__ float4 s_part[2][RG][VCOLS];  // S^T k, S^T q
+  __shared__ float4 s_u[VCOLS];
+  const long long nh = blockIdx.x;
+  const int n = (int)(nh / H), h = (int)(nh % H), tid = threadIdx.x, c = tid % VCOLS, r = tid / VCOLS;
+  const int row = slot ? slot[n] : n;
+  if (row < 0 || row >= pool_rows) {  // -1: a sequence without a row, left alone
+    if (tid == 0 && row != -1) raise_error(err, ERR_SHAPE);
+    return;
+  }
+  SV* const S = reinterpret_cast<SV*>(state + ((long long)row * H + h) * (DK * DV));
+  SV s[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) s[i] = __ldcs(S + (r + RG * i) * VCOLS + c);
+  if (tid < DK) {
+    s_q[tid] = scale * to_f(q[nh * DK + tid]);
+    s_k[tid] = to_f(k[nh * DK + tid]);
+  }
+  const float a = expf(to_f(g[nh]));
+  __syncthreads();
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 dk = zero, dq = zero;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const float4 x = widen(s[i]);
+    dk = fma4(s_k[r + RG * i], x, dk);
+    dq = fma4(s_q[r + RG * i], x, dq);
+  }
+  s_part[0][r][c] = dk;
+  s_part[1][r][c] = dq;
+  if (tid < 32) {
+    float d = 0.f;
+#pragma unroll
+    for (int e = tid; e < DK; e += 32) d = fmaf(s_q[e], s_k[e], d);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (tid == 0) s_qk = d;
+  }
+  __syncthreads();
+  if (tid < VCOLS) {
+    float4 x = zero;
+#pragma unroll
+    for (int i = 0; i < RG; ++i) x = fma4(1.f, s_part[0][i][tid], x);
+    const float4 vv = widen(reinterpret_cast<const TV*>(v + nh * DV)[tid]);
+    const float b = to_f(beta[nh]);
+    s_u[tid] = make_float4(b * fmaf(-a, x.x, vv.x), b * fmaf(-a, x.y, vv.y), b * fmaf(-a, x.z, vv.z), b * fmaf(-a, x.w, vv.w));
+  }
+  __syncthreads();
+  const float4 u = s_u[c];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const float4 x = widen(s[i]);
+    const float kk = s_k[r + RG * i];
+    put4(S + (r + RG * i) * VCOLS + c,
+         make_float4(fmaf(a, x.x, kk * u.x), fmaf(a, x.y, kk * u.y), fmaf(a, x.z, kk * u.z), fmaf(a, x.w, kk * u.w)));
+  }
+  if (tid < VCOLS) {
+    float4 x = zero;
+#pragma unroll
+    for (int i = 0; i < RG; ++i) x = fma4(1.f, s_part[1][i][tid], x);
+    const float qk = s_qk;
+    put4(reinterpret_cast<TV*>(o + nh * DV) + tid,
+         make_float4(fmaf(a, x.x, qk * u.x), fmaf(a, x.y, qk * u.y), fmaf(a, x.z, qk * u.z), fmaf(a, x.w, qk * u.w)));
+  }
+}
+
+template <class T, class ST>
+void launch(const DeltaArgs& a, void* state, const int32_t* slot, int pool_rows, cudaStream_t st) {
+  delta_decode_kernel<T, ST><<<(unsigned)((long long)a.n_seq * a.H), StepCfg<ST>::THREADS, 0, st>>>(
+      (const T*)a.q, (const T*)a.k, (const T*)a.v, (const T*)a.g, (const T*)a.beta, a.scale, (ST*)state, slot, pool_rows,
+      (T*)a.o, a.H, a.err);
+}
+
+}  // namespace
+
+cudaError_t launch_delta_decode(const DeltaArgs& a, int dtype_f32, int state_bf16, void* state, const int32_t* slot,
+                                int pool_rows, cudaStream_t st) {
+  using BF = __nv_bfloat16;
+  if (dtype_f32 && !state_bf16) launch<float, float>(a, state, slot, pool_rows, st);
+  else if (dtype_f32) launch<float, BF>(a, state, slot, pool_rows, st);
+  else if (!state_bf16) launch<BF, float>(a, state, slot, pool_rows, st);
+  else launch<BF, BF>(a, state, slot, pool_rows, st);
+  return cudaGetLastError();
+}
+
+}  // namespace gla
