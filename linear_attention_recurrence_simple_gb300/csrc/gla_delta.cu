@@ -8,7 +8,6 @@ cudaError_t launch_delta_decode(const DeltaArgs& a, int dtype_f32, int state_bf1
 cudaError_t launch_slot_plan(const int32_t* new_len, const int32_t* held, const int32_t* seen, int N, int rows, int budget,
                              int32_t* cu, int32_t* slot, int32_t* start, int32_t* row, int32_t* token_seq, int32_t* token_pos,
                              unsigned* err, cudaStream_t st);
-cudaError_t launch_delta_simt_fwd_bf16(const DeltaArgs& a, cudaStream_t stream);
 cudaError_t launch_delta_simt_bwd_bf16(const DeltaArgs& a, cudaStream_t stream);
 int check_chunk_sizes(int n_seq, int T, int H, int dk, int dv, int dtype, const int32_t* cu_seqlens, long long* tokens);
 }  // namespace gla
@@ -29,10 +28,10 @@ int check_sizes(int n_seq, int T, int H, int dk, int dv, int dtype, const int32_
   return GLA_OK;
 }
 
-size_t ws_bytes_of(int n_seq, int T, int H, bool packed, bool bwd) {
+size_t ws_bytes_of(int n_seq, int T, int H, bool packed, bool bwd, int dtype) {
   if (n_seq < 0 || T < 0 || H < 1) return 0;
-  const long long tokens = packed ? (long long)T : (long long)n_seq * T;
-  return 256 + gla::delta_simt_ws_bytes(gla::delta_slots(n_seq, T, packed), tokens, H, bwd);
+  const long long tokens = packed ? (long long)T : (long long)n_seq * T, slots = gla::delta_slots(n_seq, T, packed);
+  return 256 + (dtype == GLA_BF16 && !bwd ? gla::delta_tc_ws_bytes(slots, H) : gla::delta_simt_ws_bytes(slots, tokens, H, bwd));
 }
 
 }  // namespace
@@ -40,12 +39,10 @@ size_t ws_bytes_of(int n_seq, int T, int H, bool packed, bool bwd) {
 extern "C" {
 
 size_t gla_delta_workspace_bytes(int n_seq, int T, int H, int packed, int dtype) {
-  (void)dtype;
-  return ws_bytes_of(n_seq, T, H, packed != 0, false);
+  return ws_bytes_of(n_seq, T, H, packed != 0, false, dtype);
 }
 size_t gla_delta_bwd_workspace_bytes(int n_seq, int T, int H, int packed, int dtype) {
-  (void)dtype;
-  return ws_bytes_of(n_seq, T, H, packed != 0, true);
+  return ws_bytes_of(n_seq, T, H, packed != 0, true, dtype);
 }
 
 int gla_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* h0, int h0_rows,
@@ -87,7 +84,7 @@ int gla_delta_fwd(const void* q, const void* k, const void* v, const void* g, co
   a.H = H;
   a.ws = (uint8_t*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
-  return status_of(dtype == GLA_F32 ? gla::launch_delta_simt_fwd(a, st) : gla::launch_delta_simt_fwd_bf16(a, st));
+  return status_of(dtype == GLA_F32 ? gla::launch_delta_simt_fwd(a, st) : gla::launch_delta_tc_fwd(a, st));
 }
 
 int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* h0, float scale,

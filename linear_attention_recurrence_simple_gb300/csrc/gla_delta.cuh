@@ -112,8 +112,10 @@ __device__ __forceinline__ int delta_row(const int32_t* row, int rows, int n, un
 // of what is left between them, whatever was decayed before.  Whole warp; x0, x1 are the log decays of tokens
 // 2 lane and 2 lane + 1.  Values below -120 count as -120: exp of it is zero in fp32.
 constexpr float LOG_FLOOR = -120.f;
+template <bool BASE2 = false>  // sums of the logs to base 2
 __device__ __forceinline__ void delta_sums(float x0, float x1, float2& s0, float2& s1) {
-  const double d0 = x0 < LOG_FLOOR ? LOG_FLOOR : x0, d1 = x1 < LOG_FLOOR ? LOG_FLOOR : x1;
+  const double unit = BASE2 ? 1.4426950408889634 : 1.0;
+  const double d0 = unit * (x0 < LOG_FLOOR ? LOG_FLOOR : x0), d1 = unit * (x1 < LOG_FLOOR ? LOG_FLOOR : x1);
   double run = d0 + d1;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -154,6 +156,8 @@ __device__ __forceinline__ void delta_solve_column(const float* m, const float* 
 int current_device_state(unsigned** err, unsigned long long* wait_ns);
 cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t stream);
 cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t stream);
+cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t stream);
+size_t delta_tc_ws_bytes(long long slots, int H);
 size_t delta_simt_ws_bytes(long long slots, long long tokens, int H, bool bwd);
 
 }  // namespace gla
