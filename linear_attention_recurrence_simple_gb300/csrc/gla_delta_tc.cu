@@ -90,6 +90,10 @@ __device__ __forceinline__ void box_store(const CUtensorMap* map, uint32_t src, 
                : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
@@ -151,164 +155,251 @@ constexpr uint32_t W_GT = 32768;                          // e^G, beta: fp32 [64
 constexpr uint32_t W_FWD = W_GT + 512;
 
 // ---- prep -------------------------------------------------------------------------------------
-// 160 threads: warps 0-3 take the products' 128 rows (K's, then Q's) out of tensor memory; warps 2 and 3 then solve
-// for the rows of P^, warps 0, 1 and 4 for those of K^.
-constexpr int MSTR = DC + 4;
+// One CTA of 4 warps a (chunk, head), all products on mma.sync (m16n8k16): the blocks are 16 wide and each step
+// of the substitution waits for the one before, and accumulators are the next product's A operand as they stand.
+//   1  warp w: rows 16 w .. of Q K^T (P, kept in registers), and K K^T's blocks that (B M)'s column block 3 - w needs:
+//      off the diagonal as B operands (hi + lo) in shared memory, on it in fp32
+//   2  the diagonal blocks' inverses (1 + B M_bb)^-1 by substitution, one thread a row, fp32
+//   3  slabs of 16 rows y of y (1 + B M) = r, block by block from the last: Y_b = (R_b - sum_c Y_c BM_cb) W_b, each
+//      product hi hi + hi lo + lo hi; a slab's rows leave through shared memory as one contiguous copy
+// fp32 sums; what is carried from block to block has 16 bits.
+constexpr int PREP_THREADS = 128;
 struct PrepSmem {
-  static constexpr uint32_t P0 = 0, P1 = 16384, M = 24576, G = M + DC * MSTR * 4, B = G + DC * 8, BAR = B + DC * 4, BYTES = BAR + 32;
+  static constexpr uint32_t P0 = 0, P1 = 16384, STAGE = 24576, DM = STAGE, FRAG = STAGE + 4 * 4096, G = FRAG + 10 * 1024, B = G + DC * 8,
+                            BAR = B + DC * 4, BYTES = BAR + 16;
 };
+static_assert(4 * 16 * 20 * 4 <= 4 * 4096, "the diagonal blocks take the stages' place");
 
-// Rows y of y (1 + BM) = r, last element first: y_m is final once the later ones are; each takes its multiple of row
-// m of BM off the elements before it.
-__device__ __forceinline__ void solve_row(const float* bm, float2 (&r)[DC / 2]) {
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Piece c (8 columns) of row r of K or Q.
+__device__ __forceinline__ uint32_t kq_at(uint32_t sb, bool is_q, int r, int c) {
+  return sb + (c < 8 ? PrepSmem::P0 + (is_q ? 8192u : 0u) + sw128(r, c) : PrepSmem::P1 + (is_q ? 4096u : 0u) + sw64(r, c - 8));
+}
+// 16 x 16 block of X Y^T, rows r0 .. of X and n0 .. of Y: two accumulators of 8 columns.
+__device__ __forceinline__ void block_dot(float (&d)[2][4], uint32_t sb, bool x_is_q, int r0, int n0) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int m = DC - 1; m > 0; --m) {
-    const float y = -((m & 1) ? r[m / 2].y : r[m / 2].x);
-    const float2 yy = make_float2(y, y);
+  for (int i = 0; i < 4; ++i) d[0][i] = d[1][i] = 0.f;
 #pragma unroll
-    for (int j = 0; j < m; j += 4) {  // (BM is zero from the diagonal on)
-      const float4 w = *reinterpret_cast<const float4*>(bm + m * MSTR + j);
-      r[j / 2] = fmadd2(yy, make_float2(w.x, w.y), r[j / 2]);
-      if (j + 2 < m) r[j / 2 + 1] = fmadd2(yy, make_float2(w.z, w.w), r[j / 2 + 1]);
-    }
+  for (int ks = 0; ks < 6; ++ks) {
+    uint32_t x[4], y[4];
+    ldsm4(x, kq_at(sb, x_is_q, r0 + (lane & 15), 2 * ks + (lane >> 4)));
+    ldsm4(y, kq_at(sb, false, n0 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
+    mma(d[0], x, y[0], y[1]);
+    mma(d[1], x, y[2], y[3]);
   }
 }
+// Accumulators of 16 columns as an A operand, hi and lo.
+__device__ __forceinline__ void to_operand(const float (&x)[2][4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2(make_float2(x[i >> 1][2 * (i & 1)], x[i >> 1][2 * (i & 1) + 1]), hi[i], lo[i]);
+}
+// d += (hi + lo) times a 16 x 16 block of B operands, hi and lo
+__device__ __forceinline__ void block_mul(float (&d)[2][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const uint8_t* frag) {
+  const uint4 h = *reinterpret_cast<const uint4*>(frag + 16 * (threadIdx.x & 31)), l = *reinterpret_cast<const uint4*>(frag + 512 + 16 * (threadIdx.x & 31));
+  mma(d[0], lo, h.x, h.y);
+  mma(d[1], lo, h.z, h.w);
+  mma(d[0], hi, l.x, l.y);
+  mma(d[1], hi, l.z, l.w);
+  mma(d[0], hi, h.x, h.y);
+  mma(d[1], hi, h.z, h.w);
+}
+// Places of the B operands: -(B M) block (c, b), c > b, and the inverse of diagonal block b.
+__device__ __forceinline__ constexpr int frag_off(int c, int b) { return c * (c - 1) / 2 + b; }
+__device__ __forceinline__ constexpr int frag_diag(int b) { return 6 + b; }
 
-__global__ void __launch_bounds__(160, 3) delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
+// A slab's rows, blocks `top` .. 0 (the ones above are zero in r): solved, and copied out (128-byte rows; with
+// `lo_out` what the rounding to bf16 leaves, too).
+__device__ __forceinline__ void solve_slab(float (&r)[4][2][4], int top, const uint8_t* frags, uint8_t* sm, uint8_t* hi_out, uint8_t* lo_out) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* const stage = sm + PrepSmem::STAGE + 4096 * (threadIdx.x >> 5);
+  uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+  for (int b = 3; b >= 0; --b) {
+    if (b <= top) {
+#pragma unroll
+      for (int c = 3; c > b; --c)
+        if (c <= top) block_mul(r[b], hi[c], lo[c], frags + 1024 * frag_off(c, b));
+      to_operand(r[b], hi[b], lo[b]);
+      float y[2][4] = {};
+      block_mul(y, hi[b], lo[b], frags + 1024 * frag_diag(b));
+      to_operand(y, hi[b], lo[b]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) hi[b][i] = lo[b][i] = 0u;
+    }
+  }
+  if (lane == 0) stores_read();
+  __syncwarp();
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // rows g, g + 8; columns 16 b + 2 t, and 8 on
+      const uint32_t at = sw128(g + 8 * (i & 1), 2 * b + (i >> 1)) + 4 * t;
+      *reinterpret_cast<uint32_t*>(stage + at) = hi[b][i];
+      *reinterpret_cast<uint32_t*>(stage + 2048 + at) = lo[b][i];
+    }
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    bulk_store(hi_out, smem_u32(stage), 2048);
+    if (lo_out) bulk_store(lo_out, smem_u32(stage + 2048), 2048);
+    stores_commit();
+  }
+}
+// Rows a0 .. of (diag(w) K)^T, w a token's weight.
+template <class W>
+__device__ __forceinline__ void transposed_slab(float (&r)[4][2][4], const uint32_t (&raw)[4][4], int len, W weight) {
+  const int t = threadIdx.x & 3;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int j = 16 * b + 8 * n + 2 * t;
+      const float w0 = weight(j), w1 = weight(j + 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = widen2(raw[b][2 * n + i]);
+        r[b][n][2 * i] = j < len ? w0 * x.x : 0.f;
+        r[b][n][2 * i + 1] = j + 1 < len ? w1 * x.y : 0.f;
+      }
+    }
+}
+__device__ __forceinline__ void load_transposed(uint32_t (&raw)[4][4], uint32_t sb, bool is_q, int a0) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) ldsm4t(raw[b], kq_at(sb, is_q, 16 * b + 8 * (lane >> 4) + (lane & 7), a0 / 8 + ((lane >> 3) & 1)));
+}
+
+__global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
-  float* const bm = reinterpret_cast<float*>(sm + PrepSmem::M);
+  float* const dm = reinterpret_cast<float*>(sm + PrepSmem::DM);   // [4][16][20]: diagonal blocks of B M
+  uint8_t* const frags = sm + PrepSmem::FRAG;
   float2* const sg = reinterpret_cast<float2*>(sm + PrepSmem::G);  // sums of log2 decays
   float* const sbeta = reinterpret_cast<float*>(sm + PrepSmem::B);
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + PrepSmem::BAR);
-  uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + PrepSmem::BAR + 16);
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + PrepSmem::BAR + 20);
-  const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x, warp = tid >> 5;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + PrepSmem::BAR + 8);
+  const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const DeltaChunk ch = chunk_of_slot(a, slot);
   if (ch.len == 0) return;
   uint8_t* const ws = a.ws + ((long long)slot * a.H + h) * W_FWD;
-  if (warp == 4) tm_alloc<64>(slot_tm);
   if (tid == 0) {
     mbar_init(bar, 1);
-    mbar_init(bar + 1, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
-    load_kq(maps, sb + PrepSmem::P0, sb + PrepSmem::P1, bar + 1, h, (int)ch.t0);
+    load_kq(maps, sb + PrepSmem::P0, sb + PrepSmem::P1, bar, h, (int)ch.t0);
   }
   if (warp == 1) {
-    const __nv_bfloat16* g = (const __nv_bfloat16*)a.g + ch.t0 * a.H + h;
-    const __nv_bfloat16* b = (const __nv_bfloat16*)a.beta + ch.t0 * a.H + h;
+    const __nv_bfloat16* gp = (const __nv_bfloat16*)a.g + ch.t0 * a.H + h;
+    const __nv_bfloat16* bp = (const __nv_bfloat16*)a.beta + ch.t0 * a.H + h;
     float x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int i = 2 * (tid & 31) + e;
-      x[e] = i < ch.len ? to_f(g[(long long)i * a.H]) : 0.f;
-      sbeta[i] = i < ch.len ? to_f(b[(long long)i * a.H]) : 0.f;
+      const int i = 2 * lane + e;
+      x[e] = i < ch.len ? to_f(gp[(long long)i * a.H]) : 0.f;
+      sbeta[i] = i < ch.len ? to_f(bp[(long long)i * a.H]) : 0.f;
     }
     float2 s0, s1;
     delta_sums<true>(x[0], x[1], s0, s1);
-    sg[2 * (tid & 31)] = s0;
-    sg[2 * (tid & 31) + 1] = s1;
+    sg[2 * lane] = s0;
+    sg[2 * lane + 1] = s1;
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *slot_tm;
-  // (all threads: each reads K's columns later)
-  bool ok = mbar_wait(bar + 1, 0, a.wait_ns, abort_flag);
-  if (tid == 0 && ok) {
-    const SDesc d0 = sdesc(sb + PrepSmem::P0, 16, 1024, LAYOUT_SW128), d1 = sdesc(sb + PrepSmem::P1, 16, 512, LAYOUT_SW64);
-#pragma unroll
-    for (int kk = 0; kk < 6; ++kk) {
-      const SDesc d = kk < 4 ? d0 + kk * 32u : d1 + (kk - 4) * 32u;
-      umma(tmem, d, d, idesc_bf16(128, 64, 0, 0), kk > 0);
-    }
-    umma_commit(bar);
-  }
-  float2 r[DC / 2];
-  const int i = tid & 63;
-  __syncwarp();
-  if (warp < 4) {
-    ok = ok && mbar_wait(bar, 0, a.wait_ns, abort_flag);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
-      const bool is_k = warp < 2;
-      const float2 gi = sg[i];
-      const float bi = sbeta[i];
-      const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t d[32];
-        tmem_ld32(lane_addr + half * 32u, d);
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          float x[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = half * 32 + j + e;
-            const float2 gj = sg[col];
-            const float w = exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * __uint_as_float(d[j + e]);
-            x[e] = (is_k ? col < i : col <= i) && i < ch.len ? w : 0.f;
-          }
-          r[(half * 32 + j) / 2] = make_float2(x[0], x[1]);
-          r[(half * 32 + j) / 2 + 1] = make_float2(x[2], x[3]);
-          if (is_k)
-            *reinterpret_cast<float4*>(bm + i * MSTR + half * 32 + j) = make_float4(bi * x[0], bi * x[1], bi * x[2], bi * x[3]);
-        }
-      }
-    }
-  }
-  tc_fence_before();
-  const bool gone = __syncthreads_or(!ok);
-  if (warp == 4) {
-    if (gone) {  // (nothing is left in flight: the copy, and the product, if it was issued)
-      mbar_wait_drain(bar + 1, 0, DRAIN_NS, a.err);
+  bool ok = mbar_wait(bar, 0, a.wait_ns, abort_flag);
+  if (__syncthreads_or(!ok)) {
+    if (tid == 0) {
+      raise_error(a.err, ERR_TIMEOUT);
       mbar_wait_drain(bar, 0, DRAIN_NS, a.err);
     }
-    __syncwarp();
-    tc_fence_after();
-    tm_free<64>(tmem);
-  }
-  if (gone) {
-    if (tid == 0) raise_error(a.err, ERR_TIMEOUT);
     return;
   }
-  if (tid < 64) {
+  auto decay = [&](int i, int j) {  // of token j's part in token i
+    const float2 x = sg[i], y = sg[j];
+    return exp2_fast((x.x - y.x) + (x.y - y.y));
+  };
+  // 1: P's rows (those behind the last token may hold another sequence's)
+  float r[4][2][4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (b <= warp) {
+      block_dot(r[b], sb, true, 16 * warp, 16 * b);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 16 * warp + g + 8 * (e >> 1), j = 16 * b + 8 * n + 2 * t + (e & 1);
+          r[b][n][e] = j <= i && i < ch.len ? decay(i, j) * r[b][n][e] : 0.f;
+        }
+    }
+#pragma unroll
+  for (int jb = 0; jb < 4; ++jb) {
+    const int mb = 3 - warp;
+    if (jb > mb) continue;
+    float x[2][4];  // rows j, columns m
+    block_dot(x, sb, false, 16 * jb, 16 * mb);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 16 * jb + g + 8 * (e >> 1), m = 16 * mb + 8 * n + 2 * t + (e & 1);
+        x[n][e] = j < m && m < ch.len ? -sbeta[m] * (decay(m, j) * x[n][e]) : 0.f;
+        if (jb == mb) dm[(mb * 16 + (m & 15)) * 20 + (j & 15)] = x[n][e];
+      }
+    if (jb != mb) {  // rows of x are the operand's columns
+      uint32_t hi[4], lo[4];
+      to_operand(x, hi, lo);
+      uint8_t* const f = frags + 1024 * frag_off(mb, jb) + 16 * lane;
+      *reinterpret_cast<uint4*>(f) = make_uint4(hi[0], hi[2], hi[1], hi[3]);
+      *reinterpret_cast<uint4*>(f + 512) = make_uint4(lo[0], lo[2], lo[1], lo[3]);
+    }
+  }
+  __syncthreads();
+  // 2: warp b, lane i < 16: row i of the inverse of diagonal block b
+  if (lane < 16) {
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) y[j] = j == lane ? 1.f : 0.f;
+#pragma unroll
+    for (int m = 15; m > 0; --m)
+#pragma unroll
+      for (int j = 0; j < m; ++j) y[j] = fmaf(y[m], dm[(warp * 16 + m) * 20 + j], y[j]);
+    __nv_bfloat16* const f = reinterpret_cast<__nv_bfloat16*>(frags + 1024 * frag_diag(warp));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {  // operand element (k = lane, n = j)
+      const int at = (((j & 7) * 4 + ((lane & 7) >> 1)) * 4 + (j >> 3) * 2 + (lane >> 3)) * 2 + (lane & 1);
+      const __nv_bfloat16 x = __float2bfloat16_rn(y[j]);
+      f[at] = x;
+      f[256 + at] = __float2bfloat16_rn(y[j] - __bfloat162float(x));
+    }
+  }
+  if (tid < DC) {
     float* const gt = reinterpret_cast<float*>(ws + W_GT);
     gt[tid] = exp2_fast(sg[tid].x + sg[tid].y);
     gt[DC + tid] = sbeta[tid];
   }
-  const bool is_p = warp == 2 || warp == 3;
-  const int row = is_p ? i : warp == 4 ? 64 + (tid & 31) : tid;  // row of P^, or of K^ (d_k)
-  if (!is_p) {
-    const float2 last = sg[DC - 1];
-#pragma unroll
-    for (int j = 0; j < DC; j += 2) {
-      float x[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t at = row < 64 ? PrepSmem::P0 + sw128(j + e, row >> 3) + (row & 7) * 2
-                                     : PrepSmem::P1 + sw64(j + e, (row - 64) >> 3) + (row & 7) * 2;
-        const float2 gj = sg[j + e];
-        const float k = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(sm + at));
-        x[e] = j + e < ch.len ? exp2_fast((last.x - gj.x) + (last.y - gj.y)) * k : 0.f;
-      }
-      r[j / 2] = make_float2(x[0], x[1]);
-    }
+  __syncthreads();
+  // 3: the rows of P^, then those of K^: two slabs for the warps with short rows of P, one for the others
+  solve_slab(r, warp, frags, sm, ws + W_PH + 2048 * warp, nullptr);
+  const int slab0 = warp < 2 ? 2 * warp : 2 + warp, slabs = warp < 2 ? 2 : 1;
+  for (int x = slab0; x < slab0 + slabs; ++x) {
+    uint32_t raw[4][4];
+    load_transposed(raw, sb, false, 16 * x);
+    transposed_slab(r, raw, ch.len, [&](int j) { return decay(DC - 1, j); });
+    solve_slab(r, 3, frags, sm, ws + W_KD + 2048 * x, ws + W_KD + 12288 + 2048 * x);
   }
-  solve_row(bm, r);
-  uint8_t* const out = ws + (is_p ? W_PH : W_KD) + row * 128;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split2(r[4 * c + e], hi[e], lo[e]);
-    const uint32_t at = (uint32_t)((c ^ (row & 7)) << 4);
-    *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if (!is_p) *reinterpret_cast<uint4*>(out + 12288 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  }
+  if (lane == 0) stores_read();
 }
 
 // ---- scan -----------------------------------------------------------------------------------
@@ -624,7 +715,7 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
                       box_map(&m.q0, a.q, DK, a.H, tokens, 64, DC) && box_map(&m.q1, a.q, DK, a.H, tokens, 32, DC) &&
                       box_map(&m.v, a.v, DV, a.H, tokens, 64, DC) && box_map(&m.o, a.o, DV, a.H, tokens, 32, 32)))
     return cudaErrorInvalidValue;
-  if (a.slots > 0) delta_prep_kernel<<<(unsigned)a.slots * a.H, 160, PrepSmem::BYTES, st>>>(m, a);
+  if (a.slots > 0) delta_prep_kernel<<<(unsigned)a.slots * a.H, PREP_THREADS, PrepSmem::BYTES, st>>>(m, a);
   delta_scan_kernel<<<(unsigned)a.n_seq * a.H * NTILE, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a);
   return cudaGetLastError();
 }
