@@ -8,7 +8,6 @@ cudaError_t launch_delta_decode(const DeltaArgs& a, int dtype_f32, int state_bf1
 cudaError_t launch_slot_plan(const int32_t* new_len, const int32_t* held, const int32_t* seen, int N, int rows, int budget,
                              int32_t* cu, int32_t* slot, int32_t* start, int32_t* row, int32_t* token_seq, int32_t* token_pos,
                              unsigned* err, cudaStream_t st);
-cudaError_t launch_delta_simt_bwd_bf16(const DeltaArgs& a, cudaStream_t stream);
 int check_chunk_sizes(int n_seq, int T, int H, int dk, int dv, int dtype, const int32_t* cu_seqlens, long long* tokens);
 }  // namespace gla
 
@@ -18,20 +17,23 @@ bool off16(const void* p) { return ((uintptr_t)p & 15u) != 0; }
 bool off4(const void* p) { return ((uintptr_t)p & 3u) != 0; }
 int status_of(cudaError_t e) { return e == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH; }
 
-// Sizes of a chunked call; chunk places and CTAs stay below 2^31.
+// Sizes of a chunked call; the states of all chunk places, in rows, stay below 2^31 (and so do CTAs).
 int check_sizes(int n_seq, int T, int H, int dk, int dv, int dtype, const int32_t* cu, long long* tokens, int* slots) {
   const int rc = gla::check_chunk_sizes(n_seq, T, H, dk, dv, dtype, cu, tokens);
   if (rc) return rc;
   const long long s = gla::delta_slots(n_seq, T, cu != nullptr);
-  if (s * H >= (1ll << 31)) return GLA_ERR_SHAPE;
+  if (s * H * GLA_DK >= (1ll << 31)) return GLA_ERR_SHAPE;
   *slots = (int)s;
   return GLA_OK;
 }
 
+// The workspace's first 256-byte boundary (the sizes have room for it).
+uint8_t* ws_start(void* p) { return (uint8_t*)(((uintptr_t)p + 255) & ~(uintptr_t)255); }
+
 size_t ws_bytes_of(int n_seq, int T, int H, bool packed, bool bwd, int dtype) {
   if (n_seq < 0 || T < 0 || H < 1) return 0;
   const long long tokens = packed ? (long long)T : (long long)n_seq * T, slots = gla::delta_slots(n_seq, T, packed);
-  return 256 + (dtype == GLA_BF16 && !bwd ? gla::delta_tc_ws_bytes(slots, H) : gla::delta_simt_ws_bytes(slots, tokens, H, bwd));
+  return 256 + (dtype == GLA_BF16 ? gla::delta_tc_ws_bytes(slots, tokens, H, bwd) : gla::delta_simt_ws_bytes(slots, tokens, H, bwd));
 }
 
 }  // namespace
@@ -82,7 +84,7 @@ int gla_delta_fwd(const void* q, const void* k, const void* v, const void* g, co
   a.n_seq = n_seq;
   a.T = T;
   a.H = H;
-  a.ws = (uint8_t*)workspace;
+  a.ws = ws_start(workspace);
   cudaStream_t st = (cudaStream_t)stream;
   return status_of(dtype == GLA_F32 ? gla::launch_delta_simt_fwd(a, st) : gla::launch_delta_tc_fwd(a, st));
 }
@@ -126,9 +128,9 @@ int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, co
   a.n_seq = n_seq;
   a.T = T;
   a.H = H;
-  a.ws = (uint8_t*)workspace;
+  a.ws = ws_start(workspace);
   cudaStream_t st = (cudaStream_t)stream;
-  return status_of(dtype == GLA_F32 ? gla::launch_delta_simt_bwd(a, st) : gla::launch_delta_simt_bwd_bf16(a, st));
+  return status_of(dtype == GLA_F32 ? gla::launch_delta_simt_bwd(a, st) : gla::launch_delta_tc_bwd(a, st));
 }
 
 static int delta_decode(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale, void* state,

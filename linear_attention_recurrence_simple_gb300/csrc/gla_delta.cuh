@@ -157,7 +157,8 @@ int current_device_state(unsigned** err, unsigned long long* wait_ns);
 cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t stream);
 cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t stream);
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t stream);
-size_t delta_tc_ws_bytes(long long slots, int H);
+cudaError_t launch_delta_tc_bwd(const DeltaArgs& a, cudaStream_t stream);
+size_t delta_tc_ws_bytes(long long slots, long long tokens, int H, bool bwd);
 size_t delta_simt_ws_bytes(long long slots, long long tokens, int H, bool bwd);
 
 }  // namespace gla

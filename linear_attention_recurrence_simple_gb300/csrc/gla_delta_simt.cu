@@ -465,7 +465,5 @@ static cudaError_t simt_bwd(const DeltaArgs& a, cudaStream_t st) {
 
 cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t st) { return simt_fwd<float>(a, st); }
 cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t st) { return simt_bwd<float>(a, st); }
-// (first form of the bf16 calls)
-cudaError_t launch_delta_simt_bwd_bf16(const DeltaArgs& a, cudaStream_t st) { return simt_bwd<__nv_bfloat16>(a, st); }
 
 }  // namespace gla

@@ -100,6 +100,12 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
@@ -120,6 +126,16 @@ __device__ __forceinline__ void tm_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&r
       : "memory");
 #undef R4
 }
+// 16 columns of this thread's lane.
+__device__ __forceinline__ void tm_ld16(uint32_t ta, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(ta)
+      : "memory");
+}
 template <int COLS>
 __device__ __forceinline__ void tm_alloc(uint32_t* slot) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(COLS));
@@ -137,8 +153,11 @@ constexpr unsigned long long DRAIN_NS = 1000000000ull;
 
 // Tensor maps of a call.  K and Q: a chunk's 64 rows in two boxes, columns 0-63 (128-byte rows) and 64-95 (64-byte
 // rows).  V: 64 rows x 64 columns.  O: 32 rows x 32 columns, one a warp.
+// (backward) dO: 64 rows x 64 columns; K and Q in two boxes of 64 columns (96 on: zeros); dv as dO; X, S0 and dS1 of the
+// workspace: 64 or 96 rows x 64 columns of a (chunk place, head).
 struct DeltaMaps {
   CUtensorMap k0, k1, q0, q1, v, o;
+  CUtensorMap dO, dv, x, s0, ds;
 };
 __device__ __forceinline__ void load_kq(const DeltaMaps& m, uint32_t p0, uint32_t p1, uint64_t* bar, int h, int t) {
   mbar_expect_tx(bar, 24576);
@@ -149,10 +168,17 @@ __device__ __forceinline__ void load_kq(const DeltaMaps& m, uint32_t p0, uint32_
 }
 
 // ---- workspace of a (chunk place, head), in bytes --------------------------------------------
-// K^ hi and lo: 96 rows (d_k) x 64 tokens; P^: 64 rows x 64 tokens; as the swizzled tiles that the scan copies.
-constexpr uint32_t W_KD = 0, W_PH = 24576, W_OP = 32768;  // (one copy of W_OP bytes)
-constexpr uint32_t W_GT = 32768;                          // e^G, beta: fp32 [64] each
+// Operands as the swizzled tiles that the scans copy, 128-byte rows of 64 tokens: K^ hi and lo (96 rows, d_k), P^ or
+// (backward) Z (64 rows).  Then e^G, beta and (backward) e^(G_C - G), fp32 [64] each, and the sums of the logs to
+// base 2.
+constexpr uint32_t W_KD = 0, W_PH = 24576, W_OP = 32768, W_GT = W_OP;
 constexpr uint32_t W_FWD = W_GT + 512;
+enum { GT_F = 0, GT_B = DC, GT_E = 2 * DC, GT_SUM = 3 * DC };  // in floats
+// Backward: K~ = -(diag(e^G) K)^T (1 + B M^T)^-1 and Q~ = s (diag(e^G) Q)^T, hi and lo, P hi and lo; then what the
+// scans leave for the gradients, bf16 rows of 192: S0 and dS1 (96), X (64).
+constexpr uint32_t W_KR = W_GT + 1280, W_QT = W_KR + 24576, W_P = W_QT + 24576, W_S0 = W_P + 16384, W_DS = W_S0 + DK * DV * 2,
+                   W_X = W_DS + DK * DV * 2, W_BWD = W_X + DC * DV * 2;
+static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_S0 % 32 == 0, "copies and tensor maps");
 
 // ---- prep -------------------------------------------------------------------------------------
 // One CTA of 4 warps a (chunk, head), all products on mma.sync (m16n8k16): the blocks are 16 wide and each step
@@ -165,10 +191,12 @@ constexpr uint32_t W_FWD = W_GT + 512;
 // fp32 sums; what is carried from block to block has 16 bits.
 constexpr int PREP_THREADS = 128;
 struct PrepSmem {
-  static constexpr uint32_t P0 = 0, P1 = 16384, STAGE = 24576, DM = STAGE, FRAG = STAGE + 4 * 4096, G = FRAG + 10 * 1024, B = G + DC * 8,
-                            BAR = B + DC * 4, BYTES = BAR + 16;
+  static constexpr uint32_t P0 = 0, P1 = 16384, STAGE = 24576, DM = STAGE, G = STAGE + 4 * 4096, B = G + DC * 8, BAR = B + DC * 4,
+                            FRAG = BAR + 256;
+  static constexpr uint32_t bytes(bool bwd) { return FRAG + (bwd ? 20 : 10) * 1024; }
 };
-static_assert(4 * 16 * 20 * 4 <= 4 * 4096, "the diagonal blocks take the stages' place");
+constexpr int DM_FLOATS = 4 * 16 * 20;
+static_assert(2 * DM_FLOATS * 4 <= 4 * 4096, "the diagonal blocks take the stages' place");
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -214,31 +242,40 @@ __device__ __forceinline__ void block_mul(float (&d)[2][4], const uint32_t (&hi)
   mma(d[0], hi, h.x, h.y);
   mma(d[1], hi, h.z, h.w);
 }
-// Places of the B operands: -(B M) block (c, b), c > b, and the inverse of diagonal block b.
+// Places of the B operands: -(B M) block (c, b), c > b, and the inverse of diagonal block b; from 10 on the same of
+// (B M^T): block (b, c), b < c, and the inverse.
 __device__ __forceinline__ constexpr int frag_off(int c, int b) { return c * (c - 1) / 2 + b; }
 __device__ __forceinline__ constexpr int frag_diag(int b) { return 6 + b; }
 
-// A slab's rows, blocks `top` .. 0 (the ones above are zero in r): solved, and copied out (128-byte rows; with
-// `lo_out` what the rounding to bf16 leaves, too).
-__device__ __forceinline__ void solve_slab(float (&r)[4][2][4], int top, const uint8_t* frags, uint8_t* sm, uint8_t* hi_out, uint8_t* lo_out) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint8_t* const stage = sm + PrepSmem::STAGE + 4096 * (threadIdx.x >> 5);
+struct Slab {  // 16 rows x 64 columns as A operands, hi and lo
   uint32_t hi[4][4], lo[4][4];
+};
+// Rows r, of which blocks up to `top` are not zero, times (1 + B M)^-1, or (UP) (1 + B M^T)^-1 (top = 3).
+template <bool UP>
+__device__ __forceinline__ void solve_slab(float (&r)[4][2][4], int top, const uint8_t* frags, Slab& s) {
 #pragma unroll
-  for (int b = 3; b >= 0; --b) {
+  for (int step = 0; step < 4; ++step) {
+    const int b = UP ? step : 3 - step;
     if (b <= top) {
 #pragma unroll
-      for (int c = 3; c > b; --c)
-        if (c <= top) block_mul(r[b], hi[c], lo[c], frags + 1024 * frag_off(c, b));
-      to_operand(r[b], hi[b], lo[b]);
+      for (int before = 0; before < step; ++before) {
+        const int c = UP ? before : 3 - before;
+        if (c <= top) block_mul(r[b], s.hi[c], s.lo[c], frags + 1024 * (UP ? 10 + frag_off(b, c) : frag_off(c, b)));
+      }
+      to_operand(r[b], s.hi[b], s.lo[b]);
       float y[2][4] = {};
-      block_mul(y, hi[b], lo[b], frags + 1024 * frag_diag(b));
-      to_operand(y, hi[b], lo[b]);
+      block_mul(y, s.hi[b], s.lo[b], frags + 1024 * ((UP ? 10 : 0) + frag_diag(b)));
+      to_operand(y, s.hi[b], s.lo[b]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) hi[b][i] = lo[b][i] = 0u;
+      for (int i = 0; i < 4; ++i) s.hi[b][i] = s.lo[b][i] = 0u;
     }
   }
+}
+// A slab's rows, copied out: 128-byte rows, with `lo_out` what the rounding to bf16 leaves, too.
+__device__ __forceinline__ void store_slab(const Slab& s, uint8_t* sm, uint8_t* hi_out, uint8_t* lo_out) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* const stage = sm + PrepSmem::STAGE + 4096 * (threadIdx.x >> 5);
   if (lane == 0) stores_read();
   __syncwarp();
 #pragma unroll
@@ -246,8 +283,8 @@ __device__ __forceinline__ void solve_slab(float (&r)[4][2][4], int top, const u
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // rows g, g + 8; columns 16 b + 2 t, and 8 on
       const uint32_t at = sw128(g + 8 * (i & 1), 2 * b + (i >> 1)) + 4 * t;
-      *reinterpret_cast<uint32_t*>(stage + at) = hi[b][i];
-      *reinterpret_cast<uint32_t*>(stage + 2048 + at) = lo[b][i];
+      *reinterpret_cast<uint32_t*>(stage + at) = s.hi[b][i];
+      *reinterpret_cast<uint32_t*>(stage + 2048 + at) = s.lo[b][i];
     }
   fence_async_smem();
   __syncwarp();
@@ -281,10 +318,11 @@ __device__ __forceinline__ void load_transposed(uint32_t (&raw)[4][4], uint32_t 
   for (int b = 0; b < 4; ++b) ldsm4t(raw[b], kq_at(sb, is_q, 16 * b + 8 * (lane >> 4) + (lane & 7), a0 / 8 + ((lane >> 3) & 1)));
 }
 
-__global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
+template <bool BWD>
+__global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
-  float* const dm = reinterpret_cast<float*>(sm + PrepSmem::DM);   // [4][16][20]: diagonal blocks of B M
+  float* const dm = reinterpret_cast<float*>(sm + PrepSmem::DM);   // [4][16][20]: diagonal blocks of B M, and of B M^T
   uint8_t* const frags = sm + PrepSmem::FRAG;
   float2* const sg = reinterpret_cast<float2*>(sm + PrepSmem::G);  // sums of log2 decays
   float* const sbeta = reinterpret_cast<float*>(sm + PrepSmem::B);
@@ -293,7 +331,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
   const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const DeltaChunk ch = chunk_of_slot(a, slot);
   if (ch.len == 0) return;
-  uint8_t* const ws = a.ws + ((long long)slot * a.H + h) * W_FWD;
+  uint8_t* const ws = a.ws + ((long long)slot * a.H + h) * (BWD ? W_BWD : W_FWD);
   if (tid == 0) {
     mbar_init(bar, 1);
     *abort_flag = 0;
@@ -329,6 +367,8 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
     const float2 x = sg[i], y = sg[j];
     return exp2_fast((x.x - y.x) + (x.y - y.y));
   };
+  // What the block's second triangle gives (B M^T's operands) stands behind the first's.
+  Slab out;
   // 1: P's rows (those behind the last token may hold another sequence's)
   float r[4][2][4];
 #pragma unroll
@@ -343,6 +383,39 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
           r[b][n][e] = j <= i && i < ch.len ? decay(i, j) * r[b][n][e] : 0.f;
         }
     }
+  if constexpr (BWD) {
+    // P as it is; then the rows of M, which are also -(B M^T)'s columns
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (b > warp) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[b][i >> 2][i & 3] = 0.f;
+      }
+      to_operand(r[b], out.hi[b], out.lo[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (b <= warp) {
+        float x[2][4];
+        block_dot(r[b], sb, false, 16 * warp, 16 * b);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 16 * warp + g + 8 * (e >> 1), j = 16 * b + 8 * n + 2 * t + (e & 1);
+            r[b][n][e] = j < i && i < ch.len ? decay(i, j) * r[b][n][e] : 0.f;
+            x[n][e] = -sbeta[j] * r[b][n][e];
+            if (b == warp) dm[DM_FLOATS + (b * 16 + (j & 15)) * 20 + (i & 15)] = x[n][e];
+          }
+        if (b != warp) {
+          uint32_t hi[4], lo[4];
+          to_operand(x, hi, lo);
+          uint8_t* const f = frags + 1024 * (10 + frag_off(warp, b)) + 16 * lane;
+          *reinterpret_cast<uint4*>(f) = make_uint4(hi[0], hi[2], hi[1], hi[3]);
+          *reinterpret_cast<uint4*>(f + 512) = make_uint4(lo[0], lo[2], lo[1], lo[3]);
+        }
+      }
+  }
 #pragma unroll
   for (int jb = 0; jb < 4; ++jb) {
     const int mb = 3 - warp;
@@ -366,38 +439,71 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
     }
   }
   __syncthreads();
-  // 2: warp b, lane i < 16: row i of the inverse of diagonal block b
-  if (lane < 16) {
+  // 2: warp b, lane i < 16: row i of the inverse of diagonal block b (lanes 16 on: of B M^T's)
+  if (lane < (BWD ? 32 : 16)) {
+    const bool up = lane >= 16;
+    const int i = lane & 15;
+    const float* const x = dm + (up ? DM_FLOATS : 0) + warp * 320;
     float y[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] = j == lane ? 1.f : 0.f;
+    for (int j = 0; j < 16; ++j) y[j] = j == i ? 1.f : 0.f;
+    if (!up) {
 #pragma unroll
-    for (int m = 15; m > 0; --m)
+      for (int m = 15; m > 0; --m)
 #pragma unroll
-      for (int j = 0; j < m; ++j) y[j] = fmaf(y[m], dm[(warp * 16 + m) * 20 + j], y[j]);
-    __nv_bfloat16* const f = reinterpret_cast<__nv_bfloat16*>(frags + 1024 * frag_diag(warp));
+        for (int j = 0; j < m; ++j) y[j] = fmaf(y[m], x[m * 20 + j], y[j]);
+    } else if (BWD) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {  // operand element (k = lane, n = j)
-      const int at = (((j & 7) * 4 + ((lane & 7) >> 1)) * 4 + (j >> 3) * 2 + (lane >> 3)) * 2 + (lane & 1);
-      const __nv_bfloat16 x = __float2bfloat16_rn(y[j]);
-      f[at] = x;
-      f[256 + at] = __float2bfloat16_rn(y[j] - __bfloat162float(x));
+      for (int m = 0; m < 15; ++m)
+#pragma unroll
+        for (int j = m + 1; j < 16; ++j) y[j] = fmaf(y[m], x[m * 20 + j], y[j]);
+    }
+    __nv_bfloat16* const f = reinterpret_cast<__nv_bfloat16*>(frags + 1024 * ((up ? 10 : 0) + frag_diag(warp)));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {  // operand element (k = i, n = j)
+      const int at = (((j & 7) * 4 + ((i & 7) >> 1)) * 4 + (j >> 3) * 2 + (i >> 3)) * 2 + (i & 1);
+      const __nv_bfloat16 v = __float2bfloat16_rn(y[j]);
+      f[at] = v;
+      f[256 + at] = __float2bfloat16_rn(y[j] - __bfloat162float(v));
     }
   }
   if (tid < DC) {
     float* const gt = reinterpret_cast<float*>(ws + W_GT);
-    gt[tid] = exp2_fast(sg[tid].x + sg[tid].y);
-    gt[DC + tid] = sbeta[tid];
+    gt[GT_F + tid] = exp2_fast(sg[tid].x + sg[tid].y);
+    gt[GT_B + tid] = sbeta[tid];
+    if (BWD) {
+      gt[GT_E + tid] = decay(DC - 1, tid);
+      reinterpret_cast<float2*>(gt + GT_SUM)[tid] = sg[tid];
+    }
   }
   __syncthreads();
-  // 3: the rows of P^, then those of K^: two slabs for the warps with short rows of P, one for the others
-  solve_slab(r, warp, frags, sm, ws + W_PH + 2048 * warp, nullptr);
+  // 3: the rows of P^ (Z), then those of K^: two slabs for the warps with short rows of P, one for the others;
+  // of K~ and Q~ the other way round
+  if (BWD) store_slab(out, sm, ws + W_P + 2048 * warp, ws + W_P + 8192 + 2048 * warp);
+  solve_slab<false>(r, warp, frags, out);
+  store_slab(out, sm, ws + W_PH + 2048 * warp, nullptr);
+  uint32_t raw[4][4];
   const int slab0 = warp < 2 ? 2 * warp : 2 + warp, slabs = warp < 2 ? 2 : 1;
   for (int x = slab0; x < slab0 + slabs; ++x) {
-    uint32_t raw[4][4];
     load_transposed(raw, sb, false, 16 * x);
     transposed_slab(r, raw, ch.len, [&](int j) { return decay(DC - 1, j); });
-    solve_slab(r, 3, frags, sm, ws + W_KD + 2048 * x, ws + W_KD + 12288 + 2048 * x);
+    solve_slab<false>(r, 3, frags, out);
+    store_slab(out, sm, ws + W_KD + 2048 * x, ws + W_KD + 12288 + 2048 * x);
+  }
+  if constexpr (BWD) {
+    const int up0 = warp < 2 ? warp : 2 * warp - 2;
+    auto from_start = [&](int j) { return exp2_fast(sg[j].x + sg[j].y); };
+    for (int x = up0; x < up0 + 3 - slabs; ++x) {
+      load_transposed(raw, sb, false, 16 * x);
+      transposed_slab(r, raw, ch.len, [&](int j) { return -from_start(j); });
+      solve_slab<true>(r, 3, frags, out);
+      store_slab(out, sm, ws + W_KR + 2048 * x, ws + W_KR + 12288 + 2048 * x);
+      load_transposed(raw, sb, true, 16 * x);
+      transposed_slab(r, raw, ch.len, [&](int j) { return a.scale * from_start(j); });
+#pragma unroll
+      for (int b = 0; b < 4; ++b) to_operand(r[b], out.hi[b], out.lo[b]);
+      store_slab(out, sm, ws + W_QT + 2048 * x, ws + W_QT + 12288 + 2048 * x);
+    }
   }
   if (lane == 0) stores_read();
 }
@@ -410,6 +516,8 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
 // K^ B R the other; the next chunk has them the other way round, so that only the state's way (product, residual,
 // product, state) is waited for and the outputs are written while the next chunk's first product runs.
 // Warps 3 and 7, which have no state rows, have the issuing threads: of the copies and of the products.
+// STATES (the backward's forward pass): K's rows stand in 64-127 and rows 0-63 are not looked at; Z is in P^'s place,
+// X = R - Z B R and every chunk's S0 go to the workspace instead of outputs.
 constexpr int TN = 64, NTILE = DV / TN, SCAN_THREADS = 256, ISSUER = 224, LOADER = 96;
 struct ScanSmem {
   static constexpr uint32_t KQ0 = 0, KQ1 = 16384, OP = 24576, S = OP + W_OP, BR = S + 24576, V = BR + 16384, OUT = V + 8192,
@@ -418,6 +526,7 @@ struct ScanSmem {
 };
 enum { SB_A = 0, SB_C, SB_O, SB_KQ, SB_V, SB_KD, SB_PH, SB_DRAIN, SB_N };
 
+template <bool STATES>
 __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
@@ -429,17 +538,24 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   const int row = (tid & 31) + 32 * q;  // lane of the products
   const int tok = row & 63;
   const int col0 = tile * TN + 32 * half;
-  const bool k_row = q < 2, s_row = q < 3, issuer = tid == ISSUER, loader = tid == LOADER;
+  const bool r_row = STATES == (q >= 2), o_row = q >= 2, s_row = q < 3, issuer = tid == ISSUER, loader = tid == LOADER;
   const DeltaSeq s = delta_seq(a, n);
   const int nc = (s.len + DC - 1) / DC;
   const int from = a.h0 ? delta_row(a.h0_row, a.h0_rows, n, a.err) : -1;
 
-  auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * W_FWD; };
+  auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * (STATES ? W_BWD : W_FWD); };
   // (the loader) a chunk's operands, each as soon as the chunk before is done with their place
   int loads[4] = {};
   auto load_rows = [&](int c) {
     ++loads[0];
-    load_kq(maps, sb + ScanSmem::KQ0, sb + ScanSmem::KQ1, &bar[SB_KQ], h, (int)(s.begin + (long long)c * DC));
+    const int t = (int)(s.begin + (long long)c * DC);
+    if (STATES) {
+      mbar_expect_tx(&bar[SB_KQ], 12288);
+      box_load(sb + ScanSmem::KQ0 + 8192, &maps.k0, &bar[SB_KQ], 0, h, t);
+      box_load(sb + ScanSmem::KQ1 + 4096, &maps.k1, &bar[SB_KQ], 64, h, t);
+    } else {
+      load_kq(maps, sb + ScanSmem::KQ0, sb + ScanSmem::KQ1, &bar[SB_KQ], h, t);
+    }
   };
   auto load_v = [&](int c) {
     ++loads[1];
@@ -461,9 +577,11 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   auto prefetch = [&](int c) {
     const int t = (int)(s.begin + (long long)c * DC);
     box_prefetch(&maps.k0, 0, h, t);
-    box_prefetch(&maps.q0, 0, h, t);
     box_prefetch(&maps.k1, 64, h, t);
-    box_prefetch(&maps.q1, 64, h, t);
+    if (!STATES) {
+      box_prefetch(&maps.q0, 0, h, t);
+      box_prefetch(&maps.q1, 64, h, t);
+    }
     box_prefetch(&maps.v, tile * TN, h, t);
     bulk_prefetch(ws_of(c), W_FWD);
   };
@@ -480,16 +598,18 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
       S[2 * x + 1] = make_float2(w.z, w.w);
     }
   }
-  auto put_state = [&](int x) {  // hi and lo of 16 columns of the state row, the next product's operand
+  // hi and lo of 16 columns of the state row, the operand of chunk c's product
+  auto put_state = [&](int x, [[maybe_unused]] int c) {
+    uint32_t hi[8], lo[8];
 #pragma unroll
-    for (int c = 2 * x; c < 2 * x + 2; ++c) {
-      uint32_t hi[4], lo[4];
+    for (int e = 0; e < 8; ++e) split2(S[8 * x + e], hi[e], lo[e]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split2(S[4 * c + e], hi[e], lo[e]);
-      const uint32_t at = sb + ScanSmem::S + sw128(row, 4 * half + c);
-      st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-      st_shared_v4(at + 12288, lo[0], lo[1], lo[2], lo[3]);
+    for (int p = 0; p < 2; ++p) {
+      const uint32_t at = sb + ScanSmem::S + sw128(row, 4 * half + 2 * x + p);
+      st_shared_v4(at, hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+      st_shared_v4(at + 12288, lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
     }
+    if (STATES) st_global_v8(ws_of(c) + W_S0 + (row * DV + col0 + 16 * x) * 2, hi);
   };
   if (nc > 0) {
     if (warp == 0) tm_alloc<256>(slot_tm);
@@ -505,17 +625,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
       if (nc > 1) prefetch(1);
     }
     if (s_row) {
-      put_state(0);
-      put_state(1);
+      put_state(0, 0);
+      put_state(1, 0);
     }
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
     const uint32_t tmem = *slot_tm;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    float2 qs[16];
+    float2 keep[16];  // e^G Q S0, or (STATES) R
     bool ok = true;
-    // The outputs of chunk c (Q's warps), from the place that its first product had.
+    // The outputs of chunk c (rows 64-127), from the place that its first product had.
     const uint32_t stage = sb + ScanSmem::OUT + 2048u * ((q & 1) + 2 * half);  // this warp's 32 rows x 32 columns
     auto outputs = [&](int c) {
       ok = mbar_wait(&bar[SB_O], c & 1, a.wait_ns, abort_flag);
@@ -534,10 +654,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         tm_ld16x2(from_tm + 16 * x, from_tm + 64 + 16 * x, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 y = fmul2(both(a.scale), fadd2(qs[8 * x + e], halves(d, e)));
+          const float2 y = STATES ? fsub2(keep[8 * x + e], halves(d, e)) : fmul2(both(a.scale), fadd2(keep[8 * x + e], halves(d, e)));
           w[e] = bf2(y.x, y.y);
         }
-        if (left >= DC) {
+        if (STATES) {  // (zeros behind the last token, as its R)
+          st_global_v8(ws_of(c) + W_X + (tok * DV + col0 + 16 * x) * 2, w);
+        } else if (left >= DC) {
           st_shared_v4(stage + sw64(tid & 31, 2 * x), w[0], w[1], w[2], w[3]);
           st_shared_v4(stage + sw64(tid & 31, 2 * x + 1), w[4], w[5], w[6], w[7]);
         } else if (tok < left) {  // a sequence's last rows: no box is written past them
@@ -546,7 +668,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
-      if (left >= DC) {
+      if (!STATES && left >= DC) {
         fence_async_smem();
         __syncwarp();
         if ((tid & 31) == 0) box_store(&maps.o, stage, col0, h, (int)(t0 + 32 * (q & 1)));
@@ -566,7 +688,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
       }
       __syncwarp();
       ok = true;
-      if (!k_row && c > 0) outputs(c - 1);
+      if (o_row && c > 0) outputs(c - 1);
       ok = ok && mbar_wait(&bar[SB_V], ph, a.wait_ns, abort_flag) && mbar_wait(&bar[SB_A], ph, a.wait_ns, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       float last = 0.f;
@@ -581,7 +703,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         for (int x = 0; x < 2; ++x) {
           uint32_t d[32];
           tm_ld16x2(at_a + lanes + 32 * half + 16 * x, at_a + lanes + 64 + 32 * half + 16 * x, d);
-          if (k_row) {
+          if (r_row) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const uint32_t piece = sw128(tok, 4 * half + 2 * x + p);
@@ -590,15 +712,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float2 r = fmul2(both(b_row), fmadd2(both(-f_row), halves(d, 4 * p + e), widen2(vw[e])));
-                split2(live ? r : both(0.f), hi[e], lo[e]);
+                float2 r = fmadd2(both(-f_row), halves(d, 4 * p + e), widen2(vw[e]));
+                r = live ? r : both(0.f);
+                if (STATES) keep[8 * x + 4 * p + e] = r;
+                split2(fmul2(both(b_row), r), hi[e], lo[e]);
               }
               st_shared_v4(sb + ScanSmem::BR + piece, hi[0], hi[1], hi[2], hi[3]);
               st_shared_v4(sb + ScanSmem::BR + 8192 + piece, lo[0], lo[1], lo[2], lo[3]);
             }
-          } else {
+          } else if (!STATES) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) qs[8 * x + e] = fmul2(both(f_row), halves(d, e));
+            for (int e = 0; e < 8; ++e) keep[8 * x + e] = fmul2(both(f_row), halves(d, e));
           }
         }
       }
@@ -636,7 +760,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           tm_ld16x2(at_c + lanes + 32 * half + 16 * x, at_c + lanes + 64 + 32 * half + 16 * x, d);
 #pragma unroll
           for (int e = 0; e < 8; ++e) S[8 * x + e] = fmadd2(both(last), S[8 * x + e], halves(d, e));
-          if (c + 1 < nc) put_state(x);
+          if (c + 1 < nc) put_state(x, c + 1);
         }
       }
       fence_async_smem();
@@ -645,8 +769,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
     }
     bool gone = c < nc;
     ok = true;
-    if (!gone && !k_row) outputs(nc - 1);
-    if (!k_row && (tid & 31) == 0) stores_read();
+    if (!gone && o_row) outputs(nc - 1);
+    if (o_row && (tid & 31) == 0) stores_read();
     tc_fence_before();
     gone = __syncthreads_or(gone || !ok);
     if (gone) {
@@ -667,7 +791,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
     }
     if (gone) return;
   }
-  if (a.hT && s_row) {
+  if (!STATES && a.hT && s_row) {
     const int to = delta_row(a.hT_row, a.hT_rows, n, a.err);
     if (to >= 0) {
       float4* dst = reinterpret_cast<float4*>(a.hT + (((long long)to * a.H + h) * DK + row) * DV + col0);
@@ -677,15 +801,618 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   }
 }
 
+// ---- reverse scan ---------------------------------------------------------------------------
+// One CTA a (sequence, head, 64 columns of d_v), chunks from the last: with dS1 = dL/dS1 of the chunk,
+//     dU = s P^T dO + diag(E) K dS1,   w = B dU,   dS0 = e^(G_C) dS1 + Q~ dO + K~ w,   dv = B (dU - Z^T w)
+// (E = e^(G_C - G)): again two dependent products a chunk.  P^T dO and Q~ dO need no state and are issued a chunk
+// ahead.  dbeta's part of the CTA's columns is (dU - Z^T w) . X.
+// 320 threads, one CTA an SM (the operands take 190 KB): warps 0-7 as in the scan (rows 0-63: tokens; 0-95: the
+// state), warp 8 issues the products, warp 9 the copies; every hand-over through an mbarrier.
+// Tensor memory: P^T dO [0,64), Q~ dO [64,192) (by chunk parity), K dS1 [192,320) and K~ w [320,448) as [hi | lo],
+// Z^T w [448,512).
+constexpr int RSCAN_THREADS = 320;
+struct RSmem {
+  // of the chunk ahead (two places): Q~ hi, lo; P hi, lo; dO
+  static constexpr uint32_t EARLY = 0, E_QT = 0, E_P = 24576, E_DO = 40960, E_BYTES = 49152;
+  // K~ hi, lo and Z; K; the state; w; two places of e^G, beta, E.  Products of 128 rows read past operands of 64 and 96
+  // rows; what stands there is either as still as the operand or (8 KB behind Z, behind K) never written, and the
+  // rows it gives are not looked at.
+  static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 16384, S = K1 + 8192, W = S + 24576, GT = W + 16384,
+                            BAR = GT + 2 * 768, BYTES = BAR + 192;
+  static_assert(BYTES <= 232448, "shared memory");
+};
+// (A warp that waits for a phase has to get there before the phase after next: each is tied to something that the warp
+// itself hands over later, K's to nothing that warps 0-7 do, so the decays that come with it have barriers of their own.)
+enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_ZF, RB_DRAIN, RB_GT, RB_N = RB_GT + 2 };
+constexpr uint32_t RT_P = 0, RT_Q = 64, RT_A = 192, RT_C = 320, RT_Z = 448;
+
+__global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, float* dbeta_part) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + RSmem::BAR);
+  uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + RSmem::BAR + 8 * RB_N);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + RSmem::BAR + 8 * RB_N + 4);
+  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = nh / a.H;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = (warp >> 2) & 1;
+  const int row = lane + 32 * q, col0 = tile * TN + 32 * half;
+  const bool t_row = warp < 8 && q < 2, s_row = warp < 8 && q < 3;
+  const DeltaSeq s = delta_seq(a, n);
+  const int nc = (s.len + DC - 1) / DC;
+  const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
+  auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * W_BWD; };
+
+  float2 S[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) S[x] = both(0.f);
+  if (s_row && a.dhT) {
+    const float4* src = reinterpret_cast<const float4*>(a.dhT + (((long long)n * a.H + h) * DK + row) * DV + col0);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float4 w = src[x];
+      S[2 * x] = make_float2(w.x, w.y);
+      S[2 * x + 1] = make_float2(w.z, w.w);
+    }
+  }
+  if (nc > 0) {
+    if (warp == 9) {
+      tm_alloc<512>(slot_tm);
+      if (lane == 0) {
+        for (int x = 0; x < RB_N; ++x) mbar_init(&bar[x], x == RB_SR ? 192 : x == RB_WR || x == RB_ZF ? 128 : 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot_tm;
+    auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
+    bool ok = true;
+    if (warp == 9) {
+      if (lane == 0) {
+        // copies: each as soon as what stood in its place has been used
+        int loads[4] = {};  // EARLY's two places, K, K~
+        auto load_early = [&](int it) {
+          const int c = nc - 1 - it, p = it & 1;
+          const uint32_t to = sb + RSmem::EARLY + p * RSmem::E_BYTES;
+          ++loads[p];
+          mbar_expect_tx(&bar[RB_EF + p], RSmem::E_BYTES);
+          bulk_load(to + RSmem::E_QT, ws_of(c) + W_QT, 24576, &bar[RB_EF + p]);
+          bulk_load(to + RSmem::E_P, ws_of(c) + W_P, 16384, &bar[RB_EF + p]);
+          box_load(to + RSmem::E_DO, &maps.dO, &bar[RB_EF + p], tile * TN, h, (int)(s.begin + (long long)c * DC));
+        };
+        auto load_k = [&](int it) {
+          const int c = nc - 1 - it, t = (int)(s.begin + (long long)c * DC);
+          ++loads[2];
+          mbar_expect_tx(&bar[RB_K], 12288);
+          mbar_expect_tx(&bar[RB_GT + (it & 1)], 768);
+          box_load(sb + RSmem::K0, &maps.k0, &bar[RB_K], 0, h, t);
+          box_load(sb + RSmem::K1, &maps.k1, &bar[RB_K], 64, h, t);
+          bulk_load(sb + RSmem::GT + (it & 1) * 768, ws_of(c) + W_GT, 768, &bar[RB_GT + (it & 1)]);
+        };
+        auto load_kr = [&](int it) {
+          const int c = nc - 1 - it;
+          ++loads[3];
+          mbar_expect_tx(&bar[RB_KR], 32768);
+          bulk_load(sb + RSmem::KR, ws_of(c) + W_KR, 24576, &bar[RB_KR]);
+          bulk_load(sb + RSmem::KR + 24576, ws_of(c) + W_PH, 8192, &bar[RB_KR]);
+        };
+        auto prefetch = [&](int it) {
+          const int c = nc - 1 - it, t = (int)(s.begin + (long long)c * DC);
+          box_prefetch(&maps.k0, 0, h, t);
+          box_prefetch(&maps.k1, 64, h, t);
+          box_prefetch(&maps.dO, tile * TN, h, t);
+          bulk_prefetch(ws_of(c) + W_PH, 8192 + 1280);
+          bulk_prefetch(ws_of(c) + W_KR, 24576 + 24576 + 16384);
+        };
+        load_early(0);
+        load_k(0);
+        load_kr(0);
+        if (nc > 1) load_early(1);
+        for (int it = 0; it < nc && ok; ++it) {
+          if (it + 2 < nc) prefetch(it + 2);
+          ok = wait(RB_E + (it & 1), it >> 1);
+          if (ok && it + 2 < nc) load_early(it + 2);
+          ok = ok && wait(RB_A, it);
+          if (ok && it + 1 < nc) load_k(it + 1);
+          ok = ok && wait(RB_Z, it);
+          if (ok && it + 1 < nc) load_kr(it + 1);
+        }
+        for (int x = 0; x < 4; ++x)
+          if (loads[x]) mbar_wait_drain(&bar[RB_EF + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
+        for (int it = max(0, loads[2] - 2); it < loads[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      // products
+      const int rest = s.len - (nc - 1) * DC;  // tokens of the last chunk
+      if (rest < DC) {  // rows of dO behind them hold the next sequence's
+        ok = wait(RB_EF, 0);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok)
+          for (int r = rest; r < DC; ++r) *reinterpret_cast<uint32_t*>(sm + RSmem::EARLY + RSmem::E_DO + r * 128 + 4 * lane) = 0u;
+        fence_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) {
+        auto early = [&](int it) {
+          const int p = it & 1;
+          if (!wait(RB_EF + p, it >> 1)) return false;
+          tc_fence_after();
+          const uint32_t from = sb + RSmem::EARLY + p * RSmem::E_BYTES;
+          const SDesc dp = sdesc(from + RSmem::E_P, 8192, 1024, LAYOUT_SW128), dq = sdesc(from + RSmem::E_QT, 16, 1024, LAYOUT_SW128);
+          const SDesc dd = sdesc(from + RSmem::E_DO, 8192, 1024, LAYOUT_SW128);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma(tmem + RT_P, dp + (kk >> 2) * 8192u + (kk & 3) * 2048u, dd + (kk & 3) * 2048u, idesc_bf16(128, 64, 1, 1), kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma(tmem + RT_Q + 64 * p, dq + (kk >> 2) * 12288u + (kk & 3) * 32u, dd + (kk & 3) * 2048u, idesc_bf16(128, 64, 0, 1), kk > 0);
+          umma_commit(&bar[RB_E + p]);
+          return true;
+        };
+        ok = ok && early(0);
+        for (int it = 0; it < nc && ok; ++it) {
+          ok = wait(RB_K, it) && wait(RB_SR, it);
+          if (!ok) break;
+          tc_fence_after();
+          const SDesc k0 = sdesc(sb + RSmem::K0, 16, 1024, LAYOUT_SW128), k1 = sdesc(sb + RSmem::K1, 16, 512, LAYOUT_SW64);
+          const SDesc ds = sdesc(sb + RSmem::S, 12288, 1024, LAYOUT_SW128);
+#pragma unroll
+          for (int kk = 0; kk < 6; ++kk)
+            umma(tmem + RT_A, kk < 4 ? k0 + kk * 32u : k1 + (kk - 4) * 32u, ds + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          umma_commit(&bar[RB_A]);
+          ok = wait(RB_KR, it) && wait(RB_WR, it);
+          if (!ok) break;
+          tc_fence_after();
+          const SDesc dr = sdesc(sb + RSmem::KR, 16, 1024, LAYOUT_SW128), dz = sdesc(sb + RSmem::KR + 24576, 8192, 1024, LAYOUT_SW128);
+          const SDesc dw = sdesc(sb + RSmem::W, 8192, 1024, LAYOUT_SW128);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma(tmem + RT_C, dr + (kk >> 2) * 12288u + (kk & 3) * 32u, dw + (kk & 3) * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          umma_commit(&bar[RB_C]);
+          ok = it == 0 || wait(RB_ZF, it - 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma(tmem + RT_Z, dz + kk * 2048u, dw + kk * 2048u, idesc_bf16(128, 64, 1, 1), kk > 0);
+          umma_commit(&bar[RB_Z]);
+          if (it + 1 < nc) ok = early(it + 1);
+        }
+        umma_commit(&bar[RB_DRAIN]);
+        mbar_wait_drain(&bar[RB_DRAIN], 0, DRAIN_NS, a.err);
+      }
+      __syncwarp();
+    } else if (s_row) {  // (nothing waits for warps 3 and 7, so they may not wait for the others either)
+      const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 32u * half;
+      // bf16 of dS1 of chunk c for the gradients, and hi and lo for the chunk's product
+      auto put_state = [&](int x, int c) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split2(S[8 * x + e], hi[e], lo[e]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t at = sb + RSmem::S + sw128(row, 4 * half + 2 * x + p);
+          st_shared_v4(at, hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+          st_shared_v4(at + 12288, lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
+        }
+        st_global_v8(ws_of(c) + W_DS + (row * DV + col0 + 16 * x) * 2, hi);
+      };
+      put_state(0, nc - 1);
+      put_state(1, nc - 1);
+      fence_async_smem();
+      mbar_arrive(&bar[RB_SR]);
+      float2 du[16];
+      for (int it = 0; it < nc; ++it) {
+        const int c = nc - 1 - it;
+        const bool live = row < s.len - c * DC;  // (of a token row)
+        uint4 xr[4];
+        if (t_row) {
+          const uint4* src = reinterpret_cast<const uint4*>(ws_of(c) + W_X + (row * DV + col0) * 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xr[i] = __ldcg(src + i);
+        }
+        ok = wait(RB_GT + (it & 1), it >> 1) && wait(RB_E + (it & 1), it >> 1) && wait(RB_A, it);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const float* gt = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * 768);
+        const float last = gt[GT_F + DC - 1];
+        const float b_row = t_row ? gt[GT_B + row] : 0.f;
+        if (t_row) {
+          const float e_row = gt[GT_E + row];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t d[32], p[32], hi[8], lo[8];
+            tm_ld16x2(lanes + RT_A + 16 * x, lanes + RT_A + 64 + 16 * x, d);
+            tm_ld16(lanes + RT_P + 16 * x, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float2 r = fmadd2(both(e_row), halves(d, e),
+                                fmul2(both(a.scale), make_float2(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]))));
+              r = live ? r : both(0.f);
+              du[8 * x + e] = r;
+              split2(fmul2(both(b_row), r), hi[e], lo[e]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t at = sb + RSmem::W + sw128(row, 4 * half + 2 * x + i);
+              st_shared_v4(at, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+              st_shared_v4(at + 8192, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+            }
+          }
+          fence_async_smem();
+          tc_fence_before();
+          mbar_arrive(&bar[RB_WR]);
+        }
+        ok = wait(RB_C, it);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t d[32], y[32];
+          tm_ld16x2(lanes + RT_C + 16 * x, lanes + RT_C + 64 + 16 * x, d);
+          tm_ld16(lanes + RT_Q + 64 * (it & 1) + 16 * x, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            S[8 * x + e] = fmadd2(both(last), S[8 * x + e],
+                                  fadd2(halves(d, e), make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]))));
+          if (c > 0) put_state(x, c - 1);
+        }
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bar[RB_SR]);
+        if (t_row) {
+          ok = wait(RB_Z, it);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          float2 part = both(0.f);
+          __nv_bfloat16* dst = (__nv_bfloat16*)a.dv + ((s.begin + (long long)c * DC + row) * a.H + h) * DV + col0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t z[32], w[8];
+            tm_ld16(lanes + RT_Z + 16 * x, z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint4 x4 = xr[2 * x + e / 4];
+              const float2 t = fsub2(du[8 * x + e], make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])));
+              part = fmadd2(t, widen2(e % 4 == 0 ? x4.x : e % 4 == 1 ? x4.y : e % 4 == 2 ? x4.z : x4.w), part);
+              const float2 y = fmul2(both(b_row), t);
+              w[e] = bf2(y.x, y.y);
+            }
+            if (live) {
+              reinterpret_cast<uint4*>(dst)[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst)[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&bar[RB_ZF]);
+          if (live) dbeta_part[((long long)(2 * tile + half) * tokens + s.begin + (long long)c * DC + row) * a.H + h] = part.x + part.y;
+        }
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+      tc_fence_after();
+      tm_free<512>(tmem);
+    }
+    if (*abort_flag) {
+      if (tid == 0) raise_error(a.err, ERR_TIMEOUT);
+      return;
+    }
+  }
+  if (a.dh0 && s_row) {
+    float4* dst = reinterpret_cast<float4*>(a.dh0 + (((long long)n * a.H + h) * DK + row) * DV + col0);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) dst[x] = make_float4(S[2 * x].x, S[2 * x].y, S[2 * x + 1].x, S[2 * x + 1].y);
+  }
+}
+
+// ---- gradients of a chunk --------------------------------------------------------------------
+// One CTA a (chunk, head).  Over d_v in three panels of 64 columns: [dO; dR] [X; S0]^T (128 x 160) and X dS1^T
+// (64 x 96); then, with Es = s (dO U^T) . D and Fm = -(dR U^T) . D,
+//     dq = s e^G dO S0^T + Es K
+//     dk = (E U dS1^T + Es^T Q + Fm^T K) + (-e^G dR S0^T + Fm K)
+//     dG = q . dq - k . (first) + k . (second), and at the chunk's end sum_j k_j . (E U dS1^T)_j + e^(G_C) <dS1, S0>
+//     dg_t = sum of dG_i, i >= t
+// 256 threads: warp w has lanes 32 (w % 4) .. and 48 columns of d_k (w / 4); lanes 0-63 have dq and the first part of
+// dk, 64-127 the second.  2 CTAs an SM.
+constexpr int GRAD_THREADS = 256;
+struct GSmem {
+  // a panel: [dO; dR], [X; S0], dS1.  Then (phase 2) Es and Fm in the place of [X; S0], the second part of dk, fp32, from
+  // the start on.  K and Q in two panels of 64 columns; dk's E U dS1^T, fp32.
+  static constexpr uint32_t DOR = 0, XS = 16384, DS = XS + 20480, K = DS + 12288, Q = K + 16384, DKS = Q + 16384, EF = XS, PART = 0;
+  static constexpr uint32_t GT = DKS + DC * 97 * 4, DG = GT + 1280, RED = DG + 4 * DC * 4, BAR = RED + 32, BYTES = BAR + 64;
+  static_assert(BYTES <= 115712, "two CTAs an SM");
+  static_assert(DC * 97 * 4 <= DS && K % 1024 == 0 && GT % 16 == 0, "phase 2");
+};
+enum { GB_KQ = 0, GB_IN, GB_MMA, GB_DRAIN, GB_N };
+constexpr uint32_t GT_DS = 160, GT_X2 = 96;  // tensor memory: X dS1^T; phase 2's second product
+
+__global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, const float* dbeta_part) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + GSmem::BAR);
+  uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + GSmem::BAR + 8 * GB_N);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + GSmem::BAR + 8 * GB_N + 4);
+  const float* const gt = reinterpret_cast<const float*>(sm + GSmem::GT);
+  const float2* const sums = reinterpret_cast<const float2*>(sm + GSmem::GT + 4 * GT_SUM);
+  float* const dgp = reinterpret_cast<float*>(sm + GSmem::DG);
+  float* const red = reinterpret_cast<float*>(sm + GSmem::RED);
+  const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = warp >> 2;
+  const DeltaChunk ch = chunk_of_slot(a, slot);
+  if (ch.len == 0) return;
+  const int idx = slot * a.H + h;
+  const uint8_t* const ws = a.ws + (long long)idx * W_BWD;
+  const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
+  const bool first = q < 2;             // dq and the first part of dk
+  const int i = (lane + 32 * q) & 63;   // token
+  const bool live = i < ch.len;
+  int panels = 0;
+  auto load_panel = [&](int p) {
+    ++panels;
+    mbar_expect_tx(&bar[GB_IN], 49152);
+    box_load(sb + GSmem::DOR, &maps.dO, &bar[GB_IN], 64 * p, h, (int)ch.t0);
+    box_load(sb + GSmem::DOR + 8192, &maps.dv, &bar[GB_IN], 64 * p, h, (int)ch.t0);
+    box_load(sb + GSmem::XS, &maps.x, &bar[GB_IN], 64 * p, 0, idx);
+    box_load(sb + GSmem::XS + 8192, &maps.s0, &bar[GB_IN], 64 * p, 0, idx);
+    box_load(sb + GSmem::DS, &maps.ds, &bar[GB_IN], 64 * p, 0, idx);
+  };
+  if (warp == 1) tm_alloc<256>(slot_tm);
+  if (tid == 0) {
+    for (int x = 0; x < GB_N; ++x) mbar_init(&bar[x], 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+    load_panel(0);
+    mbar_expect_tx(&bar[GB_KQ], 4 * 8192 + 1280);
+    for (int p = 0; p < 2; ++p) {
+      box_load(sb + GSmem::K + 8192 * p, &maps.k0, &bar[GB_KQ], 64 * p, h, (int)ch.t0);
+      box_load(sb + GSmem::Q + 8192 * p, &maps.q0, &bar[GB_KQ], 64 * p, h, (int)ch.t0);
+    }
+    bulk_load(sb + GSmem::GT, ws + W_GT, 1280, &bar[GB_KQ]);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot_tm;
+  const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+  bool ok = true, gone = false;
+  float frob = 0.f;  // <dS1, S0>, this thread's part
+  for (int p = 0; p < 3; ++p) {
+    ok = ok && mbar_wait(&bar[GB_IN], p & 1, a.wait_ns, abort_flag);
+    if (tid == 0 && ok) {
+      const SDesc da = sdesc(sb + GSmem::DOR, 16, 1024, LAYOUT_SW128), dx = sdesc(sb + GSmem::XS, 16, 1024, LAYOUT_SW128);
+      const SDesc ds = sdesc(sb + GSmem::DS, 16, 1024, LAYOUT_SW128);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) umma(tmem, da + kk * 32u, dx + kk * 32u, idesc_bf16(128, 160, 0, 0), p + kk > 0);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_DS, dx + kk * 32u, ds + kk * 32u, idesc_bf16(128, 96, 0, 0), p + kk > 0);
+      umma_commit(&bar[GB_MMA]);
+    }
+    __syncwarp();
+    if (ok)
+#pragma unroll
+      for (int e = tid; e < DK * 8; e += GRAD_THREADS) {  // (768 pieces of 16 bytes; the two tiles are swizzled alike)
+        const uint4 x = ld_shared_v4(sb + GSmem::XS + 8192 + 16 * e), y = ld_shared_v4(sb + GSmem::DS + 16 * e);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 u = widen2(xw[w]), v = widen2(yw[w]);
+          frob = fmaf(u.x, v.x, fmaf(u.y, v.y, frob));
+        }
+      }
+    ok = ok && mbar_wait(&bar[GB_MMA], p & 1, a.wait_ns, abort_flag);
+    gone = __syncthreads_or(!ok);
+    if (gone) break;
+    if (tid == 0 && p < 2) load_panel(p + 1);
+  }
+  float at_end = 0.f;
+  float2 acc[24];  // s e^G dO S0^T, or -e^G dR S0^T: this thread's 48 columns of d_k
+  if (!gone) {
+    tc_fence_after();
+    ok = mbar_wait(&bar[GB_KQ], 0, a.wait_ns, abort_flag);
+    gone = __syncthreads_or(!ok);
+  }
+  if (!gone && ch.len < DC) {  // rows of K and Q behind the last token hold the next sequence's
+    for (int e = tid; e < 4 * (DC - ch.len) * 8; e += GRAD_THREADS) {
+      const int r = ch.len + (e >> 3) % (DC - ch.len), t = (e >> 3) / (DC - ch.len);
+      st_shared_v4(sb + GSmem::K + 8192 * t + 128 * r + 16 * (e & 7), 0u, 0u, 0u, 0u);
+    }
+    __syncthreads();
+  }
+  // 16-byte piece c (0 .. 5) of this thread's columns of row i of K or Q
+  auto piece = [&](uint32_t base, int c) {
+    const int x = 6 * half + c;
+    return ld_shared_v4(base + (x < 8 ? sw128(i, x) : 8192u + sw128(i, x - 8)));
+  };
+  if (!gone) {
+    const float2 gi = sums[i];
+    const float f_row = gt[GT_F + i], e_row = gt[GT_E + i] * gt[GT_B + i];
+    // Es and Fm
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint32_t d[32], w[8];
+      tm_ld16(lanes + 32 * half + 16 * x, d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float y[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int j = 32 * half + 16 * x + 2 * e + b;
+          const float2 gj = sums[j];
+          const float t = exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * (gt[GT_B + j] * __uint_as_float(d[2 * e + b]));
+          y[b] = live && (first ? j <= i : j < i) ? (first ? a.scale * t : -t) : 0.f;
+        }
+        w[e] = bf2(y[0], y[1]);
+      }
+      const uint32_t to = sb + GSmem::EF + (first ? 0u : 8192u);
+      st_shared_v4(to + sw128(i, 4 * half + 2 * x), w[0], w[1], w[2], w[3]);
+      st_shared_v4(to + sw128(i, 4 * half + 2 * x + 1), w[4], w[5], w[6], w[7]);
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      uint32_t d[32];
+      tm_ld16(lanes + 64 + 48 * half + 16 * x, d);
+      const float2 w = both(first ? a.scale * f_row : -f_row);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[8 * x + e] = fmul2(w, make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+    }
+    if (first) {
+      float* const dks = reinterpret_cast<float*>(sm + GSmem::DKS) + i * 97 + 48 * half;
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        uint32_t d[32];
+        tm_ld16(lanes + GT_DS + 48 * half + 16 * x, d);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 k4 = piece(sb + GSmem::K, 2 * x + c);
+          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 k = widen2(kw[e]);
+            const float y0 = e_row * __uint_as_float(d[8 * c + 2 * e]), y1 = e_row * __uint_as_float(d[8 * c + 2 * e + 1]);
+            dks[16 * x + 8 * c + 2 * e] = y0;
+            dks[16 * x + 8 * c + 2 * e + 1] = y1;
+            if (live) at_end = fmaf(k.x, y0, fmaf(k.y, y1, at_end));
+          }
+        }
+      }
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      const SDesc ef = sdesc(sb + GSmem::EF, 16, 1024, LAYOUT_SW128), et = sdesc(sb + GSmem::EF, 8192, 1024, LAYOUT_SW128);
+      const SDesc dk = sdesc(sb + GSmem::K, 8192, 1024, LAYOUT_SW128), dq = sdesc(sb + GSmem::Q, 8192, 1024, LAYOUT_SW128);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) umma(tmem, ef + kk * 32u, dk + kk * 2048u, idesc_bf16(128, 96, 0, 1), kk > 0);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + kk * 2048u, dq + kk * 2048u, idesc_bf16(128, 96, 1, 1), kk > 0);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + 8192u + kk * 2048u, dk + kk * 2048u, idesc_bf16(128, 96, 1, 1), 1);
+      umma_commit(&bar[GB_MMA]);
+    }
+    __syncwarp();
+    ok = mbar_wait(&bar[GB_MMA], 1, a.wait_ns, abort_flag);
+    gone = __syncthreads_or(!ok);
+  }
+  if (!gone) {
+    tc_fence_after();
+    float dg = 0.f;
+    float* const part = reinterpret_cast<float*>(sm + GSmem::PART) + i * 97 + 48 * half;
+    const float* const dks = reinterpret_cast<const float*>(sm + GSmem::DKS) + i * 97 + 48 * half;
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      uint32_t d[32];
+      tm_ld16(lanes + 48 * half + 16 * x, d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[8 * x + e] = fadd2(acc[8 * x + e], make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint4 r4 = piece(first ? sb + GSmem::Q : sb + GSmem::K, 2 * x + c);
+        const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = acc[8 * x + 4 * c + e], r = widen2(rw[e]);
+          dg = fmaf(r.x, y.x, fmaf(r.y, y.y, dg));
+          if (!first) {
+            part[16 * x + 8 * c + 2 * e] = y.x;
+            part[16 * x + 8 * c + 2 * e + 1] = y.y;
+          }
+        }
+        if (first && live) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = bf2(acc[8 * x + 4 * c + e].x, acc[8 * x + 4 * c + e].y);
+          reinterpret_cast<uint4*>((__nv_bfloat16*)a.dq + ((ch.t0 + i) * a.H + h) * DK + 48 * half)[2 * x + c] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    __syncthreads();
+    if (first) {
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        uint32_t d[32];
+        tm_ld16(lanes + GT_X2 + 48 * half + 16 * x, d);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 k4 = piece(sb + GSmem::K, 2 * x + c);
+          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = 16 * x + 8 * c + 2 * e;
+            const float2 k = widen2(kw[e]);
+            const float y0 = dks[at] + __uint_as_float(d[8 * c + 2 * e]), y1 = dks[at + 1] + __uint_as_float(d[8 * c + 2 * e + 1]);
+            dg = fmaf(-k.x, y0, fmaf(-k.y, y1, dg));
+            w[e] = bf2(y0 + part[at], y1 + part[at + 1]);
+          }
+          if (live)
+            reinterpret_cast<uint4*>((__nv_bfloat16*)a.dk + ((ch.t0 + i) * a.H + h) * DK + 48 * half)[2 * x + c] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    dgp[(first ? 0 : 128) + 64 * half + i] = live ? dg : 0.f;
+    at_end = fmaf(gt[GT_F + DC - 1], frob, at_end);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) at_end += __shfl_xor_sync(0xffffffffu, at_end, off);
+    if (lane == 0) red[warp] = at_end;
+  } else if (tid == 0) {
+    raise_error(a.err, ERR_TIMEOUT);
+    // the copies and products that were issued end before their memory is given up
+    umma_commit(&bar[GB_DRAIN]);
+    mbar_wait_drain(&bar[GB_DRAIN], 0, DRAIN_NS, a.err);
+    mbar_wait_drain(&bar[GB_IN], (panels - 1) & 1, DRAIN_NS, a.err);
+    mbar_wait_drain(&bar[GB_KQ], 0, DRAIN_NS, a.err);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tm_free<256>(tmem);
+  }
+  if (gone) return;
+  if (warp == 0) {  // dg_t: what hangs on G_i, i >= t, and on the chunk's end
+    float end = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) end += red[w];
+    auto at = [&](int t) { return (dgp[t] + dgp[64 + t]) + (dgp[128 + t] + dgp[192 + t]); };
+    const float lo = at(2 * lane), hi = at(2 * lane + 1);
+    float run = lo + hi;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const float up = __shfl_down_sync(0xffffffffu, run, off);
+      if (lane + off < 32) run += up;
+    }
+    const float behind = run - (lo + hi);
+    __nv_bfloat16* dst = (__nv_bfloat16*)a.dg + ch.t0 * a.H + h;
+    if (2 * lane < ch.len) dst[(long long)(2 * lane) * a.H] = __float2bfloat16_rn(run + end);
+    if (2 * lane + 1 < ch.len) dst[(long long)(2 * lane + 1) * a.H] = __float2bfloat16_rn(behind + hi + end);
+  } else if (tid >= 64 && tid - 64 < ch.len) {
+    const long long t = ch.t0 + tid - 64;
+    float b = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2 * NTILE; ++x) b += dbeta_part[((long long)x * tokens + t) * a.H + h];
+    ((__nv_bfloat16*)a.dbeta)[t * a.H + h] = __float2bfloat16_rn(b);
+  }
+}
+
 }  // namespace
 
-size_t delta_tc_ws_bytes(long long slots, int H) { return (size_t)slots * H * W_FWD; }
+size_t delta_tc_ws_bytes(long long slots, long long tokens, int H, bool bwd) {
+  return (size_t)slots * H * (bwd ? W_BWD : W_FWD) + (bwd ? (size_t)2 * NTILE * tokens * H * 4 : 0);
+}
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-// A [tokens, H, d] bf16 tensor in boxes of `cols` columns (64: 128-byte swizzle, 32: 64-byte) x one head x `rows` tokens.
-static bool box_map(CUtensorMap* m, const void* base, int d, int H, long long tokens, int cols, int rows) {
+// bf16 [d2][d1][d0], strides in bytes, in boxes of `cols` (64: 128-byte swizzle, 32: 64-byte) x r1 x r2.
+static bool map3(CUtensorMap* m, const void* base, long long d0, long long d1, long long d2, long long s1, long long s2, int cols,
+                 int r1, int r2) {
   static const EncodeTiledFn fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -693,30 +1420,69 @@ static bool box_map(CUtensorMap* m, const void* base, int d, int H, long long to
                        q == cudaDriverEntryPointSuccess;
     return found ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
   }();
-  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
-  const cuuint32_t box[3] = {(cuuint32_t)cols, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2}, strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)r1, (cuuint32_t)r2}, step[3] = {1, 1, 1};
   return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// A [tokens, H, d] tensor in boxes of one head.
+static bool rows_map(CUtensorMap* m, const void* base, int d, const DeltaArgs& a, int cols, int rows) {
+  const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
+  return map3(m, base, d, a.H, tokens, 2ll * d, 2ll * a.H * d, cols, 1, rows);
+}
+static bool input_maps(DeltaMaps& m, const DeltaArgs& a) {
+  return rows_map(&m.k0, a.k, DK, a, 64, DC) && rows_map(&m.k1, a.k, DK, a, 32, DC) && rows_map(&m.q0, a.q, DK, a, 64, DC) &&
+         rows_map(&m.q1, a.q, DK, a, 32, DC) && rows_map(&m.v, a.v, DV, a, 64, DC);
+}
+template <class F>
+static cudaError_t allow(F* f, uint32_t bytes) {
+  return cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
 
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
   static OncePerDevice<CudaDeviceApi> once;
-  cudaError_t e = once([] {
-    const cudaError_t x = cudaFuncSetAttribute(delta_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepSmem::BYTES);
-    return x != cudaSuccess ? x : cudaFuncSetAttribute(delta_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ScanSmem::BYTES);
+  const cudaError_t e = once([] {
+    const cudaError_t x = allow(delta_prep_kernel<false>, PrepSmem::bytes(false));
+    return x != cudaSuccess ? x : allow(delta_scan_kernel<false>, ScanSmem::BYTES);
   });
   if (e != cudaSuccess) return e;
-  const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
   DeltaMaps m;
   memset(&m, 0, sizeof(m));
-  if (tokens > 0 && !(box_map(&m.k0, a.k, DK, a.H, tokens, 64, DC) && box_map(&m.k1, a.k, DK, a.H, tokens, 32, DC) &&
-                      box_map(&m.q0, a.q, DK, a.H, tokens, 64, DC) && box_map(&m.q1, a.q, DK, a.H, tokens, 32, DC) &&
-                      box_map(&m.v, a.v, DV, a.H, tokens, 64, DC) && box_map(&m.o, a.o, DV, a.H, tokens, 32, 32)))
-    return cudaErrorInvalidValue;
-  if (a.slots > 0) delta_prep_kernel<<<(unsigned)a.slots * a.H, PREP_THREADS, PrepSmem::BYTES, st>>>(m, a);
-  delta_scan_kernel<<<(unsigned)a.n_seq * a.H * NTILE, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a);
+  const unsigned chunks = (unsigned)a.slots * a.H, units = (unsigned)a.n_seq * a.H * NTILE;
+  if (a.cu_seqlens ? a.T > 0 : a.slots > 0) {
+    if (!(input_maps(m, a) && rows_map(&m.o, a.o, DV, a, 32, 32))) return cudaErrorInvalidValue;
+    delta_prep_kernel<false><<<chunks, PREP_THREADS, PrepSmem::bytes(false), st>>>(m, a);
+  }
+  delta_scan_kernel<false><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_delta_tc_bwd(const DeltaArgs& a, cudaStream_t st) {
+  static OncePerDevice<CudaDeviceApi> once;
+  const cudaError_t e = once([] {
+    for (cudaError_t x : {allow(delta_prep_kernel<true>, PrepSmem::bytes(true)), allow(delta_scan_kernel<true>, ScanSmem::BYTES),
+                          allow(delta_rscan_kernel, RSmem::BYTES), allow(delta_grads_kernel, GSmem::BYTES)})
+      if (x != cudaSuccess) return x;
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
+  DeltaMaps m;
+  memset(&m, 0, sizeof(m));
+  const unsigned chunks = (unsigned)a.slots * a.H, units = (unsigned)a.n_seq * a.H * NTILE;
+  float* const part = reinterpret_cast<float*>(a.ws + (long long)a.slots * a.H * W_BWD);
+  const bool some = a.cu_seqlens ? a.T > 0 : a.slots > 0;
+  if (some) {
+    const long long all = (long long)a.slots * a.H;
+    if (!(input_maps(m, a) && rows_map(&m.dO, a.dO, DV, a, 64, DC) && rows_map(&m.dv, a.dv, DV, a, 64, DC) &&
+          map3(&m.x, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 64, DC, 1) && map3(&m.s0, a.ws + W_S0, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) &&
+          map3(&m.ds, a.ws + W_DS, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1)))
+      return cudaErrorInvalidValue;
+    delta_prep_kernel<true><<<chunks, PREP_THREADS, PrepSmem::bytes(true), st>>>(m, a);
+    delta_scan_kernel<true><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a);
+  }
+  delta_rscan_kernel<<<units, RSCAN_THREADS, RSmem::BYTES, st>>>(m, a, part);
+  if (some) delta_grads_kernel<<<chunks, GRAD_THREADS, GSmem::BYTES, st>>>(m, a, part);
   return cudaGetLastError();
 }
 
