@@ -100,12 +100,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// 32 bytes to a 32-byte aligned address.
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
 __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
@@ -158,6 +152,7 @@ constexpr unsigned long long DRAIN_NS = 1000000000ull;
 struct DeltaMaps {
   CUtensorMap k0, k1, q0, q1, v, o;
   CUtensorMap dO, dv, x, s0, ds;
+  CUtensorMap dvo, xo;  // (to write: 32 rows x 32 columns, one a warp)
 };
 __device__ __forceinline__ void load_kq(const DeltaMaps& m, uint32_t p0, uint32_t p1, uint64_t* bar, int h, int t) {
   mbar_expect_tx(bar, 24576);
@@ -509,22 +504,25 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 }
 
 // ---- scan -----------------------------------------------------------------------------------
-// 256 threads: warp w has lanes 32 (w % 4) .. of the products' rows and columns 32 (w / 4) .. of the tile's 64.
+// Warps 0-7: warp w has lanes 32 (w % 4) .. of the products' rows and columns 32 (w / 4) .. of the tile's 64.
 // Rows of [K; Q] S: 0-63 K's (warps of w % 4 < 2), 64-127 Q's; rows of K^ B R: 0-95 the state's; rows of P^ B R:
-// 64-127.  A thread keeps its 32 columns of a state row in fp32 registers.  Tensor memory: two places of 128
+// 64-127.  A thread keeps its 32 columns of a state row in fp32 registers.  One thread of warp 8 issues all products
+// and copies.  Hand-overs through mbarriers, so that only the state's way (product, residual, product, state) is waited
+// for: a chunk's outputs are written while the next chunk's first product runs.  Tensor memory: two places of 128
 // columns ([hi | lo]), 2 CTAs an SM.  A chunk's [K; Q] S and, once that is in registers, its P^ B R have the one, its
-// K^ B R the other; the next chunk has them the other way round, so that only the state's way (product, residual,
-// product, state) is waited for and the outputs are written while the next chunk's first product runs.
-// Warps 3 and 7, which have no state rows, have the issuing threads: of the copies and of the products.
+// K^ B R the other; the next chunk has them the other way round.
 // STATES (the backward's forward pass): K's rows stand in 64-127 and rows 0-63 are not looked at; Z is in P^'s place,
 // X = R - Z B R and every chunk's S0 go to the workspace instead of outputs.
-constexpr int TN = 64, NTILE = DV / TN, SCAN_THREADS = 256, ISSUER = 224, LOADER = 96;
+constexpr int TN = 64, NTILE = DV / TN, SCAN_THREADS = 288;
 struct ScanSmem {
   static constexpr uint32_t KQ0 = 0, KQ1 = 16384, OP = 24576, S = OP + W_OP, BR = S + 24576, V = BR + 16384, OUT = V + 8192,
-                            GT = OUT + 8192, BAR = GT + 512, BYTES = BAR + 96;
+                            GT = OUT + 8192, BAR = GT + 512, BYTES = BAR + 112;
   static_assert(BYTES <= 115712, "two CTAs an SM");
 };
-enum { SB_A = 0, SB_C, SB_O, SB_KQ, SB_V, SB_KD, SB_PH, SB_DRAIN, SB_N };
+// Products ([K; Q] S, K^ B R, P^ B R), copies (K and Q; V and decays; K^; P^), hand-overs (the state, B R and the first
+// product read; the outputs' product read).  Whoever waits for a phase hands something over before the next one of the
+// same barrier can end.
+enum { SB_A = 0, SB_C, SB_O, SB_KQ, SB_V, SB_KD, SB_PH, SB_SR, SB_WR, SB_OF, SB_DRAIN, SB_N };
 
 template <bool STATES>
 __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
@@ -534,57 +532,15 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + ScanSmem::BAR + 8 * SB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + ScanSmem::BAR + 8 * SB_N + 4);
   const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = nh / a.H;
-  const int tid = threadIdx.x, warp = tid >> 5, q = warp & 3, half = warp >> 2;
+  const int tid = threadIdx.x, warp = tid >> 5, q = warp & 3, half = (warp >> 2) & 1;
   const int row = (tid & 31) + 32 * q;  // lane of the products
   const int tok = row & 63;
   const int col0 = tile * TN + 32 * half;
-  const bool r_row = STATES == (q >= 2), o_row = q >= 2, s_row = q < 3, issuer = tid == ISSUER, loader = tid == LOADER;
+  const bool r_row = STATES == (q >= 2), o_row = q >= 2, s_row = warp < 8 && q < 3;
   const DeltaSeq s = delta_seq(a, n);
   const int nc = (s.len + DC - 1) / DC;
   const int from = a.h0 ? delta_row(a.h0_row, a.h0_rows, n, a.err) : -1;
-
-  auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * (STATES ? W_BWD : W_FWD); };
-  // (the loader) a chunk's operands, each as soon as the chunk before is done with their place
-  int loads[4] = {};
-  auto load_rows = [&](int c) {
-    ++loads[0];
-    const int t = (int)(s.begin + (long long)c * DC);
-    if (STATES) {
-      mbar_expect_tx(&bar[SB_KQ], 12288);
-      box_load(sb + ScanSmem::KQ0 + 8192, &maps.k0, &bar[SB_KQ], 0, h, t);
-      box_load(sb + ScanSmem::KQ1 + 4096, &maps.k1, &bar[SB_KQ], 64, h, t);
-    } else {
-      load_kq(maps, sb + ScanSmem::KQ0, sb + ScanSmem::KQ1, &bar[SB_KQ], h, t);
-    }
-  };
-  auto load_v = [&](int c) {
-    ++loads[1];
-    mbar_expect_tx(&bar[SB_V], 8192 + 512);
-    box_load(sb + ScanSmem::V, &maps.v, &bar[SB_V], tile * TN, h, (int)(s.begin + (long long)c * DC));
-    bulk_load(sb + ScanSmem::GT, ws_of(c) + W_GT, 512, &bar[SB_V]);
-  };
-  auto load_kd = [&](int c) {
-    ++loads[2];
-    mbar_expect_tx(&bar[SB_KD], W_PH);
-    bulk_load(sb + ScanSmem::OP + W_KD, ws_of(c) + W_KD, W_PH, &bar[SB_KD]);
-  };
-  auto load_ph = [&](int c) {
-    ++loads[3];
-    mbar_expect_tx(&bar[SB_PH], W_OP - W_PH);
-    bulk_load(sb + ScanSmem::OP + W_PH, ws_of(c) + W_PH, W_OP - W_PH, &bar[SB_PH]);
-  };
-  // What chunk c will load, into L2.
-  auto prefetch = [&](int c) {
-    const int t = (int)(s.begin + (long long)c * DC);
-    box_prefetch(&maps.k0, 0, h, t);
-    box_prefetch(&maps.k1, 64, h, t);
-    if (!STATES) {
-      box_prefetch(&maps.q0, 0, h, t);
-      box_prefetch(&maps.q1, 64, h, t);
-    }
-    box_prefetch(&maps.v, tile * TN, h, t);
-    bulk_prefetch(ws_of(c), W_FWD);
-  };
+  auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
 
   float2 S[16];
 #pragma unroll
@@ -598,111 +554,188 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
       S[2 * x + 1] = make_float2(w.z, w.w);
     }
   }
-  // hi and lo of 16 columns of the state row, the operand of chunk c's product
-  auto put_state = [&](int x, [[maybe_unused]] int c) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) split2(S[8 * x + e], hi[e], lo[e]);
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const uint32_t at = sb + ScanSmem::S + sw128(row, 4 * half + 2 * x + p);
-      st_shared_v4(at, hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
-      st_shared_v4(at + 12288, lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
-    }
-    if (STATES) st_global_v8(ws_of(c) + W_S0 + (row * DV + col0 + 16 * x) * 2, hi);
-  };
   if (nc > 0) {
-    if (warp == 0) tm_alloc<256>(slot_tm);
-    if (loader) {
-      for (int x = 0; x < SB_N; ++x) mbar_init(&bar[x], 1);
-      *abort_flag = 0;
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      fence_async_smem();
-      load_rows(0);
-      load_v(0);
-      load_kd(0);
-      load_ph(0);
-      if (nc > 1) prefetch(1);
+    if (warp == 8) {
+      tm_alloc<256>(slot_tm);
+      if (tid == 256) {
+        for (int x = 0; x < SB_N; ++x) mbar_init(&bar[x], x == SB_SR ? 192 : x == SB_WR ? 256 : x == SB_OF ? 128 : 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+      }
     }
-    if (s_row) {
-      put_state(0, 0);
-      put_state(1, 0);
-    }
-    fence_async_smem();
     tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     const uint32_t tmem = *slot_tm;
-    const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    float2 keep[16];  // e^G Q S0, or (STATES) R
     bool ok = true;
-    // The outputs of chunk c (rows 64-127), from the place that its first product had.
-    const uint32_t stage = sb + ScanSmem::OUT + 2048u * ((q & 1) + 2 * half);  // this warp's 32 rows x 32 columns
-    auto outputs = [&](int c) {
-      ok = mbar_wait(&bar[SB_O], c & 1, a.wait_ns, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      if (loader && c + 1 < nc) load_ph(c + 1);
-      tc_fence_after();
-      const uint32_t from_tm = tmem + lanes + (c & 1) * 128u + 32u * half;
-      const int left = s.len - c * DC;
-      const long long t0 = s.begin + (long long)c * DC;
-      if ((tid & 31) == 0) stores_read();
-      __syncwarp();
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t d[32], w[8];
-        tm_ld16x2(from_tm + 16 * x, from_tm + 64 + 16 * x, d);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 y = STATES ? fsub2(keep[8 * x + e], halves(d, e)) : fmul2(both(a.scale), fadd2(keep[8 * x + e], halves(d, e)));
-          w[e] = bf2(y.x, y.y);
-        }
-        if (STATES) {  // (zeros behind the last token, as its R)
-          st_global_v8(ws_of(c) + W_X + (tok * DV + col0 + 16 * x) * 2, w);
-        } else if (left >= DC) {
-          st_shared_v4(stage + sw64(tid & 31, 2 * x), w[0], w[1], w[2], w[3]);
-          st_shared_v4(stage + sw64(tid & 31, 2 * x + 1), w[4], w[5], w[6], w[7]);
-        } else if (tok < left) {  // a sequence's last rows: no box is written past them
-          uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + ((t0 + tok) * a.H + h) * DV + col0);
-          dst[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      }
-      if (!STATES && left >= DC) {
-        fence_async_smem();
-        __syncwarp();
-        if ((tid & 31) == 0) box_store(&maps.o, stage, col0, h, (int)(t0 + 32 * (q & 1)));
-      }
-    };
-    int c = 0;
-    for (; c < nc; ++c) {
-      const uint32_t ph = c & 1, at_a = tmem + ph * 128u, at_c = tmem + (ph ^ 1) * 128u;
-      if (issuer && mbar_wait(&bar[SB_KQ], ph, a.wait_ns, abort_flag)) {
-        tc_fence_after();
+    if (warp == 8) {
+      if (tid == 256) {
+        auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * (STATES ? W_BWD : W_FWD); };
+        // a chunk's operands, each as soon as the chunk before is done with their place
+        int loads[4] = {};
+        auto load_rows = [&](int c) {
+          ++loads[0];
+          const int t = (int)(s.begin + (long long)c * DC);
+          if (STATES) {
+            mbar_expect_tx(&bar[SB_KQ], 12288);
+            box_load(sb + ScanSmem::KQ0 + 8192, &maps.k0, &bar[SB_KQ], 0, h, t);
+            box_load(sb + ScanSmem::KQ1 + 4096, &maps.k1, &bar[SB_KQ], 64, h, t);
+          } else {
+            load_kq(maps, sb + ScanSmem::KQ0, sb + ScanSmem::KQ1, &bar[SB_KQ], h, t);
+          }
+        };
+        auto load_v = [&](int c) {
+          ++loads[1];
+          mbar_expect_tx(&bar[SB_V], 8192 + 512);
+          box_load(sb + ScanSmem::V, &maps.v, &bar[SB_V], tile * TN, h, (int)(s.begin + (long long)c * DC));
+          bulk_load(sb + ScanSmem::GT, ws_of(c) + W_GT, 512, &bar[SB_V]);
+        };
+        auto load_kd = [&](int c) {
+          ++loads[2];
+          mbar_expect_tx(&bar[SB_KD], W_PH);
+          bulk_load(sb + ScanSmem::OP + W_KD, ws_of(c) + W_KD, W_PH, &bar[SB_KD]);
+        };
+        auto load_ph = [&](int c) {
+          ++loads[3];
+          mbar_expect_tx(&bar[SB_PH], W_OP - W_PH);
+          bulk_load(sb + ScanSmem::OP + W_PH, ws_of(c) + W_PH, W_OP - W_PH, &bar[SB_PH]);
+        };
+        // what chunk c will load, into L2
+        auto prefetch = [&](int c) {
+          const int t = (int)(s.begin + (long long)c * DC);
+          box_prefetch(&maps.k0, 0, h, t);
+          box_prefetch(&maps.k1, 64, h, t);
+          if (!STATES) {
+            box_prefetch(&maps.q0, 0, h, t);
+            box_prefetch(&maps.q1, 64, h, t);
+          }
+          box_prefetch(&maps.v, tile * TN, h, t);
+          bulk_prefetch(ws_of(c), W_FWD);
+        };
+        load_rows(0);
+        load_v(0);
+        load_kd(0);
+        load_ph(0);
+        if (nc > 1) prefetch(1);
         const SDesc d0 = sdesc(sb + ScanSmem::KQ0, 16, 1024, LAYOUT_SW128), d1 = sdesc(sb + ScanSmem::KQ1, 16, 512, LAYOUT_SW64);
-        const SDesc ds = sdesc(sb + ScanSmem::S, 12288, 1024, LAYOUT_SW128);
+        const SDesc ds = sdesc(sb + ScanSmem::S, 12288, 1024, LAYOUT_SW128), db = sdesc(sb + ScanSmem::BR, 8192, 1024, LAYOUT_SW128);
+        const SDesc dk = sdesc(sb + ScanSmem::OP + W_KD, 16, 1024, LAYOUT_SW128);
+        const SDesc dp = sdesc(sb + ScanSmem::OP + W_PH - 8192, 16, 1024, LAYOUT_SW128);  // P^ in rows 64-127
+        for (int c = 0; c < nc; ++c) {
+          const uint32_t at_a = tmem + (c & 1) * 128u, at_c = tmem + ((c & 1) ^ 1) * 128u;
+          if (!(ok = wait(SB_KQ, c) && wait(SB_SR, c))) break;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 6; ++kk)
-          umma(at_a, kk < 4 ? d0 + kk * 32u : d1 + (kk - 4) * 32u, ds + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
-        umma_commit(&bar[SB_A]);
+          for (int kk = 0; kk < 6; ++kk)
+            umma(at_a, kk < 4 ? d0 + kk * 32u : d1 + (kk - 4) * 32u, ds + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          umma_commit(&bar[SB_A]);
+          // (the state's high halves are what the gradients take of it)
+          if (STATES) box_store(&maps.s0, sb + ScanSmem::S, tile * TN, 0, (s.slot0 + c) * a.H + h);
+          if (c > 0) {
+            if (!(ok = wait(SB_O, c - 1))) break;
+            load_ph(c);
+          }
+          if (!(ok = wait(SB_A, c))) break;
+          if (c + 1 < nc) load_rows(c + 1);
+          if (!(ok = wait(SB_KD, c) && (c == 0 || wait(SB_OF, c - 1)) && wait(SB_WR, c))) break;
+          if (STATES) stores_read();  // (the state is written again once the next product is there)
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma(at_c, dk + (kk >> 2) * 12288u + (kk & 3) * 32u, db + (kk & 3) * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          umma_commit(&bar[SB_C]);
+          if (!(ok = wait(SB_PH, c))) break;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma(at_a, dp + kk * 32u, db + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          umma_commit(&bar[SB_O]);
+          if (c + 1 < nc) load_v(c + 1);
+          if (c + 2 < nc) prefetch(c + 2);
+          if (!(ok = wait(SB_C, c))) break;
+          if (c + 1 < nc) load_kd(c + 1);
+        }
+        // what was issued ends before its memory is given up
+        umma_commit(&bar[SB_DRAIN]);
+        mbar_wait_drain(&bar[SB_DRAIN], 0, DRAIN_NS, a.err);
+        for (int x = 0; x < 4; ++x) mbar_wait_drain(&bar[SB_KQ + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
+        stores_read();
       }
       __syncwarp();
-      ok = true;
-      if (o_row && c > 0) outputs(c - 1);
-      ok = ok && mbar_wait(&bar[SB_V], ph, a.wait_ns, abort_flag) && mbar_wait(&bar[SB_A], ph, a.wait_ns, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      float last = 0.f;
-      if (ok) {
-        if (loader && c + 1 < nc) load_rows(c + 1);
+    } else {
+      const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 32u * half;
+      // hi and lo of 16 columns of the state row, the next product's operand
+      auto put_state = [&](int x) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split2(S[8 * x + e], hi[e], lo[e]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t at = sb + ScanSmem::S + sw128(row, 4 * half + 2 * x + p);
+          st_shared_v4(at, hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+          st_shared_v4(at + 12288, lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
+        }
+      };
+      if (s_row) {
+        put_state(0);
+        put_state(1);
+        fence_async_smem();
+        mbar_arrive(&bar[SB_SR]);
+      }
+      float2 keep[16];  // e^G Q S0, or (STATES) R
+      // The outputs of chunk c (rows 64-127), from the place that its first product had.
+      const uint32_t stage = sb + ScanSmem::OUT + 2048u * ((q & 1) + 2 * half);  // this warp's 32 rows x 32 columns
+      auto outputs = [&](int c) {
+        ok = __all_sync(0xffffffffu, wait(SB_O, c));
+        if (!ok) return;
         tc_fence_after();
-        const float* gt = reinterpret_cast<const float*>(sm + ScanSmem::GT);
-        const float f_row = gt[tok], b_row = gt[DC + tok];
-        const bool live = tok < s.len - c * DC;  // (rows behind the last hold the next sequence's)
-        last = gt[DC - 1];
+        const uint32_t from_tm = lanes + (c & 1) * 128u;
+        const int left = s.len - c * DC;
+        const long long t0 = s.begin + (long long)c * DC;
+        if ((tid & 31) == 0) stores_read();
+        __syncwarp();
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          uint32_t d[32], w[8];
+          tm_ld16x2(from_tm + 16 * x, from_tm + 64 + 16 * x, d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 y = STATES ? fsub2(keep[8 * x + e], halves(d, e)) : fmul2(both(a.scale), fadd2(keep[8 * x + e], halves(d, e)));
+            w[e] = bf2(y.x, y.y);
+          }
+          if (STATES || left >= DC) {  // (X: zeros behind the last token, as its R)
+            st_shared_v4(stage + sw64(tid & 31, 2 * x), w[0], w[1], w[2], w[3]);
+            st_shared_v4(stage + sw64(tid & 31, 2 * x + 1), w[4], w[5], w[6], w[7]);
+          } else if (tok < left) {  // a sequence's last rows: no box is written past them
+            uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + ((t0 + tok) * a.H + h) * DV + col0);
+            dst[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&bar[SB_OF]);
+        if (STATES || left >= DC) {
+          fence_async_smem();
+          __syncwarp();
+          if ((tid & 31) == 0) {
+            if (STATES) box_store(&maps.xo, stage, col0, 32 * (q & 1), (s.slot0 + c) * a.H + h);
+            else box_store(&maps.o, stage, col0, h, (int)(t0 + 32 * (q & 1)));
+          }
+        }
+      };
+      for (int c = 0; c < nc; ++c) {
+        const uint32_t at_a = lanes + (c & 1) * 128u, at_c = lanes + ((c & 1) ^ 1) * 128u;
+        if (o_row && c > 0) outputs(c - 1);
+        ok = ok && wait(SB_V, c) && wait(SB_A, c);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const float* gt = reinterpret_cast<const float*>(sm + ScanSmem::GT);
+        const float f_row = gt[GT_F + tok], b_row = gt[GT_B + tok], last = gt[GT_F + DC - 1];
+        const bool live = tok < s.len - c * DC;  // (rows behind the last hold the next sequence's)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (STATES && !r_row) break;
           uint32_t d[32];
-          tm_ld16x2(at_a + lanes + 32 * half + 16 * x, at_a + lanes + 64 + 32 * half + 16 * x, d);
+          tm_ld16x2(at_a + 16 * x, at_a + 64 + 16 * x, d);
           if (r_row) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -720,76 +753,43 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
               st_shared_v4(sb + ScanSmem::BR + piece, hi[0], hi[1], hi[2], hi[3]);
               st_shared_v4(sb + ScanSmem::BR + 8192 + piece, lo[0], lo[1], lo[2], lo[3]);
             }
-          } else if (!STATES) {
+          } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) keep[8 * x + e] = fmul2(both(f_row), halves(d, e));
           }
         }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      if (__syncthreads_or(!ok)) break;
-      if (issuer) {
-        tc_fence_after();
-        const SDesc dk = sdesc(sb + ScanSmem::OP + W_KD, 16, 1024, LAYOUT_SW128);
-        const SDesc dp = sdesc(sb + ScanSmem::OP + W_PH - 8192, 16, 1024, LAYOUT_SW128);  // P^ in rows 64-127
-        const SDesc db = sdesc(sb + ScanSmem::BR, 8192, 1024, LAYOUT_SW128);
-        if (mbar_wait(&bar[SB_KD], ph, a.wait_ns, abort_flag)) {
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bar[SB_WR]);
+        if (s_row) {
+          if (!(ok = __all_sync(0xffffffffu, wait(SB_C, c)))) break;
+          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma(at_c, dk + (kk >> 2) * 12288u + (kk & 3) * 32u, db + (kk & 3) * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
-          umma_commit(&bar[SB_C]);
-        }
-        if (mbar_wait(&bar[SB_PH], ph, a.wait_ns, abort_flag)) {
+          for (int x = 0; x < 2; ++x) {
+            uint32_t d[32];
+            tm_ld16x2(at_c + 16 * x, at_c + 64 + 16 * x, d);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma(at_a, dp + kk * 32u, db + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
-          umma_commit(&bar[SB_O]);
+            for (int e = 0; e < 8; ++e) S[8 * x + e] = fmadd2(both(last), S[8 * x + e], halves(d, e));
+            if (c + 1 < nc) put_state(x);
+          }
+          fence_async_smem();
+          tc_fence_before();
+          mbar_arrive(&bar[SB_SR]);
         }
       }
-      __syncwarp();
-      if (loader && c + 1 < nc) load_v(c + 1);
-      if (loader && c + 2 < nc) prefetch(c + 2);
-      ok = mbar_wait(&bar[SB_C], ph, a.wait_ns, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok && loader && c + 1 < nc) load_kd(c + 1);
-      if (ok && s_row) {
-        tc_fence_after();
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t d[32];
-          tm_ld16x2(at_c + lanes + 32 * half + 16 * x, at_c + lanes + 64 + 32 * half + 16 * x, d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) S[8 * x + e] = fmadd2(both(last), S[8 * x + e], halves(d, e));
-          if (c + 1 < nc) put_state(x, c + 1);
-        }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      if (__syncthreads_or(!ok)) break;
+      if (o_row && ok) outputs(nc - 1);
+      if (o_row && (tid & 31) == 0) stores_read();
     }
-    bool gone = c < nc;
-    ok = true;
-    if (!gone && o_row) outputs(nc - 1);
-    if (o_row && (tid & 31) == 0) stores_read();
     tc_fence_before();
-    gone = __syncthreads_or(gone || !ok);
-    if (gone) {
-      // What was issued ends before its memory is given up: the products, and the last copy of each kind (the ones
-      // before have been waited for).
-      if (issuer) {
-        raise_error(a.err, ERR_TIMEOUT);
-        umma_commit(&bar[SB_DRAIN]);
-        mbar_wait_drain(&bar[SB_DRAIN], 0, DRAIN_NS, a.err);
-      }
-      if (loader)
-        for (int x = 0; x < 4; ++x) mbar_wait_drain(&bar[SB_KQ + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
-      __syncthreads();
-    }
-    if (warp == 0) {
+    __syncthreads();
+    if (warp == 8) {
       tc_fence_after();
       tm_free<256>(tmem);
     }
-    if (gone) return;
+    if (*abort_flag) {
+      if (tid == 0) raise_error(a.err, ERR_TIMEOUT);
+      return;
+    }
   }
   if (!STATES && a.hT && s_row) {
     const int to = delta_row(a.hT_row, a.hT_rows, n, a.err);
@@ -806,24 +806,26 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 //     dU = s P^T dO + diag(E) K dS1,   w = B dU,   dS0 = e^(G_C) dS1 + Q~ dO + K~ w,   dv = B (dU - Z^T w)
 // (E = e^(G_C - G)): again two dependent products a chunk.  P^T dO and Q~ dO need no state and are issued a chunk
 // ahead.  dbeta's part of the CTA's columns is (dU - Z^T w) . X.
-// 320 threads, one CTA an SM (the operands take 190 KB): warps 0-7 as in the scan (rows 0-63: tokens; 0-95: the
-// state), warp 8 issues the products, warp 9 the copies; every hand-over through an mbarrier.
+// 512 threads, one CTA an SM (the operands take 220 KB): warps 0-7 have the state's rows (0-95; columns as in the scan),
+// warps 8-15 the tokens' (0-63), so that neither waits for what the other writes out; of the warps that have no rows, 11
+// issues the products and 15 the copies.  Every hand-over through an mbarrier.
 // Tensor memory: P^T dO [0,64), Q~ dO [64,192) (by chunk parity), K dS1 [192,320) and K~ w [320,448) as [hi | lo],
 // Z^T w [448,512).
-constexpr int RSCAN_THREADS = 320;
+constexpr int RSCAN_THREADS = 512;
 struct RSmem {
-  // of the chunk ahead (two places): Q~ hi, lo; P hi, lo; dO
-  static constexpr uint32_t EARLY = 0, E_QT = 0, E_P = 24576, E_DO = 40960, E_BYTES = 49152;
+  // of the chunk ahead (two places): Q~ hi, lo; P hi, lo; dO; X
+  static constexpr uint32_t EARLY = 0, E_QT = 0, E_P = 24576, E_DO = 40960, E_X = 49152, E_BYTES = 57344;
   // K~ hi, lo and Z; K; the state; w; two places of e^G, beta, E.  Products of 128 rows read past operands of 64 and 96
   // rows; what stands there is either as still as the operand or (8 KB behind Z, behind K) never written, and the
   // rows it gives are not looked at.
-  static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 16384, S = K1 + 8192, W = S + 24576, GT = W + 16384,
-                            BAR = GT + 2 * 768, BYTES = BAR + 192;
+  static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 16384, S = K1 + 8192, W = S + 24576, OUT = W + 16384, GT = OUT + 8192,
+                            BAR = GT + 2 * 768, BYTES = BAR + 144;
   static_assert(BYTES <= 232448, "shared memory");
 };
-// (A warp that waits for a phase has to get there before the phase after next: each is tied to something that the warp
-// itself hands over later, K's to nothing that warps 0-7 do, so the decays that come with it have barriers of their own.)
-enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_ZF, RB_DRAIN, RB_GT, RB_N = RB_GT + 2 };
+// Products and copies, then hand-overs: the state, w, Z^T w and X read.  Whoever waits for a phase of a barrier hands
+// something over before the next one can end; where that would not hold (E's, the decays', ZF) there are two, by the
+// chunk's parity.
+enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_DRAIN, RB_ZF, RB_GT = RB_ZF + 2, RB_N = RB_GT + 2 };
 constexpr uint32_t RT_P = 0, RT_Q = 64, RT_A = 192, RT_C = 320, RT_Z = 448;
 
 __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, float* dbeta_part) {
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
   const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = nh / a.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = (warp >> 2) & 1;
   const int row = lane + 32 * q, col0 = tile * TN + 32 * half;
-  const bool t_row = warp < 8 && q < 2, s_row = warp < 8 && q < 3;
+  const bool t_row = warp >= 8 && q < 2, s_row = warp < 8 && q < 3;
   const DeltaSeq s = delta_seq(a, n);
   const int nc = (s.len + DC - 1) / DC;
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
@@ -854,10 +856,10 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
     }
   }
   if (nc > 0) {
-    if (warp == 9) {
+    if (warp == 15) {
       tm_alloc<512>(slot_tm);
       if (lane == 0) {
-        for (int x = 0; x < RB_N; ++x) mbar_init(&bar[x], x == RB_SR ? 192 : x == RB_WR || x == RB_ZF ? 128 : 1);
+        for (int x = 0; x < RB_N; ++x) mbar_init(&bar[x], x == RB_SR ? 192 : x == RB_WR || x == RB_ZF || x == RB_ZF + 1 ? 128 : 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
@@ -869,7 +871,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
     const uint32_t tmem = *slot_tm;
     auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
     bool ok = true;
-    if (warp == 9) {
+    if (warp == 15) {
       if (lane == 0) {
         // copies: each as soon as what stood in its place has been used
         int loads[4] = {};  // EARLY's two places, K, K~
@@ -881,6 +883,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           bulk_load(to + RSmem::E_QT, ws_of(c) + W_QT, 24576, &bar[RB_EF + p]);
           bulk_load(to + RSmem::E_P, ws_of(c) + W_P, 16384, &bar[RB_EF + p]);
           box_load(to + RSmem::E_DO, &maps.dO, &bar[RB_EF + p], tile * TN, h, (int)(s.begin + (long long)c * DC));
+          box_load(to + RSmem::E_X, &maps.x, &bar[RB_EF + p], tile * TN, 0, (s.slot0 + c) * a.H + h);
         };
         auto load_k = [&](int it) {
           const int c = nc - 1 - it, t = (int)(s.begin + (long long)c * DC);
@@ -912,19 +915,19 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         if (nc > 1) load_early(1);
         for (int it = 0; it < nc && ok; ++it) {
           if (it + 2 < nc) prefetch(it + 2);
-          ok = wait(RB_E + (it & 1), it >> 1);
-          if (ok && it + 2 < nc) load_early(it + 2);
-          ok = ok && wait(RB_A, it);
+          ok = wait(RB_A, it);
           if (ok && it + 1 < nc) load_k(it + 1);
           ok = ok && wait(RB_Z, it);
           if (ok && it + 1 < nc) load_kr(it + 1);
+          ok = ok && wait(RB_ZF + (it & 1), it >> 1);  // (X has been read; its other products are long done)
+          if (ok && it + 2 < nc) load_early(it + 2);
         }
         for (int x = 0; x < 4; ++x)
           if (loads[x]) mbar_wait_drain(&bar[RB_EF + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
         for (int it = max(0, loads[2] - 2); it < loads[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
       }
       __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == 11) {
       // products
       const int rest = s.len - (nc - 1) * DC;  // tokens of the last chunk
       if (rest < DC) {  // rows of dO behind them hold the next sequence's
@@ -963,16 +966,19 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           for (int kk = 0; kk < 6; ++kk)
             umma(tmem + RT_A, kk < 4 ? k0 + kk * 32u : k1 + (kk - 4) * 32u, ds + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
           umma_commit(&bar[RB_A]);
+          // (the state's high halves are what the gradients take of it)
+          box_store(&maps.ds, sb + RSmem::S, tile * TN, 0, (s.slot0 + nc - 1 - it) * a.H + h);
           ok = wait(RB_KR, it) && wait(RB_WR, it);
           if (!ok) break;
           tc_fence_after();
+          stores_read();  // (the state is written again once the next product is there)
           const SDesc dr = sdesc(sb + RSmem::KR, 16, 1024, LAYOUT_SW128), dz = sdesc(sb + RSmem::KR + 24576, 8192, 1024, LAYOUT_SW128);
           const SDesc dw = sdesc(sb + RSmem::W, 8192, 1024, LAYOUT_SW128);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma(tmem + RT_C, dr + (kk >> 2) * 12288u + (kk & 3) * 32u, dw + (kk & 3) * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
           umma_commit(&bar[RB_C]);
-          ok = it == 0 || wait(RB_ZF, it - 1);
+          ok = it == 0 || wait(RB_ZF + ((it - 1) & 1), (it - 1) >> 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -983,12 +989,12 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         }
         umma_commit(&bar[RB_DRAIN]);
         mbar_wait_drain(&bar[RB_DRAIN], 0, DRAIN_NS, a.err);
+        stores_read();
       }
       __syncwarp();
-    } else if (s_row) {  // (nothing waits for warps 3 and 7, so they may not wait for the others either)
+    } else if (s_row) {
       const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 32u * half;
-      // bf16 of dS1 of chunk c for the gradients, and hi and lo for the chunk's product
-      auto put_state = [&](int x, int c) {
+      auto put_state = [&](int x) {  // hi and lo for the next chunk's product
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) split2(S[8 * x + e], hi[e], lo[e]);
@@ -998,57 +1004,16 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           st_shared_v4(at, hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
           st_shared_v4(at + 12288, lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
         }
-        st_global_v8(ws_of(c) + W_DS + (row * DV + col0 + 16 * x) * 2, hi);
       };
-      put_state(0, nc - 1);
-      put_state(1, nc - 1);
+      put_state(0);
+      put_state(1);
       fence_async_smem();
       mbar_arrive(&bar[RB_SR]);
-      float2 du[16];
       for (int it = 0; it < nc; ++it) {
-        const int c = nc - 1 - it;
-        const bool live = row < s.len - c * DC;  // (of a token row)
-        uint4 xr[4];
-        if (t_row) {
-          const uint4* src = reinterpret_cast<const uint4*>(ws_of(c) + W_X + (row * DV + col0) * 2);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) xr[i] = __ldcg(src + i);
-        }
-        ok = wait(RB_GT + (it & 1), it >> 1) && wait(RB_E + (it & 1), it >> 1) && wait(RB_A, it);
+        ok = wait(RB_GT + (it & 1), it >> 1) && wait(RB_C, it);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const float* gt = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * 768);
-        const float last = gt[GT_F + DC - 1];
-        const float b_row = t_row ? gt[GT_B + row] : 0.f;
-        if (t_row) {
-          const float e_row = gt[GT_E + row];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t d[32], p[32], hi[8], lo[8];
-            tm_ld16x2(lanes + RT_A + 16 * x, lanes + RT_A + 64 + 16 * x, d);
-            tm_ld16(lanes + RT_P + 16 * x, p);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float2 r = fmadd2(both(e_row), halves(d, e),
-                                fmul2(both(a.scale), make_float2(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]))));
-              r = live ? r : both(0.f);
-              du[8 * x + e] = r;
-              split2(fmul2(both(b_row), r), hi[e], lo[e]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t at = sb + RSmem::W + sw128(row, 4 * half + 2 * x + i);
-              st_shared_v4(at, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-              st_shared_v4(at + 8192, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-            }
-          }
-          fence_async_smem();
-          tc_fence_before();
-          mbar_arrive(&bar[RB_WR]);
-        }
-        ok = wait(RB_C, it);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after();
+        const float last = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * 768)[GT_F + DC - 1];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t d[32], y[32];
@@ -1058,43 +1023,93 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           for (int e = 0; e < 8; ++e)
             S[8 * x + e] = fmadd2(both(last), S[8 * x + e],
                                   fadd2(halves(d, e), make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]))));
-          if (c > 0) put_state(x, c - 1);
+          if (it + 1 < nc) put_state(x);
         }
         fence_async_smem();
         tc_fence_before();
         mbar_arrive(&bar[RB_SR]);
-        if (t_row) {
-          ok = wait(RB_Z, it);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          tc_fence_after();
-          float2 part = both(0.f);
-          __nv_bfloat16* dst = (__nv_bfloat16*)a.dv + ((s.begin + (long long)c * DC + row) * a.H + h) * DV + col0;
+      }
+    } else if (t_row) {
+      const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 32u * half;
+      const uint32_t stage = sb + RSmem::OUT + 2048u * (q + 2 * half);  // this warp's 32 rows x 32 columns
+      float2 du[16];
+      for (int it = 0; it < nc; ++it) {
+        const int c = nc - 1 - it, left = s.len - c * DC;
+        const bool live = row < left;
+        ok = wait(RB_GT + (it & 1), it >> 1) && wait(RB_E + (it & 1), it >> 1) && wait(RB_A, it);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const float* gt = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * 768);
+        const float b_row = gt[GT_B + row], e_row = gt[GT_E + row];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t z[32], w[8];
-            tm_ld16(lanes + RT_Z + 16 * x, z);
+        for (int x = 0; x < 2; ++x) {
+          uint32_t d[32], p[32], hi[8], lo[8];
+          tm_ld16x2(lanes + RT_A + 16 * x, lanes + RT_A + 64 + 16 * x, d);
+          tm_ld16(lanes + RT_P + 16 * x, p);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint4 x4 = xr[2 * x + e / 4];
-              const float2 t = fsub2(du[8 * x + e], make_float2(__uint_as_float(z[2 * e]), __uint_as_float(z[2 * e + 1])));
-              part = fmadd2(t, widen2(e % 4 == 0 ? x4.x : e % 4 == 1 ? x4.y : e % 4 == 2 ? x4.z : x4.w), part);
+          for (int e = 0; e < 8; ++e) {
+            float2 r = fmadd2(both(e_row), halves(d, e),
+                              fmul2(both(a.scale), make_float2(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]))));
+            r = live ? r : both(0.f);  // (rows behind the last hold the next sequence's)
+            du[8 * x + e] = r;
+            split2(fmul2(both(b_row), r), hi[e], lo[e]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t at = sb + RSmem::W + sw128(row, 4 * half + 2 * x + i);
+            st_shared_v4(at, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+            st_shared_v4(at + 8192, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bar[RB_WR]);
+        if (lane == 0) stores_read();
+        ok = wait(RB_EF + (it & 1), it >> 1) && wait(RB_Z, it);  // (X came with the chunk's early operands)
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        float2 part = both(0.f);
+        const long long t0 = s.begin + (long long)c * DC;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t z[32], w[8];
+          tm_ld16(lanes + RT_Z + 16 * x, z);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 x4 = ld_shared_v4(sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES + RSmem::E_X + sw128(row, 4 * half + 2 * x + i));
+            const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = 4 * i + e;
+              const float2 t = fsub2(du[8 * x + at], make_float2(__uint_as_float(z[2 * at]), __uint_as_float(z[2 * at + 1])));
+              part = fmadd2(t, widen2(xw[e]), part);
               const float2 y = fmul2(both(b_row), t);
-              w[e] = bf2(y.x, y.y);
-            }
-            if (live) {
-              reinterpret_cast<uint4*>(dst)[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(dst)[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+              w[at] = bf2(y.x, y.y);
             }
           }
-          tc_fence_before();
-          mbar_arrive(&bar[RB_ZF]);
-          if (live) dbeta_part[((long long)(2 * tile + half) * tokens + s.begin + (long long)c * DC + row) * a.H + h] = part.x + part.y;
+          if (left >= DC) {
+            st_shared_v4(stage + sw64(lane, 2 * x), w[0], w[1], w[2], w[3]);
+            st_shared_v4(stage + sw64(lane, 2 * x + 1), w[4], w[5], w[6], w[7]);
+          } else if (live) {  // a sequence's last rows: no box is written past them
+            uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.dv + ((t0 + row) * a.H + h) * DV + col0);
+            dst[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
         }
+        tc_fence_before();
+        mbar_arrive(&bar[RB_ZF + (it & 1)]);
+        if (left >= DC) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) box_store(&maps.dvo, stage, col0, h, (int)(t0 + 32 * q));
+        }
+        if (live) dbeta_part[((long long)(2 * tile + half) * tokens + t0 + row) * a.H + h] = part.x + part.y;
       }
+      if (lane == 0) stores_read();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 15) {
       tc_fence_after();
       tm_free<512>(tmem);
     }
@@ -1476,7 +1491,8 @@ cudaError_t launch_delta_tc_bwd(const DeltaArgs& a, cudaStream_t st) {
     const long long all = (long long)a.slots * a.H;
     if (!(input_maps(m, a) && rows_map(&m.dO, a.dO, DV, a, 64, DC) && rows_map(&m.dv, a.dv, DV, a, 64, DC) &&
           map3(&m.x, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 64, DC, 1) && map3(&m.s0, a.ws + W_S0, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) &&
-          map3(&m.ds, a.ws + W_DS, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1)))
+          map3(&m.ds, a.ws + W_DS, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) && map3(&m.xo, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 32, 32, 1) &&
+          rows_map(&m.dvo, a.dv, DV, a, 32, 32)))
       return cudaErrorInvalidValue;
     delta_prep_kernel<true><<<chunks, PREP_THREADS, PrepSmem::bytes(true), st>>>(m, a);
     delta_scan_kernel<true><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a);
