@@ -758,10 +758,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# The current device without the call's check that CUDA is set up (a CUDA tensor is at hand).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _run(fn, where, dev, *args):
     """Calls the library with `dev` current, on its current stream."""
     i = dev.index
-    if torch.cuda.current_device() == i:
+    if _current_device() == i:
         rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
@@ -1161,7 +1165,7 @@ def gla_slot_plan(new_len, held, seen, pool_rows: int, budget: int, out=None):
         raise ValueError("budget must not be negative")
     sizes = (N + 1, N, N, N, budget, budget)
     if out is None:
-        out = SlotPlan(*torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes))
+        out = SlotPlan(*torch.empty(3 * N + N + 1 + 2 * budget, dtype=torch.int32, device=dev).split_with_sizes(sizes))
     else:
         for name, t, size in zip(SlotPlan._fields, out, sizes):
             _good(t, "out." + name, torch.int32, dev, size)

@@ -17,13 +17,17 @@ namespace {
 constexpr int VCOLS = DV / 4;  // 48 four-column vectors of a row
 template <class ST> struct StepCfg;
 template <> struct StepCfg<float> { static constexpr int THREADS = 576, MIN_BLOCKS = 2; };
-template <> struct StepCfg<__nv_bfloat16> { static constexpr int THREADS = 288, MIN_BLOCKS = 4; };
+template <> struct StepCfg<__nv_bfloat16> { static constexpr int THREADS = 288, MIN_BLOCKS = 3; };
 
 __device__ __forceinline__ float4 widen(float4 x) { return x; }
 __device__ __forceinline__ float4 widen(uint2 u) {
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
                      __uint_as_float(u.y & 0xFFFF0000u));
 }
+// Keeps a packed vector packed: the compiler would otherwise hold on to its widened form, twice the registers, from
+// one use to the next.
+__device__ __forceinline__ void stay(float4&) {}
+__device__ __forceinline__ void stay(uint2& x) { asm volatile("" : "+r"(x.x), "+r"(x.y)); }
 __device__ __forceinline__ uint2 pack4(float4 x) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
@@ -48,8 +52,8 @@ delta_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
   using TV = typename Vec4<T>::type;
   __shared__ float s_q[DK], s_k[DK];
   __shared__ float s_qk;
+  __shared__ float4 s_v[VCOLS];
   __shared__ float4 s_part[2][RG][VCOLS];  // S^T k, S^T q
-  __shared__ float4 s_u[VCOLS];
   const long long nh = blockIdx.x;
   const int n = (int)(nh / H), h = (int)(nh % H), tid = threadIdx.x, c = tid % VCOLS, r = tid / VCOLS;
   const int row = slot ? slot[n] : n;
@@ -65,7 +69,8 @@ delta_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     s_q[tid] = scale * to_f(q[nh * DK + tid]);
     s_k[tid] = to_f(k[nh * DK + tid]);
   }
-  const float a = expf(to_f(g[nh]));
+  if (tid >= DK && tid < DK + VCOLS) s_v[tid - DK] = widen(reinterpret_cast<const TV*>(v + nh * DV)[tid - DK]);
+  const float a = expf(to_f(g[nh])), b = to_f(beta[nh]);
   __syncthreads();
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 dk = zero, dq = zero;
@@ -86,18 +91,15 @@ delta_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     if (tid == 0) s_qk = d;
   }
   __syncthreads();
-  if (tid < VCOLS) {
-    float4 x = zero;
+  // every thread for its own columns: another barrier would cost more than these sums
+  float4 u = zero;
 #pragma unroll
-    for (int i = 0; i < RG; ++i) x = fma4(1.f, s_part[0][i][tid], x);
-    const float4 vv = widen(reinterpret_cast<const TV*>(v + nh * DV)[tid]);
-    const float b = to_f(beta[nh]);
-    s_u[tid] = make_float4(b * fmaf(-a, x.x, vv.x), b * fmaf(-a, x.y, vv.y), b * fmaf(-a, x.z, vv.z), b * fmaf(-a, x.w, vv.w));
-  }
-  __syncthreads();
-  const float4 u = s_u[c];
+  for (int i = 0; i < RG; ++i) u = fma4(1.f, s_part[0][i][c], u);
+  const float4 vv = s_v[c];
+  u = make_float4(b * fmaf(-a, u.x, vv.x), b * fmaf(-a, u.y, vv.y), b * fmaf(-a, u.z, vv.z), b * fmaf(-a, u.w, vv.w));
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
+    stay(s[i]);
     const float4 x = widen(s[i]);
     const float kk = s_k[r + RG * i];
     put4(S + (r + RG * i) * VCOLS + c,

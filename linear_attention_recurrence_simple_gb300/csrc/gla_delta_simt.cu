@@ -6,8 +6,10 @@
 //           tiles are independent.  In the backward it keeps each chunk's S0 and X instead of writing o
 //   rscan   the same in reverse for dS; writes dv, dS1 of every chunk and its columns' part of dbeta
 //   grads   one CTA a (chunk, head): dq, dk, dg, and dbeta's parts summed in tile order
-// The operands of a product stand in shared memory with an odd row stride; every thread has a small tile of the
-// result in registers.  Bound by shared-memory loads (about 0.7 a multiply-add).
+// The operands of a product stand in shared memory with the summed index contiguous (where both ways are needed,
+// twice), so that a thread reads four of its steps at once: rows of 4 mod 32 words apart, free of bank conflicts.
+// Every thread has a small tile of the result in registers.  Few CTAs on short calls: bound by latency, so a chunk's
+// loads go out together, in vectors.
 #include "gla_delta.cuh"
 #include "gla_once.cuh"
 
@@ -17,8 +19,8 @@ namespace {
 constexpr int SB = 32;             // columns of d_v a scan CTA has
 constexpr int SNB = DV / SB;       // 6
 constexpr int THREADS = 256;
-constexpr int KS = DK + 1, CS = DC + 1, BS = SB + 1;  // row strides in shared memory
-constexpr int ZS = DC + 4;         // the solve reads rows in vectors of four
+constexpr int KS = DK + 4, CS = DC + 4, BS = SB + 4;  // row strides in shared memory
+constexpr int I16 = 16 * CS, K16 = 16 * KS, B16 = 16 * BS;  // a thread's rows are 16 apart
 
 // Workspace of a (chunk place, head), in floats.
 constexpr long long WS_Z = 0, WS_P = WS_Z + DC * DC, WS_GT = WS_P + DC * DC, WS_FWD = WS_GT + 5 * DC;
@@ -29,60 +31,97 @@ template <bool BWD>
 __device__ __forceinline__ float* ws_of(const DeltaArgs& a, int slot, int h) {
   return reinterpret_cast<float*>(a.ws) + ((long long)slot * a.H + h) * (BWD ? WS_BWD : WS_FWD);
 }
-// rows [0, C) of a [tokens, H, D] tensor, columns [c0, c0 + W), zeros from row `len` on
-template <int W, int STRIDE, class T>
-__device__ __forceinline__ void load_rows(float* dst, const T* src, long long t0, int len, int H, int h, int D, int c0) {
-  for (int e = threadIdx.x; e < DC * W; e += THREADS) {
-    const int i = e / W, c = e % W;
-    dst[i * STRIDE + c] = i < len ? to_f(src[((t0 + i) * H + h) * D + c0 + c]) : 0.f;
+// N vectors of four, this thread's x-th being vector tid + x * THREADS of the source: loaded together, then placed.
+template <int N, class G, class P>
+__device__ __forceinline__ void copy4(G get, P put) {
+  constexpr int PER = (N + THREADS - 1) / THREADS;
+  float4 v[PER];
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int e = threadIdx.x + x * THREADS;
+    v[x] = N % THREADS == 0 || e < N ? get(e) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int e = threadIdx.x + x * THREADS;
+    if (N % THREADS == 0 || e < N) put(e, v[x]);
   }
 }
-// acc[r][c] += sum_k A(k, row r) B(k, column c): rows i0 + r * IS, columns j0 + c * JS
-template <int NR, int NC, int K, class FA, class FB>
-__device__ __forceinline__ void gemm(float (&acc)[NR][NC], FA fa, FB fb) {
+__device__ __forceinline__ void put_row(float* at, float4 v) { *reinterpret_cast<float4*>(at) = v; }
+template <int STRIDE>
+__device__ __forceinline__ void put_column(float* at, float4 v) {
+  at[0] = v.x;
+  at[STRIDE] = v.y;
+  at[2 * STRIDE] = v.z;
+  at[3 * STRIDE] = v.w;
+}
+// Rows [0, C) of a [tokens, H, D] tensor, columns [c0, c0 + W), zeros from row `len` on.
+template <int W, class P>
+__device__ __forceinline__ void load_rows(const float* src, long long t0, int len, int H, int h, int D, int c0, P put) {
+  copy4<DC * W / 4>(
+      [&](int e) {
+        const int i = e / (W / 4), c = e % (W / 4) * 4;
+        return i < len ? *reinterpret_cast<const float4*>(src + ((t0 + i) * H + h) * D + c0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      },
+      [&](int e, float4 v) { put(e / (W / 4), e % (W / 4) * 4, v); });
+}
+// Rows [0, R) x W floats, row stride LD, of the workspace.
+template <int R, int W, int LD, class P>
+__device__ __forceinline__ void load_ws(const float* src, P put) {
+  copy4<R * W / 4>([&](int e) { return *reinterpret_cast<const float4*>(src + e / (W / 4) * LD + e % (W / 4) * 4); },
+                   [&](int e, float4 v) { put(e / (W / 4), e % (W / 4) * 4, v); });
+}
+// acc[r][c] += sum_k A[r * AS + k] B[c * BS + k]
+template <int NR, int NC, int K, int AS, int BS>
+__device__ __forceinline__ void gemm(float (&acc)[NR][NC], const float* a, const float* b) {
 #pragma unroll 4
-  for (int k = 0; k < K; ++k) {
-    float x[NR], y[NC];
+  for (int k = 0; k < K; k += 4) {
+    float4 x[NR], y[NC];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) x[r] = fa(k, r);
+    for (int r = 0; r < NR; ++r) x[r] = *reinterpret_cast<const float4*>(a + r * AS + k);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) y[c] = fb(k, c);
+    for (int c = 0; c < NC; ++c) y[c] = *reinterpret_cast<const float4*>(b + c * BS + k);
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) acc[r][c] = fmaf(x[r], y[c], acc[r][c]);
+      for (int c = 0; c < NC; ++c)
+        acc[r][c] = fmaf(x[r].x, y[c].x, fmaf(x[r].y, y[c].y, fmaf(x[r].z, y[c].z, fmaf(x[r].w, y[c].w, acc[r][c]))));
   }
 }
 
 // ---- prep -------------------------------------------------------------------------------------
-template <class T, bool BWD>
+constexpr int PREP_FLOATS = 2 * DC * KS + 2 * DC * CS;
+
+template <bool BWD>
 __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArgs a) {
-  extern __shared__ float sm[];
-  float* const sk = sm;                // [64][97], then M and M B [64][68]
+  extern __shared__ __align__(16) float sm[];
+  float* const sk = sm;             // [64][100]
   float* const sq = sk + DC * KS;
+  float* const m = sq + DC * KS;    // [64][68]: M and M B
+  float* const mb = m + DC * CS;
   __shared__ float2 sg[DC];
   __shared__ float sb[DC];
   const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
   const DeltaChunk ch = chunk_of_slot(a, slot);
   if (ch.len == 0) return;
   float* const ws = ws_of<BWD>(a, slot, h);
-  load_rows<DK, KS>(sk, (const T*)a.k, ch.t0, ch.len, a.H, h, DK, 0);
-  load_rows<DK, KS>(sq, (const T*)a.q, ch.t0, ch.len, a.H, h, DK, 0);
   if (tid < 32) {
-    const T* g = (const T*)a.g + ch.t0 * a.H + h;
-    const T* b = (const T*)a.beta + ch.t0 * a.H + h;
+    const float* g = (const float*)a.g + ch.t0 * a.H + h;
+    const float* b = (const float*)a.beta + ch.t0 * a.H + h;
     float x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * tid + e;
-      x[e] = i < ch.len ? to_f(g[(long long)i * a.H]) : 0.f;
-      sb[i] = i < ch.len ? to_f(b[(long long)i * a.H]) : 0.f;
+      x[e] = i < ch.len ? g[(long long)i * a.H] : 0.f;
+      sb[i] = i < ch.len ? b[(long long)i * a.H] : 0.f;
     }
     float2 s0, s1;
     delta_sums(x[0], x[1], s0, s1);
     sg[2 * tid] = s0;
     sg[2 * tid + 1] = s1;
   }
+  load_rows<DK>((const float*)a.k, ch.t0, ch.len, a.H, h, DK, 0, [&](int i, int c, float4 v) { put_row(sk + i * KS + c, v); });
+  load_rows<DK>((const float*)a.q, ch.t0, ch.len, a.H, h, DK, 0, [&](int i, int c, float4 v) { put_row(sq + i * KS + c, v); });
   __syncthreads();
   if (tid < DC) {
     ws[WS_GT + GT_HI + tid] = sg[tid].x;
@@ -93,11 +132,8 @@ __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArg
   }
   const int ti = tid / 16, tj = tid % 16;
   float kk[4][4] = {}, qk[4][4] = {};
-  gemm<4, 4, DK>(kk, [&](int x, int r) { return sk[(ti + 16 * r) * KS + x]; }, [&](int x, int c) { return sk[(tj + 16 * c) * KS + x]; });
-  gemm<4, 4, DK>(qk, [&](int x, int r) { return sq[(ti + 16 * r) * KS + x]; }, [&](int x, int c) { return sk[(tj + 16 * c) * KS + x]; });
-  __syncthreads();
-  float* const m = sm;
-  float* const mb = sm + DC * ZS;
+  gemm<4, 4, DK, K16, K16>(kk, sk + ti * KS, sk + tj * KS);
+  gemm<4, 4, DK, K16, K16>(qk, sq + ti * KS, sk + tj * KS);
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -106,100 +142,111 @@ __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArg
       const float d = j <= i ? delta_decay(sg[i], sg[j]) : 0.f;
       ws[WS_P + i * DC + j] = j <= i ? d * qk[r][c] : 0.f;
       const float x = j < i ? d * kk[r][c] : 0.f;
-      m[i * ZS + j] = x;
-      mb[i * ZS + j] = x * sb[j];
+      m[i * CS + j] = x;
+      mb[i * CS + j] = x * sb[j];
     }
   __syncthreads();
   if (tid < DC) {
     float z[DC];
-    delta_solve_column<ZS>(m, mb, tid, z);
+    delta_solve_column<CS>(m, mb, tid, z);
 #pragma unroll
     for (int i = 0; i < DC; ++i) ws[WS_Z + i * DC + tid] = z[i];
   }
 }
 
 // ---- forward scan ---------------------------------------------------------------------------
-constexpr int SCAN_FLOATS = DK * BS + 2 * DC * KS + 2 * DC * CS + 2 * DC * BS + 3 * DC;
+constexpr int SCAN_FLOATS = SB * KS + 2 * DC * KS + DK * CS + 2 * DC * CS + 2 * SB * CS + 3 * DC;
 
-template <class T, bool BWD>
+template <bool BWD>
 __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArgs a) {
-  extern __shared__ float sm[];
-  float* const S = sm;                 // [96][33]
-  float* const sk = S + DK * BS;       // [64][97]
+  extern __shared__ __align__(16) float sm[];
+  float* const S = sm;                 // [32][100]: columns of the state
+  float* const sk = S + SB * KS;       // [64][100]
   float* const sq = sk + DC * KS;
-  float* const sz = sq + DC * KS;      // [64][65]
+  float* const st = sq + DC * KS;      // [96][68]: K^T, weighted with e^(G_C - G)
+  float* const sz = st + DK * CS;      // [64][68]
   float* const sp = sz + DC * CS;
-  float* const sr = sp + DC * CS;      // [64][33]: B R
-  float* const su = sr + DC * BS;      // [64][33]: U
-  float* const sf = su + DC * BS;      // e^G, e^(G_C - G), beta
+  float* const sr = sp + DC * CS;      // [32][68]: columns of B R
+  float* const su = sr + SB * CS;      // [32][68]: columns of U
+  float* const sf = su + SB * CS;      // e^G, e^(G_C - G), beta
   const int tile = blockIdx.x % SNB, nh = blockIdx.x / SNB, h = nh % a.H, n = nh / a.H, tid = threadIdx.x;
   const int c0 = tile * SB;
   const DeltaSeq s = delta_seq(a, n);
   const int from = a.h0 ? delta_row(a.h0_row, a.h0_rows, n, a.err) : -1;
-  for (int e = tid; e < DK * SB; e += THREADS)
-    S[e / SB * BS + e % SB] = from >= 0 ? a.h0[(((long long)from * a.H + h) * DK + e / SB) * DV + c0 + e % SB] : 0.f;
+  if (from >= 0)
+    load_ws<DK, SB, DV>(a.h0 + ((long long)from * a.H + h) * (DK * DV) + c0, [&](int x, int c, float4 v) { put_column<KS>(S + c * KS + x, v); });
+  else
+    for (int e = tid; e < SB * KS; e += THREADS) S[e] = 0.f;
   const int ti = tid / 16, tj = tid % 16;  // rows ti + 16 r, columns tj + 16 c
   for (int c = 0; c * DC < s.len; ++c) {
     const int len = min(DC, s.len - c * DC);
     const long long t0 = s.begin + (long long)c * DC;
     float* const ws = ws_of<BWD>(a, s.slot0 + c, h);
+    float v[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        v[i][j] = ti + 16 * i < len ? ((const float*)a.v)[((t0 + ti + 16 * i) * a.H + h) * DV + c0 + tj + 16 * j] : 0.f;
     __syncthreads();
-    load_rows<DK, KS>(sk, (const T*)a.k, t0, len, a.H, h, DK, 0);
-    if (!BWD) load_rows<DK, KS>(sq, (const T*)a.q, t0, len, a.H, h, DK, 0);
-    for (int e = tid; e < DC * DC; e += THREADS) {
-      sz[e / DC * CS + e % DC] = ws[WS_Z + e];
-      if (!BWD) sp[e / DC * CS + e % DC] = ws[WS_P + e];
-    }
     if (tid < 3 * DC) sf[tid] = ws[WS_GT + GT_F + tid];
-    if (BWD)
-      for (int e = tid; e < DK * SB; e += THREADS) ws[WS_S0 + e / SB * DV + c0 + e % SB] = S[e / SB * BS + e % SB];
+    load_rows<DK>((const float*)a.k, t0, len, a.H, h, DK, 0, [&](int i, int x, float4 y) {
+      put_row(sk + i * KS + x, y);
+      put_column<CS>(st + x * CS + i, y);
+    });
+    if (!BWD) load_rows<DK>((const float*)a.q, t0, len, a.H, h, DK, 0, [&](int i, int x, float4 y) { put_row(sq + i * KS + x, y); });
+    load_ws<DC, DC, DC>(ws + WS_Z, [&](int i, int j, float4 y) { put_row(sz + i * CS + j, y); });
+    if (!BWD) load_ws<DC, DC, DC>(ws + WS_P, [&](int i, int j, float4 y) { put_row(sp + i * CS + j, y); });
     __syncthreads();
+    if (BWD)
+      for (int e = tid; e < DK * SB; e += THREADS) ws[WS_S0 + e / SB * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
     float ks[4][2] = {}, qs[4][2] = {}, r[4][2];
-    gemm<4, 2, DK>(ks, [&](int x, int i) { return sk[(ti + 16 * i) * KS + x]; }, [&](int x, int j) { return S[x * BS + tj + 16 * j]; });
-    if (!BWD)
-      gemm<4, 2, DK>(qs, [&](int x, int i) { return sq[(ti + 16 * i) * KS + x]; }, [&](int x, int j) { return S[x * BS + tj + 16 * j]; });
+    gemm<4, 2, DK, K16, K16>(ks, sk + ti * KS, S + tj * KS);
+    if (!BWD) gemm<4, 2, DK, K16, K16>(qs, sq + ti * KS, S + tj * KS);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = ti + 16 * i, col = tj + 16 * j;
-        const float v = row < len ? to_f(((const T*)a.v)[((t0 + row) * a.H + h) * DV + c0 + col]) : 0.f;
-        r[i][j] = fmaf(-sf[row], ks[i][j], v);
-        sr[row * BS + col] = sf[2 * DC + row] * r[i][j];
+        const int row = ti + 16 * i;
+        r[i][j] = fmaf(-sf[row], ks[i][j], v[i][j]);
+        sr[(tj + 16 * j) * CS + row] = sf[2 * DC + row] * r[i][j];
       }
     __syncthreads();
     float zr[4][2] = {};
-    gemm<4, 2, DC>(zr, [&](int x, int i) { return sz[(ti + 16 * i) * CS + x]; }, [&](int x, int j) { return sr[x * BS + tj + 16 * j]; });
+    gemm<4, 2, DC, I16, I16>(zr, sz + ti * CS, sr + tj * CS);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = ti + 16 * i, col = tj + 16 * j;
         const float x = r[i][j] - zr[i][j];
-        su[row * BS + col] = sf[2 * DC + row] * x;
+        su[col * CS + row] = sf[2 * DC + row] * x;
         if (BWD) ws[WS_X + row * DV + c0 + col] = x;
       }
     __syncthreads();
     if (!BWD) {
       float pu[4][2] = {};
-      gemm<4, 2, DC>(pu, [&](int x, int i) { return sp[(ti + 16 * i) * CS + x]; }, [&](int x, int j) { return su[x * BS + tj + 16 * j]; });
+      gemm<4, 2, DC, I16, I16>(pu, sp + ti * CS, su + tj * CS);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int row = ti + 16 * i, col = tj + 16 * j;
+          const int row = ti + 16 * i;
           if (row < len)
-            ((T*)a.o)[((t0 + row) * a.H + h) * DV + c0 + col] = from_f<T>(a.scale * fmaf(sf[row], qs[i][j], pu[i][j]));
+            ((float*)a.o)[((t0 + row) * a.H + h) * DV + c0 + tj + 16 * j] = a.scale * fmaf(sf[row], qs[i][j], pu[i][j]);
         }
     }
+    // e^(G_C - G) goes to U, which nothing else reads any more
+    for (int e = tid; e < SB * DC; e += THREADS) sr[e / DC * CS + e % DC] = sf[DC + e % DC] * su[e / DC * CS + e % DC];
+    __syncthreads();
     float ds[6][2] = {};
-    gemm<6, 2, DC>(ds, [&](int x, int i) { return sk[x * KS + ti + 16 * i] * sf[DC + x]; }, [&](int x, int j) { return su[x * BS + tj + 16 * j]; });
+    gemm<6, 2, DC, I16, I16>(ds, st + ti * CS, sr + tj * CS);
     const float last = sf[DC - 1];
 #pragma unroll
     for (int i = 0; i < 6; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float* const at = S + (ti + 16 * i) * BS + tj + 16 * j;  // (this thread's own, and nothing reads S here)
+        float* const at = S + (tj + 16 * j) * KS + ti + 16 * i;  // (this thread's own, and nothing reads S here)
         *at = fmaf(last, *at, ds[i][j]);
       }
   }
@@ -208,60 +255,70 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
     const int to = delta_row(a.hT_row, a.hT_rows, n, a.err);
     if (to >= 0)
       for (int e = tid; e < DK * SB; e += THREADS)
-        a.hT[(((long long)to * a.H + h) * DK + e / SB) * DV + c0 + e % SB] = S[e / SB * BS + e % SB];
+        a.hT[(((long long)to * a.H + h) * DK + e / SB) * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
   }
 }
 
 // ---- reverse scan ---------------------------------------------------------------------------
-// (the same shared memory as the scan: dO in the place of U, and the part of dbeta behind the decays)
-template <class T>
+constexpr int RSCAN_FLOATS = SB * KS + DC * KS + 2 * DK * CS + 2 * DC * CS + 3 * SB * CS + 3 * DC;
+
 __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaArgs a, float* dbeta_part) {
-  extern __shared__ float sm[];
-  float* const S = sm;  // dS
-  float* const sk = S + DK * BS;
-  float* const sq = sk + DC * KS;
-  float* const sz = sq + DC * KS;
-  float* const sp = sz + DC * CS;
-  float* const sw = sp + DC * CS;   // B dU, then -e^G dR
-  float* const sd = sw + DC * BS;   // dO
-  float* const sf = sd + DC * BS;
+  extern __shared__ __align__(16) float sm[];
+  float* const S = sm;              // [32][100]: columns of dS
+  float* const sk = S + SB * KS;    // [64][100]
+  float* const skt = sk + DC * KS;  // [96][68]: K^T, Q^T
+  float* const sqt = skt + DK * CS;
+  float* const szt = sqt + DK * CS; // [64][68]: Z^T, P^T
+  float* const spt = szt + DC * CS;
+  float* const sw = spt + DC * CS;  // [32][68]: columns of B dU, of -e^G dR
+  float* const sn = sw + SB * CS;
+  float* const sd = sn + SB * CS;   // [32][68]: columns of dO, then weighted with s e^G
+  float* const sf = sd + SB * CS;
   const int tile = blockIdx.x % SNB, nh = blockIdx.x / SNB, h = nh % a.H, n = nh / a.H, tid = threadIdx.x;
   const int c0 = tile * SB;
   const DeltaSeq s = delta_seq(a, n);
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
-  for (int e = tid; e < DK * SB; e += THREADS)
-    S[e / SB * BS + e % SB] = a.dhT ? a.dhT[(((long long)n * a.H + h) * DK + e / SB) * DV + c0 + e % SB] : 0.f;
+  if (a.dhT)
+    load_ws<DK, SB, DV>(a.dhT + ((long long)n * a.H + h) * (DK * DV) + c0, [&](int x, int c, float4 v) { put_column<KS>(S + c * KS + x, v); });
+  else
+    for (int e = tid; e < SB * KS; e += THREADS) S[e] = 0.f;
   const int ti = tid / 16, tj = tid % 16;
   for (int c = (s.len + DC - 1) / DC - 1; c >= 0; --c) {
     const int len = min(DC, s.len - c * DC);
     const long long t0 = s.begin + (long long)c * DC;
     float* const ws = ws_of<true>(a, s.slot0 + c, h);
+    float x[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) x[i][j] = ws[WS_X + (ti + 16 * i) * DV + c0 + tj + 16 * j];
     __syncthreads();
-    load_rows<DK, KS>(sk, (const T*)a.k, t0, len, a.H, h, DK, 0);
-    load_rows<DK, KS>(sq, (const T*)a.q, t0, len, a.H, h, DK, 0);
-    load_rows<SB, BS>(sd, (const T*)a.dO, t0, len, a.H, h, DV, c0);
-    for (int e = tid; e < DC * DC; e += THREADS) {
-      sz[e / DC * CS + e % DC] = ws[WS_Z + e];
-      sp[e / DC * CS + e % DC] = ws[WS_P + e];
-    }
     if (tid < 3 * DC) sf[tid] = ws[WS_GT + GT_F + tid];
-    for (int e = tid; e < DK * SB; e += THREADS) ws[WS_DS + e / SB * DV + c0 + e % SB] = S[e / SB * BS + e % SB];
+    load_rows<DK>((const float*)a.k, t0, len, a.H, h, DK, 0, [&](int i, int e, float4 y) {
+      put_row(sk + i * KS + e, y);
+      put_column<CS>(skt + e * CS + i, y);
+    });
+    load_rows<DK>((const float*)a.q, t0, len, a.H, h, DK, 0, [&](int i, int e, float4 y) { put_column<CS>(sqt + e * CS + i, y); });
+    load_rows<SB>((const float*)a.dO, t0, len, a.H, h, DV, c0, [&](int i, int e, float4 y) { put_column<CS>(sd + e * CS + i, y); });
+    load_ws<DC, DC, DC>(ws + WS_Z, [&](int i, int j, float4 y) { put_column<CS>(szt + j * CS + i, y); });
+    load_ws<DC, DC, DC>(ws + WS_P, [&](int i, int j, float4 y) { put_column<CS>(spt + j * CS + i, y); });
     __syncthreads();
+    for (int e = tid; e < DK * SB; e += THREADS) ws[WS_DS + e / SB * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
     float kd[4][2] = {}, pd[4][2] = {}, du[4][2];
-    gemm<4, 2, DK>(kd, [&](int x, int i) { return sk[(ti + 16 * i) * KS + x]; }, [&](int x, int j) { return S[x * BS + tj + 16 * j]; });
-    gemm<4, 2, DC>(pd, [&](int x, int i) { return sp[x * CS + ti + 16 * i]; }, [&](int x, int j) { return sd[x * BS + tj + 16 * j]; });
+    gemm<4, 2, DK, K16, K16>(kd, sk + ti * KS, S + tj * KS);
+    gemm<4, 2, DC, I16, I16>(pd, spt + ti * CS, sd + tj * CS);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = ti + 16 * i;
         du[i][j] = fmaf(sf[DC + row], kd[i][j], a.scale * pd[i][j]);
-        sw[row * BS + tj + 16 * j] = sf[2 * DC + row] * du[i][j];
+        sw[(tj + 16 * j) * CS + row] = sf[2 * DC + row] * du[i][j];
       }
     __syncthreads();
     float zw[4][2] = {}, part[4] = {};
-    gemm<4, 2, DC>(zw, [&](int x, int i) { return sz[x * CS + ti + 16 * i]; }, [&](int x, int j) { return sw[x * BS + tj + 16 * j]; });
-    __syncthreads();
+    gemm<4, 2, DC, I16, I16>(zw, szt + ti * CS, sw + tj * CS);
+    for (int e = tid; e < SB * DC; e += THREADS) sd[e / DC * CS + e % DC] *= a.scale * sf[e % DC];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = ti + 16 * i;
@@ -269,9 +326,9 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
       for (int j = 0; j < 2; ++j) {
         const int col = tj + 16 * j;
         const float dut = du[i][j] - zw[i][j], dr = sf[2 * DC + row] * dut;
-        part[i] = fmaf(dut, ws[WS_X + row * DV + c0 + col], part[i]);
-        if (row < len) ((T*)a.dv)[((t0 + row) * a.H + h) * DV + c0 + col] = from_f<T>(dr);
-        sw[row * BS + col] = -sf[row] * dr;
+        part[i] = fmaf(dut, x[i][j], part[i]);
+        if (row < len) ((float*)a.dv)[((t0 + row) * a.H + h) * DV + c0 + col] = dr;
+        sn[col * CS + row] = -sf[row] * dr;
       }
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) part[i] += __shfl_xor_sync(0xffffffffu, part[i], off);
@@ -279,38 +336,40 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
     }
     __syncthreads();
     float ds[6][2] = {};
-    gemm<6, 2, DC>(ds, [&](int x, int i) { return sq[x * KS + ti + 16 * i] * (a.scale * sf[x]); }, [&](int x, int j) { return sd[x * BS + tj + 16 * j]; });
-    gemm<6, 2, DC>(ds, [&](int x, int i) { return sk[x * KS + ti + 16 * i]; }, [&](int x, int j) { return sw[x * BS + tj + 16 * j]; });
+    gemm<6, 2, DC, I16, I16>(ds, sqt + ti * CS, sd + tj * CS);
+    gemm<6, 2, DC, I16, I16>(ds, skt + ti * CS, sn + tj * CS);
     const float last = sf[DC - 1];
 #pragma unroll
     for (int i = 0; i < 6; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float* const at = S + (ti + 16 * i) * BS + tj + 16 * j;
+        float* const at = S + (tj + 16 * j) * KS + ti + 16 * i;
         *at = fmaf(last, *at, ds[i][j]);
       }
   }
   __syncthreads();
   if (a.dh0)
     for (int e = tid; e < DK * SB; e += THREADS)
-      a.dh0[(((long long)n * a.H + h) * DK + e / SB) * DV + c0 + e % SB] = S[e / SB * BS + e % SB];
+      a.dh0[(((long long)n * a.H + h) * DK + e / SB) * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
 }
 
 // ---- gradients of the chunk ------------------------------------------------------------------
-constexpr int GRAD_FLOATS = 2 * DC * KS + 3 * DC * BS + 2 * DK * BS + 2 * DC;
-static_assert(2 * DC * CS <= 3 * DC * BS + 2 * DK * BS, "the masked products take the pieces' place");
+// pieces of 32 columns: dO, dR, U [64][36], S0, dS1 [96][36]; then Es, Fm and their transposes [64][68] in their place, and
+// K^T, Q^T [96][68]
+constexpr int PIECES = 3 * DC * BS + 2 * DK * BS, GRAD_FLOATS = 2 * DC * KS + 2 * DK * CS + (PIECES > 4 * DC * CS ? PIECES : 4 * DC * CS) + DC;
 
-template <class T>
 __global__ void __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaArgs a, const float* dbeta_part) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   float* const sk = sm;
   float* const sq = sk + DC * KS;
-  float* const sdo = sq + DC * KS;       // [64][33] dO, dR, U
+  float* const skt = sq + DC * KS;
+  float* const sqt = skt + DK * CS;
+  float* const sdo = sqt + DK * CS;
   float* const sdr = sdo + DC * BS;
   float* const su = sdr + DC * BS;
-  float* const ss = su + DC * BS;        // [96][33] S0, dS1
+  float* const ss = su + DC * BS;
   float* const sd = ss + DK * BS;
-  float* const sdg = sd + DK * BS;       // [64] dG
+  float* const sdg = sm + GRAD_FLOATS - DC;  // [64] dG
   __shared__ float red[THREADS / 32];
   const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
   const DeltaChunk ch = chunk_of_slot(a, slot);
@@ -318,49 +377,55 @@ __global__ void __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaAr
   const float* const ws = ws_of<true>(a, slot, h);
   const float* const gt = ws + WS_GT;
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
-  load_rows<DK, KS>(sk, (const T*)a.k, ch.t0, ch.len, a.H, h, DK, 0);
-  load_rows<DK, KS>(sq, (const T*)a.q, ch.t0, ch.len, a.H, h, DK, 0);
+  load_rows<DK>((const float*)a.k, ch.t0, ch.len, a.H, h, DK, 0, [&](int i, int c, float4 v) {
+    put_row(sk + i * KS + c, v);
+    put_column<CS>(skt + c * CS + i, v);
+  });
+  load_rows<DK>((const float*)a.q, ch.t0, ch.len, a.H, h, DK, 0, [&](int i, int c, float4 v) {
+    put_row(sq + i * KS + c, v);
+    put_column<CS>(sqt + c * CS + i, v);
+  });
   const int ti = tid / 16, tj = tid % 16;
   float dp[4][4] = {}, dm[4][4] = {}, dqi[4][6] = {}, dkr[4][6] = {}, dks[4][6] = {}, frob = 0.f;
   for (int c0 = 0; c0 < DV; c0 += SB) {
     __syncthreads();
-    load_rows<SB, BS>(sdo, (const T*)a.dO, ch.t0, ch.len, a.H, h, DV, c0);
-    load_rows<SB, BS>(sdr, (const T*)a.dv, ch.t0, ch.len, a.H, h, DV, c0);
-    for (int e = tid; e < DC * SB; e += THREADS) {
-      const int i = e / SB;
-      su[i * BS + e % SB] = i < ch.len ? gt[GT_B + i] * ws[WS_X + i * DV + c0 + e % SB] : 0.f;
-    }
-    for (int e = tid; e < DK * SB; e += THREADS) {
-      const float x = ws[WS_S0 + e / SB * DV + c0 + e % SB], y = ws[WS_DS + e / SB * DV + c0 + e % SB];
-      ss[e / SB * BS + e % SB] = x;
-      sd[e / SB * BS + e % SB] = y;
-      frob = fmaf(x, y, frob);
-    }
+    load_rows<SB>((const float*)a.dO, ch.t0, ch.len, a.H, h, DV, c0, [&](int i, int c, float4 v) { put_row(sdo + i * BS + c, v); });
+    load_rows<SB>((const float*)a.dv, ch.t0, ch.len, a.H, h, DV, c0, [&](int i, int c, float4 v) { put_row(sdr + i * BS + c, v); });
+    load_ws<DC, SB, DV>(ws + WS_X + c0, [&](int i, int c, float4 v) {
+      const float b = gt[GT_B + i];
+      put_row(su + i * BS + c, make_float4(b * v.x, b * v.y, b * v.z, b * v.w));
+    });
+    load_ws<DK, SB, DV>(ws + WS_S0 + c0, [&](int x, int c, float4 v) { put_row(ss + x * BS + c, v); });
+    load_ws<DK, SB, DV>(ws + WS_DS + c0, [&](int x, int c, float4 v) { put_row(sd + x * BS + c, v); });
     __syncthreads();
-    gemm<4, 4, SB>(dp, [&](int x, int i) { return sdo[(ti + 16 * i) * BS + x]; }, [&](int x, int j) { return su[(tj + 16 * j) * BS + x]; });
-    gemm<4, 4, SB>(dm, [&](int x, int i) { return sdr[(ti + 16 * i) * BS + x]; }, [&](int x, int j) { return su[(tj + 16 * j) * BS + x]; });
-    gemm<4, 6, SB>(dqi, [&](int x, int i) { return sdo[(ti + 16 * i) * BS + x]; }, [&](int x, int j) { return ss[(tj + 16 * j) * BS + x]; });
-    gemm<4, 6, SB>(dkr, [&](int x, int i) { return sdr[(ti + 16 * i) * BS + x]; }, [&](int x, int j) { return ss[(tj + 16 * j) * BS + x]; });
-    gemm<4, 6, SB>(dks, [&](int x, int i) { return su[(ti + 16 * i) * BS + x]; }, [&](int x, int j) { return sd[(tj + 16 * j) * BS + x]; });
+    for (int e = tid; e < DK * SB; e += THREADS) frob = fmaf(ss[e / SB * BS + e % SB], sd[e / SB * BS + e % SB], frob);
+    gemm<4, 4, SB, B16, B16>(dp, sdo + ti * BS, su + tj * BS);
+    gemm<4, 4, SB, B16, B16>(dm, sdr + ti * BS, su + tj * BS);
+    gemm<4, 6, SB, B16, B16>(dqi, sdo + ti * BS, ss + tj * BS);
+    gemm<4, 6, SB, B16, B16>(dkr, sdr + ti * BS, ss + tj * BS);
+    gemm<4, 6, SB, B16, B16>(dks, su + ti * BS, sd + tj * BS);
   }
   __syncthreads();
-  float* const es = sdo;              // [64][65] Es, F
-  float* const fm = sdo + DC * CS;
+  float* const es = sdo;              // [64][68] Es, Fm, and their transposes
+  float* const fm = es + DC * CS;
+  float* const est = fm + DC * CS;
+  float* const fmt = est + DC * CS;
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int i = ti + 16 * r, j = tj + 16 * c;
       const float d = j <= i ? delta_decay(make_float2(gt[GT_HI + i], gt[GT_LO + i]), make_float2(gt[GT_HI + j], gt[GT_LO + j])) : 0.f;
-      es[i * CS + j] = j <= i ? a.scale * d * dp[r][c] : 0.f;
-      fm[i * CS + j] = j < i ? -d * dm[r][c] : 0.f;
+      const float e = j <= i ? a.scale * d * dp[r][c] : 0.f, f = j < i ? -d * dm[r][c] : 0.f;
+      es[i * CS + j] = est[j * CS + i] = e;
+      fm[i * CS + j] = fmt[j * CS + i] = f;
     }
   __syncthreads();
-  float q1[4][6] = {}, k1[4][6] = {}, k2[4][6] = {};  // Es K;  Es^T Q + F^T K;  F K
-  gemm<4, 6, DC>(q1, [&](int x, int i) { return es[(ti + 16 * i) * CS + x]; }, [&](int x, int j) { return sk[x * KS + tj + 16 * j]; });
-  gemm<4, 6, DC>(k1, [&](int x, int i) { return es[x * CS + ti + 16 * i]; }, [&](int x, int j) { return sq[x * KS + tj + 16 * j]; });
-  gemm<4, 6, DC>(k1, [&](int x, int i) { return fm[x * CS + ti + 16 * i]; }, [&](int x, int j) { return sk[x * KS + tj + 16 * j]; });
-  gemm<4, 6, DC>(k2, [&](int x, int i) { return fm[(ti + 16 * i) * CS + x]; }, [&](int x, int j) { return sk[x * KS + tj + 16 * j]; });
+  float q1[4][6] = {}, k1[4][6] = {}, k2[4][6] = {};  // Es K;  Es^T Q + Fm^T K;  Fm K
+  gemm<4, 6, DC, I16, I16>(q1, es + ti * CS, skt + tj * CS);
+  gemm<4, 6, DC, I16, I16>(k1, est + ti * CS, sqt + tj * CS);
+  gemm<4, 6, DC, I16, I16>(k1, fmt + ti * CS, skt + tj * CS);
+  gemm<4, 6, DC, I16, I16>(k2, fm + ti * CS, skt + tj * CS);
   float at_end = 0.f;  // sum_j k_j . (e^(G_C - G_j) dS1 u_j), this thread's part
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -376,8 +441,8 @@ __global__ void __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaAr
       at_end = fmaf(k, e * dks[r][c], at_end);
       dg = fmaf(q, dq, fmaf(k, plus - minus, dg));
       if (i < ch.len) {
-        ((T*)a.dq)[((ch.t0 + i) * a.H + h) * DK + x] = from_f<T>(dq);
-        ((T*)a.dk)[((ch.t0 + i) * a.H + h) * DK + x] = from_f<T>(minus + plus);
+        ((float*)a.dq)[((ch.t0 + i) * a.H + h) * DK + x] = dq;
+        ((float*)a.dk)[((ch.t0 + i) * a.H + h) * DK + x] = minus + plus;
       }
     }
 #pragma unroll
@@ -393,42 +458,39 @@ __global__ void __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaAr
     float end = 0.f;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) end += red[w];
-    const float hi = sdg[2 * tid + 1];
-    float run = sdg[2 * tid] + hi;
+    const float lo = sdg[2 * tid], hi = sdg[2 * tid + 1];
+    float run = lo + hi;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const float up = __shfl_down_sync(0xffffffffu, run, off);
       if (tid + off < 32) run += up;
     }
-    const float pair = run - (sdg[2 * tid] + hi);  // behind this pair
-    sdg[2 * tid] = run + end;
-    sdg[2 * tid + 1] = pair + hi + end;
-  }
-  __syncthreads();
-  if (tid < ch.len) {
+    const float behind = run - (lo + hi);
+    float* const dst = (float*)a.dg + ch.t0 * a.H + h;
+    if (2 * tid < ch.len) dst[(long long)(2 * tid) * a.H] = run + end;
+    if (2 * tid + 1 < ch.len) dst[(long long)(2 * tid + 1) * a.H] = behind + hi + end;
+  } else if (tid >= 64 && tid - 64 < ch.len) {
+    const long long t = ch.t0 + tid - 64;
     float b = 0.f;
 #pragma unroll
-    for (int t = 0; t < SNB; ++t) b += dbeta_part[((long long)t * tokens + ch.t0 + tid) * a.H + h];
-    ((T*)a.dg)[(ch.t0 + tid) * a.H + h] = from_f<T>(sdg[tid]);
-    ((T*)a.dbeta)[(ch.t0 + tid) * a.H + h] = from_f<T>(b);
+    for (int x = 0; x < SNB; ++x) b += dbeta_part[((long long)x * tokens + t) * a.H + h];
+    ((float*)a.dbeta)[t * a.H + h] = b;
   }
 }
 
-constexpr int PREP_BYTES = 2 * DC * KS * 4, SCAN_BYTES = SCAN_FLOATS * 4, GRAD_BYTES = GRAD_FLOATS * 4;
-static_assert(2 * DC * ZS <= 2 * DC * KS, "M and M B take the place of K and Q");
+constexpr int PREP_BYTES = PREP_FLOATS * 4, SCAN_BYTES = SCAN_FLOATS * 4, RSCAN_BYTES = RSCAN_FLOATS * 4, GRAD_BYTES = GRAD_FLOATS * 4;
+static_assert(SCAN_BYTES <= 232448 && RSCAN_BYTES <= 232448 && GRAD_BYTES <= 232000, "shared memory");
 
 template <class F>
 cudaError_t allow(F* f, int bytes) {
   return cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
-
-template <class T>
 cudaError_t allow_all() {
   static OncePerDevice<CudaDeviceApi> once;
   return once([] {
-    for (cudaError_t e : {allow(delta_prep_simt_kernel<T, false>, PREP_BYTES), allow(delta_prep_simt_kernel<T, true>, PREP_BYTES),
-                          allow(delta_scan_simt_kernel<T, false>, SCAN_BYTES), allow(delta_scan_simt_kernel<T, true>, SCAN_BYTES),
-                          allow(delta_rscan_simt_kernel<T>, SCAN_BYTES), allow(delta_grads_simt_kernel<T>, GRAD_BYTES)})
+    for (cudaError_t e : {allow(delta_prep_simt_kernel<false>, PREP_BYTES), allow(delta_prep_simt_kernel<true>, PREP_BYTES),
+                          allow(delta_scan_simt_kernel<false>, SCAN_BYTES), allow(delta_scan_simt_kernel<true>, SCAN_BYTES),
+                          allow(delta_rscan_simt_kernel, RSCAN_BYTES), allow(delta_grads_simt_kernel, GRAD_BYTES)})
       if (e != cudaSuccess) return e;
     return cudaSuccess;
   });
@@ -440,30 +502,25 @@ size_t delta_simt_ws_bytes(long long slots, long long tokens, int H, bool bwd) {
   return (size_t)slots * H * (bwd ? WS_BWD : WS_FWD) * 4 + (bwd ? (size_t)SNB * tokens * H * 4 : 0);
 }
 
-template <class T>
-static cudaError_t simt_fwd(const DeltaArgs& a, cudaStream_t st) {
-  cudaError_t e = allow_all<T>();
+cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t st) {
+  const cudaError_t e = allow_all();
   if (e != cudaSuccess) return e;
-  if (a.slots > 0) delta_prep_simt_kernel<T, false><<<(unsigned)a.slots * a.H, THREADS, PREP_BYTES, st>>>(a);
-  delta_scan_simt_kernel<T, false><<<(unsigned)a.n_seq * a.H * SNB, THREADS, SCAN_BYTES, st>>>(a);
+  if (a.slots > 0) delta_prep_simt_kernel<false><<<(unsigned)a.slots * a.H, THREADS, PREP_BYTES, st>>>(a);
+  delta_scan_simt_kernel<false><<<(unsigned)a.n_seq * a.H * SNB, THREADS, SCAN_BYTES, st>>>(a);
   return cudaGetLastError();
 }
-template <class T>
-static cudaError_t simt_bwd(const DeltaArgs& a, cudaStream_t st) {
-  cudaError_t e = allow_all<T>();
+cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t st) {
+  const cudaError_t e = allow_all();
   if (e != cudaSuccess) return e;
   float* part = reinterpret_cast<float*>(a.ws) + (long long)a.slots * a.H * WS_BWD;
   const unsigned chunks = (unsigned)a.slots * a.H, units = (unsigned)a.n_seq * a.H * SNB;
   if (a.slots > 0) {
-    delta_prep_simt_kernel<T, true><<<chunks, THREADS, PREP_BYTES, st>>>(a);
-    delta_scan_simt_kernel<T, true><<<units, THREADS, SCAN_BYTES, st>>>(a);
+    delta_prep_simt_kernel<true><<<chunks, THREADS, PREP_BYTES, st>>>(a);
+    delta_scan_simt_kernel<true><<<units, THREADS, SCAN_BYTES, st>>>(a);
   }
-  delta_rscan_simt_kernel<T><<<units, THREADS, SCAN_BYTES, st>>>(a, part);
-  if (a.slots > 0) delta_grads_simt_kernel<T><<<chunks, THREADS, GRAD_BYTES, st>>>(a, part);
+  delta_rscan_simt_kernel<<<units, THREADS, RSCAN_BYTES, st>>>(a, part);
+  if (a.slots > 0) delta_grads_simt_kernel<<<chunks, THREADS, GRAD_BYTES, st>>>(a, part);
   return cudaGetLastError();
 }
-
-cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t st) { return simt_fwd<float>(a, st); }
-cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t st) { return simt_bwd<float>(a, st); }
 
 }  // namespace gla
