@@ -16,7 +16,7 @@ namespace {
 
 constexpr int VCOLS = DV / 4;  // 48 four-column vectors of a row
 template <class ST> struct StepCfg;
-template <> struct StepCfg<float> { static constexpr int THREADS = 576, MIN_BLOCKS = 2; };
+template <> struct StepCfg<float> { static constexpr int THREADS = 288, MIN_BLOCKS = 2; };
 template <> struct StepCfg<__nv_bfloat16> { static constexpr int THREADS = 288, MIN_BLOCKS = 3; };
 
 __device__ __forceinline__ float4 widen(float4 x) { return x; }
