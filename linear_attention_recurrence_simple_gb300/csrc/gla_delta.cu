@@ -33,7 +33,7 @@ uint8_t* ws_start(void* p) { return (uint8_t*)(((uintptr_t)p + 255) & ~(uintptr_
 size_t ws_bytes_of(int n_seq, int T, int H, bool packed, bool bwd, int dtype) {
   if (n_seq < 0 || T < 0 || H < 1) return 0;
   const long long tokens = packed ? (long long)T : (long long)n_seq * T, slots = gla::delta_slots(n_seq, T, packed);
-  return 256 + (dtype == GLA_BF16 ? gla::delta_tc_ws_bytes(slots, tokens, H, bwd) : gla::delta_simt_ws_bytes(slots, tokens, H, bwd));
+  return 256 + (dtype == GLA_BF16 ? gla::delta_tc_ws_bytes(n_seq, slots, tokens, H, bwd) : gla::delta_simt_ws_bytes(slots, tokens, H, bwd));
 }
 
 }  // namespace

@@ -40,6 +40,7 @@ struct DeltaArgs {
   unsigned* err;
   unsigned long long wait_ns;
   uint8_t* ws;               // workspace
+  int32_t* order;            // sequences from the longest on (tensor-core kernels, packed calls), or null
 };
 
 // Places for the chunks of a call: sequence n's begin at base(n) = begin / C + n, which leaves room for
@@ -71,7 +72,7 @@ __device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs& a, int n) {
   return s;
 }
 
-// The chunk at a place: its first token and its tokens (0: the place is empty).
+// The chunk at a place: its first token and its tokens (0: the place is empty).  Whole warps.
 struct DeltaChunk {
   long long t0;
   int len;
@@ -79,13 +80,19 @@ struct DeltaChunk {
 __device__ __forceinline__ DeltaChunk chunk_of_slot(const DeltaArgs& a, int slot) {
   int n;
   if (a.cu_seqlens) {
-    int lo = 0, hi = a.n_seq - 1;  // the last sequence with slot0 <= slot
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      const int b = min(max(a.cu_seqlens[mid], 0), a.T);
-      if (b / DC + mid <= slot) lo = mid; else hi = mid - 1;
+    // the last sequence with slot0 <= slot: 32 candidates a look
+    const int lane = threadIdx.x & 31;
+    int lo = 0, step = 1;
+    while ((long long)32 * step < a.n_seq) step *= 32;
+    for (;; step /= 32) {
+      const long long at = lo + (long long)lane * step;
+      bool below = false;
+      if (at < a.n_seq) below = min(max(a.cu_seqlens[at], 0), a.T) / DC + (int)at <= slot;
+      const unsigned v = __ballot_sync(0xffffffffu, below);  // (a run of ones: slot0 grows with n)
+      lo += max(__popc(v) - 1, 0) * step;
+      if (step == 1) break;
     }
-    n = lo;
+    n = min(lo, a.n_seq - 1);
   } else {
     n = slot / ((a.T + DC - 1) / DC);
   }
@@ -109,24 +116,43 @@ __device__ __forceinline__ int delta_row(const int32_t* row, int rows, int n, un
 }
 
 // Running sums of a chunk's log decays, each as two fp32 (hi + lo): a difference of two of them keeps 24 bits
-// of what is left between them, whatever was decayed before.  Whole warp; x0, x1 are the log decays of tokens
-// 2 lane and 2 lane + 1.  Values below -120 count as -120: exp of it is zero in fp32.
+// of what is left between them, whatever was decayed before.  Summed as whole numbers of 2^-40 (fp64 adds are slow
+// here), so that a sum is off by 64 2^-41 at most.  Whole warp; x0, x1 are the log decays of tokens 2 lane and
+// 2 lane + 1.  Values below -120 count as -120: exp of it is zero in fp32.
 constexpr float LOG_FLOOR = -120.f;
+constexpr float LOG_CEIL = 16384.f;  // (exp of it is an infinity; the sums stay within 63 bits)
 template <bool BASE2 = false>  // sums of the logs to base 2
+__device__ __forceinline__ long long delta_fixed(float x) {
+  const float one = 1099511627776.f;  // 2^40
+  x = fminf(fmaxf(x, LOG_FLOOR), LOG_CEIL);
+  if (!BASE2) return __float2ll_rn(x * one);
+  const float hi = x * 1.44269502f, lo = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -hi));  // log2(e) in two
+  return __float2ll_rn(hi * one) + __float2ll_rn(lo * one);
+}
+__device__ __forceinline__ float2 delta_two(long long x, float bad) {
+  const float hi = __ll2float_rn(x);
+  const float lo = __ll2float_rn(x - __float2ll_rn(hi));
+  return make_float2(fmaf(hi, 9.094947017729282e-13f, bad), lo * 9.094947017729282e-13f);
+}
+template <bool BASE2 = false>
 __device__ __forceinline__ void delta_sums(float x0, float x1, float2& s0, float2& s1) {
-  const double unit = BASE2 ? 1.4426950408889634 : 1.0;
-  const double d0 = unit * (x0 < LOG_FLOOR ? LOG_FLOOR : x0), d1 = unit * (x1 < LOG_FLOOR ? LOG_FLOOR : x1);
-  double run = d0 + d1;
+  const long long d0 = delta_fixed<BASE2>(x0), d1 = delta_fixed<BASE2>(x1);
+  // NaN from a token on where it is NaN, or +inf
+  const float bad0 = x0 > LOG_FLOOR ? 0.f * x0 : x0 <= LOG_FLOOR ? 0.f : x0, bad1 = x1 > LOG_FLOOR ? 0.f * x1 : x1 <= LOG_FLOOR ? 0.f : x1;
+  long long run = d0 + d1;
+  float bad = bad0 + bad1;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const double up = __shfl_up_sync(0xffffffffu, run, off);
-    if ((int)(threadIdx.x & 31) >= off) run += up;
+    const long long up = __shfl_up_sync(0xffffffffu, run, off);
+    const float b = __shfl_up_sync(0xffffffffu, bad, off);
+    if ((int)(threadIdx.x & 31) >= off) {
+      run += up;
+      bad += b;
+    }
   }
-  const double a = run - d1;
-  s0.x = (float)a;
-  s0.y = (float)(a - (double)s0.x);
-  s1.x = (float)run;
-  s1.y = (float)(run - (double)s1.x);
+  const float before = __shfl_up_sync(0xffffffffu, bad, 1);
+  s0 = delta_two(run - d1, ((threadIdx.x & 31) ? before : 0.f) + bad0);
+  s1 = delta_two(run, bad);
 }
 // exp(G_i - G_j)
 __device__ __forceinline__ float delta_decay(float2 gi, float2 gj) { return expf((gi.x - gj.x) + (gi.y - gj.y)); }
@@ -156,9 +182,9 @@ __device__ __forceinline__ void delta_solve_column(const float* m, const float* 
 int current_device_state(unsigned** err, unsigned long long* wait_ns);
 cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t stream);
 cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t stream);
-cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t stream);
-cudaError_t launch_delta_tc_bwd(const DeltaArgs& a, cudaStream_t stream);
-size_t delta_tc_ws_bytes(long long slots, long long tokens, int H, bool bwd);
+cudaError_t launch_delta_tc_fwd(DeltaArgs a, cudaStream_t stream);
+cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t stream);
+size_t delta_tc_ws_bytes(int n_seq, long long slots, long long tokens, int H, bool bwd);
 size_t delta_simt_ws_bytes(long long slots, long long tokens, int H, bool bwd);
 
 }  // namespace gla

@@ -182,25 +182,25 @@ static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_S0 % 32
 //      off the diagonal as B operands (hi + lo) in shared memory, on it in fp32
 //   2  the diagonal blocks' inverses (1 + B M_bb)^-1 by substitution, one thread a row, fp32
 //   3  slabs of 16 rows y of y (1 + B M) = r, block by block from the last: Y_b = (R_b - sum_c Y_c BM_cb) W_b, each
-//      product hi hi + hi lo + lo hi; a slab's rows leave through shared memory as one contiguous copy
+//      product hi hi + hi lo + lo hi
 // fp32 sums; what is carried from block to block has 16 bits.
 constexpr int PREP_THREADS = 128;
 struct PrepSmem {
-  static constexpr uint32_t P0 = 0, P1 = 16384, STAGE = 24576, DM = STAGE, G = STAGE + 4 * 4096, B = G + DC * 8, BAR = B + DC * 4,
-                            FRAG = BAR + 256;
+  static constexpr uint32_t P0 = 0, P1 = 16384, STAGE = 24576, DM = STAGE, G = STAGE + 4 * 4096, B = G + DC * 8, F = B + DC * 4, E = F + DC * 4,
+                            CF = E + DC * 4, RF = CF + DC * 4, BAR = RF + 3 * DC * 4, FRAG = BAR + 256;
   static constexpr uint32_t bytes(bool bwd) { return FRAG + (bwd ? 20 : 10) * 1024; }
 };
 constexpr int DM_FLOATS = 4 * 16 * 20;
-static_assert(2 * DM_FLOATS * 4 <= 4 * 4096, "the diagonal blocks take the stages' place");
+static_assert(2 * DM_FLOATS * 4 <= 4 * 4096 && PrepSmem::FRAG % 16 == 0, "the diagonal blocks take the stages' place");
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -227,9 +227,8 @@ __device__ __forceinline__ void to_operand(const float (&x)[2][4], uint32_t (&hi
 #pragma unroll
   for (int i = 0; i < 4; ++i) split2(make_float2(x[i >> 1][2 * (i & 1)], x[i >> 1][2 * (i & 1) + 1]), hi[i], lo[i]);
 }
-// d += (hi + lo) times a 16 x 16 block of B operands, hi and lo
-__device__ __forceinline__ void block_mul(float (&d)[2][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const uint8_t* frag) {
-  const uint4 h = *reinterpret_cast<const uint4*>(frag + 16 * (threadIdx.x & 31)), l = *reinterpret_cast<const uint4*>(frag + 512 + 16 * (threadIdx.x & 31));
+// d += (hi + lo) times a 16 x 16 block of B operands, hi (h) and lo (l)
+__device__ __forceinline__ void block_mul(float (&d)[2][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint4 h, uint4 l) {
   mma(d[0], lo, h.x, h.y);
   mma(d[1], lo, h.z, h.w);
   mma(d[0], hi, l.x, l.y);
@@ -245,25 +244,36 @@ __device__ __forceinline__ constexpr int frag_diag(int b) { return 6 + b; }
 struct Slab {  // 16 rows x 64 columns as A operands, hi and lo
   uint32_t hi[4][4], lo[4][4];
 };
-// Rows r, of which blocks up to `top` are not zero, times (1 + B M)^-1, or (UP) (1 + B M^T)^-1 (top = 3).
-template <bool UP>
-__device__ __forceinline__ void solve_slab(float (&r)[4][2][4], int top, const uint8_t* frags, Slab& s) {
+// Rows r, of which blocks up to `top` are not zero, times (1 + B M)^-1, or (UP) (1 + B M^T)^-1 (top = 3).  N slabs at
+// a time: they share the operands' loads, and each waits less on its own products.
+template <bool UP, int N>
+__device__ __forceinline__ void solve_slabs(float (&r)[N][4][2][4], const int (&top)[N], const uint8_t* frags, Slab (&s)[N]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int step = 0; step < 4; ++step) {
     const int b = UP ? step : 3 - step;
-    if (b <= top) {
 #pragma unroll
-      for (int before = 0; before < step; ++before) {
-        const int c = UP ? before : 3 - before;
-        if (c <= top) block_mul(r[b], s.hi[c], s.lo[c], frags + 1024 * (UP ? 10 + frag_off(b, c) : frag_off(c, b)));
+    for (int before = 0; before < step; ++before) {
+      const int c = UP ? before : 3 - before;
+      const uint8_t* f = frags + 1024 * (UP ? 10 + frag_off(b, c) : frag_off(c, b)) + 16 * lane;
+      const uint4 h = *reinterpret_cast<const uint4*>(f), l = *reinterpret_cast<const uint4*>(f + 512);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (c <= top[i]) block_mul(r[i][b], s[i].hi[c], s[i].lo[c], h, l);
+    }
+    const uint8_t* f = frags + 1024 * ((UP ? 10 : 0) + frag_diag(b)) + 16 * lane;
+    const uint4 h = *reinterpret_cast<const uint4*>(f), l = *reinterpret_cast<const uint4*>(f + 512);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (b <= top[i]) {
+        to_operand(r[i][b], s[i].hi[b], s[i].lo[b]);
+        float y[2][4] = {};
+        block_mul(y, s[i].hi[b], s[i].lo[b], h, l);
+        to_operand(y, s[i].hi[b], s[i].lo[b]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i].hi[b][e] = s[i].lo[b][e] = 0u;
       }
-      to_operand(r[b], s.hi[b], s.lo[b]);
-      float y[2][4] = {};
-      block_mul(y, s.hi[b], s.lo[b], frags + 1024 * ((UP ? 10 : 0) + frag_diag(b)));
-      to_operand(y, s.hi[b], s.lo[b]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s.hi[b][i] = s.lo[b][i] = 0u;
     }
   }
 }
@@ -289,41 +299,59 @@ __device__ __forceinline__ void store_slab(const Slab& s, uint8_t* sm, uint8_t* 
     stores_commit();
   }
 }
-// Rows a0 .. of (diag(w) K)^T, w a token's weight.
-template <class W>
-__device__ __forceinline__ void transposed_slab(float (&r)[4][2][4], const uint32_t (&raw)[4][4], int len, W weight) {
-  const int t = threadIdx.x & 3;
+// Rows a0 .. of (diag(w) K)^T, w the tokens' weights, times `sign`.
+__device__ __forceinline__ void transposed_slab(float (&r)[4][2][4], uint32_t sb, bool is_q, int a0, const float* w, float sign) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll
-  for (int b = 0; b < 4; ++b)
+  for (int b = 0; b < 4; ++b) {
+    uint32_t raw[4];
+    ldsm4t(raw, kq_at(sb, is_q, 16 * b + 8 * (lane >> 4) + (lane & 7), a0 / 8 + ((lane >> 3) & 1)));
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const int j = 16 * b + 8 * n + 2 * t;
-      const float w0 = weight(j), w1 = weight(j + 1);
+      const float2 ww = fmul2(both(sign), *reinterpret_cast<const float2*>(w + 16 * b + 8 * n + 2 * t));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 x = widen2(raw[b][2 * n + i]);
-        r[b][n][2 * i] = j < len ? w0 * x.x : 0.f;
-        r[b][n][2 * i + 1] = j + 1 < len ? w1 * x.y : 0.f;
+        const float2 x = fmul2(ww, widen2(raw[2 * n + i]));
+        r[b][n][2 * i] = x.x;
+        r[b][n][2 * i + 1] = x.y;
       }
     }
-}
-__device__ __forceinline__ void load_transposed(uint32_t (&raw)[4][4], uint32_t sb, bool is_q, int a0) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) ldsm4t(raw[b], kq_at(sb, is_q, 16 * b + 8 * (lane >> 4) + (lane & 7), a0 / 8 + ((lane >> 3) & 1)));
+  }
 }
 
 template <bool BWD>
 __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
-  float* const dm = reinterpret_cast<float*>(sm + PrepSmem::DM);   // [4][16][20]: diagonal blocks of B M, and of B M^T
+  float* const dm = reinterpret_cast<float*>(sm + PrepSmem::DM);   // [4][16][20]: diagonal blocks of -B M, and of -B M^T
   uint8_t* const frags = sm + PrepSmem::FRAG;
   float2* const sg = reinterpret_cast<float2*>(sm + PrepSmem::G);  // sums of log2 decays
   float* const sbeta = reinterpret_cast<float*>(sm + PrepSmem::B);
+  // e^G, e^(G_C - G); and the decays between blocks in two factors that are both at most 1: from token j to the end of its
+  // block, and from there (end of block 0, 1, 2) to token i of a later block
+  float* const sf = reinterpret_cast<float*>(sm + PrepSmem::F);
+  float* const se = reinterpret_cast<float*>(sm + PrepSmem::E);
+  float* const cf = reinterpret_cast<float*>(sm + PrepSmem::CF);
+  float* const rf = reinterpret_cast<float*>(sm + PrepSmem::RF);
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + PrepSmem::BAR);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + PrepSmem::BAR + 8);
   const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  if (a.order && h == 0 && slot < a.n_seq) {  // (there are at least as many places as sequences)
+    // this sequence's rank by its length, for the scans: their longest units go first
+    auto length = [&](int n) { return a.cu_seqlens[n + 1] - a.cu_seqlens[n]; };
+    const int mine = length(slot);
+    int rank = 0;
+    for (int j = tid; j < a.n_seq; j += PREP_THREADS) {
+      const int l = length(j);
+      rank += l > mine || (l == mine && j < slot);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, off);
+    if (lane == 0) dm[warp] = __int_as_float(rank);
+    __syncthreads();
+    if (tid == 0) a.order[__float_as_int(dm[0]) + __float_as_int(dm[1]) + __float_as_int(dm[2]) + __float_as_int(dm[3])] = slot;
+    __syncthreads();
+  }
   const DeltaChunk ch = chunk_of_slot(a, slot);
   if (ch.len == 0) return;
   uint8_t* const ws = a.ws + ((long long)slot * a.H + h) * (BWD ? W_BWD : W_FWD);
@@ -350,7 +378,23 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     sg[2 * lane + 1] = s1;
   }
   __syncthreads();
+  auto decay = [&](int i, int j) {  // of token j's part in token i
+    const float2 x = sg[i], y = sg[j];
+    return exp2_fast((x.x - y.x) + (x.y - y.y));
+  };
+  for (int e = tid; e < 6 * DC; e += PREP_THREADS) {
+    const int i = e & 63, what = e >> 6;
+    if (what == 0) sf[i] = exp2_fast(sg[i].x + sg[i].y);
+    else if (what == 1) se[i] = decay(DC - 1, i);
+    else if (what == 2) cf[i] = decay(i | 15, i);
+    else if (i >= 16 * (what - 2)) rf[(what - 3) * DC + i] = decay(i, 16 * (what - 2) - 1);
+  }
   bool ok = mbar_wait(bar, 0, a.wait_ns, abort_flag);
+  if (ok && ch.len < DC)  // rows behind the last token may hold another sequence's
+    for (int e = tid; e < 2 * (DC - ch.len) * 12; e += PREP_THREADS) {
+      const int is_q = e / ((DC - ch.len) * 12), r = ch.len + e / 12 % (DC - ch.len);
+      st_shared_v4(kq_at(sb, is_q != 0, r, e % 12), 0u, 0u, 0u, 0u);
+    }
   if (__syncthreads_or(!ok)) {
     if (tid == 0) {
       raise_error(a.err, ERR_TIMEOUT);
@@ -358,79 +402,97 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     }
     return;
   }
-  auto decay = [&](int i, int j) {  // of token j's part in token i
-    const float2 x = sg[i], y = sg[j];
-    return exp2_fast((x.x - y.x) + (x.y - y.y));
-  };
-  // What the block's second triangle gives (B M^T's operands) stands behind the first's.
-  Slab out;
-  // 1: P's rows (those behind the last token may hold another sequence's)
-  float r[4][2][4];
+  // A block of Q K^T or K K^T, rows i of block rb and columns j of block cb <= rb, times the decays: on the diagonal
+  // only j < i (or, `with`, j <= i).
+  auto decayed = [&](float (&x)[2][4], int rb, int cb, bool with) {
+    if (rb > cb) {
+      const float r0 = rf[cb * DC + 16 * rb + g], r1 = rf[cb * DC + 16 * rb + g + 8];
 #pragma unroll
-  for (int b = 0; b < 4; ++b)
-    if (b <= warp) {
-      block_dot(r[b], sb, true, 16 * warp, 16 * b);
+      for (int n = 0; n < 2; ++n) {
+        const float2 c = *reinterpret_cast<const float2*>(cf + 16 * cb + 8 * n + 2 * t);
+        const float2 y0 = fmul2(fmul2(both(r0), c), make_float2(x[n][0], x[n][1])), y1 = fmul2(fmul2(both(r1), c), make_float2(x[n][2], x[n][3]));
+        x[n][0] = y0.x;
+        x[n][1] = y0.y;
+        x[n][2] = y1.x;
+        x[n][3] = y1.y;
+      }
+    } else {
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = 16 * warp + g + 8 * (e >> 1), j = 16 * b + 8 * n + 2 * t + (e & 1);
-          r[b][n][e] = j <= i && i < ch.len ? decay(i, j) * r[b][n][e] : 0.f;
+          const int i = g + 8 * (e >> 1), j = 8 * n + 2 * t + (e & 1);
+          x[n][e] = j < i || (with && j == i) ? decay(16 * rb + i, 16 * rb + j) * x[n][e] : 0.f;
         }
     }
+  };
+  // A block's operand (rows of x are its columns), hi and lo.
+  auto put_frag = [&](const float (&x)[2][4], int id) {
+    uint32_t hi[4], lo[4];
+    to_operand(x, hi, lo);
+    uint8_t* const f = frags + 1024 * id + 16 * lane;
+    *reinterpret_cast<uint4*>(f) = make_uint4(hi[0], hi[2], hi[1], hi[3]);
+    *reinterpret_cast<uint4*>(f + 512) = make_uint4(lo[0], lo[2], lo[1], lo[3]);
+  };
+  // 1: P's rows (BWD: written as they are, and M's rows in their place, which are also -(B M^T)'s columns)
+  float r[2][4][2][4];
+  Slab out[2];
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    if (b <= warp) {
+      block_dot(r[1][b], sb, true, 16 * warp, 16 * b);
+      decayed(r[1][b], warp, b, true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[1][b][i >> 2][i & 3] = 0.f;
+    }
   if constexpr (BWD) {
-    // P as it is; then the rows of M, which are also -(B M^T)'s columns
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      if (b > warp) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[b][i >> 2][i & 3] = 0.f;
-      }
-      to_operand(r[b], out.hi[b], out.lo[b]);
-    }
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
+      to_operand(r[1][b], out[0].hi[b], out[0].lo[b]);
       if (b <= warp) {
+        block_dot(r[1][b], sb, false, 16 * warp, 16 * b);
+        decayed(r[1][b], warp, b, false);
         float x[2][4];
-        block_dot(r[b], sb, false, 16 * warp, 16 * b);
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i = 16 * warp + g + 8 * (e >> 1), j = 16 * b + 8 * n + 2 * t + (e & 1);
-            r[b][n][e] = j < i && i < ch.len ? decay(i, j) * r[b][n][e] : 0.f;
-            x[n][e] = -sbeta[j] * r[b][n][e];
-            if (b == warp) dm[DM_FLOATS + (b * 16 + (j & 15)) * 20 + (i & 15)] = x[n][e];
+            const int j = 8 * n + 2 * t + (e & 1);
+            x[n][e] = -sbeta[16 * b + j] * r[1][b][n][e];
+            if (b == warp) dm[DM_FLOATS + (b * 16 + j) * 20 + g + 8 * (e >> 1)] = x[n][e];
           }
-        if (b != warp) {
-          uint32_t hi[4], lo[4];
-          to_operand(x, hi, lo);
-          uint8_t* const f = frags + 1024 * (10 + frag_off(warp, b)) + 16 * lane;
-          *reinterpret_cast<uint4*>(f) = make_uint4(hi[0], hi[2], hi[1], hi[3]);
-          *reinterpret_cast<uint4*>(f + 512) = make_uint4(lo[0], lo[2], lo[1], lo[3]);
-        }
+        if (b != warp) put_frag(x, 10 + frag_off(warp, b));
       }
+    }
   }
+  const int mb = 3 - warp;
 #pragma unroll
   for (int jb = 0; jb < 4; ++jb) {
-    const int mb = 3 - warp;
     if (jb > mb) continue;
     float x[2][4];  // rows j, columns m
     block_dot(x, sb, false, 16 * jb, 16 * mb);
+    if (jb != mb) {
+      const float c0 = cf[16 * jb + g], c1 = cf[16 * jb + g + 8];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = 16 * jb + g + 8 * (e >> 1), m = 16 * mb + 8 * n + 2 * t + (e & 1);
-        x[n][e] = j < m && m < ch.len ? -sbeta[m] * (decay(m, j) * x[n][e]) : 0.f;
-        if (jb == mb) dm[(mb * 16 + (m & 15)) * 20 + (j & 15)] = x[n][e];
+      for (int n = 0; n < 2; ++n) {
+        const int m = 16 * mb + 8 * n + 2 * t;
+        const float2 w = fmul2(*reinterpret_cast<const float2*>(rf + jb * DC + m), *reinterpret_cast<const float2*>(sbeta + m));
+        const float2 y0 = fmul2(fmul2(both(-c0), w), make_float2(x[n][0], x[n][1])), y1 = fmul2(fmul2(both(-c1), w), make_float2(x[n][2], x[n][3]));
+        x[n][0] = y0.x;
+        x[n][1] = y0.y;
+        x[n][2] = y1.x;
+        x[n][3] = y1.y;
       }
-    if (jb != mb) {  // rows of x are the operand's columns
-      uint32_t hi[4], lo[4];
-      to_operand(x, hi, lo);
-      uint8_t* const f = frags + 1024 * frag_off(mb, jb) + 16 * lane;
-      *reinterpret_cast<uint4*>(f) = make_uint4(hi[0], hi[2], hi[1], hi[3]);
-      *reinterpret_cast<uint4*>(f + 512) = make_uint4(lo[0], lo[2], lo[1], lo[3]);
+      put_frag(x, frag_off(mb, jb));
+    } else {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = g + 8 * (e >> 1), m = 8 * n + 2 * t + (e & 1);
+          dm[(mb * 16 + m) * 20 + j] = j < m ? -sbeta[16 * mb + m] * (decay(16 * mb + m, 16 * mb + j) * x[n][e]) : 0.f;
+        }
     }
   }
   __syncthreads();
@@ -464,40 +526,61 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
   }
   if (tid < DC) {
     float* const gt = reinterpret_cast<float*>(ws + W_GT);
-    gt[GT_F + tid] = exp2_fast(sg[tid].x + sg[tid].y);
+    gt[GT_F + tid] = sf[tid];
     gt[GT_B + tid] = sbeta[tid];
     if (BWD) {
-      gt[GT_E + tid] = decay(DC - 1, tid);
+      gt[GT_E + tid] = se[tid];
       reinterpret_cast<float2*>(gt + GT_SUM)[tid] = sg[tid];
     }
   }
   __syncthreads();
-  // 3: the rows of P^ (Z), then those of K^: two slabs for the warps with short rows of P, one for the others;
-  // of K~ and Q~ the other way round
-  if (BWD) store_slab(out, sm, ws + W_P + 2048 * warp, ws + W_P + 8192 + 2048 * warp);
-  solve_slab<false>(r, warp, frags, out);
-  store_slab(out, sm, ws + W_PH + 2048 * warp, nullptr);
-  uint32_t raw[4][4];
-  const int slab0 = warp < 2 ? 2 * warp : 2 + warp, slabs = warp < 2 ? 2 : 1;
-  for (int x = slab0; x < slab0 + slabs; ++x) {
-    load_transposed(raw, sb, false, 16 * x);
-    transposed_slab(r, raw, ch.len, [&](int j) { return decay(DC - 1, j); });
-    solve_slab<false>(r, 3, frags, out);
-    store_slab(out, sm, ws + W_KD + 2048 * x, ws + W_KD + 12288 + 2048 * x);
+  // 3: the rows of P^ (Z) and K^, two slabs at a time: warps 0 and 1 two of K^ and then their short one of P^, warps 2 and 3
+  // one of each; of K~ (and Q~) the other way round
+  if (BWD) store_slab(out[0], sm, ws + W_P + 2048 * warp, ws + W_P + 8192 + 2048 * warp);
+  auto store_kd = [&](const Slab& s, int x) { store_slab(s, sm, ws + W_KD + 2048 * x, ws + W_KD + 12288 + 2048 * x); };
+  if (warp >= 2) {
+    transposed_slab(r[0], sb, false, 16 * (2 + warp), se, 1.f);
+    solve_slabs<false, 2>(r, {3, warp}, frags, out);
+    store_kd(out[0], 2 + warp);
+    store_slab(out[1], sm, ws + W_PH + 2048 * warp, nullptr);
+  } else {
+    {
+      float p[1][4][2][4];
+      Slab one[1];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[0][b][i >> 2][i & 3] = r[1][b][i >> 2][i & 3];
+      solve_slabs<false, 1>(p, {warp}, frags, one);
+      store_slab(one[0], sm, ws + W_PH + 2048 * warp, nullptr);
+    }
+    transposed_slab(r[0], sb, false, 32 * warp, se, 1.f);
+    transposed_slab(r[1], sb, false, 32 * warp + 16, se, 1.f);
+    solve_slabs<false, 2>(r, {3, 3}, frags, out);
+    store_kd(out[0], 2 * warp);
+    store_kd(out[1], 2 * warp + 1);
   }
   if constexpr (BWD) {
-    const int up0 = warp < 2 ? warp : 2 * warp - 2;
-    auto from_start = [&](int j) { return exp2_fast(sg[j].x + sg[j].y); };
-    for (int x = up0; x < up0 + 3 - slabs; ++x) {
-      load_transposed(raw, sb, false, 16 * x);
-      transposed_slab(r, raw, ch.len, [&](int j) { return -from_start(j); });
-      solve_slab<true>(r, 3, frags, out);
-      store_slab(out, sm, ws + W_KR + 2048 * x, ws + W_KR + 12288 + 2048 * x);
-      load_transposed(raw, sb, true, 16 * x);
-      transposed_slab(r, raw, ch.len, [&](int j) { return a.scale * from_start(j); });
+    auto store_kr = [&](const Slab& s, int x) { store_slab(s, sm, ws + W_KR + 2048 * x, ws + W_KR + 12288 + 2048 * x); };
+    const int up0 = warp < 2 ? warp : 2 * warp - 2, ups = warp < 2 ? 1 : 2;
+    if (warp >= 2) {
+      transposed_slab(r[0], sb, false, 16 * up0, sf, -1.f);
+      transposed_slab(r[1], sb, false, 16 * up0 + 16, sf, -1.f);
+      solve_slabs<true, 2>(r, {3, 3}, frags, out);
+      store_kr(out[0], up0);
+      store_kr(out[1], up0 + 1);
+    } else {
+      float p[1][4][2][4];
+      Slab one[1];
+      transposed_slab(p[0], sb, false, 16 * up0, sf, -1.f);
+      solve_slabs<true, 1>(p, {3}, frags, one);
+      store_kr(one[0], up0);
+    }
+    for (int x = up0; x < up0 + ups; ++x) {
+      transposed_slab(r[0], sb, true, 16 * x, sf, a.scale);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) to_operand(r[b], out.hi[b], out.lo[b]);
-      store_slab(out, sm, ws + W_QT + 2048 * x, ws + W_QT + 12288 + 2048 * x);
+      for (int b = 0; b < 4; ++b) to_operand(r[0][b], out[0].hi[b], out[0].lo[b]);
+      store_slab(out[0], sm, ws + W_QT + 2048 * x, ws + W_QT + 12288 + 2048 * x);
     }
   }
   if (lane == 0) stores_read();
@@ -506,16 +589,21 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 // ---- scan -----------------------------------------------------------------------------------
 // Warps 0-7: warp w has lanes 32 (w % 4) .. of the products' rows and columns 32 (w / 4) .. of the tile's 64.
 // Rows of [K; Q] S: 0-63 K's (warps of w % 4 < 2), 64-127 Q's; rows of K^ B R: 0-95 the state's; rows of P^ B R:
-// 64-127.  A thread keeps its 32 columns of a state row in fp32 registers.  One thread of warp 8 issues all products
-// and copies.  Hand-overs through mbarriers, so that only the state's way (product, residual, product, state) is waited
-// for: a chunk's outputs are written while the next chunk's first product runs.  Tensor memory: two places of 128
-// columns ([hi | lo]), 2 CTAs an SM.  A chunk's [K; Q] S and, once that is in registers, its P^ B R have the one, its
+// 64-127.  A warp's lanes are also its scheduler's, and K's rows have most of the work, so every other CTA (of the two
+// that an SM holds) has it the other way round: Q's rows and P^'s first, the state's in 32-127.  A thread keeps its 32
+// columns of a state row in fp32 registers.  One thread of warp 8 issues the products, one of warp 9 the copies.
+// Hand-overs through mbarriers, so that only the state's way (product, residual, product, state) is waited for: a
+// chunk's outputs are written while the next chunk's first product runs.  Tensor memory: two places of 128 columns
+// ([hi | lo]), 2 CTAs an SM.  A chunk's [K; Q] S and, once that is in registers, its P^ B R have the one, its
 // K^ B R the other; the next chunk has them the other way round.
-// STATES (the backward's forward pass): K's rows stand in 64-127 and rows 0-63 are not looked at; Z is in P^'s place,
-// X = R - Z B R and every chunk's S0 go to the workspace instead of outputs.
-constexpr int TN = 64, NTILE = DV / TN, SCAN_THREADS = 288;
+// STATES (the backward's forward pass): K's rows stand in Q's place and the other half is not looked at; Z is in P^'s
+// place, X = R - Z B R and every chunk's S0 go to the workspace instead of outputs.
+constexpr int TN = 64, NTILE = DV / TN, SCAN_THREADS = 320;
 struct ScanSmem {
-  static constexpr uint32_t KQ0 = 0, KQ1 = 16384, OP = 24576, S = OP + W_OP, BR = S + 24576, V = BR + 16384, OUT = V + 8192,
+  // Products of 128 rows read past operands of 64 and 96 rows, on the side that the lanes call for; what stands there
+  // (the state before K^, P^ behind it, K^ before P^, B R behind it) is as still as the operand meanwhile, and the rows
+  // it gives are not looked at.
+  static constexpr uint32_t KQ0 = 0, KQ1 = 16384, S = 24576, OP = S + 24576, BR = OP + W_OP, V = BR + 16384, OUT = V + 8192,
                             GT = OUT + 8192, BAR = GT + 512, BYTES = BAR + 112;
   static_assert(BYTES <= 115712, "two CTAs an SM");
 };
@@ -525,18 +613,20 @@ struct ScanSmem {
 enum { SB_A = 0, SB_C, SB_O, SB_KQ, SB_V, SB_KD, SB_PH, SB_SR, SB_WR, SB_OF, SB_DRAIN, SB_N };
 
 template <bool STATES>
-__global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
+__global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, int flip_every) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + ScanSmem::BAR);
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + ScanSmem::BAR + 8 * SB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + ScanSmem::BAR + 8 * SB_N + 4);
-  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = nh / a.H;
+  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = a.order ? a.order[nh / a.H] : nh / a.H;
   const int tid = threadIdx.x, warp = tid >> 5, q = warp & 3, half = (warp >> 2) & 1;
   const int row = (tid & 31) + 32 * q;  // lane of the products
   const int tok = row & 63;
   const int col0 = tile * TN + 32 * half;
-  const bool r_row = STATES == (q >= 2), o_row = q >= 2, s_row = warp < 8 && q < 3;
+  const bool flip = !STATES && ((blockIdx.x / flip_every) & 1);
+  const bool o_row = (q >= 2) != flip, r_row = STATES == o_row, s_row = warp < 8 && (flip ? q > 0 : q < 3);
+  const int srow = flip ? row - 32 : row;  // state row
   const DeltaSeq s = delta_seq(a, n);
   const int nc = (s.len + DC - 1) / DC;
   const int from = a.h0 ? delta_row(a.h0_row, a.h0_rows, n, a.err) : -1;
@@ -546,7 +636,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 #pragma unroll
   for (int x = 0; x < 16; ++x) S[x] = both(0.f);
   if (s_row && from >= 0) {
-    const float4* src = reinterpret_cast<const float4*>(a.h0 + (((long long)from * a.H + h) * DK + row) * DV + col0);
+    const float4* src = reinterpret_cast<const float4*>(a.h0 + (((long long)from * a.H + h) * DK + srow) * DV + col0);
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       const float4 w = src[x];
@@ -569,20 +659,21 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
     tc_fence_after();
     const uint32_t tmem = *slot_tm;
     bool ok = true;
-    if (warp == 8) {
-      if (tid == 256) {
-        auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * (STATES ? W_BWD : W_FWD); };
+    auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * (STATES ? W_BWD : W_FWD); };
+    if (warp == 9) {
+      if (tid == 288) {
         // a chunk's operands, each as soon as the chunk before is done with their place
         int loads[4] = {};
         auto load_rows = [&](int c) {
           ++loads[0];
           const int t = (int)(s.begin + (long long)c * DC);
-          if (STATES) {
-            mbar_expect_tx(&bar[SB_KQ], 12288);
-            box_load(sb + ScanSmem::KQ0 + 8192, &maps.k0, &bar[SB_KQ], 0, h, t);
-            box_load(sb + ScanSmem::KQ1 + 4096, &maps.k1, &bar[SB_KQ], 64, h, t);
-          } else {
-            load_kq(maps, sb + ScanSmem::KQ0, sb + ScanSmem::KQ1, &bar[SB_KQ], h, t);
+          const uint32_t other = STATES != flip ? 1 : 0;  // K's half: the first, or the second
+          mbar_expect_tx(&bar[SB_KQ], STATES ? 12288 : 24576);
+          box_load(sb + ScanSmem::KQ0 + 8192 * other, &maps.k0, &bar[SB_KQ], 0, h, t);
+          box_load(sb + ScanSmem::KQ1 + 4096 * other, &maps.k1, &bar[SB_KQ], 64, h, t);
+          if (!STATES) {
+            box_load(sb + ScanSmem::KQ0 + 8192 * (1 - other), &maps.q0, &bar[SB_KQ], 0, h, t);
+            box_load(sb + ScanSmem::KQ1 + 4096 * (1 - other), &maps.q1, &bar[SB_KQ], 64, h, t);
           }
         };
         auto load_v = [&](int c) {
@@ -618,10 +709,26 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         load_kd(0);
         load_ph(0);
         if (nc > 1) prefetch(1);
+        for (int c = 0; c + 1 < nc && ok; ++c) {
+          if (c + 2 < nc) prefetch(c + 2);
+          if (!(ok = wait(SB_A, c))) break;
+          load_rows(c + 1);
+          if (!(ok = wait(SB_WR, c))) break;  // (V and the decays have been read)
+          load_v(c + 1);
+          if (!(ok = wait(SB_C, c))) break;
+          load_kd(c + 1);
+          if (!(ok = wait(SB_O, c))) break;
+          load_ph(c + 1);
+        }
+        for (int x = 0; x < 4; ++x) mbar_wait_drain(&bar[SB_KQ + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      if (tid == 256) {
         const SDesc d0 = sdesc(sb + ScanSmem::KQ0, 16, 1024, LAYOUT_SW128), d1 = sdesc(sb + ScanSmem::KQ1, 16, 512, LAYOUT_SW64);
         const SDesc ds = sdesc(sb + ScanSmem::S, 12288, 1024, LAYOUT_SW128), db = sdesc(sb + ScanSmem::BR, 8192, 1024, LAYOUT_SW128);
-        const SDesc dk = sdesc(sb + ScanSmem::OP + W_KD, 16, 1024, LAYOUT_SW128);
-        const SDesc dp = sdesc(sb + ScanSmem::OP + W_PH - 8192, 16, 1024, LAYOUT_SW128);  // P^ in rows 64-127
+        const SDesc dk = sdesc(sb + ScanSmem::OP + W_KD - (flip ? 4096 : 0), 16, 1024, LAYOUT_SW128);
+        const SDesc dp = sdesc(sb + ScanSmem::OP + W_PH - (flip ? 0 : 8192), 16, 1024, LAYOUT_SW128);
         for (int c = 0; c < nc; ++c) {
           const uint32_t at_a = tmem + (c & 1) * 128u, at_c = tmem + ((c & 1) ^ 1) * 128u;
           if (!(ok = wait(SB_KQ, c) && wait(SB_SR, c))) break;
@@ -632,12 +739,6 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           umma_commit(&bar[SB_A]);
           // (the state's high halves are what the gradients take of it)
           if (STATES) box_store(&maps.s0, sb + ScanSmem::S, tile * TN, 0, (s.slot0 + c) * a.H + h);
-          if (c > 0) {
-            if (!(ok = wait(SB_O, c - 1))) break;
-            load_ph(c);
-          }
-          if (!(ok = wait(SB_A, c))) break;
-          if (c + 1 < nc) load_rows(c + 1);
           if (!(ok = wait(SB_KD, c) && (c == 0 || wait(SB_OF, c - 1)) && wait(SB_WR, c))) break;
           if (STATES) stores_read();  // (the state is written again once the next product is there)
           tc_fence_after();
@@ -649,15 +750,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma(at_a, dp + kk * 32u, db + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
           umma_commit(&bar[SB_O]);
-          if (c + 1 < nc) load_v(c + 1);
-          if (c + 2 < nc) prefetch(c + 2);
-          if (!(ok = wait(SB_C, c))) break;
-          if (c + 1 < nc) load_kd(c + 1);
         }
         // what was issued ends before its memory is given up
         umma_commit(&bar[SB_DRAIN]);
         mbar_wait_drain(&bar[SB_DRAIN], 0, DRAIN_NS, a.err);
-        for (int x = 0; x < 4; ++x) mbar_wait_drain(&bar[SB_KQ + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
         stores_read();
       }
       __syncwarp();
@@ -670,7 +766,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         for (int e = 0; e < 8; ++e) split2(S[8 * x + e], hi[e], lo[e]);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const uint32_t at = sb + ScanSmem::S + sw128(row, 4 * half + 2 * x + p);
+          const uint32_t at = sb + ScanSmem::S + sw128(srow, 4 * half + 2 * x + p);
           st_shared_v4(at, hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
           st_shared_v4(at + 12288, lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
         }
@@ -682,7 +778,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         mbar_arrive(&bar[SB_SR]);
       }
       float2 keep[16];  // e^G Q S0, or (STATES) R
-      // The outputs of chunk c (rows 64-127), from the place that its first product had.
+      // The outputs of chunk c, from the place that its first product had.
       const uint32_t stage = sb + ScanSmem::OUT + 2048u * ((q & 1) + 2 * half);  // this warp's 32 rows x 32 columns
       auto outputs = [&](int c) {
         ok = __all_sync(0xffffffffu, wait(SB_O, c));
@@ -794,7 +890,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   if (!STATES && a.hT && s_row) {
     const int to = delta_row(a.hT_row, a.hT_rows, n, a.err);
     if (to >= 0) {
-      float4* dst = reinterpret_cast<float4*>(a.hT + (((long long)to * a.H + h) * DK + row) * DV + col0);
+      float4* dst = reinterpret_cast<float4*>(a.hT + (((long long)to * a.H + h) * DK + srow) * DV + col0);
 #pragma unroll
       for (int x = 0; x < 8; ++x) dst[x] = make_float4(S[2 * x].x, S[2 * x].y, S[2 * x + 1].x, S[2 * x + 1].y);
     }
@@ -806,9 +902,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 //     dU = s P^T dO + diag(E) K dS1,   w = B dU,   dS0 = e^(G_C) dS1 + Q~ dO + K~ w,   dv = B (dU - Z^T w)
 // (E = e^(G_C - G)): again two dependent products a chunk.  P^T dO and Q~ dO need no state and are issued a chunk
 // ahead.  dbeta's part of the CTA's columns is (dU - Z^T w) . X.
-// 512 threads, one CTA an SM (the operands take 220 KB): warps 0-7 have the state's rows (0-95; columns as in the scan),
-// warps 8-15 the tokens' (0-63), so that neither waits for what the other writes out; of the warps that have no rows, 11
-// issues the products and 15 the copies.  Every hand-over through an mbarrier.
+// 512 threads, one CTA an SM (the operands take 214 KB): warps 0-7 have the state's rows (0-95; columns as in the scan),
+// warps 8-15 the tokens' (64-127: other schedulers), so that neither waits for what the other writes out; of the warps
+// that have no rows, 8 issues the products and 12 the copies.  Every hand-over through an mbarrier.
 // Tensor memory: P^T dO [0,64), Q~ dO [64,192) (by chunk parity), K dS1 [192,320) and K~ w [320,448) as [hi | lo],
 // Z^T w [448,512).
 constexpr int RSCAN_THREADS = 512;
@@ -816,10 +912,10 @@ struct RSmem {
   // of the chunk ahead (two places): Q~ hi, lo; P hi, lo; dO; X
   static constexpr uint32_t EARLY = 0, E_QT = 0, E_P = 24576, E_DO = 40960, E_X = 49152, E_BYTES = 57344;
   // K~ hi, lo and Z; K; the state; w; two places of e^G, beta, E.  Products of 128 rows read past operands of 64 and 96
-  // rows; what stands there is either as still as the operand or (8 KB behind Z, behind K) never written, and the
-  // rows it gives are not looked at.
-  static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 16384, S = K1 + 8192, W = S + 24576, OUT = W + 16384, GT = OUT + 8192,
-                            BAR = GT + 2 * 768, BYTES = BAR + 144;
+  // rows: before K, whose rows are the second half, 8 KB that are never written; before Z and P, and behind K~ and Q~, what
+  // is as still as the operand itself.  The rows that gives are not looked at.
+  static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 8192, S = K1 + 4096, W = S + 24576, OUT = W + 16384,
+                            GT = OUT + 8192, BAR = GT + 2 * 768, BYTES = BAR + 144;
   static_assert(BYTES <= 232448, "shared memory");
 };
 // Products and copies, then hand-overs: the state, w, Z^T w and X read.  Whoever waits for a phase of a barrier hands
@@ -834,10 +930,11 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + RSmem::BAR);
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + RSmem::BAR + 8 * RB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + RSmem::BAR + 8 * RB_N + 4);
-  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = nh / a.H;
+  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = a.order ? a.order[nh / a.H] : nh / a.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = (warp >> 2) & 1;
   const int row = lane + 32 * q, col0 = tile * TN + 32 * half;
-  const bool t_row = warp >= 8 && q < 2, s_row = warp < 8 && q < 3;
+  const bool t_row = warp >= 8 && q >= 2, s_row = warp < 8 && q < 3;
+  const int tok = row - 64;  // (of a token row)
   const DeltaSeq s = delta_seq(a, n);
   const int nc = (s.len + DC - 1) / DC;
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
@@ -856,7 +953,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
     }
   }
   if (nc > 0) {
-    if (warp == 15) {
+    if (warp == 12) {
       tm_alloc<512>(slot_tm);
       if (lane == 0) {
         for (int x = 0; x < RB_N; ++x) mbar_init(&bar[x], x == RB_SR ? 192 : x == RB_WR || x == RB_ZF || x == RB_ZF + 1 ? 128 : 1);
@@ -871,7 +968,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
     const uint32_t tmem = *slot_tm;
     auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
     bool ok = true;
-    if (warp == 15) {
+    if (warp == 12) {
       if (lane == 0) {
         // copies: each as soon as what stood in its place has been used
         int loads[4] = {};  // EARLY's two places, K, K~
@@ -927,7 +1024,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         for (int it = max(0, loads[2] - 2); it < loads[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
       }
       __syncwarp();
-    } else if (warp == 11) {
+    } else if (warp == 8) {
       // products
       const int rest = s.len - (nc - 1) * DC;  // tokens of the last chunk
       if (rest < DC) {  // rows of dO behind them hold the next sequence's
@@ -944,7 +1041,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           if (!wait(RB_EF + p, it >> 1)) return false;
           tc_fence_after();
           const uint32_t from = sb + RSmem::EARLY + p * RSmem::E_BYTES;
-          const SDesc dp = sdesc(from + RSmem::E_P, 8192, 1024, LAYOUT_SW128), dq = sdesc(from + RSmem::E_QT, 16, 1024, LAYOUT_SW128);
+          const SDesc dp = sdesc(from + RSmem::E_P - 8192, 8192, 1024, LAYOUT_SW128), dq = sdesc(from + RSmem::E_QT, 16, 1024, LAYOUT_SW128);
           const SDesc dd = sdesc(from + RSmem::E_DO, 8192, 1024, LAYOUT_SW128);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -960,7 +1057,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           ok = wait(RB_K, it) && wait(RB_SR, it);
           if (!ok) break;
           tc_fence_after();
-          const SDesc k0 = sdesc(sb + RSmem::K0, 16, 1024, LAYOUT_SW128), k1 = sdesc(sb + RSmem::K1, 16, 512, LAYOUT_SW64);
+          const SDesc k0 = sdesc(sb + RSmem::K0 - 8192, 16, 1024, LAYOUT_SW128), k1 = sdesc(sb + RSmem::K1 - 4096, 16, 512, LAYOUT_SW64);
           const SDesc ds = sdesc(sb + RSmem::S, 12288, 1024, LAYOUT_SW128);
 #pragma unroll
           for (int kk = 0; kk < 6; ++kk)
@@ -972,7 +1069,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           if (!ok) break;
           tc_fence_after();
           stores_read();  // (the state is written again once the next product is there)
-          const SDesc dr = sdesc(sb + RSmem::KR, 16, 1024, LAYOUT_SW128), dz = sdesc(sb + RSmem::KR + 24576, 8192, 1024, LAYOUT_SW128);
+          const SDesc dr = sdesc(sb + RSmem::KR, 16, 1024, LAYOUT_SW128), dz = sdesc(sb + RSmem::KR + 24576 - 8192, 8192, 1024, LAYOUT_SW128);
           const SDesc dw = sdesc(sb + RSmem::W, 8192, 1024, LAYOUT_SW128);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -1031,16 +1128,16 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
       }
     } else if (t_row) {
       const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 32u * half;
-      const uint32_t stage = sb + RSmem::OUT + 2048u * (q + 2 * half);  // this warp's 32 rows x 32 columns
+      const uint32_t stage = sb + RSmem::OUT + 2048u * (q - 2 + 2 * half);  // this warp's 32 rows x 32 columns
       float2 du[16];
       for (int it = 0; it < nc; ++it) {
         const int c = nc - 1 - it, left = s.len - c * DC;
-        const bool live = row < left;
+        const bool live = tok < left;
         ok = wait(RB_GT + (it & 1), it >> 1) && wait(RB_E + (it & 1), it >> 1) && wait(RB_A, it);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float* gt = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * 768);
-        const float b_row = gt[GT_B + row], e_row = gt[GT_E + row];
+        const float b_row = gt[GT_B + tok], e_row = gt[GT_E + tok];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t d[32], p[32], hi[8], lo[8];
@@ -1056,7 +1153,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t at = sb + RSmem::W + sw128(row, 4 * half + 2 * x + i);
+            const uint32_t at = sb + RSmem::W + sw128(tok, 4 * half + 2 * x + i);
             st_shared_v4(at, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
             st_shared_v4(at + 8192, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
           }
@@ -1076,7 +1173,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           tm_ld16(lanes + RT_Z + 16 * x, z);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint4 x4 = ld_shared_v4(sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES + RSmem::E_X + sw128(row, 4 * half + 2 * x + i));
+            const uint4 x4 = ld_shared_v4(sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES + RSmem::E_X + sw128(tok, 4 * half + 2 * x + i));
             const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -1091,7 +1188,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
             st_shared_v4(stage + sw64(lane, 2 * x), w[0], w[1], w[2], w[3]);
             st_shared_v4(stage + sw64(lane, 2 * x + 1), w[4], w[5], w[6], w[7]);
           } else if (live) {  // a sequence's last rows: no box is written past them
-            uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.dv + ((t0 + row) * a.H + h) * DV + col0);
+            uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.dv + ((t0 + tok) * a.H + h) * DV + col0);
             dst[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
             dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
           }
@@ -1101,15 +1198,15 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         if (left >= DC) {
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) box_store(&maps.dvo, stage, col0, h, (int)(t0 + 32 * q));
+          if (lane == 0) box_store(&maps.dvo, stage, col0, h, (int)(t0 + 32 * (q - 2)));
         }
-        if (live) dbeta_part[((long long)(2 * tile + half) * tokens + t0 + row) * a.H + h] = part.x + part.y;
+        if (live) dbeta_part[((long long)(2 * tile + half) * tokens + t0 + tok) * a.H + h] = part.x + part.y;
       }
       if (lane == 0) stores_read();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 15) {
+    if (warp == 12) {
       tc_fence_after();
       tm_free<512>(tmem);
     }
@@ -1182,6 +1279,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
     load_panel(0);
+    for (int p = 1; p < 3; ++p) {  // the other panels, into L2
+      box_prefetch(&maps.dO, 64 * p, h, (int)ch.t0);
+      box_prefetch(&maps.dv, 64 * p, h, (int)ch.t0);
+    }
+    bulk_prefetch(ws + W_S0, W_BWD - W_S0);
     mbar_expect_tx(&bar[GB_KQ], 4 * 8192 + 1280);
     for (int p = 0; p < 2; ++p) {
       box_load(sb + GSmem::K + 8192 * p, &maps.k0, &bar[GB_KQ], 64 * p, h, (int)ch.t0);
@@ -1418,8 +1520,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
 
 }  // namespace
 
-size_t delta_tc_ws_bytes(long long slots, long long tokens, int H, bool bwd) {
-  return (size_t)slots * H * (bwd ? W_BWD : W_FWD) + (bwd ? (size_t)2 * NTILE * tokens * H * 4 : 0);
+size_t delta_tc_ws_bytes(int n_seq, long long slots, long long tokens, int H, bool bwd) {
+  return (size_t)slots * H * (bwd ? W_BWD : W_FWD) + (bwd ? (size_t)2 * NTILE * tokens * H * 4 : 0) + (size_t)n_seq * 4;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1450,12 +1552,18 @@ static bool input_maps(DeltaMaps& m, const DeltaArgs& a) {
   return rows_map(&m.k0, a.k, DK, a, 64, DC) && rows_map(&m.k1, a.k, DK, a, 32, DC) && rows_map(&m.q0, a.q, DK, a, 64, DC) &&
          rows_map(&m.q1, a.q, DK, a, 32, DC) && rows_map(&m.v, a.v, DV, a, 64, DC);
 }
+// CTAs b and b + this many are likely to share an SM.
+static int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
 template <class F>
 static cudaError_t allow(F* f, uint32_t bytes) {
   return cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
+cudaError_t launch_delta_tc_fwd(DeltaArgs a, cudaStream_t st) {
   static OncePerDevice<CudaDeviceApi> once;
   const cudaError_t e = once([] {
     const cudaError_t x = allow(delta_prep_kernel<false>, PrepSmem::bytes(false));
@@ -1465,15 +1573,17 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
   DeltaMaps m;
   memset(&m, 0, sizeof(m));
   const unsigned chunks = (unsigned)a.slots * a.H, units = (unsigned)a.n_seq * a.H * NTILE;
-  if (a.cu_seqlens ? a.T > 0 : a.slots > 0) {
+  const bool some = a.cu_seqlens ? a.T > 0 : a.slots > 0;
+  if (some && a.cu_seqlens && a.n_seq > 1) a.order = reinterpret_cast<int32_t*>(a.ws + (long long)a.slots * a.H * W_FWD);
+  if (some) {
     if (!(input_maps(m, a) && rows_map(&m.o, a.o, DV, a, 32, 32))) return cudaErrorInvalidValue;
     delta_prep_kernel<false><<<chunks, PREP_THREADS, PrepSmem::bytes(false), st>>>(m, a);
   }
-  delta_scan_kernel<false><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a);
+  delta_scan_kernel<false><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a, sm_count());
   return cudaGetLastError();
 }
 
-cudaError_t launch_delta_tc_bwd(const DeltaArgs& a, cudaStream_t st) {
+cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t st) {
   static OncePerDevice<CudaDeviceApi> once;
   const cudaError_t e = once([] {
     for (cudaError_t x : {allow(delta_prep_kernel<true>, PrepSmem::bytes(true)), allow(delta_scan_kernel<true>, ScanSmem::BYTES),
@@ -1487,6 +1597,8 @@ cudaError_t launch_delta_tc_bwd(const DeltaArgs& a, cudaStream_t st) {
   const unsigned chunks = (unsigned)a.slots * a.H, units = (unsigned)a.n_seq * a.H * NTILE;
   float* const part = reinterpret_cast<float*>(a.ws + (long long)a.slots * a.H * W_BWD);
   const bool some = a.cu_seqlens ? a.T > 0 : a.slots > 0;
+  const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
+  if (some && a.cu_seqlens && a.n_seq > 1) a.order = reinterpret_cast<int32_t*>(part + 2ll * NTILE * tokens * a.H);
   if (some) {
     const long long all = (long long)a.slots * a.H;
     if (!(input_maps(m, a) && rows_map(&m.dO, a.dO, DV, a, 64, DC) && rows_map(&m.dv, a.dv, DV, a, 64, DC) &&
@@ -1495,7 +1607,7 @@ cudaError_t launch_delta_tc_bwd(const DeltaArgs& a, cudaStream_t st) {
           rows_map(&m.dvo, a.dv, DV, a, 32, 32)))
       return cudaErrorInvalidValue;
     delta_prep_kernel<true><<<chunks, PREP_THREADS, PrepSmem::bytes(true), st>>>(m, a);
-    delta_scan_kernel<true><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a);
+    delta_scan_kernel<true><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a, sm_count());
   }
   delta_rscan_kernel<<<units, RSCAN_THREADS, RSmem::BYTES, st>>>(m, a, part);
   if (some) delta_grads_kernel<<<chunks, GRAD_THREADS, GSmem::BYTES, st>>>(m, a, part);
