@@ -143,6 +143,18 @@ __device__ __forceinline__ void tm_free(uint32_t tmem) {
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
 
+// mbar_wait with a look first: try_wait takes its time even where the phase has ended.  (For a thread that mostly finds
+// it ended: the reverse scan's issuer, 228 -> 213 us; the scans, whose two CTAs share an SM, lose 3 % to 10 % by it.)
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, volatile int* abort) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0 || mbar_wait(bar, parity, limit_ns, abort);
+}
+
 constexpr unsigned long long DRAIN_NS = 1000000000ull;
 
 // Tensor maps of a call.  K and Q: a chunk's 64 rows in two boxes, columns 0-63 (128-byte rows) and 64-95 (64-byte
@@ -900,29 +912,28 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 // ---- reverse scan ---------------------------------------------------------------------------
 // One CTA a (sequence, head, 64 columns of d_v), chunks from the last: with dS1 = dL/dS1 of the chunk,
 //     dU = s P^T dO + diag(E) K dS1,   w = B dU,   dS0 = e^(G_C) dS1 + Q~ dO + K~ w,   dv = B (dU - Z^T w)
-// (E = e^(G_C - G)): again two dependent products a chunk.  P^T dO and Q~ dO need no state and are issued a chunk
-// ahead.  dbeta's part of the CTA's columns is (dU - Z^T w) . X.
+// (E = e^(G_C - G)): again two dependent products a chunk.  P^T dO and Q~ dO need no state; they go to the tensor cores
+// while the state's way waits for registers: Q~ dO behind K dS1, the next chunk's P^T dO behind Z^T w.  dbeta's part of the CTA's columns is (dU - Z^T w) . X.
 // 512 threads, one CTA an SM (the operands take 214 KB): warps 0-7 have the state's rows (0-95; columns as in the scan),
 // warps 8-15 the tokens' (64-127: other schedulers), so that neither waits for what the other writes out; of the warps
 // that have no rows, 8 issues the products and 12 the copies.  Every hand-over through an mbarrier.
-// Tensor memory: P^T dO [0,64), Q~ dO [64,192) (by chunk parity), K dS1 [192,320) and K~ w [320,448) as [hi | lo],
-// Z^T w [448,512).
+// Tensor memory: P^T dO [0,64), Q~ dO [64,128), K dS1 [128,256) and K~ w [256,384) as [hi | lo], Z^T w [384,448).
 constexpr int RSCAN_THREADS = 512;
 struct RSmem {
-  // of the chunk ahead (two places): Q~ hi, lo; P hi, lo; dO; X
+  // of the chunk ahead (two places): Q~ hi, lo; P hi, lo; dO; and X, which is used last
   static constexpr uint32_t EARLY = 0, E_QT = 0, E_P = 24576, E_DO = 40960, E_X = 49152, E_BYTES = 57344;
   // K~ hi, lo and Z; K; the state; w; two places of e^G, beta, E.  Products of 128 rows read past operands of 64 and 96
   // rows: before K, whose rows are the second half, 8 KB that are never written; before Z and P, and behind K~ and Q~, what
   // is as still as the operand itself.  The rows that gives are not looked at.
   static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 8192, S = K1 + 4096, W = S + 24576, OUT = W + 16384,
-                            GT = OUT + 8192, BAR = GT + 2 * 768, BYTES = BAR + 144;
+                            GT = OUT + 8192, BAR = GT + 2 * 768, BYTES = BAR + 160;
   static_assert(BYTES <= 232448, "shared memory");
 };
 // Products and copies, then hand-overs: the state, w, Z^T w and X read.  Whoever waits for a phase of a barrier hands
 // something over before the next one can end; where that would not hold (E's, the decays', ZF) there are two, by the
 // chunk's parity.
-enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_DRAIN, RB_ZF, RB_GT = RB_ZF + 2, RB_N = RB_GT + 2 };
-constexpr uint32_t RT_P = 0, RT_Q = 64, RT_A = 192, RT_C = 320, RT_Z = 448;
+enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_DRAIN, RB_ZF, RB_GT = RB_ZF + 2, RB_X = RB_GT + 2, RB_N = RB_X + 2 };
+constexpr uint32_t RT_P = 0, RT_Q = 64, RT_A = 128, RT_C = 256, RT_Z = 384;
 
 __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, float* dbeta_part) {
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -967,20 +978,25 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
     tc_fence_after();
     const uint32_t tmem = *slot_tm;
     auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
+    auto look = [&](int b, int k) { return bar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };  // (the issuing thread)
     bool ok = true;
     if (warp == 12) {
       if (lane == 0) {
         // copies: each as soon as what stood in its place has been used
-        int loads[4] = {};  // EARLY's two places, K, K~
+        int loads[4] = {}, xs = 0;  // EARLY's two places, K, K~; X
         auto load_early = [&](int it) {
           const int c = nc - 1 - it, p = it & 1;
           const uint32_t to = sb + RSmem::EARLY + p * RSmem::E_BYTES;
           ++loads[p];
-          mbar_expect_tx(&bar[RB_EF + p], RSmem::E_BYTES);
+          mbar_expect_tx(&bar[RB_EF + p], RSmem::E_X);
           bulk_load(to + RSmem::E_QT, ws_of(c) + W_QT, 24576, &bar[RB_EF + p]);
           bulk_load(to + RSmem::E_P, ws_of(c) + W_P, 16384, &bar[RB_EF + p]);
           box_load(to + RSmem::E_DO, &maps.dO, &bar[RB_EF + p], tile * TN, h, (int)(s.begin + (long long)c * DC));
-          box_load(to + RSmem::E_X, &maps.x, &bar[RB_EF + p], tile * TN, 0, (s.slot0 + c) * a.H + h);
+        };
+        auto load_x = [&](int it) {
+          const int c = nc - 1 - it, p = it & 1;
+          mbar_expect_tx(&bar[RB_X + p], 8192);
+          box_load(sb + RSmem::EARLY + p * RSmem::E_BYTES + RSmem::E_X, &maps.x, &bar[RB_X + p], tile * TN, 0, (s.slot0 + c) * a.H + h);
         };
         auto load_k = [&](int it) {
           const int c = nc - 1 - it, t = (int)(s.begin + (long long)c * DC);
@@ -1010,18 +1026,22 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         load_k(0);
         load_kr(0);
         if (nc > 1) load_early(1);
+        for (; xs < min(nc, 2); ++xs) load_x(xs);
         for (int it = 0; it < nc && ok; ++it) {
           if (it + 2 < nc) prefetch(it + 2);
           ok = wait(RB_A, it);
           if (ok && it + 1 < nc) load_k(it + 1);
+          ok = ok && wait(RB_C, it);
+          if (ok && it + 2 < nc) load_early(it + 2);
           ok = ok && wait(RB_Z, it);
           if (ok && it + 1 < nc) load_kr(it + 1);
-          ok = ok && wait(RB_ZF + (it & 1), it >> 1);  // (X has been read; its other products are long done)
-          if (ok && it + 2 < nc) load_early(it + 2);
+          ok = ok && wait(RB_ZF + (it & 1), it >> 1);
+          if (ok && it + 2 < nc) load_x(xs++);
         }
         for (int x = 0; x < 4; ++x)
           if (loads[x]) mbar_wait_drain(&bar[RB_EF + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
         for (int it = max(0, loads[2] - 2); it < loads[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
+        for (int it = max(0, xs - 2); it < xs; ++it) mbar_wait_drain(&bar[RB_X + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
       }
       __syncwarp();
     } else if (warp == 8) {
@@ -1036,25 +1056,21 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         __syncwarp();
       }
       if (lane == 0) {
-        auto early = [&](int it) {
+        auto early = [&](int it) {  // P^T dO
           const int p = it & 1;
-          if (!wait(RB_EF + p, it >> 1)) return false;
+          if (!look(RB_EF + p, it >> 1)) return false;
           tc_fence_after();
           const uint32_t from = sb + RSmem::EARLY + p * RSmem::E_BYTES;
-          const SDesc dp = sdesc(from + RSmem::E_P - 8192, 8192, 1024, LAYOUT_SW128), dq = sdesc(from + RSmem::E_QT, 16, 1024, LAYOUT_SW128);
-          const SDesc dd = sdesc(from + RSmem::E_DO, 8192, 1024, LAYOUT_SW128);
+          const SDesc dp = sdesc(from + RSmem::E_P - 8192, 8192, 1024, LAYOUT_SW128), dd = sdesc(from + RSmem::E_DO, 8192, 1024, LAYOUT_SW128);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma(tmem + RT_P, dp + (kk >> 2) * 8192u + (kk & 3) * 2048u, dd + (kk & 3) * 2048u, idesc_bf16(128, 64, 1, 1), kk > 0);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma(tmem + RT_Q + 64 * p, dq + (kk >> 2) * 12288u + (kk & 3) * 32u, dd + (kk & 3) * 2048u, idesc_bf16(128, 64, 0, 1), kk > 0);
           umma_commit(&bar[RB_E + p]);
           return true;
         };
         ok = ok && early(0);
         for (int it = 0; it < nc && ok; ++it) {
-          ok = wait(RB_K, it) && wait(RB_SR, it);
+          ok = look(RB_K, it) && look(RB_SR, it);
           if (!ok) break;
           tc_fence_after();
           const SDesc k0 = sdesc(sb + RSmem::K0 - 8192, 16, 1024, LAYOUT_SW128), k1 = sdesc(sb + RSmem::K1 - 4096, 16, 512, LAYOUT_SW64);
@@ -1065,7 +1081,14 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           umma_commit(&bar[RB_A]);
           // (the state's high halves are what the gradients take of it)
           box_store(&maps.ds, sb + RSmem::S, tile * TN, 0, (s.slot0 + nc - 1 - it) * a.H + h);
-          ok = wait(RB_KR, it) && wait(RB_WR, it);
+          {  // Q~ dO (its operands came with P's)
+            const uint32_t from = sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES;
+            const SDesc dq = sdesc(from + RSmem::E_QT, 16, 1024, LAYOUT_SW128), dd = sdesc(from + RSmem::E_DO, 8192, 1024, LAYOUT_SW128);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma(tmem + RT_Q, dq + (kk >> 2) * 12288u + (kk & 3) * 32u, dd + (kk & 3) * 2048u, idesc_bf16(128, 64, 0, 1), kk > 0);
+          }
+          ok = look(RB_KR, it) && wait(RB_WR, it);
           if (!ok) break;
           tc_fence_after();
           stores_read();  // (the state is written again once the next product is there)
@@ -1075,7 +1098,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           for (int kk = 0; kk < 8; ++kk)
             umma(tmem + RT_C, dr + (kk >> 2) * 12288u + (kk & 3) * 32u, dw + (kk & 3) * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
           umma_commit(&bar[RB_C]);
-          ok = it == 0 || wait(RB_ZF + ((it - 1) & 1), (it - 1) >> 1);
+          ok = it == 0 || look(RB_ZF + ((it - 1) & 1), (it - 1) >> 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -1115,7 +1138,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         for (int x = 0; x < 2; ++x) {
           uint32_t d[32], y[32];
           tm_ld16x2(lanes + RT_C + 16 * x, lanes + RT_C + 64 + 16 * x, d);
-          tm_ld16(lanes + RT_Q + 64 * (it & 1) + 16 * x, y);
+          tm_ld16(lanes + RT_Q + 16 * x, y);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             S[8 * x + e] = fmadd2(both(last), S[8 * x + e],
@@ -1162,7 +1185,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         tc_fence_before();
         mbar_arrive(&bar[RB_WR]);
         if (lane == 0) stores_read();
-        ok = wait(RB_EF + (it & 1), it >> 1) && wait(RB_Z, it);  // (X came with the chunk's early operands)
+        ok = wait(RB_X + (it & 1), it >> 1) && wait(RB_Z, it);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         float2 part = both(0.f);
@@ -1527,21 +1550,45 @@ size_t delta_tc_ws_bytes(int n_seq, long long slots, long long tokens, int H, bo
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-// bf16 [d2][d1][d0], strides in bytes, in boxes of `cols` (64: 128-byte swizzle, 32: 64-byte) x r1 x r2.
+typedef CUresult (*ReplaceAddressFn)(CUtensorMap*, void*);
+template <class F>
+static F driver_fn(const char* name) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  const bool found = cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess;
+  return found ? reinterpret_cast<F>(p) : nullptr;
+}
+// bf16 [d2][d1][d0], strides in bytes, in boxes of `cols` (64: 128-byte swizzle, 32: 64-byte) x r1 x r2.  Encoding a map
+// takes the host a microsecond, and a call has up to 13: each thread keeps the last ones that it encoded, by their shape, and
+// gives them the call's address.
 static bool map3(CUtensorMap* m, const void* base, long long d0, long long d1, long long d2, long long s1, long long s2, int cols,
                  int r1, int r2) {
-  static const EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-                       q == cudaDriverEntryPointSuccess;
-    return found ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
-  }();
+  static const EncodeTiledFn encode = driver_fn<EncodeTiledFn>("cuTensorMapEncodeTiled");
+  static const ReplaceAddressFn replace = driver_fn<ReplaceAddressFn>("cuTensorMapReplaceAddress");
+  struct Kept {
+    long long key[8];
+    CUtensorMap map;
+  };
+  constexpr int KEPT = 32;
+  static thread_local Kept kept[KEPT];
+  static thread_local unsigned next = 0;
+  const long long key[8] = {d0, d1, d2, s1, s2, cols, r1, r2};
+  if (!encode || !replace) return false;
+  for (const Kept& k : kept)
+    if (memcmp(k.key, key, sizeof(key)) == 0) {
+      *m = k.map;
+      return replace(m, const_cast<void*>(base)) == CUDA_SUCCESS;
+    }
   const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2}, strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
   const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)r1, (cuuint32_t)r2}, step[3] = {1, 1, 1};
-  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  if (encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  Kept& k = kept[next++ % KEPT];
+  memcpy(k.key, key, sizeof(key));
+  k.map = *m;
+  return true;
 }
 // A [tokens, H, d] tensor in boxes of one head.
 static bool rows_map(CUtensorMap* m, const void* base, int d, const DeltaArgs& a, int cols, int rows) {
