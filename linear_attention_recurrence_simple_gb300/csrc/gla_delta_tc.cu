@@ -1249,21 +1249,23 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 // One CTA a (chunk, head).  Over d_v in three panels of 64 columns: [dO; dR] [X; S0]^T (128 x 160) and X dS1^T
 // (64 x 96); then, with Es = s (dO U^T) . D and Fm = -(dR U^T) . D,
 //     dq = s e^G dO S0^T + Es K
-//     dk = (E U dS1^T + Es^T Q + Fm^T K) + (-e^G dR S0^T + Fm K)
-//     dG = q . dq - k . (first) + k . (second), and at the chunk's end sum_j k_j . (E U dS1^T)_j + e^(G_C) <dS1, S0>
+//     dk = E U dS1^T - e^G dR S0^T + Fm K + (Es^T Q + Fm^T K)
+//     dG = q . dq - k . (E U dS1^T + Es^T Q + Fm^T K) + k . (Fm K - e^G dR S0^T), and at the chunk's end
+//          sum_j k_j . (E U dS1^T)_j + e^(G_C) <dS1, S0>
 //     dg_t = sum of dG_i, i >= t
-// 256 threads: warp w has lanes 32 (w % 4) .. and 48 columns of d_k (w / 4); lanes 0-63 have dq and the first part of
-// dk, 64-127 the second.  2 CTAs an SM.
-constexpr int GRAD_THREADS = 256;
+// 288 threads, 2 CTAs an SM: warps 0-7 have lanes 32 (w % 4) .. of the products' rows and 48 columns of d_k (w / 4); rows
+// 0-63 have dq, 64-127 all of dk.  Warp 8 issues copies and products.  Panels have two places, K and Q come into the second.
+// Bound by latency and, of 196 KB a chunk and head, by HBM.
+constexpr int GRAD_THREADS = 288;
 struct GSmem {
-  // a panel: [dO; dR], [X; S0], dS1.  Then (phase 2) Es and Fm in the place of [X; S0], the second part of dk, fp32, from
-  // the start on.  K and Q in two panels of 64 columns; dk's E U dS1^T, fp32.
-  static constexpr uint32_t DOR = 0, XS = 16384, DS = XS + 20480, K = DS + 12288, Q = K + 16384, DKS = Q + 16384, EF = XS, PART = 0;
-  static constexpr uint32_t GT = DKS + DC * 97 * 4, DG = GT + 1280, RED = DG + 4 * DC * 4, BAR = RED + 32, BYTES = BAR + 64;
+  // a panel: [dO; dR], [X; S0], dS1; later Es and Fm in the first place, K and Q (two tiles of 64 columns each) in the second.
+  // (Products of 128 rows read before X, Es and Fm what is as still as they are.)
+  static constexpr uint32_t DOR = 0, XS = 16384, DS = XS + 20480, PANEL = DS + 12288, K = PANEL, Q = K + 16384, EF = 8192;
+  static constexpr uint32_t GT = 2 * PANEL, CF = GT + 1280, DG = CF + 128, RED = DG + 4 * DC * 4, BAR = RED + 32, BYTES = BAR + 112;
   static_assert(BYTES <= 115712, "two CTAs an SM");
-  static_assert(DC * 97 * 4 <= DS && K % 1024 == 0 && GT % 16 == 0, "phase 2");
 };
-enum { GB_KQ = 0, GB_IN, GB_MMA, GB_DRAIN, GB_N };
+// Copies, the panels read by the threads, products.  (One phase of each, but for the first place's two panels.)
+enum { GB_KQ = 0, GB_IN, GB_FR = GB_IN + 2, GB_MMA = GB_FR + 2, GB_ONE = GB_MMA + 2, GB_EF, GB_TWO, GB_DRAIN, GB_N };
 constexpr uint32_t GT_DS = 160, GT_X2 = 96;  // tensor memory: X dS1^T; phase 2's second product
 
 __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, const float* dbeta_part) {
@@ -1274,69 +1276,120 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + GSmem::BAR + 8 * GB_N + 4);
   const float* const gt = reinterpret_cast<const float*>(sm + GSmem::GT);
   const float2* const sums = reinterpret_cast<const float2*>(sm + GSmem::GT + 4 * GT_SUM);
+  float* const cf = reinterpret_cast<float*>(sm + GSmem::CF);
   float* const dgp = reinterpret_cast<float*>(sm + GSmem::DG);
   float* const red = reinterpret_cast<float*>(sm + GSmem::RED);
-  const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = warp >> 2;
+  const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = (warp >> 2) & 1;
   const DeltaChunk ch = chunk_of_slot(a, slot);
   if (ch.len == 0) return;
   const int idx = slot * a.H + h;
   const uint8_t* const ws = a.ws + (long long)idx * W_BWD;
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
-  const bool first = q < 2;             // dq and the first part of dk
-  const int i = (lane + 32 * q) & 63;   // token
+  const bool first = q < 2;            // dq; else dk
+  const int i = (lane + 32 * q) & 63;  // token
   const bool live = i < ch.len;
-  int panels = 0;
-  auto load_panel = [&](int p) {
-    ++panels;
-    mbar_expect_tx(&bar[GB_IN], 49152);
-    box_load(sb + GSmem::DOR, &maps.dO, &bar[GB_IN], 64 * p, h, (int)ch.t0);
-    box_load(sb + GSmem::DOR + 8192, &maps.dv, &bar[GB_IN], 64 * p, h, (int)ch.t0);
-    box_load(sb + GSmem::XS, &maps.x, &bar[GB_IN], 64 * p, 0, idx);
-    box_load(sb + GSmem::XS + 8192, &maps.s0, &bar[GB_IN], 64 * p, 0, idx);
-    box_load(sb + GSmem::DS, &maps.ds, &bar[GB_IN], 64 * p, 0, idx);
-  };
-  if (warp == 1) tm_alloc<256>(slot_tm);
-  if (tid == 0) {
-    for (int x = 0; x < GB_N; ++x) mbar_init(&bar[x], 1);
-    *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    fence_async_smem();
-    load_panel(0);
-    for (int p = 1; p < 3; ++p) {  // the other panels, into L2
-      box_prefetch(&maps.dO, 64 * p, h, (int)ch.t0);
-      box_prefetch(&maps.dv, 64 * p, h, (int)ch.t0);
+  if (warp == 8) {
+    tm_alloc<256>(slot_tm);
+    if (lane == 0) {
+      for (int x = 0; x < GB_N; ++x) mbar_init(&bar[x], x == GB_FR || x == GB_FR + 1 || x == GB_EF ? 256 : 1);
+      *abort_flag = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      fence_async_smem();
     }
-    bulk_prefetch(ws + W_S0, W_BWD - W_S0);
-    mbar_expect_tx(&bar[GB_KQ], 4 * 8192 + 1280);
-    for (int p = 0; p < 2; ++p) {
-      box_load(sb + GSmem::K + 8192 * p, &maps.k0, &bar[GB_KQ], 64 * p, h, (int)ch.t0);
-      box_load(sb + GSmem::Q + 8192 * p, &maps.q0, &bar[GB_KQ], 64 * p, h, (int)ch.t0);
-    }
-    bulk_load(sb + GSmem::GT, ws + W_GT, 1280, &bar[GB_KQ]);
+  } else if (tid < 80) {
+    reinterpret_cast<uint4*>(sm + GSmem::GT)[tid] = reinterpret_cast<const uint4*>(ws + W_GT)[tid];
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot_tm;
   const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-  bool ok = true, gone = false;
-  float frob = 0.f;  // <dS1, S0>, this thread's part
-  for (int p = 0; p < 3; ++p) {
-    ok = ok && mbar_wait(&bar[GB_IN], p & 1, a.wait_ns, abort_flag);
-    if (tid == 0 && ok) {
-      const SDesc da = sdesc(sb + GSmem::DOR, 16, 1024, LAYOUT_SW128), dx = sdesc(sb + GSmem::XS, 16, 1024, LAYOUT_SW128);
-      const SDesc ds = sdesc(sb + GSmem::DS, 16, 1024, LAYOUT_SW128);
+  auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
+  bool ok = true;
+  if (warp == 8) {
+    if (lane == 0) {
+      const int t = (int)ch.t0;
+      int panels = 0, kqs = 0;
+      auto load_panel = [&](int p) {
+        ++panels;
+        const uint32_t to = sb + (p & 1) * GSmem::PANEL;
+        uint64_t* const in = &bar[GB_IN + (p & 1)];
+        mbar_expect_tx(in, GSmem::PANEL);
+        box_load(to + GSmem::DOR, &maps.dO, in, 64 * p, h, t);
+        box_load(to + GSmem::DOR + 8192, &maps.dv, in, 64 * p, h, t);
+        box_load(to + GSmem::XS, &maps.x, in, 64 * p, 0, idx);
+        box_load(to + GSmem::XS + 8192, &maps.s0, in, 64 * p, 0, idx);
+        box_load(to + GSmem::DS, &maps.ds, in, 64 * p, 0, idx);
+      };
+      auto products = [&](int p) {
+        const uint32_t at = sb + (p & 1) * GSmem::PANEL;
+        tc_fence_after();
+        const SDesc da = sdesc(at + GSmem::DOR, 16, 1024, LAYOUT_SW128), dx = sdesc(at + GSmem::XS, 16, 1024, LAYOUT_SW128);
+        const SDesc dx2 = sdesc(at + GSmem::XS - 8192, 16, 1024, LAYOUT_SW128), ds = sdesc(at + GSmem::DS, 16, 1024, LAYOUT_SW128);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) umma(tmem, da + kk * 32u, dx + kk * 32u, idesc_bf16(128, 160, 0, 0), p + kk > 0);
+        for (int kk = 0; kk < 4; ++kk) umma(tmem, da + kk * 32u, dx + kk * 32u, idesc_bf16(128, 160, 0, 0), p + kk > 0);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_DS, dx + kk * 32u, ds + kk * 32u, idesc_bf16(128, 96, 0, 0), p + kk > 0);
-      umma_commit(&bar[GB_MMA]);
+        for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_DS, dx2 + kk * 32u, ds + kk * 32u, idesc_bf16(128, 96, 0, 0), p + kk > 0);
+        umma_commit(&bar[GB_MMA + p]);
+      };
+      load_panel(0);
+      load_panel(1);
+      // what comes later, into L2
+      box_prefetch(&maps.dO, 128, h, t);
+      box_prefetch(&maps.dv, 128, h, t);
+      bulk_prefetch(ws + W_S0, W_BWD - W_S0);
+      for (int p = 0; p < 2; ++p) {
+        box_prefetch(&maps.k0, 64 * p, h, t);
+        box_prefetch(&maps.q0, 64 * p, h, t);
+      }
+      do {
+        if (!(ok = wait(GB_IN, 0))) break;
+        products(0);
+        if (!(ok = wait(GB_IN + 1, 0))) break;
+        products(1);
+        if (!(ok = wait(GB_MMA, 0) && wait(GB_FR, 0))) break;
+        load_panel(2);
+        if (!(ok = wait(GB_MMA + 1, 0) && wait(GB_FR + 1, 0))) break;
+        ++kqs;
+        mbar_expect_tx(&bar[GB_KQ], 4 * 8192);
+        for (int p = 0; p < 2; ++p) {
+          box_load(sb + GSmem::K + 8192 * p, &maps.k0, &bar[GB_KQ], 64 * p, h, t);
+          box_load(sb + GSmem::Q + 8192 * p, &maps.q0, &bar[GB_KQ], 64 * p, h, t);
+        }
+        if (!(ok = wait(GB_IN, 1))) break;
+        products(2);
+        if (!(ok = wait(GB_EF, 0))) break;
+        tc_fence_after();
+        const SDesc ef = sdesc(sb + GSmem::EF, 16, 1024, LAYOUT_SW128), et = sdesc(sb + GSmem::EF - 8192, 8192, 1024, LAYOUT_SW128);
+        const SDesc dk = sdesc(sb + GSmem::K, 8192, 1024, LAYOUT_SW128), dq = sdesc(sb + GSmem::Q, 8192, 1024, LAYOUT_SW128);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma(tmem, ef + kk * 32u, dk + kk * 2048u, idesc_bf16(128, 96, 0, 1), kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + kk * 2048u, dq + kk * 2048u, idesc_bf16(128, 96, 1, 1), kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + 8192u + kk * 2048u, dk + kk * 2048u, idesc_bf16(128, 96, 1, 1), 1);
+        umma_commit(&bar[GB_TWO]);
+      } while (false);
+      // what was issued ends before its memory is given up
+      umma_commit(&bar[GB_DRAIN]);
+      mbar_wait_drain(&bar[GB_DRAIN], 0, DRAIN_NS, a.err);
+      for (int p = max(0, panels - 2); p < panels; ++p) mbar_wait_drain(&bar[GB_IN + (p & 1)], p >> 1, DRAIN_NS, a.err);
+      if (kqs) mbar_wait_drain(&bar[GB_KQ], 0, DRAIN_NS, a.err);
     }
     __syncwarp();
-    if (ok)
+  } else {
+    if (tid < 32) {  // decay and strength of tokens 0-31 in those of 32-63: from there to token 31
+      const float2 x = sums[31], y = sums[tid];
+      cf[tid] = exp2_fast((x.x - y.x) + (x.y - y.y)) * gt[GT_B + tid];
+    }
+    float frob = 0.f;  // <dS1, S0>, this thread's part
+    for (int p = 0; p < 3 && ok; ++p) {
+      const uint32_t at = sb + (p & 1) * GSmem::PANEL;
+      ok = __all_sync(0xffffffffu, wait(GB_IN + (p & 1), p >> 1));
+      if (!ok) break;
 #pragma unroll
-      for (int e = tid; e < DK * 8; e += GRAD_THREADS) {  // (768 pieces of 16 bytes; the two tiles are swizzled alike)
-        const uint4 x = ld_shared_v4(sb + GSmem::XS + 8192 + 16 * e), y = ld_shared_v4(sb + GSmem::DS + 16 * e);
+      for (int e = tid; e < DK * 8; e += 256) {  // (768 pieces of 16 bytes; the two tiles are swizzled alike)
+        const uint4 x = ld_shared_v4(at + GSmem::XS + 8192 + 16 * e), y = ld_shared_v4(at + GSmem::DS + 16 * e);
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -1344,178 +1397,152 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
           frob = fmaf(u.x, v.x, fmaf(u.y, v.y, frob));
         }
       }
-    ok = ok && mbar_wait(&bar[GB_MMA], p & 1, a.wait_ns, abort_flag);
-    gone = __syncthreads_or(!ok);
-    if (gone) break;
-    if (tid == 0 && p < 2) load_panel(p + 1);
-  }
-  float at_end = 0.f;
-  float2 acc[24];  // s e^G dO S0^T, or -e^G dR S0^T: this thread's 48 columns of d_k
-  if (!gone) {
-    tc_fence_after();
-    ok = mbar_wait(&bar[GB_KQ], 0, a.wait_ns, abort_flag);
-    gone = __syncthreads_or(!ok);
-  }
-  if (!gone && ch.len < DC) {  // rows of K and Q behind the last token hold the next sequence's
-    for (int e = tid; e < 4 * (DC - ch.len) * 8; e += GRAD_THREADS) {
-      const int r = ch.len + (e >> 3) % (DC - ch.len), t = (e >> 3) / (DC - ch.len);
-      st_shared_v4(sb + GSmem::K + 8192 * t + 128 * r + 16 * (e & 7), 0u, 0u, 0u, 0u);
+      if (p < 2) mbar_arrive(&bar[GB_FR + p]);
     }
-    __syncthreads();
-  }
-  // 16-byte piece c (0 .. 5) of this thread's columns of row i of K or Q
-  auto piece = [&](uint32_t base, int c) {
-    const int x = 6 * half + c;
-    return ld_shared_v4(base + (x < 8 ? sw128(i, x) : 8192u + sw128(i, x - 8)));
-  };
-  if (!gone) {
-    const float2 gi = sums[i];
-    const float f_row = gt[GT_F + i], e_row = gt[GT_E + i] * gt[GT_B + i];
-    // Es and Fm
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      uint32_t d[32], w[8];
-      tm_ld16(lanes + 32 * half + 16 * x, d);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float y[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int j = 32 * half + 16 * x + 2 * e + b;
-          const float2 gj = sums[j];
-          const float t = exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * (gt[GT_B + j] * __uint_as_float(d[2 * e + b]));
-          y[b] = live && (first ? j <= i : j < i) ? (first ? a.scale * t : -t) : 0.f;
-        }
-        w[e] = bf2(y[0], y[1]);
-      }
-      const uint32_t to = sb + GSmem::EF + (first ? 0u : 8192u);
-      st_shared_v4(to + sw128(i, 4 * half + 2 * x), w[0], w[1], w[2], w[3]);
-      st_shared_v4(to + sw128(i, 4 * half + 2 * x + 1), w[4], w[5], w[6], w[7]);
-    }
-#pragma unroll
-    for (int x = 0; x < 3; ++x) {
-      uint32_t d[32];
-      tm_ld16(lanes + 64 + 48 * half + 16 * x, d);
-      const float2 w = both(first ? a.scale * f_row : -f_row);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[8 * x + e] = fmul2(w, make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
-    }
-    if (first) {
-      float* const dks = reinterpret_cast<float*>(sm + GSmem::DKS) + i * 97 + 48 * half;
-#pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        uint32_t d[32];
-        tm_ld16(lanes + GT_DS + 48 * half + 16 * x, d);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 k4 = piece(sb + GSmem::K, 2 * x + c);
-          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 k = widen2(kw[e]);
-            const float y0 = e_row * __uint_as_float(d[8 * c + 2 * e]), y1 = e_row * __uint_as_float(d[8 * c + 2 * e + 1]);
-            dks[16 * x + 8 * c + 2 * e] = y0;
-            dks[16 * x + 8 * c + 2 * e + 1] = y1;
-            if (live) at_end = fmaf(k.x, y0, fmaf(k.y, y1, at_end));
-          }
-        }
-      }
-    }
-    fence_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (tid == 0) {
+    ok = ok && wait(GB_KQ, 0) && wait(GB_ONE, 0);
+    ok = __all_sync(0xffffffffu, ok);
+    // 16-byte piece c (0 .. 5) of this thread's columns of row i of K or Q
+    auto piece = [&](uint32_t base, int c) {
+      const int x = 6 * half + c;
+      return ld_shared_v4(base + (x < 8 ? sw128(i, x) : 8192u + sw128(i, x - 8)));
+    };
+    float at_end = 0.f, dg = 0.f;
+    float2 acc[24];  // s e^G dO S0^T, or E U dS1^T - e^G dR S0^T: this thread's 48 columns of d_k
+    if (ok) {
       tc_fence_after();
-      const SDesc ef = sdesc(sb + GSmem::EF, 16, 1024, LAYOUT_SW128), et = sdesc(sb + GSmem::EF, 8192, 1024, LAYOUT_SW128);
-      const SDesc dk = sdesc(sb + GSmem::K, 8192, 1024, LAYOUT_SW128), dq = sdesc(sb + GSmem::Q, 8192, 1024, LAYOUT_SW128);
+      if (ch.len < DC)  // rows of K and Q behind the last token hold the next sequence's
+        for (int e = tid; e < 4 * (DC - ch.len) * 8; e += 256) {
+          const int r = ch.len + (e >> 3) % (DC - ch.len), x = (e >> 3) / (DC - ch.len);
+          st_shared_v4(sb + GSmem::K + 8192 * x + 128 * r + 16 * (e & 7), 0u, 0u, 0u, 0u);
+        }
+      const float2 gi = sums[i];
+      const float sign = first ? a.scale : -1.f;
+      // Es and Fm: columns 32 half .. of row i, three kinds of blocks of 32 x 32
+      const uint32_t to = sb + GSmem::EF + (first ? 0u : 8192u);
+      const int rows = q & 1;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) umma(tmem, ef + kk * 32u, dk + kk * 2048u, idesc_bf16(128, 96, 0, 1), kk > 0);
+      for (int x = 0; x < 2; ++x) {
+        uint32_t w[8];
+        if (half > rows) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + kk * 2048u, dq + kk * 2048u, idesc_bf16(128, 96, 1, 1), kk > 0);
+          for (int e = 0; e < 8; ++e) w[e] = 0u;
+        } else {
+          uint32_t d[32];
+          tm_ld16(lanes + 32 * half + 16 * x, d);
+          if (half < rows) {
+            const float2 m = sums[31];
+            const float f = live ? sign * exp2_fast((gi.x - m.x) + (gi.y - m.y)) : 0.f;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + 8192u + kk * 2048u, dk + kk * 2048u, idesc_bf16(128, 96, 1, 1), 1);
-      umma_commit(&bar[GB_MMA]);
-    }
-    __syncwarp();
-    ok = mbar_wait(&bar[GB_MMA], 1, a.wait_ns, abort_flag);
-    gone = __syncthreads_or(!ok);
-  }
-  if (!gone) {
-    tc_fence_after();
-    float dg = 0.f;
-    float* const part = reinterpret_cast<float*>(sm + GSmem::PART) + i * 97 + 48 * half;
-    const float* const dks = reinterpret_cast<const float*>(sm + GSmem::DKS) + i * 97 + 48 * half;
+            for (int e = 0; e < 8; ++e) {
+              const float2 c = *reinterpret_cast<const float2*>(cf + 16 * x + 2 * e);
+              const float2 y = fmul2(fmul2(both(f), c), make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+              w[e] = live ? bf2(y.x, y.y) : 0u;
+            }
+          } else {
 #pragma unroll
-    for (int x = 0; x < 3; ++x) {
-      uint32_t d[32];
-      tm_ld16(lanes + 48 * half + 16 * x, d);
+            for (int e = 0; e < 8; ++e) {
+              float y[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[8 * x + e] = fadd2(acc[8 * x + e], make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint4 r4 = piece(first ? sb + GSmem::Q : sb + GSmem::K, 2 * x + c);
-        const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 y = acc[8 * x + 4 * c + e], r = widen2(rw[e]);
-          dg = fmaf(r.x, y.x, fmaf(r.y, y.y, dg));
-          if (!first) {
-            part[16 * x + 8 * c + 2 * e] = y.x;
-            part[16 * x + 8 * c + 2 * e + 1] = y.y;
+              for (int b = 0; b < 2; ++b) {
+                const int j = 32 * half + 16 * x + 2 * e + b;
+                const float2 gj = sums[j];
+                const float v = exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * (sign * gt[GT_B + j] * __uint_as_float(d[2 * e + b]));
+                y[b] = live && (first ? j <= i : j < i) ? v : 0.f;
+              }
+              w[e] = bf2(y[0], y[1]);
+            }
           }
         }
-        if (first && live) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = bf2(acc[8 * x + 4 * c + e].x, acc[8 * x + 4 * c + e].y);
-          reinterpret_cast<uint4*>((__nv_bfloat16*)a.dq + ((ch.t0 + i) * a.H + h) * DK + 48 * half)[2 * x + c] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        st_shared_v4(to + sw128(i, 4 * half + 2 * x), w[0], w[1], w[2], w[3]);
+        st_shared_v4(to + sw128(i, 4 * half + 2 * x + 1), w[4], w[5], w[6], w[7]);
       }
-    }
-    __syncthreads();
-    if (first) {
+      const float f_row = sign * gt[GT_F + i], e_row = gt[GT_E + i] * gt[GT_B + i];
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
         uint32_t d[32];
-        tm_ld16(lanes + GT_X2 + 48 * half + 16 * x, d);
+        tm_ld16(lanes + 64 + 48 * half + 16 * x, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[8 * x + e] = fmul2(both(f_row), make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+      }
+      if (!first) {
+        float2 with = both(0.f), less = both(0.f);  // k . (-e^G dR S0^T), k . (E U dS1^T)
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          uint32_t d[32];
+          tm_ld16(lanes + GT_DS + 48 * half + 16 * x, d);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint4 k4 = piece(sb + GSmem::K, 2 * x + c);
+            const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 k = widen2(kw[e]);
+              const float2 y = fmul2(both(e_row), make_float2(__uint_as_float(d[8 * c + 2 * e]), __uint_as_float(d[8 * c + 2 * e + 1])));
+              float2& z = acc[8 * x + 4 * c + e];
+              with = fmadd2(k, z, with);
+              less = fmadd2(k, y, less);
+              z = fadd2(z, y);
+            }
+          }
+        }
+        at_end = live ? less.x + less.y : 0.f;
+        dg = (with.x + with.y) - (less.x + less.y);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(&bar[GB_EF]);
+      ok = __all_sync(0xffffffffu, wait(GB_TWO, 0));
+    }
+    if (ok) {
+      tc_fence_after();
+      float2 with = both(0.f), less = both(0.f);
+      __nv_bfloat16* const dst = (__nv_bfloat16*)(first ? a.dq : a.dk) + ((ch.t0 + i) * a.H + h) * DK + 48 * half;
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        uint32_t d[32], y[32];
+        tm_ld16(lanes + 48 * half + 16 * x, d);
+        if (!first) tm_ld16(lanes + GT_X2 + 48 * half + 16 * x, y);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint4 k4 = piece(sb + GSmem::K, 2 * x + c);
-          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+          const uint4 r4 = piece(first ? sb + GSmem::Q : sb + GSmem::K, 2 * x + c);
+          const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int at = 16 * x + 8 * c + 2 * e;
-            const float2 k = widen2(kw[e]);
-            const float y0 = dks[at] + __uint_as_float(d[8 * c + 2 * e]), y1 = dks[at + 1] + __uint_as_float(d[8 * c + 2 * e + 1]);
-            dg = fmaf(-k.x, y0, fmaf(-k.y, y1, dg));
-            w[e] = bf2(y0 + part[at], y1 + part[at + 1]);
+            const int at = 8 * c + 2 * e;
+            const float2 r = widen2(rw[e]), u = make_float2(__uint_as_float(d[at]), __uint_as_float(d[at + 1]));
+            float2 z = fadd2(acc[8 * x + 4 * c + e], u);
+            if (first) {
+              with = fmadd2(r, z, with);
+            } else {
+              const float2 v = make_float2(__uint_as_float(y[at]), __uint_as_float(y[at + 1]));
+              with = fmadd2(r, u, with);
+              less = fmadd2(r, v, less);
+              z = fadd2(z, v);
+            }
+            w[e] = bf2(z.x, z.y);
           }
-          if (live)
-            reinterpret_cast<uint4*>((__nv_bfloat16*)a.dk + ((ch.t0 + i) * a.H + h) * DK + 48 * half)[2 * x + c] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (live) reinterpret_cast<uint4*>(dst)[2 * x + c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-    }
-    dgp[(first ? 0 : 128) + 64 * half + i] = live ? dg : 0.f;
-    at_end = fmaf(gt[GT_F + DC - 1], frob, at_end);
+      dg += (with.x + with.y) - (less.x + less.y);
+      dgp[(first ? 0 : 128) + 64 * half + i] = live ? dg : 0.f;
+      at_end = fmaf(gt[GT_F + DC - 1], frob, at_end);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) at_end += __shfl_xor_sync(0xffffffffu, at_end, off);
-    if (lane == 0) red[warp] = at_end;
-  } else if (tid == 0) {
-    raise_error(a.err, ERR_TIMEOUT);
-    // the copies and products that were issued end before their memory is given up
-    umma_commit(&bar[GB_DRAIN]);
-    mbar_wait_drain(&bar[GB_DRAIN], 0, DRAIN_NS, a.err);
-    mbar_wait_drain(&bar[GB_IN], (panels - 1) & 1, DRAIN_NS, a.err);
-    mbar_wait_drain(&bar[GB_KQ], 0, DRAIN_NS, a.err);
+      for (int off = 16; off > 0; off >>= 1) at_end += __shfl_xor_sync(0xffffffffu, at_end, off);
+      if (lane == 0) red[warp] = at_end;
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 8) {
     tc_fence_after();
     tm_free<256>(tmem);
   }
-  if (gone) return;
+  if (*abort_flag) {
+    if (tid == 0) raise_error(a.err, ERR_TIMEOUT);
+    return;
+  }
   if (warp == 0) {  // dg_t: what hangs on G_i, i >= t, and on the chunk's end
     float end = 0.f;
 #pragma unroll
