@@ -165,6 +165,8 @@ struct DeltaMaps {
   CUtensorMap k0, k1, q0, q1, v, o;
   CUtensorMap dO, dv, x, s0, ds;
   CUtensorMap dvo, xo;  // (to write: 32 rows x 32 columns, one a warp)
+  CUtensorMap xsd;      // X, S0 and dS1: 256 rows x 64 columns
+  CUtensorMap dqo, dko; // (to write: 32 rows x 48 columns)
 };
 __device__ __forceinline__ void load_kq(const DeltaMaps& m, uint32_t p0, uint32_t p1, uint64_t* bar, int h, int t) {
   mbar_expect_tx(bar, 24576);
@@ -182,10 +184,10 @@ constexpr uint32_t W_KD = 0, W_PH = 24576, W_OP = 32768, W_GT = W_OP;
 constexpr uint32_t W_FWD = W_GT + 512;
 enum { GT_F = 0, GT_B = DC, GT_E = 2 * DC, GT_SUM = 3 * DC };  // in floats
 // Backward: K~ = -(diag(e^G) K)^T (1 + B M^T)^-1 and Q~ = s (diag(e^G) Q)^T, hi and lo, P hi and lo; then what the
-// scans leave for the gradients, bf16 rows of 192: S0 and dS1 (96), X (64).
-constexpr uint32_t W_KR = W_GT + 1280, W_QT = W_KR + 24576, W_P = W_QT + 24576, W_S0 = W_P + 16384, W_DS = W_S0 + DK * DV * 2,
-                   W_X = W_DS + DK * DV * 2, W_BWD = W_X + DC * DV * 2;
-static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_S0 % 32 == 0, "copies and tensor maps");
+// scans leave for the gradients, bf16 rows of 192: X (64), S0 and dS1 (96), one 256-row tile.
+constexpr uint32_t W_KR = W_GT + 1280, W_QT = W_KR + 24576, W_P = W_QT + 24576, W_X = W_P + 16384, W_S0 = W_X + DC * DV * 2,
+                   W_DS = W_S0 + DK * DV * 2, W_BWD = W_DS + DK * DV * 2;
+static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_X % 32 == 0, "copies and tensor maps");
 
 // ---- prep -------------------------------------------------------------------------------------
 // One CTA of 4 warps a (chunk, head), all products on mma.sync (m16n8k16): the blocks are 16 wide and each step
@@ -732,7 +734,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           if (!(ok = wait(SB_O, c))) break;
           load_ph(c + 1);
         }
-        for (int x = 0; x < 4; ++x) mbar_wait_drain(&bar[SB_KQ + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
+        // what was issued ends before its memory is given up (else everything has been waited for)
+        for (int x = 0; x < 4 && !ok; ++x) mbar_wait_drain(&bar[SB_KQ + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
       }
       __syncwarp();
     } else if (warp == 8) {
@@ -763,9 +766,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           for (int kk = 0; kk < 4; ++kk) umma(at_a, dp + kk * 32u, db + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
           umma_commit(&bar[SB_O]);
         }
-        // what was issued ends before its memory is given up
-        umma_commit(&bar[SB_DRAIN]);
-        mbar_wait_drain(&bar[SB_DRAIN], 0, DRAIN_NS, a.err);
+        if (!ok) {
+          umma_commit(&bar[SB_DRAIN]);
+          mbar_wait_drain(&bar[SB_DRAIN], 0, DRAIN_NS, a.err);
+        }
         stores_read();
       }
       __syncwarp();
@@ -1038,10 +1042,12 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           ok = ok && wait(RB_ZF + (it & 1), it >> 1);
           if (ok && it + 2 < nc) load_x(xs++);
         }
-        for (int x = 0; x < 4; ++x)
-          if (loads[x]) mbar_wait_drain(&bar[RB_EF + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
-        for (int it = max(0, loads[2] - 2); it < loads[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
-        for (int it = max(0, xs - 2); it < xs; ++it) mbar_wait_drain(&bar[RB_X + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
+        if (!ok) {  // what was issued ends before its memory is given up (else everything has been waited for)
+          for (int x = 0; x < 4; ++x)
+            if (loads[x]) mbar_wait_drain(&bar[RB_EF + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
+          for (int it = max(0, loads[2] - 2); it < loads[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
+          for (int it = max(0, xs - 2); it < xs; ++it) mbar_wait_drain(&bar[RB_X + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
+        }
       }
       __syncwarp();
     } else if (warp == 8) {
@@ -1107,8 +1113,10 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           umma_commit(&bar[RB_Z]);
           if (it + 1 < nc) ok = early(it + 1);
         }
-        umma_commit(&bar[RB_DRAIN]);
-        mbar_wait_drain(&bar[RB_DRAIN], 0, DRAIN_NS, a.err);
+        if (!ok) {
+          umma_commit(&bar[RB_DRAIN]);
+          mbar_wait_drain(&bar[RB_DRAIN], 0, DRAIN_NS, a.err);
+        }
         stores_read();
       }
       __syncwarp();
@@ -1259,10 +1267,11 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 constexpr int GRAD_THREADS = 288;
 struct GSmem {
   // a panel: [dO; dR], [X; S0], dS1; later Es and Fm in the first place, K and Q (two tiles of 64 columns each) in the second.
-  // (Products of 128 rows read before X, Es and Fm what is as still as they are.)
-  static constexpr uint32_t DOR = 0, XS = 16384, DS = XS + 20480, PANEL = DS + 12288, K = PANEL, Q = K + 16384, EF = 8192;
+  // (Products of 128 rows read before X, Es and Fm what is as still as they are.)  dq and dk leave from behind Es and Fm.
+  static constexpr uint32_t DOR = 0, XS = 16384, DS = XS + 20480, PANEL = DS + 12288, K = PANEL, Q = K + 16384, EF = 8192, OUT = EF + 16384;
   static constexpr uint32_t GT = 2 * PANEL, CF = GT + 1280, DG = CF + 128, RED = DG + 4 * DC * 4, BAR = RED + 32, BYTES = BAR + 112;
   static_assert(BYTES <= 115712, "two CTAs an SM");
+  static_assert(OUT + 8 * 32 * 96 <= PANEL, "8 warps' rows");
 };
 // Copies, the panels read by the threads, products.  (One phase of each, but for the first place's two panels.)
 enum { GB_KQ = 0, GB_IN, GB_FR = GB_IN + 2, GB_MMA = GB_FR + 2, GB_ONE = GB_MMA + 2, GB_EF, GB_TWO, GB_DRAIN, GB_N };
@@ -1296,8 +1305,6 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       fence_async_smem();
     }
-  } else if (tid < 80) {
-    reinterpret_cast<uint4*>(sm + GSmem::GT)[tid] = reinterpret_cast<const uint4*>(ws + W_GT)[tid];
   }
   tc_fence_before();
   __syncthreads();
@@ -1314,12 +1321,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
         ++panels;
         const uint32_t to = sb + (p & 1) * GSmem::PANEL;
         uint64_t* const in = &bar[GB_IN + (p & 1)];
-        mbar_expect_tx(in, GSmem::PANEL);
+        mbar_expect_tx(in, GSmem::PANEL + (p == 0 ? 1280 : 0));
         box_load(to + GSmem::DOR, &maps.dO, in, 64 * p, h, t);
         box_load(to + GSmem::DOR + 8192, &maps.dv, in, 64 * p, h, t);
-        box_load(to + GSmem::XS, &maps.x, in, 64 * p, 0, idx);
-        box_load(to + GSmem::XS + 8192, &maps.s0, in, 64 * p, 0, idx);
-        box_load(to + GSmem::DS, &maps.ds, in, 64 * p, 0, idx);
+        box_load(to + GSmem::XS, &maps.xsd, in, 64 * p, 0, idx);
+        if (p == 0) bulk_load(sb + GSmem::GT, ws + W_GT, 1280, in);
       };
       auto products = [&](int p) {
         const uint32_t at = sb + (p & 1) * GSmem::PANEL;
@@ -1337,7 +1343,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
       // what comes later, into L2
       box_prefetch(&maps.dO, 128, h, t);
       box_prefetch(&maps.dv, 128, h, t);
-      bulk_prefetch(ws + W_S0, W_BWD - W_S0);
+      bulk_prefetch(ws + W_X, W_BWD - W_X);
       for (int p = 0; p < 2; ++p) {
         box_prefetch(&maps.k0, 64 * p, h, t);
         box_prefetch(&maps.q0, 64 * p, h, t);
@@ -1345,10 +1351,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
       do {
         if (!(ok = wait(GB_IN, 0))) break;
         products(0);
-        if (!(ok = wait(GB_IN + 1, 0))) break;
-        products(1);
         if (!(ok = wait(GB_MMA, 0) && wait(GB_FR, 0))) break;
         load_panel(2);
+        if (!(ok = wait(GB_IN + 1, 0))) break;
+        products(1);
         if (!(ok = wait(GB_MMA + 1, 0) && wait(GB_FR + 1, 0))) break;
         ++kqs;
         mbar_expect_tx(&bar[GB_KQ], 4 * 8192);
@@ -1370,23 +1376,24 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
         for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + 8192u + kk * 2048u, dk + kk * 2048u, idesc_bf16(128, 96, 1, 1), 1);
         umma_commit(&bar[GB_TWO]);
       } while (false);
-      // what was issued ends before its memory is given up
-      umma_commit(&bar[GB_DRAIN]);
-      mbar_wait_drain(&bar[GB_DRAIN], 0, DRAIN_NS, a.err);
-      for (int p = max(0, panels - 2); p < panels; ++p) mbar_wait_drain(&bar[GB_IN + (p & 1)], p >> 1, DRAIN_NS, a.err);
-      if (kqs) mbar_wait_drain(&bar[GB_KQ], 0, DRAIN_NS, a.err);
+      if (!ok) {  // what was issued ends before its memory is given up (else everything has been waited for)
+        umma_commit(&bar[GB_DRAIN]);
+        mbar_wait_drain(&bar[GB_DRAIN], 0, DRAIN_NS, a.err);
+        for (int p = max(0, panels - 2); p < panels; ++p) mbar_wait_drain(&bar[GB_IN + (p & 1)], p >> 1, DRAIN_NS, a.err);
+        if (kqs) mbar_wait_drain(&bar[GB_KQ], 0, DRAIN_NS, a.err);
+      }
     }
     __syncwarp();
   } else {
-    if (tid < 32) {  // decay and strength of tokens 0-31 in those of 32-63: from there to token 31
-      const float2 x = sums[31], y = sums[tid];
-      cf[tid] = exp2_fast((x.x - y.x) + (x.y - y.y)) * gt[GT_B + tid];
-    }
     float frob = 0.f;  // <dS1, S0>, this thread's part
     for (int p = 0; p < 3 && ok; ++p) {
       const uint32_t at = sb + (p & 1) * GSmem::PANEL;
       ok = __all_sync(0xffffffffu, wait(GB_IN + (p & 1), p >> 1));
       if (!ok) break;
+      if (p == 0 && tid < 32) {  // decay and strength of tokens 0-31 in those of 32-63: from there to token 31
+        const float2 x = sums[31], y = sums[tid];
+        cf[tid] = exp2_fast((x.x - y.x) + (x.y - y.y)) * gt[GT_B + tid];
+      }
 #pragma unroll
       for (int e = tid; e < DK * 8; e += 256) {  // (768 pieces of 16 bytes; the two tiles are swizzled alike)
         const uint4 x = ld_shared_v4(at + GSmem::XS + 8192 + 16 * e), y = ld_shared_v4(at + GSmem::DS + 16 * e);
@@ -1496,7 +1503,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
     if (ok) {
       tc_fence_after();
       float2 with = both(0.f), less = both(0.f);
-      __nv_bfloat16* const dst = (__nv_bfloat16*)(first ? a.dq : a.dk) + ((ch.t0 + i) * a.H + h) * DK + 48 * half;
+      const uint32_t stage = sb + GSmem::OUT + 3072u * warp;  // 32 rows x 48 columns
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
         uint32_t d[32], y[32];
@@ -1522,15 +1529,27 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
             }
             w[e] = bf2(z.x, z.y);
           }
-          if (live) reinterpret_cast<uint4*>(dst)[2 * x + c] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (ch.len == DC)
+            st_shared_v4(stage + 96 * lane + 16 * (2 * x + c), w[0], w[1], w[2], w[3]);
+          else if (live)  // a sequence's last rows: no box is written past them
+            reinterpret_cast<uint4*>((__nv_bfloat16*)(first ? a.dq : a.dk) + ((ch.t0 + i) * a.H + h) * DK + 48 * half)[2 * x + c] =
+                make_uint4(w[0], w[1], w[2], w[3]);
         }
+      }
+      if (ch.len == DC) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) box_store(first ? &maps.dqo : &maps.dko, stage, 48 * half, h, (int)ch.t0 + 32 * (q & 1));
       }
       dg += (with.x + with.y) - (less.x + less.y);
       dgp[(first ? 0 : 128) + 64 * half + i] = live ? dg : 0.f;
       at_end = fmaf(gt[GT_F + DC - 1], frob, at_end);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) at_end += __shfl_xor_sync(0xffffffffu, at_end, off);
-      if (lane == 0) red[warp] = at_end;
+      if (lane == 0) {
+        red[warp] = at_end;
+        stores_read();
+      }
     }
   }
   tc_fence_before();
@@ -1585,8 +1604,8 @@ static F driver_fn(const char* name) {
   const bool found = cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess;
   return found ? reinterpret_cast<F>(p) : nullptr;
 }
-// bf16 [d2][d1][d0], strides in bytes, in boxes of `cols` (64: 128-byte swizzle, 32: 64-byte) x r1 x r2.  Encoding a map
-// takes the host a microsecond, and a call has up to 13: each thread keeps the last ones that it encoded, by their shape, and
+// bf16 [d2][d1][d0], strides in bytes, in boxes of `cols` (64: 128-byte swizzle, 32: 64-byte, 48: none) x r1 x r2.  Encoding a map
+// takes the host a microsecond, and a call has up to 16: each thread keeps the last ones that it encoded, by their shape, and
 // gives them the call's address.
 static bool map3(CUtensorMap* m, const void* base, long long d0, long long d1, long long d2, long long s1, long long s2, int cols,
                  int r1, int r2) {
@@ -1609,7 +1628,7 @@ static bool map3(CUtensorMap* m, const void* base, long long d0, long long d1, l
   const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2}, strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
   const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)r1, (cuuint32_t)r2}, step[3] = {1, 1, 1};
   if (encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
   Kept& k = kept[next++ % KEPT];
@@ -1678,7 +1697,8 @@ cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t st) {
     if (!(input_maps(m, a) && rows_map(&m.dO, a.dO, DV, a, 64, DC) && rows_map(&m.dv, a.dv, DV, a, 64, DC) &&
           map3(&m.x, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 64, DC, 1) && map3(&m.s0, a.ws + W_S0, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) &&
           map3(&m.ds, a.ws + W_DS, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) && map3(&m.xo, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 32, 32, 1) &&
-          rows_map(&m.dvo, a.dv, DV, a, 32, 32)))
+          rows_map(&m.dvo, a.dv, DV, a, 32, 32) && map3(&m.xsd, a.ws + W_X, DV, 256, all, 2 * DV, W_BWD, 64, 256, 1) &&
+          rows_map(&m.dqo, a.dq, DK, a, 48, 32) && rows_map(&m.dko, a.dk, DK, a, 48, 32)))
       return cudaErrorInvalidValue;
     delta_prep_kernel<true><<<chunks, PREP_THREADS, PrepSmem::bytes(true), st>>>(m, a);
     delta_scan_kernel<true><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a, sm_count());
