@@ -133,6 +133,43 @@ def test_backward_equal_lengths_and_no_states(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_sequences_and_heads(dtype):
+    """More (sequence, head)s than the GPU runs at a time, of several chunks and a ragged last one."""
+    b = Batch(21, [200] * 4, 40, dtype, packed=False)
+    o, hT = gla.gla_delta_fwd(*b.inputs(), h0=b.h0.cuda())
+    check_fwd(b, o, hT, b.h0)
+    grads = gla.gla_delta_bwd(*b.inputs(), *b.dev("dO"), h0=b.h0.cuda(), dhT=b.dhT.cuda())
+    check_bwd(b, grads, b.h0, b.dhT)
+
+
+@pytest.mark.parametrize("N,T,H", [(13, 200, 16), (51, 65, 1), (1, 700, 103), (5, 128, 32), (40, 300, 16), (304, 70, 1)])
+def test_equal_lengths_as_packed(N, T, H):
+    """The same bits from a call of equal lengths and from a packed one of those sequences."""
+    b = Batch(22, [T] * N, H, BF, packed=False)
+    x, dO, h0, dhT = b.inputs(), b.dev("dO")[0], b.h0.cuda(), b.dhT.cuda()
+    cu = i32(range(0, N * T + 1, T))
+    flat = [t.reshape(N * T, *t.shape[2:]) for t in (*x, dO)]
+    for _ in range(3):
+        o, hT = gla.gla_delta_fwd(*x, h0=h0)
+        o2, hT2 = gla.gla_delta_fwd(*flat[:5], h0=h0, cu_seqlens=cu)
+        assert torch.equal(o.reshape(o2.shape), o2) and torch.equal(hT, hT2)
+    grads = gla.gla_delta_bwd(*x, dO, h0=h0, dhT=dhT)
+    for a, c in zip(grads, gla.gla_delta_bwd(*flat, h0=h0, dhT=dhT, cu_seqlens=cu)):
+        assert torch.equal(a.reshape(c.shape), c)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_packed_sequences(dtype):
+    """Offsets of thousands of sequences: places of chunks, the order of the scans, empty sequences among them."""
+    lens = [(7 * i) % 5 for i in range(1100)] + [130, 0, 64, 1] + [i % 3 for i in range(1500)]
+    b = Batch(23, lens, 1, dtype)
+    o, hT = gla.gla_delta_fwd(*b.inputs(), h0=b.h0.cuda(), cu_seqlens=b.cu_dev)
+    check_fwd(b, o, hT, b.h0)
+    grads = gla.gla_delta_bwd(*b.inputs(), *b.dev("dO"), h0=b.h0.cuda(), dhT=b.dhT.cuda(), cu_seqlens=b.cu_dev)
+    check_bwd(b, grads, b.h0, b.dhT)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_backward_without_tokens(dtype):
     x = [torch.empty(2, 0, 1, d, dtype=dtype, device="cuda") for d in (DK, DK, DV)]
     g = torch.empty(2, 0, 1, dtype=dtype, device="cuda")
