@@ -432,8 +432,8 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
                    void* dk, void* dv, float* dpool, const int32_t* cu_seqlens, int n_seq, int T, int H, int dk_size,
                    int dv_size, int dtype, void* workspace, size_t ws_bytes, gla_stream_t stream);
 
-/* The gated delta rule (no counterpart in the paper; the recurrence of Gated DeltaNet layers).  Per head the same
- * 96 x 192 state, with a decay and a writing strength of every token's own, both learned:
+/* The gated delta rule (no counterpart in the paper).  Per head the same 96 x 192 state, with a decay and a writing
+ * strength of every token's own, both learned:
  *     S_t = a_t S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - a_t S_{t-1}^T k_t),   a_t = exp(g_t),
  *     o_t = S_t^T (scale q_t):
  * what the decayed state holds under the key is replaced, by the share beta_t, with the value.
@@ -445,6 +445,10 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
  * handled in chunks of 64; an infinity or a NaN in a token reaches every output of its chunk and what follows it in
  * its sequence, and nothing of another sequence.  cu_seqlens is checked on the device: offsets that decrease or pass
  * T are clamped and record GLA_ERR_SHAPE.
+ * bf16 calls hold what carries a state from chunk to chunk in fp32 and in pairs of bf16 (16 bits: hT and dh0 are 3 to
+ * 5e-6 of the norm from the exact ones); what only feeds an output of dtype bf16 may be rounded to bf16 once more.
+ * Sizes: chunk places (n_seq * ceil(T / 64); packed T_total / 64 + n_seq) * H * 96, and rows of h0
+ * and hT * H * 96, below 2^31, else GLA_ERR_SHAPE.
  * Calls may be captured into a graph after a first call of the same kind on the device; calls that may overlap need
  * workspaces of their own. */
 

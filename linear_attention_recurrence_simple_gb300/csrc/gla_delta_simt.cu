@@ -8,8 +8,9 @@
 //   grads   one CTA a (chunk, head): dq, dk, dg, and dbeta's parts summed in tile order
 // The operands of a product stand in shared memory with the summed index contiguous (where both ways are needed,
 // twice), so that a thread reads four of its steps at once: rows of 4 mod 32 words apart, free of bank conflicts.
-// Every thread has a small tile of the result in registers.  Few CTAs on short calls: bound by latency, so a chunk's
-// loads go out together, in vectors.
+// Every thread has a small tile of the result in registers.  A chunk's loads go out together, in vectors, while the chunk
+// before it is computed (2 x 130 tokens x 4 heads: scan 26 -> 25 us, rscan 44 -> 42, 14 us a chunk).  Bound by the reads
+// from shared memory (a 4 x 2 tile takes six vectors for 32 FMAs), short calls also by their few CTAs.
 #include "gla_delta.cuh"
 #include "gla_once.cuh"
 
@@ -31,22 +32,29 @@ template <bool BWD>
 __device__ __forceinline__ float* ws_of(const DeltaArgs& a, int slot, int h) {
   return reinterpret_cast<float*>(a.ws) + ((long long)slot * a.H + h) * (BWD ? WS_BWD : WS_FWD);
 }
-// N vectors of four, this thread's x-th being vector tid + x * THREADS of the source: loaded together, then placed.
-template <int N, class G, class P>
-__device__ __forceinline__ void copy4(G get, P put) {
-  constexpr int PER = (N + THREADS - 1) / THREADS;
+// N vectors of four, this thread's x-th being vector tid + x * THREADS of the source: loaded together, then placed, with
+// other work between the two where there is some.
+template <int N>
+struct Held {
+  static constexpr int PER = (N + THREADS - 1) / THREADS;
   float4 v[PER];
+  template <class G>
+  __device__ __forceinline__ void fetch(G get) {
 #pragma unroll
-  for (int x = 0; x < PER; ++x) {
-    const int e = threadIdx.x + x * THREADS;
-    v[x] = N % THREADS == 0 || e < N ? get(e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < PER; ++x) {
+      const int e = threadIdx.x + x * THREADS;
+      v[x] = N % THREADS == 0 || e < N ? get(e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
+  template <class P>
+  __device__ __forceinline__ void place(P put) const {
 #pragma unroll
-  for (int x = 0; x < PER; ++x) {
-    const int e = threadIdx.x + x * THREADS;
-    if (N % THREADS == 0 || e < N) put(e, v[x]);
+    for (int x = 0; x < PER; ++x) {
+      const int e = threadIdx.x + x * THREADS;
+      if (N % THREADS == 0 || e < N) put(e, v[x]);
+    }
   }
-}
+};
 __device__ __forceinline__ void put_row(float* at, float4 v) { *reinterpret_cast<float4*>(at) = v; }
 template <int STRIDE>
 __device__ __forceinline__ void put_column(float* at, float4 v) {
@@ -56,20 +64,35 @@ __device__ __forceinline__ void put_column(float* at, float4 v) {
   at[3 * STRIDE] = v.w;
 }
 // Rows [0, C) of a [tokens, H, D] tensor, columns [c0, c0 + W), zeros from row `len` on.
-template <int W, class P>
-__device__ __forceinline__ void load_rows(const float* src, long long t0, int len, int H, int h, int D, int c0, P put) {
-  copy4<DC * W / 4>(
-      [&](int e) {
-        const int i = e / (W / 4), c = e % (W / 4) * 4;
-        return i < len ? *reinterpret_cast<const float4*>(src + ((t0 + i) * H + h) * D + c0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-      },
-      [&](int e, float4 v) { put(e / (W / 4), e % (W / 4) * 4, v); });
-}
+template <int W>
+struct Rows : Held<DC * W / 4> {
+  __device__ __forceinline__ void fetch(const void* src, long long t0, int len, int H, int h, int D, int c0) {
+    Held<DC * W / 4>::fetch([&](int e) {
+      const int i = e / (W / 4), c = e % (W / 4) * 4;
+      return i < len ? *reinterpret_cast<const float4*>((const float*)src + ((t0 + i) * H + h) * D + c0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    });
+  }
+  template <class P>
+  __device__ __forceinline__ void place(P put) const {
+    Held<DC * W / 4>::place([&](int e, float4 v) { put(e / (W / 4), e % (W / 4) * 4, v); });
+  }
+};
 // Rows [0, R) x W floats, row stride LD, of the workspace.
+template <int R, int W, int LD>
+struct Block : Held<R * W / 4> {
+  __device__ __forceinline__ void fetch(const float* src) {
+    Held<R * W / 4>::fetch([&](int e) { return *reinterpret_cast<const float4*>(src + e / (W / 4) * LD + e % (W / 4) * 4); });
+  }
+  template <class P>
+  __device__ __forceinline__ void place(P put) const {
+    Held<R * W / 4>::place([&](int e, float4 v) { put(e / (W / 4), e % (W / 4) * 4, v); });
+  }
+};
 template <int R, int W, int LD, class P>
-__device__ __forceinline__ void load_ws(const float* src, P put) {
-  copy4<R * W / 4>([&](int e) { return *reinterpret_cast<const float4*>(src + e / (W / 4) * LD + e % (W / 4) * 4); },
-                   [&](int e, float4 v) { put(e / (W / 4), e % (W / 4) * 4, v); });
+__device__ __forceinline__ void load_block(const float* src, P put) {
+  Block<R, W, LD> b;
+  b.fetch(src);
+  b.place(put);
 }
 // acc[r][c] += sum_k A[r * AS + k] B[c * BS + k]
 template <int NR, int NC, int K, int AS, int BS>
@@ -120,8 +143,11 @@ __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArg
     sg[2 * tid] = s0;
     sg[2 * tid + 1] = s1;
   }
-  load_rows<DK>((const float*)a.k, ch.t0, ch.len, a.H, h, DK, 0, [&](int i, int c, float4 v) { put_row(sk + i * KS + c, v); });
-  load_rows<DK>((const float*)a.q, ch.t0, ch.len, a.H, h, DK, 0, [&](int i, int c, float4 v) { put_row(sq + i * KS + c, v); });
+  Rows<DK> k, q;
+  k.fetch(a.k, ch.t0, ch.len, a.H, h, DK, 0);
+  q.fetch(a.q, ch.t0, ch.len, a.H, h, DK, 0);
+  k.place([&](int i, int c, float4 v) { put_row(sk + i * KS + c, v); });
+  q.place([&](int i, int c, float4 v) { put_row(sq + i * KS + c, v); });
   __syncthreads();
   if (tid < DC) {
     ws[WS_GT + GT_HI + tid] = sg[tid].x;
@@ -174,33 +200,53 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
   const DeltaSeq s = delta_seq(a, n);
   const int from = a.h0 ? delta_row(a.h0_row, a.h0_rows, n, a.err) : -1;
   if (from >= 0)
-    load_ws<DK, SB, DV>(a.h0 + ((long long)from * a.H + h) * (DK * DV) + c0, [&](int x, int c, float4 v) { put_column<KS>(S + c * KS + x, v); });
+    load_block<DK, SB, DV>(a.h0 + ((long long)from * a.H + h) * (DK * DV) + c0, [&](int x, int c, float4 v) { put_column<KS>(S + c * KS + x, v); });
   else
     for (int e = tid; e < SB * KS; e += THREADS) S[e] = 0.f;
   const int ti = tid / 16, tj = tid % 16;  // rows ti + 16 r, columns tj + 16 c
-  for (int c = 0; c * DC < s.len; ++c) {
+  // A chunk's inputs, fetched while the one before is computed.
+  Rows<DK> k, q;
+  Block<DC, DC, DC> z, p;
+  float v[4][2], f = 0.f;
+  auto fetch = [&](int c) {
     const int len = min(DC, s.len - c * DC);
     const long long t0 = s.begin + (long long)c * DC;
-    float* const ws = ws_of<BWD>(a, s.slot0 + c, h);
-    float v[4][2];
+    const float* const ws = ws_of<BWD>(a, s.slot0 + c, h);
+    k.fetch(a.k, t0, len, a.H, h, DK, 0);
+    if (!BWD) q.fetch(a.q, t0, len, a.H, h, DK, 0);
+    z.fetch(ws + WS_Z);
+    if (!BWD) p.fetch(ws + WS_P);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         v[i][j] = ti + 16 * i < len ? ((const float*)a.v)[((t0 + ti + 16 * i) * a.H + h) * DV + c0 + tj + 16 * j] : 0.f;
+    if (tid < 3 * DC) f = ws[WS_GT + GT_F + tid];
+  };
+  if (s.len > 0) fetch(0);
+  for (int c = 0; c * DC < s.len; ++c) {
+    const int len = min(DC, s.len - c * DC);
+    const long long t0 = s.begin + (long long)c * DC;
+    float* const ws = ws_of<BWD>(a, s.slot0 + c, h);
     __syncthreads();
-    if (tid < 3 * DC) sf[tid] = ws[WS_GT + GT_F + tid];
-    load_rows<DK>((const float*)a.k, t0, len, a.H, h, DK, 0, [&](int i, int x, float4 y) {
+    if (tid < 3 * DC) sf[tid] = f;
+    k.place([&](int i, int x, float4 y) {
       put_row(sk + i * KS + x, y);
       put_column<CS>(st + x * CS + i, y);
     });
-    if (!BWD) load_rows<DK>((const float*)a.q, t0, len, a.H, h, DK, 0, [&](int i, int x, float4 y) { put_row(sq + i * KS + x, y); });
-    load_ws<DC, DC, DC>(ws + WS_Z, [&](int i, int j, float4 y) { put_row(sz + i * CS + j, y); });
-    if (!BWD) load_ws<DC, DC, DC>(ws + WS_P, [&](int i, int j, float4 y) { put_row(sp + i * CS + j, y); });
+    if (!BWD) q.place([&](int i, int x, float4 y) { put_row(sq + i * KS + x, y); });
+    z.place([&](int i, int j, float4 y) { put_row(sz + i * CS + j, y); });
+    if (!BWD) p.place([&](int i, int j, float4 y) { put_row(sp + i * CS + j, y); });
+    float r[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) r[i][j] = v[i][j];
     __syncthreads();
+    if ((c + 1) * DC < s.len) fetch(c + 1);
     if (BWD)
       for (int e = tid; e < DK * SB; e += THREADS) ws[WS_S0 + e / SB * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
-    float ks[4][2] = {}, qs[4][2] = {}, r[4][2];
+    float ks[4][2] = {}, qs[4][2] = {};
     gemm<4, 2, DK, K16, K16>(ks, sk + ti * KS, S + tj * KS);
     if (!BWD) gemm<4, 2, DK, K16, K16>(qs, sq + ti * KS, S + tj * KS);
 #pragma unroll
@@ -208,7 +254,7 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = ti + 16 * i;
-        r[i][j] = fmaf(-sf[row], ks[i][j], v[i][j]);
+        r[i][j] = fmaf(-sf[row], ks[i][j], r[i][j]);
         sr[(tj + 16 * j) * CS + row] = sf[2 * DC + row] * r[i][j];
       }
     __syncthreads();
@@ -279,30 +325,53 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
   const DeltaSeq s = delta_seq(a, n);
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
   if (a.dhT)
-    load_ws<DK, SB, DV>(a.dhT + ((long long)n * a.H + h) * (DK * DV) + c0, [&](int x, int c, float4 v) { put_column<KS>(S + c * KS + x, v); });
+    load_block<DK, SB, DV>(a.dhT + ((long long)n * a.H + h) * (DK * DV) + c0, [&](int x, int c, float4 v) { put_column<KS>(S + c * KS + x, v); });
   else
     for (int e = tid; e < SB * KS; e += THREADS) S[e] = 0.f;
   const int ti = tid / 16, tj = tid % 16;
-  for (int c = (s.len + DC - 1) / DC - 1; c >= 0; --c) {
+  // A chunk's inputs, fetched while the one before is computed.
+  Rows<DK> k, q;
+  Rows<SB> d;
+  Block<DC, DC, DC> z, p;
+  float xs[4][2], f = 0.f;
+  auto fetch = [&](int c) {
+    const int len = min(DC, s.len - c * DC);
+    const long long t0 = s.begin + (long long)c * DC;
+    const float* const ws = ws_of<true>(a, s.slot0 + c, h);
+    k.fetch(a.k, t0, len, a.H, h, DK, 0);
+    q.fetch(a.q, t0, len, a.H, h, DK, 0);
+    d.fetch(a.dO, t0, len, a.H, h, DV, c0);
+    z.fetch(ws + WS_Z);
+    p.fetch(ws + WS_P);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) xs[i][j] = ws[WS_X + (ti + 16 * i) * DV + c0 + tj + 16 * j];
+    if (tid < 3 * DC) f = ws[WS_GT + GT_F + tid];
+  };
+  const int nc = (s.len + DC - 1) / DC;
+  if (nc > 0) fetch(nc - 1);
+  for (int c = nc - 1; c >= 0; --c) {
     const int len = min(DC, s.len - c * DC);
     const long long t0 = s.begin + (long long)c * DC;
     float* const ws = ws_of<true>(a, s.slot0 + c, h);
+    __syncthreads();
+    if (tid < 3 * DC) sf[tid] = f;
+    k.place([&](int i, int e, float4 y) {
+      put_row(sk + i * KS + e, y);
+      put_column<CS>(skt + e * CS + i, y);
+    });
+    q.place([&](int i, int e, float4 y) { put_column<CS>(sqt + e * CS + i, y); });
+    d.place([&](int i, int e, float4 y) { put_column<CS>(sd + e * CS + i, y); });
+    z.place([&](int i, int j, float4 y) { put_column<CS>(szt + j * CS + i, y); });
+    p.place([&](int i, int j, float4 y) { put_column<CS>(spt + j * CS + i, y); });
     float x[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) x[i][j] = ws[WS_X + (ti + 16 * i) * DV + c0 + tj + 16 * j];
+      for (int j = 0; j < 2; ++j) x[i][j] = xs[i][j];
     __syncthreads();
-    if (tid < 3 * DC) sf[tid] = ws[WS_GT + GT_F + tid];
-    load_rows<DK>((const float*)a.k, t0, len, a.H, h, DK, 0, [&](int i, int e, float4 y) {
-      put_row(sk + i * KS + e, y);
-      put_column<CS>(skt + e * CS + i, y);
-    });
-    load_rows<DK>((const float*)a.q, t0, len, a.H, h, DK, 0, [&](int i, int e, float4 y) { put_column<CS>(sqt + e * CS + i, y); });
-    load_rows<SB>((const float*)a.dO, t0, len, a.H, h, DV, c0, [&](int i, int e, float4 y) { put_column<CS>(sd + e * CS + i, y); });
-    load_ws<DC, DC, DC>(ws + WS_Z, [&](int i, int j, float4 y) { put_column<CS>(szt + j * CS + i, y); });
-    load_ws<DC, DC, DC>(ws + WS_P, [&](int i, int j, float4 y) { put_column<CS>(spt + j * CS + i, y); });
-    __syncthreads();
+    if (c > 0) fetch(c - 1);
     for (int e = tid; e < DK * SB; e += THREADS) ws[WS_DS + e / SB * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
     float kd[4][2] = {}, pd[4][2] = {}, du[4][2];
     gemm<4, 2, DK, K16, K16>(kd, sk + ti * KS, S + tj * KS);
@@ -354,78 +423,114 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
 }
 
 // ---- gradients of the chunk ------------------------------------------------------------------
-// pieces of 32 columns: dO, dR, U [64][36], S0, dS1 [96][36]; then Es, Fm and their transposes [64][68] in their place, and
-// K^T, Q^T [96][68]
-constexpr int PIECES = 3 * DC * BS + 2 * DK * BS, GRAD_FLOATS = 2 * DC * KS + 2 * DK * CS + (PIECES > 4 * DC * CS ? PIECES : 4 * DC * CS) + DC;
+// A cluster of two CTAs a (chunk, head), each with 32 rows of Es and Fm, which both need whole and write to each other,
+// and with 48 columns of d_k: short calls have few chunks (2 sequences of 130 tokens, 4 heads: 68 us with one CTA, 47.5
+// with two; bound by shared memory, two vectors read for every five or six FMAs a lane).  Pieces of 32 columns
+// of d_v: dO, dR, U [64][36], S0, dS1 [48][36], the next piece's loads in flight; then Es, Fm and their transposes
+// [64][68] in their place.  K and Q [64][52], K^T and Q^T [48][68].
+constexpr int HK = DK / 2, HS = HK + 4;
+constexpr int PIECES = 3 * DC * BS + 2 * HK * BS, GRAD_FLOATS = 2 * DC * HS + 2 * HK * CS + (PIECES > 4 * DC * CS ? PIECES : 4 * DC * CS) + 2 * DC + 8;
 
-__global__ void __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaArgs a, const float* dbeta_part) {
+__device__ __forceinline__ uint32_t peer_of(const float* at, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(at)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void put_peer(uint32_t at, float v) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaArgs a, const float* dbeta_part) {
   extern __shared__ __align__(16) float sm[];
   float* const sk = sm;
-  float* const sq = sk + DC * KS;
-  float* const skt = sq + DC * KS;
-  float* const sqt = skt + DK * CS;
-  float* const sdo = sqt + DK * CS;
+  float* const sq = sk + DC * HS;
+  float* const skt = sq + DC * HS;
+  float* const sqt = skt + HK * CS;
+  float* const sdo = sqt + HK * CS;
   float* const sdr = sdo + DC * BS;
   float* const su = sdr + DC * BS;
   float* const ss = su + DC * BS;
-  float* const sd = ss + DK * BS;
-  float* const sdg = sm + GRAD_FLOATS - DC;  // [64] dG
+  float* const sd = ss + HK * BS;
+  float* const sdg = sm + GRAD_FLOATS - 2 * DC - 8;  // [2][64] dG of the two CTAs' columns; [2] what hangs on G_C
   __shared__ float red[THREADS / 32];
-  const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
+  const int unit = blockIdx.x / 2, rank = blockIdx.x % 2, slot = unit / a.H, h = unit % a.H, tid = threadIdx.x, x0 = rank * HK;
   const DeltaChunk ch = chunk_of_slot(a, slot);
-  if (ch.len == 0) return;
+  if (ch.len == 0) return;  // (both)
   const float* const ws = ws_of<true>(a, slot, h);
   const float* const gt = ws + WS_GT;
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
-  load_rows<DK>((const float*)a.k, ch.t0, ch.len, a.H, h, DK, 0, [&](int i, int c, float4 v) {
-    put_row(sk + i * KS + c, v);
+  Rows<HK> k, q;
+  Rows<SB> pdo, pdr;
+  Block<DC, SB, DV> px;
+  Block<HK, SB, DV> ps, pd;
+  auto fetch = [&](int c0) {
+    pdo.fetch(a.dO, ch.t0, ch.len, a.H, h, DV, c0);
+    pdr.fetch(a.dv, ch.t0, ch.len, a.H, h, DV, c0);
+    px.fetch(ws + WS_X + c0);
+    ps.fetch(ws + WS_S0 + x0 * DV + c0);
+    pd.fetch(ws + WS_DS + x0 * DV + c0);
+  };
+  k.fetch(a.k, ch.t0, ch.len, a.H, h, DK, x0);
+  q.fetch(a.q, ch.t0, ch.len, a.H, h, DK, x0);
+  fetch(0);
+  k.place([&](int i, int c, float4 v) {
+    put_row(sk + i * HS + c, v);
     put_column<CS>(skt + c * CS + i, v);
   });
-  load_rows<DK>((const float*)a.q, ch.t0, ch.len, a.H, h, DK, 0, [&](int i, int c, float4 v) {
-    put_row(sq + i * KS + c, v);
+  q.place([&](int i, int c, float4 v) {
+    put_row(sq + i * HS + c, v);
     put_column<CS>(sqt + c * CS + i, v);
   });
-  const int ti = tid / 16, tj = tid % 16;
-  float dp[4][4] = {}, dm[4][4] = {}, dqi[4][6] = {}, dkr[4][6] = {}, dks[4][6] = {}, frob = 0.f;
+  const int ti = tid / 16, tj = tid % 16, i0 = rank * (DC / 2) + ti;  // rows i0, i0 + 16 of Es and Fm
+  float dp[2][4] = {}, dm[2][4] = {}, dqi[4][3] = {}, dkr[4][3] = {}, dks[4][3] = {}, frob = 0.f;
   for (int c0 = 0; c0 < DV; c0 += SB) {
     __syncthreads();
-    load_rows<SB>((const float*)a.dO, ch.t0, ch.len, a.H, h, DV, c0, [&](int i, int c, float4 v) { put_row(sdo + i * BS + c, v); });
-    load_rows<SB>((const float*)a.dv, ch.t0, ch.len, a.H, h, DV, c0, [&](int i, int c, float4 v) { put_row(sdr + i * BS + c, v); });
-    load_ws<DC, SB, DV>(ws + WS_X + c0, [&](int i, int c, float4 v) {
+    pdo.place([&](int i, int c, float4 v) { put_row(sdo + i * BS + c, v); });
+    pdr.place([&](int i, int c, float4 v) { put_row(sdr + i * BS + c, v); });
+    px.place([&](int i, int c, float4 v) {
       const float b = gt[GT_B + i];
       put_row(su + i * BS + c, make_float4(b * v.x, b * v.y, b * v.z, b * v.w));
     });
-    load_ws<DK, SB, DV>(ws + WS_S0 + c0, [&](int x, int c, float4 v) { put_row(ss + x * BS + c, v); });
-    load_ws<DK, SB, DV>(ws + WS_DS + c0, [&](int x, int c, float4 v) { put_row(sd + x * BS + c, v); });
+    ps.place([&](int x, int c, float4 v) { put_row(ss + x * BS + c, v); });
+    pd.place([&](int x, int c, float4 v) { put_row(sd + x * BS + c, v); });
     __syncthreads();
-    for (int e = tid; e < DK * SB; e += THREADS) frob = fmaf(ss[e / SB * BS + e % SB], sd[e / SB * BS + e % SB], frob);
-    gemm<4, 4, SB, B16, B16>(dp, sdo + ti * BS, su + tj * BS);
-    gemm<4, 4, SB, B16, B16>(dm, sdr + ti * BS, su + tj * BS);
-    gemm<4, 6, SB, B16, B16>(dqi, sdo + ti * BS, ss + tj * BS);
-    gemm<4, 6, SB, B16, B16>(dkr, sdr + ti * BS, ss + tj * BS);
-    gemm<4, 6, SB, B16, B16>(dks, su + ti * BS, sd + tj * BS);
+    if (c0 + SB < DV) fetch(c0 + SB);
+    for (int e = tid; e < HK * SB; e += THREADS) frob = fmaf(ss[e / SB * BS + e % SB], sd[e / SB * BS + e % SB], frob);
+    gemm<2, 4, SB, B16, B16>(dp, sdo + i0 * BS, su + tj * BS);
+    gemm<2, 4, SB, B16, B16>(dm, sdr + i0 * BS, su + tj * BS);
+    gemm<4, 3, SB, B16, B16>(dqi, sdo + ti * BS, ss + tj * BS);
+    gemm<4, 3, SB, B16, B16>(dkr, sdr + ti * BS, ss + tj * BS);
+    gemm<4, 3, SB, B16, B16>(dks, su + ti * BS, sd + tj * BS);
   }
-  __syncthreads();
+  cluster_sync();  // (neither reads its pieces any more)
   float* const es = sdo;              // [64][68] Es, Fm, and their transposes
   float* const fm = es + DC * CS;
   float* const est = fm + DC * CS;
   float* const fmt = est + DC * CS;
+  const uint32_t peer = peer_of(es, rank ^ 1);
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int i = ti + 16 * r, j = tj + 16 * c;
+      const int i = i0 + 16 * r, j = tj + 16 * c;
       const float d = j <= i ? delta_decay(make_float2(gt[GT_HI + i], gt[GT_LO + i]), make_float2(gt[GT_HI + j], gt[GT_LO + j])) : 0.f;
       const float e = j <= i ? a.scale * d * dp[r][c] : 0.f, f = j < i ? -d * dm[r][c] : 0.f;
-      es[i * CS + j] = est[j * CS + i] = e;
-      fm[i * CS + j] = fmt[j * CS + i] = f;
+      const int at = i * CS + j, att = 2 * DC * CS + j * CS + i;
+      es[at] = es[att] = e;
+      fm[at] = fm[att] = f;
+      put_peer(peer + 4 * at, e);
+      put_peer(peer + 4 * att, e);
+      put_peer(peer + 4 * (DC * CS + at), f);
+      put_peer(peer + 4 * (DC * CS + att), f);
     }
-  __syncthreads();
-  float q1[4][6] = {}, k1[4][6] = {}, k2[4][6] = {};  // Es K;  Es^T Q + Fm^T K;  Fm K
-  gemm<4, 6, DC, I16, I16>(q1, es + ti * CS, skt + tj * CS);
-  gemm<4, 6, DC, I16, I16>(k1, est + ti * CS, sqt + tj * CS);
-  gemm<4, 6, DC, I16, I16>(k1, fmt + ti * CS, skt + tj * CS);
-  gemm<4, 6, DC, I16, I16>(k2, fm + ti * CS, skt + tj * CS);
+  cluster_sync();
+  float q1[4][3] = {}, k1[4][3] = {}, k2[4][3] = {};  // Es K;  Es^T Q + Fm^T K;  Fm K
+  gemm<4, 3, DC, I16, I16>(q1, es + ti * CS, skt + tj * CS);
+  gemm<4, 3, DC, I16, I16>(k1, est + ti * CS, sqt + tj * CS);
+  gemm<4, 3, DC, I16, I16>(k1, fmt + ti * CS, skt + tj * CS);
+  gemm<4, 3, DC, I16, I16>(k2, fm + ti * CS, skt + tj * CS);
+  const uint32_t first = peer_of(sdg, 0);
   float at_end = 0.f;  // sum_j k_j . (e^(G_C - G_j) dS1 u_j), this thread's part
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -433,32 +538,37 @@ __global__ void __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaAr
     const float f = gt[GT_F + i], e = gt[GT_E + i];
     float dg = 0.f;
 #pragma unroll
-    for (int c = 0; c < 6; ++c) {
+    for (int c = 0; c < 3; ++c) {
       const int x = tj + 16 * c;
-      const float q = sq[i * KS + x], k = sk[i * KS + x];
+      const float q = sq[i * HS + x], k = sk[i * HS + x];
       const float dq = fmaf(a.scale * f, dqi[r][c], q1[r][c]);
       const float minus = fmaf(e, dks[r][c], k1[r][c]), plus = fmaf(-f, dkr[r][c], k2[r][c]);
       at_end = fmaf(k, e * dks[r][c], at_end);
       dg = fmaf(q, dq, fmaf(k, plus - minus, dg));
       if (i < ch.len) {
-        ((float*)a.dq)[((ch.t0 + i) * a.H + h) * DK + x] = dq;
-        ((float*)a.dk)[((ch.t0 + i) * a.H + h) * DK + x] = minus + plus;
+        ((float*)a.dq)[((ch.t0 + i) * a.H + h) * DK + x0 + x] = dq;
+        ((float*)a.dk)[((ch.t0 + i) * a.H + h) * DK + x0 + x] = minus + plus;
       }
     }
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) dg += __shfl_xor_sync(0xffffffffu, dg, off);
-    if (tj == 0) sdg[i] = dg;
+    if (tj == 0) put_peer(first + 4 * (rank * DC + i), dg);
   }
   at_end = fmaf(gt[GT_F + DC - 1], frob, at_end);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) at_end += __shfl_xor_sync(0xffffffffu, at_end, off);
   if ((tid & 31) == 0) red[tid / 32] = at_end;
   __syncthreads();
-  if (tid < 32) {  // dg_t = the sum of dG_i over i >= t, and of what hangs on G_C
+  if (tid == 0) {
     float end = 0.f;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) end += red[w];
-    const float lo = sdg[2 * tid], hi = sdg[2 * tid + 1];
+    put_peer(first + 4 * (2 * DC + rank), end);
+  }
+  cluster_sync();  // (after it the second CTA touches only its own memory)
+  if (rank == 0 && tid < 32) {  // dg_t = the sum of dG_i over i >= t, and of what hangs on G_C
+    const float end = sdg[2 * DC] + sdg[2 * DC + 1];
+    const float lo = sdg[2 * tid] + sdg[DC + 2 * tid], hi = sdg[2 * tid + 1] + sdg[DC + 2 * tid + 1];
     float run = lo + hi;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -469,8 +579,8 @@ __global__ void __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaAr
     float* const dst = (float*)a.dg + ch.t0 * a.H + h;
     if (2 * tid < ch.len) dst[(long long)(2 * tid) * a.H] = run + end;
     if (2 * tid + 1 < ch.len) dst[(long long)(2 * tid + 1) * a.H] = behind + hi + end;
-  } else if (tid >= 64 && tid - 64 < ch.len) {
-    const long long t = ch.t0 + tid - 64;
+  } else if (rank == 1 && tid < ch.len) {
+    const long long t = ch.t0 + tid;
     float b = 0.f;
 #pragma unroll
     for (int x = 0; x < SNB; ++x) b += dbeta_part[((long long)x * tokens + t) * a.H + h];
@@ -519,7 +629,7 @@ cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t st) {
     delta_scan_simt_kernel<true><<<units, THREADS, SCAN_BYTES, st>>>(a);
   }
   delta_rscan_simt_kernel<<<units, THREADS, RSCAN_BYTES, st>>>(a, part);
-  if (a.slots > 0) delta_grads_simt_kernel<<<chunks, THREADS, GRAD_BYTES, st>>>(a, part);
+  if (a.slots > 0) delta_grads_simt_kernel<<<2 * chunks, THREADS, GRAD_BYTES, st>>>(a, part);
   return cudaGetLastError();
 }
 
