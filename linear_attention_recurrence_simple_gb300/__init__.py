@@ -1012,6 +1012,9 @@ def gla_delta_bwd_workspace_bytes(n_seq: int, T: int, H: int, packed: bool, dtyp
                                                             int(dtype_code)))
 
 
+_SCALE = DK ** -0.5
+
+
 def _delta_call(q, k, v, g, beta, cu_seqlens):
     """Checks what the chunked gated delta calls share."""
     dev = _device_of(q, "q")
@@ -1023,8 +1026,13 @@ def _delta_call(q, k, v, g, beta, cu_seqlens):
         _good(cu_seqlens, "cu_seqlens", torch.int32, dev)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [n_seq + 1]")
-    n_seq, T, H = _layout(q, k, v, cu_seqlens)
-    if g.shape != q.shape[:-1] or beta.shape != g.shape:
+    shape = q.shape
+    lead = shape[:-1]
+    if cu_seqlens is None and len(lead) == 3 and shape[3] == DK and k.shape == shape and v.shape == (*lead, DV):
+        n_seq, T, H = lead
+    else:
+        n_seq, T, H = _layout(q, k, v, cu_seqlens)
+    if g.shape != lead or beta.shape != lead:
         raise ValueError("g and beta must have the shape of q without its last dimension")
     return dev, dt, n_seq, T, H
 
@@ -1068,7 +1076,7 @@ def gla_delta_fwd(q, k, v, g, beta, scale=None, h0=None, h0_row=None, hT=None, h
         workspace = torch.empty(lib.gla_delta_workspace_bytes(n_seq, T, H, int(cu_seqlens is not None), dt),
                                 dtype=torch.uint8, device=dev)
     _run(lib.gla_delta_fwd, "gla_delta_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-         beta.data_ptr(), _addr(h0), h0_rows, _addr(h0_row), DK ** -0.5 if scale is None else float(scale), o.data_ptr(),
+         beta.data_ptr(), _addr(h0), h0_rows, _addr(h0_row), _SCALE if scale is None else float(scale), o.data_ptr(),
          _addr(hT), hT_rows, _addr(hT_row), _addr(cu_seqlens), n_seq, T, H, DK, DV, dt, workspace.data_ptr(),
          workspace.numel() * workspace.element_size())
     return o, hT
@@ -1092,7 +1100,7 @@ def gla_delta_bwd(q, k, v, g, beta, dO, scale=None, h0=None, dhT=None, cu_seqlen
         workspace = torch.empty(lib.gla_delta_bwd_workspace_bytes(n_seq, T, H, int(cu_seqlens is not None), dt),
                                 dtype=torch.uint8, device=dev)
     _run(lib.gla_delta_bwd, "gla_delta_bwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-         beta.data_ptr(), _addr(h0), DK ** -0.5 if scale is None else float(scale), dO.data_ptr(), _addr(dhT),
+         beta.data_ptr(), _addr(h0), _SCALE if scale is None else float(scale), dO.data_ptr(), _addr(dhT),
          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _addr(dh0), _addr(cu_seqlens),
          n_seq, T, H, DK, DV, dt, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dv, dg, dbeta, dh0
@@ -1108,15 +1116,17 @@ def gla_delta_decode_step(q, k, v, g, beta, state, slot=None, scale=None, o=None
     if not _like(dev.index, q.dtype, q, k, v, g, beta):
         for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
             _need(t, name, q.dtype, dev)
-    if q.dim() != 3 or q.shape[2] != DK or k.shape != q.shape or v.shape != (*q.shape[:2], DV):
+    shape = q.shape
+    N, H, dk = shape if len(shape) == 3 else (0, 0, 0)
+    if dk != DK or k.shape != shape or v.shape != (N, H, DV):
         raise ValueError("expected q, k [N, H, 96] and v [N, H, 192]")
-    N, H = q.shape[:2]
     if g.shape != (N, H) or beta.shape != (N, H):
         raise ValueError("g and beta must be [N, H]")
     if not isinstance(state, torch.Tensor) or state.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("state must be float32 or bfloat16")
     _good(state, "state", state.dtype, dev)
-    if state.dim() != 4 or state.shape[1:] != (H, DK, DV):
+    shape = state.shape
+    if len(shape) != 4 or shape != (shape[0], H, DK, DV):
         raise ValueError("state must be [P, H, 96, 192]")
     if slot is not None:
         _good(slot, "slot", torch.int32, dev)
@@ -1129,7 +1139,7 @@ def gla_delta_decode_step(q, k, v, g, beta, state, slot=None, scale=None, o=None
     fn, where = ((lib.gla_delta_decode_step_bf16_state, "gla_delta_decode_step_bf16_state")
                  if state.dtype == torch.bfloat16 else (lib.gla_delta_decode_step, "gla_delta_decode_step"))
     _run(fn, where, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-         DK ** -0.5 if scale is None else float(scale), state.data_ptr(), _addr(slot), state.shape[0], o.data_ptr(),
+         _SCALE if scale is None else float(scale), state.data_ptr(), _addr(slot), shape[0], o.data_ptr(),
          N, H, DK, DV, dt)
     return o
 
@@ -1156,22 +1166,28 @@ def gla_slot_plan(new_len, held, seen, pool_rows: int, budget: int, out=None):
     lib = _libs.get(_use_debug) or load_library()
     dev = _device_of(new_len, "new_len")
     N, budget = new_len.numel(), int(budget)
-    for name, t in (("new_len", new_len), ("held", held), ("seen", seen)):
-        if t is not None or name != "seen":
-            _good(t, name, torch.int32, dev)
-            if t.shape != (N,):
-                raise ValueError(f"{name} must be [N]")
+    maps = (new_len, held) if seen is None else (new_len, held, seen)
+    if not _like(dev.index, torch.int32, *maps):
+        for name, t in zip(("new_len", "held", "seen"), maps):
+            _need(t, name, torch.int32, dev)
+    for t in maps:
+        if t.shape != (N,):
+            raise ValueError("new_len, held and seen must be [N]")
     if budget < 0:
         raise ValueError("budget must not be negative")
     sizes = (N + 1, N, N, N, budget, budget)
-    if out is None:
-        out = SlotPlan(*torch.empty(3 * N + N + 1 + 2 * budget, dtype=torch.int32, device=dev).split_with_sizes(sizes))
+    if out is None:  # (the views are made while the kernel runs)
+        flat = torch.empty(4 * N + 1 + 2 * budget, dtype=torch.int32, device=dev)
+        at = flat.data_ptr() + 4 * N + 4
+        end = at + 12 * N
+        places = flat.data_ptr(), at, at + 4 * N, at + 8 * N, end, end + 4 * budget
     else:
         for name, t, size in zip(SlotPlan._fields, out, sizes):
             _good(t, "out." + name, torch.int32, dev, size)
+        places = [t.data_ptr() for t in out]
     _run(lib.gla_slot_plan, "gla_slot_plan", dev, new_len.data_ptr(), held.data_ptr(), _addr(seen), N, int(pool_rows),
-         budget, *(t.data_ptr() for t in out))
-    return out
+         budget, *places)
+    return SlotPlan(*flat.split_with_sizes(sizes)) if out is None else out
 
 
 def gla_get_device_error(device=None) -> int:
