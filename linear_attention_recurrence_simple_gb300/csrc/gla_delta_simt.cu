@@ -185,6 +185,7 @@ constexpr int SCAN_FLOATS = SB * KS + 2 * DC * KS + DK * CS + 2 * DC * CS + 2 * 
 
 template <bool BWD>
 __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArgs a) {
+  wait_for_previous();
   extern __shared__ __align__(16) float sm[];
   float* const S = sm;                 // [32][100]: columns of the state
   float* const sk = S + SB * KS;       // [64][100]
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
 constexpr int RSCAN_FLOATS = SB * KS + DC * KS + 2 * DK * CS + 2 * DC * CS + 3 * SB * CS + 3 * DC;
 
 __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaArgs a, float* dbeta_part) {
+  wait_for_previous();
   extern __shared__ __align__(16) float sm[];
   float* const S = sm;              // [32][100]: columns of dS
   float* const sk = S + SB * KS;    // [64][100]
@@ -442,6 +444,7 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void put_peer(uint32_t at, float v) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads_simt_kernel(const DeltaArgs a, const float* dbeta_part) {
+  wait_for_previous();
   extern __shared__ __align__(16) float sm[];
   float* const sk = sm;
   float* const sq = sk + DC * HS;
@@ -616,8 +619,8 @@ cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t st) {
   const cudaError_t e = allow_all();
   if (e != cudaSuccess) return e;
   if (a.slots > 0) delta_prep_simt_kernel<false><<<(unsigned)a.slots * a.H, THREADS, PREP_BYTES, st>>>(a);
-  delta_scan_simt_kernel<false><<<(unsigned)a.n_seq * a.H * SNB, THREADS, SCAN_BYTES, st>>>(a);
-  return cudaGetLastError();
+  const cudaError_t scan = launch_behind(delta_scan_simt_kernel<false>, (unsigned)a.n_seq * a.H * SNB, THREADS, SCAN_BYTES, st, a);
+  return scan != cudaSuccess ? scan : cudaGetLastError();
 }
 cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t st) {
   const cudaError_t e = allow_all();
@@ -626,11 +629,12 @@ cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t st) {
   const unsigned chunks = (unsigned)a.slots * a.H, units = (unsigned)a.n_seq * a.H * SNB;
   if (a.slots > 0) {
     delta_prep_simt_kernel<true><<<chunks, THREADS, PREP_BYTES, st>>>(a);
-    delta_scan_simt_kernel<true><<<units, THREADS, SCAN_BYTES, st>>>(a);
+    const cudaError_t scan = launch_behind(delta_scan_simt_kernel<true>, units, THREADS, SCAN_BYTES, st, a);
+    if (scan != cudaSuccess) return scan;
   }
-  delta_rscan_simt_kernel<<<units, THREADS, RSCAN_BYTES, st>>>(a, part);
-  if (a.slots > 0) delta_grads_simt_kernel<<<2 * chunks, THREADS, GRAD_BYTES, st>>>(a, part);
-  return cudaGetLastError();
+  cudaError_t last = launch_behind(delta_rscan_simt_kernel, units, THREADS, RSCAN_BYTES, st, a, part);
+  if (a.slots > 0 && last == cudaSuccess) last = launch_behind(delta_grads_simt_kernel, 2 * chunks, THREADS, GRAD_BYTES, st, a, part);
+  return last != cudaSuccess ? last : cudaGetLastError();
 }
 
 }  // namespace gla

@@ -628,6 +628,7 @@ enum { SB_A = 0, SB_C, SB_O, SB_KQ, SB_V, SB_KD, SB_PH, SB_SR, SB_WR, SB_OF, SB_
 
 template <bool STATES>
 __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, int flip_every) {
+  wait_for_previous();
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + ScanSmem::BAR);
@@ -940,6 +941,7 @@ enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_
 constexpr uint32_t RT_P = 0, RT_Q = 64, RT_A = 128, RT_C = 256, RT_Z = 384;
 
 __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, float* dbeta_part) {
+  wait_for_previous();
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + RSmem::BAR);
@@ -1278,6 +1280,7 @@ enum { GB_KQ = 0, GB_IN, GB_FR = GB_IN + 2, GB_MMA = GB_FR + 2, GB_ONE = GB_MMA 
 constexpr uint32_t GT_DS = 160, GT_X2 = 96;  // tensor memory: X dS1^T; phase 2's second product
 
 __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, const float* dbeta_part) {
+  wait_for_previous();
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + GSmem::BAR);
@@ -1672,8 +1675,8 @@ cudaError_t launch_delta_tc_fwd(DeltaArgs a, cudaStream_t st) {
     if (!(input_maps(m, a) && rows_map(&m.o, a.o, DV, a, 32, 32))) return cudaErrorInvalidValue;
     delta_prep_kernel<false><<<chunks, PREP_THREADS, PrepSmem::bytes(false), st>>>(m, a);
   }
-  delta_scan_kernel<false><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a, sm_count());
-  return cudaGetLastError();
+  const cudaError_t scan = launch_behind(delta_scan_kernel<false>, units, SCAN_THREADS, ScanSmem::BYTES, st, m, a, sm_count());
+  return scan != cudaSuccess ? scan : cudaGetLastError();
 }
 
 cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t st) {
@@ -1701,11 +1704,12 @@ cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t st) {
           rows_map(&m.dqo, a.dq, DK, a, 48, 32) && rows_map(&m.dko, a.dk, DK, a, 48, 32)))
       return cudaErrorInvalidValue;
     delta_prep_kernel<true><<<chunks, PREP_THREADS, PrepSmem::bytes(true), st>>>(m, a);
-    delta_scan_kernel<true><<<units, SCAN_THREADS, ScanSmem::BYTES, st>>>(m, a, sm_count());
+    const cudaError_t scan = launch_behind(delta_scan_kernel<true>, units, SCAN_THREADS, ScanSmem::BYTES, st, m, a, sm_count());
+    if (scan != cudaSuccess) return scan;
   }
-  delta_rscan_kernel<<<units, RSCAN_THREADS, RSmem::BYTES, st>>>(m, a, part);
-  if (some) delta_grads_kernel<<<chunks, GRAD_THREADS, GSmem::BYTES, st>>>(m, a, part);
-  return cudaGetLastError();
+  cudaError_t last = launch_behind(delta_rscan_kernel, units, RSCAN_THREADS, RSmem::BYTES, st, m, a, part);
+  if (some && last == cudaSuccess) last = launch_behind(delta_grads_kernel, chunks, GRAD_THREADS, GSmem::BYTES, st, m, a, part);
+  return last != cudaSuccess ? last : cudaGetLastError();
 }
 
 }  // namespace gla
