@@ -1,14 +1,21 @@
 // The gated delta rule on the 5th-generation tensor cores (bf16 calls).  Formulas: gla_delta.cuh.
 //
-//   prep    one CTA a (chunk, head): KK^T and QK^T on the tensor cores, the decays, and the triangular system, solved
-//           once for everything that it multiplies: rows y with y (1 + B M) = r by back substitution, one thread a
-//           row, in fp32.  With r the rows of P and of (diag(e^(G_C - G)) K)^T it gives P^ and K^, and the chunk is
+//   prep    one CTA a (chunk, head): K K^T and Q K^T, the decays, and the triangular system, solved once for everything
+//           that it multiplies: rows y with y (1 + B M) = r, 16 x 16 blocks by back substitution.  With r the rows of P
+//           and of (diag(e^(G_C - G)) K)^T it gives P^ and K^, and the chunk is
 //               O = s (diag(e^G) Q S0 + P^ B R),   S1 = e^(G_C) S0 + K^ B R,   R = V - diag(e^G) K S0:
 //           U is never formed, and two dependent products are left between a state and the next instead of three.
+//           Backward: also Z, P, Q~ = s (diag(e^G) Q)^T and K~ = -(diag(e^G) K)^T (1 + B M^T)^-1.
 //   scan    one CTA a (sequence, head, 64 columns of d_v), chunks in order: [K; Q] S0 (one M = 128 product), then
-//           K^ B R and P^ B R.  Tiles of d_v are independent.
-// What carries the state is held in two bf16 (hi + lo: 16 bits): S, B R and K^; [hi | lo] stand beside each other
-// as N = 128 columns of one product.  P^ and the outputs are one bf16.
+//           K^ B R and P^ B R.  Tiles of d_v are independent.  Backward: the same pass, which keeps each chunk's S0 and X
+//   rscan   the same from the last chunk on: dU = s P^T dO + E K dS1, w = B dU, dS0 = e^(G_C) dS1 + Q~ dO + K~ w; writes
+//           dv, every chunk's dS1 and its columns' part of dbeta
+//   grads   one CTA a (chunk, head): dq, dk, dg, and dbeta's parts summed in tile order
+// What carries the state is held in two bf16 (hi + lo: 16 bits): S, B R, K^, and K~, Q~, P, w, dS; [hi | lo] stand beside
+// each other as N = 128 columns of one product.  What only feeds a bf16 output (P^, Z, X, S0 and dS1 for the gradients) is one
+// bf16: o is 2.1e-3 of the norm from the exact one, of which its own rounding is 1.7e-3, dq, dk and dg 3e-3.
+// What the chunk's length costs: longer chunks halve the scans' steps, but prep and grads grow with its square; 64 tokens
+// are also the 128 rows of [K; Q] and the 128 bytes of a swizzled row.
 #include <cuda.h>
 #include <string.h>
 
@@ -198,6 +205,10 @@ static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_X % 32 
 //   3  slabs of 16 rows y of y (1 + B M) = r, block by block from the last: Y_b = (R_b - sum_c Y_c BM_cb) W_b, each
 //      product hi hi + hi lo + lo hi
 // fp32 sums; what is carried from block to block has 16 bits.
+// Bound by the latency of its chain (loads, products, a substitution of 16 steps, four of blocks) at 16 (backward 12) warps
+// an SM, held there by 124 (151) registers and 54 (64) KB: 8 sequences of 2,048 tokens x 16 heads, 4,096 CTAs, 69 us
+// (141), of which the bytes written take 20 (64).  With the products on tcgen05 and one thread a row of the substitution
+// 137.
 constexpr int PREP_THREADS = 128;
 struct PrepSmem {
   static constexpr uint32_t P0 = 0, P1 = 16384, STAGE = 24576, DM = STAGE, G = STAGE + 4 * 4096, B = G + DC * 8, F = B + DC * 4, E = F + DC * 4,
@@ -612,6 +623,9 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 // K^ B R the other; the next chunk has them the other way round.
 // STATES (the backward's forward pass): K's rows stand in Q's place and the other half is not looked at; Z is in P^'s
 // place, X = R - Z B R and every chunk's S0 go to the workspace instead of outputs.
+// Bound by the chain from state to state, about 4,400 cycles a chunk with two CTAs an SM (three hand-overs between threads and
+// tensor cores, two products, 64 x 64 values to registers and back twice): 8 x 2,048 tokens x 16 heads, 384 CTAs on 304
+// places, 150 us (STATES 161-175); 24 ragged sequences x 7 heads 66 us.  With barriers between the steps 239 us (the call).
 constexpr int TN = 64, NTILE = DV / TN, SCAN_THREADS = 320;
 struct ScanSmem {
   // Products of 128 rows read past operands of 64 and 96 rows, on the side that the lanes call for; what stands there
@@ -634,6 +648,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + ScanSmem::BAR);
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + ScanSmem::BAR + 8 * SB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + ScanSmem::BAR + 8 * SB_N + 4);
+  int* const issued = reinterpret_cast<int*>(sm + ScanSmem::BAR + 8 * SB_N + 8);  // [4] copies to each place
   const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = a.order ? a.order[nh / a.H] : nh / a.H;
   const int tid = threadIdx.x, warp = tid >> 5, q = warp & 3, half = (warp >> 2) & 1;
   const int row = (tid & 31) + 32 * q;  // lane of the products
@@ -735,8 +750,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           if (!(ok = wait(SB_O, c))) break;
           load_ph(c + 1);
         }
-        // what was issued ends before its memory is given up (else everything has been waited for)
-        for (int x = 0; x < 4 && !ok; ++x) mbar_wait_drain(&bar[SB_KQ + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
+        for (int x = 0; x < 4; ++x) issued[x] = loads[x];
       }
       __syncwarp();
     } else if (warp == 8) {
@@ -766,10 +780,6 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) umma(at_a, dp + kk * 32u, db + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
           umma_commit(&bar[SB_O]);
-        }
-        if (!ok) {
-          umma_commit(&bar[SB_DRAIN]);
-          mbar_wait_drain(&bar[SB_DRAIN], 0, DRAIN_NS, a.err);
         }
         stores_read();
       }
@@ -895,6 +905,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {  // what was issued ends before its memory is given up (else everything has been waited for)
+      for (int x = 0; x < 4 && tid == 288; ++x) mbar_wait_drain(&bar[SB_KQ + x], (issued[x] - 1) & 1, DRAIN_NS, a.err);
+      if (tid == 256) {
+        umma_commit(&bar[SB_DRAIN]);
+        mbar_wait_drain(&bar[SB_DRAIN], 0, DRAIN_NS, a.err);
+      }
+      __syncthreads();
+    }
     if (warp == 8) {
       tc_fence_after();
       tm_free<256>(tmem);
@@ -918,10 +936,14 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 // One CTA a (sequence, head, 64 columns of d_v), chunks from the last: with dS1 = dL/dS1 of the chunk,
 //     dU = s P^T dO + diag(E) K dS1,   w = B dU,   dS0 = e^(G_C) dS1 + Q~ dO + K~ w,   dv = B (dU - Z^T w)
 // (E = e^(G_C - G)): again two dependent products a chunk.  P^T dO and Q~ dO need no state; they go to the tensor cores
-// while the state's way waits for registers: Q~ dO behind K dS1, the next chunk's P^T dO behind Z^T w.  dbeta's part of the CTA's columns is (dU - Z^T w) . X.
+// while the state's way waits for registers: Q~ dO behind K dS1, the next chunk's P^T dO behind Z^T w.  dbeta's part of the
+// CTA's columns is (dU - Z^T w) . X.
 // 512 threads, one CTA an SM (the operands take 214 KB): warps 0-7 have the state's rows (0-95; columns as in the scan),
 // warps 8-15 the tokens' (64-127: other schedulers), so that neither waits for what the other writes out; of the warps
 // that have no rows, 8 issues the products and 12 the copies.  Every hand-over through an mbarrier.
+// Bound as the scan, 4,700 cycles a chunk: 8 x 2,048 tokens x 16 heads 210 us, 384 CTAs on 152 places; HBM 49 % busy;
+// with the products in the order of the formulas 242 us.  Units of equal length run in whole rounds (2.5 here: the last
+// half full); cutting all chunks evenly over the CTAs, states handed over between them, was no gain: 231 us.
 // Tensor memory: P^T dO [0,64), Q~ dO [64,128), K dS1 [128,256) and K~ w [256,384) as [hi | lo], Z^T w [384,448).
 constexpr int RSCAN_THREADS = 512;
 struct RSmem {
@@ -931,7 +953,7 @@ struct RSmem {
   // rows: before K, whose rows are the second half, 8 KB that are never written; before Z and P, and behind K~ and Q~, what
   // is as still as the operand itself.  The rows that gives are not looked at.
   static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 8192, S = K1 + 4096, W = S + 24576, OUT = W + 16384,
-                            GT = OUT + 8192, BAR = GT + 2 * 768, BYTES = BAR + 160;
+                            GT = OUT + 8192, BAR = GT + 2 * 768, BYTES = BAR + 176;
   static_assert(BYTES <= 232448, "shared memory");
 };
 // Products and copies, then hand-overs: the state, w, Z^T w and X read.  Whoever waits for a phase of a barrier hands
@@ -947,6 +969,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + RSmem::BAR);
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + RSmem::BAR + 8 * RB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + RSmem::BAR + 8 * RB_N + 4);
+  int* const issued = reinterpret_cast<int*>(sm + RSmem::BAR + 8 * RB_N + 8);  // [5] copies: EARLY's two places, K, K~; X
   const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = a.order ? a.order[nh / a.H] : nh / a.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = (warp >> 2) & 1;
   const int row = lane + 32 * q, col0 = tile * TN + 32 * half;
@@ -1044,12 +1067,8 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           ok = ok && wait(RB_ZF + (it & 1), it >> 1);
           if (ok && it + 2 < nc) load_x(xs++);
         }
-        if (!ok) {  // what was issued ends before its memory is given up (else everything has been waited for)
-          for (int x = 0; x < 4; ++x)
-            if (loads[x]) mbar_wait_drain(&bar[RB_EF + x], (loads[x] - 1) & 1, DRAIN_NS, a.err);
-          for (int it = max(0, loads[2] - 2); it < loads[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
-          for (int it = max(0, xs - 2); it < xs; ++it) mbar_wait_drain(&bar[RB_X + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
-        }
+        for (int x = 0; x < 4; ++x) issued[x] = loads[x];
+        issued[4] = xs;
       }
       __syncwarp();
     } else if (warp == 8) {
@@ -1114,10 +1133,6 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
             umma(tmem + RT_Z, dz + kk * 2048u, dw + kk * 2048u, idesc_bf16(128, 64, 1, 1), kk > 0);
           umma_commit(&bar[RB_Z]);
           if (it + 1 < nc) ok = early(it + 1);
-        }
-        if (!ok) {
-          umma_commit(&bar[RB_DRAIN]);
-          mbar_wait_drain(&bar[RB_DRAIN], 0, DRAIN_NS, a.err);
         }
         stores_read();
       }
@@ -1239,6 +1254,19 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {  // what was issued ends before its memory is given up (else everything has been waited for)
+      if (warp == 12 && lane == 0) {
+        for (int x = 0; x < 4; ++x)
+          if (issued[x]) mbar_wait_drain(&bar[RB_EF + x], (issued[x] - 1) & 1, DRAIN_NS, a.err);
+        for (int it = max(0, issued[2] - 2); it < issued[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
+        for (int it = max(0, issued[4] - 2); it < issued[4]; ++it) mbar_wait_drain(&bar[RB_X + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
+      }
+      if (warp == 8 && lane == 0) {
+        umma_commit(&bar[RB_DRAIN]);
+        mbar_wait_drain(&bar[RB_DRAIN], 0, DRAIN_NS, a.err);
+      }
+      __syncthreads();
+    }
     if (warp == 12) {
       tc_fence_after();
       tm_free<512>(tmem);
@@ -1265,7 +1293,8 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 //     dg_t = sum of dG_i, i >= t
 // 288 threads, 2 CTAs an SM: warps 0-7 have lanes 32 (w % 4) .. of the products' rows and 48 columns of d_k (w / 4); rows
 // 0-63 have dq, 64-127 all of dk.  Warp 8 issues copies and products.  Panels have two places, K and Q come into the second.
-// Bound by latency and, of 196 KB a chunk and head, by HBM.
+// Bound by HBM (196 KB a chunk and head, 62 % busy) and by latency: 8 x 2,048 tokens x 16 heads 165 us, 4.9 TB/s; with one
+// place for the panels and three boxes instead of one 190 us.
 constexpr int GRAD_THREADS = 288;
 struct GSmem {
   // a panel: [dO; dR], [X; S0], dS1; later Es and Fm in the first place, K and Q (two tiles of 64 columns each) in the second.
@@ -1379,9 +1408,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
         for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + 8192u + kk * 2048u, dk + kk * 2048u, idesc_bf16(128, 96, 1, 1), 1);
         umma_commit(&bar[GB_TWO]);
       } while (false);
-      if (!ok) {  // what was issued ends before its memory is given up (else everything has been waited for)
-        umma_commit(&bar[GB_DRAIN]);
-        mbar_wait_drain(&bar[GB_DRAIN], 0, DRAIN_NS, a.err);
+      if (!ok) {  // the copies end before their memory is given up (else they have all been waited for)
         for (int p = max(0, panels - 2); p < panels; ++p) mbar_wait_drain(&bar[GB_IN + (p & 1)], p >> 1, DRAIN_NS, a.err);
         if (kqs) mbar_wait_drain(&bar[GB_KQ], 0, DRAIN_NS, a.err);
       }
@@ -1557,6 +1584,13 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {  // (and the products, before tensor memory is given back)
+    if (warp == 8 && lane == 0) {
+      umma_commit(&bar[GB_DRAIN]);
+      mbar_wait_drain(&bar[GB_DRAIN], 0, DRAIN_NS, a.err);
+    }
+    __syncthreads();
+  }
   if (warp == 8) {
     tc_fence_after();
     tm_free<256>(tmem);

@@ -459,3 +459,22 @@ def test_scale_default_and_debug_build():
         assert gla.gla_get_device_error() == 0
     for a, c in zip(want, got):
         assert torch.equal(a, c), far(a, c)
+
+
+def test_waits_that_run_out():
+    """With a limit of 1 us a wait that blocks gives up: the call ends, the error is reported, the next one is right."""
+    b = Batch(24, [700] * 3, 16, BF, packed=False)
+    x, dO, h0 = b.inputs(), b.dev("dO")[0], b.h0.cuda()
+    want = [*gla.gla_delta_fwd(*x, h0=h0), *gla.gla_delta_bwd(*x, dO, h0=h0)]
+    assert gla.gla_get_device_error() == 0
+    for call in (lambda: gla.gla_delta_fwd(*x, h0=h0), lambda: gla.gla_delta_bwd(*x, dO, h0=h0)):
+        gla.gla_set_wait_limit_ns(1000)
+        try:
+            call()
+            assert gla.gla_get_device_error() == -8
+        finally:
+            gla.gla_set_wait_limit_ns(2_000_000_000)
+    got = [*gla.gla_delta_fwd(*x, h0=h0), *gla.gla_delta_bwd(*x, dO, h0=h0)]
+    assert gla.gla_get_device_error() == 0
+    for a, c in zip(want, got):
+        assert torch.equal(a, c)
