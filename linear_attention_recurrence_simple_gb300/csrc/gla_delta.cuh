@@ -107,7 +107,7 @@ __device__ __forceinline__ DeltaChunk chunk_of_slot(const DeltaArgs& a, int slot
 }
 
 // A call's kernels follow each other without the gap of a launch: CTAs of the next one take the places that the last CTAs
-// of this one leave, and wait for its end (and so for all before it) before they read anything (backward, fp32, 2 x 130
+// of this one leave, and wait for its end (and so for all before it) before they read anything (backward, fp32, 2 x 150
 // tokens x 4 heads: 129 -> 123 us; bf16, 40 packed sequences x 16 heads: 570 -> 558 us; a call for the next kernel at
 // the start of a CTA is slower, 132 and 561 us: what comes early takes room from what runs).
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

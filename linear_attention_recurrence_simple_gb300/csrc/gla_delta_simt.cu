@@ -9,7 +9,7 @@
 // The operands of a product stand in shared memory with the summed index contiguous (where both ways are needed,
 // twice), so that a thread reads four of its steps at once: rows of 4 mod 32 words apart, free of bank conflicts.
 // Every thread has a small tile of the result in registers.  A chunk's loads go out together, in vectors, while the chunk
-// before it is computed (2 x 130 tokens x 4 heads: scan 26 -> 25 us, rscan 44 -> 42, 14 us a chunk).  Bound by the reads
+// before it is computed (2 sequences of up to 150 tokens x 4 heads: scan 26 -> 25 us, rscan 44 -> 42, 14 us a chunk).  Bound by the reads
 // from shared memory (a 4 x 2 tile takes six vectors for 32 FMAs), short calls also by their few CTAs.
 #include "gla_delta.cuh"
 #include "gla_once.cuh"
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
 
 // ---- gradients of the chunk ------------------------------------------------------------------
 // A cluster of two CTAs a (chunk, head), each with 32 rows of Es and Fm, which both need whole and write to each other,
-// and with 48 columns of d_k: short calls have few chunks (2 sequences of 130 tokens, 4 heads: 68 us with one CTA, 47.5
+// and with 48 columns of d_k: short calls have few chunks (2 sequences of up to 150 tokens, 4 heads: 68 us with one CTA, 47.5
 // with two; bound by shared memory, two vectors read for every five or six FMAs a lane).  Pieces of 32 columns
 // of d_v: dO, dR, U [64][36], S0, dS1 [48][36], the next piece's loads in flight; then Es, Fm and their transposes
 // [64][68] in their place.  K and Q [64][52], K^T and Q^T [48][68].
