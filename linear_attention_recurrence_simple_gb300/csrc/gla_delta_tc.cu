@@ -1630,12 +1630,14 @@ size_t delta_tc_ws_bytes(int n_seq, long long slots, long long tokens, int H, bo
   return (size_t)slots * H * (bwd ? W_BWD : W_FWD) + (bwd ? (size_t)2 * NTILE * tokens * H * 4 : 0) + (size_t)n_seq * 4;
 }
 
+namespace {
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 typedef CUresult (*ReplaceAddressFn)(CUtensorMap*, void*);
 template <class F>
-static F driver_fn(const char* name) {
+F driver_fn(const char* name) {
   void* p = nullptr;
   cudaDriverEntryPointQueryResult q;
   const bool found = cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess;
@@ -1644,7 +1646,7 @@ static F driver_fn(const char* name) {
 // bf16 [d2][d1][d0], strides in bytes, in boxes of `cols` (64: 128-byte swizzle, 32: 64-byte, 48: none) x r1 x r2.  Encoding a map
 // takes the host a microsecond, and a call has up to 16: each thread keeps the last ones that it encoded, by their shape, and
 // gives them the call's address.
-static bool map3(CUtensorMap* m, const void* base, long long d0, long long d1, long long d2, long long s1, long long s2, int cols,
+bool map3(CUtensorMap* m, const void* base, long long d0, long long d1, long long d2, long long s1, long long s2, int cols,
                  int r1, int r2) {
   static const EncodeTiledFn encode = driver_fn<EncodeTiledFn>("cuTensorMapEncodeTiled");
   static const ReplaceAddressFn replace = driver_fn<ReplaceAddressFn>("cuTensorMapReplaceAddress");
@@ -1674,24 +1676,26 @@ static bool map3(CUtensorMap* m, const void* base, long long d0, long long d1, l
   return true;
 }
 // A [tokens, H, d] tensor in boxes of one head.
-static bool rows_map(CUtensorMap* m, const void* base, int d, const DeltaArgs& a, int cols, int rows) {
+bool rows_map(CUtensorMap* m, const void* base, int d, const DeltaArgs& a, int cols, int rows) {
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
   return map3(m, base, d, a.H, tokens, 2ll * d, 2ll * a.H * d, cols, 1, rows);
 }
-static bool input_maps(DeltaMaps& m, const DeltaArgs& a) {
+bool input_maps(DeltaMaps& m, const DeltaArgs& a) {
   return rows_map(&m.k0, a.k, DK, a, 64, DC) && rows_map(&m.k1, a.k, DK, a, 32, DC) && rows_map(&m.q0, a.q, DK, a, 64, DC) &&
          rows_map(&m.q1, a.q, DK, a, 32, DC) && rows_map(&m.v, a.v, DV, a, 64, DC);
 }
 // CTAs b and b + this many are likely to share an SM.
-static int sm_count() {
+int sm_count() {
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   return sms;
 }
 template <class F>
-static cudaError_t allow(F* f, uint32_t bytes) {
+cudaError_t allow(F* f, uint32_t bytes) {
   return cudaFuncSetAttribute((const void*)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
+
+}  // namespace
 
 cudaError_t launch_delta_tc_fwd(DeltaArgs a, cudaStream_t st) {
   static OncePerDevice<CudaDeviceApi> once;
