@@ -440,7 +440,8 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
  *   g, beta      [n_seq, T, H] (or packed [T_total, H]; [N, H] in the decode step), dtype `dtype`: the natural
  *                log of the decay (<= 0 in use; -inf allowed, a reset; values below -120 count as -120) and the
  *                strength.  beta times the squared length of k is meant to lie in [0, 2]: beyond that the
- *                recurrence itself grows.  (Keys of unit length and strengths in [0, 1] are the usual form.)
+ *                recurrence itself grows.  (Keys of unit length and strengths in [0, 1] are the usual form.)  They
+ *                and their gradients need the alignment of their type only: a slice of a packed array will do.
  * q, k, v, o, states, scale, cu_seqlens, dtype and the layouts are those of gla_chunk_fwd.  A call's tokens are
  * handled in chunks of 64; an infinity or a NaN in a token reaches every output of its chunk and what follows it in
  * its sequence, and nothing of another sequence.  cu_seqlens is checked on the device: offsets that decrease or pass

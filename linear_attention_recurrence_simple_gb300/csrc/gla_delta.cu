@@ -15,6 +15,8 @@ namespace {
 
 bool off16(const void* p) { return ((uintptr_t)p & 15u) != 0; }
 bool off4(const void* p) { return ((uintptr_t)p & 3u) != 0; }
+// g, beta and their gradients are read and written an element at a time: a step's slice of a packed array may start anywhere
+bool off_element(const void* p, int dtype) { return ((uintptr_t)p & (dtype == GLA_F32 ? 3u : 1u)) != 0; }
 int status_of(cudaError_t e) { return e == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH; }
 
 // Sizes of a chunked call; the states of all chunk places, in rows, stay below 2^31 (and so do CTAs).
@@ -60,8 +62,9 @@ int gla_delta_fwd(const void* q, const void* k, const void* v, const void* g, co
   if ((long long)h0_rows * H * GLA_DK >= (1ll << 31) || (long long)hT_rows * H * GLA_DK >= (1ll << 31)) return GLA_ERR_SHAPE;
   if (n_seq == 0) return GLA_OK;
   if (tokens > 0 && (!q || !k || !v || !g || !beta || !o)) return GLA_ERR_NULL;
-  for (const void* p : {q, k, v, g, beta, (const void*)o, (const void*)h0, (const void*)hT})
+  for (const void* p : {q, k, v, (const void*)o, (const void*)h0, (const void*)hT})
     if (off16(p)) return GLA_ERR_ALIGN;
+  if (off_element(g, dtype) || off_element(beta, dtype)) return GLA_ERR_ALIGN;
   if (off4(h0_row) || off4(hT_row)) return GLA_ERR_ALIGN;
   if (!workspace || ws_bytes < gla_delta_workspace_bytes(n_seq, T, H, cu_seqlens != nullptr, dtype)) return GLA_ERR_WORKSPACE;
   if (off16(workspace)) return GLA_ERR_ALIGN;
@@ -101,9 +104,10 @@ int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, co
   if (tokens > 0)
     for (const void* p : {q, k, v, g, beta, dO, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)dg, (const void*)dbeta})
       if (!p) return GLA_ERR_NULL;
-  for (const void* p : {q, k, v, g, beta, dO, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)dg,
-                        (const void*)dbeta, (const void*)h0, (const void*)dhT, (const void*)dh0})
+  for (const void* p : {q, k, v, dO, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)h0, (const void*)dhT, (const void*)dh0})
     if (off16(p)) return GLA_ERR_ALIGN;
+  for (const void* p : {g, beta, (const void*)dg, (const void*)dbeta})
+    if (off_element(p, dtype)) return GLA_ERR_ALIGN;
   if (!workspace || ws_bytes < gla_delta_bwd_workspace_bytes(n_seq, T, H, cu_seqlens != nullptr, dtype)) return GLA_ERR_WORKSPACE;
   if (off16(workspace)) return GLA_ERR_ALIGN;
   rc = gla::current_device_state(&a.err, &a.wait_ns);
@@ -141,10 +145,11 @@ static int delta_decode(const void* q, const void* k, const void* v, const void*
   if (N < 0 || H < 1 || pool_rows < 0 || (long long)N * H >= (1ll << 31)) return GLA_ERR_SHAPE;
   if (!slot && pool_rows < N) return GLA_ERR_SHAPE;
   if (N == 0) return GLA_OK;
-  for (const void* p : {q, k, v, g, beta, (const void*)state, (const void*)o}) {
+  for (const void* p : {q, k, v, g, beta, (const void*)state, (const void*)o})
     if (!p) return GLA_ERR_NULL;
+  for (const void* p : {q, k, v, (const void*)state, (const void*)o})
     if (off16(p)) return GLA_ERR_ALIGN;
-  }
+  if (off_element(g, dtype) || off_element(beta, dtype)) return GLA_ERR_ALIGN;
   if (off4(slot)) return GLA_ERR_ALIGN;
   gla::DeltaArgs a = {};
   const int rc = gla::current_device_state(&a.err, &a.wait_ns);

@@ -18,6 +18,8 @@ BIG = 1 << 40
 def lib():
     return gla.load_library()
 
+GATES = ("g", "beta", "dg", "dbeta")  # aligned to their element
+
 
 def fwd(lib, q=A, k=A, v=A, g=A, beta=A, h0=A, h0_rows=9, h0_row=None, o=A, hT=A, hT_rows=9, hT_row=None, cu=None, n=3, T=7,
         H=2, dk=96, dv=192, dt=0, ws=A, wsb=BIG):
@@ -53,7 +55,7 @@ def test_chunked_argument_errors(lib, call):
     for name in names:
         assert call(lib, **{name: None}) == NULL, name
     for name in names + ["h0"] + (["hT"] if call is fwd else ["dhT", "dh0"]):
-        assert call(lib, **{name: MIS}) == ALIGN, name
+        assert call(lib, **{name: A + 1 if name in GATES else MIS}) == ALIGN, name
     assert call(lib, ws=None) == WS
     assert call(lib, wsb=1000) == WS
     assert call(lib, ws=MIS) == ALIGN
@@ -79,7 +81,7 @@ def test_decode_argument_errors(lib):
             assert step(lib, bf16, **kw) == SHAPE, kw
         for name in ("q", "k", "v", "g", "beta", "state", "o"):
             assert step(lib, bf16, **{name: None}) == NULL, name
-            assert step(lib, bf16, **{name: MIS}) == ALIGN, name
+            assert step(lib, bf16, **{name: A + 1 if name in GATES else MIS}) == ALIGN, name
         assert step(lib, bf16, slot=A + 2) == ALIGN
         assert step(lib, bf16, N=0, q=None) == OK
 

@@ -478,3 +478,46 @@ def test_waits_that_run_out():
     assert gla.gla_get_device_error() == 0
     for a, c in zip(want, got):
         assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta", "dO"])
+def test_nan_beside_a_ragged_end(name, dtype):
+    """Chunks that end inside a sequence's last 64 tokens share their rows with the next sequence's first ones: a NaN there
+    stays out of every result of the sequence before it, of the one after it and of the other head."""
+    b = Batch(25, [100, 70, 65], 2, dtype)
+
+    def run():
+        x, dO = b.inputs(), b.dev("dO")[0]
+        o, hT = gla.gla_delta_fwd(*x, h0=b.h0.cuda(), cu_seqlens=b.cu_dev)
+        *rows, dh0 = gla.gla_delta_bwd(*x, dO, h0=b.h0.cuda(), dhT=b.dhT.cuda(), cu_seqlens=b.cu_dev)
+        return [o, *rows], [hT, dh0]
+
+    rows, states = run()
+    b.x[name][103, 1] = float("nan")
+    rows2, states2 = run()
+    for x, y in zip(rows, rows2):
+        assert torch.equal(x[:100], y[:100]) and torch.equal(x[170:], y[170:]) and torch.equal(x[:, 0], y[:, 0])
+    for x, y in zip(states, states2):
+        assert torch.equal(x[[0, 2]], y[[0, 2]]) and torch.equal(x[:, 0], y[:, 0])
+    assert not all(bool(torch.isfinite(y).all()) for y in rows2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_slices_of_a_packed_array(dtype):
+    """Three heads: a token's gates are 6 or 12 bytes, so that slices of g and beta start off 16-byte boundaries."""
+    b = Batch(26, [90], 3, dtype)
+    x, dO = b.inputs(), b.dev("dO")[0]
+    part, cu = [t[17:80] for t in x], i32([0, 63])
+    own = [t.clone() for t in part]
+    for t, c in zip(gla.gla_delta_fwd(*part, cu_seqlens=cu), gla.gla_delta_fwd(*own, cu_seqlens=cu)):
+        assert torch.equal(t, c)
+    for t, c in zip(gla.gla_delta_bwd(*part, dO[17:80], cu_seqlens=cu), gla.gla_delta_bwd(*own, dO[17:80].clone(), cu_seqlens=cu)):
+        assert torch.equal(t, c)
+    pool = torch.randn(5, 3, DK, DV, device="cuda")
+    a, c = pool.clone(), pool.clone()
+    assert torch.equal(gla.gla_delta_decode_step(*[t[13:18] for t in x], a), gla.gla_delta_decode_step(*[t[13:18].clone() for t in x], c))
+    assert torch.equal(a, c)
+    flat = torch.zeros(90 * 3 * DK + 1, dtype=dtype, device="cuda")[1:].view(90, 3, DK)
+    with pytest.raises(gla.GlaError):
+        gla.gla_delta_fwd(flat, *x[1:], cu_seqlens=b.cu_dev)
