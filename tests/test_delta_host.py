@@ -10,6 +10,7 @@ from tests.delta_helpers import DK, DV, ref_bwd, ref_fwd
 
 OK, NULL, SHAPE, DTYPE, ALIGN, UNSUP, WS = 0, -1, -2, -3, -4, -5, -6
 A, MIS = 0x10000, 0x10004  # fake device addresses, never dereferenced
+GATES = ("g", "beta", "dg", "dbeta")  # aligned to their element
 P = ctypes.c_void_p
 BIG = 1 << 40
 
@@ -17,8 +18,6 @@ BIG = 1 << 40
 @pytest.fixture(scope="module")
 def lib():
     return gla.load_library()
-
-GATES = ("g", "beta", "dg", "dbeta")  # aligned to their element
 
 
 def fwd(lib, q=A, k=A, v=A, g=A, beta=A, h0=A, h0_rows=9, h0_row=None, o=A, hT=A, hT_rows=9, hT_row=None, cu=None, n=3, T=7,
