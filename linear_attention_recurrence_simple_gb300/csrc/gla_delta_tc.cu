@@ -626,6 +626,8 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 // Bound by the chain from state to state, about 4,400 cycles a chunk with two CTAs an SM (three hand-overs between threads and
 // tensor cores, two products, 64 x 64 values to registers and back twice): 8 x 2,048 tokens x 16 heads, 384 CTAs on 304
 // places, 150 us (STATES 161-175); 24 ragged sequences x 7 heads 66 us.  With barriers between the steps 239 us (the call).
+// Cutting the units into parts that fill whole rounds (a CTA a part, states handed over, the same bits) took 160 us: a CTA that
+// has its SM to itself is faster, so that a last round that is part full loses little.
 constexpr int TN = 64, NTILE = DV / TN, SCAN_THREADS = 320;
 struct ScanSmem {
   // Products of 128 rows read past operands of 64 and 96 rows, on the side that the lanes call for; what stands there
@@ -942,8 +944,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 // warps 8-15 the tokens' (64-127: other schedulers), so that neither waits for what the other writes out; of the warps
 // that have no rows, 8 issues the products and 12 the copies.  Every hand-over through an mbarrier.
 // Bound as the scan, 4,700 cycles a chunk: 8 x 2,048 tokens x 16 heads 210 us, 384 CTAs on 152 places; HBM 49 % busy;
-// with the products in the order of the formulas 242 us.  Units of equal length run in whole rounds (2.5 here: the last
-// half full); cutting all chunks evenly over the CTAs, states handed over between them, was no gain: 231 us.
+// with the products in the order of the formulas 242 us; in parts, as above, 248.
 // Tensor memory: P^T dO [0,64), Q~ dO [64,128), K dS1 [128,256) and K~ w [256,384) as [hi | lo], Z^T w [384,448).
 constexpr int RSCAN_THREADS = 512;
 struct RSmem {
