@@ -559,48 +559,26 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     }
   }
   __syncthreads();
-  // 3: the rows of P^ (Z) and K^, two slabs at a time: warps 0 and 1 two of K^ and then their short one of P^, warps 2 and 3
-  // one of each; of K~ (and Q~) the other way round
+  // 3: the rows of P^ (Z) and K^, two slabs at a time: every warp one of each, then warps 0 and 1, whose slab of P^ is short,
+  // another one of K^; of K~ (and Q~) warps 2 and 3 two.  (One copy of the code for all of that: the kernel is long enough
+  // for its instructions to be fetched slower than they run.)
   if (BWD) store_slab(out[0], sm, ws + W_P + 2048 * warp, ws + W_P + 8192 + 2048 * warp);
-  auto store_kd = [&](const Slab& s, int x) { store_slab(s, sm, ws + W_KD + 2048 * x, ws + W_KD + 12288 + 2048 * x); };
-  if (warp >= 2) {
-    transposed_slab(r[0], sb, false, 16 * (2 + warp), se, 1.f);
-    solve_slabs<false, 2>(r, {3, warp}, frags, out);
-    store_kd(out[0], 2 + warp);
-    store_slab(out[1], sm, ws + W_PH + 2048 * warp, nullptr);
-  } else {
-    {
-      float p[1][4][2][4];
-      Slab one[1];
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[0][b][i >> 2][i & 3] = r[1][b][i >> 2][i & 3];
-      solve_slabs<false, 1>(p, {warp}, frags, one);
-      store_slab(one[0], sm, ws + W_PH + 2048 * warp, nullptr);
-    }
-    transposed_slab(r[0], sb, false, 32 * warp, se, 1.f);
-    transposed_slab(r[1], sb, false, 32 * warp + 16, se, 1.f);
-    solve_slabs<false, 2>(r, {3, 3}, frags, out);
-    store_kd(out[0], 2 * warp);
-    store_kd(out[1], 2 * warp + 1);
+#pragma unroll 1
+  for (int x = warp; x < 6; x += 4) {
+    transposed_slab(r[0], sb, false, 16 * x, se, 1.f);
+    solve_slabs<false, 2>(r, {3, x == warp ? warp : -1}, frags, out);
+    store_slab(out[0], sm, ws + W_KD + 2048 * x, ws + W_KD + 12288 + 2048 * x);
+    if (x == warp) store_slab(out[1], sm, ws + W_PH + 2048 * warp, nullptr);
   }
   if constexpr (BWD) {
     auto store_kr = [&](const Slab& s, int x) { store_slab(s, sm, ws + W_KR + 2048 * x, ws + W_KR + 12288 + 2048 * x); };
     const int up0 = warp < 2 ? warp : 2 * warp - 2, ups = warp < 2 ? 1 : 2;
-    if (warp >= 2) {
-      transposed_slab(r[0], sb, false, 16 * up0, sf, -1.f);
-      transposed_slab(r[1], sb, false, 16 * up0 + 16, sf, -1.f);
-      solve_slabs<true, 2>(r, {3, 3}, frags, out);
-      store_kr(out[0], up0);
-      store_kr(out[1], up0 + 1);
-    } else {
-      float p[1][4][2][4];
-      Slab one[1];
-      transposed_slab(p[0], sb, false, 16 * up0, sf, -1.f);
-      solve_slabs<true, 1>(p, {3}, frags, one);
-      store_kr(one[0], up0);
-    }
+    transposed_slab(r[0], sb, false, 16 * up0, sf, -1.f);
+    if (ups > 1) transposed_slab(r[1], sb, false, 16 * up0 + 16, sf, -1.f);
+    solve_slabs<true, 2>(r, {3, ups > 1 ? 3 : -1}, frags, out);
+    store_kr(out[0], up0);
+    if (ups > 1) store_kr(out[1], up0 + 1);
+#pragma unroll 1
     for (int x = up0; x < up0 + ups; ++x) {
       transposed_slab(r[0], sb, true, 16 * x, sf, a.scale);
 #pragma unroll
