@@ -427,28 +427,41 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     }
     return;
   }
-  // A block of Q K^T or K K^T, rows i of block rb and columns j of block cb <= rb, times the decays: on the diagonal
-  // only j < i (or, `with`, j <= i).
-  auto decayed = [&](float (&x)[2][4], int rb, int cb, bool with) {
-    if (rb > cb) {
-      const float r0 = rf[cb * DC + 16 * rb + g], r1 = rf[cb * DC + 16 * rb + g + 8];
+  // A block of Q K^T or K K^T, rows i of block rb and columns j of block cb, times the decays: off the diagonal (cb < rb),
+  // and on it, where only j < i (or, `with`, j <= i).
+  auto off_diagonal = [&](float (&x)[2][4], bool is_q, int rb, int cb) {
+    block_dot(x, sb, is_q, 16 * rb, 16 * cb);
+    const float r0 = rf[cb * DC + 16 * rb + g], r1 = rf[cb * DC + 16 * rb + g + 8];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float2 c = *reinterpret_cast<const float2*>(cf + 16 * cb + 8 * n + 2 * t);
-        const float2 y0 = fmul2(fmul2(both(r0), c), make_float2(x[n][0], x[n][1])), y1 = fmul2(fmul2(both(r1), c), make_float2(x[n][2], x[n][3]));
-        x[n][0] = y0.x;
-        x[n][1] = y0.y;
-        x[n][2] = y1.x;
-        x[n][3] = y1.y;
+    for (int n = 0; n < 2; ++n) {
+      const float2 c = *reinterpret_cast<const float2*>(cf + 16 * cb + 8 * n + 2 * t);
+      const float2 y0 = fmul2(fmul2(both(r0), c), make_float2(x[n][0], x[n][1])), y1 = fmul2(fmul2(both(r1), c), make_float2(x[n][2], x[n][3]));
+      x[n][0] = y0.x;
+      x[n][1] = y0.y;
+      x[n][2] = y1.x;
+      x[n][3] = y1.y;
+    }
+  };
+  auto on_diagonal = [&](float (&x)[2][4], bool is_q, int rb, bool with) {
+    block_dot(x, sb, is_q, 16 * rb, 16 * rb);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = g + 8 * (e >> 1), j = 8 * n + 2 * t + (e & 1);
+        x[n][e] = j < i || (with && j == i) ? decay(16 * rb + i, 16 * rb + j) * x[n][e] : 0.f;
       }
-    } else {
+  };
+  // This warp's 16 rows of either, in r[1]
+  auto rows_of = [&](float (&x)[4][2][4], bool is_q) {
+    float d[2][4];
+    on_diagonal(d, is_q, warp, is_q);
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+    for (int b = 0; b < 4; ++b) {
+      if (b < 3 && b < warp) off_diagonal(x[b], is_q, warp, b);
+      else
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = g + 8 * (e >> 1), j = 8 * n + 2 * t + (e & 1);
-          x[n][e] = j < i || (with && j == i) ? decay(16 * rb + i, 16 * rb + j) * x[n][e] : 0.f;
-        }
+        for (int i = 0; i < 8; ++i) x[b][i >> 2][i & 3] = b == warp ? d[i >> 2][i & 3] : 0.f;
     }
   };
   // A block's operand (rows of x are its columns), hi and lo.
@@ -462,39 +475,29 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
   // 1: P's rows (BWD: written as they are, and M's rows in their place, which are also -(B M^T)'s columns)
   float r[2][4][2][4];
   Slab out[2];
-#pragma unroll
-  for (int b = 0; b < 4; ++b)
-    if (b <= warp) {
-      block_dot(r[1][b], sb, true, 16 * warp, 16 * b);
-      decayed(r[1][b], warp, b, true);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[1][b][i >> 2][i & 3] = 0.f;
-    }
+  rows_of(r[1], true);
   if constexpr (BWD) {
 #pragma unroll
+    for (int b = 0; b < 4; ++b) to_operand(r[1][b], out[0].hi[b], out[0].lo[b]);
+    rows_of(r[1], false);
+#pragma unroll
     for (int b = 0; b < 4; ++b) {
-      to_operand(r[1][b], out[0].hi[b], out[0].lo[b]);
-      if (b <= warp) {
-        block_dot(r[1][b], sb, false, 16 * warp, 16 * b);
-        decayed(r[1][b], warp, b, false);
-        float x[2][4];
+      if (b > warp) continue;
+      float x[2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = 8 * n + 2 * t + (e & 1);
-            x[n][e] = -sbeta[16 * b + j] * r[1][b][n][e];
-            if (b == warp) dm[DM_FLOATS + (b * 16 + j) * 20 + g + 8 * (e >> 1)] = x[n][e];
-          }
-        if (b != warp) put_frag(x, 10 + frag_off(warp, b));
-      }
+        for (int e = 0; e < 4; ++e) {
+          const int j = 8 * n + 2 * t + (e & 1);
+          x[n][e] = -sbeta[16 * b + j] * r[1][b][n][e];
+          if (b == warp) dm[DM_FLOATS + (b * 16 + j) * 20 + g + 8 * (e >> 1)] = x[n][e];
+        }
+      if (b != warp) put_frag(x, 10 + frag_off(warp, b));
     }
   }
   const int mb = 3 - warp;
-#pragma unroll
-  for (int jb = 0; jb < 4; ++jb) {
-    if (jb > mb) continue;
+#pragma unroll 1
+  for (int jb = 0; jb <= mb; ++jb) {
     float x[2][4];  // rows j, columns m
     block_dot(x, sb, false, 16 * jb, 16 * mb);
     if (jb != mb) {
