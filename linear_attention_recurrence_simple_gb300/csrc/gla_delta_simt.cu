@@ -63,29 +63,50 @@ __device__ __forceinline__ void put_column(float* at, float4 v) {
   at[2 * STRIDE] = v.z;
   at[3 * STRIDE] = v.w;
 }
+// Vector e of rows of W floats: a warp has 8 rows x 64 bytes, so that columns, too, go to shared memory without conflicts (a
+// row after the other, its stores have 12 of 32 lanes on a bank).
+template <int W>
+struct At {
+  int row, col;
+  __device__ __forceinline__ explicit At(int e) {
+    const int tile = e / 32, lane = e % 32;
+    row = 8 * (tile / (W / 16)) + lane / 4;
+    col = 16 * (tile % (W / 16)) + 4 * (lane % 4);
+  }
+};
 // Rows [0, C) of a [tokens, H, D] tensor, columns [c0, c0 + W), zeros from row `len` on.
 template <int W>
 struct Rows : Held<DC * W / 4> {
   __device__ __forceinline__ void fetch(const void* src, long long t0, int len, int H, int h, int D, int c0) {
     Held<DC * W / 4>::fetch([&](int e) {
-      const int i = e / (W / 4), c = e % (W / 4) * 4;
-      return i < len ? *reinterpret_cast<const float4*>((const float*)src + ((t0 + i) * H + h) * D + c0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const At<W> at(e);
+      return at.row < len ? *reinterpret_cast<const float4*>((const float*)src + ((t0 + at.row) * H + h) * D + c0 + at.col)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
     });
   }
   template <class P>
   __device__ __forceinline__ void place(P put) const {
-    Held<DC * W / 4>::place([&](int e, float4 v) { put(e / (W / 4), e % (W / 4) * 4, v); });
+    Held<DC * W / 4>::place([&](int e, float4 v) {
+      const At<W> at(e);
+      put(at.row, at.col, v);
+    });
   }
 };
 // Rows [0, R) x W floats, row stride LD, of the workspace.
 template <int R, int W, int LD>
 struct Block : Held<R * W / 4> {
   __device__ __forceinline__ void fetch(const float* src) {
-    Held<R * W / 4>::fetch([&](int e) { return *reinterpret_cast<const float4*>(src + e / (W / 4) * LD + e % (W / 4) * 4); });
+    Held<R * W / 4>::fetch([&](int e) {
+      const At<W> at(e);
+      return *reinterpret_cast<const float4*>(src + at.row * LD + at.col);
+    });
   }
   template <class P>
   __device__ __forceinline__ void place(P put) const {
-    Held<R * W / 4>::place([&](int e, float4 v) { put(e / (W / 4), e % (W / 4) * 4, v); });
+    Held<R * W / 4>::place([&](int e, float4 v) {
+      const At<W> at(e);
+      put(at.row, at.col, v);
+    });
   }
 };
 template <int R, int W, int LD, class P>
