@@ -20,8 +20,7 @@ namespace {
 constexpr int SB = 32;             // columns of d_v a scan CTA has
 constexpr int SNB = DV / SB;       // 6
 constexpr int THREADS = 256;
-constexpr int KS = DK + 4, CS = DC + 4, BS = SB + 4;  // row strides in shared memory
-constexpr int I16 = 16 * CS, K16 = 16 * KS, B16 = 16 * BS;  // a thread's rows are 16 apart
+constexpr int KS = DK + 16, CS = DC + 16, BS = SB + 16;  // row strides in shared memory: 16 mod 32 words
 
 // Workspace of a (chunk place, head), in floats.
 constexpr long long WS_Z = 0, WS_P = WS_Z + DC * DC, WS_GT = WS_P + DC * DC, WS_FWD = WS_GT + 5 * DC;
@@ -115,23 +114,86 @@ __device__ __forceinline__ void load_block(const float* src, P put) {
   b.fetch(src);
   b.place(put);
 }
-// acc[r][c] += sum_k A[r * AS + k] B[c * BS + k]
-template <int NR, int NC, int K, int AS, int BS>
-__device__ __forceinline__ void gemm(float (&acc)[NR][NC], const float* a, const float* b) {
-#pragma unroll 4
-  for (int k = 0; k < K; k += 4) {
-    float4 x[NR], y[NC];
+// A fp32 value as two of tf32, 11 bits each: the first rounded, the second cut off by the products, 2^-22 of it left out.
+// (In whole numbers: the conversion instruction has a quarter of their rate.  Of a NaN the second is one.)
+__device__ __forceinline__ void two(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// acc += sum_k A[row * AS + k] B[col * BS + k] over the warp's MB blocks of 16 rows from `a` on and NT of 8 columns from `b` on,
+// each product in three of tf32.  acc[m][n][e]: row 16 m + lane / 4 + 8 (e / 2), column 8 n + 2 (lane % 4) + e % 2.
+// A lane reads four of k at once: its elements 4 t .. 4 t + 3 stand for the products' k = t and t + 4, twice.
+template <int MB, int NT, int K, int AS, int BS>
+__device__ __forceinline__ void gemm(float (&acc)[MB][NT][4], const float* a, const float* b) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  a += g * AS + 4 * t;
+  b += g * BS + 4 * t;
+#pragma unroll 2
+  for (int k = 0; k < K; k += 16) {
+    float4 x[MB][2], y[NT];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) x[r] = *reinterpret_cast<const float4*>(a + r * AS + k);
+    for (int m = 0; m < MB; ++m) {
+      x[m][0] = *reinterpret_cast<const float4*>(a + 16 * m * AS + k);
+      x[m][1] = *reinterpret_cast<const float4*>(a + (16 * m + 8) * AS + k);
+    }
 #pragma unroll
-    for (int c = 0; c < NC; ++c) y[c] = *reinterpret_cast<const float4*>(b + c * BS + k);
+    for (int n = 0; n < NT; ++n) y[n] = *reinterpret_cast<const float4*>(b + 8 * n * BS + k);
+    float part[MB][NT][4] = {}, small[MB][NT][4] = {};  // (the tensor cores' sums are cut off, not rounded: short ones, added up in fp32)
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
+    for (int half = 0; half < 2; ++half) {
+      uint32_t ah[MB][4], al[MB][4], bh[NT][2], bl[NT][2];
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        acc[r][c] = fmaf(x[r].x, y[c].x, fmaf(x[r].y, y[c].y, fmaf(x[r].z, y[c].z, fmaf(x[r].w, y[c].w, acc[r][c]))));
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          two(half ? x[m][r].z : x[m][r].x, ah[m][r], al[m][r]);
+          two(half ? x[m][r].w : x[m][r].y, ah[m][2 + r], al[m][2 + r]);
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        two(half ? y[n].z : y[n].x, bh[n][0], bl[n][0]);
+        two(half ? y[n].w : y[n].y, bh[n][1], bl[n][1]);
+      }
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(small[m][n], al[m], bh[n]);
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(small[m][n], ah[m], bl[n]);
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma(part[m][n], ah[m], bh[n]);
+    }
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[m][n][e] += part[m][n][e] + small[m][n][e];
   }
 }
+// This thread's rows and columns of such a product whose warps stand in rows of `across`, each with 16 MB rows and 8 NT columns.
+template <int MB, int NT>
+struct Mine {
+  int warp_row, warp_col, g, t;
+  __device__ __forceinline__ explicit Mine(int across) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    warp_row = warp / across * 16 * MB;
+    warp_col = warp % across * 8 * NT;
+    g = lane / 4;
+    t = lane % 4;
+  }
+  __device__ __forceinline__ int row(int m, int e) const { return warp_row + 16 * m + g + 8 * (e / 2); }
+  __device__ __forceinline__ int col(int n, int e) const { return warp_col + 8 * n + 2 * t + e % 2; }
+};
 
 // ---- prep -------------------------------------------------------------------------------------
 constexpr int PREP_FLOATS = 2 * DC * KS + 2 * DC * CS;
@@ -177,18 +239,18 @@ __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArg
     ws[WS_GT + GT_E + tid] = delta_decay(sg[DC - 1], sg[tid]);
     ws[WS_GT + GT_B + tid] = sb[tid];
   }
-  const int ti = tid / 16, tj = tid % 16;
-  float kk[4][4] = {}, qk[4][4] = {};
-  gemm<4, 4, DK, K16, K16>(kk, sk + ti * KS, sk + tj * KS);
-  gemm<4, 4, DK, K16, K16>(qk, sq + ti * KS, sk + tj * KS);
+  const Mine<1, 4> my(2);
+  float kk[1][4][4] = {}, qk[1][4][4] = {};
+  gemm<1, 4, DK, KS, KS>(kk, sk + my.warp_row * KS, sk + my.warp_col * KS);
+  gemm<1, 4, DK, KS, KS>(qk, sq + my.warp_row * KS, sk + my.warp_col * KS);
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int i = ti + 16 * r, j = tj + 16 * c;
+    for (int e = 0; e < 4; ++e) {
+      const int i = my.row(0, e), j = my.col(c, e);
       const float d = j <= i ? delta_decay(sg[i], sg[j]) : 0.f;
-      ws[WS_P + i * DC + j] = j <= i ? d * qk[r][c] : 0.f;
-      const float x = j < i ? d * kk[r][c] : 0.f;
+      ws[WS_P + i * DC + j] = j <= i ? d * qk[0][c][e] : 0.f;
+      const float x = j < i ? d * kk[0][c][e] : 0.f;
       m[i * CS + j] = x;
       mb[i * CS + j] = x * sb[j];
     }
@@ -225,11 +287,12 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
     load_block<DK, SB, DV>(a.h0 + ((long long)from * a.H + h) * (DK * DV) + c0, [&](int x, int c, float4 v) { put_column<KS>(S + c * KS + x, v); });
   else
     for (int e = tid; e < SB * KS; e += THREADS) S[e] = 0.f;
-  const int ti = tid / 16, tj = tid % 16;  // rows ti + 16 r, columns tj + 16 c
+  const Mine<1, 2> my(2);  // of [64][32]
+  const Mine<3, 1> dk(4);  // of [96][32]
   // A chunk's inputs, fetched while the one before is computed.
   Rows<DK> k, q;
   Block<DC, DC, DC> z, p;
-  float v[4][2], f = 0.f;
+  float v[2][4], f = 0.f;
   auto fetch = [&](int c) {
     const int len = min(DC, s.len - c * DC);
     const long long t0 = s.begin + (long long)c * DC;
@@ -239,10 +302,14 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
     z.fetch(ws + WS_Z);
     if (!BWD) p.fetch(ws + WS_P);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        v[i][j] = ti + 16 * i < len ? ((const float*)a.v)[((t0 + ti + 16 * i) * a.H + h) * DV + c0 + tj + 16 * j] : 0.f;
+      for (int e = 0; e < 4; e += 2) {
+        float2 x = make_float2(0.f, 0.f);
+        if (my.row(0, e) < len) x = *reinterpret_cast<const float2*>((const float*)a.v + ((t0 + my.row(0, e)) * a.H + h) * DV + c0 + my.col(n, e));
+        v[n][e] = x.x;
+        v[n][e + 1] = x.y;
+      }
     if (tid < 3 * DC) f = ws[WS_GT + GT_F + tid];
   };
   if (s.len > 0) fetch(0);
@@ -259,63 +326,62 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
     if (!BWD) q.place([&](int i, int x, float4 y) { put_row(sq + i * KS + x, y); });
     z.place([&](int i, int j, float4 y) { put_row(sz + i * CS + j, y); });
     if (!BWD) p.place([&](int i, int j, float4 y) { put_row(sp + i * CS + j, y); });
-    float r[4][2];
+    float r[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) r[i][j] = v[i][j];
+      for (int e = 0; e < 4; ++e) r[n][e] = v[n][e];
     __syncthreads();
     if ((c + 1) * DC < s.len) fetch(c + 1);
     if (BWD)
       for (int e = tid; e < DK * SB; e += THREADS) ws[WS_S0 + e / SB * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
-    float ks[4][2] = {}, qs[4][2] = {};
-    gemm<4, 2, DK, K16, K16>(ks, sk + ti * KS, S + tj * KS);
-    if (!BWD) gemm<4, 2, DK, K16, K16>(qs, sq + ti * KS, S + tj * KS);
+    float ks[1][2][4] = {}, qs[1][2][4] = {};
+    gemm<1, 2, DK, KS, KS>(ks, sk + my.warp_row * KS, S + my.warp_col * KS);
+    if (!BWD) gemm<1, 2, DK, KS, KS>(qs, sq + my.warp_row * KS, S + my.warp_col * KS);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = ti + 16 * i;
-        r[i][j] = fmaf(-sf[row], ks[i][j], r[i][j]);
-        sr[(tj + 16 * j) * CS + row] = sf[2 * DC + row] * r[i][j];
+      for (int e = 0; e < 4; ++e) {
+        const int row = my.row(0, e);
+        r[n][e] = fmaf(-sf[row], ks[0][n][e], r[n][e]);
+        sr[my.col(n, e) * CS + row] = sf[2 * DC + row] * r[n][e];
       }
     __syncthreads();
-    float zr[4][2] = {};
-    gemm<4, 2, DC, I16, I16>(zr, sz + ti * CS, sr + tj * CS);
+    float zr[1][2][4] = {};
+    gemm<1, 2, DC, CS, CS>(zr, sz + my.warp_row * CS, sr + my.warp_col * CS);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = ti + 16 * i, col = tj + 16 * j;
-        const float x = r[i][j] - zr[i][j];
+      for (int e = 0; e < 4; ++e) {
+        const int row = my.row(0, e), col = my.col(n, e);
+        const float x = r[n][e] - zr[0][n][e];
         su[col * CS + row] = sf[2 * DC + row] * x;
         if (BWD) ws[WS_X + row * DV + c0 + col] = x;
       }
     __syncthreads();
     if (!BWD) {
-      float pu[4][2] = {};
-      gemm<4, 2, DC, I16, I16>(pu, sp + ti * CS, su + tj * CS);
+      float pu[1][2][4] = {};
+      gemm<1, 2, DC, CS, CS>(pu, sp + my.warp_row * CS, su + my.warp_col * CS);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = ti + 16 * i;
-          if (row < len)
-            ((float*)a.o)[((t0 + row) * a.H + h) * DV + c0 + tj + 16 * j] = a.scale * fmaf(sf[row], qs[i][j], pu[i][j]);
+        for (int e = 0; e < 4; ++e) {
+          const int row = my.row(0, e);
+          if (row < len) ((float*)a.o)[((t0 + row) * a.H + h) * DV + c0 + my.col(n, e)] = a.scale * fmaf(sf[row], qs[0][n][e], pu[0][n][e]);
         }
     }
     // e^(G_C - G) goes to U, which nothing else reads any more
     for (int e = tid; e < SB * DC; e += THREADS) sr[e / DC * CS + e % DC] = sf[DC + e % DC] * su[e / DC * CS + e % DC];
     __syncthreads();
-    float ds[6][2] = {};
-    gemm<6, 2, DC, I16, I16>(ds, st + ti * CS, sr + tj * CS);
+    float ds[3][1][4] = {};
+    gemm<3, 1, DC, CS, CS>(ds, st + dk.warp_row * CS, sr + dk.warp_col * CS);
     const float last = sf[DC - 1];
 #pragma unroll
-    for (int i = 0; i < 6; ++i)
+    for (int m = 0; m < 3; ++m)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float* const at = S + (tj + 16 * j) * KS + ti + 16 * i;  // (this thread's own, and nothing reads S here)
-        *at = fmaf(last, *at, ds[i][j]);
+      for (int e = 0; e < 4; ++e) {
+        float* const at = S + dk.col(0, e) * KS + dk.row(m, e);  // (this thread's own, and nothing reads S here)
+        *at = fmaf(last, *at, ds[m][0][e]);
       }
   }
   __syncthreads();
@@ -351,12 +417,13 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
     load_block<DK, SB, DV>(a.dhT + ((long long)n * a.H + h) * (DK * DV) + c0, [&](int x, int c, float4 v) { put_column<KS>(S + c * KS + x, v); });
   else
     for (int e = tid; e < SB * KS; e += THREADS) S[e] = 0.f;
-  const int ti = tid / 16, tj = tid % 16;
+  const Mine<1, 2> my(2);  // of [64][32]
+  const Mine<3, 1> dk(4);  // of [96][32]
   // A chunk's inputs, fetched while the one before is computed.
   Rows<DK> k, q;
   Rows<SB> d;
   Block<DC, DC, DC> z, p;
-  float xs[4][2], f = 0.f;
+  float xs[2][4], f = 0.f;
   auto fetch = [&](int c) {
     const int len = min(DC, s.len - c * DC);
     const long long t0 = s.begin + (long long)c * DC;
@@ -367,9 +434,13 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
     z.fetch(ws + WS_Z);
     p.fetch(ws + WS_P);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) xs[i][j] = ws[WS_X + (ti + 16 * i) * DV + c0 + tj + 16 * j];
+      for (int e = 0; e < 4; e += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(ws + WS_X + my.row(0, e) * DV + c0 + my.col(n, e));
+        xs[n][e] = x.x;
+        xs[n][e + 1] = x.y;
+      }
     if (tid < 3 * DC) f = ws[WS_GT + GT_F + tid];
   };
   const int nc = (s.len + DC - 1) / DC;
@@ -388,55 +459,57 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
     d.place([&](int i, int e, float4 y) { put_column<CS>(sd + e * CS + i, y); });
     z.place([&](int i, int j, float4 y) { put_column<CS>(szt + j * CS + i, y); });
     p.place([&](int i, int j, float4 y) { put_column<CS>(spt + j * CS + i, y); });
-    float x[4][2];
+    float x[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) x[i][j] = xs[i][j];
+      for (int e = 0; e < 4; ++e) x[n][e] = xs[n][e];
     __syncthreads();
     if (c > 0) fetch(c - 1);
     for (int e = tid; e < DK * SB; e += THREADS) ws[WS_DS + e / SB * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
-    float kd[4][2] = {}, pd[4][2] = {}, du[4][2];
-    gemm<4, 2, DK, K16, K16>(kd, sk + ti * KS, S + tj * KS);
-    gemm<4, 2, DC, I16, I16>(pd, spt + ti * CS, sd + tj * CS);
+    float kd[1][2][4] = {}, pd[1][2][4] = {}, du[2][4];
+    gemm<1, 2, DK, KS, KS>(kd, sk + my.warp_row * KS, S + my.warp_col * KS);
+    gemm<1, 2, DC, CS, CS>(pd, spt + my.warp_row * CS, sd + my.warp_col * CS);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = ti + 16 * i;
-        du[i][j] = fmaf(sf[DC + row], kd[i][j], a.scale * pd[i][j]);
-        sw[(tj + 16 * j) * CS + row] = sf[2 * DC + row] * du[i][j];
+      for (int e = 0; e < 4; ++e) {
+        const int row = my.row(0, e);
+        du[n][e] = fmaf(sf[DC + row], kd[0][n][e], a.scale * pd[0][n][e]);
+        sw[my.col(n, e) * CS + row] = sf[2 * DC + row] * du[n][e];
       }
     __syncthreads();
-    float zw[4][2] = {}, part[4] = {};
-    gemm<4, 2, DC, I16, I16>(zw, szt + ti * CS, sw + tj * CS);
+    float zw[1][2][4] = {}, part[2] = {};
+    gemm<1, 2, DC, CS, CS>(zw, szt + my.warp_row * CS, sw + my.warp_col * CS);
     for (int e = tid; e < SB * DC; e += THREADS) sd[e / DC * CS + e % DC] *= a.scale * sf[e % DC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = ti + 16 * i;
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = tj + 16 * j;
-        const float dut = du[i][j] - zw[i][j], dr = sf[2 * DC + row] * dut;
-        part[i] = fmaf(dut, x[i][j], part[i]);
+      for (int e = 0; e < 4; ++e) {
+        const int row = my.row(0, e), col = my.col(n, e);
+        const float dut = du[n][e] - zw[0][n][e], dr = sf[2 * DC + row] * dut;
+        part[e / 2] = fmaf(dut, x[n][e], part[e / 2]);
         if (row < len) ((float*)a.dv)[((t0 + row) * a.H + h) * DV + c0 + col] = dr;
         sn[col * CS + row] = -sf[row] * dr;
       }
 #pragma unroll
-      for (int off = 8; off > 0; off >>= 1) part[i] += __shfl_xor_sync(0xffffffffu, part[i], off);
-      if (tj == 0 && row < len) dbeta_part[((long long)tile * tokens + t0 + row) * a.H + h] = part[i];
+    for (int i = 0; i < 2; ++i) {
+      part[i] += __shfl_xor_sync(0xffffffffu, part[i], 1);
+      part[i] += __shfl_xor_sync(0xffffffffu, part[i], 2);
+      const int row = my.row(0, 2 * i);
+      if (my.t == 0 && row < len) dbeta_part[((long long)(2 * tile + (my.warp_col > 0)) * tokens + t0 + row) * a.H + h] = part[i];
     }
     __syncthreads();
-    float ds[6][2] = {};
-    gemm<6, 2, DC, I16, I16>(ds, sqt + ti * CS, sd + tj * CS);
-    gemm<6, 2, DC, I16, I16>(ds, skt + ti * CS, sn + tj * CS);
+    float ds[3][1][4] = {};
+    gemm<3, 1, DC, CS, CS>(ds, sqt + dk.warp_row * CS, sd + dk.warp_col * CS);
+    gemm<3, 1, DC, CS, CS>(ds, skt + dk.warp_row * CS, sn + dk.warp_col * CS);
     const float last = sf[DC - 1];
 #pragma unroll
-    for (int i = 0; i < 6; ++i)
+    for (int m = 0; m < 3; ++m)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float* const at = S + (tj + 16 * j) * KS + ti + 16 * i;
-        *at = fmaf(last, *at, ds[i][j]);
+      for (int e = 0; e < 4; ++e) {
+        float* const at = S + dk.col(0, e) * KS + dk.row(m, e);
+        *at = fmaf(last, *at, ds[m][0][e]);
       }
   }
   __syncthreads();
@@ -452,7 +525,7 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
 // of d_v: dO, dR, U [64][36], S0, dS1 [48][36], the next piece's loads in flight; then Es, Fm and their transposes
 // [64][68] in their place.  K and Q [64][52], K^T and Q^T [48][68].
 constexpr int HK = DK / 2, HS = HK + 4;
-constexpr int PIECES = 3 * DC * BS + 2 * HK * BS, GRAD_FLOATS = 2 * DC * HS + 2 * HK * CS + (PIECES > 4 * DC * CS ? PIECES : 4 * DC * CS) + 2 * DC + 8;
+constexpr int PIECES = 3 * DC * BS + 2 * HK * BS, GRAD_FLOATS = 2 * DC * HS + 2 * HK * CS + (PIECES > 4 * DC * CS ? PIECES : 4 * DC * CS) + 4 * DC + 8;
 
 __device__ __forceinline__ uint32_t peer_of(const float* at, uint32_t rank) {
   uint32_t r;
@@ -476,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
   float* const su = sdr + DC * BS;
   float* const ss = su + DC * BS;
   float* const sd = ss + HK * BS;
-  float* const sdg = sm + GRAD_FLOATS - 2 * DC - 8;  // [2][64] dG of the two CTAs' columns; [2] what hangs on G_C
+  float* const sdg = sm + GRAD_FLOATS - 4 * DC - 8;  // [4][64] dG of two CTAs' columns, by halves; [2] what hangs on G_C
   __shared__ float red[THREADS / 32];
   const int unit = blockIdx.x / 2, rank = blockIdx.x % 2, slot = unit / a.H, h = unit % a.H, tid = threadIdx.x, x0 = rank * HK;
   const DeltaChunk ch = chunk_of_slot(a, slot);
@@ -506,8 +579,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
     put_row(sq + i * HS + c, v);
     put_column<CS>(sqt + c * CS + i, v);
   });
-  const int ti = tid / 16, tj = tid % 16, i0 = rank * (DC / 2) + ti;  // rows i0, i0 + 16 of Es and Fm
-  float dp[2][4] = {}, dm[2][4] = {}, dqi[4][3] = {}, dkr[4][3] = {}, dks[4][3] = {}, frob = 0.f;
+  const Mine<1, 2> pair(4);  // of [32][64]: rows i0 .. of Es and Fm
+  const Mine<1, 3> my(2);    // of [64][48]
+  const int i0 = rank * (DC / 2);
+  float dp[1][2][4] = {}, dm[1][2][4] = {}, dqi[1][3][4] = {}, dkr[1][3][4] = {}, dks[1][3][4] = {}, frob = 0.f;
   for (int c0 = 0; c0 < DV; c0 += SB) {
     __syncthreads();
     pdo.place([&](int i, int c, float4 v) { put_row(sdo + i * BS + c, v); });
@@ -521,11 +596,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
     __syncthreads();
     if (c0 + SB < DV) fetch(c0 + SB);
     for (int e = tid; e < HK * SB; e += THREADS) frob = fmaf(ss[e / SB * BS + e % SB], sd[e / SB * BS + e % SB], frob);
-    gemm<2, 4, SB, B16, B16>(dp, sdo + i0 * BS, su + tj * BS);
-    gemm<2, 4, SB, B16, B16>(dm, sdr + i0 * BS, su + tj * BS);
-    gemm<4, 3, SB, B16, B16>(dqi, sdo + ti * BS, ss + tj * BS);
-    gemm<4, 3, SB, B16, B16>(dkr, sdr + ti * BS, ss + tj * BS);
-    gemm<4, 3, SB, B16, B16>(dks, su + ti * BS, sd + tj * BS);
+    gemm<1, 2, SB, BS, BS>(dp, sdo + (i0 + pair.warp_row) * BS, su + pair.warp_col * BS);
+    gemm<1, 2, SB, BS, BS>(dm, sdr + (i0 + pair.warp_row) * BS, su + pair.warp_col * BS);
+    gemm<1, 3, SB, BS, BS>(dqi, sdo + my.warp_row * BS, ss + my.warp_col * BS);
+    gemm<1, 3, SB, BS, BS>(dkr, sdr + my.warp_row * BS, ss + my.warp_col * BS);
+    gemm<1, 3, SB, BS, BS>(dks, su + my.warp_row * BS, sd + my.warp_col * BS);
   }
   cluster_sync();  // (neither reads its pieces any more)
   float* const es = sdo;              // [64][68] Es, Fm, and their transposes
@@ -534,12 +609,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
   float* const fmt = est + DC * CS;
   const uint32_t peer = peer_of(es, rank ^ 1);
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int i = i0 + 16 * r, j = tj + 16 * c;
+      const int i = i0 + pair.row(0, c), j = pair.col(n, c);
       const float d = j <= i ? delta_decay(make_float2(gt[GT_HI + i], gt[GT_LO + i]), make_float2(gt[GT_HI + j], gt[GT_LO + j])) : 0.f;
-      const float e = j <= i ? a.scale * d * dp[r][c] : 0.f, f = j < i ? -d * dm[r][c] : 0.f;
+      const float e = j <= i ? a.scale * d * dp[0][n][c] : 0.f, f = j < i ? -d * dm[0][n][c] : 0.f;
       const int at = i * CS + j, att = 2 * DC * CS + j * CS + i;
       es[at] = es[att] = e;
       fm[at] = fm[att] = f;
@@ -549,34 +624,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
       put_peer(peer + 4 * (DC * CS + att), f);
     }
   cluster_sync();
-  float q1[4][3] = {}, k1[4][3] = {}, k2[4][3] = {};  // Es K;  Es^T Q + Fm^T K;  Fm K
-  gemm<4, 3, DC, I16, I16>(q1, es + ti * CS, skt + tj * CS);
-  gemm<4, 3, DC, I16, I16>(k1, est + ti * CS, sqt + tj * CS);
-  gemm<4, 3, DC, I16, I16>(k1, fmt + ti * CS, skt + tj * CS);
-  gemm<4, 3, DC, I16, I16>(k2, fm + ti * CS, skt + tj * CS);
+  float q1[1][3][4] = {}, k1[1][3][4] = {}, k2[1][3][4] = {};  // Es K;  Es^T Q + Fm^T K;  Fm K
+  gemm<1, 3, DC, CS, CS>(q1, es + my.warp_row * CS, skt + my.warp_col * CS);
+  gemm<1, 3, DC, CS, CS>(k1, est + my.warp_row * CS, sqt + my.warp_col * CS);
+  gemm<1, 3, DC, CS, CS>(k1, fmt + my.warp_row * CS, skt + my.warp_col * CS);
+  gemm<1, 3, DC, CS, CS>(k2, fm + my.warp_row * CS, skt + my.warp_col * CS);
   const uint32_t first = peer_of(sdg, 0);
   float at_end = 0.f;  // sum_j k_j . (e^(G_C - G_j) dS1 u_j), this thread's part
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = ti + 16 * r;
+  for (int r = 0; r < 2; ++r) {
+    const int i = my.row(0, 2 * r);
     const float f = gt[GT_F + i], e = gt[GT_E + i];
     float dg = 0.f;
 #pragma unroll
-    for (int c = 0; c < 3; ++c) {
-      const int x = tj + 16 * c;
-      const float q = sq[i * HS + x], k = sk[i * HS + x];
-      const float dq = fmaf(a.scale * f, dqi[r][c], q1[r][c]);
-      const float minus = fmaf(e, dks[r][c], k1[r][c]), plus = fmaf(-f, dkr[r][c], k2[r][c]);
-      at_end = fmaf(k, e * dks[r][c], at_end);
-      dg = fmaf(q, dq, fmaf(k, plus - minus, dg));
+    for (int n = 0; n < 3; ++n) {
+      float dq[2], dk[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int c = 2 * r + x, col = my.col(n, c);
+        const float q = sq[i * HS + col], k = sk[i * HS + col];
+        dq[x] = fmaf(a.scale * f, dqi[0][n][c], q1[0][n][c]);
+        const float minus = fmaf(e, dks[0][n][c], k1[0][n][c]), plus = fmaf(-f, dkr[0][n][c], k2[0][n][c]);
+        dk[x] = minus + plus;
+        at_end = fmaf(k, e * dks[0][n][c], at_end);
+        dg = fmaf(q, dq[x], fmaf(k, plus - minus, dg));
+      }
       if (i < ch.len) {
-        ((float*)a.dq)[((ch.t0 + i) * a.H + h) * DK + x0 + x] = dq;
-        ((float*)a.dk)[((ch.t0 + i) * a.H + h) * DK + x0 + x] = minus + plus;
+        const long long at = ((ch.t0 + i) * a.H + h) * DK + x0 + my.col(n, 0);
+        *reinterpret_cast<float2*>((float*)a.dq + at) = make_float2(dq[0], dq[1]);
+        *reinterpret_cast<float2*>((float*)a.dk + at) = make_float2(dk[0], dk[1]);
       }
     }
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) dg += __shfl_xor_sync(0xffffffffu, dg, off);
-    if (tj == 0) put_peer(first + 4 * (rank * DC + i), dg);
+    dg += __shfl_xor_sync(0xffffffffu, dg, 1);
+    dg += __shfl_xor_sync(0xffffffffu, dg, 2);
+    if (my.t == 0) put_peer(first + 4 * ((2 * rank + (my.warp_col > 0)) * DC + i), dg);
   }
   at_end = fmaf(gt[GT_F + DC - 1], frob, at_end);
 #pragma unroll
@@ -587,12 +668,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
     float end = 0.f;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) end += red[w];
-    put_peer(first + 4 * (2 * DC + rank), end);
+    put_peer(first + 4 * (4 * DC + rank), end);
   }
   cluster_sync();  // (after it the second CTA touches only its own memory)
   if (rank == 0 && tid < 32) {  // dg_t = the sum of dG_i over i >= t, and of what hangs on G_C
-    const float end = sdg[2 * DC] + sdg[2 * DC + 1];
-    const float lo = sdg[2 * tid] + sdg[DC + 2 * tid], hi = sdg[2 * tid + 1] + sdg[DC + 2 * tid + 1];
+    const float end = sdg[4 * DC] + sdg[4 * DC + 1];
+    float lo = 0.f, hi = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      lo += sdg[x * DC + 2 * tid];
+      hi += sdg[x * DC + 2 * tid + 1];
+    }
     float run = lo + hi;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -607,7 +693,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
     const long long t = ch.t0 + tid;
     float b = 0.f;
 #pragma unroll
-    for (int x = 0; x < SNB; ++x) b += dbeta_part[((long long)x * tokens + t) * a.H + h];
+    for (int x = 0; x < 2 * SNB; ++x) b += dbeta_part[((long long)x * tokens + t) * a.H + h];
     ((float*)a.dbeta)[t * a.H + h] = b;
   }
 }
@@ -633,7 +719,7 @@ cudaError_t allow_all() {
 }  // namespace
 
 size_t delta_simt_ws_bytes(long long slots, long long tokens, int H, bool bwd) {
-  return (size_t)slots * H * (bwd ? WS_BWD : WS_FWD) * 4 + (bwd ? (size_t)SNB * tokens * H * 4 : 0);
+  return (size_t)slots * H * (bwd ? WS_BWD : WS_FWD) * 4 + (bwd ? (size_t)2 * SNB * tokens * H * 4 : 0);
 }
 
 cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t st) {
