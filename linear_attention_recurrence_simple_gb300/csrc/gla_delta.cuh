@@ -178,27 +178,6 @@ __device__ __forceinline__ void delta_sums(float x0, float x1, float2& s0, float
 __device__ __forceinline__ float delta_decay(float2 gi, float2 gj) { return expf((gi.x - gj.x) + (gi.y - gj.y)); }
 __device__ __forceinline__ float delta_decay0(float2 gi) { return expf(gi.x + gi.y); }
 
-// Z = (1 + M B)^-1 M by forward substitution, one thread a column: z_i = M_ic - sum_{j < i} (M B)_ij z_j.
-// `m` and `mb` are [64][stride] in shared memory, zero on and above the diagonal; rows 16-byte aligned.
-template <int STRIDE>
-__device__ __forceinline__ void delta_solve_column(const float* m, const float* mb, int c, float (&z)[DC]) {
-#pragma unroll
-  for (int i = 0; i < DC; ++i) z[i] = 0.f;
-#pragma unroll
-  for (int i = 1; i < DC; ++i) {
-    float s0 = c < i ? m[i * STRIDE + c] : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-    for (int j = 0; j < i; j += 4) {
-      const float4 w = *reinterpret_cast<const float4*>(mb + i * STRIDE + j);
-      s0 = fmaf(-w.x, z[j], s0);
-      if (j + 1 < i) s1 = fmaf(-w.y, z[j + 1], s1);
-      if (j + 2 < i) s2 = fmaf(-w.z, z[j + 2], s2);
-      if (j + 3 < i) s3 = fmaf(-w.w, z[j + 3], s3);
-    }
-    z[i] = (s0 + s1) + (s2 + s3);
-  }
-}
-
 int current_device_state(unsigned** err, unsigned long long* wait_ns);
 cudaError_t launch_delta_simt_fwd(const DeltaArgs& a, cudaStream_t stream);
 cudaError_t launch_delta_simt_bwd(const DeltaArgs& a, cudaStream_t stream);

@@ -1,16 +1,19 @@
-// The gated delta rule in fp32 on the CUDA cores (the all-fp32 mode).
+// The gated delta rule in fp32 (the all-fp32 mode).
 //
 // Four kernels, see gla_delta.cuh for the formulas:
 //   prep    one CTA a (chunk, head): decays, P, M and the triangular system's Z
 //   scan    one CTA a (sequence, head, 32 columns of d_v): the chunks in order; columns of S never meet, so the
 //           tiles are independent.  In the backward it keeps each chunk's S0 and X instead of writing o
 //   rscan   the same in reverse for dS; writes dv, dS1 of every chunk and its columns' part of dbeta
-//   grads   one CTA a (chunk, head): dq, dk, dg, and dbeta's parts summed in tile order
-// The operands of a product stand in shared memory with the summed index contiguous (where both ways are needed,
-// twice), so that a thread reads four of its steps at once: rows of 4 mod 32 words apart, free of bank conflicts.
-// Every thread has a small tile of the result in registers.  A chunk's loads go out together, in vectors, while the chunk
-// before it is computed (2 sequences of up to 150 tokens x 4 heads: scan 26 -> 25 us, rscan 44 -> 42, 14 us a chunk).  Bound by the reads
-// from shared memory (a 4 x 2 tile takes six vectors for 32 FMAs), short calls also by their few CTAs.
+//   grads   two CTAs a (chunk, head): dq, dk, dg, and dbeta's parts summed in tile order
+// States, sums and everything between products are fp32.  The products are three of tf32 each (mma.sync): an operand keeps 22
+// bits, sums are of 16 terms in the tensor cores, which cut them off, and of those in fp32: 1.8e-7 of the norm from the exact
+// result, against 2.4e-7 with FMAs throughout and 1.5e-6 with the tensor cores' sums over all terms.  With FMAs the reads
+// from shared memory were the bound (a 4 x 2 tile of a thread takes six vectors for 32 FMAs): 2 sequences of up to 150 tokens x
+// 4 heads, scan 24 -> 22 us, rscan 36 -> 33, grads 49 -> 30; backward 117 -> 95.
+// Operands stand in shared memory with the summed index contiguous (where both ways are needed, twice).  A chunk's loads go
+// out together, in vectors, while the chunk before it is computed.  Bound by latency: eight warps an SM, and short calls have
+// few CTAs.
 #include "gla_delta.cuh"
 #include "gla_once.cuh"
 
@@ -128,12 +131,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const
 // acc += sum_k A[row * AS + k] B[col * BS + k] over the warp's MB blocks of 16 rows from `a` on and NT of 8 columns from `b` on,
 // each product in three of tf32.  acc[m][n][e]: row 16 m + lane / 4 + 8 (e / 2), column 8 n + 2 (lane % 4) + e % 2.
 // A lane reads four of k at once: its elements 4 t .. 4 t + 3 stand for the products' k = t and t + 4, twice.
-template <int MB, int NT, int K, int AS, int BS>
+template <int MB, int NT, int K, int AS, int BS, int UNROLL = 2>
 __device__ __forceinline__ void gemm(float (&acc)[MB][NT][4], const float* a, const float* b) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
   a += g * AS + 4 * t;
   b += g * BS + 4 * t;
-#pragma unroll 2
+#pragma unroll UNROLL
   for (int k = 0; k < K; k += 16) {
     float4 x[MB][2], y[NT];
 #pragma unroll
@@ -241,8 +244,8 @@ __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArg
   }
   const Mine<1, 4> my(2);
   float kk[1][4][4] = {}, qk[1][4][4] = {};
-  gemm<1, 4, DK, KS, KS>(kk, sk + my.warp_row * KS, sk + my.warp_col * KS);
-  gemm<1, 4, DK, KS, KS>(qk, sq + my.warp_row * KS, sk + my.warp_col * KS);
+  gemm<1, 4, DK, KS, KS, 1>(kk, sk + my.warp_row * KS, sk + my.warp_col * KS);
+  gemm<1, 4, DK, KS, KS, 1>(qk, sq + my.warp_row * KS, sk + my.warp_col * KS);
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -256,10 +259,39 @@ __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArg
     }
   __syncthreads();
   if (tid < DC) {
-    float z[DC];
-    delta_solve_column<CS>(m, mb, tid, z);
+    // Z = (1 + M B)^-1 M by forward substitution, a thread a column, 16 rows at a time: z_i = M_ic - sum_{j < i} (M B)_ij z_j.
+    // (Loops over the blocks: written out, the code takes longer to be fetched than to run: prep 17 us instead of 13.)
+    float* const z = sq;  // [64][64], Q is done with
+#pragma unroll 1
+    for (int b = 0; b < DC; b += 16) {
+      float y[16];
 #pragma unroll
-    for (int i = 0; i < DC; ++i) ws[WS_Z + i * DC + tid] = z[i];
+      for (int r = 0; r < 16; ++r) y[r] = m[(b + r) * CS + tid];
+#pragma unroll 1
+      for (int j = 0; j < b; j += 4) {
+        const float z0 = z[j * DC + tid], z1 = z[(j + 1) * DC + tid], z2 = z[(j + 2) * DC + tid], z3 = z[(j + 3) * DC + tid];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float4 w = *reinterpret_cast<const float4*>(mb + (b + r) * CS + j);
+          y[r] = fmaf(-w.w, z3, fmaf(-w.z, z2, fmaf(-w.y, z1, fmaf(-w.x, z0, y[r]))));
+        }
+      }
+#pragma unroll
+      for (int r = 1; r < 16; ++r)
+#pragma unroll
+        for (int j = 0; j < r; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(mb + (b + r) * CS + b + j);
+          y[r] = fmaf(-w.x, y[j], y[r]);
+          if (j + 1 < r) y[r] = fmaf(-w.y, y[j + 1], y[r]);
+          if (j + 2 < r) y[r] = fmaf(-w.z, y[j + 2], y[r]);
+          if (j + 3 < r) y[r] = fmaf(-w.w, y[j + 3], y[r]);
+        }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        z[(b + r) * DC + tid] = y[r];
+        ws[WS_Z + (b + r) * DC + tid] = y[r];
+      }
+    }
   }
 }
 
