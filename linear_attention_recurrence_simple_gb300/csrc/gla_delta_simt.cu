@@ -295,6 +295,14 @@ __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArg
   }
 }
 
+// The state's columns (as rows of S) to rows of DV: a warp has four rows x 32 bytes, as a compromise between both sides' orders.
+__device__ __forceinline__ void store_state(const float* S, float* to) {
+  for (int e = threadIdx.x; e < DK * SB; e += THREADS) {
+    const int c = e / 32 % 4 * 8 + e % 8, x = e / 128 * 4 + e % 32 / 8;
+    to[x * DV + c] = S[c * KS + x];
+  }
+}
+
 // ---- forward scan ---------------------------------------------------------------------------
 constexpr int SCAN_FLOATS = SB * KS + 2 * DC * KS + DK * CS + 2 * DC * CS + 2 * SB * CS + 3 * DC;
 
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
     __syncthreads();
     if ((c + 1) * DC < s.len) fetch(c + 1);
     if (BWD)
-      for (int e = tid; e < DK * SB; e += THREADS) ws[WS_S0 + e / SB * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
+      store_state(S, ws + WS_S0 + c0);
     float ks[1][2][4] = {}, qs[1][2][4] = {};
     gemm<1, 2, DK, KS, KS>(ks, sk + my.warp_row * KS, S + my.warp_col * KS);
     if (!BWD) gemm<1, 2, DK, KS, KS>(qs, sq + my.warp_row * KS, S + my.warp_col * KS);
@@ -420,8 +428,7 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
   if (!BWD && a.hT) {
     const int to = delta_row(a.hT_row, a.hT_rows, n, a.err);
     if (to >= 0)
-      for (int e = tid; e < DK * SB; e += THREADS)
-        a.hT[(((long long)to * a.H + h) * DK + e / SB) * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
+      store_state(S, a.hT + ((long long)to * a.H + h) * (DK * DV) + c0);
   }
 }
 
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
       for (int e = 0; e < 4; ++e) x[n][e] = xs[n][e];
     __syncthreads();
     if (c > 0) fetch(c - 1);
-    for (int e = tid; e < DK * SB; e += THREADS) ws[WS_DS + e / SB * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
+    store_state(S, ws + WS_DS + c0);
     float kd[1][2][4] = {}, pd[1][2][4] = {}, du[2][4];
     gemm<1, 2, DK, KS, KS>(kd, sk + my.warp_row * KS, S + my.warp_col * KS);
     gemm<1, 2, DC, CS, CS>(pd, spt + my.warp_row * CS, sd + my.warp_col * CS);
@@ -546,8 +553,7 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
   }
   __syncthreads();
   if (a.dh0)
-    for (int e = tid; e < DK * SB; e += THREADS)
-      a.dh0[(((long long)n * a.H + h) * DK + e / SB) * DV + c0 + e % SB] = S[e % SB * KS + e / SB];
+    store_state(S, a.dh0 + ((long long)n * a.H + h) * (DK * DV) + c0);
 }
 
 // ---- gradients of the chunk ------------------------------------------------------------------
