@@ -448,6 +448,7 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
  * T are clamped and record GLA_ERR_SHAPE.
  * bf16 calls hold what carries a state from chunk to chunk in fp32 and in pairs of bf16 (16 bits: hT and dh0 are 3 to
  * 5e-6 of the norm from the exact ones); what only feeds an output of dtype bf16 may be rounded to bf16 once more.
+ * fp32 calls keep 22 bits of each operand of a product, and everything else in fp32 (2 to 4e-7 of the norm).
  * Sizes: chunk places (n_seq * ceil(T / 64); packed T_total / 64 + n_seq) * H * 96, and rows of h0
  * and hT * H * 96, below 2^31, else GLA_ERR_SHAPE.
  * Calls may be captured into a graph after a first call of the same kind on the device; calls that may overlap need

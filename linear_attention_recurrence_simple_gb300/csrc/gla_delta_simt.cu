@@ -10,7 +10,8 @@
 // bits, sums are of 16 terms in the tensor cores, which cut them off, and of those in fp32: 1.8e-7 of the norm from the exact
 // result, against 2.4e-7 with FMAs throughout and 1.5e-6 with the tensor cores' sums over all terms.  With FMAs the reads
 // from shared memory were the bound (a 4 x 2 tile of a thread takes six vectors for 32 FMAs): 2 sequences of up to 150 tokens x
-// 4 heads, scan 24 -> 22 us, rscan 36 -> 33, grads 49 -> 30; backward 117 -> 95.
+// 4 heads, scan 24 -> 22 us, rscan 36 -> 33, grads 49 -> 30; backward 117 -> 95 (with what came after, prep 13, scan 21, rscan
+// 31, grads 30; 90).
 // Operands stand in shared memory with the summed index contiguous (where both ways are needed, twice).  A chunk's loads go
 // out together, in vectors, while the chunk before it is computed.  Bound by latency: eight warps an SM, and short calls have
 // few CTAs.
@@ -558,8 +559,7 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
 
 // ---- gradients of the chunk ------------------------------------------------------------------
 // A cluster of two CTAs a (chunk, head), each with 32 rows of Es and Fm, which both need whole and write to each other,
-// and with 48 columns of d_k: short calls have few chunks (2 sequences of up to 150 tokens, 4 heads: 68 us with one CTA, 47.5
-// with two; bound by shared memory, two vectors read for every five or six FMAs a lane).  Pieces of 32 columns
+// and with 48 columns of d_k: short calls have few chunks (one CTA took 1.4 times as long).  Pieces of 32 columns
 // of d_v: dO, dR, U [64][36], S0, dS1 [48][36], the next piece's loads in flight; then Es, Fm and their transposes
 // [64][68] in their place.  K and Q [64][52], K^T and Q^T [48][68].
 constexpr int HK = DK / 2, HS = HK + 4;

@@ -206,8 +206,8 @@ static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_X % 32 
 //      product hi hi + hi lo + lo hi
 // fp32 sums; what is carried from block to block has 16 bits.
 // Bound by the latency of its chain (loads, products, a substitution of 16 steps, four of blocks) at 16 (backward 12) warps
-// an SM, held there by 124 (151) registers and 54 (64) KB: 8 sequences of 2,048 tokens x 16 heads, 4,096 CTAs, 69 us
-// (141), of which the bytes written take 20 (64).  With the products on tcgen05 and one thread a row of the substitution
+// an SM, held there by 128 (156) registers and 54 (64) KB: 8 sequences of 2,048 tokens x 16 heads, 4,096 CTAs, 70 us
+// (131), of which the bytes written take 20 (64).  With the products on tcgen05 and one thread a row of the substitution
 // 137.
 constexpr int PREP_THREADS = 128;
 struct PrepSmem {
@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 // 512 threads, one CTA an SM (the operands take 214 KB): warps 0-7 have the state's rows (0-95; columns as in the scan),
 // warps 8-15 the tokens' (64-127: other schedulers), so that neither waits for what the other writes out; of the warps
 // that have no rows, 8 issues the products and 12 the copies.  Every hand-over through an mbarrier.
-// Bound as the scan, 4,700 cycles a chunk: 8 x 2,048 tokens x 16 heads 210 us, 384 CTAs on 152 places; HBM 49 % busy;
+// Bound as the scan, 4,700 cycles a chunk: 8 x 2,048 tokens x 16 heads 214 us, 384 CTAs on 152 places; HBM 49 % busy;
 // with the products in the order of the formulas 242 us; in parts, as above, 248.
 // Tensor memory: P^T dO [0,64), Q~ dO [64,128), K dS1 [128,256) and K~ w [256,384) as [hi | lo], Z^T w [384,448).
 constexpr int RSCAN_THREADS = 512;
