@@ -207,7 +207,7 @@ static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_X % 32 
 // fp32 sums; what is carried from block to block has 16 bits.
 // Bound by the latency of its chain (loads, products, a substitution of 16 steps, four of blocks) at 16 (backward 12) warps
 // an SM, held there by 128 (156) registers and 54 (64) KB: 8 sequences of 2,048 tokens x 16 heads, 4,096 CTAs, 70 us
-// (131), of which the bytes written take 20 (64).  With the products on tcgen05 and one thread a row of the substitution
+// (128), of which the bytes written take 20 (64).  With the products on tcgen05 and one thread a row of the substitution
 // 137.
 constexpr int PREP_THREADS = 128;
 struct PrepSmem {
@@ -345,7 +345,7 @@ __device__ __forceinline__ void transposed_slab(float (&r)[4][2][4], uint32_t sb
 }
 
 template <bool BWD>
-__global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a) {
+__global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, int ahead) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   float* const dm = reinterpret_cast<float*>(sm + PrepSmem::DM);   // [4][16][20]: diagonal blocks of -B M, and of -B M^T
@@ -386,6 +386,27 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
     load_kq(maps, sb + PrepSmem::P0, sb + PrepSmem::P1, bar, h, (int)ch.t0);
+  }
+  if (!BWD && warp == 3 && blockIdx.x + (unsigned)ahead < gridDim.x) {
+    // What a CTA that comes when this one is done will read, into L2: the gates' latency is the start of its chain (8 x 2,048
+    // tokens x 16 heads: 71.7 -> 70.2 us; with the backward's three CTAs an SM and its stores 128 -> 130).
+    const unsigned unit = blockIdx.x + ahead;
+    const int h2 = unit % a.H;
+    const DeltaChunk later = chunk_of_slot(a, unit / a.H);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (2 * lane + e < later.len) {
+        const long long at = (later.t0 + 2 * lane + e) * a.H + h2;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"((const __nv_bfloat16*)a.g + at));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"((const __nv_bfloat16*)a.beta + at));
+      }
+    if (lane == 0 && later.len > 0) {
+      box_prefetch(&maps.k0, 0, h2, (int)later.t0);
+      box_prefetch(&maps.q0, 0, h2, (int)later.t0);
+      box_prefetch(&maps.k1, 64, h2, (int)later.t0);
+      box_prefetch(&maps.q1, 64, h2, (int)later.t0);
+    }
+    __syncwarp();
   }
   if (warp == 1) {
     const __nv_bfloat16* gp = (const __nv_bfloat16*)a.g + ch.t0 * a.H + h;
@@ -490,7 +511,7 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
         for (int e = 0; e < 4; ++e) {
           const int j = 8 * n + 2 * t + (e & 1);
           x[n][e] = -sbeta[16 * b + j] * r[1][b][n][e];
-          if (b == warp) dm[DM_FLOATS + (b * 16 + j) * 20 + g + 8 * (e >> 1)] = x[n][e];
+          if (b == warp) dm[DM_FLOATS + (b * 16 + 15 - j) * 20 + 15 - (g + 8 * (e >> 1))] = x[n][e];
         }
       if (b != warp) put_frag(x, 10 + frag_off(warp, b));
     }
@@ -524,29 +545,25 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     }
   }
   __syncthreads();
-  // 2: warp b, lane i < 16: row i of the inverse of diagonal block b (lanes 16 on: of B M^T's)
+  // 2: warp b, lane i < 16: row i of the inverse of diagonal block b.  Lanes 16 on: of B M^T's, which stands there in the
+  // opposite order of rows and columns, so that all lanes run the same.
   if (lane < (BWD ? 32 : 16)) {
-    const bool up = lane >= 16;
+    const bool up = BWD && lane >= 16;
     const int i = lane & 15;
     const float* const x = dm + (up ? DM_FLOATS : 0) + warp * 320;
     float y[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) y[j] = j == i ? 1.f : 0.f;
-    if (!up) {
 #pragma unroll
-      for (int m = 15; m > 0; --m)
+    for (int m = 15; m > 0; --m)
 #pragma unroll
-        for (int j = 0; j < m; ++j) y[j] = fmaf(y[m], x[m * 20 + j], y[j]);
-    } else if (BWD) {
-#pragma unroll
-      for (int m = 0; m < 15; ++m)
-#pragma unroll
-        for (int j = m + 1; j < 16; ++j) y[j] = fmaf(y[m], x[m * 20 + j], y[j]);
-    }
+      for (int j = 0; j < m; ++j) y[j] = fmaf(y[m], x[m * 20 + j], y[j]);
     __nv_bfloat16* const f = reinterpret_cast<__nv_bfloat16*>(frags + 1024 * ((up ? 10 : 0) + frag_diag(warp)));
+    const int flip = up ? 15 : 0, k = i ^ flip;  // (15 - i is i ^ 15)
+    const int at_k = (((k & 7) >> 1) * 4 + (k >> 3)) * 2 + (k & 1);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {  // operand element (k = i, n = j)
-      const int at = (((j & 7) * 4 + ((i & 7) >> 1)) * 4 + (j >> 3) * 2 + (i >> 3)) * 2 + (i & 1);
+    for (int j = 0; j < 16; ++j) {  // operand element (k, n)
+      const int n = j ^ flip, at = (n & 7) * 32 + (n >> 3) * 4 + at_k;
       const __nv_bfloat16 v = __float2bfloat16_rn(y[j]);
       f[at] = v;
       f[256 + at] = __float2bfloat16_rn(y[j] - __bfloat162float(v));
@@ -1693,7 +1710,7 @@ cudaError_t launch_delta_tc_fwd(DeltaArgs a, cudaStream_t st) {
   if (some && a.cu_seqlens && a.n_seq > 1) a.order = reinterpret_cast<int32_t*>(a.ws + (long long)a.slots * a.H * W_FWD);
   if (some) {
     if (!(input_maps(m, a) && rows_map(&m.o, a.o, DV, a, 32, 32))) return cudaErrorInvalidValue;
-    delta_prep_kernel<false><<<chunks, PREP_THREADS, PrepSmem::bytes(false), st>>>(m, a);
+    delta_prep_kernel<false><<<chunks, PREP_THREADS, PrepSmem::bytes(false), st>>>(m, a, 4 * sm_count());
   }
   const cudaError_t scan = launch_behind(delta_scan_kernel<false>, units, SCAN_THREADS, ScanSmem::BYTES, st, m, a, sm_count());
   return scan != cudaSuccess ? scan : cudaGetLastError();
@@ -1723,7 +1740,7 @@ cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t st) {
           rows_map(&m.dvo, a.dv, DV, a, 32, 32) && map3(&m.xsd, a.ws + W_X, DV, 256, all, 2 * DV, W_BWD, 64, 256, 1) &&
           rows_map(&m.dqo, a.dq, DK, a, 48, 32) && rows_map(&m.dko, a.dk, DK, a, 48, 32)))
       return cudaErrorInvalidValue;
-    delta_prep_kernel<true><<<chunks, PREP_THREADS, PrepSmem::bytes(true), st>>>(m, a);
+    delta_prep_kernel<true><<<chunks, PREP_THREADS, PrepSmem::bytes(true), st>>>(m, a, 0);
     const cudaError_t scan = launch_behind(delta_scan_kernel<true>, units, SCAN_THREADS, ScanSmem::BYTES, st, m, a, sm_count());
     if (scan != cudaSuccess) return scan;
   }
