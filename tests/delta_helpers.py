@@ -1,9 +1,9 @@
 """The gated delta rule in 64 bits, token by token (tests only), inputs for it, and its bounds.
 
 Bounds (2-norm of the error over 2-norm of the result, and the largest error over its rms).
-  fp32 outputs of fp32 calls: sums of at most 192 + 64 products with 24 bits, a few of them in a row, errors of
-      random sign: sqrt(256) 2^-24 each, 1e-6; the gates' exp 2^-22 more.  1e-5, and 40 times that for the largest
-      of at most 10^6 elements (5 sigma, and operands up to 8 rms).
+  fp32 outputs of fp32 calls: sums of at most 192 + 64 products whose operands keep 22 bits, a few of them in a row,
+      errors of random sign: sqrt(256) 2^-22 each if all were the largest, 4e-6; the gates' exp 2^-22 more.  1e-5,
+      and 40 times that for the largest of at most 10^6 elements (5 sigma, and operands up to 8 rms).
   states of bf16 calls: operands that are not bf16 are sums of two, each rounding off by 2^-8: 2^-16 of the
       operand.  Along the way from a state to the next, four are split (state, weighted residuals, Z, weighted updates):
       4 2^-16 = 6e-5 if all errors were the largest and of one sign; at random signs and uniform in the binade the
