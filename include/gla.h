@@ -512,9 +512,11 @@ int gla_delta_decode_step_bf16_state(const void* q, const void* k, const void* v
  *   token_seq, token_pos   [budget]: request and place (seen + the place in this step) of each packed token, -1
  *                behind the last; both or neither NULL.
  * Inputs and outputs must not overlap, but that row may be held.  pool_rows from 1 to GLA_PLAN_MAX_ROWS, N up to
- * GLA_PLAN_MAX_REQUESTS (else GLA_ERR_SHAPE, GLA_ERR_UNSUPPORTED).  Pointers 4-byte aligned. */
+ * GLA_PLAN_MAX_REQUESTS, budget (where token_seq and token_pos are given) up to GLA_PLAN_MAX_BUDGET; else GLA_ERR_SHAPE
+ * (too small) or GLA_ERR_UNSUPPORTED (too large).  Pointers 4-byte aligned. */
 #define GLA_PLAN_MAX_ROWS (1 << 19)
 #define GLA_PLAN_MAX_REQUESTS (1 << 20)
+#define GLA_PLAN_MAX_BUDGET (1 << 30)
 int gla_slot_plan(const int32_t* new_len, const int32_t* held, const int32_t* seen, int N, int pool_rows, int budget,
                   int32_t* cu_seqlens, int32_t* slot, int32_t* start_row, int32_t* row, int32_t* token_seq,
                   int32_t* token_pos, gla_stream_t stream);

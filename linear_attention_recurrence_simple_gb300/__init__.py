@@ -45,6 +45,8 @@ EXPORTS = ("gla_workspace_bytes", "gla_bwd_workspace_bytes", "gla_chunk_fwd", "g
            "gla_delta_workspace_bytes", "gla_delta_bwd_workspace_bytes", "gla_delta_decode_step",
            "gla_delta_decode_step_bf16_state", "gla_slot_plan")
 NOALLOC_MAX_SEQS = 16384
+PLAN_MAX_ROWS, PLAN_MAX_BUDGET = 1 << 19, 1 << 30
+GLA_ERR_SHAPE, GLA_ERR_UNSUPPORTED = -2, -5
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libgla.so")
@@ -1160,12 +1162,17 @@ def gla_slot_plan(new_len, held, seen, pool_rows: int, budget: int, out=None):
     ``new_len`` ``[N]`` int32: tokens each request brings (0: none now; negative: it has finished); ``held`` ``[N]``
     int32: the pool row it holds, or -1; ``seen`` ``[N]`` int32: its tokens before this step, or None for zeros.  Of
     ``budget`` tokens each request in turn gets what it brings; one without a row takes the lowest of the
-    ``pool_rows`` that is free.  Returns a :class:`SlotPlan` (``out``: one to write to): ``cu_seqlens``, ``start_row``
+    ``pool_rows`` (at most 2^19) that is free; budgets go up to 2^30.  Returns a :class:`SlotPlan` (``out``: one to write to): ``cu_seqlens``, ``start_row``
     and ``slot`` are :func:`gla_delta_fwd`'s ``cu_seqlens``, ``h0_row`` and ``hT_row``, ``row`` the next step's
     ``held``, ``token_seq`` and ``token_pos`` each packed token's request and place (-1 behind the last)."""
     lib = _libs.get(_use_debug) or load_library()
+    pool_rows, budget = int(pool_rows), int(budget)
+    if pool_rows > PLAN_MAX_ROWS or budget > PLAN_MAX_BUDGET:  # (before anything is allocated, and before a C int wraps)
+        raise GlaError(GLA_ERR_UNSUPPORTED, "gla_slot_plan")
+    if pool_rows < 1:
+        raise GlaError(GLA_ERR_SHAPE, "gla_slot_plan")
     dev = _device_of(new_len, "new_len")
-    N, budget = new_len.numel(), int(budget)
+    N = new_len.numel()
     maps = (new_len, held) if seen is None else (new_len, held, seen)
     if not _like(dev.index, torch.int32, *maps):
         for name, t in zip(("new_len", "held", "seen"), maps):
@@ -1185,7 +1192,7 @@ def gla_slot_plan(new_len, held, seen, pool_rows: int, budget: int, out=None):
         for name, t, size in zip(SlotPlan._fields, out, sizes):
             _good(t, "out." + name, torch.int32, dev, size)
         places = [t.data_ptr() for t in out]
-    _run(lib.gla_slot_plan, "gla_slot_plan", dev, new_len.data_ptr(), held.data_ptr(), _addr(seen), N, int(pool_rows),
+    _run(lib.gla_slot_plan, "gla_slot_plan", dev, new_len.data_ptr(), held.data_ptr(), _addr(seen), N, pool_rows,
          budget, *places)
     return SlotPlan(*flat.split_with_sizes(sizes)) if out is None else out
 

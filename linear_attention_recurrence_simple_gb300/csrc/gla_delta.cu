@@ -182,6 +182,7 @@ int gla_slot_plan(const int32_t* new_len, const int32_t* held, const int32_t* se
                   int32_t* token_pos, gla_stream_t stream) {
   if (N < 0 || pool_rows < 1 || budget < 0) return GLA_ERR_SHAPE;
   if (pool_rows > GLA_PLAN_MAX_ROWS || N > GLA_PLAN_MAX_REQUESTS) return GLA_ERR_UNSUPPORTED;
+  if ((token_seq || token_pos) && budget > GLA_PLAN_MAX_BUDGET) return GLA_ERR_UNSUPPORTED;
   if (!cu_seqlens || !token_seq != !token_pos) return GLA_ERR_NULL;
   if (N > 0 && (!new_len || !held || !slot || !start_row || !row)) return GLA_ERR_NULL;
   for (const void* p : {(const void*)new_len, (const void*)held, (const void*)seen, (const void*)cu_seqlens,

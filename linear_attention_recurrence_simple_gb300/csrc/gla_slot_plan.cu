@@ -165,7 +165,8 @@ slot_plan_kernel(const int32_t* __restrict__ new_len, const int32_t* __restrict_
   }
   if (!ends) return;
   __syncthreads();
-  for (int t = blockIdx.x * THREADS + tid; t < budget; t += gridDim.x * THREADS) token_place(s_cu, seen, N, t, token_seq, token_pos);
+  for (int t = blockIdx.x * THREADS + tid; t < budget; t += gridDim.x * THREADS)  // (below 2^31: GLA_PLAN_MAX_BUDGET)
+    token_place(s_cu, seen, N, t, token_seq, token_pos);
 }
 
 __global__ void __launch_bounds__(256)

@@ -1,0 +1,36 @@
+"""Host-only checks of limits that the gated delta calls and the slot plan state: sizes past them are refused before any
+CUDA call (fake addresses, never dereferenced)."""
+import ctypes
+
+import pytest
+import torch
+
+import linear_attention_recurrence_simple_gb300 as gla
+
+NULL, SHAPE, UNSUP = -1, -2, -5
+P, A = ctypes.c_void_p, 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return gla.load_library()
+
+
+@pytest.mark.parametrize("budget", [2 ** 30 + 1, 2 ** 31 - 65536, 2 ** 31 - 1])
+def test_plan_budgets_that_token_places_cannot_count_are_refused(lib, budget):
+    """Places of tokens are counted in 32 bits, a whole grid at a time."""
+    def plan(seq, pos, cu=None, N=0):
+        return lib.gla_slot_plan(P(A), P(A), None, N, 9, budget, P(cu), P(A), P(A), P(A), P(seq), P(pos), None)
+
+    assert plan(A, A) == UNSUP       # (before the missing cu_seqlens is looked at)
+    assert plan(None, A) == UNSUP and plan(A, None) == UNSUP
+    assert plan(None, None) == NULL  # without places a budget is a number to compare with
+
+
+def test_plan_binding_refuses_before_a_c_int_wraps():
+    x = torch.zeros(3, dtype=torch.int32)
+    for rows, budget, status in ((2 ** 32 + 4, 8, UNSUP), (2 ** 19 + 1, 8, UNSUP), (4, 2 ** 30 + 1, UNSUP), (4, 2 ** 32 + 8, UNSUP),
+                                 (0, 8, SHAPE), (-2 ** 32 + 4, 8, SHAPE)):
+        with pytest.raises(gla.GlaError) as e:
+            gla.gla_slot_plan(x, x, None, rows, budget)
+        assert e.value.status == status
