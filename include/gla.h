@@ -487,13 +487,24 @@ int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, co
 /* One decode step for N sequences, in place on a pool of states, fp32 or (_bf16_state) bf16.
  *   q, k [N, H, 96]; v, o [N, H, 192]; g, beta [N, H]; state, slot, pool_rows as in gla_decode_step (rows distinct),
  *   but that a slot of -1 leaves its sequence alone (state and o untouched) without an error.  N * H below 2^31.
- * The readout uses the update before a bf16 pool rounds it. */
+ * The readout uses the update before a bf16 pool rounds it.  Every sequence goes on from what its row holds: a row that
+ * was another sequence's has to be cleared first, or left to the call below. */
 int gla_delta_decode_step(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale,
                           float* state, const int32_t* slot, int pool_rows, void* o, int N, int H, int dk, int dv,
                           int dtype, gla_stream_t stream);
 int gla_delta_decode_step_bf16_state(const void* q, const void* k, const void* v, const void* g, const void* beta,
                                      float scale, void* state, const int32_t* slot, int pool_rows, void* o, int N,
                                      int H, int dk, int dv, int dtype, gla_stream_t stream);
+
+/* The same step where a sequence's state need not stand in the row that it ends in.
+ *   state_dtype  GLA_F32 or GLA_BF16, the pool's type.
+ *   start_row    [N] int32 device: the row that sequence n goes on from; -1: from zeros, and what the row of its slot
+ *                holds is not read (not even a NaN); NULL: its slot's row.  Rows may repeat, and may be other rows than
+ *                slot[n], as long as no other sequence of the call writes them.  Any other row outside the pool records
+ *                GLA_ERR_SHAPE and starts from zeros.  Where slot is -1 the sequence is left alone as above. */
+int gla_delta_decode_step_rows(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale,
+                               void* state, int state_dtype, const int32_t* slot, const int32_t* start_row, int pool_rows,
+                               void* o, int N, int H, int dk, int dv, int dtype, gla_stream_t stream);
 
 /* One serving step's maps, built on the device from the requests' lengths, so that a step needs no host
  * synchronisation (and can be captured: all sizes are fixed).
@@ -506,8 +517,10 @@ int gla_delta_decode_step_bf16_state(const void* q, const void* k, const void* v
  * Requests are served in order: one that brings tokens and holds no row takes the lowest free one (without one it gets
  * no tokens); each gets its tokens until `budget` tokens are handed out, the one at the limit a part of them.
  *   cu_seqlens   [N + 1]: packed offsets of the tokens handed out.
- *   slot         [N]: row of a request that has tokens in this step, else -1 (hT_row, and the decode step's slot).
- *   start_row    [N]: the row it goes on from, -1 where it is new or has no tokens (h0_row).
+ *   slot         [N]: row of a request that has tokens in this step, else -1 (hT_row, and the decode step's slot).  A row that
+ *                has become free is the next request's, and holds what the last one left: start_row goes with it.
+ *   start_row    [N]: the row it goes on from, -1 where it is new or has no tokens (h0_row, and
+ *                gla_delta_decode_step_rows' start_row).
  *   row          [N]: the row it holds after the step, -1: none (the next step's held).
  *   token_seq, token_pos   [budget]: request and place (seen + the place in this step) of each packed token, -1
  *                behind the last; both or neither NULL.

@@ -43,7 +43,7 @@ EXPORTS = ("gla_workspace_bytes", "gla_bwd_workspace_bytes", "gla_chunk_fwd", "g
            "gla_prefix_decode_step", "gla_tail_append", "gla_tail_read", "gla_tail_fold", "gla_prefix_fwd",
            "gla_prefix_bwd", "gla_prefix_bwd_workspace_bytes", "gla_debug_give_up", "gla_delta_fwd", "gla_delta_bwd",
            "gla_delta_workspace_bytes", "gla_delta_bwd_workspace_bytes", "gla_delta_decode_step",
-           "gla_delta_decode_step_bf16_state", "gla_slot_plan")
+           "gla_delta_decode_step_bf16_state", "gla_delta_decode_step_rows", "gla_slot_plan")
 NOALLOC_MAX_SEQS = 16384
 PLAN_MAX_ROWS, PLAN_MAX_BUDGET = 1 << 19, 1 << 30
 GLA_ERR_SHAPE, GLA_ERR_UNSUPPORTED = -2, -5
@@ -158,6 +158,8 @@ def load_library(build: bool = True, debug: bool | None = None):
         for fn in (lib.gla_delta_decode_step, lib.gla_delta_decode_step_bf16_state):
             fn.argtypes = [P, P, P, P, P, F, P, P, I, P, I, I, I, I, I, P]
             fn.restype = I
+        lib.gla_delta_decode_step_rows.argtypes = [P, P, P, P, P, F, P, I, P, P, I, P, I, I, I, I, I, P]
+        lib.gla_delta_decode_step_rows.restype = I
         lib.gla_slot_plan.argtypes = [P, P, P, I, I, I, P, P, P, P, P, P, P]
         lib.gla_slot_plan.restype = I
         _libs[debug] = lib
@@ -1108,10 +1110,12 @@ def gla_delta_bwd(q, k, v, g, beta, dO, scale=None, h0=None, dhT=None, cu_seqlen
     return dq, dk, dv, dg, dbeta, dh0
 
 
-def gla_delta_decode_step(q, k, v, g, beta, state, slot=None, scale=None, o=None):
+def gla_delta_decode_step(q, k, v, g, beta, state, slot=None, scale=None, o=None, start_row=None):
     """One decode step of the gated delta rule on the pool ``state [P, H, 96, 192]`` (fp32 or bf16, updated in
     place).  q, k ``[N, H, 96]``; v ``[N, H, 192]``; g, beta ``[N, H]``; ``slot`` ``[N]`` int32 pool rows (-1: the
-    sequence is left alone) or None (row n).  Returns ``o [N, H, 192]``."""
+    sequence is left alone, its row of ``o`` as it was) or None (row n); ``start_row`` ``[N]`` int32 rows to go on from
+    (-1: from zeros, whatever the slot's row holds) or None (the slot's row).  A :class:`SlotPlan` has both: a row that
+    it gives to a new request still holds the last one's state.  Returns ``o [N, H, 192]``."""
     lib = _libs.get(_use_debug) or load_library()
     dev = _device_of(q, "q")
     dt = _dtype_code(q)
@@ -1138,6 +1142,15 @@ def gla_delta_decode_step(q, k, v, g, beta, state, slot=None, scale=None, o=None
         o = torch.empty_like(v)
     else:
         _good(o, "o", v.dtype, dev, v.numel())
+    if start_row is not None:
+        _good(start_row, "start_row", torch.int32, dev)
+        if start_row.shape != (N,):
+            raise ValueError("start_row must be [N]")
+        _run(lib.gla_delta_decode_step_rows, "gla_delta_decode_step_rows", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             g.data_ptr(), beta.data_ptr(), _SCALE if scale is None else float(scale), state.data_ptr(),
+             GLA_BF16 if state.dtype == torch.bfloat16 else GLA_F32, _addr(slot), start_row.data_ptr(), shape[0],
+             o.data_ptr(), N, H, DK, DV, dt)
+        return o
     fn, where = ((lib.gla_delta_decode_step_bf16_state, "gla_delta_decode_step_bf16_state")
                  if state.dtype == torch.bfloat16 else (lib.gla_delta_decode_step, "gla_delta_decode_step"))
     _run(fn, where, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
@@ -1163,7 +1176,8 @@ def gla_slot_plan(new_len, held, seen, pool_rows: int, budget: int, out=None):
     int32: the pool row it holds, or -1; ``seen`` ``[N]`` int32: its tokens before this step, or None for zeros.  Of
     ``budget`` tokens each request in turn gets what it brings; one without a row takes the lowest of the
     ``pool_rows`` (at most 2^19) that is free; budgets go up to 2^30.  Returns a :class:`SlotPlan` (``out``: one to write to): ``cu_seqlens``, ``start_row``
-    and ``slot`` are :func:`gla_delta_fwd`'s ``cu_seqlens``, ``h0_row`` and ``hT_row``, ``row`` the next step's
+    and ``slot`` are :func:`gla_delta_fwd`'s ``cu_seqlens``, ``h0_row`` and ``hT_row`` (``start_row`` and ``slot`` also
+    :func:`gla_delta_decode_step`'s, where every request brings one token), ``row`` the next step's
     ``held``, ``token_seq`` and ``token_pos`` each packed token's request and place (-1 behind the last)."""
     lib = _libs.get(_use_debug) or load_library()
     pool_rows, budget = int(pool_rows), int(budget)

@@ -4,7 +4,7 @@
 
 namespace gla {
 cudaError_t launch_delta_decode(const DeltaArgs& a, int dtype_f32, int state_bf16, void* state, const int32_t* slot,
-                                int pool_rows, cudaStream_t st);
+                                const int32_t* start_row, int pool_rows, cudaStream_t st);
 cudaError_t launch_slot_plan(const int32_t* new_len, const int32_t* held, const int32_t* seen, int N, int rows, int budget,
                              int32_t* cu, int32_t* slot, int32_t* start, int32_t* row, int32_t* token_seq, int32_t* token_pos,
                              unsigned* err, cudaStream_t st);
@@ -138,8 +138,8 @@ int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, co
 }
 
 static int delta_decode(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale, void* state,
-                        int state_bf16, const int32_t* slot, int pool_rows, void* o, int N, int H, int dk, int dv, int dtype,
-                        gla_stream_t stream) {
+                        int state_bf16, const int32_t* slot, const int32_t* start_row, int pool_rows, void* o, int N, int H, int dk,
+                        int dv, int dtype, gla_stream_t stream) {
   if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_DTYPE;
   if (dk != GLA_DK || dv != GLA_DV) return GLA_ERR_UNSUPPORTED;
   if (N < 0 || H < 1 || pool_rows < 0 || (long long)N * H >= (1ll << 31)) return GLA_ERR_SHAPE;
@@ -150,7 +150,7 @@ static int delta_decode(const void* q, const void* k, const void* v, const void*
   for (const void* p : {q, k, v, (const void*)state, (const void*)o})
     if (off16(p)) return GLA_ERR_ALIGN;
   if (off_element(g, dtype) || off_element(beta, dtype)) return GLA_ERR_ALIGN;
-  if (off4(slot)) return GLA_ERR_ALIGN;
+  if (off4(slot) || off4(start_row)) return GLA_ERR_ALIGN;
   gla::DeltaArgs a = {};
   const int rc = gla::current_device_state(&a.err, &a.wait_ns);
   if (rc) return rc;
@@ -163,18 +163,27 @@ static int delta_decode(const void* q, const void* k, const void* v, const void*
   a.scale = scale;
   a.n_seq = N;
   a.H = H;
-  return status_of(gla::launch_delta_decode(a, dtype == GLA_F32, state_bf16, state, slot, pool_rows, (cudaStream_t)stream));
+  return status_of(gla::launch_delta_decode(a, dtype == GLA_F32, state_bf16, state, slot, start_row, pool_rows,
+                                            (cudaStream_t)stream));
 }
 
 int gla_delta_decode_step(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale,
                           float* state, const int32_t* slot, int pool_rows, void* o, int N, int H, int dk, int dv, int dtype,
                           gla_stream_t stream) {
-  return delta_decode(q, k, v, g, beta, scale, state, 0, slot, pool_rows, o, N, H, dk, dv, dtype, stream);
+  return delta_decode(q, k, v, g, beta, scale, state, 0, slot, nullptr, pool_rows, o, N, H, dk, dv, dtype, stream);
 }
 int gla_delta_decode_step_bf16_state(const void* q, const void* k, const void* v, const void* g, const void* beta,
                                      float scale, void* state, const int32_t* slot, int pool_rows, void* o, int N, int H,
                                      int dk, int dv, int dtype, gla_stream_t stream) {
-  return delta_decode(q, k, v, g, beta, scale, state, 1, slot, pool_rows, o, N, H, dk, dv, dtype, stream);
+  return delta_decode(q, k, v, g, beta, scale, state, 1, slot, nullptr, pool_rows, o, N, H, dk, dv, dtype, stream);
+}
+
+int gla_delta_decode_step_rows(const void* q, const void* k, const void* v, const void* g, const void* beta, float scale,
+                               void* state, int state_dtype, const int32_t* slot, const int32_t* start_row, int pool_rows,
+                               void* o, int N, int H, int dk, int dv, int dtype, gla_stream_t stream) {
+  if (state_dtype != GLA_BF16 && state_dtype != GLA_F32) return GLA_ERR_DTYPE;
+  return delta_decode(q, k, v, g, beta, scale, state, state_dtype == GLA_BF16, slot, start_row, pool_rows, o, N, H, dk, dv, dtype,
+                      stream);
 }
 
 int gla_slot_plan(const int32_t* new_len, const int32_t* held, const int32_t* seen, int N, int pool_rows, int budget,

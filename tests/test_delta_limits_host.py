@@ -34,3 +34,19 @@ def test_plan_binding_refuses_before_a_c_int_wraps():
         with pytest.raises(gla.GlaError) as e:
             gla.gla_slot_plan(x, x, None, rows, budget)
         assert e.value.status == status
+
+
+def test_decode_from_rows_argument_errors(lib):
+    NULL, DTYPE, ALIGN = -1, -3, -4
+
+    def step(q=A, state=A, sdt=1, slot=None, start=A, rows=9, o=A, N=3, H=2, dk=96, dt=0):
+        return lib.gla_delta_decode_step_rows(P(q), P(A), P(A), P(A), P(A), 0.1, P(state), sdt, P(slot), P(start), rows, P(o),
+                                              N, H, dk, 192, dt, None)
+
+    for sdt in (0, 1):
+        assert step(sdt=sdt, dt=2) == DTYPE and step(sdt=sdt, dk=95) == UNSUP
+        assert step(sdt=sdt, rows=2) == SHAPE and step(sdt=sdt, N=2 ** 30, slot=A) == SHAPE
+        assert step(sdt=sdt, q=None) == NULL and step(sdt=sdt, state=None) == NULL
+        assert step(sdt=sdt, start=A + 2) == ALIGN and step(sdt=sdt, o=A + 4) == ALIGN
+        assert step(sdt=sdt, N=0, q=None, start=None) == 0
+    assert step(sdt=2) == DTYPE and step(sdt=-1) == DTYPE
