@@ -445,7 +445,8 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
  * q, k, v, o, states, scale, cu_seqlens, dtype and the layouts are those of gla_chunk_fwd.  A call's tokens are
  * handled in chunks of 64; an infinity or a NaN in a token reaches every output of its chunk and what follows it in
  * its sequence, and nothing of another sequence.  cu_seqlens is checked on the device: offsets that decrease or pass
- * T are clamped and record GLA_ERR_SHAPE.
+ * T are clamped and record GLA_ERR_SHAPE.  Its last offset may stand below T (a step under its budget): the forward
+ * leaves such rows of o as they were, the backward writes zeros to the gradients of such rows.
  * bf16 calls hold what carries a state from chunk to chunk in fp32 and in pairs of bf16 (16 bits: hT and dh0 are 3 to
  * 5e-6 of the norm from the exact ones); what only feeds an output of dtype bf16 may be rounded to bf16 once more.
  * fp32 calls keep 22 bits of each operand of a product, and everything else in fp32 (2 to 4e-7 of the norm).

@@ -1065,7 +1065,8 @@ def gla_delta_fwd(q, k, v, g, beta, scale=None, h0=None, h0_row=None, hT=None, h
     of the decay) and ``beta`` ``[B, T, H]`` or ``[T_total, H]``, all of one type.  ``h0`` fp32 ``[P, H, 96, 192]``
     with ``h0_row`` ``[n_seq]`` int32 (rows may repeat; -1: zeros), or None for row n; ``hT`` and ``hT_row`` likewise
     (rows distinct; -1: not wanted).  ``hT`` may be ``h0``: sequences then go on from rows of a pool and end in
-    them.  Without ``hT``, ``[n_seq, H, 96, 192]`` is allocated (or None, if not requested)."""
+    them.  Without ``hT``, ``[n_seq, H, 96, 192]`` is allocated (or None, if not requested).  Packed rows behind the last
+    offset are left as they were in ``o``: without one to write to they hold whatever that memory held."""
     lib = _libs.get(_use_debug) or load_library()
     dev, dt, n_seq, T, H = _delta_call(q, k, v, g, beta, cu_seqlens)
     h0_rows = _delta_states(h0, h0_row, n_seq, H, dev, "h0")
@@ -1089,7 +1090,8 @@ def gla_delta_fwd(q, k, v, g, beta, scale=None, h0=None, h0_row=None, hT=None, h
 def gla_delta_bwd(q, k, v, g, beta, dO, scale=None, h0=None, dhT=None, cu_seqlens=None, need_dh0: bool = True,
                   workspace=None):
     """Backward of :func:`gla_delta_fwd` (``gla_delta_bwd``).  Returns ``(dq, dk, dv, dg, dbeta, dh0)`` (``dh0``
-    None if not requested); ``h0`` and ``dhT`` fp32 ``[n_seq, H, 96, 192]``, or None for zeros."""
+    None if not requested); ``h0`` and ``dhT`` fp32 ``[n_seq, H, 96, 192]``, or None for zeros.  The gradients of packed
+    rows behind the last offset are zeros."""
     lib = _libs.get(_use_debug) or load_library()
     dev, dt, n_seq, T, H = _delta_call(q, k, v, g, beta, cu_seqlens)
     _good(dO, "dO", q.dtype, dev)

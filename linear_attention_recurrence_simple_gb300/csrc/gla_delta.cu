@@ -1,4 +1,6 @@
 // C entries of the gated delta rule and of the slot plan: argument checks, workspace sizes, dispatch.
+#include <utility>
+
 #include "gla.h"
 #include "gla_delta.cuh"
 
@@ -100,7 +102,7 @@ int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, co
   gla::DeltaArgs a = {};
   int rc = check_sizes(n_seq, T, H, dk_size, dv_size, dtype, cu_seqlens, &tokens, &a.slots);
   if (rc) return rc;
-  if (n_seq == 0) return GLA_OK;
+  if (n_seq == 0 && tokens == 0) return GLA_OK;
   if (tokens > 0)
     for (const void* p : {q, k, v, g, beta, dO, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)dg, (const void*)dbeta})
       if (!p) return GLA_ERR_NULL;
@@ -108,6 +110,14 @@ int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, co
     if (off16(p)) return GLA_ERR_ALIGN;
   for (const void* p : {g, beta, (const void*)dg, (const void*)dbeta})
     if (off_element(p, dtype)) return GLA_ERR_ALIGN;
+  if (n_seq == 0) {  // rows of no sequence
+    const size_t gates = (size_t)tokens * H * (dtype == GLA_F32 ? 4 : 2);
+    for (const auto& [p, n] : {std::pair<void*, size_t>{dq, GLA_DK}, {dk, GLA_DK}, {dv, GLA_DV}, {dg, 1}, {dbeta, 1}}) {
+      const cudaError_t e = cudaMemsetAsync(p, 0, n * gates, (cudaStream_t)stream);
+      if (e != cudaSuccess) return status_of(e);
+    }
+    return GLA_OK;
+  }
   if (!workspace || ws_bytes < gla_delta_bwd_workspace_bytes(n_seq, T, H, cu_seqlens != nullptr, dtype)) return GLA_ERR_WORKSPACE;
   if (off16(workspace)) return GLA_ERR_ALIGN;
   rc = gla::current_device_state(&a.err, &a.wait_ns);

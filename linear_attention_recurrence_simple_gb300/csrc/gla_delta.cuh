@@ -135,6 +135,29 @@ __device__ __forceinline__ int delta_row(const int32_t* row, int rows, int n, un
   return -1;
 }
 
+// Packed rows of no sequence (in front of the first offset, behind the last): nothing depends on them, so their gradients
+// are zero.  Place p has rows 64 p .. of the packed array (there are at least as many places as that takes).  Whole CTA.
+template <class T>
+__device__ __noinline__ void zero_spare_rows(const DeltaArgs& a, int place, int h) {
+  if (!a.cu_seqlens) return;
+  const int first = min(max(a.cu_seqlens[0], 0), a.T), last = min(max(a.cu_seqlens[a.n_seq], 0), a.T);
+  const long long t0 = (long long)place * DC, t1 = min(t0 + DC, (long long)a.T);
+  if (t0 >= first && t1 <= last) return;
+  const int lane = threadIdx.x & 31;
+  constexpr int KV = DK * (int)sizeof(T) / 16, VV = DV * (int)sizeof(T) / 16;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (long long t = t0 + threadIdx.x / 32; t < t1; t += blockDim.x / 32) {
+    if (t >= first && t < last) continue;
+    const long long row = t * a.H + h;
+    if (!GLA_IN_BOUNDS(row >= 0 && row < (long long)a.T * a.H, a.err)) continue;
+    for (int e = lane; e < VV; e += 32) {
+      if (e < KV) reinterpret_cast<uint4*>((T*)a.dq + row * DK)[e] = reinterpret_cast<uint4*>((T*)a.dk + row * DK)[e] = zero;
+      reinterpret_cast<uint4*>((T*)a.dv + row * DV)[e] = zero;
+    }
+    if (lane == 0) ((T*)a.dg)[row] = ((T*)a.dbeta)[row] = from_f<T>(0.f);
+  }
+}
+
 // Running sums of a chunk's log decays, each as two fp32 (hi + lo): a difference of two of them keeps 24 bits
 // of what is left between them, whatever was decayed before.  Summed as whole numbers of 2^-40 (fp64 adds are slow
 // here), so that a sum is off by 64 2^-41 at most.  Whole warp; x0, x1 are the log decays of tokens 2 lane and

@@ -591,7 +591,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
   __shared__ float red[THREADS / 32];
   const int unit = blockIdx.x / 2, rank = blockIdx.x % 2, slot = unit / a.H, h = unit % a.H, tid = threadIdx.x, x0 = rank * HK;
   const DeltaChunk ch = chunk_of_slot(a, slot);
-  if (ch.len == 0) return;  // (both)
+  if (ch.len == 0) {  // (both)
+    if (rank == 0) zero_spare_rows<float>(a, slot, h);
+    return;
+  }
   const float* const ws = ws_of<true>(a, slot, h);
   const float* const gt = ws + WS_GT;
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
@@ -734,6 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
     for (int x = 0; x < 2 * SNB; ++x) b += dbeta_part[((long long)x * tokens + t) * a.H + h];
     ((float*)a.dbeta)[t * a.H + h] = b;
   }
+  if (rank == 0) zero_spare_rows<float>(a, slot, h);
 }
 
 constexpr int PREP_BYTES = PREP_FLOATS * 4, SCAN_BYTES = SCAN_FLOATS * 4, RSCAN_BYTES = RSCAN_FLOATS * 4, GRAD_BYTES = GRAD_FLOATS * 4;

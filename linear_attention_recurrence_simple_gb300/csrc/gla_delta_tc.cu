@@ -1321,7 +1321,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
   float* const red = reinterpret_cast<float*>(sm + GSmem::RED);
   const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = (warp >> 2) & 1;
   const DeltaChunk ch = chunk_of_slot(a, slot);
-  if (ch.len == 0) return;
+  if (ch.len == 0) {
+    zero_spare_rows<__nv_bfloat16>(a, slot, h);
+    return;
+  }
   const int idx = slot * a.H + h;
   const uint8_t* const ws = a.ws + (long long)idx * W_BWD;
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
@@ -1621,6 +1624,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
     for (int x = 0; x < 2 * NTILE; ++x) b += dbeta_part[((long long)x * tokens + t) * a.H + h];
     ((__nv_bfloat16*)a.dbeta)[t * a.H + h] = __float2bfloat16_rn(b);
   }
+  zero_spare_rows<__nv_bfloat16>(a, slot, h);
 }
 
 }  // namespace
