@@ -43,8 +43,8 @@ __device__ __forceinline__ float4 fma4(float a, float4 x, float4 y) {
   return make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
 }
 
-// ROWS_FROM: start_row says where each state comes from.  (A step in place has a kernel without it: with the choice at run
-// time 1,280 x 16 on an fp32 pool take 470 us instead of 444.)
+// ROWS_FROM: start_row says where each state comes from.  (A step in place has a kernel without it: 1,280 x 16 on an fp32
+// pool take 440 us without and 452 with it, in one kernel with the choice at run time 470; all from zeros 251.)
 template <class T, class ST, bool ROWS_FROM>
 __global__ void __launch_bounds__(StepCfg<ST>::THREADS, StepCfg<ST>::MIN_BLOCKS)
 delta_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ g,
@@ -60,11 +60,11 @@ delta_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
   const long long nh = blockIdx.x;
   const int n = (int)(nh / H), h = (int)(nh % H), tid = threadIdx.x, c = tid % VCOLS, r = tid / VCOLS;
   const int row = slot ? slot[n] : n;
+  int from = ROWS_FROM ? start_row[n] : row;  // (with the slot: one latency)
   if (row < 0 || row >= pool_rows) {  // -1: a sequence without a row, left alone
     if (tid == 0 && row != -1) raise_error(err, ERR_SHAPE);
     return;
   }
-  int from = ROWS_FROM ? start_row[n] : row;
   if (ROWS_FROM && (from < 0 || from >= pool_rows)) {  // -1: from zeros, whatever the row holds
     if (tid == 0 && from != -1) raise_error(err, ERR_SHAPE);
     from = -1;
