@@ -1687,6 +1687,10 @@ bool input_maps(DeltaMaps& m, const DeltaArgs& a) {
   return rows_map(&m.k0, a.k, DK, a, 64, DC) && rows_map(&m.k1, a.k, DK, a, 32, DC) && rows_map(&m.q0, a.q, DK, a, 64, DC) &&
          rows_map(&m.q1, a.q, DK, a, 32, DC) && rows_map(&m.v, a.v, DV, a, 64, DC);
 }
+// Whether the scans take a packed call's longest sequences first.  Each is compared with all others, which 16,384 of them can
+// still afford (as the fixed-decay calls have it); with more, the units are many rounds, and their order gains nothing.
+constexpr int ORDER_MAX_SEQS = 16384;
+bool ordered(const DeltaArgs& a) { return a.cu_seqlens && a.n_seq > 1 && a.n_seq <= ORDER_MAX_SEQS; }
 // CTAs b and b + this many are likely to share an SM.
 int sm_count() {
   int dev = 0, sms = 152;
@@ -1711,7 +1715,7 @@ cudaError_t launch_delta_tc_fwd(DeltaArgs a, cudaStream_t st) {
   memset(&m, 0, sizeof(m));
   const unsigned chunks = (unsigned)a.slots * a.H, units = (unsigned)a.n_seq * a.H * NTILE;
   const bool some = a.cu_seqlens ? a.T > 0 : a.slots > 0;
-  if (some && a.cu_seqlens && a.n_seq > 1) a.order = reinterpret_cast<int32_t*>(a.ws + (long long)a.slots * a.H * W_FWD);
+  if (some && ordered(a)) a.order = reinterpret_cast<int32_t*>(a.ws + (long long)a.slots * a.H * W_FWD);
   if (some) {
     if (!(input_maps(m, a) && rows_map(&m.o, a.o, DV, a, 32, 32))) return cudaErrorInvalidValue;
     delta_prep_kernel<false><<<chunks, PREP_THREADS, PrepSmem::bytes(false), st>>>(m, a, 4 * sm_count());
@@ -1735,7 +1739,7 @@ cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t st) {
   float* const part = reinterpret_cast<float*>(a.ws + (long long)a.slots * a.H * W_BWD);
   const bool some = a.cu_seqlens ? a.T > 0 : a.slots > 0;
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;
-  if (some && a.cu_seqlens && a.n_seq > 1) a.order = reinterpret_cast<int32_t*>(part + 2ll * NTILE * tokens * a.H);
+  if (some && ordered(a)) a.order = reinterpret_cast<int32_t*>(part + 2ll * NTILE * tokens * a.H);
   if (some) {
     const long long all = (long long)a.slots * a.H;
     if (!(input_maps(m, a) && rows_map(&m.dO, a.dO, DV, a, 64, DC) && rows_map(&m.dv, a.dv, DV, a, 64, DC) &&
