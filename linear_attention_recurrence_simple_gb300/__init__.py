@@ -1080,6 +1080,8 @@ def gla_delta_fwd(q, k, v, g, beta, scale=None, h0=None, h0_row=None, hT=None, h
     if workspace is None:
         workspace = torch.empty(lib.gla_delta_workspace_bytes(n_seq, T, H, int(cu_seqlens is not None), dt),
                                 dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", None, dev)
     _run(lib.gla_delta_fwd, "gla_delta_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
          beta.data_ptr(), _addr(h0), h0_rows, _addr(h0_row), _SCALE if scale is None else float(scale), o.data_ptr(),
          _addr(hT), hT_rows, _addr(hT_row), _addr(cu_seqlens), n_seq, T, H, DK, DV, dt, workspace.data_ptr(),
@@ -1105,6 +1107,8 @@ def gla_delta_bwd(q, k, v, g, beta, dO, scale=None, h0=None, dhT=None, cu_seqlen
     if workspace is None:
         workspace = torch.empty(lib.gla_delta_bwd_workspace_bytes(n_seq, T, H, int(cu_seqlens is not None), dt),
                                 dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", None, dev)
     _run(lib.gla_delta_bwd, "gla_delta_bwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
          beta.data_ptr(), _addr(h0), _SCALE if scale is None else float(scale), dO.data_ptr(), _addr(dhT),
          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _addr(dh0), _addr(cu_seqlens),
