@@ -50,3 +50,19 @@ def test_decode_from_rows_argument_errors(lib):
         assert step(sdt=sdt, start=A + 2) == ALIGN and step(sdt=sdt, o=A + 4) == ALIGN
         assert step(sdt=sdt, N=0, q=None, start=None) == 0
     assert step(sdt=2) == DTYPE and step(sdt=-1) == DTYPE
+
+
+def test_workspace_sizes_are_those_stated():
+    """Bytes of a (chunk place, head) as include/gla.h has them, beside 256 bytes, the order and dbeta's parts."""
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "gla.h")).read()
+    stated = [int(x.replace(",", "")) for x in re.search(r"Workspaces: ([\d,]+) bytes.*?\(fp32 ([\d,]+)\).*?forward, ([\d,]+).*?\(fp32 ([\d,]+)\)",
+                                                         re.sub(r"\n \* ?", " ", text)).groups()]
+    N, T, H = 5, 64 * 700, 7
+    places = T // 64 + N
+    sizes = [(gla.gla_delta_workspace_bytes, 0), (gla.gla_delta_workspace_bytes, 1), (gla.gla_delta_bwd_workspace_bytes, 0),
+             (gla.gla_delta_bwd_workspace_bytes, 1)]
+    for (f, code), bytes_ in zip(sizes, stated):
+        size, least = f(N, T, H, True, code), places * H * bytes_
+        assert least <= size <= least + 256 + 4 * N + (48 * T * H if f is gla.gla_delta_bwd_workspace_bytes else 0), (f, code)
