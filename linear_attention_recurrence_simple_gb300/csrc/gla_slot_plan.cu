@@ -76,10 +76,12 @@ __device__ __forceinline__ void token_place(const int32_t* cu, const int32_t* se
 }
 
 // `ends`: the offsets are kept in shared memory and this CTA's tokens are written from there.
+// held and row may be the same array (no __restrict__): a thread reads a request's held, the last time too, before it writes
+// that request's row.
 __global__ void __launch_bounds__(THREADS, 1)
-slot_plan_kernel(const int32_t* __restrict__ new_len, const int32_t* __restrict__ held, const int32_t* __restrict__ seen, int N,
+slot_plan_kernel(const int32_t* __restrict__ new_len, const int32_t* held, const int32_t* __restrict__ seen, int N,
                  int rows, int budget, int32_t* __restrict__ cu, int32_t* __restrict__ slot, int32_t* __restrict__ start,
-                 int32_t* __restrict__ row, int32_t* __restrict__ token_seq, int32_t* __restrict__ token_pos, bool ends, unsigned* err) {
+                 int32_t* row, int32_t* __restrict__ token_seq, int32_t* __restrict__ token_pos, bool ends, unsigned* err) {
   extern __shared__ uint32_t sm[];
   __shared__ long long sums[2][WARPS];
   const int tid = threadIdx.x, words = (rows + 31) / 32;
