@@ -849,7 +849,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         const uint32_t at_a = lanes + (c & 1) * 128u, at_c = lanes + ((c & 1) ^ 1) * 128u;
         if (o_row && c > 0) outputs(c - 1);
         ok = ok && wait(SB_V, c) && wait(SB_A, c);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        // (one answer for the warp: lanes may leave a wait that runs out with different ones, and outputs() below is for all or none)
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const float* gt = reinterpret_cast<const float*>(sm + ScanSmem::GT);
         const float f_row = gt[GT_F + tok], b_row = gt[GT_B + tok], last = gt[GT_F + DC - 1];
