@@ -562,7 +562,10 @@ int gla_set_wait_limit_ns(unsigned long long ns);
  * warp of every CTA of gla_prefix_decode_step's bf16 kernel (its second) and of gla_tail_fold's bf16 and MXFP8
  * kernel gives up its wait for chunk `chunk` (of its own, from 0; below 4,096) as if the limit had passed.  role:
  * the decode's wait for keys (0) or values (1); the fold's issuing (0), widening (1; from chunk 2 on) or, for the
- * last chunk, storing warps (2).  role -1: no more. */
+ * last chunk, storing warps (2).  In the bf16 kernels of gla_delta_fwd and gla_delta_bwd `chunk` is 1024 x kernel (0: prep,
+ * 1: either scan, 2: reverse scan, 3: gradients) + 32 x the mbarrier's number + its phase (below 32), and those of the
+ * role that wait for it give up: the thread of the copies (0), that of the products (1) or the other warps (2).
+ * role -1: no more. */
 int gla_debug_give_up(int role, int chunk);
 
 /* Human-readable name of a gla_status value. */

@@ -186,8 +186,8 @@ def gla_debug_bounds() -> int:
 
 
 def gla_debug_give_up(role: int, chunk: int = 0) -> None:
-    """Makes one warp of the tails' decode and fold kernels give up its wait for ``chunk`` (debug-bounds build
-    only, for tests of the bounded waits; ``role`` -1: no more)."""
+    """Makes one warp of the tails' decode and fold kernels, or a role of the gated delta kernels, give up its wait for
+    ``chunk`` (debug-bounds build only, for tests of the bounded waits; ``role`` -1: no more)."""
     _check(load_library().gla_debug_give_up(int(role), int(chunk)), "gla_debug_give_up")
 
 

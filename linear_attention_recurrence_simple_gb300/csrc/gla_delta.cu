@@ -72,6 +72,7 @@ int gla_delta_fwd(const void* q, const void* k, const void* v, const void* g, co
   if (off16(workspace)) return GLA_ERR_ALIGN;
   rc = gla::current_device_state(&a.err, &a.wait_ns);
   if (rc) return rc;
+  a.wait_ns |= gla::debug_give_up();
   a.q = q;
   a.k = k;
   a.v = v;
@@ -122,6 +123,7 @@ int gla_delta_bwd(const void* q, const void* k, const void* v, const void* g, co
   if (off16(workspace)) return GLA_ERR_ALIGN;
   rc = gla::current_device_state(&a.err, &a.wait_ns);
   if (rc) return rc;
+  a.wait_ns |= gla::debug_give_up();
   a.q = q;
   a.k = k;
   a.v = v;

@@ -150,16 +150,21 @@ __device__ __forceinline__ void tm_free(uint32_t tmem) {
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 __device__ __forceinline__ uint32_t sw64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
 
-// mbar_wait with a look first: try_wait takes its time even where the phase has ended.  (For a thread that mostly finds
+// Who waits, for gla_debug_give_up: the role is 0 for the thread of the copies, 1 for that of the products, 2 for the warps
+// with rows; the chunk is the kernel, the barrier and the phase in one number (phases past 31 are not told apart: -1).
+enum { IN_PREP = 0, IN_SCAN, IN_RSCAN, IN_GRADS };
+__device__ __forceinline__ constexpr int wait_code(int kernel, int bar, int k) { return k < 32 ? kernel << 10 | bar << 5 | k : -1; }
+// mbar_wait_at with a look first: try_wait takes its time even where the phase has ended.  (For a thread that mostly finds
 // it ended: the reverse scan's issuer, 228 -> 213 us; the scans, whose two CTAs share an SM, lose 3 % to 10 % by it.)
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, volatile int* abort) {
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, volatile int* abort, int role, int code) {
+  if constexpr (kDebugBounds) return mbar_wait_at(bar, parity, limit_ns, abort, role, code);
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
-  return ok != 0 || mbar_wait(bar, parity, limit_ns, abort);
+  return ok != 0 || mbar_wait_at(bar, parity, limit_ns, abort, role, code);
 }
 
 constexpr unsigned long long DRAIN_NS = 1000000000ull;
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     else if (what == 2) cf[i] = decay(i | 15, i);
     else if (i >= 16 * (what - 2)) rf[(what - 3) * DC + i] = decay(i, 16 * (what - 2) - 1);
   }
-  bool ok = mbar_wait(bar, 0, a.wait_ns, abort_flag);
+  bool ok = mbar_wait_at(bar, 0, a.wait_ns, abort_flag, 2, wait_code(IN_PREP, 0, 0));
   if (ok && ch.len < DC)  // rows behind the last token may hold another sequence's
     for (int e = tid; e < 2 * (DC - ch.len) * 12; e += PREP_THREADS) {
       const int is_q = e / ((DC - ch.len) * 12), r = ch.len + e / 12 % (DC - ch.len);
@@ -660,7 +665,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   const DeltaSeq s = delta_seq(a, n);
   const int nc = (s.len + DC - 1) / DC;
   const int from = a.h0 ? delta_row(a.h0_row, a.h0_rows, n, a.err) : -1;
-  auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
+  const int role = warp == 9 ? 0 : warp == 8 ? 1 : 2;
+  auto wait = [&](int b, int k) { return mbar_wait_at(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag, role, wait_code(IN_SCAN, b, k)); };
 
   float2 S[16];
 #pragma unroll
@@ -1006,8 +1012,11 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot_tm;
-    auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
-    auto look = [&](int b, int k) { return bar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };  // (the issuing thread)
+    const int role = warp == 12 ? 0 : warp == 8 ? 1 : 2;
+    auto wait = [&](int b, int k) { return mbar_wait_at(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag, role, wait_code(IN_RSCAN, b, k)); };
+    auto look = [&](int b, int k) {  // (the issuing thread)
+      return bar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag, role, wait_code(IN_RSCAN, b, k));
+    };
     bool ok = true;
     if (warp == 12) {
       if (lane == 0) {
@@ -1346,7 +1355,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
   tc_fence_after();
   const uint32_t tmem = *slot_tm;
   const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-  auto wait = [&](int b, int k) { return mbar_wait(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag); };
+  const int role = warp == 8 ? 1 : 2;
+  auto wait = [&](int b, int k) { return mbar_wait_at(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag, role, wait_code(IN_GRADS, b, k)); };
   bool ok = true;
   if (warp == 8) {
     if (lane == 0) {
