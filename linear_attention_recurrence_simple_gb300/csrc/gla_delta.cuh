@@ -69,7 +69,16 @@ __device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs& a, int n) {
     s.len = a.T;
     s.slot0 = n * ((a.T + DC - 1) / DC);
   }
+  if (!GLA_IN_BOUNDS(s.len == 0 || (s.begin >= 0 && s.begin + s.len <= (a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T) &&
+                                    s.slot0 >= 0 && s.slot0 + (s.len + DC - 1) / DC <= a.slots), a.err))
+    s.len = 0;
   return s;
+}
+// The sequence of a scan's rank-th unit.
+__device__ __forceinline__ int delta_unit(const DeltaArgs& a, int rank) {
+  int n = a.order && GLA_IN_BOUNDS(rank < a.n_seq, a.err) ? a.order[rank] : rank;
+  if (!GLA_IN_BOUNDS(n >= 0 && n < a.n_seq, a.err)) n = 0;
+  return n;
 }
 
 // The chunk at a place: its first token and its tokens (0: the place is empty).  Whole warps.

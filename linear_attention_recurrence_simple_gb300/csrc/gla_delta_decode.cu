@@ -69,6 +69,7 @@ delta_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     if (tid == 0 && from != -1) raise_error(err, ERR_SHAPE);
     from = -1;
   }
+  if (!GLA_IN_BOUNDS(row >= 0 && row < pool_rows && from >= -1 && from < pool_rows && h < H, err)) return;
   SV* const S = reinterpret_cast<SV*>(state + ((long long)row * H + h) * (DK * DV));
   SV s[ROWS];
   if (ROWS_FROM && from < 0) {

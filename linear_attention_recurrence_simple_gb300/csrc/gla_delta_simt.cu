@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArg
   float* const sr = sp + DC * CS;      // [32][68]: columns of B R
   float* const su = sr + SB * CS;      // [32][68]: columns of U
   float* const sf = su + SB * CS;      // e^G, e^(G_C - G), beta
-  const int tile = blockIdx.x % SNB, nh = blockIdx.x / SNB, h = nh % a.H, n = nh / a.H, tid = threadIdx.x;
+  const int tile = blockIdx.x % SNB, nh = blockIdx.x / SNB, h = nh % a.H, n = delta_unit(a, nh / a.H), tid = threadIdx.x;
   const int c0 = tile * SB;
   const DeltaSeq s = delta_seq(a, n);
   const int from = a.h0 ? delta_row(a.h0_row, a.h0_rows, n, a.err) : -1;
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
   float* const sn = sw + SB * CS;
   float* const sd = sn + SB * CS;   // [32][68]: columns of dO, then weighted with s e^G
   float* const sf = sd + SB * CS;
-  const int tile = blockIdx.x % SNB, nh = blockIdx.x / SNB, h = nh % a.H, n = nh / a.H, tid = threadIdx.x;
+  const int tile = blockIdx.x % SNB, nh = blockIdx.x / SNB, h = nh % a.H, n = delta_unit(a, nh / a.H), tid = threadIdx.x;
   const int c0 = tile * SB;
   const DeltaSeq s = delta_seq(a, n);
   const long long tokens = a.cu_seqlens ? (long long)a.T : (long long)a.n_seq * a.T;

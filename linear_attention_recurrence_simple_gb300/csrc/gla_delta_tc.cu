@@ -379,7 +379,8 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     for (int off = 16; off > 0; off >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, off);
     if (lane == 0) dm[warp] = __int_as_float(rank);
     __syncthreads();
-    if (tid == 0) a.order[__float_as_int(dm[0]) + __float_as_int(dm[1]) + __float_as_int(dm[2]) + __float_as_int(dm[3])] = slot;
+    const int at = __float_as_int(dm[0]) + __float_as_int(dm[1]) + __float_as_int(dm[2]) + __float_as_int(dm[3]);
+    if (tid == 0 && GLA_IN_BOUNDS(at >= 0 && at < a.n_seq, a.err)) a.order[at] = slot;
     __syncthreads();
   }
   const DeltaChunk ch = chunk_of_slot(a, slot);
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + ScanSmem::BAR + 8 * SB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + ScanSmem::BAR + 8 * SB_N + 4);
   int* const issued = reinterpret_cast<int*>(sm + ScanSmem::BAR + 8 * SB_N + 8);  // [4] copies to each place
-  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = a.order ? a.order[nh / a.H] : nh / a.H;
+  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = delta_unit(a, nh / a.H);
   const int tid = threadIdx.x, warp = tid >> 5, q = warp & 3, half = (warp >> 2) & 1;
   const int row = (tid & 31) + 32 * q;  // lane of the products
   const int tok = row & 63;
@@ -976,7 +977,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + RSmem::BAR + 8 * RB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + RSmem::BAR + 8 * RB_N + 4);
   int* const issued = reinterpret_cast<int*>(sm + RSmem::BAR + 8 * RB_N + 8);  // [5] copies: EARLY's two places, K, K~; X
-  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = a.order ? a.order[nh / a.H] : nh / a.H;
+  const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = delta_unit(a, nh / a.H);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = (warp >> 2) & 1;
   const int row = lane + 32 * q, col0 = tile * TN + 32 * half;
   const bool t_row = warp >= 8 && q >= 2, s_row = warp < 8 && q < 3;

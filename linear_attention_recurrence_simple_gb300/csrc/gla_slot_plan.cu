@@ -60,14 +60,17 @@ __device__ __forceinline__ Request request_of(int len, int h, int rows, int budg
   return r;
 }
 
-__device__ __forceinline__ void token_place(const int32_t* cu, const int32_t* seen, int N, int t, int32_t* token_seq, int32_t* token_pos) {
+__device__ __forceinline__ void token_place(const int32_t* cu, const int32_t* seen, int N, int budget, int t, int32_t* token_seq,
+                                            int32_t* token_pos, unsigned* err) {
   int seq = -1, pos = -1;
+  if (!GLA_IN_BOUNDS(t >= 0 && t < budget, err)) return;
   if (t < cu[N]) {
     int lo = 0, hi = N - 1;  // the first request whose end is behind t
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
       if (cu[mid + 1] > t) hi = mid; else lo = mid + 1;
     }
+    if (!GLA_IN_BOUNDS(N > 0 && lo >= 0 && lo < N && t >= cu[lo] && t < cu[lo + 1], err)) return;
     seq = lo;
     pos = (seen ? seen[lo] : 0) + t - cu[lo];
   }
@@ -155,6 +158,7 @@ slot_plan_kernel(const int32_t* __restrict__ new_len, const int32_t* held, const
       uint32_t bits = ~used[lo];
       for (uint32_t skip = (uint32_t)i - before[lo]; skip > 0; --skip) bits &= bits - 1;
       mine = 32 * lo + __ffs((int)bits) - 1;
+      if (!GLA_IN_BOUNDS(lo >= 0 && lo < words && bits != 0 && mine < rows, err)) mine = -1;
     }
     cu[n] = begin;
     row[n] = mine;
@@ -168,14 +172,14 @@ slot_plan_kernel(const int32_t* __restrict__ new_len, const int32_t* held, const
   if (!ends) return;
   __syncthreads();
   for (int t = blockIdx.x * THREADS + tid; t < budget; t += gridDim.x * THREADS)  // (below 2^31: GLA_PLAN_MAX_BUDGET)
-    token_place(s_cu, seen, N, t, token_seq, token_pos);
+    token_place(s_cu, seen, N, budget, t, token_seq, token_pos, err);
 }
 
 __global__ void __launch_bounds__(256)
 slot_plan_tokens_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ seen, int N, int budget,
-                        int32_t* __restrict__ token_seq, int32_t* __restrict__ token_pos) {
+                        int32_t* __restrict__ token_seq, int32_t* __restrict__ token_pos, unsigned* err) {
   const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t < budget) token_place(cu, seen, N, t, token_seq, token_pos);
+  if (t < budget) token_place(cu, seen, N, budget, t, token_seq, token_pos, err);
 }
 
 }  // namespace
@@ -193,7 +197,7 @@ cudaError_t launch_slot_plan(const int32_t* new_len, const int32_t* held, const 
   const unsigned ctas = ends && row != held ? (unsigned)min(64, (budget + TOKENS - 1) / TOKENS) : 1u;
   slot_plan_kernel<<<ctas, THREADS, ends ? with_ends : maps, st>>>(new_len, held, seen, N, rows, budget, cu, slot, start, row, token_seq,
                                                                    token_pos, ends, err);
-  if (tokens && !ends) slot_plan_tokens_kernel<<<(budget + 255) / 256, 256, 0, st>>>(cu, seen, N, budget, token_seq, token_pos);
+  if (tokens && !ends) slot_plan_tokens_kernel<<<(budget + 255) / 256, 256, 0, st>>>(cu, seen, N, budget, token_seq, token_pos, err);
   return cudaGetLastError();
 }
 
