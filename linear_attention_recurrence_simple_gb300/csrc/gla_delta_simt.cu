@@ -205,9 +205,9 @@ constexpr int PREP_FLOATS = 2 * DC * KS + 2 * DC * CS;
 template <bool BWD>
 __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArgs a) {
   extern __shared__ __align__(16) float sm[];
-  float* const sk = sm;             // [64][100]
+  float* const sk = sm;             // [DC][KS]
   float* const sq = sk + DC * KS;
-  float* const m = sq + DC * KS;    // [64][68]: M and M B
+  float* const m = sq + DC * KS;    // [DC][CS]: M and M B
   float* const mb = m + DC * CS;
   __shared__ float2 sg[DC];
   __shared__ float sb[DC];
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(THREADS) delta_prep_simt_kernel(const DeltaArg
   if (tid < DC) {
     // Z = (1 + M B)^-1 M by forward substitution, a thread a column, 16 rows at a time: z_i = M_ic - sum_{j < i} (M B)_ij z_j.
     // (Loops over the blocks: written out, the code takes longer to be fetched than to run: prep 17 us instead of 13.)
-    float* const z = sq;  // [64][64], Q is done with
+    float* const z = sq;  // [DC][DC], Q is done with
 #pragma unroll 1
     for (int b = 0; b < DC; b += 16) {
       float y[16];
@@ -311,14 +311,14 @@ template <bool BWD>
 __global__ void __launch_bounds__(THREADS) delta_scan_simt_kernel(const DeltaArgs a) {
   wait_for_previous();
   extern __shared__ __align__(16) float sm[];
-  float* const S = sm;                 // [32][100]: columns of the state
-  float* const sk = S + SB * KS;       // [64][100]
+  float* const S = sm;                 // [SB][KS]: columns of the state
+  float* const sk = S + SB * KS;       // [DC][KS]
   float* const sq = sk + DC * KS;
-  float* const st = sq + DC * KS;      // [96][68]: K^T, weighted with e^(G_C - G)
-  float* const sz = st + DK * CS;      // [64][68]
+  float* const st = sq + DC * KS;      // [DK][CS]: K^T
+  float* const sz = st + DK * CS;      // [DC][CS]
   float* const sp = sz + DC * CS;
-  float* const sr = sp + DC * CS;      // [32][68]: columns of B R
-  float* const su = sr + SB * CS;      // [32][68]: columns of U
+  float* const sr = sp + DC * CS;      // [SB][CS]: columns of B R, then of e^(G_C - G) U
+  float* const su = sr + SB * CS;      // [SB][CS]: columns of U
   float* const sf = su + SB * CS;      // e^G, e^(G_C - G), beta
   const int tile = blockIdx.x % SNB, nh = blockIdx.x / SNB, h = nh % a.H, n = delta_unit(a, nh / a.H), tid = threadIdx.x;
   const int c0 = tile * SB;
@@ -439,15 +439,15 @@ constexpr int RSCAN_FLOATS = SB * KS + DC * KS + 2 * DK * CS + 2 * DC * CS + 3 *
 __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaArgs a, float* dbeta_part) {
   wait_for_previous();
   extern __shared__ __align__(16) float sm[];
-  float* const S = sm;              // [32][100]: columns of dS
-  float* const sk = S + SB * KS;    // [64][100]
-  float* const skt = sk + DC * KS;  // [96][68]: K^T, Q^T
+  float* const S = sm;              // [SB][KS]: columns of dS
+  float* const sk = S + SB * KS;    // [DC][KS]
+  float* const skt = sk + DC * KS;  // [DK][CS]: K^T, Q^T
   float* const sqt = skt + DK * CS;
-  float* const szt = sqt + DK * CS; // [64][68]: Z^T, P^T
+  float* const szt = sqt + DK * CS; // [DC][CS]: Z^T, P^T
   float* const spt = szt + DC * CS;
-  float* const sw = spt + DC * CS;  // [32][68]: columns of B dU, of -e^G dR
+  float* const sw = spt + DC * CS;  // [SB][CS]: columns of B dU, of -e^G dR
   float* const sn = sw + SB * CS;
-  float* const sd = sn + SB * CS;   // [32][68]: columns of dO, then weighted with s e^G
+  float* const sd = sn + SB * CS;   // [SB][CS]: columns of dO, then weighted with s e^G
   float* const sf = sd + SB * CS;
   const int tile = blockIdx.x % SNB, nh = blockIdx.x / SNB, h = nh % a.H, n = delta_unit(a, nh / a.H), tid = threadIdx.x;
   const int c0 = tile * SB;
@@ -560,8 +560,8 @@ __global__ void __launch_bounds__(THREADS) delta_rscan_simt_kernel(const DeltaAr
 // ---- gradients of the chunk ------------------------------------------------------------------
 // A cluster of two CTAs a (chunk, head), each with 32 rows of Es and Fm, which both need whole and write to each other,
 // and with 48 columns of d_k: short calls have few chunks (one CTA took 1.4 times as long).  Pieces of 32 columns
-// of d_v: dO, dR, U [64][36], S0, dS1 [48][36], the next piece's loads in flight; then Es, Fm and their transposes
-// [64][68] in their place.  K and Q [64][52], K^T and Q^T [48][68].
+// of d_v: dO, dR, U [DC][BS], S0, dS1 [HK][BS], the next piece's loads in flight; then Es, Fm and their transposes
+// [DC][CS] in their place.  K and Q [DC][HS], K^T and Q^T [HK][CS].
 constexpr int HK = DK / 2, HS = HK + 4;
 constexpr int PIECES = 3 * DC * BS + 2 * HK * BS, GRAD_FLOATS = 2 * DC * HS + 2 * HK * CS + (PIECES > 4 * DC * CS ? PIECES : 4 * DC * CS) + 4 * DC + 8;
 
@@ -644,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS) delta_grads
     gemm<1, 3, SB, BS, BS>(dks, su + my.warp_row * BS, sd + my.warp_col * BS);
   }
   cluster_sync();  // (neither reads its pieces any more)
-  float* const es = sdo;              // [64][68] Es, Fm, and their transposes
+  float* const es = sdo;              // [DC][CS] Es, Fm, and their transposes
   float* const fm = es + DC * CS;
   float* const est = fm + DC * CS;
   float* const fmt = est + DC * CS;
