@@ -12,8 +12,10 @@
 //           dv, every chunk's dS1 and its columns' part of dbeta
 //   grads   one CTA a (chunk, head): dq, dk, dg, and dbeta's parts summed in tile order
 // What carries the state is held in two bf16 (hi + lo: 16 bits): S, B R, K^, and K~, Q~, P, w, dS; [hi | lo] stand beside
-// each other as N = 128 columns of one product.  What only feeds a bf16 output (P^, Z, X, S0 and dS1 for the gradients) is one
-// bf16: o is 2.1e-3 of the norm from the exact one, of which its own rounding is 1.7e-3, dq, dk and dg 3e-3.
+// each other as N = 128 columns of one product.  So are X and the chunk's Es and Fm, which nearly every gradient goes through.
+// What else only feeds a bf16 output (P^, Z, S0 and dS1 for the gradients) is one bf16: o is 2.1e-3 of the norm from the
+// exact one, of which its own rounding is 1.7e-3, dq and dk 2.0e-3, dg 2.4e-3 (with X, Es and Fm in one bf16 3.0e-3, and the
+// backward of 8 x 2,048 x 16 in 675 us instead of 720).
 // What the chunk's length costs: longer chunks halve the scans' steps, but prep and grads grow with its square; 64 tokens
 // are also the 128 rows of [K; Q] and the 128 bytes of a swizzled row.
 #include <cuda.h>
@@ -176,8 +178,8 @@ constexpr unsigned long long DRAIN_NS = 1000000000ull;
 struct DeltaMaps {
   CUtensorMap k0, k1, q0, q1, v, o;
   CUtensorMap dO, dv, x, s0, ds;
-  CUtensorMap dvo, xo;  // (to write: 32 rows x 32 columns, one a warp)
-  CUtensorMap xsd;      // X, S0 and dS1: 256 rows x 64 columns
+  CUtensorMap dvo, xo, xlo;  // (to write: 32 rows x 32 columns, one a warp)
+  CUtensorMap xsd;      // X, S0 and dS1, half of their rows: 160 rows x 64 columns
   CUtensorMap dqo, dko; // (to write: 32 rows x 48 columns)
 };
 __device__ __forceinline__ void load_kq(const DeltaMaps& m, uint32_t p0, uint32_t p1, uint64_t* bar, int h, int t) {
@@ -196,9 +198,9 @@ constexpr uint32_t W_KD = 0, W_PH = 24576, W_OP = 32768, W_GT = W_OP;
 constexpr uint32_t W_FWD = W_GT + 512;
 enum { GT_F = 0, GT_B = DC, GT_E = 2 * DC, GT_SUM = 3 * DC };  // in floats
 // Backward: K~ = -(diag(e^G) K)^T (1 + B M^T)^-1 and Q~ = s (diag(e^G) Q)^T, hi and lo, P hi and lo; then what the
-// scans leave for the gradients, bf16 rows of 192: X (64), S0 and dS1 (96), one 256-row tile.
-constexpr uint32_t W_KR = W_GT + 1280, W_QT = W_KR + 24576, W_P = W_QT + 24576, W_X = W_P + 16384, W_S0 = W_X + DC * DV * 2,
-                   W_DS = W_S0 + DK * DV * 2, W_BWD = W_DS + DK * DV * 2;
+// scans leave for the gradients, bf16 rows of 192: X hi and lo (64 each), S0 and dS1 (96), one 320-row tile.
+constexpr uint32_t W_KR = W_GT + 1280, W_QT = W_KR + 24576, W_P = W_QT + 24576, W_X = W_P + 16384, W_XL = W_X + DC * DV * 2,
+                   W_S0 = W_XL + DC * DV * 2, W_DS = W_S0 + DK * DV * 2, W_BWD = W_DS + DK * DV * 2;
 static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_X % 32 == 0, "copies and tensor maps");
 
 // ---- prep -------------------------------------------------------------------------------------
@@ -814,6 +816,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
       float2 keep[16];  // e^G Q S0, or (STATES) R
       // The outputs of chunk c, from the place that its first product had.
       const uint32_t stage = sb + ScanSmem::OUT + 2048u * ((q & 1) + 2 * half);  // this warp's 32 rows x 32 columns
+      const uint32_t stage_lo = sb + ScanSmem::KQ0 + 2048u * ((q & 1) + 2 * half);  // (STATES: Q's place, whose products nobody looks at)
       auto outputs = [&](int c) {
         ok = __all_sync(0xffffffffu, wait(SB_O, c));
         if (!ok) return;
@@ -825,12 +828,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         __syncwarp();
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          uint32_t d[32], w[8];
+          uint32_t d[32], w[8], lo[8];
           tm_ld16x2(from_tm + 16 * x, from_tm + 64 + 16 * x, d);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 y = STATES ? fsub2(keep[8 * x + e], halves(d, e)) : fmul2(both(a.scale), fadd2(keep[8 * x + e], halves(d, e)));
-            w[e] = bf2(y.x, y.y);
+            if (STATES) split2(y, w[e], lo[e]);
+            else w[e] = bf2(y.x, y.y);
+          }
+          if (STATES) {
+            st_shared_v4(stage_lo + sw64(tid & 31, 2 * x), lo[0], lo[1], lo[2], lo[3]);
+            st_shared_v4(stage_lo + sw64(tid & 31, 2 * x + 1), lo[4], lo[5], lo[6], lo[7]);
           }
           if (STATES || left >= DC) {  // (X: zeros behind the last token, as its R)
             st_shared_v4(stage + sw64(tid & 31, 2 * x), w[0], w[1], w[2], w[3]);
@@ -847,8 +855,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           fence_async_smem();
           __syncwarp();
           if ((tid & 31) == 0) {
-            if (STATES) box_store(&maps.xo, stage, col0, 32 * (q & 1), (s.slot0 + c) * a.H + h);
-            else box_store(&maps.o, stage, col0, h, (int)(t0 + 32 * (q & 1)));
+            if (STATES) {
+              box_store(&maps.xo, stage, col0, 32 * (q & 1), (s.slot0 + c) * a.H + h);
+              box_store(&maps.xlo, stage_lo, col0, 32 * (q & 1), (s.slot0 + c) * a.H + h);
+            } else box_store(&maps.o, stage, col0, h, (int)(t0 + 32 * (q & 1)));
           }
         }
       };
@@ -1307,10 +1317,14 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 // place for the panels and three boxes instead of one 190 us.
 constexpr int GRAD_THREADS = 288;
 struct GSmem {
-  // a panel: [dO; dR], [X; S0], dS1; later Es and Fm in the first place, K and Q (two tiles of 64 columns each) in the second.
-  // (Products of 128 rows read before X, Es and Fm what is as still as they are.)  dq and dk leave from behind Es and Fm.
-  static constexpr uint32_t DOR = 0, XS = 16384, DS = XS + 20480, PANEL = DS + 12288, K = PANEL, Q = K + 16384, EF = 8192, OUT = EF + 16384;
-  static constexpr uint32_t GT = 2 * PANEL, CF = GT + 1280, DG = CF + 128, RED = DG + 4 * DC * 4, BAR = RED + 32, BYTES = BAR + 112;
+  // a panel: [dO; dR], X hi and lo, S0, dS1; later Es and Fm, hi and lo, where the first place's dO, dR and X were (S0 and dS1 may
+  // still be read), K and Q (two tiles of 64 columns each) and behind them dq and dk on their way out in the second.
+  // (Products of 128 rows read before X, Es and Fm what is as still as they are: the first place stands behind the second.)
+  static constexpr uint32_t DOR = 0, X = 16384, XL = X + 8192, S0 = XL + 8192, DS = S0 + 12288, PANEL = DS + 12288;
+  static constexpr uint32_t K = 0, Q = K + 16384, OUT = Q + 16384, EF = PANEL;
+  static constexpr uint32_t GT = 2 * PANEL, CF = GT + 768, BAR = CF + 128, BYTES = BAR + 112;
+  static constexpr uint32_t DG = PANEL + DS, RED = DG + 4 * DC * 4;  // (once all products have been)
+  __device__ static constexpr uint32_t place(int p) { return p & 1 ? 0u : PANEL; }
   static_assert(BYTES <= 115712, "two CTAs an SM");
   static_assert(OUT + 8 * 32 * 96 <= PANEL, "8 warps' rows");
 };
@@ -1325,8 +1339,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + GSmem::BAR);
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + GSmem::BAR + 8 * GB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + GSmem::BAR + 8 * GB_N + 4);
-  const float* const gt = reinterpret_cast<const float*>(sm + GSmem::GT);
-  const float2* const sums = reinterpret_cast<const float2*>(sm + GSmem::GT + 4 * GT_SUM);
+  const float* const strength = reinterpret_cast<const float*>(sm + GSmem::GT);
+  const float2* const sums = reinterpret_cast<const float2*>(sm + GSmem::GT + 4 * DC);
   float* const cf = reinterpret_cast<float*>(sm + GSmem::CF);
   float* const dgp = reinterpret_cast<float*>(sm + GSmem::DG);
   float* const red = reinterpret_cast<float*>(sm + GSmem::RED);
@@ -1365,23 +1379,32 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
       int panels = 0, kqs = 0;
       auto load_panel = [&](int p) {
         ++panels;
-        const uint32_t to = sb + (p & 1) * GSmem::PANEL;
+        const uint32_t to = sb + GSmem::place(p);
         uint64_t* const in = &bar[GB_IN + (p & 1)];
-        mbar_expect_tx(in, GSmem::PANEL + (p == 0 ? 1280 : 0));
+        mbar_expect_tx(in, GSmem::PANEL + (p == 0 ? 768 : 0));
         box_load(to + GSmem::DOR, &maps.dO, in, 64 * p, h, t);
         box_load(to + GSmem::DOR + 8192, &maps.dv, in, 64 * p, h, t);
-        box_load(to + GSmem::XS, &maps.xsd, in, 64 * p, 0, idx);
-        if (p == 0) bulk_load(sb + GSmem::GT, ws + W_GT, 1280, in);
+        box_load(to + GSmem::X, &maps.xsd, in, 64 * p, 0, idx);
+        box_load(to + GSmem::X + 20480, &maps.xsd, in, 64 * p, 160, idx);
+        if (p == 0) {
+          bulk_load(sb + GSmem::GT, ws + W_GT + 4 * GT_B, 256, in);
+          bulk_load(sb + GSmem::GT + 256, ws + W_GT + 4 * GT_SUM, 512, in);
+        }
       };
       auto products = [&](int p) {
-        const uint32_t at = sb + (p & 1) * GSmem::PANEL;
+        const uint32_t at = sb + GSmem::place(p);
         tc_fence_after();
-        const SDesc da = sdesc(at + GSmem::DOR, 16, 1024, LAYOUT_SW128), dx = sdesc(at + GSmem::XS, 16, 1024, LAYOUT_SW128);
-        const SDesc dx2 = sdesc(at + GSmem::XS - 8192, 16, 1024, LAYOUT_SW128), ds = sdesc(at + GSmem::DS, 16, 1024, LAYOUT_SW128);
+        const SDesc da = sdesc(at + GSmem::DOR, 16, 1024, LAYOUT_SW128), dx = sdesc(at + GSmem::X, 16, 1024, LAYOUT_SW128);
+        const SDesc ds0 = sdesc(at + GSmem::S0, 16, 1024, LAYOUT_SW128), ds = sdesc(at + GSmem::DS, 16, 1024, LAYOUT_SW128);
+        const SDesc dx2 = sdesc(at + GSmem::X - 8192, 16, 1024, LAYOUT_SW128);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma(tmem, da + kk * 32u, dx + kk * 32u, idesc_bf16(128, 160, 0, 0), p + kk > 0);
+        for (int kk = 0; kk < 8; ++kk)  // (X: hi, then lo)
+          umma(tmem, da + (kk & 3) * 32u, dx + (kk >> 2) * 8192u + (kk & 3) * 32u, idesc_bf16(128, 64, 0, 0), p + kk > 0);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_DS, dx2 + kk * 32u, ds + kk * 32u, idesc_bf16(128, 96, 0, 0), p + kk > 0);
+        for (int kk = 0; kk < 4; ++kk) umma(tmem + 64, da + kk * 32u, ds0 + kk * 32u, idesc_bf16(128, 96, 0, 0), p + kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma(tmem + GT_DS, dx2 + (kk >> 2) * 8192u + (kk & 3) * 32u, ds + (kk & 3) * 32u, idesc_bf16(128, 96, 0, 0), p + kk > 0);
         umma_commit(&bar[GB_MMA + p]);
       };
       load_panel(0);
@@ -1415,11 +1438,14 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
         const SDesc ef = sdesc(sb + GSmem::EF, 16, 1024, LAYOUT_SW128), et = sdesc(sb + GSmem::EF - 8192, 8192, 1024, LAYOUT_SW128);
         const SDesc dk = sdesc(sb + GSmem::K, 8192, 1024, LAYOUT_SW128), dq = sdesc(sb + GSmem::Q, 8192, 1024, LAYOUT_SW128);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma(tmem, ef + kk * 32u, dk + kk * 2048u, idesc_bf16(128, 96, 0, 1), kk > 0);
+        for (int kk = 0; kk < 8; ++kk)  // (hi, then lo)
+          umma(tmem, ef + (kk >> 2) * 16384u + (kk & 3) * 32u, dk + (kk & 3) * 2048u, idesc_bf16(128, 96, 0, 1), kk > 0);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + kk * 2048u, dq + kk * 2048u, idesc_bf16(128, 96, 1, 1), kk > 0);
+        for (int kk = 0; kk < 8; ++kk)
+          umma(tmem + GT_X2, et + (kk >> 2) * 16384u + (kk & 3) * 2048u, dq + (kk & 3) * 2048u, idesc_bf16(128, 96, 1, 1), kk > 0);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma(tmem + GT_X2, et + 8192u + kk * 2048u, dk + kk * 2048u, idesc_bf16(128, 96, 1, 1), 1);
+        for (int kk = 0; kk < 8; ++kk)
+          umma(tmem + GT_X2, et + 8192u + (kk >> 2) * 16384u + (kk & 3) * 2048u, dk + (kk & 3) * 2048u, idesc_bf16(128, 96, 1, 1), 1);
         umma_commit(&bar[GB_TWO]);
       } while (false);
       if (!ok) {  // the copies end before their memory is given up (else they have all been waited for)
@@ -1431,16 +1457,16 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
   } else {
     float frob = 0.f;  // <dS1, S0>, this thread's part
     for (int p = 0; p < 3 && ok; ++p) {
-      const uint32_t at = sb + (p & 1) * GSmem::PANEL;
+      const uint32_t at = sb + GSmem::place(p);
       ok = __all_sync(0xffffffffu, wait(GB_IN + (p & 1), p >> 1));
       if (!ok) break;
       if (p == 0 && tid < 32) {  // decay and strength of tokens 0-31 in those of 32-63: from there to token 31
         const float2 x = sums[31], y = sums[tid];
-        cf[tid] = exp2_fast((x.x - y.x) + (x.y - y.y)) * gt[GT_B + tid];
+        cf[tid] = exp2_fast((x.x - y.x) + (x.y - y.y)) * strength[tid];
       }
 #pragma unroll
       for (int e = tid; e < DK * 8; e += 256) {  // (768 pieces of 16 bytes; the two tiles are swizzled alike)
-        const uint4 x = ld_shared_v4(at + GSmem::XS + 8192 + 16 * e), y = ld_shared_v4(at + GSmem::DS + 16 * e);
+        const uint4 x = ld_shared_v4(at + GSmem::S0 + 16 * e), y = ld_shared_v4(at + GSmem::DS + 16 * e);
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -1468,15 +1494,15 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
         }
       const float2 gi = sums[i];
       const float sign = first ? a.scale : -1.f;
-      // Es and Fm: columns 32 half .. of row i, three kinds of blocks of 32 x 32
+      // Es and Fm, hi and lo: columns 32 half .. of row i, three kinds of blocks of 32 x 32
       const uint32_t to = sb + GSmem::EF + (first ? 0u : 8192u);
       const int rows = q & 1;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        uint32_t w[8];
+        uint32_t w[8], lo[8];
         if (half > rows) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = 0u;
+          for (int e = 0; e < 8; ++e) w[e] = lo[e] = 0u;
         } else {
           uint32_t d[32];
           tm_ld16(lanes + 32 * half + 16 * x, d);
@@ -1487,7 +1513,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
             for (int e = 0; e < 8; ++e) {
               const float2 c = *reinterpret_cast<const float2*>(cf + 16 * x + 2 * e);
               const float2 y = fmul2(fmul2(both(f), c), make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
-              w[e] = live ? bf2(y.x, y.y) : 0u;
+              split2(live ? y : both(0.f), w[e], lo[e]);
             }
           } else {
 #pragma unroll
@@ -1497,17 +1523,20 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
               for (int b = 0; b < 2; ++b) {
                 const int j = 32 * half + 16 * x + 2 * e + b;
                 const float2 gj = sums[j];
-                const float v = exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * (sign * gt[GT_B + j] * __uint_as_float(d[2 * e + b]));
+                const float v = exp2_fast((gi.x - gj.x) + (gi.y - gj.y)) * (sign * strength[j] * __uint_as_float(d[2 * e + b]));
                 y[b] = live && (first ? j <= i : j < i) ? v : 0.f;
               }
-              w[e] = bf2(y[0], y[1]);
+              split2(make_float2(y[0], y[1]), w[e], lo[e]);
             }
           }
         }
         st_shared_v4(to + sw128(i, 4 * half + 2 * x), w[0], w[1], w[2], w[3]);
         st_shared_v4(to + sw128(i, 4 * half + 2 * x + 1), w[4], w[5], w[6], w[7]);
+        st_shared_v4(to + 16384u + sw128(i, 4 * half + 2 * x), lo[0], lo[1], lo[2], lo[3]);
+        st_shared_v4(to + 16384u + sw128(i, 4 * half + 2 * x + 1), lo[4], lo[5], lo[6], lo[7]);
       }
-      const float f_row = sign * gt[GT_F + i], e_row = gt[GT_E + i] * gt[GT_B + i];
+      const float2 gl = sums[DC - 1];
+      const float f_row = sign * exp2_fast(gi.x + gi.y), e_row = exp2_fast((gl.x - gi.x) + (gl.y - gi.y)) * strength[i];
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
         uint32_t d[32];
@@ -1587,7 +1616,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) delta_grads_kernel(const __gr
       }
       dg += (with.x + with.y) - (less.x + less.y);
       dgp[(first ? 0 : 128) + 64 * half + i] = live ? dg : 0.f;
-      at_end = fmaf(gt[GT_F + DC - 1], frob, at_end);
+      at_end = fmaf(exp2_fast(sums[DC - 1].x + sums[DC - 1].y), frob, at_end);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) at_end += __shfl_xor_sync(0xffffffffu, at_end, off);
       if (lane == 0) {
@@ -1757,7 +1786,8 @@ cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t st) {
     if (!(input_maps(m, a) && rows_map(&m.dO, a.dO, DV, a, 64, DC) && rows_map(&m.dv, a.dv, DV, a, 64, DC) &&
           map3(&m.x, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 64, DC, 1) && map3(&m.s0, a.ws + W_S0, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) &&
           map3(&m.ds, a.ws + W_DS, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) && map3(&m.xo, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 32, 32, 1) &&
-          rows_map(&m.dvo, a.dv, DV, a, 32, 32) && map3(&m.xsd, a.ws + W_X, DV, 256, all, 2 * DV, W_BWD, 64, 256, 1) &&
+          rows_map(&m.dvo, a.dv, DV, a, 32, 32) && map3(&m.xsd, a.ws + W_X, DV, 320, all, 2 * DV, W_BWD, 64, 160, 1) &&
+          map3(&m.xlo, a.ws + W_XL, DV, DC, all, 2 * DV, W_BWD, 32, 32, 1) &&
           rows_map(&m.dqo, a.dq, DK, a, 48, 32) && rows_map(&m.dko, a.dk, DK, a, 48, 32)))
       return cudaErrorInvalidValue;
     delta_prep_kernel<true><<<chunks, PREP_THREADS, PrepSmem::bytes(true), st>>>(m, a, 0);
