@@ -452,7 +452,7 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
  * fp32 calls keep 22 bits of each operand of a product, and everything else in fp32 (2 to 4e-7 of the norm).
  * Sizes: chunk places (n_seq * ceil(T / 64); packed T_total / 64 + n_seq) * H * 96, and rows of h0
  * and hT * H * 96, below 2^31, else GLA_ERR_SHAPE.
- * Workspaces: 33,280 bytes (fp32 34,048) for each chunk place and head in the forward, 222,464 (fp32 230,656) and 24 (48) a
+ * Workspaces: 33,344 bytes (fp32 34,048) for each chunk place and head in the forward, 223,232 (fp32 230,656) and 24 (48) a
  * token and head in the backward, which keeps every chunk's states: 0.14 GB and 0.9 GB (fp32 0.14 and 0.96) for 16,384
  * tokens of 16 heads in one sequence, in proportion to the tokens.
  * Calls may be captured into a graph after a first call of the same kind on the device; calls that may overlap need

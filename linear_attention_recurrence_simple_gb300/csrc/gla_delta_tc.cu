@@ -11,14 +11,16 @@
 //   rscan   the same from the last chunk on: dU = s P^T dO + E K dS1, w = B dU, dS0 = e^(G_C) dS1 + Q~ dO + K~ w; writes
 //           dv, every chunk's dS1 and its columns' part of dbeta
 //   grads   one CTA a (chunk, head): dq, dk, dg, and dbeta's parts summed in tile order
-// What carries the state is held in two bf16 (hi + lo: 16 bits): S, B R, K^, and K~, Q~, P, w, dS; [hi | lo] stand beside
-// each other as N = 128 columns of one product.  So are X and the chunk's Es and Fm, which nearly every gradient goes through.
-// What else only feeds a bf16 output (P^, Z, S0 and dS1 for the gradients) is one bf16: o is 2.1e-3 of the norm from the
-// exact one, of which its own rounding is 1.7e-3, dq and dk 2.0e-3, dg 2.4e-3 (with X, Es and Fm in one bf16 3.0e-3, and the
-// backward of 8 x 2,048 x 16 in 675 us instead of 720).
+// States are fp32; what carries them from chunk to chunk enters the products as two halves, [hi | lo] beside each other as N = 128
+// columns.  K^, B R and K~, w are two fp16 (22 bits), as are prep's operands; S, dS, Q~ and P, beside operands that are
+// exact in bf16, two bf16 (16 bits).  For fp16's range keys are brought to a length of 1/2 to 1, and residuals scaled by a
+// bound (see prep and the scan).  P^ and Z are one fp16.  X, Es and Fm, which nearly every gradient goes through, are two
+// bf16; S0 and dS1 for the gradients one.  hT is 0.3 to 0.9e-6 of the norm from the exact one (with two bf16 throughout 4.4e-6),
+// o 1.7e-3, its own rounding (2.1e-3), dq and dk 2.0e-3, dg 2.4e-3 (with X, Es and Fm in one bf16 3.0e-3).
 // What the chunk's length costs: longer chunks halve the scans' steps, but prep and grads grow with its square; 64 tokens
 // are also the 128 rows of [K; Q] and the 128 bytes of a swizzled row.
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <string.h>
 
 #include "gla_delta.cuh"
@@ -66,16 +68,90 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return o;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-// columns 2 e and 2 e + 1 of a product that stands as [hi | lo], the halves added
+__device__ __forceinline__ float2 pair(const uint32_t (&d)[32], int e) { return make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])); }
+// columns 2 e and 2 e + 1 of a product that stands as [hi | lo], the halves added.  (Beside each other: a product's A operand is read
+// once for both, and that reading is what bounds these products; both into the same 64 columns, one after the other, the
+// scans take 60 us more.)
 __device__ __forceinline__ float2 halves(const uint32_t (&d)[32], int e) {
-  return fadd2(make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])),
-               make_float2(__uint_as_float(d[16 + 2 * e]), __uint_as_float(d[17 + 2 * e])));
+  return fadd2(pair(d, e), make_float2(__uint_as_float(d[16 + 2 * e]), __uint_as_float(d[17 + 2 * e])));
 }
 // A pair as two bf16 pairs, hi + lo.
 __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   hi = bf2(x.x, x.y);
   const float2 r = fsub2(x, widen2(hi));
   lo = bf2(r.x, r.y);
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// The same in fp16: 22 bits, for values that a power of two has brought into its range.
+__device__ __forceinline__ uint32_t hf2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void split2h(float2 x, uint32_t& hi, uint32_t& lo) {
+  // (cut off, not rounded: the first then needs no conversion back, and the second keeps 11 bits of what is left)
+  const float2 h = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xFFFFE000u), __uint_as_float(__float_as_uint(x.y) & 0xFFFFE000u));
+  const float2 r = fsub2(x, h);
+  hi = hf2(h.x, h.y);
+  lo = hf2(r.x, r.y);
+}
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) { return idesc_bf16(M, N, a_mn, b_mn) & ~(1u << 7 | 1u << 10); }
+// The power of two that brings `top` to 2^T .. 2^(T + 1), and its inverse.  (Of values below 2^-112 or so, and of zero, one that
+// brings them less far: both stay normal numbers.)
+template <int T>
+__device__ __forceinline__ float2 pow2_to(float top) {
+  const int e = min(max((int)(__float_as_uint(top) >> 23), T + 1), 254);
+  return make_float2(__uint_as_float((uint32_t)(254 + T - e) << 23), __uint_as_float((uint32_t)(e - T) << 23));
+}
+__device__ __forceinline__ float finite_size(float x) { return fabsf(x) < __int_as_float(0x7f800000) ? fabsf(x) : 0.f; }
+// The largest magnitude of a thread's values (a NaN does not count), and of a warp's.
+__device__ __forceinline__ float most_of(const float2 (&x)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = fmaxf(m, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+  return m;
+}
+__device__ __forceinline__ float warp_most(float m) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))); }
+__device__ __forceinline__ float most_of4(const float* m) {
+  const float4 x = *reinterpret_cast<const float4*>(m);
+  return fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+}
+// The largest finite magnitude in the first rows of a tile of 64 x 64 bf16 in 128-byte rows, by a whole warp.
+__device__ __forceinline__ float most_of_tile(uint32_t tile, int rows) {
+  const int lane = threadIdx.x & 31;
+  __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 4
+  for (int e = lane; e < 8 * rows; e += 32) {
+    const uint4 x = ld_shared_v4(tile + 16 * e);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    __nv_bfloat162 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    m = __hmax2(m, __hmax2(__hmax2(y[0], y[1]), __hmax2(y[2], y[3])));
+  }
+  float top = fmaxf(__low2float(m), __high2float(m));
+  if (!(top < __int_as_float(0x7f800000))) {
+    top = 0.f;
+#pragma unroll 1
+    for (int e = lane; e < 8 * rows; e += 32) {
+      const uint4 x = ld_shared_v4(tile + 16 * e);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(finite_size(__uint_as_float(w[i] << 16)), finite_size(__uint_as_float(w[i] & 0xFFFF0000u))));
+    }
+  }
+  return warp_most(top);
+}
+// (a power of two for the smallest residuals, times a large weight)
+__device__ __forceinline__ float no_more(float x) { return fminf(fmaxf(x, -3e38f), 3e38f); }
+// pow2_to for a bound that need not be a number: then nothing is.
+template <int T>
+__device__ __forceinline__ float2 pow2_of_bound(float bound) {
+  const float2 p = pow2_to<T>(bound);
+  return bound < __int_as_float(0x7f800000) ? p : both(__int_as_float(0x7fc00000));
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -104,11 +180,6 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
 }
 __device__ __forceinline__ void stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
@@ -191,17 +262,27 @@ __device__ __forceinline__ void load_kq(const DeltaMaps& m, uint32_t p0, uint32_
 }
 
 // ---- workspace of a (chunk place, head), in bytes --------------------------------------------
-// Operands as the swizzled tiles that the scans copy, 128-byte rows of 64 tokens: K^ hi and lo (96 rows, d_k), P^ or
-// (backward) Z (64 rows).  Then e^G, beta and (backward) e^(G_C - G), fp32 [64] each, and the sums of the logs to
-// base 2.
+// Operands as the swizzled tiles that the scans copy, 128-byte rows of 64 tokens, fp16: K^ hi and lo (96 rows, d_k), P^ or
+// (backward) Z (64 rows), all of keys of length 1/2 to 1 (see prep).  Then in fp32: e^G; beta times the power of two of
+// the key's length; numbers (below); (backward) the powers; beta; e^(G_C - G) (64 each); the sums of the logs to base 2.
 constexpr uint32_t W_KD = 0, W_PH = 24576, W_OP = 32768, W_GT = W_OP;
-constexpr uint32_t W_FWD = W_GT + 512;
-enum { GT_F = 0, GT_B = DC, GT_E = 2 * DC, GT_SUM = 3 * DC };  // in floats
-// Backward: K~ = -(diag(e^G) K)^T (1 + B M^T)^-1 and Q~ = s (diag(e^G) Q)^T, hi and lo, P hi and lo; then what the
+enum { GT_F = 0, GT_BC = DC, GT_SC = 2 * DC, GT_C = GT_SC + 16, GT_B = GT_C + DC, GT_E = GT_B + DC, GT_SUM = GT_E + DC, GT_ALL = GT_SUM + 2 * DC };  // in floats
+// Numbers: what the products of P^'s rows (16 each) and of K~ are to be multiplied with; and what bounds what the scans bring to
+// fp16, |S| the length of a state's column, v and d the largest of V and dO:
+//     |c beta R| <= CB v + UB |S|,  |c beta dU| <= UE |dS1| + UP d,  |dS0| <= LG (e^(G_C) |dS1| + WQ d)
+// and for |S1| (with x = beta |k|^2, e = v - k . S, a write turns |S|^2 to |S|^2 + 2 beta v e - beta (2 - x) e^2, which is
+// |S|^2 + beta v^2 / (2 - x) at most: a state's length grows with the root of the tokens)
+//     |S1| <= LG sqrt(e^(2 G_C) |S|^2 + A v^2)  (A >= 0),  or, where an x is near 2, LG (e^(G_C) |S| - A v)
+enum { SC_PH = 0, SC_KR = 4, SC_CB, SC_UB, SC_LG, SC_A, SC_UE, SC_UP, SC_WQ };
+constexpr uint32_t GT_SCAN = 4 * GT_C, GT_STATES = 4 * GT_B, GT_RSCAN = 4 * GT_SUM;  // what the scans read of it, in bytes
+constexpr float OP_SCALE = 64.f;  // K^ and Z, which are 1 at most (but where a recurrence grows), stand times this
+constexpr float ROOT_DK = 10.f;  // the length of a column of 96 over its largest, and some
+constexpr uint32_t W_FWD = W_GT + GT_SCAN;
+// Backward: K~ = -(diag(e^G) K)^T (1 + B M^T)^-1 in fp16, hi and lo; Q~ = s (diag(e^G) Q)^T and P in bf16, hi and lo; then what the
 // scans leave for the gradients, bf16 rows of 192: X hi and lo (64 each), S0 and dS1 (96), one 320-row tile.
-constexpr uint32_t W_KR = W_GT + 1280, W_QT = W_KR + 24576, W_P = W_QT + 24576, W_X = W_P + 16384, W_XL = W_X + DC * DV * 2,
+constexpr uint32_t W_KR = W_GT + 2048, W_QT = W_KR + 24576, W_P = W_QT + 24576, W_X = W_P + 16384, W_XL = W_X + DC * DV * 2,
                    W_S0 = W_XL + DC * DV * 2, W_DS = W_S0 + DK * DV * 2, W_BWD = W_DS + DK * DV * 2;
-static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_X % 32 == 0, "copies and tensor maps");
+static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && 4 * GT_ALL <= 2048 && GT_RSCAN % 16 == 0 && (4 * GT_B) % 16 == 0 && W_KR % 16 == 0 && W_X % 32 == 0, "copies and tensor maps");
 
 // ---- prep -------------------------------------------------------------------------------------
 // One CTA of 4 warps a (chunk, head), all products on mma.sync (m16n8k16): the blocks are 16 wide and each step
@@ -209,9 +290,11 @@ static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_X % 32 
 //   1  warp w: rows 16 w .. of Q K^T (P, kept in registers), and K K^T's blocks that (B M)'s column block 3 - w needs:
 //      off the diagonal as B operands (hi + lo) in shared memory, on it in fp32
 //   2  the diagonal blocks' inverses (1 + B M_bb)^-1 by substitution, one thread a row, fp32
-//   3  slabs of 16 rows y of y (1 + B M) = r, block by block from the last: Y_b = (R_b - sum_c Y_c BM_cb) W_b, each
-//      product hi hi + hi lo + lo hi
-// fp32 sums; what is carried from block to block has 16 bits.
+//   3  slabs of 16 rows y of y (1 + B M) = r, block by block from the last: R'_b = R_b - sum_c Y_c BM_cb,
+//      Y_b = R'_b + R'_b (W_b - 1), each product hi hi + hi lo + lo hi
+// fp32 sums; operands are two fp16 (22 bits).  For its range keys are brought to a length of 1/2 to 1 by powers of two c_j, exactly:
+// with k = c k', k u^T = k' (c u)^T, where c u = (c beta) x, so that K^, P^ and Z come out as those of k', and the scans weigh
+// their residuals with c beta instead of beta; the system is (1 + C B M C^-1), whose entries are below 4 where beta |k|^2 <= 2.
 // Bound by the latency of its chain (loads, products, a substitution of 16 steps, four of blocks) at 16 (backward 12) warps
 // an SM, held there by 128 (156) registers and 54 (64) KB: 8 sequences of 2,048 tokens x 16 heads, 4,096 CTAs, 70 us
 // (128), of which the bytes written take 20 (64).  With the products on tcgen05 and one thread a row of the substitution
@@ -219,7 +302,8 @@ static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && W_KR % 16 == 0 && W_X % 32 
 constexpr int PREP_THREADS = 128;
 struct PrepSmem {
   static constexpr uint32_t P0 = 0, P1 = 16384, STAGE = 24576, DM = STAGE, G = STAGE + 4 * 4096, B = G + DC * 8, F = B + DC * 4, E = F + DC * 4,
-                            CF = E + DC * 4, RF = CF + DC * 4, BAR = RF + 3 * DC * 4, FRAG = BAR + 256;
+                            CF = E + DC * 4, RF = CF + DC * 4, BAR = RF + 3 * DC * 4, PM = BAR + 16, C = BAR + 256, IC = C + DC * 4, BC = IC + DC * 4,
+                            LG = BC + DC * 4, NK = LG + DC * 4, EK = NK + DC * 4, FK = EK + DC * 4, FRAG = FK + DC * 4;
   static constexpr uint32_t bytes(bool bwd) { return FRAG + (bwd ? 20 : 10) * 1024; }
 };
 constexpr int DM_FLOATS = 4 * 16 * 20;
@@ -240,8 +324,8 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 __device__ __forceinline__ uint32_t kq_at(uint32_t sb, bool is_q, int r, int c) {
   return sb + (c < 8 ? PrepSmem::P0 + (is_q ? 8192u : 0u) + sw128(r, c) : PrepSmem::P1 + (is_q ? 4096u : 0u) + sw64(r, c - 8));
 }
-// 16 x 16 block of X Y^T, rows r0 .. of X and n0 .. of Y: two accumulators of 8 columns.
-__device__ __forceinline__ void block_dot(float (&d)[2][4], uint32_t sb, bool x_is_q, int r0, int n0) {
+// 16 x 16 block of X Y^T, rows r0 .. of X and n0 .. of Y (K or Q): two accumulators of 8 columns.
+__device__ __forceinline__ void block_dot(float (&d)[2][4], uint32_t sb, bool x_is_q, int r0, int n0, bool y_is_q = false) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) d[0][i] = d[1][i] = 0.f;
@@ -249,27 +333,37 @@ __device__ __forceinline__ void block_dot(float (&d)[2][4], uint32_t sb, bool x_
   for (int ks = 0; ks < 6; ++ks) {
     uint32_t x[4], y[4];
     ldsm4(x, kq_at(sb, x_is_q, r0 + (lane & 15), 2 * ks + (lane >> 4)));
-    ldsm4(y, kq_at(sb, false, n0 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
+    ldsm4(y, kq_at(sb, y_is_q, n0 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
     mma(d[0], x, y[0], y[1]);
     mma(d[1], x, y[2], y[3]);
   }
 }
-// Accumulators of 16 columns as an A operand, hi and lo.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Accumulators of 16 columns as an A operand, hi and lo, in fp16 or (BF) bf16.
+template <bool BF = false>
 __device__ __forceinline__ void to_operand(const float (&x)[2][4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) split2(make_float2(x[i >> 1][2 * (i & 1)], x[i >> 1][2 * (i & 1) + 1]), hi[i], lo[i]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = make_float2(x[i >> 1][2 * (i & 1)], x[i >> 1][2 * (i & 1) + 1]);
+    if (BF) split2(y, hi[i], lo[i]);
+    else split2h(y, hi[i], lo[i]);
+  }
 }
 // d += (hi + lo) times a 16 x 16 block of B operands, hi (h) and lo (l)
 __device__ __forceinline__ void block_mul(float (&d)[2][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint4 h, uint4 l) {
-  mma(d[0], lo, h.x, h.y);
-  mma(d[1], lo, h.z, h.w);
-  mma(d[0], hi, l.x, l.y);
-  mma(d[1], hi, l.z, l.w);
-  mma(d[0], hi, h.x, h.y);
-  mma(d[1], hi, h.z, h.w);
+  mma_f16(d[0], lo, h.x, h.y);
+  mma_f16(d[1], lo, h.z, h.w);
+  mma_f16(d[0], hi, l.x, l.y);
+  mma_f16(d[1], hi, l.z, l.w);
+  mma_f16(d[0], hi, h.x, h.y);
+  mma_f16(d[1], hi, h.z, h.w);
 }
-// Places of the B operands: -(B M) block (c, b), c > b, and the inverse of diagonal block b; from 10 on the same of
-// (B M^T): block (b, c), b < c, and the inverse.
+// Places of the B operands: -(B M) block (c, b), c > b, and the inverse of diagonal block b without its ones; from 10 on the
+// same of (B M^T): block (b, c), b < c, and the inverse.
 __device__ __forceinline__ constexpr int frag_off(int c, int b) { return c * (c - 1) / 2 + b; }
 __device__ __forceinline__ constexpr int frag_diag(int b) { return 6 + b; }
 
@@ -287,21 +381,22 @@ __device__ __forceinline__ void solve_slabs(float (&r)[N][4][2][4], const int (&
 #pragma unroll
     for (int before = 0; before < step; ++before) {
       const int c = UP ? before : 3 - before;
-      const uint8_t* f = frags + 1024 * (UP ? 10 + frag_off(b, c) : frag_off(c, b)) + 16 * lane;
+      const int id = UP ? 10 + frag_off(b, c) : frag_off(c, b);
+      const uint8_t* f = frags + 1024 * id + 16 * lane;
       const uint4 h = *reinterpret_cast<const uint4*>(f), l = *reinterpret_cast<const uint4*>(f + 512);
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (c <= top[i]) block_mul(r[i][b], s[i].hi[c], s[i].lo[c], h, l);
     }
-    const uint8_t* f = frags + 1024 * ((UP ? 10 : 0) + frag_diag(b)) + 16 * lane;
+    const int id = (UP ? 10 : 0) + frag_diag(b);
+    const uint8_t* f = frags + 1024 * id + 16 * lane;
     const uint4 h = *reinterpret_cast<const uint4*>(f), l = *reinterpret_cast<const uint4*>(f + 512);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (b <= top[i]) {
         to_operand(r[i][b], s[i].hi[b], s[i].lo[b]);
-        float y[2][4] = {};
-        block_mul(y, s[i].hi[b], s[i].lo[b], h, l);
-        to_operand(y, s[i].hi[b], s[i].lo[b]);
+        block_mul(r[i][b], s[i].hi[b], s[i].lo[b], h, l);
+        to_operand(r[i][b], s[i].hi[b], s[i].lo[b]);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[i].hi[b][e] = s[i].lo[b][e] = 0u;
@@ -309,7 +404,14 @@ __device__ __forceinline__ void solve_slabs(float (&r)[N][4][2][4], const int (&
     }
   }
 }
-// A slab's rows, copied out: 128-byte rows, with `lo_out` what the rounding to bf16 leaves, too.
+// The largest of a slab's values.
+__device__ __forceinline__ float most_of_slab(const float (&r)[4][2][4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) m = fmaxf(m, finite_size(r[e >> 3][(e >> 2) & 1][e & 3]));
+  return warp_most(m);
+}
+// A slab's rows, copied out: 128-byte rows, with `lo_out` what the rounding of the first leaves, too.
 __device__ __forceinline__ void store_slab(const Slab& s, uint8_t* sm, uint8_t* hi_out, uint8_t* lo_out) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* const stage = sm + PrepSmem::STAGE + 4096 * (threadIdx.x >> 5);
@@ -357,6 +459,15 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
   const uint32_t sb = smem_u32(sm);
   float* const dm = reinterpret_cast<float*>(sm + PrepSmem::DM);   // [4][16][20]: diagonal blocks of -B M, and of -B M^T
   uint8_t* const frags = sm + PrepSmem::FRAG;
+  float* const pm = reinterpret_cast<float*>(sm + PrepSmem::PM);  // [4] (backward) the largest |q|^2 of 16
+  // the powers of two of the keys' lengths, their inverses; c beta; the weights of K^'s and K~'s right-hand sides
+  float* const sc = reinterpret_cast<float*>(sm + PrepSmem::C);
+  float* const sic = reinterpret_cast<float*>(sm + PrepSmem::IC);
+  float* const sbc = reinterpret_cast<float*>(sm + PrepSmem::BC);
+  float* const slg = reinterpret_cast<float*>(sm + PrepSmem::LG);  // what a token lets the state grow by, to base 2: 0 in use
+  float* const snk = reinterpret_cast<float*>(sm + PrepSmem::NK);  // |k|^2
+  float* const sek = reinterpret_cast<float*>(sm + PrepSmem::EK);
+  float* const sfk = reinterpret_cast<float*>(sm + PrepSmem::FK);
   float2* const sg = reinterpret_cast<float2*>(sm + PrepSmem::G);  // sums of log2 decays
   float* const sbeta = reinterpret_cast<float*>(sm + PrepSmem::B);
   // e^G, e^(G_C - G); and the decays between blocks in two factors that are both at most 1: from token j to the end of its
@@ -425,6 +536,7 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
       const int i = 2 * lane + e;
       x[e] = i < ch.len ? to_f(gp[(long long)i * a.H]) : 0.f;
       sbeta[i] = i < ch.len ? to_f(bp[(long long)i * a.H]) : 0.f;
+      slg[i] = 1.44269502f * fmaxf(x[e], 0.f);
     }
     float2 s0, s1;
     delta_sums<true>(x[0], x[1], s0, s1);
@@ -456,8 +568,40 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     }
     return;
   }
+  // The keys' lengths are the diagonal of K K^T, whose block mb this warp needs below anyway.
+  const int mb = 3 - warp;
+  float kk[2][4];
+  block_dot(kk, sb, false, 16 * mb, 16 * mb);
+  const float2 kr_scale = pow2_to<6>(sf[0]);  // (e^G falls from token to token)
+  if (t == g >> 1) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int j = 16 * mb + 8 * n + g;
+      // c = 2^(e / 2), rounded up, for |k|^2 in 2^(e - 1) .. 2^e (1 for a key of zeros)
+      const float size = (g & 1) ? kk[n][2 * n + 1] : kk[n][2 * n];
+      const int e = (int)(__float_as_uint(size) >> 23) - 126, half = size > 0.f && e < 129 ? (e + 1) >> 1 : 0;
+      const float c = __uint_as_float((uint32_t)(127 + half) << 23), ic = __uint_as_float((uint32_t)(127 - half) << 23);
+      snk[j] = size;
+      sc[j] = c;
+      sic[j] = ic;
+      sbc[j] = c * sbeta[j];
+      sek[j] = OP_SCALE * ic * se[j];
+      if (BWD) sfk[j] = kr_scale.x * ic * sf[j];
+      cf[j] *= ic;
+      // (a write turns the state's columns by 1 - beta k k^T)
+      const float turn = fabsf(fmaf(-sbeta[j], size, 1.f));
+      if (!(turn <= 1.f + 1.f / 32)) slg[j] += log2f(turn);  // (beta 2 and keys of length 1 but for their rounding: left out)
+    }
+  }
+  if constexpr (BWD) {
+    float qq[2][4];
+    block_dot(qq, sb, true, 16 * warp, 16 * warp, true);
+    const float most = warp_most(t == g >> 1 ? fmaxf(finite_size((g & 1) ? qq[0][1] : qq[0][0]), finite_size((g & 1) ? qq[1][3] : qq[1][2])) : 0.f);
+    if (lane == 0) pm[warp] = most;
+  }
+  __syncthreads();
   // A block of Q K^T or K K^T, rows i of block rb and columns j of block cb, times the decays: off the diagonal (cb < rb),
-  // and on it, where only j < i (or, `with`, j <= i).
+  // and on it, where only j < i (or, `with`, j <= i); of keys k_j / c_j.
   auto off_diagonal = [&](float (&x)[2][4], bool is_q, int rb, int cb) {
     block_dot(x, sb, is_q, 16 * rb, 16 * cb);
     const float r0 = rf[cb * DC + 16 * rb + g], r1 = rf[cb * DC + 16 * rb + g + 8];
@@ -478,7 +622,7 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = g + 8 * (e >> 1), j = 8 * n + 2 * t + (e & 1);
-        x[n][e] = j < i || (with && j == i) ? decay(16 * rb + i, 16 * rb + j) * x[n][e] : 0.f;
+        x[n][e] = j < i || (with && j == i) ? decay(16 * rb + i, 16 * rb + j) * (sic[16 * rb + j] * x[n][e]) : 0.f;
       }
   };
   // This warp's 16 rows of either, in r[1]
@@ -505,10 +649,22 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
   float r[2][4][2][4];
   Slab out[2];
   rows_of(r[1], true);
+  float most_p = 0.f;
+  if constexpr (!BWD) most_p = most_of_slab(r[1]);
   if constexpr (BWD) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) to_operand(r[1][b], out[0].hi[b], out[0].lo[b]);
+    for (int b = 0; b < 4; ++b) {  // (P itself: what it is of the keys as they are)
+      float x[2][4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e >> 2][e & 3] = sc[16 * b + 8 * (e >> 2) + 2 * t + (e & 1)] * r[1][b][e >> 2][e & 3];
+      to_operand<true>(x, out[0].hi[b], out[0].lo[b]);
+    }
     rows_of(r[1], false);
+    const float i0 = sic[16 * warp + g], i1 = sic[16 * warp + g + 8];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[1][b][e >> 2][e & 3] *= e & 2 ? i1 : i0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       if (b > warp) continue;
@@ -518,23 +674,22 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = 8 * n + 2 * t + (e & 1);
-          x[n][e] = -sbeta[16 * b + j] * r[1][b][n][e];
+          x[n][e] = -(sbc[16 * b + j] * sc[16 * b + j]) * r[1][b][n][e];
           if (b == warp) dm[DM_FLOATS + (b * 16 + 15 - j) * 20 + 15 - (g + 8 * (e >> 1))] = x[n][e];
         }
       if (b != warp) put_frag(x, 10 + frag_off(warp, b));
     }
   }
-  const int mb = 3 - warp;
 #pragma unroll 1
   for (int jb = 0; jb <= mb; ++jb) {
-    float x[2][4];  // rows j, columns m
-    block_dot(x, sb, false, 16 * jb, 16 * mb);
     if (jb != mb) {
+      float x[2][4];  // rows j, columns m
+      block_dot(x, sb, false, 16 * jb, 16 * mb);
       const float c0 = cf[16 * jb + g], c1 = cf[16 * jb + g + 8];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const int m = 16 * mb + 8 * n + 2 * t;
-        const float2 w = fmul2(*reinterpret_cast<const float2*>(rf + jb * DC + m), *reinterpret_cast<const float2*>(sbeta + m));
+        const float2 w = fmul2(*reinterpret_cast<const float2*>(rf + jb * DC + m), *reinterpret_cast<const float2*>(sbc + m));
         const float2 y0 = fmul2(fmul2(both(-c0), w), make_float2(x[n][0], x[n][1])), y1 = fmul2(fmul2(both(-c1), w), make_float2(x[n][2], x[n][3]));
         x[n][0] = y0.x;
         x[n][1] = y0.y;
@@ -548,7 +703,7 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = g + 8 * (e >> 1), m = 8 * n + 2 * t + (e & 1);
-          dm[(mb * 16 + m) * 20 + j] = j < m ? -sbeta[16 * mb + m] * (decay(16 * mb + m, 16 * mb + j) * x[n][e]) : 0.f;
+          dm[(mb * 16 + m) * 20 + j] = j < m ? -sbc[16 * mb + m] * (decay(16 * mb + m, 16 * mb + j) * (sic[16 * mb + j] * kk[n][e])) : 0.f;
         }
     }
   }
@@ -566,24 +721,67 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     for (int m = 15; m > 0; --m)
 #pragma unroll
       for (int j = 0; j < m; ++j) y[j] = fmaf(y[m], x[m * 20 + j], y[j]);
-    __nv_bfloat16* const f = reinterpret_cast<__nv_bfloat16*>(frags + 1024 * ((up ? 10 : 0) + frag_diag(warp)));
+    const int id = (up ? 10 : 0) + frag_diag(warp);
+    __half* const f = reinterpret_cast<__half*>(frags + 1024 * id);
     const int flip = up ? 15 : 0, k = i ^ flip;  // (15 - i is i ^ 15)
     const int at_k = (((k & 7) >> 1) * 4 + (k >> 3)) * 2 + (k & 1);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {  // operand element (k, n)
       const int n = j ^ flip, at = (n & 7) * 32 + (n >> 3) * 4 + at_k;
-      const __nv_bfloat16 v = __float2bfloat16_rn(y[j]);
+      const float x = j == i ? 0.f : y[j];
+      const __half v = __float2half_rn(x);
       f[at] = v;
-      f[256 + at] = __float2bfloat16_rn(y[j] - __bfloat162float(v));
+      f[256 + at] = __float2half_rn(x - __half2float(v));
     }
   }
+  float* const gt = reinterpret_cast<float*>(ws + W_GT);
   if (tid < DC) {
-    float* const gt = reinterpret_cast<float*>(ws + W_GT);
     gt[GT_F + tid] = sf[tid];
-    gt[GT_B + tid] = sbeta[tid];
+    gt[GT_BC + tid] = sbc[tid];
     if (BWD) {
+      gt[GT_C + tid] = sc[tid];
+      gt[GT_B + tid] = sbeta[tid];
       gt[GT_E + tid] = se[tid];
       reinterpret_cast<float2*>(gt + GT_SUM)[tid] = sg[tid];
+    }
+  }
+  if (warp == 3) {
+    float cb = 0.f, ub = 0.f, ue = 0.f, up = 0.f, lg = 0.f, root = 0.f, linear = -1.f;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int j = lane + 32 * y;
+      const float c = sc[j], size = fabsf(sbc[j]), x = sbeta[j] * snk[j];
+      cb = fmaxf(cb, finite_size(size));
+      ub = fmaxf(ub, finite_size(sf[j] * c * size));
+      if (BWD) ue = fmaxf(ue, finite_size(se[j] * c * size));
+      if (BWD) up = fmaxf(up, finite_size(c * size));
+      lg += slg[j];
+      if (x >= 0.f && x <= 1.5f) root = fmaxf(root, __fdividef(sbeta[j], 2.f - x));
+      else linear = 1.f;
+    }
+    cb = warp_most(cb);
+    ub = warp_most(ub);
+    root = warp_most(root);
+    const bool near_two = __any_sync(0xffffffffu, linear > 0.f);
+    if (__any_sync(0xffffffffu, lg != 0.f))
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) lg += __shfl_xor_sync(0xffffffffu, lg, off);
+    if (lane == 0) {
+      gt[GT_SC + SC_CB] = cb;
+      gt[GT_SC + SC_UB] = ub;
+      gt[GT_SC + SC_LG] = exp2_fast(lg);
+      gt[GT_SC + SC_A] = near_two ? -DC * cb : DC * root;
+    }
+    if (BWD) {
+      ue = warp_most(ue);
+      up = warp_most(up);
+      const float wq = DC * fabsf(a.scale) * sqrtf(most_of4(pm));
+      if (lane == 0) {
+        gt[GT_SC + SC_UE] = ue;
+        gt[GT_SC + SC_UP] = wq * up;
+        gt[GT_SC + SC_WQ] = wq;
+        gt[GT_SC + SC_KR] = kr_scale.y;
+      }
     }
   }
   __syncthreads();
@@ -591,9 +789,15 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
   // another one of K^; of K~ (and Q~) warps 2 and 3 two.  (One copy of the code for all of that: the kernel is long enough
   // for its instructions to be fetched slower than they run.)
   if (BWD) store_slab(out[0], sm, ws + W_P + 2048 * warp, ws + W_P + 8192 + 2048 * warp);
+  {  // P^'s rows by what their largest calls for, with room for what the solution grows by
+    const float2 by = BWD ? both(OP_SCALE) : pow2_to<4>(most_p);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) r[1][e >> 3][(e >> 2) & 1][e & 3] *= by.x;
+    if (!BWD && lane == 0) gt[GT_SC + SC_PH + warp] = by.y;
+  }
 #pragma unroll 1
   for (int x = warp; x < 6; x += 4) {
-    transposed_slab(r[0], sb, false, 16 * x, se, 1.f);
+    transposed_slab(r[0], sb, false, 16 * x, sek, 1.f);
     solve_slabs<false, 2>(r, {3, x == warp ? warp : -1}, frags, out);
     store_slab(out[0], sm, ws + W_KD + 2048 * x, ws + W_KD + 12288 + 2048 * x);
     if (x == warp) store_slab(out[1], sm, ws + W_PH + 2048 * warp, nullptr);
@@ -601,8 +805,8 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
   if constexpr (BWD) {
     auto store_kr = [&](const Slab& s, int x) { store_slab(s, sm, ws + W_KR + 2048 * x, ws + W_KR + 12288 + 2048 * x); };
     const int up0 = warp < 2 ? warp : 2 * warp - 2, ups = warp < 2 ? 1 : 2;
-    transposed_slab(r[0], sb, false, 16 * up0, sf, -1.f);
-    if (ups > 1) transposed_slab(r[1], sb, false, 16 * up0 + 16, sf, -1.f);
+    transposed_slab(r[0], sb, false, 16 * up0, sfk, -1.f);
+    if (ups > 1) transposed_slab(r[1], sb, false, 16 * up0 + 16, sfk, -1.f);
     solve_slabs<true, 2>(r, {3, ups > 1 ? 3 : -1}, frags, out);
     store_kr(out[0], up0);
     if (ups > 1) store_kr(out[1], up0 + 1);
@@ -610,7 +814,7 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     for (int x = up0; x < up0 + ups; ++x) {
       transposed_slab(r[0], sb, true, 16 * x, sf, a.scale);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) to_operand(r[0][b], out[0].hi[b], out[0].lo[b]);
+      for (int b = 0; b < 4; ++b) to_operand<true>(r[0][b], out[0].hi[b], out[0].lo[b]);
       store_slab(out[0], sm, ws + W_QT + 2048 * x, ws + W_QT + 12288 + 2048 * x);
     }
   }
@@ -640,13 +844,14 @@ struct ScanSmem {
   // (the state before K^, P^ behind it, K^ before P^, B R behind it) is as still as the operand meanwhile, and the rows
   // it gives are not looked at.
   static constexpr uint32_t KQ0 = 0, KQ1 = 16384, S = 24576, OP = S + 24576, BR = OP + W_OP, V = BR + 16384, OUT = V + 8192,
-                            GT = OUT + 8192, BAR = GT + 512, BYTES = BAR + 112;
+                            GT = OUT + 8192, BAR = GT + GT_STATES, MX = BAR + 128, BYTES = MX + 48;
   static_assert(BYTES <= 115712, "two CTAs an SM");
 };
 // Products ([K; Q] S, K^ B R, P^ B R), copies (K and Q; V and decays; K^; P^), hand-overs (the state, B R and the first
 // product read; the outputs' product read).  Whoever waits for a phase hands something over before the next one of the
 // same barrier can end.
-enum { SB_A = 0, SB_C, SB_O, SB_KQ, SB_V, SB_KD, SB_PH, SB_SR, SB_WR, SB_OF, SB_DRAIN, SB_N };
+// (MX: the power of two for the residuals is there.)
+enum { SB_A = 0, SB_C, SB_O, SB_KQ, SB_V, SB_KD, SB_PH, SB_SR, SB_WR, SB_OF, SB_MX, SB_DRAIN, SB_N };
 
 template <bool STATES>
 __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, int flip_every) {
@@ -657,6 +862,10 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + ScanSmem::BAR + 8 * SB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + ScanSmem::BAR + 8 * SB_N + 4);
   int* const issued = reinterpret_cast<int*>(sm + ScanSmem::BAR + 8 * SB_N + 8);  // [4] copies to each place
+  // by the chunk's parity, the power of two that brings c beta R to fp16, and its inverse [2]; the largest of the first state, of
+  // its six warps
+  float2* const by = reinterpret_cast<float2*>(sm + ScanSmem::MX);
+  float* const most_s = reinterpret_cast<float*>(by + 2);
   const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = delta_unit(a, nh / a.H);
   const int tid = threadIdx.x, warp = tid >> 5, q = warp & 3, half = (warp >> 2) & 1;
   const int row = (tid & 31) + 32 * q;  // lane of the products
@@ -700,8 +909,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
     bool ok = true;
     auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * (STATES ? W_BWD : W_FWD); };
     if (warp == 9) {
-      if (tid == 288) {
-        // a chunk's operands, each as soon as the chunk before is done with their place
+      {
+        // One thread's: a chunk's operands, each as soon as the chunk before is done with their place.
         int loads[4] = {};
         auto load_rows = [&](int c) {
           ++loads[0];
@@ -717,9 +926,9 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         };
         auto load_v = [&](int c) {
           ++loads[1];
-          mbar_expect_tx(&bar[SB_V], 8192 + 512);
+          mbar_expect_tx(&bar[SB_V], 8192 + (STATES ? GT_STATES : GT_SCAN));
           box_load(sb + ScanSmem::V, &maps.v, &bar[SB_V], tile * TN, h, (int)(s.begin + (long long)c * DC));
-          bulk_load(sb + ScanSmem::GT, ws_of(c) + W_GT, 512, &bar[SB_V]);
+          bulk_load(sb + ScanSmem::GT, ws_of(c) + W_GT, STATES ? GT_STATES : GT_SCAN, &bar[SB_V]);
         };
         auto load_kd = [&](int c) {
           ++loads[2];
@@ -743,23 +952,55 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           box_prefetch(&maps.v, tile * TN, h, t);
           bulk_prefetch(ws_of(c), W_FWD);
         };
-        load_rows(0);
-        load_v(0);
-        load_kd(0);
-        load_ph(0);
-        if (nc > 1) prefetch(1);
-        for (int c = 0; c + 1 < nc && ok; ++c) {
-          if (c + 2 < nc) prefetch(c + 2);
-          if (!(ok = wait(SB_A, c))) break;
-          load_rows(c + 1);
-          if (!(ok = wait(SB_WR, c))) break;  // (V and the decays have been read)
-          load_v(c + 1);
-          if (!(ok = wait(SB_C, c))) break;
-          load_kd(c + 1);
-          if (!(ok = wait(SB_O, c))) break;
-          load_ph(c + 1);
+        // The warp's: what bounds c beta R of chunk c (its largest, or the state's, would have to go from warp to warp on the state's way,
+        // 20 to 60 us more) and the power of two that brings that to fp16.
+        float length = 0.f;  // of a column of the state, at most
+        auto bound = [&](int c) {
+          ok = __all_sync(0xffffffffu, ok && wait(SB_V, c) && (c > 0 || wait(SB_SR, 0)));
+          if (!ok) return;
+          const float v = most_of_tile(sb + ScanSmem::V, min(DC, s.len - c * DC));
+          const float* gt = reinterpret_cast<const float*>(sm + ScanSmem::GT + 4 * GT_SC);
+          const float cb = gt[SC_CB], ub = gt[SC_UB], growth = gt[SC_LG], grown = gt[SC_A], last = gt[GT_F + DC - 1 - GT_SC];
+          if (c == 0) {
+            const float2* m = reinterpret_cast<const float2*>(most_s);
+            length = ROOT_DK * fmaxf(fmaxf(fmaxf(m[0].x, m[0].y), fmaxf(m[1].x, m[1].y)), fmaxf(m[2].x, m[2].y));
+          }
+          const float2 p = pow2_of_bound<14>(cb * v + ub * length);
+          if (tid == 288) {
+            by[c & 1] = p;
+            mbar_arrive(&bar[SB_MX]);
+          }
+          length *= last;
+          const float add = grown >= 0.f ? sqrtf(grown) * v : -grown * v, most = fmaxf(length, add);
+          length = growth * (grown >= 0.f && most > 1e-18f && most < 1e18f ? sqrtf(fmaf(length, length, add * add)) : length + add);
+        };
+        if (tid == 288) {
+          load_rows(0);
+          load_v(0);
+          load_kd(0);
+          load_ph(0);
+          if (nc > 1) prefetch(1);
         }
-        for (int x = 0; x < 4; ++x) issued[x] = loads[x];
+        bound(0);
+        for (int c = 0; c + 1 < nc && ok; ++c) {
+          if (tid == 288) {
+            if (c + 2 < nc) prefetch(c + 2);
+            ok = wait(SB_A, c);
+            if (ok) load_rows(c + 1);
+            ok = ok && wait(SB_WR, c);  // (V and the decays have been read)
+            if (ok) load_v(c + 1);
+            ok = ok && wait(SB_C, c);
+            if (ok) load_kd(c + 1);
+          }
+          __syncwarp();
+          bound(c + 1);
+          if (tid == 288 && ok) {
+            ok = wait(SB_O, c);
+            if (ok) load_ph(c + 1);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);  // (one answer for the warp)
+        }
+        for (int x = 0; x < 4 && tid == 288; ++x) issued[x] = loads[x];
       }
       __syncwarp();
     } else if (warp == 8) {
@@ -775,6 +1016,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 #pragma unroll
           for (int kk = 0; kk < 6; ++kk)
             umma(at_a, kk < 4 ? d0 + kk * 32u : d1 + (kk - 4) * 32u, ds + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          if (!(ok = wait(SB_MX, c))) break;  // (whoever has waited for the product then has the bound, too)
           umma_commit(&bar[SB_A]);
           // (the state's high halves are what the gradients take of it)
           if (STATES) box_store(&maps.s0, sb + ScanSmem::S, tile * TN, 0, (s.slot0 + c) * a.H + h);
@@ -782,12 +1024,12 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           if (STATES) stores_read();  // (the state is written again once the next product is there)
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma(at_c, dk + (kk >> 2) * 12288u + (kk & 3) * 32u, db + (kk & 3) * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          for (int kk = 0; kk < 8; ++kk)  // hi [hi | lo], lo hi
+            umma(at_c, dk + (kk >> 2) * 12288u + (kk & 3) * 32u, db + (kk & 3) * 2048u, idesc_f16(128, kk < 4 ? 128 : 64, 0, 1), kk > 0);
           umma_commit(&bar[SB_C]);
           if (!(ok = wait(SB_PH, c))) break;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma(at_a, dp + kk * 32u, db + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          for (int kk = 0; kk < 4; ++kk) umma(at_a, dp + kk * 32u, db + kk * 2048u, idesc_f16(128, 128, 0, 1), kk > 0);
           umma_commit(&bar[SB_O]);
         }
         stores_read();
@@ -810,10 +1052,13 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
       if (s_row) {
         put_state(0);
         put_state(1);
+        const float most = warp_most(most_of(S));
+        if ((tid & 31) == 0) most_s[(flip ? q - 1 : q) + 3 * half] = most;
         fence_async_smem();
         mbar_arrive(&bar[SB_SR]);
       }
       float2 keep[16];  // e^G Q S0, or (STATES) R
+      float o_by = 0.f;  // what P^'s, or Z's, row of a product is to be multiplied with
       // The outputs of chunk c, from the place that its first product had.
       const uint32_t stage = sb + ScanSmem::OUT + 2048u * ((q & 1) + 2 * half);  // this warp's 32 rows x 32 columns
       const uint32_t stage_lo = sb + ScanSmem::KQ0 + 2048u * ((q & 1) + 2 * half);  // (STATES: Q's place, whose products nobody looks at)
@@ -824,6 +1069,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         const uint32_t from_tm = lanes + (c & 1) * 128u;
         const int left = s.len - c * DC;
         const long long t0 = s.begin + (long long)c * DC;
+        const float f = o_by;
         if ((tid & 31) == 0) stores_read();
         __syncwarp();
 #pragma unroll
@@ -832,7 +1078,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           tm_ld16x2(from_tm + 16 * x, from_tm + 64 + 16 * x, d);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 y = STATES ? fsub2(keep[8 * x + e], halves(d, e)) : fmul2(both(a.scale), fadd2(keep[8 * x + e], halves(d, e)));
+            const float2 y = STATES ? fmadd2(both(-f), halves(d, e), keep[8 * x + e]) : fmul2(both(a.scale), fmadd2(both(f), halves(d, e), keep[8 * x + e]));
             if (STATES) split2(y, w[e], lo[e]);
             else w[e] = bf2(y.x, y.y);
           }
@@ -870,14 +1116,15 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const float* gt = reinterpret_cast<const float*>(sm + ScanSmem::GT);
-        const float f_row = gt[GT_F + tok], b_row = gt[GT_B + tok], last = gt[GT_F + DC - 1];
+        const float2 p2 = by[c & 1];
+        const float f_row = gt[GT_F + tok], last = gt[GT_F + DC - 1], br = no_more(gt[GT_BC + tok] * p2.x), f = p2.y * (1.f / OP_SCALE);
+        if (o_row) o_by = STATES ? f * gt[GT_C + tok] : p2.y * gt[GT_SC + SC_PH + (tok >> 4)];
         const bool live = tok < s.len - c * DC;  // (rows behind the last hold the next sequence's)
+        if (r_row) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (STATES && !r_row) break;
-          uint32_t d[32];
-          tm_ld16x2(at_a + 16 * x, at_a + 64 + 16 * x, d);
-          if (r_row) {
+          for (int x = 0; x < 2; ++x) {
+            uint32_t d[32];
+            tm_ld16x2(at_a + 16 * x, at_a + 64 + 16 * x, d);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const uint32_t piece = sw128(tok, 4 * half + 2 * x + p);
@@ -889,12 +1136,17 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
                 float2 r = fmadd2(both(-f_row), halves(d, 4 * p + e), widen2(vw[e]));
                 r = live ? r : both(0.f);
                 if (STATES) keep[8 * x + 4 * p + e] = r;
-                split2(fmul2(both(b_row), r), hi[e], lo[e]);
+                split2h(fmul2(both(br), r), hi[e], lo[e]);
               }
               st_shared_v4(sb + ScanSmem::BR + piece, hi[0], hi[1], hi[2], hi[3]);
               st_shared_v4(sb + ScanSmem::BR + 8192 + piece, lo[0], lo[1], lo[2], lo[3]);
             }
-          } else {
+          }
+        } else if (!STATES) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t d[32];
+            tm_ld16x2(at_a + 16 * x, at_a + 64 + 16 * x, d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) keep[8 * x + e] = fmul2(both(f_row), halves(d, e));
           }
@@ -903,6 +1155,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
         tc_fence_before();
         mbar_arrive(&bar[SB_WR]);
         if (s_row) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[e] = fmul2(both(last), S[e]);
           if (!(ok = __all_sync(0xffffffffu, wait(SB_C, c)))) break;
           tc_fence_after();
 #pragma unroll
@@ -910,7 +1164,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
             uint32_t d[32];
             tm_ld16x2(at_c + 16 * x, at_c + 64 + 16 * x, d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) S[8 * x + e] = fmadd2(both(last), S[8 * x + e], halves(d, e));
+            for (int e = 0; e < 8; ++e) S[8 * x + e] = fmadd2(both(f), halves(d, e), S[8 * x + e]);
             if (c + 1 < nc) put_state(x);
           }
           fence_async_smem();
@@ -970,13 +1224,13 @@ struct RSmem {
   // rows: before K, whose rows are the second half, 8 KB that are never written; before Z and P, and behind K~ and Q~, what
   // is as still as the operand itself.  The rows that gives are not looked at.
   static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 8192, S = K1 + 4096, W = S + 24576, OUT = W + 16384,
-                            GT = OUT + 8192, BAR = GT + 2 * 768, BYTES = BAR + 176;
+                            GT = OUT + 8192, BAR = GT + 2 * GT_RSCAN, MX = BAR + 192, BYTES = MX + 64;
   static_assert(BYTES <= 232448, "shared memory");
 };
 // Products and copies, then hand-overs: the state, w, Z^T w and X read.  Whoever waits for a phase of a barrier hands
 // something over before the next one can end; where that would not hold (E's, the decays', ZF) there are two, by the
 // chunk's parity.
-enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_DRAIN, RB_ZF, RB_GT = RB_ZF + 2, RB_X = RB_GT + 2, RB_N = RB_X + 2 };
+enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_DRAIN, RB_ZF, RB_GT = RB_ZF + 2, RB_X = RB_GT + 2, RB_MX = RB_X + 2, RB_N = RB_MX + 2 };
 constexpr uint32_t RT_P = 0, RT_Q = 64, RT_A = 128, RT_C = 256, RT_Z = 384;
 
 __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, float* dbeta_part) {
@@ -987,6 +1241,9 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + RSmem::BAR + 8 * RB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + RSmem::BAR + 8 * RB_N + 4);
   int* const issued = reinterpret_cast<int*>(sm + RSmem::BAR + 8 * RB_N + 8);  // [5] copies: EARLY's two places, K, K~; X
+  // by the chunk's parity, the power of two that brings w to fp16, and its inverse [2]; the largest of the last dS, of its six warps
+  float2* const by = reinterpret_cast<float2*>(sm + RSmem::MX);
+  float* const most_s = reinterpret_cast<float*>(by + 2);
   const int tile = blockIdx.x % NTILE, nh = blockIdx.x / NTILE, h = nh % a.H, n = delta_unit(a, nh / a.H);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, half = (warp >> 2) & 1;
   const int row = lane + 32 * q, col0 = tile * TN + 32 * half;
@@ -1051,10 +1308,10 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           const int c = nc - 1 - it, t = (int)(s.begin + (long long)c * DC);
           ++loads[2];
           mbar_expect_tx(&bar[RB_K], 12288);
-          mbar_expect_tx(&bar[RB_GT + (it & 1)], 768);
+          mbar_expect_tx(&bar[RB_GT + (it & 1)], GT_RSCAN);
           box_load(sb + RSmem::K0, &maps.k0, &bar[RB_K], 0, h, t);
           box_load(sb + RSmem::K1, &maps.k1, &bar[RB_K], 64, h, t);
-          bulk_load(sb + RSmem::GT + (it & 1) * 768, ws_of(c) + W_GT, 768, &bar[RB_GT + (it & 1)]);
+          bulk_load(sb + RSmem::GT + (it & 1) * GT_RSCAN, ws_of(c) + W_GT, GT_RSCAN, &bar[RB_GT + (it & 1)]);
         };
         auto load_kr = [&](int it) {
           const int c = nc - 1 - it;
@@ -1068,7 +1325,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           box_prefetch(&maps.k0, 0, h, t);
           box_prefetch(&maps.k1, 64, h, t);
           box_prefetch(&maps.dO, tile * TN, h, t);
-          bulk_prefetch(ws_of(c) + W_PH, 8192 + 1280);
+          bulk_prefetch(ws_of(c) + W_PH, 8192 + 4 * GT_ALL);
           bulk_prefetch(ws_of(c) + W_KR, 24576 + 24576 + 16384);
         };
         load_early(0);
@@ -1125,6 +1382,8 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 #pragma unroll
           for (int kk = 0; kk < 6; ++kk)
             umma(tmem + RT_A, kk < 4 ? k0 + kk * 32u : k1 + (kk - 4) * 32u, ds + kk * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          ok = look(RB_MX + (it & 1), it >> 1);  // (whoever has waited for the product then has the bound, too)
+          if (!ok) break;
           umma_commit(&bar[RB_A]);
           // (the state's high halves are what the gradients take of it)
           box_store(&maps.ds, sb + RSmem::S, tile * TN, 0, (s.slot0 + nc - 1 - it) * a.H + h);
@@ -1142,21 +1401,40 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           const SDesc dr = sdesc(sb + RSmem::KR, 16, 1024, LAYOUT_SW128), dz = sdesc(sb + RSmem::KR + 24576 - 8192, 8192, 1024, LAYOUT_SW128);
           const SDesc dw = sdesc(sb + RSmem::W, 8192, 1024, LAYOUT_SW128);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma(tmem + RT_C, dr + (kk >> 2) * 12288u + (kk & 3) * 32u, dw + (kk & 3) * 2048u, idesc_bf16(128, 128, 0, 1), kk > 0);
+          for (int kk = 0; kk < 8; ++kk)  // hi [hi | lo], lo hi
+            umma(tmem + RT_C, dr + (kk >> 2) * 12288u + (kk & 3) * 32u, dw + (kk & 3) * 2048u, idesc_f16(128, kk < 4 ? 128 : 64, 0, 1), kk > 0);
           umma_commit(&bar[RB_C]);
           ok = it == 0 || look(RB_ZF + ((it - 1) & 1), (it - 1) >> 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma(tmem + RT_Z, dz + kk * 2048u, dw + kk * 2048u, idesc_bf16(128, 64, 1, 1), kk > 0);
+            umma(tmem + RT_Z, dz + kk * 2048u, dw + kk * 2048u, idesc_f16(128, 64, 1, 1), kk > 0);
           umma_commit(&bar[RB_Z]);
           if (it + 1 < nc) ok = early(it + 1);
         }
         stores_read();
       }
       __syncwarp();
+    } else if (warp == 9) {
+      // what bounds w of each chunk and the power of two that brings that to fp16
+      float length = 0.f;  // of a column of dS, at most
+      for (int it = 0; it < nc; ++it) {
+        ok = wait(RB_EF + (it & 1), it >> 1) && wait(RB_GT + (it & 1), it >> 1) && (it > 0 || wait(RB_SR, 0));
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const float d = most_of_tile(sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES + RSmem::E_DO, min(DC, s.len - (nc - 1 - it) * DC));
+        const float* gt = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * GT_RSCAN + 4 * GT_SC);
+        const float growth = gt[SC_LG];
+        if (it == 0) {
+          const float2* m = reinterpret_cast<const float2*>(most_s);
+          length = ROOT_DK * fmaxf(fmaxf(fmaxf(m[0].x, m[0].y), fmaxf(m[1].x, m[1].y)), fmaxf(m[2].x, m[2].y));
+        }
+        if (lane == 0) {
+          by[it & 1] = pow2_of_bound<14>(gt[SC_UE] * length + growth * gt[SC_UP] * d);
+          mbar_arrive(&bar[RB_MX + (it & 1)]);
+        }
+        length = growth * fmaf(gt[GT_F + DC - 1 - GT_SC], length, gt[SC_WQ] * d);
+      }
     } else if (s_row) {
       const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 32u * half;
       auto put_state = [&](int x) {  // hi and lo for the next chunk's product
@@ -1172,13 +1450,16 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
       };
       put_state(0);
       put_state(1);
+      const float most = warp_most(most_of(S));
+      if (lane == 0) most_s[q + 3 * half] = most;
       fence_async_smem();
       mbar_arrive(&bar[RB_SR]);
       for (int it = 0; it < nc; ++it) {
         ok = wait(RB_GT + (it & 1), it >> 1) && wait(RB_C, it);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const float last = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * 768)[GT_F + DC - 1];
+        const float* gt = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * GT_RSCAN);
+        const float last = gt[GT_F + DC - 1], f = by[it & 1].y * gt[GT_SC + SC_KR];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t d[32], y[32];
@@ -1186,8 +1467,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           tm_ld16(lanes + RT_Q + 16 * x, y);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            S[8 * x + e] = fmadd2(both(last), S[8 * x + e],
-                                  fadd2(halves(d, e), make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]))));
+            S[8 * x + e] = fmadd2(both(last), S[8 * x + e], fmadd2(both(f), halves(d, e), pair(y, e)));
           if (it + 1 < nc) put_state(x);
         }
         fence_async_smem();
@@ -1204,8 +1484,10 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         ok = wait(RB_GT + (it & 1), it >> 1) && wait(RB_E + (it & 1), it >> 1) && wait(RB_A, it);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const float* gt = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * 768);
+        const float* gt = reinterpret_cast<const float*>(sm + RSmem::GT + (it & 1) * GT_RSCAN);
+        const float2 p2 = by[it & 1];
         const float b_row = gt[GT_B + tok], e_row = gt[GT_E + tok];
+        const float wr = no_more(gt[GT_BC + tok] * p2.x), z_by = gt[GT_C + tok] * (p2.y / OP_SCALE);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t d[32], p[32], hi[8], lo[8];
@@ -1213,11 +1495,10 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           tm_ld16(lanes + RT_P + 16 * x, p);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float2 r = fmadd2(both(e_row), halves(d, e),
-                              fmul2(both(a.scale), make_float2(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]))));
+            float2 r = fmadd2(both(e_row), halves(d, e), fmul2(both(a.scale), pair(p, e)));
             r = live ? r : both(0.f);  // (rows behind the last hold the next sequence's)
             du[8 * x + e] = r;
-            split2(fmul2(both(b_row), r), hi[e], lo[e]);
+            split2h(fmul2(both(wr), r), hi[e], lo[e]);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -1234,6 +1515,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         float2 part = both(0.f);
+        const float2 minus_z = both(-z_by);
         const long long t0 = s.begin + (long long)c * DC;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -1246,7 +1528,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int at = 4 * i + e;
-              const float2 t = fsub2(du[8 * x + at], make_float2(__uint_as_float(z[2 * at]), __uint_as_float(z[2 * at + 1])));
+              const float2 t = fmadd2(minus_z, pair(z, at), du[8 * x + at]);
               part = fmadd2(t, widen2(xw[e]), part);
               const float2 y = fmul2(both(b_row), t);
               w[at] = bf2(y.x, y.y);

@@ -69,3 +69,60 @@ def test_keys_of_other_lengths(size, beta, dtype):
     b.x["k"] = b.x["k"] * 30 / 96 ** 0.5 * size
     b.x["beta"] = b.x["beta"] * beta / max(1.0, size * size * beta / 1.6)
     hold(b, bf16 if dtype == BF else lambda name: 2e-6)
+
+
+@pytest.mark.parametrize("size", [1e-25, 1e-8, 1e4, 1e20])
+def test_values_of_other_sizes(size):
+    """Everything is linear in (v, h0) and in (dO, dhT): sizes far outside fp16's range, or fp32's of squares, change nothing.
+    (dbeta, dg and dk are products of both, so that one goes up as the other goes down.)"""
+    b = Batch(104, LENS[:4], 3, BF)
+    for name, by in (("v", size), ("dO", 1 / size)):
+        b.x[name] = b.x[name] * by
+    b.h0, b.dhT = b.h0 * size, b.dhT / size
+    hold(b, bf16)
+
+
+@pytest.mark.parametrize("what", ["outliers", "quiet", "silent", "keys", "states"])
+def test_sizes_side_by_side(what):
+    """Tokens of very different sizes in one chunk and from chunk to chunk: each bound that the kernels go by is far above most of
+    what it bounds."""
+    b = Batch(105, [400, 64, 130, 1], 2, BF)
+    T = int(b.cu[-1])
+    if what == "outliers":      # a few values a thousand times the others
+        b.x["v"][::67] *= 1000
+        b.x["dO"][5::71] *= 1000
+    elif what == "quiet":       # large first, small after
+        b.x["v"] *= torch.where(torch.arange(T) % 400 < 100, 1000.0, 1.0)[:, None, None]
+    elif what == "silent":      # nothing is written: what there is comes from the first state
+        b.x["v"][:] = 0
+        b.x["v"][300:] = torch.randn(T - 300, 2, 192, generator=torch.Generator().manual_seed(6))
+    elif what == "keys":        # lengths over five orders, writing strengths against them
+        s = 10.0 ** (torch.arange(T) % 6 - 3.0)
+        b.x["k"] *= s[:, None, None]
+        b.x["beta"] /= (s * s)[:, None].clamp(min=1.0)
+    else:                       # first states far above what is written
+        b.h0, b.dhT = b.h0 * 1e5, b.dhT * 1e5
+    # (where all of a gradient comes from S0, dS1 and dR, it has three roundings beside its own: sqrt(4) of 1.6e-3)
+    hold(b, lambda name: bf16(name) if name in ("o", "hT", "dv", "dh0") or what not in ("keys", "states") else 3.3e-3)
+
+
+@pytest.mark.parametrize("strength", ["usual", "one", "two"])
+def test_long_sequences_without_decay(strength):
+    """States over thousands of tokens that forget nothing: against the fp32 call on the same values, whose states are 6e-7 of
+    the norm from the exact ones."""
+    b = Batch(106, [6000, 3000], 1, BF)
+    b.x["g"][:] = 0
+    if strength != "usual":
+        b.x["beta"][:] = 1.0 if strength == "one" else 1.9
+    x, dO, cu = b.inputs(), b.dev("dO")[0], b.cu_dev
+    wide = [t.float() for t in x]
+    got = [*gla.gla_delta_fwd(*x, h0=b.h0.cuda(), cu_seqlens=cu), *gla.gla_delta_bwd(*x, dO, h0=b.h0.cuda(), dhT=b.dhT.cuda(), cu_seqlens=cu)]
+    want = [*gla.gla_delta_fwd(*wide, h0=b.h0.cuda(), cu_seqlens=cu),
+            *gla.gla_delta_bwd(*wide, dO.float(), h0=b.h0.cuda(), dhT=b.dhT.cuda(), cu_seqlens=cu)]
+    errors = {n: far(g, w)[0] for n, g, w in zip(("o", "hT", *NAMES, "dh0"), got, want)}
+    print({n: f"{x:.2e}" for n, x in errors.items()})
+    # (what states have gathered over thousands of tokens outweighs what a chunk adds: as with first states above)
+    # (a strength of 1.9 leaves 0.81 of the square of what stands under a key, one of 0.5 a quarter: errors live four times as long,
+    # twice in the norm: 1.6e-3 and twice sqrt(3) of it)
+    rest = 5.8e-3 if strength == "two" else 3.3e-3
+    assert all(x <= (bf16(n) if n in ("o", "hT", "dv", "dh0") else rest) for n, x in errors.items())
