@@ -443,17 +443,19 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
  *                recurrence itself grows.  (Keys of unit length and strengths in [0, 1] are the usual form.)  They
  *                and their gradients need the alignment of their type only: a slice of a packed array will do.
  * q, k, v, o, states, scale, cu_seqlens, dtype and the layouts are those of gla_chunk_fwd.  A call's tokens are
- * handled in chunks of 64; an infinity or a NaN in a token reaches every output of its chunk and what follows it in
- * its sequence, and nothing of another sequence.  cu_seqlens is checked on the device: offsets that decrease or pass
+ * handled in chunks of 64; an infinity or a NaN in a token, or an infinity in a state, reaches every output of its chunk
+ * and what follows it in its sequence and head (in the backward also what comes before), and nothing of another.  cu_seqlens is checked on the device: offsets that decrease or pass
  * T are clamped and record GLA_ERR_SHAPE.  Its last offset may stand below T (a step under its budget): the forward
  * leaves such rows of o as they were, the backward writes zeros to the gradients of such rows.
- * bf16 calls hold what carries a state from chunk to chunk in fp32 and in pairs of bf16 (16 bits: hT and dh0 are 3 to
- * 5e-6 of the norm from the exact ones); what only feeds an output of dtype bf16 may be rounded to bf16 once more.
- * fp32 calls keep 22 bits of each operand of a product, and everything else in fp32 (2 to 4e-7 of the norm).
+ * bf16 calls hold states in fp32 and what carries them from chunk to chunk in 16 to 24 bits (hT and dh0 are 0.2 to 1.2e-6
+ * of the norm from the exact ones, up to 1e-5 where thousands of tokens forget nothing).  o, dv and dbeta are their own
+ * rounding away (1.7e-3 of the norm), dq and dk 1.7 to 2.3e-3, dg up to 2.9e-3: the states that they are made of are rounded
+ * to bf16 on the way.  A caller who wants more makes the fp32 call on the same values: it keeps 22 bits of each operand of
+ * a product, and everything else in fp32 (1 to 4e-7 of the norm, dg 8e-7).
  * Sizes: chunk places (n_seq * ceil(T / 64); packed T_total / 64 + n_seq) * H * 96, and rows of h0
  * and hT * H * 96, below 2^31, else GLA_ERR_SHAPE.
- * Workspaces: 33,344 bytes (fp32 34,048) for each chunk place and head in the forward, 223,232 (fp32 230,656) and 24 (48) a
- * token and head in the backward, which keeps every chunk's states: 0.14 GB and 0.9 GB (fp32 0.14 and 0.96) for 16,384
+ * Workspaces: 33,344 bytes (fp32 34,048) for each chunk place and head in the forward, 235,520 (fp32 230,656) and 24 (48) a
+ * token and head in the backward, which keeps every chunk's states: 0.14 GB and 1.0 GB (fp32 0.14 and 0.96) for 16,384
  * tokens of 16 heads in one sequence, in proportion to the tokens.
  * Calls may be captured into a graph after a first call of the same kind on the device; calls that may overlap need
  * workspaces of their own. */

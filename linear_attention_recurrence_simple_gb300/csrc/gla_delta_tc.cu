@@ -12,11 +12,12 @@
 //           dv, every chunk's dS1 and its columns' part of dbeta
 //   grads   one CTA a (chunk, head): dq, dk, dg, and dbeta's parts summed in tile order
 // States are fp32; what carries them from chunk to chunk enters the products as two halves, [hi | lo] beside each other as N = 128
-// columns.  K^, B R and K~, w are two fp16 (22 bits), as are prep's operands; S, dS, Q~ and P, beside operands that are
-// exact in bf16, two bf16 (16 bits).  For fp16's range keys are brought to a length of 1/2 to 1, and residuals scaled by a
-// bound (see prep and the scan).  P^ and Z are one fp16.  X, Es and Fm, which nearly every gradient goes through, are two
-// bf16; S0 and dS1 for the gradients one.  hT is 0.3 to 0.9e-6 of the norm from the exact one (with two bf16 throughout 4.4e-6),
-// o 1.7e-3, its own rounding (2.1e-3), dq and dk 2.0e-3, dg 2.4e-3 (with X, Es and Fm in one bf16 3.0e-3).
+// columns.  K^, B R and K~, w are two fp16 (22 bits), as are prep's operands; beside operands that are exact in bf16, Q~ is
+// three bf16 (24 bits) and S, dS and P two (16 bits).  For fp16's range keys are brought to a length of 1/2 to 1, and residuals
+// scaled by a bound (see prep and the scan).  P^ and Z are one fp16.  X, Es and Fm, which nearly every gradient goes through,
+// are two bf16; S0 and dS1 for the gradients one.  hT and dh0 are 0.2 to 0.9e-6 of the norm from the exact ones (with two bf16
+// throughout 4.4 and 3.1e-6), o and dbeta 1.7e-3, their own rounding (2.1 and 2.3e-3), dq and dk 2.0e-3 and dg 2.4e-3 (with X,
+// Es and Fm in one bf16 3.0e-3).  What that costs: forward of 8 x 2,048 x 16 221 -> 261 us, backward 675 -> 770.
 // What the chunk's length costs: longer chunks halve the scans' steps, but prep and grads grow with its square; 64 tokens
 // are also the 128 rows of [K; Q] and the 128 bytes of a swizzled row.
 #include <cuda.h>
@@ -244,8 +245,8 @@ constexpr unsigned long long DRAIN_NS = 1000000000ull;
 
 // Tensor maps of a call.  K and Q: a chunk's 64 rows in two boxes, columns 0-63 (128-byte rows) and 64-95 (64-byte
 // rows).  V: 64 rows x 64 columns.  O: 32 rows x 32 columns, one a warp.
-// (backward) dO: 64 rows x 64 columns; K and Q in two boxes of 64 columns (96 on: zeros); dv as dO; X, S0 and dS1 of the
-// workspace: 64 or 96 rows x 64 columns of a (chunk place, head).
+// (backward) dO: 64 rows x 64 columns; K and Q in two boxes of 64 columns (96 on: zeros); dv as dO; X (hi and lo), S0 and
+// dS1 of the workspace: 128 or 96 rows x 64 columns of a (chunk place, head).
 struct DeltaMaps {
   CUtensorMap k0, k1, q0, q1, v, o;
   CUtensorMap dO, dv, x, s0, ds;
@@ -278,9 +279,9 @@ constexpr uint32_t GT_SCAN = 4 * GT_C, GT_STATES = 4 * GT_B, GT_RSCAN = 4 * GT_S
 constexpr float OP_SCALE = 64.f;  // K^ and Z, which are 1 at most (but where a recurrence grows), stand times this
 constexpr float ROOT_DK = 10.f;  // the length of a column of 96 over its largest, and some
 constexpr uint32_t W_FWD = W_GT + GT_SCAN;
-// Backward: K~ = -(diag(e^G) K)^T (1 + B M^T)^-1 in fp16, hi and lo; Q~ = s (diag(e^G) Q)^T and P in bf16, hi and lo; then what the
+// Backward: K~ = -(diag(e^G) K)^T (1 + B M^T)^-1 in fp16, hi and lo; Q~ = s (diag(e^G) Q)^T in three bf16, P in two; then what the
 // scans leave for the gradients, bf16 rows of 192: X hi and lo (64 each), S0 and dS1 (96), one 320-row tile.
-constexpr uint32_t W_KR = W_GT + 2048, W_QT = W_KR + 24576, W_P = W_QT + 24576, W_X = W_P + 16384, W_XL = W_X + DC * DV * 2,
+constexpr uint32_t W_KR = W_GT + 2048, W_QT = W_KR + 24576, W_P = W_QT + 36864, W_X = W_P + 16384, W_XL = W_X + DC * DV * 2,
                    W_S0 = W_XL + DC * DV * 2, W_DS = W_S0 + DK * DV * 2, W_BWD = W_DS + DK * DV * 2;
 static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && 4 * GT_ALL <= 2048 && GT_RSCAN % 16 == 0 && (4 * GT_B) % 16 == 0 && W_KR % 16 == 0 && W_X % 32 == 0, "copies and tensor maps");
 
@@ -296,9 +297,9 @@ static_assert(W_FWD % 16 == 0 && W_BWD % 256 == 0 && 4 * GT_ALL <= 2048 && GT_RS
 // with k = c k', k u^T = k' (c u)^T, where c u = (c beta) x, so that K^, P^ and Z come out as those of k', and the scans weigh
 // their residuals with c beta instead of beta; the system is (1 + C B M C^-1), whose entries are below 4 where beta |k|^2 <= 2.
 // Bound by the latency of its chain (loads, products, a substitution of 16 steps, four of blocks) at 16 (backward 12) warps
-// an SM, held there by 128 (156) registers and 54 (64) KB: 8 sequences of 2,048 tokens x 16 heads, 4,096 CTAs, 70 us
-// (128), of which the bytes written take 20 (64).  With the products on tcgen05 and one thread a row of the substitution
-// 137.
+// an SM, held there by 128 (168) registers and 56 (66) KB: 8 sequences of 2,048 tokens x 16 heads, 4,096 CTAs, 77 us
+// (153), of which the bytes written take 20 (76); with operands of two bf16 and Q~ in two 69 (127).  With the products on
+// tcgen05 and one thread a row of the substitution 137.
 constexpr int PREP_THREADS = 128;
 struct PrepSmem {
   static constexpr uint32_t P0 = 0, P1 = 16384, STAGE = 24576, DM = STAGE, G = STAGE + 4 * 4096, B = G + DC * 8, F = B + DC * 4, E = F + DC * 4,
@@ -353,14 +354,18 @@ __device__ __forceinline__ void to_operand(const float (&x)[2][4], uint32_t (&hi
     else split2h(y, hi[i], lo[i]);
   }
 }
-// d += (hi + lo) times a 16 x 16 block of B operands, hi (h) and lo (l)
-__device__ __forceinline__ void block_mul(float (&d)[2][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint4 h, uint4 l) {
+// r += (hi + lo) times a 16 x 16 block of B operands, hi (h) and lo (l).  (The tensor cores cut sums off: on r, which is larger than
+// what comes to it, hT would be 0.8e-6 of the norm off instead of 0.6.)
+__device__ __forceinline__ void block_mul(float (&r)[2][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint4 h, uint4 l) {
+  float d[2][4] = {};
   mma_f16(d[0], lo, h.x, h.y);
   mma_f16(d[1], lo, h.z, h.w);
   mma_f16(d[0], hi, l.x, l.y);
   mma_f16(d[1], hi, l.z, l.w);
   mma_f16(d[0], hi, h.x, h.y);
   mma_f16(d[1], hi, h.z, h.w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i >> 2][i & 3] += d[i >> 2][i & 3];
 }
 // Places of the B operands: -(B M) block (c, b), c > b, and the inverse of diagonal block b without its ones; from 10 on the
 // same of (B M^T): block (b, c), b < c, and the inverse.
@@ -814,8 +819,15 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
     for (int x = up0; x < up0 + ups; ++x) {
       transposed_slab(r[0], sb, true, 16 * x, sf, a.scale);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) to_operand<true>(r[0][b], out[0].hi[b], out[0].lo[b]);
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // (24 bits: with it goes most of dS0)
+          const float2 y = make_float2(r[0][b][i >> 1][2 * (i & 1)], r[0][b][i >> 1][2 * (i & 1) + 1]);
+          out[0].hi[b][i] = bf2(y.x, y.y);
+          split2(fsub2(y, widen2(out[0].hi[b][i])), out[0].lo[b][i], out[1].hi[b][i]);
+        }
       store_slab(out[0], sm, ws + W_QT + 2048 * x, ws + W_QT + 12288 + 2048 * x);
+      store_slab(out[1], sm, ws + W_QT + 24576 + 2048 * x, nullptr);
     }
   }
   if (lane == 0) stores_read();
@@ -826,16 +838,18 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 // Rows of [K; Q] S: 0-63 K's (warps of w % 4 < 2), 64-127 Q's; rows of K^ B R: 0-95 the state's; rows of P^ B R:
 // 64-127.  A warp's lanes are also its scheduler's, and K's rows have most of the work, so every other CTA (of the two
 // that an SM holds) has it the other way round: Q's rows and P^'s first, the state's in 32-127.  A thread keeps its 32
-// columns of a state row in fp32 registers.  One thread of warp 8 issues the products, one of warp 9 the copies.
+// columns of a state row in fp32 registers.  One thread of warp 8 issues the products, one of warp 9 the copies; warp 9 also
+// keeps the bound by which B R is brought to fp16.
 // Hand-overs through mbarriers, so that only the state's way (product, residual, product, state) is waited for: a
 // chunk's outputs are written while the next chunk's first product runs.  Tensor memory: two places of 128 columns
 // ([hi | lo]), 2 CTAs an SM.  A chunk's [K; Q] S and, once that is in registers, its P^ B R have the one, its
 // K^ B R the other; the next chunk has them the other way round.
 // STATES (the backward's forward pass): K's rows stand in Q's place and the other half is not looked at; Z is in P^'s
 // place, X = R - Z B R and every chunk's S0 go to the workspace instead of outputs.
-// Bound by the chain from state to state, about 4,400 cycles a chunk with two CTAs an SM (three hand-overs between threads and
+// Bound by the chain from state to state, about 5,000 cycles a chunk with two CTAs an SM (three hand-overs between threads and
 // tensor cores, two products, 64 x 64 values to registers and back twice): 8 x 2,048 tokens x 16 heads, 384 CTAs on 304
-// places, 150 us (STATES 161-175); 24 ragged sequences x 7 heads 66 us.  With barriers between the steps 239 us (the call).
+// places, 176 us (STATES 180-196); 24 ragged sequences x 7 heads 76 us.  With K^ and B R in two bf16, which need no bound, 150
+// and 66; with the bound waited for by every warp 200 and 76, and with the largest of B R itself 193.
 // Cutting the units into parts that fill whole rounds (a CTA a part, states handed over, the same bits) took 160 us: a CTA that
 // has its SM to itself is faster, so that a last round that is part full loses little.
 constexpr int TN = 64, NTILE = DV / TN, SCAN_THREADS = 320;
@@ -850,7 +864,7 @@ struct ScanSmem {
 // Products ([K; Q] S, K^ B R, P^ B R), copies (K and Q; V and decays; K^; P^), hand-overs (the state, B R and the first
 // product read; the outputs' product read).  Whoever waits for a phase hands something over before the next one of the
 // same barrier can end.
-// (MX: the power of two for the residuals is there.)
+// (MX: the power of two for the residuals is there; the issuing thread waits for it before the first product is called done.)
 enum { SB_A = 0, SB_C, SB_O, SB_KQ, SB_V, SB_KD, SB_PH, SB_SR, SB_WR, SB_OF, SB_MX, SB_DRAIN, SB_N };
 
 template <bool STATES>
@@ -880,18 +894,6 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
   const int role = warp == 9 ? 0 : warp == 8 ? 1 : 2;
   auto wait = [&](int b, int k) { return mbar_wait_at(&bar[b], (uint32_t)k & 1u, a.wait_ns, abort_flag, role, wait_code(IN_SCAN, b, k)); };
 
-  float2 S[16];
-#pragma unroll
-  for (int x = 0; x < 16; ++x) S[x] = both(0.f);
-  if (s_row && from >= 0) {
-    const float4* src = reinterpret_cast<const float4*>(a.h0 + (((long long)from * a.H + h) * DK + srow) * DV + col0);
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const float4 w = src[x];
-      S[2 * x] = make_float2(w.x, w.y);
-      S[2 * x + 1] = make_float2(w.z, w.w);
-    }
-  }
   if (nc > 0) {
     if (warp == 8) {
       tm_alloc<256>(slot_tm);
@@ -905,6 +907,20 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+  }
+  float2 S[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) S[x] = both(0.f);
+  if (s_row && from >= 0) {
+    const float4* src = reinterpret_cast<const float4*>(a.h0 + (((long long)from * a.H + h) * DK + srow) * DV + col0);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float4 w = src[x];
+      S[2 * x] = make_float2(w.x, w.y);
+      S[2 * x + 1] = make_float2(w.z, w.w);
+    }
+  }
+  if (nc > 0) {
     const uint32_t tmem = *slot_tm;
     bool ok = true;
     auto ws_of = [&](int c) { return a.ws + ((long long)(s.slot0 + c) * a.H + h) * (STATES ? W_BWD : W_FWD); };
@@ -1111,6 +1127,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
       for (int c = 0; c < nc; ++c) {
         const uint32_t at_a = lanes + (c & 1) * 128u, at_c = lanes + ((c & 1) ^ 1) * 128u;
         if (o_row && c > 0) outputs(c - 1);
+        if (c == 0) ok = wait(SB_A, 0);  // (so that a limit on waits sees a CTA's first loads as one)
         ok = ok && wait(SB_V, c) && wait(SB_A, c);
         // (one answer for the warp: lanes may leave a wait that runs out with different ones, and outputs() below is for all or none)
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -1210,27 +1227,30 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 // (E = e^(G_C - G)): again two dependent products a chunk.  P^T dO and Q~ dO need no state; they go to the tensor cores
 // while the state's way waits for registers: Q~ dO behind K dS1, the next chunk's P^T dO behind Z^T w.  dbeta's part of the
 // CTA's columns is (dU - Z^T w) . X.
-// 512 threads, one CTA an SM (the operands take 214 KB): warps 0-7 have the state's rows (0-95; columns as in the scan),
+// 512 threads, one CTA an SM (the operands take 219 KB): warps 0-7 have the state's rows (0-95; columns as in the scan),
 // warps 8-15 the tokens' (64-127: other schedulers), so that neither waits for what the other writes out; of the warps
-// that have no rows, 8 issues the products and 12 the copies.  Every hand-over through an mbarrier.
-// Bound as the scan, 4,700 cycles a chunk: 8 x 2,048 tokens x 16 heads 214 us, 384 CTAs on 152 places; HBM 49 % busy;
-// with the products in the order of the formulas 242 us; in parts, as above, 248.
+// that have no rows, 8 issues the products, 12 the copies, and 9 keeps the bound by which w is brought to fp16.  Every
+// hand-over through an mbarrier.
+// Bound as the scan, 5,400 cycles a chunk: 8 x 2,048 tokens x 16 heads 245 us, 384 CTAs on 152 places; with K~, w and Q~ in two
+// bf16 each 214 us (with the products in the order of the formulas 242 us; in parts, as above, 248); with s e^G dO in three
+// bf16, made here by three warps beside the chain, for Q~ in three 303.
 // Tensor memory: P^T dO [0,64), Q~ dO [64,128), K dS1 [128,256) and K~ w [256,384) as [hi | lo], Z^T w [384,448).
 constexpr int RSCAN_THREADS = 512;
 struct RSmem {
-  // of the chunk ahead (two places): Q~ hi, lo; P hi, lo; dO; and X, which is used last
-  static constexpr uint32_t EARLY = 0, E_QT = 0, E_P = 24576, E_DO = 40960, E_X = 49152, E_BYTES = 57344;
+  // Q~ in three; of the chunk ahead (two places): P hi, lo; dO; and X hi, lo, which is used last
+  static constexpr uint32_t QT = 0, EARLY = 36864, E_P = 0, E_DO = 16384, E_X = 24576, E_BYTES = 40960;
+  static_assert(EARLY + E_P >= 8192, "what is read before P");
   // K~ hi, lo and Z; K; the state; w; two places of e^G, beta, E.  Products of 128 rows read past operands of 64 and 96
   // rows: before K, whose rows are the second half, 8 KB that are never written; before Z and P, and behind K~ and Q~, what
   // is as still as the operand itself.  The rows that gives are not looked at.
-  static constexpr uint32_t KR = 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 8192, S = K1 + 4096, W = S + 24576, OUT = W + 16384,
-                            GT = OUT + 8192, BAR = GT + 2 * GT_RSCAN, MX = BAR + 192, BYTES = MX + 64;
+  static constexpr uint32_t KR = EARLY + 2 * E_BYTES, K0 = KR + 32768 + 8192, K1 = K0 + 8192, S = K1 + 4096, W = S + 24576, OUT = W + 16384,
+                            GT = OUT + 8192, BAR = GT + 2 * GT_RSCAN, MX = BAR + 208, BYTES = MX + 64;
   static_assert(BYTES <= 232448, "shared memory");
 };
 // Products and copies, then hand-overs: the state, w, Z^T w and X read.  Whoever waits for a phase of a barrier hands
 // something over before the next one can end; where that would not hold (E's, the decays', ZF) there are two, by the
 // chunk's parity.
-enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_DRAIN, RB_ZF, RB_GT = RB_ZF + 2, RB_X = RB_GT + 2, RB_MX = RB_X + 2, RB_N = RB_MX + 2 };
+enum { RB_E = 0, RB_EF = 2, RB_K = 4, RB_KR, RB_A, RB_C, RB_Z, RB_SR, RB_WR, RB_DRAIN, RB_ZF, RB_GT = RB_ZF + 2, RB_X = RB_GT + 2, RB_MX = RB_X + 2, RB_QT = RB_MX + 2, RB_N };
 constexpr uint32_t RT_P = 0, RT_Q = 64, RT_A = 128, RT_C = 256, RT_Z = 384;
 
 __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __grid_constant__ DeltaMaps maps, const DeltaArgs a, float* dbeta_part) {
@@ -1240,7 +1260,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
   uint64_t* const bar = reinterpret_cast<uint64_t*>(sm + RSmem::BAR);
   uint32_t* const slot_tm = reinterpret_cast<uint32_t*>(sm + RSmem::BAR + 8 * RB_N);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + RSmem::BAR + 8 * RB_N + 4);
-  int* const issued = reinterpret_cast<int*>(sm + RSmem::BAR + 8 * RB_N + 8);  // [5] copies: EARLY's two places, K, K~; X
+  int* const issued = reinterpret_cast<int*>(sm + RSmem::BAR + 8 * RB_N + 8);  // [6] copies: EARLY's two places, K, K~; X; Q~
   // by the chunk's parity, the power of two that brings w to fp16, and its inverse [2]; the largest of the last dS, of its six warps
   float2* const by = reinterpret_cast<float2*>(sm + RSmem::MX);
   float* const most_s = reinterpret_cast<float*>(by + 2);
@@ -1289,19 +1309,18 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
     if (warp == 12) {
       if (lane == 0) {
         // copies: each as soon as what stood in its place has been used
-        int loads[4] = {}, xs = 0;  // EARLY's two places, K, K~; X
+        int loads[4] = {}, xs = 0, qts = 0;  // EARLY's two places, K, K~; X
         auto load_early = [&](int it) {
           const int c = nc - 1 - it, p = it & 1;
           const uint32_t to = sb + RSmem::EARLY + p * RSmem::E_BYTES;
           ++loads[p];
           mbar_expect_tx(&bar[RB_EF + p], RSmem::E_X);
-          bulk_load(to + RSmem::E_QT, ws_of(c) + W_QT, 24576, &bar[RB_EF + p]);
           bulk_load(to + RSmem::E_P, ws_of(c) + W_P, 16384, &bar[RB_EF + p]);
           box_load(to + RSmem::E_DO, &maps.dO, &bar[RB_EF + p], tile * TN, h, (int)(s.begin + (long long)c * DC));
         };
         auto load_x = [&](int it) {
           const int c = nc - 1 - it, p = it & 1;
-          mbar_expect_tx(&bar[RB_X + p], 8192);
+          mbar_expect_tx(&bar[RB_X + p], 16384);
           box_load(sb + RSmem::EARLY + p * RSmem::E_BYTES + RSmem::E_X, &maps.x, &bar[RB_X + p], tile * TN, 0, (s.slot0 + c) * a.H + h);
         };
         auto load_k = [&](int it) {
@@ -1312,6 +1331,11 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           box_load(sb + RSmem::K0, &maps.k0, &bar[RB_K], 0, h, t);
           box_load(sb + RSmem::K1, &maps.k1, &bar[RB_K], 64, h, t);
           bulk_load(sb + RSmem::GT + (it & 1) * GT_RSCAN, ws_of(c) + W_GT, GT_RSCAN, &bar[RB_GT + (it & 1)]);
+        };
+        auto load_qt = [&](int it) {
+          ++qts;
+          mbar_expect_tx(&bar[RB_QT], 36864);
+          bulk_load(sb + RSmem::QT, ws_of(nc - 1 - it) + W_QT, 36864, &bar[RB_QT]);
         };
         auto load_kr = [&](int it) {
           const int c = nc - 1 - it;
@@ -1326,11 +1350,12 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           box_prefetch(&maps.k1, 64, h, t);
           box_prefetch(&maps.dO, tile * TN, h, t);
           bulk_prefetch(ws_of(c) + W_PH, 8192 + 4 * GT_ALL);
-          bulk_prefetch(ws_of(c) + W_KR, 24576 + 24576 + 16384);
+          bulk_prefetch(ws_of(c) + W_KR, 24576 + 36864 + 16384);
         };
         load_early(0);
         load_k(0);
         load_kr(0);
+        load_qt(0);
         if (nc > 1) load_early(1);
         for (; xs < min(nc, 2); ++xs) load_x(xs);
         for (int it = 0; it < nc && ok; ++it) {
@@ -1338,6 +1363,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           ok = wait(RB_A, it);
           if (ok && it + 1 < nc) load_k(it + 1);
           ok = ok && wait(RB_C, it);
+          if (ok && it + 1 < nc) load_qt(it + 1);
           if (ok && it + 2 < nc) load_early(it + 2);
           ok = ok && wait(RB_Z, it);
           if (ok && it + 1 < nc) load_kr(it + 1);
@@ -1346,6 +1372,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         }
         for (int x = 0; x < 4; ++x) issued[x] = loads[x];
         issued[4] = xs;
+        issued[5] = qts;
       }
       __syncwarp();
     } else if (warp == 8) {
@@ -1387,12 +1414,14 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
           umma_commit(&bar[RB_A]);
           // (the state's high halves are what the gradients take of it)
           box_store(&maps.ds, sb + RSmem::S, tile * TN, 0, (s.slot0 + nc - 1 - it) * a.H + h);
-          {  // Q~ dO (its operands came with P's)
-            const uint32_t from = sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES;
-            const SDesc dq = sdesc(from + RSmem::E_QT, 16, 1024, LAYOUT_SW128), dd = sdesc(from + RSmem::E_DO, 8192, 1024, LAYOUT_SW128);
+          ok = look(RB_QT, it);
+          if (!ok) break;
+          {  // Q~ dO: lo, mid, hi (dO came with P)
+            const SDesc dq = sdesc(sb + RSmem::QT, 16, 1024, LAYOUT_SW128);
+            const SDesc dd = sdesc(sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES + RSmem::E_DO, 8192, 1024, LAYOUT_SW128);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma(tmem + RT_Q, dq + (kk >> 2) * 12288u + (kk & 3) * 32u, dd + (kk & 3) * 2048u, idesc_bf16(128, 64, 0, 1), kk > 0);
+            for (int kk = 0; kk < 12; ++kk)
+              umma(tmem + RT_Q, dq + (2 - (kk >> 2)) * 12288u + (kk & 3) * 32u, dd + (kk & 3) * 2048u, idesc_bf16(128, 64, 0, 1), kk > 0);
           }
           ok = look(RB_KR, it) && wait(RB_WR, it);
           if (!ok) break;
@@ -1524,12 +1553,13 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint4 x4 = ld_shared_v4(sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES + RSmem::E_X + sw128(tok, 4 * half + 2 * x + i));
-            const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
+            const uint4 y4 = ld_shared_v4(sb + RSmem::EARLY + (it & 1) * RSmem::E_BYTES + RSmem::E_X + 8192 + sw128(tok, 4 * half + 2 * x + i));
+            const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w}, yw[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int at = 4 * i + e;
               const float2 t = fmadd2(minus_z, pair(z, at), du[8 * x + at]);
-              part = fmadd2(t, widen2(xw[e]), part);
+              part = fmadd2(t, fadd2(widen2(xw[e]), widen2(yw[e])), part);
               const float2 y = fmul2(both(b_row), t);
               w[at] = bf2(y.x, y.y);
             }
@@ -1561,6 +1591,7 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
         for (int x = 0; x < 4; ++x)
           if (issued[x]) mbar_wait_drain(&bar[RB_EF + x], (issued[x] - 1) & 1, DRAIN_NS, a.err);
         for (int it = max(0, issued[2] - 2); it < issued[2]; ++it) mbar_wait_drain(&bar[RB_GT + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
+        mbar_wait_drain(&bar[RB_QT], (issued[5] - 1) & 1, DRAIN_NS, a.err);
         for (int it = max(0, issued[4] - 2); it < issued[4]; ++it) mbar_wait_drain(&bar[RB_X + (it & 1)], (it >> 1) & 1, DRAIN_NS, a.err);
       }
       if (warp == 8 && lane == 0) {
@@ -1595,8 +1626,8 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 //     dg_t = sum of dG_i, i >= t
 // 288 threads, 2 CTAs an SM: warps 0-7 have lanes 32 (w % 4) .. of the products' rows and 48 columns of d_k (w / 4); rows
 // 0-63 have dq, 64-127 all of dk.  Warp 8 issues copies and products.  Panels have two places, K and Q come into the second.
-// Bound by HBM (196 KB a chunk and head, 62 % busy) and by latency: 8 x 2,048 tokens x 16 heads 165 us, 4.9 TB/s; with one
-// place for the panels and three boxes instead of one 190 us.
+// Bound by HBM (220 KB a chunk and head, 58 % busy) and by latency: 8 x 2,048 tokens x 16 heads 183 us, 4.9 TB/s (X, Es and Fm in
+// one bf16: 196 KB, 165 us; with one place for the panels and three boxes instead of one 190).
 constexpr int GRAD_THREADS = 288;
 struct GSmem {
   // a panel: [dO; dR], X hi and lo, S0, dS1; later Es and Fm, hi and lo, where the first place's dO, dR and X were (S0 and dS1 may
@@ -2066,7 +2097,7 @@ cudaError_t launch_delta_tc_bwd(DeltaArgs a, cudaStream_t st) {
   if (some) {
     const long long all = (long long)a.slots * a.H;
     if (!(input_maps(m, a) && rows_map(&m.dO, a.dO, DV, a, 64, DC) && rows_map(&m.dv, a.dv, DV, a, 64, DC) &&
-          map3(&m.x, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 64, DC, 1) && map3(&m.s0, a.ws + W_S0, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) &&
+          map3(&m.x, a.ws + W_X, DV, 2 * DC, all, 2 * DV, W_BWD, 64, 2 * DC, 1) && map3(&m.s0, a.ws + W_S0, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) &&
           map3(&m.ds, a.ws + W_DS, DV, DK, all, 2 * DV, W_BWD, 64, DK, 1) && map3(&m.xo, a.ws + W_X, DV, DC, all, 2 * DV, W_BWD, 32, 32, 1) &&
           rows_map(&m.dvo, a.dv, DV, a, 32, 32) && map3(&m.xsd, a.ws + W_X, DV, 320, all, 2 * DV, W_BWD, 64, 160, 1) &&
           map3(&m.xlo, a.ws + W_XL, DV, DC, all, 2 * DV, W_BWD, 32, 32, 1) &&

@@ -8,7 +8,10 @@ a binade) / sqrt(3) = 1.6e-3.  One more rounding of that size on the way gives s
 in the tensor cores and the rest is fp32: 2^-22 x 0.72 / sqrt(3) = 1e-7 for each of the up to eight operands in a row, 3e-7 at
 random signs, and the cut of 2^-23 a sum with a sign of its own, 1.2e-7 for each of up to three in a row: 6e-7 (long sums in
 the tensor cores cut off ten times as often).  dg is what is left of three dot products (q . dq and two of k), each with an
-error of its own: sqrt(3) of that, 1.05e-6."""
+error of its own: sqrt(3) of that, 1.05e-6.  States of bf16 calls: what is split into two bf16 (the state itself, and P in the
+backward) keeps 2^-17 x 0.72 / sqrt(3) = 3.2e-6 of its part of the result, a quarter of it or less (what a chunk adds is made from
+one state, of which it replaces a part), 0.8e-6; what is split into two fp16 2^-22; sums are cut off at 2^-23 three times
+in a row, 0.3e-6 with a sign of its own: 1.5e-6 with room for few sequences."""
 import pytest
 import torch
 
@@ -48,7 +51,7 @@ def hold(b, bounds):
 
 
 def bf16(name):
-    return 2e-5 if name in ("hT", "dh0") else 3e-3 if name == "dg" else 2.5e-3
+    return 1.5e-6 if name in ("hT", "dh0") else 3e-3 if name == "dg" else 2.5e-3
 
 
 @pytest.mark.parametrize("seed", [101, 102])
@@ -125,4 +128,6 @@ def test_long_sequences_without_decay(strength):
     # (a strength of 1.9 leaves 0.81 of the square of what stands under a key, one of 0.5 a quarter: errors live four times as long,
     # twice in the norm: 1.6e-3 and twice sqrt(3) of it)
     rest = 5.8e-3 if strength == "two" else 3.3e-3
-    assert all(x <= (bf16(n) if n in ("o", "hT", "dv", "dh0") else rest) for n, x in errors.items())
+    # (and a state that forgets nothing gathers the errors of 94 chunks, at random signs: 10 times a chunk's, of which a write
+    # takes back its part)
+    assert all(x <= (1.5e-5 if n in ("hT", "dh0") else bf16(n) if n in ("o", "dv") else rest) for n, x in errors.items())

@@ -14,7 +14,7 @@ COPIES, PRODUCTS, ROWS = 0, 1, 2
 PREP, SCAN, RSCAN, GRADS = 0, 1, 2, 3
 # barriers by the order of the kernels' enumerations
 A, C, O, KQ, V, KD, PH, SR, WR, OF, MX = range(11)  # scan
-E0, E1, EF0, EF1, K, KR, RA, RC, Z, RSR, RWR, RDRAIN, ZF0, ZF1, GT0, GT1, X0, X1, MX0, MX1 = range(20)  # reverse scan
+E0, E1, EF0, EF1, K, KR, RA, RC, Z, RSR, RWR, RDRAIN, ZF0, ZF1, GT0, GT1, X0, X1, MX0, MX1, QT = range(21)  # reverse scan
 GKQ, IN0, IN1, FR0, FR1, MMA0, MMA1, ONE, EF, TWO = range(10)  # gradients
 
 SCAN_WAITS = ([(COPIES, b, k) for b in (A, WR, C, O, V) for k in (0, 1, 3)] + [(COPIES, SR, 0), (PRODUCTS, MX, 0), (PRODUCTS, MX, 4)] +
@@ -22,7 +22,7 @@ SCAN_WAITS = ([(COPIES, b, k) for b in (A, WR, C, O, V) for k in (0, 1, 3)] + [(
               [(ROWS, b, k) for b in (V, A, C, O) for k in (0, 1, 4)])
 RSCAN_WAITS = ([(COPIES, b, k) for b in (RA, RC, Z) for k in (0, 1, 4)] + [(COPIES, ZF0, 0), (COPIES, ZF1, 1)] +
                [(PRODUCTS, b, k) for b in (K, RSR, KR, RWR) for k in (0, 1, 4)] +
-               [(PRODUCTS, b, k) for b, k in ((EF0, 0), (EF1, 0), (EF0, 2), (ZF0, 0), (ZF1, 1), (MX0, 0), (MX1, 1))] +
+               [(PRODUCTS, b, k) for b, k in ((EF0, 0), (EF1, 0), (EF0, 2), (ZF0, 0), (ZF1, 1), (MX0, 0), (MX1, 1), (QT, 0), (QT, 4))] +
                [(ROWS, RSR, 0)] + [(ROWS, b, k) for b in (GT0, GT1, E0, E1, X0, X1, EF0, EF1) for k in (0, 1)] + [(ROWS, b, k) for b in (RA, RC, Z) for k in (0, 1, 4)])
 GRADS_WAITS = ([(PRODUCTS, b, 0) for b in (IN0, IN1, FR0, FR1, MMA0, MMA1, EF)] + [(PRODUCTS, IN0, 1)] +
                [(ROWS, b, 0) for b in (IN0, IN1, GKQ, ONE, TWO)] + [(ROWS, IN0, 1)])
