@@ -17,7 +17,7 @@
 // scaled by a bound (see prep and the scan).  P^ and Z are one fp16.  X, Es and Fm, which nearly every gradient goes through,
 // are two bf16; S0 and dS1 for the gradients one.  hT and dh0 are 0.2 to 0.9e-6 of the norm from the exact ones (with two bf16
 // throughout 4.4 and 3.1e-6), o and dbeta 1.7e-3, their own rounding (2.1 and 2.3e-3), dq and dk 2.0e-3 and dg 2.4e-3 (with X,
-// Es and Fm in one bf16 3.0e-3).  What that costs: forward of 8 x 2,048 x 16 221 -> 261 us, backward 675 -> 770.
+// Es and Fm in one bf16 3.0e-3).  What that costs: forward of 8 x 2,048 x 16 221 -> 256 us, backward 675 -> 771.
 // What the chunk's length costs: longer chunks halve the scans' steps, but prep and grads grow with its square; 64 tokens
 // are also the 128 rows of [K; Q] and the 128 bytes of a swizzled row.
 #include <cuda.h>
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
 // place, X = R - Z B R and every chunk's S0 go to the workspace instead of outputs.
 // Bound by the chain from state to state, about 5,000 cycles a chunk with two CTAs an SM (three hand-overs between threads and
 // tensor cores, two products, 64 x 64 values to registers and back twice): 8 x 2,048 tokens x 16 heads, 384 CTAs on 304
-// places, 176 us (STATES 180-196); 24 ragged sequences x 7 heads 76 us.  With K^ and B R in two bf16, which need no bound, 150
+// places, 176 us (STATES 181-196); 24 ragged sequences x 7 heads 76 us.  With K^ and B R in two bf16, which need no bound, 150
 // and 66; with the bound waited for by every warp 200 and 76, and with the largest of B R itself 193.
 // Cutting the units into parts that fill whole rounds (a CTA a part, states handed over, the same bits) took 160 us: a CTA that
 // has its SM to itself is faster, so that a last round that is part full loses little.
@@ -1235,7 +1235,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
 // warps 8-15 the tokens' (64-127: other schedulers), so that neither waits for what the other writes out; of the warps
 // that have no rows, 8 issues the products, 12 the copies, and 9 keeps the bound by which w is brought to fp16.  Every
 // hand-over through an mbarrier.
-// Bound as the scan, 5,400 cycles a chunk: 8 x 2,048 tokens x 16 heads 245 us, 384 CTAs on 152 places; with K~, w and Q~ in two
+// Bound as the scan, 5,400 cycles a chunk: 8 x 2,048 tokens x 16 heads 249 us, 384 CTAs on 152 places; HBM 48 % busy; with K~, w and Q~ in two
 // bf16 each 214 us (with the products in the order of the formulas 242 us; in parts, as above, 248); with s e^G dO in three
 // bf16, made here by three warps beside the chain, for Q~ in three 303.
 // Tensor memory: P^T dO [0,64), Q~ dO [64,128), K dS1 [128,256) and K~ w [256,384) as [hi | lo], Z^T w [384,448).
@@ -1630,8 +1630,8 @@ __global__ void __launch_bounds__(RSCAN_THREADS, 1) delta_rscan_kernel(const __g
 //     dg_t = sum of dG_i, i >= t
 // 288 threads, 2 CTAs an SM: warps 0-7 have lanes 32 (w % 4) .. of the products' rows and 48 columns of d_k (w / 4); rows
 // 0-63 have dq, 64-127 all of dk.  Warp 8 issues copies and products.  Panels have two places, K and Q come into the second.
-// Bound by HBM (220 KB a chunk and head, 58 % busy) and by latency: 8 x 2,048 tokens x 16 heads 183 us, 4.9 TB/s (X, Es and Fm in
-// one bf16: 196 KB, 165 us; with one place for the panels and three boxes instead of one 190).
+// Bound by HBM (220 KB a chunk and head, 62 % busy) and by latency: 8 x 2,048 tokens x 16 heads 184 us, 911 MB at 4.9 TB/s (X, Es and
+// Fm in one bf16: 196 KB, 811 MB, 165 to 172 us; with one place for the panels and three boxes instead of one 190).
 constexpr int GRAD_THREADS = 288;
 struct GSmem {
   // a panel: [dO; dR], X hi and lo, S0, dS1; later Es and Fm, hi and lo, where the first place's dO, dR and X were (S0 and dS1 may

@@ -10,7 +10,7 @@
 // One launch: every CTA computes the whole plan (a few microseconds, bound by latency: another launch, or a wait for another
 // CTA, would cost as much) and writes its share of the tokens' places from the offsets in its shared memory; the first
 // one writes the requests' maps.  Batches whose offsets do not fit there have a second launch for the tokens.
-// 48 requests and 2,048 tokens take 8 us, 5,000 requests and 65,536 tokens 18 (of a call's 23 with its binding); as two
+// 48 requests and 2,048 tokens take 8 us, 5,000 requests and 65,536 tokens 18 (of a call's 24 to 32 with its binding); as two
 // launches 34.
 #include "gla_delta.cuh"
 #include "gla_once.cuh"
