@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(PREP_THREADS, BWD ? 3 : 4) delta_prep_kernel(c
       sic[j] = ic;
       sbc[j] = c * sbeta[j];
       sek[j] = OP_SCALE * ic * se[j];
-      if (BWD) sfk[j] = kr_scale.x * ic * sf[j];
+      if (BWD) sfk[j] = ic * (kr_scale.x * sf[j]);  // (first what stays finite: after a reset 2^126 stands beside zeros)
       cf[j] *= ic;
       // (a write turns the state's columns by 1 - beta k k^T)
       const float turn = fabsf(fmaf(-sbeta[j], size, 1.f));

@@ -109,6 +109,19 @@ def test_sizes_side_by_side(what):
     hold(b, lambda name: bf16(name) if name in ("o", "hT", "dv", "dh0") or what not in ("keys", "states") else 3.3e-3)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("size", [1e-6, 1e-2, 1e3])
+@pytest.mark.parametrize("gate", [-float("inf"), -100.0, -60.0])
+def test_resets_with_keys_of_other_lengths(gate, size, dtype):
+    """Resets and all but resets, at a chunk's first token, its last one and between, beside short and long keys: finite, and as
+    near as elsewhere."""
+    b = Batch(107, [200, 64, 65], 2, dtype)
+    b.x["k"] *= size
+    b.x["beta"] /= size * size
+    b.x["g"][[0, 63, 64, 100, 200, 263, 264, 328], 0] = gate
+    hold(b, bf16 if dtype == BF else lambda name: 2e-6)
+
+
 @pytest.mark.parametrize("strength", ["usual", "one", "two"])
 def test_long_sequences_without_decay(strength):
     """States over thousands of tokens that forget nothing: against the fp32 call on the same values, whose states are 6e-7 of
