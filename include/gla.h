@@ -448,7 +448,9 @@ int gla_prefix_bwd(const void* q, const void* k, const void* v, const float* log
  * T are clamped and record GLA_ERR_SHAPE.  Its last offset may stand below T (a step under its budget): the forward
  * leaves such rows of o as they were, the backward writes zeros to the gradients of such rows.
  * bf16 calls hold states in fp32 and what carries them from chunk to chunk in 16 to 24 bits (hT and dh0 are 0.2 to 1.2e-6
- * of the norm from the exact ones, up to 1e-5 where thousands of tokens forget nothing).  o, dv and dbeta are their own
+ * of the norm from the exact ones, up to 1e-5 where thousands of tokens forget nothing; where a state has been far larger
+ * before, 3e-10 of its largest as well; where g is above 0, a state may grow by 2^8 within a chunk, which the fp32 call does
+ * not ask).  o, dv and dbeta are their own
  * rounding away (1.7e-3 of the norm), dq and dk 1.7 to 2.3e-3, dg up to 2.9e-3: the states that they are made of are rounded
  * to bf16 on the way.  A caller who wants more makes the fp32 call on the same values: it keeps 22 bits of each operand of
  * a product, and everything else in fp32 (1 to 4e-7 of the norm, dg 8e-7).

@@ -973,7 +973,8 @@ __global__ void __launch_bounds__(SCAN_THREADS, 2) delta_scan_kernel(const __gri
           bulk_prefetch(ws_of(c), W_FWD);
         };
         // The warp's: what bounds c beta R of chunk c (its largest, or the state's, would have to go from warp to warp on the state's way,
-        // 20 to 60 us more) and the power of two that brings that to fp16.
+        // 20 to 60 us more) and the power of two that brings that to fp16.  It stands for a chunk's tokens together and knows nothing of what
+        // writes take out of a state, so that what has been lost of a large one leaves 3e-10 of it.
         float length = 0.f;  // of a column of the state, at most
         auto bound = [&](int c) {
           ok = __all_sync(0xffffffffu, ok && wait(SB_V, c) && (c > 0 || wait(SB_SR, 0)));

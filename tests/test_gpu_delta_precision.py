@@ -122,6 +122,28 @@ def test_resets_with_keys_of_other_lengths(gate, size, dtype):
     hold(b, bf16 if dtype == BF else lambda name: 2e-6)
 
 
+@pytest.mark.parametrize("size", [1e3, 1e6])
+@pytest.mark.parametrize("decay", [False, True])
+def test_states_that_are_lost(decay, size):
+    """First states (and, in the backward, last gradients) far above what comes beside them, which lose in a few hundred tokens what
+    no decay says: a write takes out what stands under its key.  An error made in a chunk loses the same, so that each of up to 11
+    chunks leaves the 1.5e-6 of one chunk's states, 1.65e-5 if all had one sign.
+    With decay the state is lost within one chunk (head 0: e^-51), whose last tokens' residuals are small beside the bound that
+    brings the chunk's to fp16: 10 of the largest element, 4.4 rms, of the state (unit keys), brought to 2^13 at least, where
+    half of fp16's smallest step is 2^-38 of it.  With columns of K^ up to 2, sqrt(64) x 2 x 2^-38 x 44 / sqrt(96) = 2^-31.8 of the
+    first state's norm, which is 2.7e-10.  (K^'s own smallest steps stand at tokens that the state had reached in full, but
+    whose part decays away.)"""
+    b = Batch(108, [700, 300, 64, 33], 2, BF)
+    if not decay:
+        b.x["g"][:] = 0
+    b.h0, b.dhT = b.h0 * size, b.dhT * size
+    got = outputs(b)
+    out = {n: far(*got[n])[0] for n in ("hT", "dh0")}
+    print({n: f"{x:.2e}" for n, x in out.items()})
+    for n, first in (("hT", b.h0), ("dh0", b.dhT)):
+        assert out[n] <= 1.65e-5 + 2.0 ** -31.8 * float(first.norm()) / float(got[n][1].norm()), (n, out)
+
+
 @pytest.mark.parametrize("strength", ["usual", "one", "two"])
 def test_long_sequences_without_decay(strength):
     """States over thousands of tokens that forget nothing: against the fp32 call on the same values, whose states are 6e-7 of
